@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -21,12 +22,12 @@ from ._build import LIB as _LIB_PATH
 
 __all__ = [
     "load", "sf_bytes", "sf_offset", "q4_quantize", "tensor_amax", "q4_quantize_two_level", "fp4_gather_rows", "fp8_gather_rows", "q8_quantize", "gemm_fp4", "gemm_fp8", "gemm_fp8_multi", "gemm_fp4_multi",
-    "grouped_gemm_fp4", "grouped_gemm_fp4_swiglu_q4", "grouped_gemm_fp8", "moe_router_topk", "moe_dispatch", "moe_finalize", "moe_combine", "moe_rows_bound", "device_status",
+    "grouped_gemm_fp4", "grouped_gemm_fp4_swiglu_q4", "grouped_gemm_fp8", "moe_router_topk", "moe_dispatch", "moe_finalize", "moe_combine", "moe_rows_bound", "kv_plan", "kv_release", "kv_append", "kv_attention", "matvec_fp4", "KVCache", "device_status",
     "clear_device_status", "BSError", "EPI_STORE", "EPI_SWIGLU", "EPI_COMBINE", "EPI_ROWS", "kernel_options",
     "current_kernel_options", "FP4_ONE_CTA", "FP4_PAIR",
 ]
 
-BS_OK, BS_ERR_INVALID, BS_ERR_ALIGN, BS_ERR_UNSUPPORTED, BS_ERR_CUDA, BS_ERR_TIMEOUT, BS_ERR_OFFSETS = range(7)
+BS_OK, BS_ERR_INVALID, BS_ERR_ALIGN, BS_ERR_UNSUPPORTED, BS_ERR_CUDA, BS_ERR_TIMEOUT, BS_ERR_OFFSETS, BS_ERR_PAGES = range(8)
 DTYPE_F32, DTYPE_BF16 = 0, 1
 FMT_FP4, FMT_FP8 = 0, 1
 EPI_STORE, EPI_SWIGLU, EPI_COMBINE, EPI_ROWS = 0, 1, 2, 3
@@ -51,6 +52,31 @@ class GemmArgs(ctypes.Structure):
         ("fp8_scaling", ctypes.c_int), ("wait_timeout_us", ctypes.c_int), ("weights_ready", ctypes.c_int), ("workspace", ctypes.c_void_p),
         ("workspace_bytes", ctypes.c_size_t), ("a_tensor_scale", ctypes.c_void_p), ("b_tensor_scale", ctypes.c_void_p),
         ("fp4_decode", ctypes.c_int),
+    ]
+
+
+class KvAppendArgs(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int), ("T", ctypes.c_int64),
+        ("Hkv", ctypes.c_int), ("D", ctypes.c_int), ("k_token_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+        ("slots", ctypes.c_void_p), ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+        ("page_size", ctypes.c_int),
+    ]
+
+
+class KvAttentionArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+        ("lse", ctypes.c_void_p), ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+        ("page_size", ctypes.c_int), ("block_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64),
+        ("max_pages", ctypes.c_int), ("cu_q", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("B", ctypes.c_int),
+        ("T", ctypes.c_int64), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+        ("max_q_len", ctypes.c_int), ("softmax_scale", ctypes.c_float), ("wait_timeout_us", ctypes.c_int),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -146,6 +172,18 @@ def load(path: str | None = None):
         lib.bs_moe_finalize.argtypes = [P, P, I64, P]
         lib.bs_moe_combine.restype = I
         lib.bs_moe_combine.argtypes = [P, I64, P, I64, I64, I, I64, P, P, I64, P]
+        lib.bs_kv_plan.restype = I
+        lib.bs_kv_plan.argtypes = [P, P, I, P, I64, I, P, P, I, I, I64, P, P, P, P, P]
+        lib.bs_kv_release.restype = I
+        lib.bs_kv_release.argtypes = [P, P, I, P, I64, I, P, P, I, I, P]
+        lib.bs_kv_append.restype = I
+        lib.bs_kv_append.argtypes = [ctypes.POINTER(KvAppendArgs), P]
+        lib.bs_kv_attention_workspace_bytes.restype = SZ
+        lib.bs_kv_attention_workspace_bytes.argtypes = [ctypes.POINTER(KvAttentionArgs)]
+        lib.bs_kv_attention.restype = I
+        lib.bs_kv_attention.argtypes = [ctypes.POINTER(KvAttentionArgs), P]
+        lib.bs_fp4_matvec.restype = I
+        lib.bs_fp4_matvec.argtypes = [P, I64, I, P, P, I64, I64, F, P, P, P, I, I64, P]
         lib.bs_get_device_status.restype = I
         lib.bs_get_device_status.argtypes = [ctypes.POINTER(I)]
         lib.bs_clear_device_status.restype = I
@@ -154,7 +192,6 @@ def load(path: str | None = None):
         lib.bs_status_string.argtypes = [I]
         lib.bs_last_error.restype = ctypes.c_char_p
         lib.bs_last_error.argtypes = []
-        _ = F
         _lib = lib
         return lib
 
@@ -505,6 +542,166 @@ def moe_combine(rows, pair_of_row, T: int, k: int, out=None, row_of_pair=None, s
         row_of_pair = torch.empty(max(T * k, 1), dtype=torch.int32, device=rows.device)
     _check(load().bs_moe_combine(_ptr(rows), rows.stride(0), _ptr(pair_of_row), n_rows, T, k, H, _ptr(row_of_pair),
                                  _ptr(out), out.stride(0), _stream(stream)))
+    return out
+
+
+class KVCache(NamedTuple):
+    """One layer's 8-bit paged cache: e4m3 codes uint8 [pages, Hkv, page_size,
+    D] and fp32 scales [pages, Hkv] of keys and values."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    @classmethod
+    def empty(cls, num_pages: int, Hkv: int, page_size: int, D: int, device="cuda") -> "KVCache":
+        shape = (num_pages, Hkv, page_size, D)
+        return cls(torch.zeros(shape, dtype=torch.uint8, device=device),
+                   torch.zeros(shape, dtype=torch.uint8, device=device),
+                   torch.ones(shape[:2], dtype=torch.float32, device=device),
+                   torch.ones(shape[:2], dtype=torch.float32, device=device))
+
+
+def _check_kv_cache(cache):
+    """(k, v, k_scale, v_scale, shape) of a KVCache (or such a tuple), checked
+    for type and layout."""
+    k, v, ks, vs = cache
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape or ks.shape != shape[:2] or vs.shape != shape[:2]:
+        raise ValueError("a KV cache is codes [pages, Hkv, page_size, D] and scales [pages, Hkv], twice")
+    if k.dtype != torch.uint8 or v.dtype != torch.uint8 or ks.dtype != torch.float32 or vs.dtype != torch.float32:
+        raise TypeError("KV cache codes are uint8 (e4m3), scales float32")
+    if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+        raise ValueError("KV cache buffers must be contiguous")
+    return k, v, ks, vs, shape
+
+
+def _ints(name, *tensors):
+    for t in tensors:
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise TypeError(f"{name}: lengths, tables and slots are contiguous int32 tensors")
+
+
+def kv_plan(seq_lens, new_lens, block_table, free_pages, n_free, page_size: int, total_new: int, out=None,
+            stream=None):
+    """Block tables and slots of a step, from the requests' lengths (device
+    int32): request b takes the pages that its new tokens need from the end of
+    ``free_pages[:n_free]``; ``block_table`` [B, max_pages] is updated in place.
+    Returns (cu_new [B + 1], kv_lens [B], slots [total_new], n_free [1])."""
+    B = seq_lens.shape[0]
+    dev = seq_lens.device
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.stride(1) != 1:
+        raise TypeError("kv_plan: block_table is an int32 [B, max_pages] tensor with contiguous rows")
+    if new_lens.shape[0] != B or block_table.shape[0] != B:
+        raise ValueError("kv_plan: seq_lens, new_lens and block_table differ in the number of requests")
+    if out is None:
+        out = (torch.empty(B + 1, dtype=torch.int32, device=dev), torch.empty(B, dtype=torch.int32, device=dev),
+               torch.empty(total_new, dtype=torch.int32, device=dev), torch.empty(1, dtype=torch.int32, device=dev))
+    cu, kv, slots, left = out
+    _ints("kv_plan", seq_lens, new_lens, free_pages, n_free, cu, kv, slots, left)
+    if cu.numel() < B + 1 or kv.numel() < B or slots.numel() < total_new:
+        raise ValueError("kv_plan: outputs are [B + 1], [B], [total_new] and [1]")
+    _check((_lib or load()).bs_kv_plan(
+        seq_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(), block_table.stride(0),
+        block_table.shape[1], free_pages.data_ptr(), n_free.data_ptr(), free_pages.numel(), page_size, total_new,
+        cu.data_ptr(), kv.data_ptr(), slots.data_ptr(), left.data_ptr(), _stream(stream)))
+    return out
+
+
+def kv_release(lens, done, block_table, free_pages, n_free, page_size: int, stream=None):
+    """Give the pages of the requests with ``done[b] != 0`` (``lens[b]`` cached
+    tokens) back to the free list, in place."""
+    _ints("kv_release", lens, done, free_pages, n_free)
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.stride(1) != 1:
+        raise TypeError("kv_release: block_table is an int32 [B, max_pages] tensor with contiguous rows")
+    B = lens.shape[0]
+    if done.shape[0] != B or block_table.shape[0] != B:
+        raise ValueError("kv_release: lens, done and block_table differ in the number of requests")
+    _check((_lib or load()).bs_kv_release(
+        lens.data_ptr(), done.data_ptr(), B, block_table.data_ptr(), block_table.stride(0), block_table.shape[1],
+        free_pages.data_ptr(), n_free.data_ptr(), free_pages.numel(), page_size, _stream(stream)))
+
+
+def kv_append(k, v, slots, cache, stream=None):
+    """Quantize new keys and values [T, Hkv, D] (fp32 or bf16, any token and
+    head strides) into their slots of the 8-bit cache, in place."""
+    kc, vc, ks, vs, (pages, Hkv, page, D) = _check_kv_cache(cache)
+    T = slots.shape[0]
+    if k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D):
+        raise ValueError(f"kv_append: k and v are [{T}, {Hkv}, {D}] for these slots and this cache")
+    if k.stride(2) != 1 or v.stride(2) != 1 or k.dtype != v.dtype:
+        raise ValueError("kv_append: k and v have one type and contiguous rows of D")
+    _ints("kv_append", slots)
+    kst, vst = k.stride(), v.stride()
+    a = KvAppendArgs(k.data_ptr(), v.data_ptr(), _dt(k), T, Hkv, D, kst[0], kst[1], vst[0], vst[1], slots.data_ptr(),
+                     kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, page)
+    _check((_lib or load()).bs_kv_append(ctypes.byref(a), _stream(stream)))
+
+
+def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_scale: float | None = None, out=None,
+                 lse=None, stream=None):
+    """Causal attention of new tokens q bf16 [T, Hq, D] over the 8-bit cache
+    (their own keys and values appended first).  ``lse`` (fp32 [T, Hq], natural
+    log) is filled if given.  Returns out bf16 [T, Hq, D]."""
+    kc, vc, ks, vs, (pages, Hkv, page, D) = _check_kv_cache(cache)
+    T, Hq = q.shape[0], q.shape[1]
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
+        raise TypeError("kv_attention: q and out are bfloat16")
+    if q.shape[2] != D or out.shape != q.shape or q.stride(2) != 1 or out.stride(2) != 1:
+        raise ValueError(f"kv_attention: q and out are [T, Hq, {D}] with contiguous rows")
+    B = kv_lens.shape[0]
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.stride(1) != 1:
+        raise TypeError("kv_attention: block_table is an int32 [B, max_pages] tensor with contiguous rows")
+    if cu_q.shape[0] != B + 1 or block_table.shape[0] != B:
+        raise ValueError("kv_attention: cu_q is [B + 1], kv_lens [B] and block_table [B, max_pages]")
+    _ints("kv_attention", cu_q, kv_lens)
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous()):
+        raise ValueError("kv_attention: lse is a contiguous float32 [T, Hq] tensor")
+    qst, ost = q.stride(), out.stride()
+    a = KvAttentionArgs(q.data_ptr(), qst[0], qst[1], out.data_ptr(), ost[0], ost[1],
+                        None if lse is None else lse.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(),
+                        vs.data_ptr(), pages, page, block_table.data_ptr(), block_table.stride(0),
+                        block_table.shape[1], cu_q.data_ptr(), kv_lens.data_ptr(), B, T, Hq, Hkv, D, max_q_len,
+                        D ** -0.5 if softmax_scale is None else softmax_scale)
+    opts = getattr(_tls, "opts", None)
+    if opts:
+        a.wait_timeout_us = opts.get("wait_timeout_us", 0)
+    lib = _lib or load()
+    nbytes = int(lib.bs_kv_attention_workspace_bytes(ctypes.byref(a)))
+    if nbytes:
+        ws = _workspace(q.device, stream if stream is not None else torch.cuda.current_stream(q.device), nbytes)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+    _check(lib.bs_kv_attention(ctypes.byref(a), _stream(stream)))
+    return out
+
+
+def matvec_fp4(x, codes, sf, out_dtype=torch.bfloat16, alpha: float = 1.0, bias=None, tensor_scale=None, out=None,
+               stream=None):
+    """x [M <= 16, K] bf16 times FP4 weights (codes [N, K/2] and MMA-layout
+    scales from q4_quantize, with ``tensor_scale`` of q4_quantize_two_level):
+    Y = alpha tensor_scale x W^T + bias, x left unquantized."""
+    M, K = x.shape
+    N = codes.shape[0]
+    if x.dtype != torch.bfloat16 or x.stride(1) != 1:
+        raise TypeError("matvec_fp4: x is a bfloat16 [M, K] tensor with contiguous rows")
+    if codes.dtype != torch.uint8 or codes.shape[1] * 2 != K or not codes.is_contiguous():
+        raise ValueError(f"matvec_fp4: codes are contiguous uint8 [N, {K // 2}]")
+    if sf.numel() < (N + 127) // 128 * 128 * (K // 16):
+        raise ValueError("matvec_fp4: sf holds fewer scales than bs_sf_bytes(N, K)")
+    if bias is not None and (bias.dtype != torch.bfloat16 or bias.numel() != N or not bias.is_contiguous()):
+        raise ValueError("matvec_fp4: bias is a contiguous bfloat16 [N] tensor")
+    if tensor_scale is not None and tensor_scale.dtype != torch.float32:
+        raise TypeError("matvec_fp4: tensor_scale is a float32 tensor")
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    elif out.shape != (M, N) or out.stride(1) != 1:
+        raise ValueError(f"matvec_fp4: out is [{M}, {N}] with contiguous rows")
+    _check((_lib or load()).bs_fp4_matvec(
+        x.data_ptr(), x.stride(0), M, codes.data_ptr(), sf.data_ptr(), N, K, alpha,
+        None if tensor_scale is None else tensor_scale.data_ptr(), None if bias is None else bias.data_ptr(),
+        out.data_ptr(), _dt(out), out.stride(0), _stream(stream)))
     return out
 
 

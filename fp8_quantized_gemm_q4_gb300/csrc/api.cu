@@ -160,7 +160,8 @@ const char* bs_status_string(bs_status s) {
     case BS_ERR_UNSUPPORTED: return "unsupported combination";
     case BS_ERR_CUDA: return "CUDA error";
     case BS_ERR_TIMEOUT: return "device pipeline wait timed out";
-    case BS_ERR_OFFSETS: return "inconsistent expert offsets or ids";
+    case BS_ERR_OFFSETS: return "inconsistent offsets, lengths or ids";
+    case BS_ERR_PAGES: return "too few free cache pages";
   }
   return "unknown status";
 }
@@ -1044,6 +1045,246 @@ bs_status bs_moe_finalize(float* out32, void* out_bf16, int64_t n, bs_stream_t s
   if (!device_info(nullptr, nullptr)) return fail(BS_ERR_CUDA, "no current device");
   cudaError_t e = bsk::launch_moe_finalize(out32, out_bf16, n, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "finalize launch");
+  return BS_OK;
+}
+
+// Page sizes of the KV cache: log2, or -1.
+static int kv_page_shift(int page_size) {
+  switch (page_size) {
+    case 16: return 4;
+    case 32: return 5;
+    case 64: return 6;
+    case 128: return 7;
+  }
+  return -1;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bs_status bs_kv_plan(const int32_t* seq_lens, const int32_t* new_lens, int B, int32_t* block_table, int64_t ld_table,
+                     int max_pages, const int32_t* free_pages, const int32_t* n_free, int free_capacity,
+                     int page_size, int64_t T, int32_t* cu_new, int32_t* kv_lens, int32_t* slots,
+                     int32_t* n_free_out, bs_stream_t stream) {
+  if (B < 0 || T < 0 || T > INT32_MAX || max_pages < 0 || free_capacity < 0)
+    return fail(BS_ERR_INVALID, "kv_plan: B=%d T=%lld max_pages=%d free_capacity=%d", B, (long long)T, max_pages,
+                free_capacity);
+  if (B > bsk::kKvPlanMaxB) return fail(BS_ERR_UNSUPPORTED, "kv_plan: B=%d above %d", B, bsk::kKvPlanMaxB);
+  bsk::KvPlanParams p = {};
+  p.page_shift = kv_page_shift(page_size);
+  if (p.page_shift < 0) return fail(BS_ERR_UNSUPPORTED, "kv_plan: page_size=%d not 16, 32, 64 or 128", page_size);
+  if (!cu_new || !n_free || !n_free_out || (B > 0 && (!seq_lens || !new_lens || !kv_lens)) || (T > 0 && !slots) ||
+      (B > 0 && max_pages > 0 && !block_table) || (free_capacity > 0 && !free_pages))
+    return fail(BS_ERR_INVALID, "kv_plan: null pointer");
+  if (ld_table < max_pages) return fail(BS_ERR_INVALID, "kv_plan: ld_table=%lld below max_pages", (long long)ld_table);
+  if ((int64_t)max_pages * page_size > INT32_MAX)
+    return fail(BS_ERR_INVALID, "kv_plan: max_pages=%d pages of %d tokens pass 2^31", max_pages, page_size);
+  if (n_free_out == n_free || kv_lens == seq_lens || kv_lens == new_lens)
+    return fail(BS_ERR_INVALID, "kv_plan: n_free_out / kv_lens must not be an input buffer");
+  if (!aligned4(seq_lens) || !aligned4(new_lens) || !aligned4(block_table) || !aligned4(free_pages) ||
+      !aligned4(n_free) || !aligned4(cu_new) || !aligned4(kv_lens) || !aligned4(slots) || !aligned4(n_free_out))
+    return fail(BS_ERR_ALIGN, "kv_plan: buffers must be 4-byte aligned");
+  if (!device_info(&p.status, nullptr)) return fail(BS_ERR_CUDA, "no current device");
+  p.seq_lens = seq_lens;
+  p.new_lens = new_lens;
+  p.B = B;
+  p.table = block_table;
+  p.ld_table = ld_table;
+  p.max_pages = max_pages;
+  p.free_pages = free_pages;
+  p.n_free = n_free;
+  p.capacity = free_capacity;
+  p.T = (int)T;
+  p.cu_new = cu_new;
+  p.kv_lens = kv_lens;
+  p.slots = slots;
+  p.n_free_out = n_free_out;
+  cudaError_t e = bsk::launch_kv_plan(p, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_plan launch");
+  return BS_OK;
+}
+
+bs_status bs_kv_release(const int32_t* lens, const int32_t* done, int B, int32_t* block_table, int64_t ld_table,
+                        int max_pages, int32_t* free_pages, int32_t* n_free, int free_capacity, int page_size,
+                        bs_stream_t stream) {
+  if (B < 0 || max_pages < 0 || free_capacity < 0)
+    return fail(BS_ERR_INVALID, "kv_release: B=%d max_pages=%d free_capacity=%d", B, max_pages, free_capacity);
+  if (B > bsk::kKvPlanMaxB) return fail(BS_ERR_UNSUPPORTED, "kv_release: B=%d above %d", B, bsk::kKvPlanMaxB);
+  bsk::KvReleaseParams p = {};
+  p.page_shift = kv_page_shift(page_size);
+  if (p.page_shift < 0) return fail(BS_ERR_UNSUPPORTED, "kv_release: page_size=%d not 16, 32, 64 or 128", page_size);
+  if (B == 0 || max_pages == 0) return BS_OK;
+  if (!lens || !done || !block_table || !n_free || (free_capacity > 0 && !free_pages))
+    return fail(BS_ERR_INVALID, "kv_release: null pointer");
+  if (ld_table < max_pages) return fail(BS_ERR_INVALID, "kv_release: ld_table=%lld below max_pages", (long long)ld_table);
+  if (!aligned4(lens) || !aligned4(done) || !aligned4(block_table) || !aligned4(free_pages) || !aligned4(n_free))
+    return fail(BS_ERR_ALIGN, "kv_release: buffers must be 4-byte aligned");
+  if (!device_info(&p.status, nullptr)) return fail(BS_ERR_CUDA, "no current device");
+  p.lens = lens;
+  p.done = done;
+  p.B = B;
+  p.table = block_table;
+  p.ld_table = ld_table;
+  p.max_pages = max_pages;
+  p.free_pages = free_pages;
+  p.n_free = n_free;
+  p.capacity = free_capacity;
+  cudaError_t e = bsk::launch_kv_release(p, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_release launch");
+  return BS_OK;
+}
+
+// Cache geometry shared by append and attention.
+static bs_status check_kv_cache(const char* what, int Hkv, int D, int64_t num_pages, int page_size) {
+  if (Hkv <= 0 || num_pages < 0)
+    return fail(BS_ERR_INVALID, "%s: Hkv=%d num_pages=%lld", what, Hkv, (long long)num_pages);
+  if (D != 64 && D != 128) return fail(BS_ERR_UNSUPPORTED, "%s: D=%d not 64 or 128", what, D);
+  if (kv_page_shift(page_size) < 0)
+    return fail(BS_ERR_UNSUPPORTED, "%s: page_size=%d not 16, 32, 64 or 128", what, page_size);
+  // slots and cache rows (page, head, token) are 32-bit
+  if (num_pages > INT32_MAX / ((int64_t)Hkv * page_size))
+    return fail(BS_ERR_UNSUPPORTED, "%s: %lld pages of %d heads x %d tokens pass 2^31 rows", what, (long long)num_pages,
+                Hkv, page_size);
+  return BS_OK;
+}
+
+bs_status bs_kv_append(const bs_kv_append_args* a, bs_stream_t stream) {
+  if (!a) return fail(BS_ERR_INVALID, "kv_append: null arguments");
+  bs_status st = check_kv_cache("kv_append", a->Hkv, a->D, a->num_pages, a->page_size);
+  if (st != BS_OK) return st;
+  if (a->T < 0 || a->T > INT32_MAX) return fail(BS_ERR_INVALID, "kv_append: T=%lld", (long long)a->T);
+  if (a->dtype != BS_DTYPE_F32 && a->dtype != BS_DTYPE_BF16)
+    return fail(BS_ERR_INVALID, "kv_append: dtype %d", a->dtype);
+  if (2 * (int64_t)a->Hkv > 65535) return fail(BS_ERR_UNSUPPORTED, "kv_append: Hkv=%d", a->Hkv);
+  if (a->T == 0) return BS_OK;
+  if (!a->k || !a->v || !a->slots || !a->k_codes || !a->v_codes || !a->k_scales || !a->v_scales)
+    return fail(BS_ERR_INVALID, "kv_append: null pointer");
+  int64_t strides = 0;  // those of an axis of length 1 mean nothing
+  if (a->T > 1) strides |= a->k_token_stride | a->v_token_stride;
+  if (a->Hkv > 1) strides |= a->k_head_stride | a->v_head_stride;
+  if (strides % 8 || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->k_codes) || !aligned16(a->v_codes) ||
+      !aligned4(a->k_scales) || !aligned4(a->v_scales) || !aligned4(a->slots))
+    return fail(BS_ERR_ALIGN, "kv_append: k, v and codes must be 16-byte aligned, strides multiples of 8 elements");
+  bsk::KvAppendParams p = {};
+  if (!device_info(&p.status, nullptr)) return fail(BS_ERR_CUDA, "no current device");
+  p.x[0] = a->k;
+  p.x[1] = a->v;
+  p.tok_stride[0] = a->k_token_stride;
+  p.tok_stride[1] = a->v_token_stride;
+  p.head_stride[0] = a->k_head_stride;
+  p.head_stride[1] = a->v_head_stride;
+  p.codes[0] = a->k_codes;
+  p.codes[1] = a->v_codes;
+  p.scales[0] = a->k_scales;
+  p.scales[1] = a->v_scales;
+  p.slots = a->slots;
+  p.T = (int)a->T;
+  p.Hkv = a->Hkv;
+  p.D = a->D;
+  p.num_pages = (int)a->num_pages;
+  p.page_shift = kv_page_shift(a->page_size);
+  p.x_bf16 = a->dtype == BS_DTYPE_BF16;
+  cudaError_t e = bsk::launch_kv_append(p, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
+  return BS_OK;
+}
+
+size_t bs_kv_attention_workspace_bytes(const bs_kv_attention_args* a) {
+  (void)a;
+  return 0;
+}
+
+bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
+  if (!a) return fail(BS_ERR_INVALID, "kv_attention: null arguments");
+  bs_status st = check_kv_cache("kv_attention", a->Hkv, a->D, a->num_pages, a->page_size);
+  if (st != BS_OK) return st;
+  if (a->T < 0 || a->T > INT32_MAX || a->B < 0 || a->max_q_len < 0 || a->max_pages < 0)
+    return fail(BS_ERR_INVALID, "kv_attention: T=%lld B=%d max_q_len=%d max_pages=%d", (long long)a->T, a->B,
+                a->max_q_len, a->max_pages);
+  if (a->Hq <= 0 || a->Hq % a->Hkv) return fail(BS_ERR_INVALID, "kv_attention: Hq=%d not a multiple of Hkv=%d", a->Hq, a->Hkv);
+  if (a->Hq > 65535) return fail(BS_ERR_UNSUPPORTED, "kv_attention: Hq=%d", a->Hq);
+  if (!(a->softmax_scale > 0.0f)) return fail(BS_ERR_INVALID, "kv_attention: softmax_scale=%g", (double)a->softmax_scale);
+  if (a->wait_timeout_us < 0) return fail(BS_ERR_INVALID, "kv_attention: wait_timeout_us=%d", a->wait_timeout_us);
+  if (a->ld_table < a->max_pages) return fail(BS_ERR_INVALID, "kv_attention: ld_table=%lld below max_pages", (long long)a->ld_table);
+  if ((int64_t)a->max_pages * a->page_size > INT32_MAX)
+    return fail(BS_ERR_INVALID, "kv_attention: max_pages=%d pages of %d tokens pass 2^31", a->max_pages, a->page_size);
+  if (a->T == 0 || a->B == 0) return BS_OK;
+  if (!a->q || !a->out || !a->cu_q || !a->kv_lens || (a->max_pages > 0 && !a->block_table) ||
+      (a->num_pages > 0 && (!a->k_codes || !a->v_codes || !a->k_scales || !a->v_scales)))
+    return fail(BS_ERR_INVALID, "kv_attention: null pointer");
+  int64_t strides = 0;  // those of an axis of length 1 mean nothing
+  if (a->T > 1) strides |= a->q_token_stride | a->out_token_stride;
+  if (a->Hq > 1) strides |= a->q_head_stride | a->out_head_stride;
+  if (strides % 8 || !aligned16(a->q) ||
+      !aligned16(a->out) || !aligned16(a->k_codes) || !aligned16(a->v_codes) || !aligned4(a->k_scales) ||
+      !aligned4(a->v_scales) || !aligned4(a->block_table) || !aligned4(a->cu_q) || !aligned4(a->kv_lens) ||
+      !aligned4(a->lse))
+    return fail(BS_ERR_ALIGN, "kv_attention: q, out and codes must be 16-byte aligned, strides multiples of 8 elements");
+  bsk::KvAttentionLaunch L = {};
+  bsk::KvAttentionParams& p = L.p;
+  if (!device_info(&p.status, nullptr)) return fail(BS_ERR_CUDA, "no current device");
+  p.q = a->q;
+  p.q_tok_stride = a->q_token_stride;
+  p.q_head_stride = a->q_head_stride;
+  p.out = a->out;
+  p.out_tok_stride = a->out_token_stride;
+  p.out_head_stride = a->out_head_stride;
+  p.lse = a->lse;
+  p.k_codes = a->k_codes;
+  p.v_codes = a->v_codes;
+  p.k_scales = a->k_scales;
+  p.v_scales = a->v_scales;
+  p.table = a->block_table;
+  p.ld_table = a->ld_table;
+  p.max_pages = a->max_pages;
+  p.cu_q = a->cu_q;
+  p.kv_lens = a->kv_lens;
+  p.B = a->B;
+  p.T = (int)a->T;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  p.D = a->D;
+  p.num_pages = (int)a->num_pages;
+  p.page_shift = kv_page_shift(a->page_size);
+  p.scale_log2 = a->softmax_scale * 1.4426950408889634f;
+  cudaError_t e = bsk::launch_kv_attention(L, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_attention launch");
+  return BS_OK;
+}
+
+bs_status bs_fp4_matvec(const void* x, int64_t ldx, int M, const uint8_t* codes, const uint8_t* sf, int64_t N, int64_t K,
+                        float alpha, const float* tensor_scale, const void* bias, void* out, int out_dtype, int64_t ldo,
+                        bs_stream_t stream) {
+  if (M < 0 || N < 0 || K <= 0 || N > INT32_MAX || K > INT32_MAX)
+    return fail(BS_ERR_INVALID, "fp4_matvec: M=%d N=%lld K=%lld", M, (long long)N, (long long)K);
+  if (out_dtype != BS_DTYPE_F32 && out_dtype != BS_DTYPE_BF16)
+    return fail(BS_ERR_INVALID, "fp4_matvec: out_dtype %d", out_dtype);
+  if (M > 16) return fail(BS_ERR_UNSUPPORTED, "fp4_matvec: M=%d above 16 (bs_gemm takes more rows)", M);
+  if (K % 64) return fail(BS_ERR_ALIGN, "fp4_matvec: K=%lld not a multiple of 64", (long long)K);
+  if (M == 0 || N == 0) return BS_OK;
+  if (!x || !codes || !sf || !out) return fail(BS_ERR_INVALID, "fp4_matvec: null pointer");
+  if (ldx < K || ldo < N) return fail(BS_ERR_INVALID, "fp4_matvec: ldx=%lld / ldo=%lld below K / N", (long long)ldx, (long long)ldo);
+  const uintptr_t out_mask = out_dtype == BS_DTYPE_BF16 ? 1 : 3;
+  if (ldx % 8 || !aligned16(x) || !aligned16(codes) || !aligned16(sf) || (reinterpret_cast<uintptr_t>(out) & out_mask) ||
+      (reinterpret_cast<uintptr_t>(bias) & 1) || !aligned4(tensor_scale))
+    return fail(BS_ERR_ALIGN, "fp4_matvec: x, codes and sf must be 16-byte aligned and ldx %% 8 == 0");
+  int sms = 0;
+  if (!device_info(nullptr, &sms)) return fail(BS_ERR_CUDA, "no current device");
+  bsk::Fp4MatvecParams p = {};
+  p.x = x;
+  p.ldx = ldx;
+  p.codes = codes;
+  p.sf = sf;
+  p.M = M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.alpha = alpha;
+  p.tensor_scale = tensor_scale;
+  p.bias = bias;
+  p.out = out;
+  p.out_bf16 = out_dtype == BS_DTYPE_BF16;
+  p.ldo = ldo;
+  cudaError_t e = bsk::launch_fp4_matvec(p, sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "fp4_matvec launch");
   return BS_OK;
 }
 

@@ -256,6 +256,96 @@ cudaError_t launch_moe_combine(const float* rows, long long ld_rows, const int* 
                                long long T, int k, long long H, int* row_of_pair, void* out, long long ldo,
                                cudaStream_t stream);
 
+// Paged 8-bit cache (kv_cache.cu)
+constexpr int kKvPlanMaxB = 8192;
+struct KvPlanParams {
+  const int* seq_lens;    // [B] tokens cached so far
+  const int* new_lens;    // [B] tokens of this step
+  int B;
+  int* table;             // [B, ld_table] page ids
+  long long ld_table;
+  int max_pages;          // usable entries of a table row
+  const int* free_pages;  // [capacity]
+  const int* n_free;      // device scalar
+  int capacity;
+  int page_shift;         // log2(page_size)
+  int T;                  // entries of slots
+  int* cu_new;            // [B + 1]
+  int* kv_lens;           // [B]
+  int* slots;             // [T]
+  int* n_free_out;
+  int* status;
+};
+cudaError_t launch_kv_plan(const KvPlanParams& p, cudaStream_t stream);
+struct KvReleaseParams {
+  const int* lens;        // [B]
+  const int* done;        // [B]: nonzero = give the pages back
+  int B;
+  int* table;
+  long long ld_table;
+  int max_pages;
+  int* free_pages;
+  int* n_free;
+  int capacity;
+  int page_shift;
+  int* status;
+};
+cudaError_t launch_kv_release(const KvReleaseParams& p, cudaStream_t stream);
+struct KvAppendParams {
+  const void* x[2];       // keys, values
+  long long tok_stride[2], head_stride[2];  // elements
+  uint8_t* codes[2];      // [pages, Hkv, page, D]
+  float* scales[2];       // [pages, Hkv]
+  const int* slots;       // [T]
+  int T, Hkv, D;
+  int num_pages, page_shift;
+  int x_bf16;
+  int* status;
+};
+cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream);
+
+// Attention over the paged 8-bit cache (kv_attention.cu)
+struct KvAttentionParams {
+  const void* q;          // bf16 [T, Hq, D]
+  long long q_tok_stride, q_head_stride;
+  void* out;              // bf16 [T, Hq, D]
+  long long out_tok_stride, out_head_stride;
+  float* lse;             // [T, Hq] or null
+  const uint8_t* k_codes;
+  const uint8_t* v_codes;
+  const float* k_scales;
+  const float* v_scales;
+  const int* table;       // [B, ld_table]
+  long long ld_table;
+  int max_pages;
+  const int* cu_q;        // [B + 1]
+  const int* kv_lens;     // [B]
+  int B, T, Hq, Hkv, D;
+  int num_pages, page_shift;
+  float scale_log2;       // softmax scale * log2(e)
+  int* status;
+};
+struct KvAttentionLaunch {
+  KvAttentionParams p;
+};
+cudaError_t launch_kv_attention(const KvAttentionLaunch& L, cudaStream_t stream);
+
+// Few bf16 rows times FP4 weights (matvec_fp4.cu)
+struct Fp4MatvecParams {
+  const void* x;          // bf16 [M, ldx]
+  long long ldx;
+  const uint8_t* codes;   // [N, K/2]
+  const uint8_t* sf;      // MMA layout for [N, K]
+  int M, N, K;
+  float alpha;
+  const float* tensor_scale;  // device fp32 or null
+  const void* bias;       // bf16 [N] or null
+  void* out;
+  int out_bf16;
+  long long ldo;
+};
+cudaError_t launch_fp4_matvec(const Fp4MatvecParams& p, int sms, cudaStream_t stream);
+
 // Unique id of the CUDA context current on this thread (0 if none); keys the
 // caches of device addresses of the library's __device__ variables.
 unsigned long long current_context_id();

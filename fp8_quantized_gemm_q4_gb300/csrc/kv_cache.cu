@@ -1,0 +1,333 @@
+// kv_cache.cu -- the pages of the 8-bit KV cache: block tables and slots from
+// request lengths (kv_plan), pages given back (kv_release), and new keys and
+// values quantized into their slots (kv_append).
+//
+// Pages hold 2^page_shift tokens.  Codes are e4m3 [page][KV head][token][D],
+// one fp32 power-of-two scale per (page, KV head).
+#include <limits.h>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace bsk {
+
+// ---------------------------------------------------------------------------
+// kv_plan: with before = ceil(seq / page), after = ceil((seq + new) / page),
+// need = after - before and end = inclusive sum of need over the requests,
+// request b takes the entries n_free - 1 - (end_b - need_b) - j, j < need_b, of
+// the free list; it fits if need_b == 0 or end_b <= n_free.  Every CTA scans
+// all lengths (a few kB from L2) and then handles its own rows of the slot
+// map and its own share of the taken pages, so one launch does and nothing
+// waits on another CTA: slots read the table only below `before`, the table is
+// written only from `before` on.
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+
+// First index with v[i] > x, in the ascending v[0, n).
+__device__ __forceinline__ int upper_bound(const int* v, int n, int x) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (v[mid] > x)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+// Block-wide inclusive scan of (a, b); the sums over the block are returned
+// in ta, tb.  All threads of the block call it.
+__device__ __forceinline__ void block_scan2(long long& a, long long& b, long long& ta, long long& tb) {
+  __shared__ long long wa[32], wb[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long va = __shfl_up_sync(kFullMask, a, d), vb = __shfl_up_sync(kFullMask, b, d);
+    if (lane >= d) a += va, b += vb;
+  }
+  __syncthreads();  // the sums of an earlier call have been read
+  if (lane == 31) wa[warp] = a, wb[warp] = b;
+  __syncthreads();
+  long long sa = lane < warps ? wa[lane] : 0, sb = lane < warps ? wb[lane] : 0;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long va = __shfl_up_sync(kFullMask, sa, d), vb = __shfl_up_sync(kFullMask, sb, d);
+    if (lane >= d) sa += va, sb += vb;
+  }
+  ta = __shfl_sync(kFullMask, sa, 31);
+  tb = __shfl_sync(kFullMask, sb, 31);
+  const long long pa = __shfl_sync(kFullMask, sa, warp ? warp - 1 : 0);
+  const long long pb = __shfl_sync(kFullMask, sb, warp ? warp - 1 : 0);
+  if (warp) a += pa, b += pb;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_constant__ KvPlanParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  extern __shared__ int sm[];
+  int* cu = sm;                // [B + 1] rows before each request
+  int* ends = cu + p.B + 1;    // [B]
+  int* seqs = ends + p.B;      // [B], -1: lengths that break the contract
+  const int tid = threadIdx.x, page = 1 << p.page_shift;
+  const int n_free = min(max(*p.n_free, 0), p.capacity);
+  long long new_sum = 0, need_sum = 0;
+  if (tid == 0) cu[0] = 0;
+  for (int base = 0; base < p.B; base += kPlanThreads) {
+    const int b = base + tid;
+    long long added = 0, need = 0;
+    if (b < p.B) {
+      int seq = p.seq_lens[b];
+      added = max(p.new_lens[b], 0);
+      const long long last = (long long)seq + added;
+      if (seq < 0 || p.new_lens[b] < 0 || last > ((long long)p.max_pages << p.page_shift)) seq = -1;
+      if (seq >= 0) need = ((last + page - 1) >> p.page_shift) - (((long long)seq + page - 1) >> p.page_shift);
+      seqs[b] = seq;
+    }
+    long long new_block, need_block;
+    block_scan2(added, need, new_block, need_block);
+    if (b < p.B) {
+      cu[b + 1] = (int)min(new_sum + added, (long long)INT_MAX);
+      ends[b] = (int)min(need_sum + need, (long long)INT_MAX);
+    }
+    new_sum += new_block;
+    need_sum += need_block;
+  }
+  __syncthreads();
+  const int total = p.B ? ends[p.B - 1] : 0;
+  const int rows = cu[p.B];
+
+  if (blockIdx.x == 0) {
+    for (int b = tid; b <= p.B; b += kPlanThreads) p.cu_new[b] = cu[b];
+    for (int b = tid; b < p.B; b += kPlanThreads) {
+      const bool fits = ends[b] <= n_free || ends[b] == (b ? ends[b - 1] : 0);
+      const int seq = seqs[b];
+      p.kv_lens[b] = seq >= 0 && fits ? seq + cu[b + 1] - cu[b] : 0;
+      if (seq < 0) record_status(p.status, kStatusOffsets, 40);
+      if (!fits) record_status(p.status, kStatusPages, 41);
+    }
+    if (tid == 0) {
+      const int u = upper_bound(ends, p.B, n_free);
+      *p.n_free_out = n_free - (u ? ends[u - 1] : 0);
+      if (new_sum > p.T) record_status(p.status, kStatusOffsets, 42);
+    }
+  }
+
+  const long long first = (long long)blockIdx.x * kPlanThreads + tid, step = (long long)gridDim.x * kPlanThreads;
+  for (long long r = first; r < p.T; r += step) {
+    int slot = -1;
+    if (r < rows) {
+      const int b = upper_bound(cu + 1, p.B, (int)r);
+      const int seq = seqs[b], end0 = b ? ends[b - 1] : 0;
+      if (seq >= 0 && (ends[b] <= n_free || ends[b] == end0)) {
+        const int pos = seq + ((int)r - cu[b]);
+        const int j = pos >> p.page_shift, before = (int)(((long long)seq + page - 1) >> p.page_shift);
+        const long long id = j < before ? p.table[b * p.ld_table + j] : p.free_pages[n_free - 1 - end0 - (j - before)];
+        const long long at = (id << p.page_shift) + (pos & (page - 1));
+        if (id >= 0 && at <= INT_MAX) slot = (int)at;
+      }
+    }
+    p.slots[r] = slot;
+  }
+  for (long long e = first; e < min(total, n_free); e += step) {
+    const int b = upper_bound(ends, p.B, (int)e);
+    if (ends[b] > n_free) break;  // ends ascend: the later ones do not fit either
+    const int end0 = b ? ends[b - 1] : 0;
+    const int before = (int)(((long long)seqs[b] + page - 1) >> p.page_shift);
+    p.table[b * p.ld_table + before + ((int)e - end0)] = p.free_pages[n_free - 1 - (int)e];
+  }
+}
+
+cudaError_t launch_kv_plan(const KvPlanParams& p, cudaStream_t stream) {
+  const size_t smem = (size_t)(3 * p.B + 1) * sizeof(int);
+  static const cudaError_t attr = cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       (3 * kKvPlanMaxB + 1) * (int)sizeof(int));
+  if (attr != cudaSuccess) return attr;
+  const long long ctas = ((long long)p.T + kPlanThreads - 1) / kPlanThreads;
+  const unsigned grid = (unsigned)(ctas < 1 ? 1 : ctas > 148 ? 148 : ctas);
+  return launch_kernel(kv_plan_kernel, grid, kPlanThreads, smem, stream, 1, p);
+}
+
+// ---------------------------------------------------------------------------
+// kv_release: the pages of finished requests go back on the end of the free
+// list, in request order; their table entries become -1.  One CTA.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kPlanThreads) kv_release_kernel(const __grid_constant__ KvReleaseParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  extern __shared__ int ends[];  // [B]
+  const int tid = threadIdx.x, page = 1 << p.page_shift;
+  const int n_free = min(max(*p.n_free, 0), p.capacity);
+  long long sum = 0;
+  for (int base = 0; base < p.B; base += kPlanThreads) {
+    const int b = base + tid;
+    long long n = 0, unused = 0, block, unused_block;
+    if (b < p.B && p.done[b]) {
+      n = ((long long)p.lens[b] + page - 1) >> p.page_shift;
+      if (n < 0 || n > p.max_pages) {
+        record_status(p.status, kStatusOffsets, 43);
+        n = 0;
+      }
+    }
+    block_scan2(n, unused, block, unused_block);
+    if (b < p.B) ends[b] = (int)min(sum + n, (long long)INT_MAX);
+    sum += block;
+  }
+  __syncthreads();
+  const int room = p.capacity - n_free;
+  const int total = (int)min(sum, (long long)room);
+  for (int e = tid; e < total; e += kPlanThreads) {
+    const int b = upper_bound(ends, p.B, e);
+    int* entry = p.table + b * p.ld_table + (e - (b ? ends[b - 1] : 0));
+    p.free_pages[n_free + e] = *entry;
+    *entry = -1;
+  }
+  if (tid == 0) {
+    *p.n_free = n_free + total;
+    if (sum > room) record_status(p.status, kStatusPages, 44);
+  }
+}
+
+cudaError_t launch_kv_release(const KvReleaseParams& p, cudaStream_t stream) {
+  return launch_kernel(kv_release_kernel, 1, kPlanThreads, (size_t)p.B * sizeof(int), stream, 1, p);
+}
+
+// ---------------------------------------------------------------------------
+// kv_append.  The rows of a call that lie in one page follow one another with
+// ascending slots (a run).  A run's scale is the smallest power of two s, in
+// [2^-32, 2^64], with amax <= 448 s; a run that does not begin its page takes
+// the larger of that and the page's scale, and where the scale grows the
+// page's earlier codes are rounded again to it.  Powers of two: a quotient by
+// one is exact, and re-rounding changes only codes that fall among e4m3's
+// subnormals.
+// ---------------------------------------------------------------------------
+constexpr int kAppendWarps = 4;
+
+// log2 of the scale for this amax (>= 0)
+__device__ __forceinline__ int scale_exp(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  // amax = 1.m * 2^x; 448 = 1.75 * 2^8, so the smallest e with
+  // amax <= 1.75 * 2^(e + 8) is x - 8, or x - 7 where 1.m > 1.75
+  const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return min(max(e, -32), 64);
+}
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Eight elements of a row as floats
+template <bool kBf16>
+__device__ __forceinline__ void load8(const void* x, long long at, float (&v)[8]) {
+  if constexpr (kBf16) {
+    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) + at);
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+    }
+  } else {
+    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
+    const float4 a = f[0], b = f[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+}
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = f32x2_to_e4m3x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+template <bool kBf16, int D>
+__global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes a row, rows a pass
+  const int lane = threadIdx.x & 31, row = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  const int h = blockIdx.y >> 1, which = blockIdx.y & 1;
+  if (row >= p.T) return;
+  const int page = 1 << p.page_shift;
+  const int slot = p.slots[row];
+  if (slot < 0) return;
+  const int id = slot >> p.page_shift, off = slot & (page - 1);
+  if (id >= p.num_pages) {
+    if (lane == 0) record_status(p.status, kStatusOffsets, 45);
+    return;
+  }
+  if (row > 0 && off > 0 && p.slots[row - 1] == slot - 1) return;  // inside a run
+  // the run's length: slots ascend by one up to the page's end
+  int n = 1;
+  for (; n < page - off && row + n < p.T; n += 32) {
+    const int i = n + lane;
+    const bool in = i < page - off && row + i < p.T && p.slots[row + i] == slot + i;
+    const unsigned m = __ballot_sync(kFullMask, in);
+    if (m != kFullMask) {
+      n += __ffs(~m) - 1;
+      break;
+    }
+  }
+  n = min(n, page - off);
+  const void* x = p.x[which];
+  const long long ts = p.tok_stride[which];
+  const long long x0 = row * ts + h * p.head_stride[which] + (lane % kLanes) * 8;
+  float amax = 0.0f;
+  for (int r = lane / kLanes; r < n; r += kRows) {
+    float v[8];
+    load8<kBf16>(x, x0 + r * ts, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, d));
+  float s = exp2_int(scale_exp(amax));
+  float* scale = p.scales[which] + (long long)id * p.Hkv + h;
+  uint8_t* codes = p.codes[which] + (((long long)id * p.Hkv + h) << p.page_shift) * D + (lane % kLanes) * 8;
+  if (off > 0) {
+    const float old = *scale;
+    if (s > old) {
+      const float ratio = old / s;
+      for (int r = lane / kLanes; r < off; r += kRows) {
+        uint2* at = reinterpret_cast<uint2*>(codes + r * D);
+        const uint2 w = *at;
+        const uint32_t in[2] = {w.x, w.y};
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)(in[i >> 1] >> (16 * (i & 1))));
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+          v[2 * i] = f.x, v[2 * i + 1] = f.y;
+        }
+        *at = codes8(v, ratio);
+      }
+    }
+    s = fmaxf(s, old);
+  }
+  const float inv = 1.0f / s;
+  for (int r = lane / kLanes; r < n; r += kRows) {
+    float v[8];
+    load8<kBf16>(x, x0 + r * ts, v);
+    *reinterpret_cast<uint2*>(codes + (off + r) * D) = codes8(v, inv);
+  }
+  __syncwarp();
+  if (lane == 0) *scale = s;
+}
+
+template <bool kBf16>
+static cudaError_t launch_append(const KvAppendParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.T + kAppendWarps - 1) / kAppendWarps), (unsigned)(2 * p.Hkv), 1);
+  cfg.blockDim = dim3(kAppendWarps * 32, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return p.D == 64 ? cudaLaunchKernelEx(&cfg, kv_append_kernel<kBf16, 64>, p)
+                   : cudaLaunchKernelEx(&cfg, kv_append_kernel<kBf16, 128>, p);
+}
+
+cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream) {
+  return p.x_bf16 ? launch_append<true>(p, stream) : launch_append<false>(p, stream);
+}
+
+}  // namespace bsk

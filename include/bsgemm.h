@@ -47,7 +47,9 @@ typedef enum {
     BS_ERR_UNSUPPORTED = 3, /* valid request this library does not implement */
     BS_ERR_CUDA = 4,        /* a CUDA runtime call failed (launch, attribute, tensor-map encode) */
     BS_ERR_TIMEOUT = 5,     /* device status: a bounded pipeline wait gave up */
-    BS_ERR_OFFSETS = 6      /* device status: expert offsets / counts inconsistent */
+    BS_ERR_OFFSETS = 6,     /* device status: expert offsets / counts, request lengths, slots or page
+                               ids inconsistent */
+    BS_ERR_PAGES = 7        /* device status: a request did not fit in the free cache pages */
 } bs_status;
 
 typedef enum { BS_DTYPE_F32 = 0, BS_DTYPE_BF16 = 1 } bs_dtype;
@@ -517,10 +519,161 @@ bs_status bs_moe_combine(const float *rows, int64_t ld_rows, const int32_t *pair
                          bs_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Serving step on an 8-bit paged KV cache.
+ *
+ * The cache of one layer is four caller-owned buffers:
+ *   k_codes, v_codes   e4m3 [num_pages, Hkv, page_size, D]
+ *   k_scales, v_scales fp32 [num_pages, Hkv], positive
+ * page_size is 16, 32, 64 or 128, D 64 or 128.  A code stands for
+ * code * scale[page, head].  A request's tokens lie, in order, in the pages
+ * that its block-table row lists; slot = page id * page_size + place in page.
+ *
+ * bs_kv_plan -- block tables and slots of a step, from request lengths.
+ * With before = ceil(seq / page_size), after = ceil((seq + new) / page_size),
+ * need = after - before and end_b = the sum of need over requests 0 .. b:
+ *   request b fits if need_b == 0 or end_b <= n_free; it then takes the
+ *   entries n_free - 1 - (end_b - need_b) - j, j = 0 .. need_b - 1, of
+ *   free_pages for its pages before_b + j.
+ *   cu_new[b]  = new_0 + .. + new_{b-1}   (cu_new[B]: all rows)
+ *   kv_lens[b] = seq_b + new_b, or 0 for a request that does not fit (its
+ *                rows then see nothing, and the sticky status becomes
+ *                BS_ERR_PAGES)
+ *   slots[r]   = the slot of row r = cu_new[b] + i, token seq_b + i of request
+ *                b; -1 for rows of requests that do not fit and rows from
+ *                cu_new[B] on
+ *   n_free_out = n_free minus the pages taken
+ *
+ *   seq_lens, new_lens  int32 [B], cached and new tokens, >= 0
+ *   B           0 .. 8192
+ *   block_table int32 [B, ld_table], max_pages usable entries a row; entries
+ *               below before_b are read, entries before_b .. after_b - 1 written
+ *   free_pages  int32 [free_capacity]; n_free device int32 (clamped to
+ *               [0, free_capacity])
+ *   T           entries of slots; cu_new[B] > T sets BS_ERR_OFFSETS
+ *   n_free_out, kv_lens must not be input buffers (BS_ERR_INVALID)
+ * Negative lengths, or more pages than max_pages, set BS_ERR_OFFSETS; such a
+ * request takes no pages and gets kv_lens 0 and slots -1.
+ *
+ * bs_kv_release -- the pages of finished requests (done[b] != 0; lens[b]
+ * tokens) are put on the end of free_pages, in request order, *n_free grows by
+ * their number, and their table entries become -1.  The caller then gives the
+ * request length 0.
+ * ------------------------------------------------------------------------- */
+bs_status bs_kv_plan(const int32_t *seq_lens, const int32_t *new_lens, int B, int32_t *block_table, int64_t ld_table,
+                     int max_pages, const int32_t *free_pages, const int32_t *n_free, int free_capacity,
+                     int page_size, int64_t T, int32_t *cu_new, int32_t *kv_lens, int32_t *slots,
+                     int32_t *n_free_out, bs_stream_t stream);
+bs_status bs_kv_release(const int32_t *lens, const int32_t *done, int B, int32_t *block_table, int64_t ld_table,
+                        int max_pages, int32_t *free_pages, int32_t *n_free, int free_capacity, int page_size,
+                        bs_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * bs_kv_append -- quantize new keys and values into their slots.
+ * The rows that go into one page follow one another with ascending slots (as
+ * bs_kv_plan gives them); amax is taken over those rows and D, per head, for
+ * keys and values apart:
+ *     s    = the smallest power of two in [2^-32, 2^64] with amax <= 448 s
+ *     if the first of the rows is not the page's first token: s = max(s, the
+ *     page's scale), and where s grew, the page's earlier codes become
+ *     e4m3_rn(code * old scale / s)
+ *     code = e4m3_rn_satfinite(x / s)
+ * Dividing by a power of two is exact, and growing a scale changes only codes
+ * that fall among e4m3's subnormals.
+ *
+ *   k, v       [T, Hkv, D] fp32 or bf16 (dtype) with strides in elements; D is
+ *              contiguous, strides are multiples of 8, pointers 16-byte aligned
+ *   slots      int32 [T]; a negative slot skips its row, one past the cache
+ *              does too and sets BS_ERR_OFFSETS
+ *   codes, scales as above; other tokens of the touched pages are left alone
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    const void *k, *v;
+    int dtype;               /* bs_dtype of k and v */
+    int64_t T;
+    int Hkv, D;
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    const int32_t *slots;
+    uint8_t *k_codes, *v_codes;
+    float *k_scales, *v_scales;
+    int64_t num_pages;
+    int page_size;
+} bs_kv_append_args;
+
+bs_status bs_kv_append(const bs_kv_append_args *args, bs_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * bs_kv_attention -- causal attention of the new tokens over the cache.
+ * Query head hq reads KV head hq / (Hq / Hkv).  Row i of request b, with
+ * n = cu_q[b+1] - cu_q[b] rows, sees the cached tokens
+ * 0 .. kv_lens[b] - n + i (append first: the new tokens are in the cache):
+ *     s_t = softmax_scale * q . K_t,  lse = log sum_t exp(s_t),
+ *     out = sum_t exp(s_t - lse) V_t
+ * A row that sees no token gets out 0 and lse -infinity.  Sums are fp32; the
+ * products take q scaled by a power of two per row as fp16 (exact for every
+ * element within 2^-29 of the row's largest) and the weights exp(s - max)
+ * rounded to fp16.
+ *
+ *   q, out     bf16 [T, Hq, D], strides in elements (multiples of 8), 16-byte
+ *              aligned, D contiguous
+ *   lse        fp32 [T, Hq] (natural log), or NULL
+ *   cu_q, kv_lens  int32 [B + 1] / [B]; cu_q[0] == 0, ascending, cu_q[B] <= T;
+ *              rows from cu_q[B] on are not written
+ *   max_q_len  an upper bound of the rows of a request (0: no bound known, T)
+ *   block_table int32 [B, ld_table]; an id outside [0, num_pages) on a seen
+ *              page sets BS_ERR_OFFSETS, the page is left out
+ *   softmax_scale > 0
+ *   workspace  device scratch of bs_kv_attention_workspace_bytes(args) bytes,
+ *              with the conventions of bs_gemm_args.workspace (one buffer may
+ *              serve both)
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    const void *q;
+    int64_t q_token_stride, q_head_stride;
+    void *out;
+    int64_t out_token_stride, out_head_stride;
+    float *lse;
+    const uint8_t *k_codes, *v_codes;
+    const float *k_scales, *v_scales;
+    int64_t num_pages;
+    int page_size;
+    const int32_t *block_table;
+    int64_t ld_table;
+    int max_pages;
+    const int32_t *cu_q, *kv_lens;
+    int B;
+    int64_t T;
+    int Hq, Hkv, D;
+    int max_q_len;
+    float softmax_scale;
+    int wait_timeout_us;     /* as in bs_gemm_args */
+    void *workspace;
+    size_t workspace_bytes;
+} bs_kv_attention_args;
+
+size_t bs_kv_attention_workspace_bytes(const bs_kv_attention_args *args);
+bs_status bs_kv_attention(const bs_kv_attention_args *args, bs_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * bs_fp4_matvec -- 1 to 16 bf16 rows times FP4 weights:
+ *     y[m, n] = alpha * tensor_scale * sum_k x[m, k] * e2m1[n, k] * sf[n, k/16] + bias[n]
+ * The weights are those of bs_gemm (codes [N, K/2] and MMA-layout scales from
+ * q4_quantize or q4_quantize_two_level), the activations stay bf16: no
+ * quantization of x, fp32 accumulation.
+ *
+ *   x       bf16 [M, ldx], 16-byte aligned, ldx % 8 == 0; 0 <= M <= 16
+ *   N, K    any N >= 0; K % 64 == 0
+ *   tensor_scale device fp32 scalar or NULL (= 1); bias bf16 [N] or NULL
+ *   out     fp32 or bf16 [M, ldo], aligned to its elements, ldo >= N
+ * ------------------------------------------------------------------------- */
+bs_status bs_fp4_matvec(const void *x, int64_t ldx, int M, const uint8_t *codes, const uint8_t *sf, int64_t N,
+                        int64_t K, float alpha, const float *tensor_scale, const void *bias, void *out,
+                        int out_dtype, int64_t ldo, bs_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Status.
  * ------------------------------------------------------------------------- */
 /* Reads (synchronously) and returns the sticky device status word of the
- * current device: BS_OK, BS_ERR_TIMEOUT or BS_ERR_OFFSETS.  *detail (if not
+ * current device: BS_OK, BS_ERR_TIMEOUT, BS_ERR_OFFSETS or BS_ERR_PAGES.  *detail (if not
  * NULL) receives the raw word (error code in the low byte, site id above). */
 bs_status bs_get_device_status(int *detail);
 /* Resets the device status word of the current device to BS_OK (synchronous). */
