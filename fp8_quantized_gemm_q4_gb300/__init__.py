@@ -197,7 +197,7 @@ def load(path: str | None = None):
 
 
 def _check(status: int):
-    if status != BS_OK:
+    if status:
         lib = load()
         raise BSError(status, lib.bs_last_error().decode(errors="replace") or
                       lib.bs_status_string(status).decode())
@@ -208,8 +208,12 @@ def _ptr(t):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    """The cudaStream_t handle of ``stream``, or of the current stream of the
+    current device.  The raw handle is asked for directly: building the
+    torch.cuda.Stream object around it takes 2.9 us of a 3.1 us launch."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -364,7 +368,11 @@ _workspaces: dict = {}
 
 
 def _workspace(device, stream, nbytes: int):
-    key = (device.index, stream.cuda_stream)
+    return _workspace_of(device, stream.cuda_stream, nbytes)
+
+
+def _workspace_of(device, handle: int, nbytes: int):
+    key = (device.index, handle)
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
@@ -562,6 +570,11 @@ class KVCache(NamedTuple):
                    torch.ones(shape[:2], dtype=torch.float32, device=device))
 
 
+# Short names: a module lookup of torch.int32 and the like costs as much as
+# the check itself, and these calls are as small as a launch.
+_F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
+
+
 def _check_kv_cache(cache):
     """(k, v, k_scale, v_scale, shape) of a KVCache (or such a tuple), checked
     for type and layout."""
@@ -569,7 +582,7 @@ def _check_kv_cache(cache):
     shape = k.shape
     if len(shape) != 4 or v.shape != shape or ks.shape != shape[:2] or vs.shape != shape[:2]:
         raise ValueError("a KV cache is codes [pages, Hkv, page_size, D] and scales [pages, Hkv], twice")
-    if k.dtype != torch.uint8 or v.dtype != torch.uint8 or ks.dtype != torch.float32 or vs.dtype != torch.float32:
+    if k.dtype != _U8 or v.dtype != _U8 or ks.dtype != _F32 or vs.dtype != _F32:
         raise TypeError("KV cache codes are uint8 (e4m3), scales float32")
     if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
         raise ValueError("KV cache buffers must be contiguous")
@@ -578,8 +591,18 @@ def _check_kv_cache(cache):
 
 def _ints(name, *tensors):
     for t in tensors:
-        if t.dtype != torch.int32 or not t.is_contiguous():
+        if t.dtype != _I32 or not t.is_contiguous():
             raise TypeError(f"{name}: lengths, tables and slots are contiguous int32 tensors")
+
+
+def _check_table(name, table, B):
+    """(row stride, width) of a block table of B requests."""
+    shape, stride = table.shape, table.stride()
+    if table.dtype != _I32 or len(shape) != 2 or stride[1] != 1:
+        raise TypeError(f"{name}: block_table is an int32 [B, max_pages] tensor with contiguous rows")
+    if shape[0] != B:
+        raise ValueError(f"{name}: block_table has {shape[0]} rows for {B} requests")
+    return stride[0], shape[1]
 
 
 def kv_plan(seq_lens, new_lens, block_table, free_pages, n_free, page_size: int, total_new: int, out=None,
@@ -588,23 +611,22 @@ def kv_plan(seq_lens, new_lens, block_table, free_pages, n_free, page_size: int,
     int32): request b takes the pages that its new tokens need from the end of
     ``free_pages[:n_free]``; ``block_table`` [B, max_pages] is updated in place.
     Returns (cu_new [B + 1], kv_lens [B], slots [total_new], n_free [1])."""
-    B = seq_lens.shape[0]
-    dev = seq_lens.device
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.stride(1) != 1:
-        raise TypeError("kv_plan: block_table is an int32 [B, max_pages] tensor with contiguous rows")
-    if new_lens.shape[0] != B or block_table.shape[0] != B:
-        raise ValueError("kv_plan: seq_lens, new_lens and block_table differ in the number of requests")
+    B = seq_lens.numel()
     if out is None:
-        out = (torch.empty(B + 1, dtype=torch.int32, device=dev), torch.empty(B, dtype=torch.int32, device=dev),
-               torch.empty(total_new, dtype=torch.int32, device=dev), torch.empty(1, dtype=torch.int32, device=dev))
+        dev = seq_lens.device
+        out = (torch.empty(B + 1, dtype=_I32, device=dev), torch.empty(B, dtype=_I32, device=dev),
+               torch.empty(total_new, dtype=_I32, device=dev), torch.empty(1, dtype=_I32, device=dev))
     cu, kv, slots, left = out
     _ints("kv_plan", seq_lens, new_lens, free_pages, n_free, cu, kv, slots, left)
+    if new_lens.numel() != B:
+        raise ValueError("kv_plan: seq_lens and new_lens differ in the number of requests")
+    ld, width = _check_table("kv_plan", block_table, B)
     if cu.numel() < B + 1 or kv.numel() < B or slots.numel() < total_new:
         raise ValueError("kv_plan: outputs are [B + 1], [B], [total_new] and [1]")
     _check((_lib or load()).bs_kv_plan(
-        seq_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(), block_table.stride(0),
-        block_table.shape[1], free_pages.data_ptr(), n_free.data_ptr(), free_pages.numel(), page_size, total_new,
-        cu.data_ptr(), kv.data_ptr(), slots.data_ptr(), left.data_ptr(), _stream(stream)))
+        seq_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(), ld, width, free_pages.data_ptr(),
+        n_free.data_ptr(), free_pages.numel(), page_size, total_new, cu.data_ptr(), kv.data_ptr(), slots.data_ptr(),
+        left.data_ptr(), _stream(stream)))
     return out
 
 
@@ -612,30 +634,33 @@ def kv_release(lens, done, block_table, free_pages, n_free, page_size: int, stre
     """Give the pages of the requests with ``done[b] != 0`` (``lens[b]`` cached
     tokens) back to the free list, in place."""
     _ints("kv_release", lens, done, free_pages, n_free)
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.stride(1) != 1:
-        raise TypeError("kv_release: block_table is an int32 [B, max_pages] tensor with contiguous rows")
-    B = lens.shape[0]
-    if done.shape[0] != B or block_table.shape[0] != B:
-        raise ValueError("kv_release: lens, done and block_table differ in the number of requests")
+    B = lens.numel()
+    if done.numel() != B:
+        raise ValueError("kv_release: lens and done differ in the number of requests")
+    ld, width = _check_table("kv_release", block_table, B)
     _check((_lib or load()).bs_kv_release(
-        lens.data_ptr(), done.data_ptr(), B, block_table.data_ptr(), block_table.stride(0), block_table.shape[1],
-        free_pages.data_ptr(), n_free.data_ptr(), free_pages.numel(), page_size, _stream(stream)))
+        lens.data_ptr(), done.data_ptr(), B, block_table.data_ptr(), ld, width, free_pages.data_ptr(),
+        n_free.data_ptr(), free_pages.numel(), page_size, _stream(stream)))
 
 
 def kv_append(k, v, slots, cache, stream=None):
     """Quantize new keys and values [T, Hkv, D] (fp32 or bf16, any token and
     head strides) into their slots of the 8-bit cache, in place."""
     kc, vc, ks, vs, (pages, Hkv, page, D) = _check_kv_cache(cache)
-    T = slots.shape[0]
-    if k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D):
+    T = slots.numel()
+    shape = (T, Hkv, D)
+    if k.shape != shape or v.shape != shape:
         raise ValueError(f"kv_append: k and v are [{T}, {Hkv}, {D}] for these slots and this cache")
-    if k.stride(2) != 1 or v.stride(2) != 1 or k.dtype != v.dtype:
+    (kt, kh, kd), (vt, vh, vd) = k.stride(), v.stride()
+    dt = k.dtype
+    if kd != 1 or vd != 1 or v.dtype != dt:
         raise ValueError("kv_append: k and v have one type and contiguous rows of D")
+    if dt != _BF16 and dt != _F32:
+        raise TypeError(f"unsupported dtype {dt}")
     _ints("kv_append", slots)
-    kst, vst = k.stride(), v.stride()
-    a = KvAppendArgs(k.data_ptr(), v.data_ptr(), _dt(k), T, Hkv, D, kst[0], kst[1], vst[0], vst[1], slots.data_ptr(),
-                     kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, page)
-    _check((_lib or load()).bs_kv_append(ctypes.byref(a), _stream(stream)))
+    a = KvAppendArgs(k.data_ptr(), v.data_ptr(), DTYPE_BF16 if dt == _BF16 else DTYPE_F32, T, Hkv, D, kt, kh, vt, vh,
+                     slots.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, page)
+    _check((_lib or load()).bs_kv_append(a, _stream(stream)))
 
 
 def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_scale: float | None = None, out=None,
@@ -644,36 +669,38 @@ def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_s
     (their own keys and values appended first).  ``lse`` (fp32 [T, Hq], natural
     log) is filled if given.  Returns out bf16 [T, Hq, D]."""
     kc, vc, ks, vs, (pages, Hkv, page, D) = _check_kv_cache(cache)
-    T, Hq = q.shape[0], q.shape[1]
+    shape = q.shape
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
+        out = torch.empty(shape, dtype=_BF16, device=q.device)
+    if q.dtype != _BF16 or out.dtype != _BF16:
         raise TypeError("kv_attention: q and out are bfloat16")
-    if q.shape[2] != D or out.shape != q.shape or q.stride(2) != 1 or out.stride(2) != 1:
-        raise ValueError(f"kv_attention: q and out are [T, Hq, {D}] with contiguous rows")
-    B = kv_lens.shape[0]
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.stride(1) != 1:
-        raise TypeError("kv_attention: block_table is an int32 [B, max_pages] tensor with contiguous rows")
-    if cu_q.shape[0] != B + 1 or block_table.shape[0] != B:
-        raise ValueError("kv_attention: cu_q is [B + 1], kv_lens [B] and block_table [B, max_pages]")
+    if len(shape) != 3 or shape[2] != D or out.shape != shape:
+        raise ValueError(f"kv_attention: q and out are [T, Hq, {D}]")
+    (qt, qh, qd), (ot, oh, od) = q.stride(), out.stride()
+    if qd != 1 or od != 1:
+        raise ValueError("kv_attention: rows of q and out are contiguous")
+    T, Hq = shape[0], shape[1]
+    B = kv_lens.numel()
+    ld, width = _check_table("kv_attention", block_table, B)
+    if cu_q.numel() != B + 1:
+        raise ValueError("kv_attention: cu_q is [B + 1] and kv_lens [B]")
     _ints("kv_attention", cu_q, kv_lens)
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype != _F32 or lse.shape != shape[:2] or not lse.is_contiguous()):
         raise ValueError("kv_attention: lse is a contiguous float32 [T, Hq] tensor")
-    qst, ost = q.stride(), out.stride()
-    a = KvAttentionArgs(q.data_ptr(), qst[0], qst[1], out.data_ptr(), ost[0], ost[1],
-                        None if lse is None else lse.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(),
-                        vs.data_ptr(), pages, page, block_table.data_ptr(), block_table.stride(0),
-                        block_table.shape[1], cu_q.data_ptr(), kv_lens.data_ptr(), B, T, Hq, Hkv, D, max_q_len,
-                        D ** -0.5 if softmax_scale is None else softmax_scale)
+    a = KvAttentionArgs(q.data_ptr(), qt, qh, out.data_ptr(), ot, oh, None if lse is None else lse.data_ptr(),
+                        kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, page,
+                        block_table.data_ptr(), ld, width, cu_q.data_ptr(), kv_lens.data_ptr(), B, T, Hq, Hkv, D,
+                        max_q_len, D ** -0.5 if softmax_scale is None else softmax_scale)
     opts = getattr(_tls, "opts", None)
     if opts:
         a.wait_timeout_us = opts.get("wait_timeout_us", 0)
     lib = _lib or load()
-    nbytes = int(lib.bs_kv_attention_workspace_bytes(ctypes.byref(a)))
+    handle = _stream(stream)
+    nbytes = lib.bs_kv_attention_workspace_bytes(a)
     if nbytes:
-        ws = _workspace(q.device, stream if stream is not None else torch.cuda.current_stream(q.device), nbytes)
+        ws = _workspace_of(q.device, handle, nbytes)
         a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
-    _check(lib.bs_kv_attention(ctypes.byref(a), _stream(stream)))
+    _check(lib.bs_kv_attention(a, handle))
     return out
 
 
@@ -682,26 +709,29 @@ def matvec_fp4(x, codes, sf, out_dtype=torch.bfloat16, alpha: float = 1.0, bias=
     """x [M <= 16, K] bf16 times FP4 weights (codes [N, K/2] and MMA-layout
     scales from q4_quantize, with ``tensor_scale`` of q4_quantize_two_level):
     Y = alpha tensor_scale x W^T + bias, x left unquantized."""
-    M, K = x.shape
-    N = codes.shape[0]
-    if x.dtype != torch.bfloat16 or x.stride(1) != 1:
+    (M, K), (N, half) = x.shape, codes.shape
+    ldx, one = x.stride()
+    if x.dtype != _BF16 or one != 1:
         raise TypeError("matvec_fp4: x is a bfloat16 [M, K] tensor with contiguous rows")
-    if codes.dtype != torch.uint8 or codes.shape[1] * 2 != K or not codes.is_contiguous():
+    if codes.dtype != _U8 or half * 2 != K or not codes.is_contiguous():
         raise ValueError(f"matvec_fp4: codes are contiguous uint8 [N, {K // 2}]")
-    if sf.numel() < (N + 127) // 128 * 128 * (K // 16):
-        raise ValueError("matvec_fp4: sf holds fewer scales than bs_sf_bytes(N, K)")
-    if bias is not None and (bias.dtype != torch.bfloat16 or bias.numel() != N or not bias.is_contiguous()):
+    if sf.dtype != _U8 or sf.numel() < (N + 127) // 128 * 128 * (K // 16):
+        raise ValueError("matvec_fp4: sf are the uint8 scales of [N, K], bs_sf_bytes(N, K) of them")
+    if bias is not None and (bias.dtype != _BF16 or bias.numel() != N or not bias.is_contiguous()):
         raise ValueError("matvec_fp4: bias is a contiguous bfloat16 [N] tensor")
-    if tensor_scale is not None and tensor_scale.dtype != torch.float32:
+    if tensor_scale is not None and tensor_scale.dtype != _F32:
         raise TypeError("matvec_fp4: tensor_scale is a float32 tensor")
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=x.device)
-    elif out.shape != (M, N) or out.stride(1) != 1:
+    ldo, one = out.stride()
+    if out.shape != (M, N) or one != 1:
         raise ValueError(f"matvec_fp4: out is [{M}, {N}] with contiguous rows")
+    if M <= 1:
+        ldx, ldo = K, N   # the stride of a single row means nothing
     _check((_lib or load()).bs_fp4_matvec(
-        x.data_ptr(), x.stride(0), M, codes.data_ptr(), sf.data_ptr(), N, K, alpha,
+        x.data_ptr(), ldx, M, codes.data_ptr(), sf.data_ptr(), N, K, alpha,
         None if tensor_scale is None else tensor_scale.data_ptr(), None if bias is None else bias.data_ptr(),
-        out.data_ptr(), _dt(out), out.stride(0), _stream(stream)))
+        out.data_ptr(), _dt(out), ldo, _stream(stream)))
     return out
 
 

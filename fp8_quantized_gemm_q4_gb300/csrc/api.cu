@@ -1254,7 +1254,7 @@ bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
 bs_status bs_fp4_matvec(const void* x, int64_t ldx, int M, const uint8_t* codes, const uint8_t* sf, int64_t N, int64_t K,
                         float alpha, const float* tensor_scale, const void* bias, void* out, int out_dtype, int64_t ldo,
                         bs_stream_t stream) {
-  if (M < 0 || N < 0 || K <= 0 || N > INT32_MAX || K > INT32_MAX)
+  if (M < 0 || N < 0 || K <= 0 || N > INT32_MAX - 255 || K > INT32_MAX - 255)
     return fail(BS_ERR_INVALID, "fp4_matvec: M=%d N=%lld K=%lld", M, (long long)N, (long long)K);
   if (out_dtype != BS_DTYPE_F32 && out_dtype != BS_DTYPE_BF16)
     return fail(BS_ERR_INVALID, "fp4_matvec: out_dtype %d", out_dtype);
