@@ -375,7 +375,12 @@ def _workspace_of(device, handle: int, nbytes: int):
     key = (device.index, handle)
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        # allocated and zeroed on the stream that uses it
+        s = torch.cuda.current_stream(device)
+        if s.cuda_stream != handle:
+            s = torch.cuda.ExternalStream(handle, device=device)
+        with torch.cuda.stream(s):
+            ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
         _workspaces[key] = ws
     return ws
 

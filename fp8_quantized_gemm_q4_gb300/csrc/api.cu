@@ -349,9 +349,8 @@ static bs_status check_common(const bs_gemm_args* a, bool grouped) {
 
 // Pipeline-wait bound of the kernels launched for `a` (nanoseconds).
 constexpr unsigned long long kDefaultWaitNs = 4000000000ull;  // 4 s
-static unsigned long long wait_ns(const bs_gemm_args* a) {
-  return a->wait_timeout_us > 0 ? (unsigned long long)a->wait_timeout_us * 1000ull : kDefaultWaitNs;
-}
+static unsigned long long wait_ns_of(int us) { return us > 0 ? (unsigned long long)us * 1000ull : kDefaultWaitNs; }
+static unsigned long long wait_ns(const bs_gemm_args* a) { return wait_ns_of(a->wait_timeout_us); }
 
 // FP4 stage depth: 256 K elements (128-byte rows, 128B swizzle) measured
 // faster than 128 (64-byte rows) on GB300 even though the finer ring holds
@@ -1189,8 +1188,9 @@ bs_status bs_kv_append(const bs_kv_append_args* a, bs_stream_t stream) {
 }
 
 size_t bs_kv_attention_workspace_bytes(const bs_kv_attention_args* a) {
-  (void)a;
-  return 0;
+  int sms = 0;
+  if (!a || (a->D != 64 && a->D != 128) || !device_info(nullptr, &sms)) return 0;
+  return kStreamKCounterBytes + (size_t)bsk::kv_attention_few_grid(sms) * bsk::kv_attention_piece_bytes(a->D);
 }
 
 bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
@@ -1219,9 +1219,24 @@ bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
       !aligned4(a->v_scales) || !aligned4(a->block_table) || !aligned4(a->cu_q) || !aligned4(a->kv_lens) ||
       !aligned4(a->lse))
     return fail(BS_ERR_ALIGN, "kv_attention: q, out and codes must be 16-byte aligned, strides multiples of 8 elements");
-  bsk::KvAttentionLaunch L = {};
+  bsk::KvAttentionLaunch L;
+  memset(&L, 0, sizeof L);
   bsk::KvAttentionParams& p = L.p;
-  if (!device_info(&p.status, nullptr)) return fail(BS_ERR_CUDA, "no current device");
+  int sms = 0;
+  if (!device_info(&p.status, &sms)) return fail(BS_ERR_CUDA, "no current device");
+  const size_t need = bs_kv_attention_workspace_bytes(a);
+  if (!a->workspace || a->workspace_bytes < need)
+    return fail(BS_ERR_INVALID, "kv_attention: workspace of %zu bytes, %zu needed", a->workspace ? a->workspace_bytes : 0, need);
+  if (!aligned16(a->workspace)) return fail(BS_ERR_ALIGN, "kv_attention: workspace must be 16-byte aligned");
+  if (a->num_pages > 0) {
+    const uint64_t rows = (uint64_t)a->num_pages * a->Hkv * a->page_size;
+    const uint32_t box = (uint32_t)bsk::kv_attention_box(a->page_size);
+    const CUtensorMapSwizzle sw = a->D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    st = make_map(&L.tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a->k_codes, a->D, rows, a->D, a->D, box, sw);
+    if (st == BS_OK) st = make_map(&L.tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a->v_codes, a->D, rows, a->D, a->D, box, sw);
+    if (st != BS_OK) return st;
+  }
+  L.few_grid = bsk::kv_attention_few_grid(sms);
   p.q = a->q;
   p.q_tok_stride = a->q_token_stride;
   p.q_head_stride = a->q_head_stride;
@@ -1246,6 +1261,11 @@ bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
   p.num_pages = (int)a->num_pages;
   p.page_shift = kv_page_shift(a->page_size);
   p.scale_log2 = a->softmax_scale * 1.4426950408889634f;
+  const int64_t most = a->max_q_len ? a->max_q_len : a->T;
+  p.only_few = most * (a->Hq / a->Hkv) <= bsk::kv_attention_few_rows();
+  p.counters = static_cast<int*>(a->workspace);
+  p.work = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + kStreamKCounterBytes);
+  p.wait_ns = wait_ns_of(a->wait_timeout_us);
   cudaError_t e = bsk::launch_kv_attention(L, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv_attention launch");
   return BS_OK;

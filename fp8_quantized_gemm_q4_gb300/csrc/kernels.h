@@ -323,11 +323,21 @@ struct KvAttentionParams {
   int B, T, Hq, Hkv, D;
   int num_pages, page_shift;
   float scale_log2;       // softmax scale * log2(e)
+  int only_few;           // every request has at most 16 rows per KV head
+  float* work;            // pieces of (request, head) pairs cut between CTAs
+  int* counters;          // arrivals of those pieces (zero between calls)
   int* status;
+  unsigned long long wait_ns;
 };
 struct KvAttentionLaunch {
   KvAttentionParams p;
+  CUtensorMap tm_k, tm_v; // codes [pages * Hkv * page, D], box kv_attention_box rows x D
+  int few_grid;
 };
+int kv_attention_few_grid(int sms);
+int kv_attention_few_rows();
+size_t kv_attention_piece_bytes(int D);  // per CTA of the few-rows grid
+int kv_attention_box(int page_size);
 cudaError_t launch_kv_attention(const KvAttentionLaunch& L, cudaStream_t stream);
 
 // Few bf16 rows times FP4 weights (matvec_fp4.cu)
