@@ -1229,11 +1229,12 @@ bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
     return fail(BS_ERR_INVALID, "kv_attention: workspace of %zu bytes, %zu needed", a->workspace ? a->workspace_bytes : 0, need);
   if (!aligned16(a->workspace)) return fail(BS_ERR_ALIGN, "kv_attention: workspace must be 16-byte aligned");
   if (a->num_pages > 0) {
-    const uint64_t rows = (uint64_t)a->num_pages * a->Hkv * a->page_size;
-    const uint32_t box = (uint32_t)bsk::kv_attention_box(a->page_size);
-    const CUtensorMapSwizzle sw = a->D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-    st = make_map(&L.tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a->k_codes, a->D, rows, a->D, a->D, box, sw);
-    if (st == BS_OK) st = make_map(&L.tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a->v_codes, a->D, rows, a->D, a->D, box, sw);
+    // rows of 128 bytes: one token, or two of D = 64
+    const uint64_t rows = (uint64_t)a->num_pages * a->Hkv * a->page_size * a->D / 128;
+    const uint32_t box = (uint32_t)(bsk::kv_attention_box(a->page_size) * a->D / 128);
+    st = make_map(&L.tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a->k_codes, 128, rows, 128, 128, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st == BS_OK)
+      st = make_map(&L.tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a->v_codes, 128, rows, 128, 128, box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != BS_OK) return st;
   }
   L.few_grid = bsk::kv_attention_few_grid(sms);
@@ -1262,7 +1263,8 @@ bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
   p.page_shift = kv_page_shift(a->page_size);
   p.scale_log2 = a->softmax_scale * 1.4426950408889634f;
   const int64_t most = a->max_q_len ? a->max_q_len : a->T;
-  p.only_few = most * (a->Hq / a->Hkv) <= bsk::kv_attention_few_rows();
+  const int64_t most_rows = most * (a->Hq / a->Hkv);
+  p.most_rows = (int)(most_rows < (1 << 30) ? most_rows : (1 << 30));
   p.counters = static_cast<int*>(a->workspace);
   p.work = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + kStreamKCounterBytes);
   p.wait_ns = wait_ns_of(a->wait_timeout_us);

@@ -323,7 +323,7 @@ struct KvAttentionParams {
   int B, T, Hq, Hkv, D;
   int num_pages, page_shift;
   float scale_log2;       // softmax scale * log2(e)
-  int only_few;           // every request has at most 16 rows per KV head
+  int most_rows;          // bound of the rows per KV head of a request (at most 2^30)
   float* work;            // pieces of (request, head) pairs cut between CTAs
   int* counters;          // arrivals of those pieces (zero between calls)
   int* status;
@@ -335,7 +335,6 @@ struct KvAttentionLaunch {
   int few_grid;
 };
 int kv_attention_few_grid(int sms);
-int kv_attention_few_rows();
 size_t kv_attention_piece_bytes(int D);  // per CTA of the few-rows grid
 int kv_attention_box(int page_size);
 cudaError_t launch_kv_attention(const KvAttentionLaunch& L, cudaStream_t stream);

@@ -49,17 +49,18 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t add
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // natural log of the softmax sum 2^m l
 __device__ __forceinline__ float lse_of(float m, float l) {
   return l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// Shared memory of a tile as TMA writes it: rows of D bytes, 16-byte chunks
-// exchanged by the 128-byte (D = 128) or 64-byte (D = 64) swizzle.
+// Shared memory of a tile as TMA writes it: rows of 128 bytes (one token, or two
+// for D = 64: rows of 64 bytes came in at half the rate), their 16-byte chunks
+// exchanged by the 128-byte swizzle.
 template <int D>
 __device__ __forceinline__ int code_at(int tok, int chunk) {
-  return D == 128 ? tok * 128 + ((chunk ^ (tok & 7)) << 4) : tok * 64 + ((chunk ^ ((tok >> 1) & 3)) << 4);
+  return D == 128 ? tok * 128 + ((chunk ^ (tok & 7)) << 4)
+                  : (tok >> 1) * 128 + (((((tok & 1) << 2) | chunk) ^ ((tok >> 1) & 7)) << 4);
 }
 // Which of 8 tokens stands at place n of the MMA's token axis: any order does,
 // as long as scores, masks and V rows agree.  For D = 128 places 2 i, 2 i + 1
@@ -69,18 +70,23 @@ __device__ __forceinline__ int token_of(int n) {
   return D == 128 ? (n >> 1) | ((n & 1) << 2) : n;
 }
 
-// One step of the online softmax over 16 tokens.  u[t][e]: logit of token
-// place 8 t + 2 c + e % 2 for row g + 8 (e / 2); returns the weights as the A
-// fragment of the product with V.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+
+// One step of the online softmax over 16 tokens for 8 rows.  u[e]: logit of
+// row 2 c + e % 2 for token place g + 8 (e / 2).  Returns the weights as the B
+// fragment (places on k) of the product with V.
 template <int NA>
-__device__ __forceinline__ void softmax_step(float (&u)[2][4], float inv_sv, float (&m)[2], float (&l)[2],
-                                             float (&o)[NA][2][4], uint32_t (&pa)[4]) {
-  float mx[2];
+__device__ __forceinline__ void softmax_step(float (&u)[4], float inv_sv, float (&m)[2], float (&l)[2],
+                                             float (&o)[NA][4], uint32_t (&pb)[2]) {
+  float mx[2] = {fmaxf(u[0], u[2]), fmaxf(u[1], u[3])};
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    mx[h] = fmaxf(fmaxf(u[0][2 * h], u[0][2 * h + 1]), fmaxf(u[1][2 * h], u[1][2 * h + 1]));
-    mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFullMask, mx[h], 1));
-    mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFullMask, mx[h], 2));
+  for (int d = 4; d < 32; d <<= 1) {
+    mx[0] = fmaxf(mx[0], __shfl_xor_sync(kFullMask, mx[0], d));
+    mx[1] = fmaxf(mx[1], __shfl_xor_sync(kFullMask, mx[1], d));
   }
   if (__any_sync(kFullMask, mx[0] > m[0] + 8.0f || mx[1] > m[1] + 8.0f)) {
 #pragma unroll
@@ -90,49 +96,58 @@ __device__ __forceinline__ void softmax_step(float (&u)[2][4], float inv_sv, flo
       m[h] = up ? mx[h] : m[h];
       l[h] *= f;
 #pragma unroll
-      for (int a = 0; a < NA; ++a)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) o[a][e][2 * h] *= f, o[a][e][2 * h + 1] *= f;
+      for (int a = 0; a < NA; ++a) o[a][h] *= f, o[a][2 + h] *= f;
     }
   }
+  const float r0 = m[0] == -INFINITY ? 0.0f : m[0], r1 = m[1] == -INFINITY ? 0.0f : m[1];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float ref = m[h] == -INFINITY ? 0.0f : m[h];
-    float sum = 0.0f;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const float a = ex2(u[t][2 * h] - ref), b = ex2(u[t][2 * h + 1] - ref);
-      sum += a + b;
-      pa[2 * t + h] = pack_f16x2(a, b);
-    }
-    l[h] = fmaf(sum, inv_sv, l[h]);
+  for (int t = 0; t < 2; ++t) {
+    const float a = ex2(u[2 * t] - r0), b = ex2(u[2 * t + 1] - r1);
+    l[0] = fmaf(a, inv_sv, l[0]);
+    l[1] = fmaf(b, inv_sv, l[1]);
+    pb[t] = movmatrix_trans(pack_f16x2(a, b));
   }
 }
 
 // ---------------------------------------------------------------------------
-// Requests with at most 16 rows per KV head (decode, drafts).
+// Requests with at most kFewRows rows per KV head (decode, drafts): bound by the
+// cache stream.  Work is a list of (request, head, 8 rows) units of 64-token
+// tiles, cut into equal contiguous shares, whatever the lengths.  Three CTAs an
+// SM take one each: a producer warp keeps 64 KB of codes in flight with TMA copies
+// page by page, four consumer warps take 16 tokens of a tile each, and while one
+// CTA joins the warps' results of a unit, the other two stream (one CTA with 12
+// consumer warps lost 25 of 134 us to that).  Both products run transposed,
+// tokens and then head columns on the MMA's M and the rows on its N = 8:
+// S^T = K Q^T, O^T = V^T P^T; a group of 4 or 8 query heads fills N, where it would
+// leave half of M = 16 empty.  More than 8 rows are units of their own beside the
+// first, whose tiles they find in L2.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 64;          // cached tokens per stage
-constexpr int kRows = 16;          // rows (token i, head of the group g): r = i * G + g
-constexpr int kItems = 64;         // (request, KV head) pairs listed at a time
+constexpr int kFewRows = 16;       // most rows (token i, head of the group g): r = i * G + g
+constexpr int kItems = 32;         // units listed at a time
 constexpr int kMinTiles = 2;       // least tiles worth a CTA of its own
-constexpr int kFewThreads = 160;   // 4 consumer warps, 1 producer warp
 constexpr int kCounters = 1024;    // arrival counters at the head of the workspace
+constexpr int kFewWarps = 4;       // consumers; one more warp produces
+constexpr int kFewThreads = kFewWarps * 32 + 32;
+constexpr int kFewCtas = 3;        // an SM
 
 template <int D>
 struct FewSmem {
-  static constexpr int kStages = 640 / D;  // 80 KB of codes
+  static constexpr int kStages = 512 / D;  // 64 KB of codes
   static constexpr int kStageBytes = 2 * kTile * D;
   alignas(1024) uint8_t kv[kStages][kStageBytes];  // K rows, then V rows
-  float red[2][kRows][D];
-  float2 ml[4][kRows];
+  float red[kFewWarps / 2][8 * D];
+  float2 ml[kFewWarps][8];
   float4 group[kStages][4];  // per 16 tokens: K scale, log2 of V scale, 1 / V scale, valid tokens (int)
-  int4 item[kItems];         // request, KV head, first tile, end tile
-  long long item_at[kItems]; // the pair's first tile in the list of all
-  int tile_sum[kItems + 1];  // tiles of this CTA before each item
+  // units of this share: request, KV head, first of the 8 rows, cached tokens;
+  // first row, rows (true), rows within T; the share's tile at which the unit
+  // would begin, its end tile within the share (0: no unit)
+  int4 item[kItems];
+  int4 rows[kItems];
+  int begin[kItems], end[kItems];
   uint64_t full[kStages], empty[kStages];
-  int scan[8];
-  long long start[4];
+  int2 scan[kFewThreads / 32];
+  long long first_unit;      // of this share, counted over requests with tiles
   int abort_flag, last;
 };
 
@@ -140,37 +155,44 @@ struct FewSmem {
 __device__ __forceinline__ int cached(const KvAttentionParams& p, int b) {
   return min(max(p.kv_lens[b], 0), p.max_pages << p.page_shift);
 }
-// Tiles of a request in this kernel's list: none without rows or with more
-// than 16 per KV head, else one at least (rows that see nothing are written too).
-__device__ __forceinline__ int few_tiles(const KvAttentionParams& p, int b, int G) {
-  const long long n = p.cu_q[b + 1] - p.cu_q[b];
-  if (n <= 0 || n * G > kRows) return 0;
-  return max(1, (cached(p, b) + kTile - 1) / kTile);
+// Tiles of each unit of a request in this kernel's list: none without rows or
+// with more than kFewRows per KV head, else one at least (rows that see nothing
+// are written too).  Which kernel serves a request follows from its own rows
+// alone, so that its result does not depend on the bound that the call gives.
+__device__ __forceinline__ int few_tiles(int n, int len, int G) {
+  return n <= 0 || (long long)n * G > kFewRows ? 0 : max(1, (len + kTile - 1) / kTile);
 }
 
-// A piece of a pair that is cut between CTAs: partial sums [16][D], then
-// (m, l) of the 16 rows.  A CTA has at most two: of the pair that begins before
-// its share (0) and of one that begins in it (1).
+// A piece of a unit that is cut between CTAs: partial sums [8][D], then (m, l) of
+// the 8 rows.  A CTA has at most two: of the unit that begins before its share
+// (0) and of one that begins in it (1).
 template <int D>
 __device__ __forceinline__ long long piece_at(int cta, int first_cta) {
-  return ((long long)cta * 2 + (cta == first_cta)) * (kRows * (D + 2));
+  return ((long long)cta * 2 + (cta == first_cta)) * (8 * (D + 2));
+}
+// Place of column d of a row in a reduction buffer: 16-column windows and their
+// halves exchanged by row, so that the fragments' stores meet no bank twice.
+template <int D>
+__device__ __forceinline__ int red_at(int r, int d) {
+  return r * D + ((((d >> 4) ^ ((r >> 1) & 1)) << 4) | ((d & 15) ^ (((r >> 2) & 1) << 3)));
 }
 
 template <int D>
-__global__ void __launch_bounds__(kFewThreads, 2) kv_attention_few_kernel(const __grid_constant__ CUtensorMap tm_k,
-                                                                          const __grid_constant__ CUtensorMap tm_v,
-                                                                          const __grid_constant__ KvAttentionParams p) {
+__global__ void __launch_bounds__(kFewThreads, kFewCtas)
+    kv_attention_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                            const __grid_constant__ KvAttentionParams p) {
   extern __shared__ uint8_t smem_raw[];
   using Smem = FewSmem<D>;
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr int kStages = Smem::kStages;
+  constexpr int kStages = Smem::kStages, kWarps = kFewWarps, kThreads = kFewThreads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.Hq / p.Hkv;
   const WaitGuard wg{&sm.abort_flag, p.status, p.wait_ns};
+  auto consumer_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); };
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], 4);
+      mbar_init(&sm.empty[s], kFewWarps);
     }
     fence_barrier_init();
     sm.abort_flag = 0;
@@ -178,173 +200,185 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv_attention_few_kernel(const 
   griddep_wait();
   griddep_launch_dependents();
 
-  // All tiles of all (request, head) pairs form one list, cut into equal
-  // contiguous shares.  Each thread sums the tiles of its own requests; the one
-  // whose requests hold the share's first tile finds the pair.
-  const int per = (p.B + kFewThreads - 1) / kFewThreads;
+  // Each thread takes `per` requests in a row: their tiles and row tiles, summed
+  // over the block, place its units in the list.
+  const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  int mine = 0;
+  int row0_own = 0, n_own = 0, len_own = 0;  // of the last of them: all there is while B <= threads
+  int2 mine = make_int2(0, 0);
   for (int b = b0; b < b1; ++b) {
-    mine += few_tiles(p, b, G);
-    if (p.only_few && (long long)(p.cu_q[b + 1] - p.cu_q[b]) * G > kRows) record_status(p.status, kStatusOffsets, 53);
+    row0_own = p.cu_q[b];
+    n_own = p.cu_q[b + 1] - row0_own;
+    len_own = cached(p, b);
+    const int nt = few_tiles(n_own, len_own, G), rt = nt ? (n_own * G + 7) / 8 : 0;
+    mine.x += nt * rt;
+    mine.y += rt;
+    if ((long long)n_own * G > p.most_rows) record_status(p.status, kStatusOffsets, 53);
   }
-  int incl = mine;
+  int2 incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int v = __shfl_up_sync(kFullMask, incl, d);
-    if (lane >= d) incl += v;
+    const int x = __shfl_up_sync(kFullMask, incl.x, d), y = __shfl_up_sync(kFullMask, incl.y, d);
+    if (lane >= d) incl.x += x, incl.y += y;
   }
   if (lane == 31) sm.scan[warp] = incl;
   __syncthreads();
-  int before = incl - mine, sum = 0;
+  int2 before = make_int2(incl.x - mine.x, incl.y - mine.y);
+  int sum = 0;
 #pragma unroll
-  for (int w = 0; w < kFewThreads / 32; ++w) {
-    if (w < warp) before += sm.scan[w];
-    sum += sm.scan[w];
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const int2 v = sm.scan[w];
+    if (w < warp) before.x += v.x, before.y += v.y;
+    sum += v.x;
   }
   const long long total = (long long)sum * p.Hkv;
   const int shares = (int)min((long long)gridDim.x, (total + kMinTiles - 1) / kMinTiles);
   if ((int)blockIdx.x >= shares) return;
-  const long long t_first = total * blockIdx.x / shares, t_last = total * (blockIdx.x + 1) / shares;
-  {
-    long long at = (long long)before * p.Hkv;
-    if (t_first >= at && t_first < at + (long long)mine * p.Hkv) {
-      for (int b = b0; b < b1; ++b) {
-        const int nt = few_tiles(p, b, G);
-        if (nt && t_first < at + (long long)nt * p.Hkv) {
-          const int h = (int)((t_first - at) / nt);
-          sm.start[0] = b;
-          sm.start[1] = h;
-          sm.start[2] = at + (long long)h * nt;  // the pair's first tile
-          break;
-        }
-        at += (long long)nt * p.Hkv;
+  const long long t_first = total * blockIdx.x / shares;
+  const int tiles = (int)(total * (blockIdx.x + 1) / shares - t_first);  // of this share
+  const long long own_at = (long long)before.x * p.Hkv;
+  if (t_first >= own_at && t_first < own_at + (long long)mine.x * p.Hkv) {
+    long long at = own_at, units = (long long)before.y * p.Hkv;
+    for (int b = b0; b < b1; ++b) {
+      int n = n_own, len = len_own;
+      if (per > 1) n = p.cu_q[b + 1] - p.cu_q[b], len = cached(p, b);
+      const int nt = few_tiles(n, len, G);
+      if (!nt) continue;
+      const int u = p.Hkv * ((n * G + 7) / 8);
+      if (t_first < at + (long long)nt * u) {
+        sm.first_unit = units + (int)((t_first - at) / nt);
+        break;
       }
+      at += (long long)nt * u;
+      units += u;
     }
   }
   __syncthreads();
-  long long pair = sm.start[0] * p.Hkv + sm.start[1], pair_at = sm.start[2];
 
-  uint32_t it = 0;  // stages used so far: the same count in every role
   bool dead = false;  // producer: a wait gave up, nothing more is copied
   uint32_t issued = 0;
-  while (pair_at < t_last) {
-    // list the next pairs of this share
+  int k_done = 0;     // tiles of the share in earlier lists
+  int tile = 0;                  // consumer: the share's tile that comes next
+  uint32_t stage = 0, phase = 0;  // and where it lies
+  for (long long base = sm.first_unit; k_done < tiles; base += kItems) {
+    // list units base .. base + kItems - 1 and their tiles within the share
+    if (k_done) __syncthreads();  // the list before has been used
+    if (tid < kItems) sm.end[tid] = 0;
     __syncthreads();
-    if (warp == 0) {
-      long long at = pair_at;
-      int tiles_before = 0;
-      for (int k0 = 0; k0 < kItems; k0 += 32) {
-        const long long q = pair + k0 + lane;
-        const int b = (int)(q / p.Hkv);
-        const int nt = b < p.B ? few_tiles(p, b, G) : 0;
-        int inc = nt;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int v = __shfl_up_sync(kFullMask, inc, d);
-          if (lane >= d) inc += v;
+    {
+      long long at = own_at, units = (long long)before.y * p.Hkv;
+      for (int b = b0; b < b1 && units < base + kItems && at < t_first + tiles; ++b) {
+        int row0 = row0_own, n = n_own, len = len_own;
+        if (per > 1) row0 = p.cu_q[b], n = p.cu_q[b + 1] - row0, len = cached(p, b);
+        const int nt = few_tiles(n, len, G);
+        if (!nt) continue;
+        const int rt = (n * G + 7) / 8, u = p.Hkv * rt;
+        for (int h = (int)max(0ll, base - units); h < u && units + h < base + kItems; ++h) {
+          const long long p0 = at + (long long)h * nt - t_first;
+          if (p0 >= tiles) break;
+          const int i = (int)(units + h - base);
+          sm.item[i] = make_int4(b, h / rt, h % rt * 8, len);
+          sm.rows[i] = make_int4(row0, n, max(0, min(n, p.T - row0)), nt);
+          sm.begin[i] = (int)p0;
+          sm.end[i] = (int)min((long long)tiles, p0 + nt);
         }
-        const long long p0 = at + inc - nt;
-        const int lo = (int)max(0ll, min((long long)nt, t_first - p0)), hi = (int)max(0ll, min((long long)nt, t_last - p0));
-        sm.item[k0 + lane] = make_int4(b, (int)(q % p.Hkv), lo, hi);
-        sm.item_at[k0 + lane] = p0;
-        int cnt = hi > lo ? hi - lo : 0, ci = cnt;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int v = __shfl_up_sync(kFullMask, ci, d);
-          if (lane >= d) ci += v;
-        }
-        sm.tile_sum[k0 + lane] = tiles_before + ci - cnt;
-        tiles_before += __shfl_sync(kFullMask, ci, 31);
-        at += __shfl_sync(kFullMask, inc, 31);
-      }
-      if (lane == 0) {
-        sm.tile_sum[kItems] = tiles_before;
-        sm.start[3] = at;
+        at += (long long)nt * u;
+        units += u;
       }
     }
     __syncthreads();
-    const int tiles = sm.tile_sum[kItems];
+    const int k_end = sm.end[kItems - 1] ? sm.end[kItems - 1] : tiles;  // where this list ends in the share
 
-    if (warp == 4) {
+    if (warp == kWarps) {
       // ---- producer: lane 4 k + j prepares group j (16 tokens) of the k-th of
-      // the next eight tiles, then each tile's copies go out as its stage frees
-      const int box = min(kTile, 1 << p.page_shift);  // rows of a copy
-      for (int k0 = 0; k0 < tiles; k0 += 8) {
-        const int k = k0 + (lane >> 2), j = lane & 3;
-        int id = -1, cnt = 0, tok = 0, h = 0;
-        float ks = 0.0f, vs = 1.0f;
-        if (k < tiles) {
-          int lo = 0, hi = kItems;  // the item with tile_sum[lo] <= k < tile_sum[lo + 1]
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (sm.tile_sum[mid] <= k) lo = mid; else hi = mid;
-          }
-          const int4 im = sm.item[lo];
-          const int len = cached(p, im.x);
-          tok = (im.z + k - sm.tile_sum[lo]) * kTile + 16 * j;
-          h = im.y;
-          cnt = max(0, min(16, len - tok));
-          if (cnt > 0) {
-            id = p.table[im.x * p.ld_table + (tok >> p.page_shift)];
-            if ((unsigned)id >= (unsigned)p.num_pages) {
-              record_status(p.status, kStatusOffsets, 50);
-              id = -1;
-              cnt = 0;
-            } else {
-              ks = p.k_scales[(long long)id * p.Hkv + h];
-              vs = p.v_scales[(long long)id * p.Hkv + h];
-            }
-          }
+      // eight tiles, then each tile's copies go out as its stage frees.  Page
+      // ids are read two rounds of eight ahead and scales one, so that neither
+      // latency stands between two rounds.
+      struct Group {
+        int id, tok, h, cnt;
+        float ks, vs;
+      };
+      const int box = min(kTile, 1 << p.page_shift);  // tokens of a copy
+      const int k = lane >> 2, j = lane & 3;
+      int at_item = 0;  // this lane's unit: its tiles ascend
+      auto find = [&](int k0) {
+        Group x = {-1, 0, 0, 0, 0.0f, 1.0f};
+        if (k0 + k < k_end) {
+          while (sm.end[at_item] <= k0 + k) ++at_item;
+          const int4 im = sm.item[at_item];
+          x.tok = (k0 + k - sm.begin[at_item]) * kTile + 16 * j;
+          x.h = im.y;
+          x.cnt = max(0, min(16, im.w - x.tok));
+          if (x.cnt > 0) x.id = p.table[im.x * p.ld_table + (x.tok >> p.page_shift)];
         }
-        const bool copies = cnt > 0 && (16 * j) % box == 0;
+        return x;
+      };
+      auto scales = [&](Group& x) {
+        if (x.cnt <= 0) return;
+        if ((unsigned)x.id >= (unsigned)p.num_pages) {
+          record_status(p.status, kStatusOffsets, 50);
+          x.cnt = 0;
+          return;
+        }
+        x.ks = p.k_scales[(long long)x.id * p.Hkv + x.h];
+        x.vs = p.v_scales[(long long)x.id * p.Hkv + x.h];
+      };
+      Group now = find(k_done), next = find(k_done + 8);
+      scales(now);
+      uint32_t s = k_done % kStages, ph = (k_done / kStages) & 1;
+      for (int k0 = k_done; k0 < k_end; k0 += 8) {
+        scales(next);
+        const Group later = find(k0 + 16);
+        const bool copies = now.cnt > 0 && (16 * j) % box == 0;
         const unsigned copy_mask = __ballot_sync(kFullMask, copies);
-        const int row = (int)((((long long)id * p.Hkv + h) << p.page_shift) + (tok & ((1 << p.page_shift) - 1)));
-        const float lvs = log2f(vs), ivs = 1.0f / vs;
-        for (int i = 0; i < 8 && k0 + i < tiles; ++i) {
-          const uint32_t s = it % kStages, phase = (it / kStages) & 1;
-          const bool ok = mbar_wait(&sm.empty[s], phase ^ 1, wg, 51);
+        const long long token = (((long long)now.id * p.Hkv + now.h) << p.page_shift) + (now.tok & ((1 << p.page_shift) - 1));
+        const int row = (int)(token * D / 128);
+        const int rounds = min(8, k_end - k0);
+        float log_vs = 0.0f, inv_vs = 0.0f;
+        for (int i = 0; i < rounds; ++i) {
+          const bool ok = mbar_wait(&sm.empty[s], ph ^ 1, wg, 51);
           dead |= __any_sync(kFullMask, !ok) != 0;
-          if (dead) {
-            ++it;
-            continue;
+          if (!dead) {
+            if (k == i && copies) {
+              tma_load_2d(&sm.kv[s][16 * j * D], &tm_k, &sm.full[s], 0, row);
+              tma_load_2d(&sm.kv[s][(kTile + 16 * j) * D], &tm_v, &sm.full[s], 0, row);
+            }
+            if (i == 0) log_vs = log2f(now.vs), inv_vs = 1.0f / now.vs;  // the scales may still be on their way
+            if (k == i) sm.group[s][j] = make_float4(now.ks, log_vs, inv_vs, __int_as_float(now.cnt));
+            __syncwarp();
+            const int n = __popc((copy_mask >> (4 * i)) & 15u);
+            if (lane == 4 * i) mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(n * box * D * 2));
+            issued = k0 + i + 1;
           }
-          if ((lane >> 2) == i) sm.group[s][j] = make_float4(ks, lvs, ivs, __int_as_float(cnt));
-          __syncwarp();
-          const int n = __popc((copy_mask >> (4 * i)) & 15u);
-          if (lane == 4 * i) mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(n * box * D * 2));
-          if ((lane >> 2) == i && copies) {
-            tma_load_2d(&sm.kv[s][16 * j * D], &tm_k, &sm.full[s], 0, row);
-            tma_load_2d(&sm.kv[s][(kTile + 16 * j) * D], &tm_v, &sm.full[s], 0, row);
-          }
-          issued = ++it;
+          if (++s == kStages) s = 0, ph ^= 1;
         }
+        now = next;
+        next = later;
       }
     } else {
       // ---- consumers: warp w takes tokens 16 w .. + 15 of every tile
       const int g = lane >> 2, c = lane & 3;
       constexpr int kQ = D / 64;  // 64-wide parts of a row
       for (int im = 0; im < kItems; ++im) {
-        const int4 item = sm.item[im];
-        if (item.z >= item.w) continue;
-        const int b = item.x, h = item.y;
-        const int row0 = p.cu_q[b], n = p.cu_q[b + 1] - row0, R = min(n, p.T - row0) * G;
-        const int len = cached(p, b);
-        // q rows g and g + 8 as A fragments, fp16 by a power of two per row
-        uint32_t qa[4 * kQ][4];
+        const int end = sm.end[im];
+        if (!end) break;
+        const int4 item = sm.item[im], rows = sm.rows[im];
+        const int h = item.y, r0 = item.z, len = item.w;  // the unit's rows are r0 .. r0 + 7
+        const int row0 = rows.x, n = rows.y, R = min(8, rows.z * G - r0);
+        // q row g as a B fragment, fp16 by a power of two
+        uint32_t qb[4 * kQ][2];
         float qscale[2];
         int seen[2];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int r = g + 8 * half;
-          const bool in = r < R;
+        {
+          const int r = r0 + g;
           const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (row0 + r / G) * p.q_tok_stride +
                                    (h * G + r % G) * p.q_head_stride + 16 * c;
-          uint4 raw[2 * kQ];
+          uint32_t w[8 * kQ];
 #pragma unroll
-          for (int x = 0; x < 2 * kQ; ++x)
-            raw[x] = in ? *reinterpret_cast<const uint4*>(q + 64 * (x >> 1) + 8 * (x & 1)) : make_uint4(0, 0, 0, 0);
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
+          for (int x = 0; x < 2 * kQ; ++x) {
+            const uint4 v = g < R ? *reinterpret_cast<const uint4*>(q + 64 * (x >> 1) + 8 * (x & 1)) : make_uint4(0, 0, 0, 0);
+            w[4 * x] = v.x, w[4 * x + 1] = v.y, w[4 * x + 2] = v.z, w[4 * x + 3] = v.w;
+          }
           float amax = 0.0f;
 #pragma unroll
           for (int x = 0; x < 8 * kQ; ++x)
@@ -353,61 +387,65 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv_attention_few_kernel(const 
           amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 2));
           const int up = fp16_up(amax);
           const float mul = exp2i(up);
-          qscale[half] = exp2i(-up) * p.scale_log2;
-          seen[half] = in ? len - n + r / G + 1 : 0;
 #pragma unroll
           for (int x = 0; x < 4 * kQ; ++x)  // k step x: columns 64 (x / 4) + 16 c + 4 (x % 4) .. + 3
 #pragma unroll
             for (int y = 0; y < 2; ++y)
-              qa[x][half + 2 * y] = pack_f16x2(__uint_as_float(w[2 * x + y] << 16) * mul,
-                                               __uint_as_float(w[2 * x + y] & 0xffff0000u) * mul);
+              qb[x][y] = pack_f16x2(__uint_as_float(w[2 * x + y] << 16) * mul,
+                                    __uint_as_float(w[2 * x + y] & 0xffff0000u) * mul);
+          const float undo = exp2i(-up) * p.scale_log2;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            qscale[e] = __shfl_sync(kFullMask, undo, 4 * (2 * c + e));
+            seen[e] = 2 * c + e < R ? len - n + (r0 + 2 * c + e) / G + 1 : 0;
+          }
         }
-        const int all_seen = len - n + 1;  // tokens that every row sees
-        float o[D / 16][2][4] = {};
+        const int all_seen = len - n + r0 / G + 1;  // tokens that every row sees
+        float o[D / 16][4] = {};
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 
-        for (int t = item.z; t < item.w; ++t, ++it) {
-          const uint32_t s = it % kStages, phase = (it / kStages) & 1;
-          mbar_wait(&sm.full[s], phase, wg, 52);
-          const float4 sc = sm.group[s][warp];
+        const int begin = sm.begin[im];
+        for (; tile < end; ++tile) {
+          mbar_wait(&sm.full[stage], phase, wg, 52);
+          const float4 sc = sm.group[stage][warp];
           const int cnt = __float_as_int(sc.w);
           if (cnt > 0) {
-            uint8_t* kt = &sm.kv[s][warp * 16 * D];
-            uint8_t* vt = &sm.kv[s][(kTile + warp * 16) * D];
+            uint8_t* kt = &sm.kv[stage][warp * 16 * D];
+            uint8_t* vt = kt + kTile * D;
             if (cnt < 16) {  // codes behind the last token may stand for NaN
-              for (int x = cnt * (D / 16) + lane; x < D; x += 32) reinterpret_cast<uint4*>(vt)[x] = make_uint4(0, 0, 0, 0);
+              for (int x = cnt * (D / 16) + lane; x < D; x += 32)
+                *reinterpret_cast<uint4*>(vt + code_at<D>(x / (D / 16), x % (D / 16))) = make_uint4(0, 0, 0, 0);
               __syncwarp();
             }
-            float u[2][4] = {};
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int tok = 8 * half + token_of<D>(g);
+            float u[4] = {}, u2[4] = {};  // two chains of products
+            {
+              const int tok = token_of<D>(g);
 #pragma unroll
               for (int part = 0; part < kQ; ++part) {
-                const uint4 v = *reinterpret_cast<const uint4*>(kt + code_at<D>(tok, 4 * part + c));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                const uint4 a = *reinterpret_cast<const uint4*>(kt + code_at<D>(tok, 4 * part + c));
+                const uint4 b = *reinterpret_cast<const uint4*>(kt + code_at<D>(8 + tok, 4 * part + c));
+                const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                  mma_f16(u[half], qa[4 * part + x], e4m3x2_to_f16x2((uint16_t)w[x]), e4m3x2_to_f16x2((uint16_t)(w[x] >> 16)));
+                for (int x = 0; x < 4; ++x) {
+                  const uint32_t ka[4] = {e4m3x2_to_f16x2((uint16_t)wa[x]), e4m3x2_to_f16x2((uint16_t)wb[x]),
+                                          e4m3x2_to_f16x2((uint16_t)(wa[x] >> 16)), e4m3x2_to_f16x2((uint16_t)(wb[x] >> 16))};
+                  mma_f16(x & 1 ? u2 : u, ka, qb[4 * part + x][0], qb[4 * part + x][1]);
+                }
               }
             }
-            const float f0 = qscale[0] * sc.x, f1 = qscale[1] * sc.x;
-            const int tok0 = t * kTile + warp * 16;
+            const int tok0 = (tile - begin) * kTile + warp * 16;
+            const float f[2] = {qscale[0] * sc.x, qscale[1] * sc.x};
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) u[half][e] = fmaf(u[half][e], e < 2 ? f0 : f1, sc.y);
+            for (int e = 0; e < 4; ++e) u[e] = fmaf(u[e] + u2[e], f[e & 1], sc.y);
             if (cnt < 16 || tok0 + 16 > all_seen) {
 #pragma unroll
-              for (int half = 0; half < 2; ++half)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int tok = 8 * half + token_of<D>(2 * c + (e & 1));
-                  if (tok >= cnt || tok0 + tok >= seen[e >> 1]) u[half][e] = -INFINITY;
-                }
+              for (int e = 0; e < 4; ++e) {
+                const int tok = 8 * (e >> 1) + token_of<D>(g);
+                if (tok >= cnt || tok0 + tok >= seen[e & 1]) u[e] = -INFINITY;
+              }
             }
-            uint32_t pa[4];
-            softmax_step<D / 16>(u, sc.z, m, l, o, pa);
+            uint32_t pb[2];
+            softmax_step<D / 16>(u, sc.z, m, l, o, pb);
 #pragma unroll
             for (int a = 0; a < D / 32; ++a) {
               // lanes 8 i .. + 7 give the rows of matrix i: tokens 8 (i % 2) .. + 7 at 16-byte chunk 2 a + i / 2
@@ -416,120 +454,97 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv_attention_few_kernel(const 
               ldmatrix_x4_trans(v, smem_u32(vt + code_at<D>(tok, 2 * a + (lane >> 4))));
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
+                // a pair of codes (columns 2 g, 2 g + 1) of two tokens each: to pairs of tokens
                 const uint32_t w0 = __byte_perm(v[2 * x], 0, 0x3120), w1 = __byte_perm(v[2 * x + 1], 0, 0x3120);
-                mma_f16(o[2 * a + x][0], pa, e4m3x2_to_f16x2((uint16_t)w0), e4m3x2_to_f16x2((uint16_t)w1));
-                mma_f16(o[2 * a + x][1], pa, e4m3x2_to_f16x2((uint16_t)(w0 >> 16)), e4m3x2_to_f16x2((uint16_t)(w1 >> 16)));
+                const uint32_t va[4] = {e4m3x2_to_f16x2((uint16_t)w0), e4m3x2_to_f16x2((uint16_t)(w0 >> 16)),
+                                        e4m3x2_to_f16x2((uint16_t)w1), e4m3x2_to_f16x2((uint16_t)(w1 >> 16))};
+                mma_f16(o[2 * a + x], va, pb[0], pb[1]);
               }
             }
             if (cnt < 16) fence_proxy_async_smem();  // the zeros, before the next copy into this stage
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.empty[s]);
+          if (lane == 0) mbar_arrive(&sm.empty[stage]);
+          if (++stage == kStages) stage = 0, phase ^= 1;
         }
 
-        // ---- the four warps' (m, l, o) to one
+        // ---- the warps' (m, l, o) to one: o[a] holds columns 16 a + 2 g and + 1
+        // (e / 2) of rows 2 c and + 1 (e % 2)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          l[half] += __shfl_xor_sync(kFullMask, l[half], 1);
-          l[half] += __shfl_xor_sync(kFullMask, l[half], 2);
-          if (c == 0) sm.ml[warp][g + 8 * half] = make_float2(m[half], l[half]);
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(kFullMask, l[e], d);
+          if (g == 0) sm.ml[warp][2 * c + e] = make_float2(m[e], l[e]);
         }
         consumer_sync();
-        float M[2], L[2];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float2 x[4];
-          M[half] = -INFINITY;
-          L[half] = 0.0f;
+        for (int e = 0; e < 2; ++e) {
+          float M = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) x[w] = sm.ml[w][g + 8 * half], M[half] = fmaxf(M[half], x[w].x);
-          const float ref = M[half] == -INFINITY ? 0.0f : M[half];
+          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.ml[w][2 * c + e].x);
+          const float f = ex2(m[e] - (M == -INFINITY ? 0.0f : M));
 #pragma unroll
-          for (int w = 0; w < 4; ++w) L[half] += x[w].y * ex2(x[w].x - ref);
-          const float f = ex2(m[half] - ref);
+          for (int a = 0; a < D / 16; ++a) o[a][e] *= f, o[a][2 + e] *= f;
+        }
+        float* buf = sm.red[warp % (kWarps / 2)];
+        auto put = [&] {
 #pragma unroll
           for (int a = 0; a < D / 16; ++a)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) o[a][e][2 * half] *= f, o[a][e][2 * half + 1] *= f;
-        }
-        // element (row, 16 a + 4 c + 2 x + e) is o[a][e][2 half + x]: four in a row
-        auto put = [&](int buf, int a) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-            *reinterpret_cast<float4*>(&sm.red[buf][g + 8 * half][16 * (a ^ (g & 1)) + 4 * c]) =
-                make_float4(o[a][0][2 * half], o[a][1][2 * half], o[a][0][2 * half + 1], o[a][1][2 * half + 1]);
+            for (int e = 0; e < 2; ++e)
+              *reinterpret_cast<float2*>(buf + red_at<D>(2 * c + e, 16 * a + 2 * g)) = make_float2(o[a][e], o[a][2 + e]);
         };
-        auto add = [&](int buf, int a) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const float4 v = *reinterpret_cast<const float4*>(&sm.red[buf][g + 8 * half][16 * (a ^ (g & 1)) + 4 * c]);
-            o[a][0][2 * half] += v.x, o[a][1][2 * half] += v.y, o[a][0][2 * half + 1] += v.z, o[a][1][2 * half + 1] += v.w;
-          }
-        };
-        if (warp >= 2)
-#pragma unroll
-          for (int a = 0; a < D / 16; ++a) put(warp - 2, a);
+        if (warp >= kWarps / 2) put();
         consumer_sync();
-        if (warp < 2)
+        if (warp < kWarps / 2) {
 #pragma unroll
-          for (int a = 0; a < D / 16; ++a) add(warp, a);
-        consumer_sync();
-        // warp 0 keeps the first half of the columns, warp 1 the second
-        if (warp == 0)
+          for (int a = 0; a < D / 16; ++a)
 #pragma unroll
-          for (int a = D / 32; a < D / 16; ++a) put(0, a);
-        if (warp == 1)
-#pragma unroll
-          for (int a = 0; a < D / 32; ++a) put(1, a);
-        consumer_sync();
-        if (warp == 0)
-#pragma unroll
-          for (int a = 0; a < D / 32; ++a) add(1, a);
-        if (warp == 1)
-#pragma unroll
-          for (int a = D / 32; a < D / 16; ++a) add(0, a);
-
-        const int nt = max(1, (len + kTile - 1) / kTile);
-        if (item.z == 0 && item.w == nt) {
-          if (warp < 2) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int r = g + 8 * half;
-              if (r >= R) continue;
-              const float inv = L[half] > 0.0f ? 1.0f / L[half] : 0.0f;
-              const long long tr = row0 + r / G;
-              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + tr * p.out_tok_stride +
-                                   (h * G + r % G) * p.out_head_stride + 4 * c;
-#pragma unroll
-              for (int a = 0; a < D / 16; ++a)
-                if (a / (D / 32) == warp)
-                  *reinterpret_cast<uint2*>(dst + 16 * a) =
-                      make_uint2(pack_bf16x2(o[a][0][2 * half] * inv, o[a][1][2 * half] * inv),
-                                 pack_bf16x2(o[a][0][2 * half + 1] * inv, o[a][1][2 * half + 1] * inv));
-              if (warp == 0 && c == 0 && p.lse) p.lse[tr * p.Hq + h * G + r % G] = lse_of(M[half], L[half]);
+            for (int e = 0; e < 2; ++e) {
+              const float2 add = *reinterpret_cast<const float2*>(buf + red_at<D>(2 * c + e, 16 * a + 2 * g));
+              o[a][e] += add.x, o[a][2 + e] += add.y;
             }
+          put();
+        }
+        consumer_sync();
+        const int nt = rows.w;
+        const bool starts = begin >= 0, alone = starts && end == begin + nt;
+        // a unit cut between CTAs: this piece goes to the workspace, the last
+        // CTA to finish one joins the pieces in order
+        float* slot = p.work + ((long long)blockIdx.x * 2 + starts) * (8 * (D + 2));
+        for (int x = tid * 4; x < R * D; x += kWarps * 128) {
+          const int r = x / D, d = x % D;
+          float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int w = 0; w < kWarps / 2; ++w) {
+            const float4 v = *reinterpret_cast<const float4*>(&sm.red[w][red_at<D>(r, d)]);
+            y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
           }
+          float M = -INFINITY, L = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.ml[w][r].x);
+          const float ref = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) L += sm.ml[w][r].y * ex2(sm.ml[w][r].x - ref);
+          if (alone) {
+            const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+            const long long tr = row0 + (r0 + r) / G;
+            const int hq = h * G + (r0 + r) % G;
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + tr * p.out_tok_stride + hq * p.out_head_stride + d;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+            if (d == 0 && p.lse) p.lse[tr * p.Hq + hq] = lse_of(M, L);
+          } else {
+            *reinterpret_cast<float4*>(slot + x) = y;
+            if (d == 0) *reinterpret_cast<float2*>(slot + 8 * D + 2 * r) = make_float2(M, L);
+          }
+        }
+        if (alone) {
+          consumer_sync();  // ml and red have been read
           continue;
         }
-        // ---- a pair cut between CTAs: this piece goes to the workspace, the
-        // last CTA to finish one joins the pieces in order
-        float* slot = p.work + ((long long)blockIdx.x * 2 + (item.z == 0 ? 1 : 0)) * (kRows * (D + 2));
-        if (warp < 2) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int r = g + 8 * half;
-            if (r >= R) continue;
-#pragma unroll
-            for (int a = 0; a < D / 16; ++a)
-              if (a / (D / 32) == warp)
-                *reinterpret_cast<float4*>(slot + r * D + 16 * a + 4 * c) =
-                    make_float4(o[a][0][2 * half], o[a][1][2 * half], o[a][0][2 * half + 1], o[a][1][2 * half + 1]);
-            if (warp == 0 && c == 0) *reinterpret_cast<float2*>(slot + kRows * D + 2 * r) = make_float2(M[half], L[half]);
-          }
-          __threadfence();
-        }
-        // the shares that hold the pair's first and last tile
-        const long long first = sm.item_at[im];
+        __threadfence();
+        // the shares that hold the unit's first and last tile
+        const long long first = t_first + begin;
         const int c0 = (int)(((first + 1) * shares - 1) / total), c1 = (int)(((first + nt) * shares - 1) / total);
         consumer_sync();
         if (tid == 0) {
@@ -540,9 +555,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv_attention_few_kernel(const 
         }
         consumer_sync();
         if (sm.last) {
-          for (int r = warp; r < R; r += 4) {
+          for (int r = warp; r < R; r += kWarps) {
             float mx = -INFINITY;
-            for (int x = c0 + lane; x <= c1; x += 32) mx = fmaxf(mx, __ldcg(p.work + piece_at<D>(x, c0) + kRows * D + 2 * r));
+            for (int x = c0 + lane; x <= c1; x += 32) mx = fmaxf(mx, __ldcg(p.work + piece_at<D>(x, c0) + 8 * D + 2 * r));
 #pragma unroll
             for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, d));
             const float ref = mx == -INFINITY ? 0.0f : mx;
@@ -550,28 +565,27 @@ __global__ void __launch_bounds__(kFewThreads, 2) kv_attention_few_kernel(const 
 #pragma unroll 4
             for (int x = c0; x <= c1; ++x) {
               const float* from = p.work + piece_at<D>(x, c0);
-              const float2 e = __ldcg(reinterpret_cast<const float2*>(from + kRows * D + 2 * r));
+              const float2 e = __ldcg(reinterpret_cast<const float2*>(from + 8 * D + 2 * r));
               const float f = ex2(e.x - ref);
               sum_l += e.y * f;
 #pragma unroll
               for (int d = 0; d < D / 32; ++d) acc[d] += f * __ldcg(from + r * D + 32 * d + lane);
             }
             const float inv = sum_l > 0.0f ? 1.0f / sum_l : 0.0f;
-            const long long tr = row0 + r / G;
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + tr * p.out_tok_stride +
-                                 (h * G + r % G) * p.out_head_stride + lane;
+            const long long tr = row0 + (r0 + r) / G;
+            const int hq = h * G + (r0 + r) % G;
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + tr * p.out_tok_stride + hq * p.out_head_stride + lane;
 #pragma unroll
             for (int d = 0; d < D / 32; ++d) dst[32 * d] = __float2bfloat16(acc[d] * inv);
-            if (lane == 0 && p.lse) p.lse[tr * p.Hq + h * G + r % G] = lse_of(mx, sum_l);
+            if (lane == 0 && p.lse) p.lse[tr * p.Hq + hq] = lse_of(mx, sum_l);
           }
         }
       }
     }
-    pair += kItems;
-    pair_at = sm.start[3];
+    k_done = k_end;
   }
   // after a wait that gave up: copies in flight land before the CTA's memory goes
-  if (warp == 4 && dead)
+  if (warp == kWarps && dead)
     for (uint32_t k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
       mbar_drain(&sm.full[k % kStages], (k / kStages) & 1, 100000000ull);
 }
@@ -599,7 +613,7 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const __grid
   }
   if (lo == p.B) return;  // rows past the last request are not written
   const int n = p.cu_q[lo + 1] - p.cu_q[lo];
-  if ((long long)n * (p.Hq / p.Hkv) <= kRows) return;
+  if ((long long)n * (p.Hq / p.Hkv) <= kFewRows) return;
   const int len = min(p.kv_lens[lo], p.max_pages << p.page_shift) - n + (row - p.cu_q[lo]) + 1;
   if (tid < D)
     qs[tid] = __bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[row * p.q_tok_stride + hq * p.q_head_stride + tid]);
@@ -664,15 +678,18 @@ cudaError_t launch_few(const KvAttentionLaunch& L, cudaStream_t stream) {
 
 }  // namespace
 
-int kv_attention_few_grid(int sms) { return min(2 * sms, kCounters); }
-size_t kv_attention_piece_bytes(int D) { return (size_t)2 * kRows * (D + 2) * sizeof(float); }
+int kv_attention_few_grid(int sms) { return kFewCtas * sms < kCounters ? kFewCtas * sms : kCounters; }
+size_t kv_attention_piece_bytes(int D) { return (size_t)2 * 8 * (D + 2) * sizeof(float); }
 int kv_attention_box(int page_size) { return min(page_size, kTile); }
-int kv_attention_few_rows() { return kRows; }
 
 cudaError_t launch_kv_attention(const KvAttentionLaunch& L, cudaStream_t stream) {
   const KvAttentionParams& p = L.p;
-  cudaError_t e = p.D == 64 ? launch_few<64>(L, stream) : launch_few<128>(L, stream);
-  if (e != cudaSuccess || p.only_few) return e;
+  const int G = p.Hq / p.Hkv;
+  if (G <= kFewRows) {
+    cudaError_t e = p.D == 64 ? launch_few<64>(L, stream) : launch_few<128>(L, stream);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.most_rows <= kFewRows) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.T, (unsigned)p.Hq, 1);
   cfg.blockDim = dim3(kAttnThreads, 1, 1);
