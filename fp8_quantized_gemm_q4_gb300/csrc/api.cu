@@ -1189,8 +1189,12 @@ bs_status bs_kv_append(const bs_kv_append_args* a, bs_stream_t stream) {
 
 size_t bs_kv_attention_workspace_bytes(const bs_kv_attention_args* a) {
   int sms = 0;
-  if (!a || (a->D != 64 && a->D != 128) || !device_info(nullptr, &sms)) return 0;
-  return kStreamKCounterBytes + (size_t)bsk::kv_attention_few_grid(sms) * bsk::kv_attention_piece_bytes(a->D);
+  if (!a || (a->D != 64 && a->D != 128) || a->Hkv <= 0 || a->Hq <= 0 || !device_info(nullptr, &sms)) return 0;
+  // two pieces a CTA; the two kernels run one after the other and share the room
+  const size_t few = (size_t)bsk::kv_attention_few_grid(sms) * bsk::kv_attention_piece_bytes(a->D);
+  const size_t rows = (size_t)bsk::kv_attention_rows_grid(sms) * bsk::kv_attention_rows_piece_bytes(a->D);
+  const bool many = (a->max_q_len > 0 ? a->max_q_len : a->T) * (a->Hq / a->Hkv) > bsk::kFewRows;
+  return kStreamKCounterBytes + (many && rows > few ? rows : few);
 }
 
 bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
@@ -1238,6 +1242,7 @@ bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
     if (st != BS_OK) return st;
   }
   L.few_grid = bsk::kv_attention_few_grid(sms);
+  L.rows_grid = bsk::kv_attention_rows_grid(sms);
   p.q = a->q;
   p.q_tok_stride = a->q_token_stride;
   p.q_head_stride = a->q_head_stride;

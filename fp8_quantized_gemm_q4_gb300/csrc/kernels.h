@@ -305,6 +305,8 @@ struct KvAppendParams {
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream);
 
 // Attention over the paged 8-bit cache (kv_attention.cu)
+constexpr int kFewRows = 16;  // most rows (new tokens x heads of a group) per KV head of a request for its
+                              // few-rows kernel; kv_attention_rows.cu takes the others
 struct KvAttentionParams {
   const void* q;          // bf16 [T, Hq, D]
   long long q_tok_stride, q_head_stride;
@@ -332,11 +334,15 @@ struct KvAttentionParams {
 struct KvAttentionLaunch {
   KvAttentionParams p;
   CUtensorMap tm_k, tm_v; // codes [pages * Hkv * page, D], box kv_attention_box rows x D
-  int few_grid;
+  int few_grid, rows_grid;
 };
 int kv_attention_few_grid(int sms);
 size_t kv_attention_piece_bytes(int D);  // per CTA of the few-rows grid
 int kv_attention_box(int page_size);
+// requests with more than 16 rows per KV head (kv_attention_rows.cu)
+int kv_attention_rows_grid(int sms);
+size_t kv_attention_rows_piece_bytes(int D);
+cudaError_t launch_kv_attention_rows(const KvAttentionLaunch& L, cudaStream_t stream);
 cudaError_t launch_kv_attention(const KvAttentionLaunch& L, cudaStream_t stream);
 
 // Few bf16 rows times FP4 weights (matvec_fp4.cu)

@@ -13,29 +13,12 @@
 // fits fp16 (rounded to 11 bits, the only rounding below fp32), and o, lse
 // follow from (m, l, sum).  m moves, and the accumulators are rescaled, only
 // when max u passes m + 8.
-#include "kernels.h"
-#include "ptx.cuh"
+#include "kv_attention.cuh"
 
 namespace bsk {
 
 namespace {
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-// The power of two that brings a row with this largest element to [2^14, 2^15)
-__device__ __forceinline__ int fp16_up(float amax) {
-  const int ex = max((int)(__float_as_uint(amax) >> 23) - 127, -112);
-  return amax > 0.0f ? 14 - min(ex, 127) : 0;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -49,11 +32,6 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t add
                : "r"(addr)
                : "memory");
 }
-// natural log of the softmax sum 2^m l
-__device__ __forceinline__ float lse_of(float m, float l) {
-  return l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-}
-
 // Shared memory of a tile as TMA writes it: rows of 128 bytes (one token, or two
 // for D = 64: rows of 64 bytes came in at half the rate), their 16-byte chunks
 // exchanged by the 128-byte swizzle.
@@ -123,7 +101,6 @@ __device__ __forceinline__ void softmax_step(float (&u)[4], float inv_sv, float 
 // first, whose tiles they find in L2.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 64;          // cached tokens per stage
-constexpr int kFewRows = 16;       // most rows (token i, head of the group g): r = i * G + g
 constexpr int kItems = 32;         // units listed at a time
 constexpr int kMinTiles = 2;       // least tiles worth a CTA of its own
 constexpr int kCounters = 1024;    // arrival counters at the head of the workspace
@@ -151,10 +128,6 @@ struct FewSmem {
   int abort_flag, last;
 };
 
-// Cached tokens of a request, as far as its table row can name them.
-__device__ __forceinline__ int cached(const KvAttentionParams& p, int b) {
-  return min(max(p.kv_lens[b], 0), p.max_pages << p.page_shift);
-}
 // Tiles of each unit of a request in this kernel's list: none without rows or
 // with more than kFewRows per KV head, else one at least (rows that see nothing
 // are written too).  Which kernel serves a request follows from its own rows
@@ -590,82 +563,6 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
       mbar_drain(&sm.full[k % kStages], (k / kStages) & 1, 100000000ull);
 }
 
-// ---------------------------------------------------------------------------
-// Requests with more rows.
-// ---------------------------------------------------------------------------
-constexpr int kAttnThreads = 128;
-__device__ __forceinline__ float e4m3_val(uint32_t c) { return e4m3_to_f32(c); }
-
-// One CTA per (row, query head): a thread scores one token of a chunk of 128,
-// then owns one output element.
-template <int D>
-__global__ void __launch_bounds__(kAttnThreads) kv_attention_kernel(const __grid_constant__ KvAttentionParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
-  __shared__ float qs[D], ps[kAttnThreads], red[kAttnThreads / 32];
-  const int row = blockIdx.x, hq = blockIdx.y, tid = threadIdx.x;
-  const int h = hq / (p.Hq / p.Hkv);
-  // the request of this row: cu_q ascends
-  int lo = 0, hi = p.B;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (p.cu_q[mid + 1] > row) hi = mid; else lo = mid + 1;
-  }
-  if (lo == p.B) return;  // rows past the last request are not written
-  const int n = p.cu_q[lo + 1] - p.cu_q[lo];
-  if ((long long)n * (p.Hq / p.Hkv) <= kFewRows) return;
-  const int len = min(p.kv_lens[lo], p.max_pages << p.page_shift) - n + (row - p.cu_q[lo]) + 1;
-  if (tid < D)
-    qs[tid] = __bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[row * p.q_tok_stride + hq * p.q_head_stride + tid]);
-  __syncthreads();
-  const int page_mask = (1 << p.page_shift) - 1;
-  float m = -INFINITY, l = 0.0f, o = 0.0f;
-  for (int t0 = 0; t0 < len; t0 += kAttnThreads) {
-    const int t = t0 + tid;
-    float s = -INFINITY;
-    const int id = t < len ? p.table[lo * p.ld_table + (t >> p.page_shift)] : -1;
-    if (t < len && (unsigned)id >= (unsigned)p.num_pages) record_status(p.status, kStatusOffsets, 50);
-    if ((unsigned)id < (unsigned)p.num_pages) {
-      const long long blk = (long long)id * p.Hkv + h;
-      const uint8_t* k = p.k_codes + ((blk << p.page_shift) + (t & page_mask)) * D;
-      s = 0.0f;
-      for (int d = 0; d < D; ++d) s += qs[d] * e4m3_val(k[d]);
-      s *= p.k_scales[blk] * p.scale_log2;
-    }
-    float mx = s;
-    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, d));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
-    __syncthreads();
-    mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float mn = fmaxf(m, mx);
-    const float c = mn > -INFINITY ? exp2f(m - mn) : 1.0f, e = mn > -INFINITY ? exp2f(s - mn) : 0.0f;
-    ps[tid] = e;
-    float sum = e;
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
-    __syncthreads();
-    if ((tid & 31) == 0) red[tid >> 5] = sum;
-    __syncthreads();
-    l = l * c + (red[0] + red[1]) + (red[2] + red[3]);
-    o *= c;
-    m = mn;
-    if (tid < D) {
-      const int cnt = min(kAttnThreads, len - t0);
-      for (int i = 0; i < cnt; ++i) {
-        const int vid = p.table[lo * p.ld_table + ((t0 + i) >> p.page_shift)];
-        if ((unsigned)vid >= (unsigned)p.num_pages) continue;
-        const long long blk = (long long)vid * p.Hkv + h;
-        o += ps[i] * p.v_scales[blk] * e4m3_val(p.v_codes[((blk << p.page_shift) + ((t0 + i) & page_mask)) * D + tid]);
-      }
-    }
-    __syncthreads();
-  }
-  if (tid < D)
-    static_cast<__nv_bfloat16*>(p.out)[row * p.out_tok_stride + hq * p.out_head_stride + tid] =
-        __float2bfloat16(l > 0.0f ? o / l : 0.0f);
-  if (tid == 0 && p.lse)
-    p.lse[(long long)row * p.Hq + hq] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-}
-
 template <int D>
 cudaError_t launch_few(const KvAttentionLaunch& L, cudaStream_t stream) {
   constexpr int kSmem = (int)sizeof(FewSmem<D>) + 1024;
@@ -690,17 +587,7 @@ cudaError_t launch_kv_attention(const KvAttentionLaunch& L, cudaStream_t stream)
     if (e != cudaSuccess) return e;
   }
   if (p.most_rows <= kFewRows) return cudaSuccess;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.T, (unsigned)p.Hq, 1);
-  cfg.blockDim = dim3(kAttnThreads, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return p.D == 64 ? cudaLaunchKernelEx(&cfg, kv_attention_kernel<64>, p)
-                   : cudaLaunchKernelEx(&cfg, kv_attention_kernel<128>, p);
+  return launch_kv_attention_rows(L, stream);
 }
 
 }  // namespace bsk

@@ -1,0 +1,33 @@
+// kv_attention.cuh -- what the two attention kernels over the 8-bit cache share.
+#pragma once
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace bsk {
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// The power of two that brings a row with this largest element to [2^14, 2^15)
+__device__ __forceinline__ int fp16_up(float amax) {
+  const int ex = max((int)(__float_as_uint(amax) >> 23) - 127, -112);
+  return amax > 0.0f ? 14 - min(ex, 127) : 0;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// natural log of the softmax sum 2^m l
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// Cached tokens of a request, as far as its table row can name them.
+__device__ __forceinline__ int cached(const KvAttentionParams& p, int b) {
+  return min(max(p.kv_lens[b], 0), p.max_pages << p.page_shift);
+}
+}  // namespace bsk

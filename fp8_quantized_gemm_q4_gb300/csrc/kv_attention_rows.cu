@@ -1,0 +1,672 @@
+// kv_attention_rows.cu -- attention over the paged 8-bit cache for requests with
+// many rows (prompts, chunks): the mathematics is kv_attention.cu's, on tcgen05.
+//
+// A unit is 128 rows (row r = i * G + g: token i, head g of a KV head's group)
+// against its cached tokens in tiles of 128.  The codes are exact in fp16 but not
+// an operand type that fp16 may be multiplied with, so every tile is widened on
+// the way: warps read the codes from L2, convert them and write K and V^T to
+// shared memory as fp16 in the tensor core's 128-byte swizzled layout.  q and
+// the softmax weights are A operands in tensor memory and cost no shared
+// memory traffic.  Per tile and SM: 1024 clocks of MMA, 512 of writing and 512 of
+// the MMAs' reading 64 KB, 500 of exponentials, so the pieces balance where each
+// runs beside the others:
+//   warps 0-3   softmax, a thread per row: S from tensor memory, weights back
+//               into S's place, the running (m, l), rare rescaling of O
+//   warps 4-7   K codes -> fp16        warps 8-11  V codes -> fp16, transposed
+//   warp 12     MMA issue: S(j + 1) = Q K^T goes ahead of O += P(j) V
+//   warp 13     page ids and scales of the next tiles
+// The tiles of all units form one list that is cut into equal shares, one CTA
+// each; units cut between CTAs are joined by the last CTA to finish a piece.
+#include "kv_attention.cuh"
+
+namespace bsk {
+namespace {
+
+constexpr int kM = 128;           // rows of a unit
+constexpr int kN = 128;           // cached tokens of a tile
+constexpr int kGroups = kN / 16;  // groups of 16 tokens: each lies in one page
+constexpr int kThreads = 14 * 32;
+constexpr int kMinTiles = 2;      // least tiles worth a CTA of its own
+constexpr int kPageSlots = 8;     // tiles whose pages are known ahead
+constexpr int kCounters = 1024;   // arrival counters at the head of the workspace
+constexpr int kTmemCols = 512;
+// Tensor memory columns: S twice (P of a tile in the first half of its S), O, Q
+constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384;
+
+template <int D>
+struct RowsSmem {
+  alignas(1024) uint8_t k[2][kN * D * 2];  // [D / 64][token][64 columns]
+  alignas(1024) uint8_t v[2][D * kN * 2];  // [token / 64][column][64 tokens]
+  float4 page[kPageSlots][kGroups];        // page id (int, -1: none), K scale, log2 of V scale, 1 / V scale
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2];
+  uint64_t page_full[kPageSlots], page_empty[kPageSlots], o_done, q_full, drain;
+  long long scan[kThreads / 32];
+  long long start_at;
+  int start[3];
+  uint32_t tmem;
+  int abort_flag, last;
+};
+
+__device__ __forceinline__ uint32_t idesc_f16(int M, int N) {  // fp16 x fp16 -> fp32, both K-major
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// D[tmem] (+)= A[tmem] B[smem]^T
+__device__ __forceinline__ void mma_ts_f16(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A unit and where its tiles lie in the list
+struct Unit {
+  int b, h, rt;              // request, KV head, row tile
+  int row0, n, len, rts;     // the request's first row, rows, cached tokens, row tiles
+  int nt;                    // tiles
+  long long at;              // the first one's place in the list
+};
+__device__ __forceinline__ bool takes(int n, int G) { return n > 0 && (long long)n * G > kFewRows; }
+// Tiles that the unit's last row sees (one at least)
+__device__ __forceinline__ int unit_tiles(int n, int len, int G, int rt) {
+  const int last = (int)min((long long)n - 1, ((long long)rt * kM + kM - 1) / G);
+  return max(1, (len - n + last + 1 + kN - 1) / kN);
+}
+__device__ __forceinline__ void load_request(const KvAttentionParams& p, int G, Unit& u) {
+  u.row0 = p.cu_q[u.b];
+  u.n = p.cu_q[u.b + 1] - u.row0;
+  u.len = cached(p, u.b);
+  u.rts = (int)(((long long)u.n * G + kM - 1) / kM);
+}
+__device__ __forceinline__ void next_unit(const KvAttentionParams& p, int G, Unit& u) {
+  u.at += u.nt;
+  if (++u.rt == u.rts) {
+    u.rt = 0;
+    if (++u.h == p.Hkv) {
+      u.h = 0;
+      while (++u.b < p.B)
+        if (takes(p.cu_q[u.b + 1] - p.cu_q[u.b], G)) break;
+      if (u.b >= p.B) return;  // the list ends here, and so does the last share
+      load_request(p, G, u);
+    }
+  }
+  u.nt = unit_tiles(u.n, u.len, G, u.rt);
+}
+// The tiles of a share, one after the other
+struct Tiles {
+  Unit u;
+  int t, end;  // tile within the unit; the unit's end within the share
+  long long last;
+  __device__ __forceinline__ void open(long long first) {
+    t = (int)max(0ll, first - u.at);
+    end = (int)min((long long)u.nt, last - u.at);
+  }
+  __device__ __forceinline__ bool valid() const { return u.at + t < last; }
+  __device__ __forceinline__ void next(const KvAttentionParams& p, int G) {
+    if (++t < end) return;
+    next_unit(p, G, u);
+    open(u.at);
+  }
+};
+
+template <int D>
+__device__ __forceinline__ long long piece_at(int cta, int first_cta) {
+  return ((long long)cta * 2 + (cta == first_cta)) * (kM * (D + 2));
+}
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __grid_constant__ KvAttentionParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  using Smem = RowsSmem<D>;
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.Hq / p.Hkv;
+  const WaitGuard wg{&sm.abort_flag, p.status, p.wait_ns};
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.k_full[s], 4);
+      mbar_init(&sm.v_full[s], 4);
+      mbar_init(&sm.k_empty[s], 1);
+      mbar_init(&sm.v_empty[s], 1);
+      mbar_init(&sm.s_full[s], 1);
+      mbar_init(&sm.p_full[s], 4);
+    }
+    for (int s = 0; s < kPageSlots; ++s) {
+      mbar_init(&sm.page_full[s], 1);
+      mbar_init(&sm.page_empty[s], 12);
+    }
+    mbar_init(&sm.o_done, 1);
+    mbar_init(&sm.q_full, 4);
+    mbar_init(&sm.drain, 1);
+    fence_barrier_init();
+    sm.abort_flag = 0;
+  }
+  if (warp == 12) {
+    tmem_alloc(&sm.tmem, kTmemCols);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // Each thread sums the tiles of `per` requests in a row; the one whose
+  // requests hold the share's first tile finds its unit.
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  auto request_tiles = [&](int b) {  // of one KV head
+    const int n = p.cu_q[b + 1] - p.cu_q[b];
+    if (!takes(n, G)) return 0ll;
+    const int len = cached(p, b);
+    const int rts = (int)(((long long)n * G + kM - 1) / kM);
+    long long x = 0;
+    for (int rt = 0; rt < rts; ++rt) x += unit_tiles(n, len, G, rt);
+    return x;
+  };
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    mine += request_tiles(b);
+    if ((long long)(p.cu_q[b + 1] - p.cu_q[b]) * G > p.most_rows) record_status(p.status, kStatusOffsets, 53);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long v = __shfl_up_sync(kFullMask, incl, d);
+    if (lane >= d) incl += v;
+  }
+  if (lane == 31) sm.scan[warp] = incl;
+  __syncthreads();
+  tc_fence_after();
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sm.scan[w];
+    total += sm.scan[w];
+  }
+  total *= p.Hkv;
+  before *= p.Hkv;
+  const int shares = (int)min((long long)gridDim.x, (total + kMinTiles - 1) / kMinTiles);
+  const bool works = (int)blockIdx.x < shares;
+  const long long t_first = works ? total * blockIdx.x / shares : 0;
+  const long long t_last = works ? total * (blockIdx.x + 1) / shares : 0;
+  if (works && t_first >= before && t_first < before + mine * p.Hkv) {
+    long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      const long long x = request_tiles(b);
+      if (x && t_first < at + x * p.Hkv) {
+        const int h = (int)((t_first - at) / x);
+        at += h * x;
+        const int n = p.cu_q[b + 1] - p.cu_q[b], len = cached(p, b);
+        int rt = 0;
+        for (;; ++rt) {
+          const int nt = unit_tiles(n, len, G, rt);
+          if (t_first < at + nt) break;
+          at += nt;
+        }
+        sm.start[0] = b;
+        sm.start[1] = h;
+        sm.start[2] = rt;
+        sm.start_at = at;
+        break;
+      }
+      at += x * p.Hkv;
+    }
+  }
+  __syncthreads();
+  const uint32_t tmem = sm.tmem;
+
+  Tiles it;
+  if (works) {
+    it.u.b = sm.start[0];
+    it.u.h = sm.start[1];
+    it.u.rt = sm.start[2];
+    it.u.at = sm.start_at;
+    it.last = t_last;
+    load_request(p, G, it.u);
+    it.u.nt = unit_tiles(it.u.n, it.u.len, G, it.u.rt);
+    it.open(t_first);
+  } else {
+    it.u.at = it.last = 0;
+    it.t = 0;
+  }
+  uint32_t c = 0;  // tiles of the share so far: ring places and phases follow from it in every role
+
+  if (warp < 4) {
+    // ------------------------------------------------------------ softmax: a thread per row
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    uint32_t unit = 0;
+    while (it.valid()) {
+      __syncwarp();
+      const Unit u = it.u;
+      const int t0 = it.t, t1 = it.end;
+      const long long r = (long long)u.rt * kM + tid;
+      const int i = (int)(r / G), hq = u.h * G + (int)(r % G);
+      const bool in = r < (long long)u.n * G && u.row0 + i < p.T;
+      const int seen = in ? u.len - u.n + i + 1 : 0;
+      float qscale;
+      {
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (u.row0 + (long long)i) * p.q_tok_stride + hq * p.q_head_stride;
+        uint32_t w[D / 2];
+        float amax = 0.0f;
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) {
+          const uint4 v = in ? reinterpret_cast<const uint4*>(q)[x] : make_uint4(0, 0, 0, 0);
+          w[4 * x] = v.x, w[4 * x + 1] = v.y, w[4 * x + 2] = v.z, w[4 * x + 3] = v.w;
+        }
+#pragma unroll
+        for (int x = 0; x < D / 2; ++x)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[x] << 16)), fabsf(__uint_as_float(w[x] & 0xffff0000u))));
+        const int up = fp16_up(amax);
+        const float mul = exp2i(up);
+        qscale = exp2i(-up) * p.scale_log2;
+#pragma unroll
+        for (int x = 0; x < D / 2; ++x)
+          w[x] = pack_f16x2(__uint_as_float(w[x] << 16) * mul, __uint_as_float(w[x] & 0xffff0000u) * mul);
+#pragma unroll
+        for (int x = 0; x < D / 2; x += 16) tmem_st16(lanes + kColQ + x, w + x);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_full);
+      }
+      float m = -INFINITY, l = 0.0f;
+      for (int t = t0; t < t1; ++t, ++c) {
+        const uint32_t sb = c & 1, slot = c % kPageSlots;
+        mbar_wait(&sm.page_full[slot], (c / kPageSlots) & 1, wg, 60);
+        mbar_wait(&sm.s_full[sb], (c >> 1) & 1, wg, 61);
+        tc_fence_after();
+        const uint32_t s_at = lanes + kColS + sb * kN;
+        const int limit = seen - t * kN;  // columns that this row sees
+        const bool cut = __any_sync(kFullMask, limit < kN);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < kN / 32; ++x) {
+          uint32_t raw[32];
+          tmem_ld32(s_at + 32 * x, raw);
+          tmem_ld_wait();
+          if (cut) {
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (32 * x + y >= limit) raw[y] = __float_as_uint(-INFINITY);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float4 pg = sm.page[slot][2 * x + h];
+            float g = __uint_as_float(raw[16 * h]);
+#pragma unroll
+            for (int y = 1; y < 16; ++y) g = fmaxf(g, __uint_as_float(raw[16 * h + y]));
+            mx = fmaxf(mx, fmaf(g, qscale * pg.y, pg.z));
+          }
+        }
+        bool waited = t == t0;  // o_done of the tile before: none, or not waited for yet
+        if (__any_sync(kFullMask, mx > m + 8.0f)) {
+          const bool up = mx > m + 8.0f;
+          const float f = up ? ex2(m - mx) : 1.0f;
+          m = up ? mx : m;
+          l *= f;
+          if (t > t0) {
+            mbar_wait(&sm.o_done, (c - 1) & 1, wg, 62);
+            waited = true;
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) {
+              uint32_t o[32];
+              tmem_ld32(lanes + kColO + 32 * x, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tmem_st16(lanes + kColO + 32 * x, o);
+              tmem_st16(lanes + kColO + 32 * x + 16, o + 16);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int x = 0; x < kN / 32; ++x) {
+          uint32_t raw[32], w[16];
+          tmem_ld32(s_at + 32 * x, raw);
+          tmem_ld_wait();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float4 pg = sm.page[slot][2 * x + h];
+            const float f = qscale * pg.y, off = pg.z - ref;
+            float sum = 0.0f;
+#pragma unroll
+            for (int y = 0; y < 16; y += 2) {
+              float a = ex2(fmaf(__uint_as_float(raw[16 * h + y]), f, off));
+              float b = ex2(fmaf(__uint_as_float(raw[16 * h + y + 1]), f, off));
+              if (cut) {
+                a = 32 * x + 16 * h + y < limit ? a : 0.0f;
+                b = 32 * x + 16 * h + y + 1 < limit ? b : 0.0f;
+              }
+              sum += a + b;
+              w[8 * h + y / 2] = pack_f16x2(a, b);
+            }
+            l = fmaf(sum, pg.w, l);
+          }
+          tmem_st16(s_at + 16 * x, w);
+        }
+        tmem_st_wait();
+        // every phase of o_done is waited for in turn; the product of this tile
+        // could not begin before that of the last one anyway
+        if (!waited) mbar_wait(&sm.o_done, (c - 1) & 1, wg, 63);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.p_full[sb]);
+          mbar_arrive(&sm.page_empty[slot]);
+        }
+      }
+      // ---- the unit's rows
+      mbar_wait(&sm.o_done, (c - 1) & 1, wg, 64);
+      tc_fence_after();
+      const bool alone = t0 == 0 && t1 == u.nt;
+      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (u.row0 + (long long)i) * p.out_tok_stride + hq * p.out_head_stride;
+      float* slot = p.work + ((long long)blockIdx.x * 2 + (t0 == 0)) * (kM * (D + 2));
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) {
+        uint32_t o[32];
+        tmem_ld32(lanes + kColO + 32 * x, o);
+        tmem_ld_wait();
+        if (in && alone) {
+#pragma unroll
+          for (int y = 0; y < 32; y += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              w[z] = pack_bf16x2(__uint_as_float(o[y + 2 * z]) * inv, __uint_as_float(o[y + 2 * z + 1]) * inv);
+            *reinterpret_cast<uint4*>(dst + 32 * x + y) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else if (in) {
+#pragma unroll
+          for (int y = 0; y < 32; y += 4)
+            *reinterpret_cast<uint4*>(slot + tid * D + 32 * x + y) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      const long long lse_at = (u.row0 + (long long)i) * p.Hq + hq;
+      if (alone) {
+        if (in && p.lse) p.lse[lse_at] = lse_of(m, l);
+      } else {
+        if (in) *reinterpret_cast<float2*>(slot + kM * D + 2 * tid) = make_float2(m, l);
+        __threadfence();
+        const int c0 = (int)(((u.at + 1) * shares - 1) / total), c1 = (int)(((u.at + u.nt) * shares - 1) / total);
+        softmax_sync();
+        if (tid == 0) {
+          const int old = atomicAdd(p.counters + c0, 1);
+          __threadfence();
+          sm.last = old == c1 - c0;
+          if (sm.last) p.counters[c0] = 0;
+        }
+        softmax_sync();
+        if (sm.last && in) {
+          float mx = -INFINITY, sum = 0.0f;
+          for (int x = c0; x <= c1; ++x) mx = fmaxf(mx, __ldcg(p.work + piece_at<D>(x, c0) + kM * D + 2 * tid));
+          const float ref = mx == -INFINITY ? 0.0f : mx;
+          for (int x = c0; x <= c1; ++x) {
+            const float2 e = __ldcg(reinterpret_cast<const float2*>(p.work + piece_at<D>(x, c0) + kM * D + 2 * tid));
+            sum += e.y * ex2(e.x - ref);
+          }
+          const float by = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll 1
+          for (int d = 0; d < D; d += 32) {
+            float acc[32] = {};
+            for (int x = c0; x <= c1; ++x) {
+              const float* from = p.work + piece_at<D>(x, c0);
+              const float f = ex2(__ldcg(from + kM * D + 2 * tid) - ref);
+#pragma unroll
+              for (int y = 0; y < 32; y += 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(from + tid * D + d + y));
+                acc[y] += f * v.x, acc[y + 1] += f * v.y, acc[y + 2] += f * v.z, acc[y + 3] += f * v.w;
+              }
+            }
+#pragma unroll
+            for (int y = 0; y < 32; y += 8)
+              *reinterpret_cast<uint4*>(dst + d + y) =
+                  make_uint4(pack_bf16x2(acc[y] * by, acc[y + 1] * by), pack_bf16x2(acc[y + 2] * by, acc[y + 3] * by),
+                             pack_bf16x2(acc[y + 4] * by, acc[y + 5] * by), pack_bf16x2(acc[y + 6] * by, acc[y + 7] * by));
+          }
+          if (p.lse) p.lse[lse_at] = lse_of(mx, sum);
+        }
+      }
+      ++unit;
+      next_unit(p, G, it.u);
+      it.open(it.u.at);
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ K codes -> fp16
+    // Lane: 16 codes of a token (and the token's place among its warp's), such
+    // that eight lanes in a row store to eight different chunks.
+    constexpr int kSteps = kN * D / (128 * 16);           // 16-byte loads per thread
+    constexpr int kStepTokens = kN / kSteps;
+    const int w = warp - 4, q = lane & 3;
+    const int panel = D == 128 ? (lane >> 3) & 1 : 0;
+    const int tok = D == 128 ? w * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1) : w * 8 + (lane >> 2);
+    uint4 raw[kSteps];
+    auto load = [&](uint32_t c) {
+      const uint32_t slot = c % kPageSlots;
+      mbar_wait(&sm.page_full[slot], (c / kPageSlots) & 1, wg, 65);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int x = s * kStepTokens + tok, token = it.t * kN + x;
+        const int id = __float_as_int(sm.page[slot][x >> 4].x);
+        raw[s] = make_uint4(0, 0, 0, 0);
+        if (id >= 0 && token < it.u.len)
+          raw[s] = __ldg(reinterpret_cast<const uint4*>(
+              p.k_codes + ((((long long)id * p.Hkv + it.u.h) << p.page_shift) + (token & ((1 << p.page_shift) - 1))) * D +
+              64 * panel + 16 * q));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.page_empty[slot]);
+    };
+    if (it.valid()) load(0);
+    while (it.valid()) {
+      const uint32_t kb = c & 1;
+      uint4 now[kSteps];
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) now[s] = raw[s];
+      it.next(p, G);
+      if (it.valid()) load(c + 1);
+      mbar_wait(&sm.k_empty[kb], ((c >> 1) & 1) ^ 1, wg, 66);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int x = s * kStepTokens + tok;
+        const uint32_t row = smem_u32(sm.k[kb]) + panel * (kN * 128) + x * 128;
+        const uint32_t in[4] = {now[s].x, now[s].y, now[s].z, now[s].w};
+        uint32_t h[8];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          h[2 * y] = e4m3x2_to_f16x2((uint16_t)in[y]);
+          h[2 * y + 1] = e4m3x2_to_f16x2((uint16_t)(in[y] >> 16));
+        }
+        st_shared_v4(row + (((2 * q) ^ (x & 7)) << 4), h[0], h[1], h[2], h[3]);
+        st_shared_v4(row + (((2 * q + 1) ^ (x & 7)) << 4), h[4], h[5], h[6], h[7]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.k_full[kb]);
+      ++c;
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ V codes -> fp16, transposed
+    // Lane: 8 tokens x 4 columns, as eight 4-byte loads; four lanes share their
+    // columns and take four token groups of 8 in a row.
+    constexpr int kSteps = D / 32;                         // blocks of 32 tokens x 32 columns per warp
+    const int w = warp - 8, tl = lane & 3, dl = lane >> 2;
+    const int col = 32 * (w % (D / 32)) + 4 * dl, first = D == 128 ? 0 : 2 * (w >> 1);
+    uint32_t raw[kSteps][8];
+    auto load = [&](uint32_t c) {
+      const uint32_t slot = c % kPageSlots;
+      mbar_wait(&sm.page_full[slot], (c / kPageSlots) & 1, wg, 67);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int x = 32 * (first + s) + 8 * tl, token = it.t * kN + x;
+        const int id = __float_as_int(sm.page[slot][x >> 4].x);
+        const uint8_t* v = p.v_codes + ((((long long)id * p.Hkv + it.u.h) << p.page_shift) + (token & ((1 << p.page_shift) - 1))) * D + col;
+#pragma unroll
+        for (int y = 0; y < 8; ++y)
+          raw[s][y] = id >= 0 && token + y < it.u.len ? __ldg(reinterpret_cast<const uint32_t*>(v + y * D)) : 0u;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.page_empty[slot]);
+    };
+    if (it.valid()) load(0);
+    while (it.valid()) {
+      const uint32_t vb = c & 1;
+      uint32_t now[kSteps][8];
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int y = 0; y < 8; ++y) now[s][y] = raw[s][y];
+      it.next(p, G);
+      if (it.valid()) load(c + 1);
+      mbar_wait(&sm.v_empty[vb], ((c >> 1) & 1) ^ 1, wg, 68);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int block = first + s, chunk = (block & 1) * 4 + tl;
+        const uint32_t base = smem_u32(sm.v[vb]) + (block >> 1) * (D * 128);
+        uint32_t h[4][4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {  // tokens 2 y, 2 y + 1: columns 0, 1 and 2, 3 in pairs of tokens
+          const uint32_t a = __byte_perm(now[s][2 * y], now[s][2 * y + 1], 0x5140);
+          const uint32_t b = __byte_perm(now[s][2 * y], now[s][2 * y + 1], 0x7362);
+          h[0][y] = e4m3x2_to_f16x2((uint16_t)a);
+          h[1][y] = e4m3x2_to_f16x2((uint16_t)(a >> 16));
+          h[2][y] = e4m3x2_to_f16x2((uint16_t)b);
+          h[3][y] = e4m3x2_to_f16x2((uint16_t)(b >> 16));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          st_shared_v4(base + (col + e) * 128 + ((chunk ^ ((col + e) & 7)) << 4), h[e][0], h[e][1], h[e][2], h[e][3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.v_full[vb]);
+      ++c;
+    }
+  } else if (warp == 12) {
+    // ------------------------------------------------------------ MMA issue
+    constexpr uint32_t kPanelK = kN * 128, kPanelV = D * 128;
+    const uint32_t idesc_s = idesc_f16(kM, kN), idesc_o = idesc_f16(kM, D);
+    uint32_t unit = 0;
+    bool ok = true;
+    auto scores = [&](uint32_t c) {  // S(c) = Q K(c)^T
+      const uint32_t b = c & 1;
+      ok = ok && mbar_wait_warp(&sm.k_full[b], (c >> 1) & 1, wg, 69);
+      if (!ok) return;
+      tc_fence_after();
+      const uint64_t dk = smem_desc(smem_u32(sm.k[b]), 16, 1024, kLayoutSw128);
+      if (elect_one()) {
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+          mma_ts_f16(tmem + kColS + b * kN, tmem + kColQ + 8 * x, dk + (x / 4) * (kPanelK >> 4) + 2 * (x % 4), idesc_s, x > 0);
+        tc_commit(&sm.k_empty[b]);
+        tc_commit(&sm.s_full[b]);
+      }
+      __syncwarp();
+    };
+    while (it.valid()) {
+      const int t0 = it.t, t1 = it.end;
+      ok = ok && mbar_wait_warp(&sm.q_full, unit & 1, wg, 70);
+      tc_fence_after();
+      scores(c);
+      for (int t = t0; t < t1; ++t, ++c) {
+        // S(c + 1) goes where P(c - 1) was: its product has been issued before
+        if (t + 1 < t1) scores(c + 1);
+        const uint32_t b = c & 1;
+        ok = ok && mbar_wait_warp(&sm.v_full[b], (c >> 1) & 1, wg, 71);
+        ok = ok && mbar_wait_warp(&sm.p_full[b], (c >> 1) & 1, wg, 72);
+        if (!ok) continue;
+        tc_fence_after();
+        const uint64_t dv = smem_desc(smem_u32(sm.v[b]), 16, 1024, kLayoutSw128);
+        if (elect_one()) {
+#pragma unroll
+          for (int x = 0; x < kN / 16; ++x)
+            mma_ts_f16(tmem + kColO, tmem + kColS + b * kN + 8 * x, dv + (x / 4) * (kPanelV >> 4) + 2 * (x % 4), idesc_o,
+                       t > t0 || x > 0);
+          tc_commit(&sm.v_empty[b]);
+          tc_commit(&sm.o_done);
+        }
+        __syncwarp();
+      }
+      ++unit;
+      next_unit(p, G, it.u);
+      it.open(it.u.at);
+    }
+    if (elect_one()) {
+      tc_commit(&sm.drain);
+      mbar_drain(&sm.drain, 0, 1000000000ull);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ page ids and scales, four tiles at a time
+    while (it.valid()) {
+      const Unit u = it.u;
+      for (int t = it.t; t < it.end; t += 4) {
+        const int j = lane & 7, tt = t + (lane >> 3), token = tt * kN + 16 * j;
+        int id = -1;
+        float ks = 0.0f, log_vs = -INFINITY, inv_vs = 0.0f;
+        if (tt < it.end && token < u.len) {
+          id = p.table[u.b * p.ld_table + (token >> p.page_shift)];
+          if ((unsigned)id >= (unsigned)p.num_pages) {
+            record_status(p.status, kStatusOffsets, 50);
+            id = -1;
+          } else {
+            ks = p.k_scales[(long long)id * p.Hkv + u.h];
+            const float vs = p.v_scales[(long long)id * p.Hkv + u.h];
+            log_vs = log2f(vs);
+            inv_vs = 1.0f / vs;
+          }
+        }
+        for (int x = 0; x < 4 && t + x < it.end; ++x, ++c) {
+          const uint32_t slot = c % kPageSlots;
+          mbar_wait(&sm.page_empty[slot], ((c / kPageSlots) & 1) ^ 1, wg, 73);
+          if (lane >> 3 == x) sm.page[slot][j] = make_float4(__int_as_float(id), ks, log_vs, inv_vs);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.page_full[slot]);
+        }
+      }
+      next_unit(p, G, it.u);
+      it.open(it.u.at);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D>
+cudaError_t launch(const KvAttentionLaunch& L, cudaStream_t stream) {
+  // more than half of an SM's shared memory: one CTA an SM, as tensor memory has it
+  constexpr int kNeed = (int)sizeof(RowsSmem<D>) + 1024, kSmem = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(kv_attention_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (attr != cudaSuccess) return attr;
+  return launch_kernel(kv_attention_rows_kernel<D>, (unsigned)L.rows_grid, kThreads, kSmem, stream, 1, L.p);
+}
+
+}  // namespace
+
+int kv_attention_rows_grid(int sms) { return sms < kCounters ? sms : kCounters; }
+size_t kv_attention_rows_piece_bytes(int D) { return (size_t)2 * kM * (D + 2) * sizeof(float); }
+
+cudaError_t launch_kv_attention_rows(const KvAttentionLaunch& L, cudaStream_t stream) {
+  return L.p.D == 64 ? launch<64>(L, stream) : launch<128>(L, stream);
+}
+
+}  // namespace bsk
