@@ -67,6 +67,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // A unit and where its tiles lie in the list
@@ -256,24 +261,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       float qscale;
       {
         const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (u.row0 + (long long)i) * p.q_tok_stride + hq * p.q_head_stride;
-        uint32_t w[D / 2];
         float amax = 0.0f;
-#pragma unroll
+#pragma unroll 4
         for (int x = 0; x < D / 8; ++x) {
           const uint4 v = in ? reinterpret_cast<const uint4*>(q)[x] : make_uint4(0, 0, 0, 0);
-          w[4 * x] = v.x, w[4 * x + 1] = v.y, w[4 * x + 2] = v.z, w[4 * x + 3] = v.w;
-        }
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int x = 0; x < D / 2; ++x)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[x] << 16)), fabsf(__uint_as_float(w[x] & 0xffff0000u))));
+          for (int y = 0; y < 4; ++y)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[y] << 16)), fabsf(__uint_as_float(w[y] & 0xffff0000u))));
+        }
         const int up = fp16_up(amax);
         const float mul = exp2i(up);
         qscale = exp2i(-up) * p.scale_log2;
+#pragma unroll 1
+        for (int x = 0; x < D / 32; ++x) {
+          uint32_t w[16];
 #pragma unroll
-        for (int x = 0; x < D / 2; ++x)
-          w[x] = pack_f16x2(__uint_as_float(w[x] << 16) * mul, __uint_as_float(w[x] & 0xffff0000u) * mul);
+          for (int y = 0; y < 4; ++y) {
+            const uint4 v = in ? reinterpret_cast<const uint4*>(q)[4 * x + y] : make_uint4(0, 0, 0, 0);
+            w[4 * y] = v.x, w[4 * y + 1] = v.y, w[4 * y + 2] = v.z, w[4 * y + 3] = v.w;
+          }
 #pragma unroll
-        for (int x = 0; x < D / 2; x += 16) tmem_st16(lanes + kColQ + x, w + x);
+          for (int y = 0; y < 16; ++y)
+            w[y] = pack_f16x2(__uint_as_float(w[y] << 16) * mul, __uint_as_float(w[y] & 0xffff0000u) * mul);
+          tmem_st16(lanes + kColQ + 16 * x, w);
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -288,20 +300,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         const uint32_t s_at = lanes + kColS + sb * kN;
         const int limit = seen - t * kN;  // columns that this row sees
         const bool cut = __any_sync(kFullMask, limit < kN);
+        // The loops over S stay rolled: unrolled, the four softmax warps waited
+        // for instructions most of the time.
         float mx = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < kN / 32; ++x) {
-          uint32_t raw[32];
-          tmem_ld32(s_at + 32 * x, raw);
+#pragma unroll 1
+        for (int x = 0; x < kN; x += 64) {
+          uint32_t raw[64];
+          tmem_ld_cols<64>(s_at + x, raw);
           tmem_ld_wait();
           if (cut) {
 #pragma unroll
-            for (int y = 0; y < 32; ++y)
-              if (32 * x + y >= limit) raw[y] = __float_as_uint(-INFINITY);
+            for (int y = 0; y < 64; ++y)
+              if (x + y >= limit) raw[y] = __float_as_uint(-INFINITY);
           }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float4 pg = sm.page[slot][2 * x + h];
+          for (int h = 0; h < 4; ++h) {
+            const float4 pg = sm.page[slot][x / 16 + h];
             float g = __uint_as_float(raw[16 * h]);
 #pragma unroll
             for (int y = 1; y < 16; ++y) g = fmaxf(g, __uint_as_float(raw[16 * h + y]));
@@ -318,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             mbar_wait(&sm.o_done, (c - 1) & 1, wg, 62);
             waited = true;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < D / 32; ++x) {
               uint32_t o[32];
               tmem_ld32(lanes + kColO + 32 * x, o);
@@ -331,30 +345,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
           }
         }
         const float ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-        for (int x = 0; x < kN / 32; ++x) {
-          uint32_t raw[32], w[16];
-          tmem_ld32(s_at + 32 * x, raw);
+#pragma unroll 1
+        for (int x = 0; x < kN; x += 64) {
+          uint32_t raw[64];
+          tmem_ld_cols<64>(s_at + x, raw);
           tmem_ld_wait();
+          if (cut) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float4 pg = sm.page[slot][2 * x + h];
-            const float f = qscale * pg.y, off = pg.z - ref;
-            float sum = 0.0f;
+            for (int y = 0; y < 64; ++y)
+              if (x + y >= limit) raw[y] = __float_as_uint(-INFINITY);
+          }
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const float4 pg = sm.page[slot][x / 16 + h];
+            // a scale is positive, or 0 with pg.z = -infinity: masked scores must not meet the 0
+            const float f = fmaxf(qscale * pg.y, 1e-37f), off = pg.z - ref;
+            float s0 = 0.0f, s1 = 0.0f;
+            uint32_t w[8];
 #pragma unroll
             for (int y = 0; y < 16; y += 2) {
-              float a = ex2(fmaf(__uint_as_float(raw[16 * h + y]), f, off));
-              float b = ex2(fmaf(__uint_as_float(raw[16 * h + y + 1]), f, off));
-              if (cut) {
-                a = 32 * x + 16 * h + y < limit ? a : 0.0f;
-                b = 32 * x + 16 * h + y + 1 < limit ? b : 0.0f;
-              }
-              sum += a + b;
-              w[8 * h + y / 2] = pack_f16x2(a, b);
+              const float a = ex2(fmaf(__uint_as_float(raw[16 * h + y]), f, off));
+              const float b = ex2(fmaf(__uint_as_float(raw[16 * h + y + 1]), f, off));
+              s0 += a, s1 += b;
+              w[y / 2] = pack_f16x2(a, b);
             }
-            l = fmaf(sum, pg.w, l);
+            l = fmaf(s0 + s1, pg.w, l);
+            tmem_st8(s_at + x / 2 + 8 * h, w);
           }
-          tmem_st16(s_at + 16 * x, w);
         }
         tmem_st_wait();
         // every phase of o_done is waited for in turn; the product of this tile
@@ -374,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (u.row0 + (long long)i) * p.out_tok_stride + hq * p.out_head_stride;
       float* slot = p.work + ((long long)blockIdx.x * 2 + (t0 == 0)) * (kM * (D + 2));
-#pragma unroll
+#pragma unroll 1
       for (int x = 0; x < D / 32; ++x) {
         uint32_t o[32];
         tmem_ld32(lanes + kColO + 32 * x, o);
