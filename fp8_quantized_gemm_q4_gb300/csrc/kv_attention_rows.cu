@@ -37,7 +37,7 @@ template <int D>
 struct RowsSmem {
   alignas(1024) uint8_t k[2][kN * D * 2];  // [D / 64][token][64 columns]
   alignas(1024) uint8_t v[2][D * kN * 2];  // [token / 64][column][64 tokens]
-  float4 page[kPageSlots][kGroups];        // page id (int, -1: none), K scale, log2 of V scale, 1 / V scale
+  float4 page[kPageSlots][kGroups];        // first row of codes (int, -1: none), K scale, log2 of V scale, 1 / V scale
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2];
   uint64_t page_full[kPageSlots], page_empty[kPageSlots], o_done, q_full, drain;
   long long scan[kThreads / 32];
@@ -127,6 +127,11 @@ struct Tiles {
 template <int D>
 __device__ __forceinline__ long long piece_at(int cta, int first_cta) {
   return ((long long)cta * 2 + (cta == first_cta)) * (kM * (D + 2));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -249,48 +254,55 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
   if (warp < 4) {
     // ------------------------------------------------------------ softmax: a thread per row
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    uint32_t unit = 0;
-    while (it.valid()) {
+    // this thread's row of a unit
+    struct Row {
+      int i, hq;     // token, query head
+      bool in;
+      float qscale;
+    };
+    auto load_q = [&](const Unit& u) {  // q to tensor memory, fp16 by a power of two
+      Row w;
+      const long long r = (long long)u.rt * kM + tid;
+      w.i = (int)(r / G), w.hq = u.h * G + (int)(r % G);
+      w.in = r < (long long)u.n * G && u.row0 + w.i < p.T;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (u.row0 + (long long)w.i) * p.q_tok_stride + w.hq * p.q_head_stride;
+      uint4 v[D / 8];
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x) v[x] = w.in ? __ldg(reinterpret_cast<const uint4*>(q) + x) : make_uint4(0, 0, 0, 0);
+      float amax = 0.0f;
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x) {
+        const uint32_t y[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(y[z] << 16)), fabsf(__uint_as_float(y[z] & 0xffff0000u))));
+      }
+      const int up = fp16_up(amax);
+      const float mul = exp2i(up);
+      w.qscale = exp2i(-up) * p.scale_log2;
+#pragma unroll
+      for (int x = 0; x < D / 8; x += 2) {
+        const uint32_t y[8] = {v[x].x, v[x].y, v[x].z, v[x].w, v[x + 1].x, v[x + 1].y, v[x + 1].z, v[x + 1].w};
+        uint32_t h[8];
+#pragma unroll
+        for (int z = 0; z < 8; ++z)
+          h[z] = pack_f16x2(__uint_as_float(y[z] << 16) * mul, __uint_as_float(y[z] & 0xffff0000u) * mul);
+        tmem_st8(lanes + kColQ + 4 * x, h);
+      }
+      tmem_st_wait();
+      tc_fence_before();
       __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full);
+      return w;
+    };
+    Row row = {};
+    if (it.valid()) row = load_q(it.u);
+    while (it.valid()) {
       const Unit u = it.u;
       const int t0 = it.t, t1 = it.end;
-      const long long r = (long long)u.rt * kM + tid;
-      const int i = (int)(r / G), hq = u.h * G + (int)(r % G);
-      const bool in = r < (long long)u.n * G && u.row0 + i < p.T;
-      const int seen = in ? u.len - u.n + i + 1 : 0;
-      float qscale;
-      {
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (u.row0 + (long long)i) * p.q_tok_stride + hq * p.q_head_stride;
-        float amax = 0.0f;
-#pragma unroll 4
-        for (int x = 0; x < D / 8; ++x) {
-          const uint4 v = in ? reinterpret_cast<const uint4*>(q)[x] : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[y] << 16)), fabsf(__uint_as_float(w[y] & 0xffff0000u))));
-        }
-        const int up = fp16_up(amax);
-        const float mul = exp2i(up);
-        qscale = exp2i(-up) * p.scale_log2;
-#pragma unroll 1
-        for (int x = 0; x < D / 32; ++x) {
-          uint32_t w[16];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const uint4 v = in ? reinterpret_cast<const uint4*>(q)[4 * x + y] : make_uint4(0, 0, 0, 0);
-            w[4 * y] = v.x, w[4 * y + 1] = v.y, w[4 * y + 2] = v.z, w[4 * y + 3] = v.w;
-          }
-#pragma unroll
-          for (int y = 0; y < 16; ++y)
-            w[y] = pack_f16x2(__uint_as_float(w[y] << 16) * mul, __uint_as_float(w[y] & 0xffff0000u) * mul);
-          tmem_st16(lanes + kColQ + 16 * x, w);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_full);
-      }
+      const bool in = row.in;
+      const float qscale = row.qscale;
+      const int seen = in ? u.len - u.n + row.i + 1 : 0;
       float m = -INFINITY, l = 0.0f;
       for (int t = t0; t < t1; ++t, ++c) {
         const uint32_t sb = c & 1, slot = c % kPageSlots;
@@ -299,26 +311,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         tc_fence_after();
         const uint32_t s_at = lanes + kColS + sb * kN;
         const int limit = seen - t * kN;  // columns that this row sees
-        const bool cut = __any_sync(kFullMask, limit < kN);
-        // The loops over S stay rolled: unrolled, the four softmax warps waited
-        // for instructions most of the time.
+        // The loops over S stay rolled and short: unrolled, the softmax warps
+        // waited for instructions most of the time.
+        if (__any_sync(kFullMask, limit < kN)) {
+#pragma unroll 1
+          for (int x = 0; x < kN; x += 16) {
+            uint32_t raw[16];
+            tmem_ld16(s_at + x, raw);
+            tmem_ld_wait();
+#pragma unroll
+            for (int y = 0; y < 16; ++y)
+              if (x + y >= limit) raw[y] = __float_as_uint(-INFINITY);
+            tmem_st16(s_at + x, raw);
+          }
+          tmem_st_wait();
+        }
         float mx = -INFINITY;
 #pragma unroll 1
-        for (int x = 0; x < kN; x += 64) {
-          uint32_t raw[64];
-          tmem_ld_cols<64>(s_at + x, raw);
+        for (int x = 0; x < kN; x += 32) {
+          uint32_t raw[32];
+          tmem_ld32(s_at + x, raw);
           tmem_ld_wait();
-          if (cut) {
 #pragma unroll
-            for (int y = 0; y < 64; ++y)
-              if (x + y >= limit) raw[y] = __float_as_uint(-INFINITY);
-          }
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
+          for (int h = 0; h < 2; ++h) {
             const float4 pg = sm.page[slot][x / 16 + h];
             float g = __uint_as_float(raw[16 * h]);
 #pragma unroll
-            for (int y = 1; y < 16; ++y) g = fmaxf(g, __uint_as_float(raw[16 * h + y]));
+            for (int y = 1; y < 15; y += 2)
+              g = max3(g, __uint_as_float(raw[16 * h + y]), __uint_as_float(raw[16 * h + y + 1]));
+            g = fmaxf(g, __uint_as_float(raw[16 * h + 15]));
             mx = fmaxf(mx, fmaf(g, qscale * pg.y, pg.z));
           }
         }
@@ -346,32 +367,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         }
         const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll 1
-        for (int x = 0; x < kN; x += 64) {
-          uint32_t raw[64];
-          tmem_ld_cols<64>(s_at + x, raw);
+        for (int x = 0; x < kN; x += 32) {
+          uint32_t raw[32], w[16];
+          tmem_ld32(s_at + x, raw);
           tmem_ld_wait();
-          if (cut) {
 #pragma unroll
-            for (int y = 0; y < 64; ++y)
-              if (x + y >= limit) raw[y] = __float_as_uint(-INFINITY);
-          }
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
+          for (int h = 0; h < 2; ++h) {
             const float4 pg = sm.page[slot][x / 16 + h];
             // a scale is positive, or 0 with pg.z = -infinity: masked scores must not meet the 0
-            const float f = fmaxf(qscale * pg.y, 1e-37f), off = pg.z - ref;
-            float s0 = 0.0f, s1 = 0.0f;
-            uint32_t w[8];
+            const float f1 = fmaxf(qscale * pg.y, 1e-37f), o1 = pg.z - ref;
+            const float2 f = make_float2(f1, f1), off = make_float2(o1, o1);
+            float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int y = 0; y < 16; y += 2) {
-              const float a = ex2(fmaf(__uint_as_float(raw[16 * h + y]), f, off));
-              const float b = ex2(fmaf(__uint_as_float(raw[16 * h + y + 1]), f, off));
-              s0 += a, s1 += b;
-              w[y / 2] = pack_f16x2(a, b);
+              const float2 z = __ffma2_rn(make_float2(__uint_as_float(raw[16 * h + y]), __uint_as_float(raw[16 * h + y + 1])), f, off);
+              const float2 e = make_float2(ex2(z.x), ex2(z.y));
+              sum = __fadd2_rn(sum, e);
+              w[8 * h + y / 2] = pack_f16x2(e.x, e.y);
             }
-            l = fmaf(s0 + s1, pg.w, l);
-            tmem_st8(s_at + x / 2 + 8 * h, w);
+            l = fmaf(sum.x + sum.y, pg.w, l);
           }
+          tmem_st16(s_at + x / 2, w);
         }
         tmem_st_wait();
         // every phase of o_done is waited for in turn; the product of this tile
@@ -384,12 +400,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
           mbar_arrive(&sm.page_empty[slot]);
         }
       }
-      // ---- the unit's rows
+      // ---- the unit's rows.  Its scores are done: the next unit's q goes first,
+      // so that the next scores run beside what follows.
+      const Row was = row;
+      next_unit(p, G, it.u);
+      it.open(it.u.at);
+      __syncwarp();
+      if (it.valid()) row = load_q(it.u);
       mbar_wait(&sm.o_done, (c - 1) & 1, wg, 64);
       tc_fence_after();
       const bool alone = t0 == 0 && t1 == u.nt;
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (u.row0 + (long long)i) * p.out_tok_stride + hq * p.out_head_stride;
+      const long long tr = u.row0 + (long long)was.i, lse_at = tr * p.Hq + was.hq;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + tr * p.out_tok_stride + was.hq * p.out_head_stride;
       float* slot = p.work + ((long long)blockIdx.x * 2 + (t0 == 0)) * (kM * (D + 2));
 #pragma unroll 1
       for (int x = 0; x < D / 32; ++x) {
@@ -413,7 +436,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         __syncwarp();
       }
       tc_fence_before();
-      const long long lse_at = (u.row0 + (long long)i) * p.Hq + hq;
       if (alone) {
         if (in && p.lse) p.lse[lse_at] = lse_of(m, l);
       } else {
@@ -440,14 +462,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
 #pragma unroll 1
           for (int d = 0; d < D; d += 32) {
             float acc[32] = {};
+#pragma unroll 2
             for (int x = c0; x <= c1; ++x) {
               const float* from = p.work + piece_at<D>(x, c0);
+              float4 v[8];
+#pragma unroll
+              for (int y = 0; y < 8; ++y) v[y] = __ldcg(reinterpret_cast<const float4*>(from + tid * D + d) + y);
               const float f = ex2(__ldcg(from + kM * D + 2 * tid) - ref);
 #pragma unroll
-              for (int y = 0; y < 32; y += 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(from + tid * D + d + y));
-                acc[y] += f * v.x, acc[y + 1] += f * v.y, acc[y + 2] += f * v.z, acc[y + 3] += f * v.w;
-              }
+              for (int y = 0; y < 8; ++y)
+                acc[4 * y] += f * v[y].x, acc[4 * y + 1] += f * v[y].y, acc[4 * y + 2] += f * v[y].z, acc[4 * y + 3] += f * v[y].w;
             }
 #pragma unroll
             for (int y = 0; y < 32; y += 8)
@@ -458,9 +482,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
           if (p.lse) p.lse[lse_at] = lse_of(mx, sum);
         }
       }
-      ++unit;
-      next_unit(p, G, it.u);
-      it.open(it.u.at);
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ K codes -> fp16
@@ -471,50 +492,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
     const int w = warp - 4, q = lane & 3;
     const int panel = D == 128 ? (lane >> 3) & 1 : 0;
     const int tok = D == 128 ? w * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1) : w * 8 + (lane >> 2);
-    uint4 raw[kSteps];
-    auto load = [&](uint32_t c) {
-      const uint32_t slot = c % kPageSlots;
+    const uint8_t* codes = p.k_codes + (tok & 15) * D + 64 * panel + 16 * q;
+    for (; it.valid(); it.next(p, G), ++c) {
+      const uint32_t kb = c & 1, slot = c % kPageSlots;
       mbar_wait(&sm.page_full[slot], (c / kPageSlots) & 1, wg, 65);
+      const int left = it.u.len - it.t * kN;  // tokens from the tile's first on
+      uint4 raw[kSteps];
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const int x = s * kStepTokens + tok, token = it.t * kN + x;
-        const int id = __float_as_int(sm.page[slot][x >> 4].x);
+        const int x = s * kStepTokens + tok, first = __float_as_int(sm.page[slot][x >> 4].x);
         raw[s] = make_uint4(0, 0, 0, 0);
-        if (id >= 0 && token < it.u.len)
-          raw[s] = __ldg(reinterpret_cast<const uint4*>(
-              p.k_codes + ((((long long)id * p.Hkv + it.u.h) << p.page_shift) + (token & ((1 << p.page_shift) - 1))) * D +
-              64 * panel + 16 * q));
+        if (first >= 0 && x < left) raw[s] = __ldg(reinterpret_cast<const uint4*>(codes + (long long)first * D));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.page_empty[slot]);
-    };
-    if (it.valid()) load(0);
-    while (it.valid()) {
-      const uint32_t kb = c & 1;
-      uint4 now[kSteps];
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) now[s] = raw[s];
-      it.next(p, G);
-      if (it.valid()) load(c + 1);
       mbar_wait(&sm.k_empty[kb], ((c >> 1) & 1) ^ 1, wg, 66);
+      const uint32_t base = smem_u32(sm.k[kb]) + panel * (kN * 128) + tok * 128;
+      const uint32_t at0 = base + (((2 * q) ^ (tok & 7)) << 4), at1 = base + (((2 * q + 1) ^ (tok & 7)) << 4);
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const int x = s * kStepTokens + tok;
-        const uint32_t row = smem_u32(sm.k[kb]) + panel * (kN * 128) + x * 128;
-        const uint32_t in[4] = {now[s].x, now[s].y, now[s].z, now[s].w};
+        const uint32_t in[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
         uint32_t h[8];
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           h[2 * y] = e4m3x2_to_f16x2((uint16_t)in[y]);
           h[2 * y + 1] = e4m3x2_to_f16x2((uint16_t)(in[y] >> 16));
         }
-        st_shared_v4(row + (((2 * q) ^ (x & 7)) << 4), h[0], h[1], h[2], h[3]);
-        st_shared_v4(row + (((2 * q + 1) ^ (x & 7)) << 4), h[4], h[5], h[6], h[7]);
+        st_shared_v4(at0 + s * (kStepTokens * 128), h[0], h[1], h[2], h[3]);
+        st_shared_v4(at1 + s * (kStepTokens * 128), h[4], h[5], h[6], h[7]);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.k_full[kb]);
-      ++c;
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ V codes -> fp16, transposed
@@ -523,32 +532,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
     constexpr int kSteps = D / 32;                         // blocks of 32 tokens x 32 columns per warp
     const int w = warp - 8, tl = lane & 3, dl = lane >> 2;
     const int col = 32 * (w % (D / 32)) + 4 * dl, first = D == 128 ? 0 : 2 * (w >> 1);
-    uint32_t raw[kSteps][8];
-    auto load = [&](uint32_t c) {
-      const uint32_t slot = c % kPageSlots;
+    const uint8_t* codes = p.v_codes + (8 * (tl & 1)) * D + col;
+    for (; it.valid(); it.next(p, G), ++c) {
+      const uint32_t vb = c & 1, slot = c % kPageSlots;
       mbar_wait(&sm.page_full[slot], (c / kPageSlots) & 1, wg, 67);
+      const int left = it.u.len - it.t * kN;  // tokens from the tile's first on
+      uint32_t raw[kSteps][8];
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const int x = 32 * (first + s) + 8 * tl, token = it.t * kN + x;
-        const int id = __float_as_int(sm.page[slot][x >> 4].x);
-        const uint8_t* v = p.v_codes + ((((long long)id * p.Hkv + it.u.h) << p.page_shift) + (token & ((1 << p.page_shift) - 1))) * D + col;
+        const int x = 32 * (first + s) + 8 * tl, page_row = __float_as_int(sm.page[slot][x >> 4].x);
+        const uint8_t* v = codes + (long long)page_row * D;
+        if (page_row >= 0 && x + 8 <= left) {
 #pragma unroll
-        for (int y = 0; y < 8; ++y)
-          raw[s][y] = id >= 0 && token + y < it.u.len ? __ldg(reinterpret_cast<const uint32_t*>(v + y * D)) : 0u;
+          for (int y = 0; y < 8; ++y) raw[s][y] = __ldg(reinterpret_cast<const uint32_t*>(v + y * D));
+        } else {
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            raw[s][y] = page_row >= 0 && x + y < left ? __ldg(reinterpret_cast<const uint32_t*>(v + y * D)) : 0u;
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.page_empty[slot]);
-    };
-    if (it.valid()) load(0);
-    while (it.valid()) {
-      const uint32_t vb = c & 1;
-      uint32_t now[kSteps][8];
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-        for (int y = 0; y < 8; ++y) now[s][y] = raw[s][y];
-      it.next(p, G);
-      if (it.valid()) load(c + 1);
       mbar_wait(&sm.v_empty[vb], ((c >> 1) & 1) ^ 1, wg, 68);
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
@@ -557,8 +561,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         uint32_t h[4][4];
 #pragma unroll
         for (int y = 0; y < 4; ++y) {  // tokens 2 y, 2 y + 1: columns 0, 1 and 2, 3 in pairs of tokens
-          const uint32_t a = __byte_perm(now[s][2 * y], now[s][2 * y + 1], 0x5140);
-          const uint32_t b = __byte_perm(now[s][2 * y], now[s][2 * y + 1], 0x7362);
+          const uint32_t a = __byte_perm(raw[s][2 * y], raw[s][2 * y + 1], 0x5140);
+          const uint32_t b = __byte_perm(raw[s][2 * y], raw[s][2 * y + 1], 0x7362);
           h[0][y] = e4m3x2_to_f16x2((uint16_t)a);
           h[1][y] = e4m3x2_to_f16x2((uint16_t)(a >> 16));
           h[2][y] = e4m3x2_to_f16x2((uint16_t)b);
@@ -571,7 +575,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.v_full[vb]);
-      ++c;
     }
   } else if (warp == 12) {
     // ------------------------------------------------------------ MMA issue
@@ -633,14 +636,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       const Unit u = it.u;
       for (int t = it.t; t < it.end; t += 4) {
         const int j = lane & 7, tt = t + (lane >> 3), token = tt * kN + 16 * j;
-        int id = -1;
+        int first = -1;
         float ks = 0.0f, log_vs = -INFINITY, inv_vs = 0.0f;
         if (tt < it.end && token < u.len) {
-          id = p.table[u.b * p.ld_table + (token >> p.page_shift)];
+          const int id = p.table[u.b * p.ld_table + (token >> p.page_shift)];
           if ((unsigned)id >= (unsigned)p.num_pages) {
             record_status(p.status, kStatusOffsets, 50);
-            id = -1;
           } else {
+            first = (int)((((long long)id * p.Hkv + u.h) << p.page_shift) + (token & ((1 << p.page_shift) - 1)));
             ks = p.k_scales[(long long)id * p.Hkv + u.h];
             const float vs = p.v_scales[(long long)id * p.Hkv + u.h];
             log_vs = log2f(vs);
@@ -650,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         for (int x = 0; x < 4 && t + x < it.end; ++x, ++c) {
           const uint32_t slot = c % kPageSlots;
           mbar_wait(&sm.page_empty[slot], ((c / kPageSlots) & 1) ^ 1, wg, 73);
-          if (lane >> 3 == x) sm.page[slot][j] = make_float4(__int_as_float(id), ks, log_vs, inv_vs);
+          if (lane >> 3 == x) sm.page[slot][j] = make_float4(__int_as_float(first), ks, log_vs, inv_vs);
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.page_full[slot]);
         }
