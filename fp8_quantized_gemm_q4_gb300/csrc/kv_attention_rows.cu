@@ -10,11 +10,13 @@
 // memory traffic.  Per tile and SM: 1024 clocks of MMA, 512 of writing and 512 of
 // the MMAs' reading 64 KB, 500 of exponentials, so the pieces balance where each
 // runs beside the others:
-//   warps 0-3   softmax, a thread per row: S from tensor memory, weights back
-//               into S's place, the running (m, l), rare rescaling of O
-//   warps 4-7   K codes -> fp16        warps 8-11  V codes -> fp16, transposed
-//   warp 12     MMA issue: S(j + 1) = Q K^T goes ahead of O += P(j) V
-//   warp 13     page ids and scales of the next tiles
+//   warps 0-7   softmax, two threads per row, each half of the columns: S from
+//               tensor memory, weights back into S's place, the running (m, l),
+//               rare rescaling of O (with one thread per row the softmax alone
+//               took 2.5 times the MMAs' time)
+//   warps 8-11  K codes -> fp16        warps 12-15  V codes -> fp16, transposed
+//   warp 16     MMA issue: S(j + 1) = Q K^T goes ahead of O += P(j) V
+//   warp 17     page ids and scales of the next tiles
 // The tiles of all units form one list that is cut into equal shares, one CTA
 // each; units cut between CTAs are joined by the last CTA to finish a piece.
 #include "kv_attention.cuh"
@@ -25,12 +27,15 @@ namespace {
 constexpr int kM = 128;           // rows of a unit
 constexpr int kN = 128;           // cached tokens of a tile
 constexpr int kGroups = kN / 16;  // groups of 16 tokens: each lies in one page
-constexpr int kThreads = 14 * 32;
+constexpr int kSoft = 8, kMma = 16;  // softmax warps, the MMA warp
+constexpr int kThreads = 18 * 32;
+constexpr int kHalf = kN / 2;     // columns of S a softmax thread has
 constexpr int kMinTiles = 2;      // least tiles worth a CTA of its own
 constexpr int kPageSlots = 8;     // tiles whose pages are known ahead
 constexpr int kCounters = 1024;   // arrival counters at the head of the workspace
 constexpr int kTmemCols = 512;
-// Tensor memory columns: S twice (P of a tile in the first half of its S), O, Q
+// Tensor memory columns: S twice (the weights of 64 tokens go into the first half of
+// the 64 columns that their scores had), O, Q
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384;
 
 template <int D>
@@ -40,6 +45,7 @@ struct RowsSmem {
   float4 page[kPageSlots][kGroups];        // first row of codes (int, -1: none), K scale, log2 of V scale, 1 / V scale
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2];
   uint64_t page_full[kPageSlots], page_empty[kPageSlots], o_done, q_full, drain;
+  float swap[2][kM];                       // between the two threads of a row
   long long scan[kThreads / 32];
   long long start_at;
   int start[3];
@@ -133,7 +139,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft * 32) : "memory"); }
+__device__ __forceinline__ bool softmax_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, %2, p;\n\t"
+      "selp.b32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x), "n"(kSoft * 32)
+      : "memory");
+  return r != 0;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __grid_constant__ KvAttentionParams p) {
@@ -150,19 +168,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       mbar_init(&sm.k_empty[s], 1);
       mbar_init(&sm.v_empty[s], 1);
       mbar_init(&sm.s_full[s], 1);
-      mbar_init(&sm.p_full[s], 4);
+      mbar_init(&sm.p_full[s], kSoft);
     }
     for (int s = 0; s < kPageSlots; ++s) {
       mbar_init(&sm.page_full[s], 1);
-      mbar_init(&sm.page_empty[s], 12);
+      mbar_init(&sm.page_empty[s], kSoft + 8);
     }
     mbar_init(&sm.o_done, 1);
-    mbar_init(&sm.q_full, 4);
+    mbar_init(&sm.q_full, kSoft);
     mbar_init(&sm.drain, 1);
     fence_barrier_init();
     sm.abort_flag = 0;
   }
-  if (warp == 12) {
+  if (warp == kMma) {
     tmem_alloc(&sm.tmem, kTmemCols);
     tmem_relinquish();
     tc_fence_before();
@@ -251,43 +269,48 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
   }
   uint32_t c = 0;  // tiles of the share so far: ring places and phases follow from it in every role
 
-  if (warp < 4) {
-    // ------------------------------------------------------------ softmax: a thread per row
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    // this thread's row of a unit
+  if (warp < kSoft) {
+    // ------------------------------------------------------------ softmax: two threads per row
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const int hf = warp >> 2, r128 = tid & (kM - 1);  // half of the columns, row of the unit
     struct Row {
       int i, hq;     // token, query head
       bool in;
       float qscale;
     };
-    auto load_q = [&](const Unit& u) {  // q to tensor memory, fp16 by a power of two
+    // q to tensor memory, fp16 by a power of two
+    auto load_q = [&](const Unit& u) {
       Row w;
-      const long long r = (long long)u.rt * kM + tid;
+      const long long r = (long long)u.rt * kM + r128;
       w.i = (int)(r / G), w.hq = u.h * G + (int)(r % G);
       w.in = r < (long long)u.n * G && u.row0 + w.i < p.T;
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (u.row0 + (long long)w.i) * p.q_tok_stride + w.hq * p.q_head_stride;
-      uint4 v[D / 8];
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (u.row0 + (long long)w.i) * p.q_tok_stride +
+                               w.hq * p.q_head_stride + hf * (D / 2);
+      uint4 v[D / 16];
 #pragma unroll
-      for (int x = 0; x < D / 8; ++x) v[x] = w.in ? __ldg(reinterpret_cast<const uint4*>(q) + x) : make_uint4(0, 0, 0, 0);
+      for (int x = 0; x < D / 16; ++x) v[x] = w.in ? __ldg(reinterpret_cast<const uint4*>(q) + x) : make_uint4(0, 0, 0, 0);
       float amax = 0.0f;
 #pragma unroll
-      for (int x = 0; x < D / 8; ++x) {
+      for (int x = 0; x < D / 16; ++x) {
         const uint32_t y[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
 #pragma unroll
         for (int z = 0; z < 4; ++z)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(y[z] << 16)), fabsf(__uint_as_float(y[z] & 0xffff0000u))));
+          amax = max3(amax, fabsf(__uint_as_float(y[z] << 16)), fabsf(__uint_as_float(y[z] & 0xffff0000u)));
       }
-      const int up = fp16_up(amax);
+      softmax_sync();  // what was in swap has been read
+      sm.swap[hf][r128] = amax;
+      softmax_sync();
+      const int up = fp16_up(fmaxf(sm.swap[0][r128], sm.swap[1][r128]));
       const float mul = exp2i(up);
       w.qscale = exp2i(-up) * p.scale_log2;
 #pragma unroll
-      for (int x = 0; x < D / 8; x += 2) {
+      for (int x = 0; x < D / 16; x += 2) {
         const uint32_t y[8] = {v[x].x, v[x].y, v[x].z, v[x].w, v[x + 1].x, v[x + 1].y, v[x + 1].z, v[x + 1].w};
         uint32_t h[8];
 #pragma unroll
         for (int z = 0; z < 8; ++z)
           h[z] = pack_f16x2(__uint_as_float(y[z] << 16) * mul, __uint_as_float(y[z] & 0xffff0000u) * mul);
-        tmem_st8(lanes + kColQ + 4 * x, h);
+        tmem_st8(lanes + kColQ + hf * (D / 4) + 4 * x, h);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -303,38 +326,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       const bool in = row.in;
       const float qscale = row.qscale;
       const int seen = in ? u.len - u.n + row.i + 1 : 0;
-      float m = -INFINITY, l = 0.0f;
+      float m = -INFINITY, l = 0.0f;  // l: of this thread's columns
       for (int t = t0; t < t1; ++t, ++c) {
         const uint32_t sb = c & 1, slot = c % kPageSlots;
         mbar_wait(&sm.page_full[slot], (c / kPageSlots) & 1, wg, 60);
         mbar_wait(&sm.s_full[sb], (c >> 1) & 1, wg, 61);
         tc_fence_after();
         const uint32_t s_at = lanes + kColS + sb * kN;
-        const int limit = seen - t * kN;  // columns that this row sees
+        const int limit = seen - t * kN - hf * kHalf;  // of its columns, those that this row sees
+        const float4* page = &sm.page[slot][hf * (kGroups / 2)];
         // The loops over S stay rolled and short: unrolled, the softmax warps
         // waited for instructions most of the time.
-        if (__any_sync(kFullMask, limit < kN)) {
+        if (__any_sync(kFullMask, limit < kHalf)) {
 #pragma unroll 1
-          for (int x = 0; x < kN; x += 16) {
+          for (int x = 0; x < kHalf; x += 16) {
             uint32_t raw[16];
-            tmem_ld16(s_at + x, raw);
+            tmem_ld16(s_at + hf * kHalf + x, raw);
             tmem_ld_wait();
 #pragma unroll
             for (int y = 0; y < 16; ++y)
               if (x + y >= limit) raw[y] = __float_as_uint(-INFINITY);
-            tmem_st16(s_at + x, raw);
+            tmem_st16(s_at + hf * kHalf + x, raw);
           }
           tmem_st_wait();
         }
         float mx = -INFINITY;
 #pragma unroll 1
-        for (int x = 0; x < kN; x += 32) {
+        for (int x = 0; x < kHalf; x += 32) {
           uint32_t raw[32];
-          tmem_ld32(s_at + x, raw);
+          tmem_ld32(s_at + hf * kHalf + x, raw);
           tmem_ld_wait();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float4 pg = sm.page[slot][x / 16 + h];
+            const float4 pg = page[x / 16 + h];
             float g = __uint_as_float(raw[16 * h]);
 #pragma unroll
             for (int y = 1; y < 15; y += 2)
@@ -344,7 +368,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
           }
         }
         bool waited = t == t0;  // o_done of the tile before: none, or not waited for yet
-        if (__any_sync(kFullMask, mx > m + 8.0f)) {
+        if (softmax_any(mx > m + 8.0f)) {
+          sm.swap[hf][r128] = mx;
+          softmax_sync();
+          mx = fmaxf(sm.swap[0][r128], sm.swap[1][r128]);
           const bool up = mx > m + 8.0f;
           const float f = up ? ex2(m - mx) : 1.0f;
           m = up ? mx : m;
@@ -354,26 +381,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             waited = true;
             tc_fence_after();
 #pragma unroll 1
-            for (int x = 0; x < D / 32; ++x) {
+            for (int x = hf * (D / 2); x < (hf + 1) * (D / 2); x += 32) {
               uint32_t o[32];
-              tmem_ld32(lanes + kColO + 32 * x, o);
+              tmem_ld32(lanes + kColO + x, o);
               tmem_ld_wait();
 #pragma unroll
               for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-              tmem_st16(lanes + kColO + 32 * x, o);
-              tmem_st16(lanes + kColO + 32 * x + 16, o + 16);
+              tmem_st16(lanes + kColO + x, o);
+              tmem_st16(lanes + kColO + x + 16, o + 16);
             }
           }
         }
         const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll 1
-        for (int x = 0; x < kN; x += 32) {
+        for (int x = 0; x < kHalf; x += 32) {
           uint32_t raw[32], w[16];
-          tmem_ld32(s_at + x, raw);
+          tmem_ld32(s_at + hf * kHalf + x, raw);
           tmem_ld_wait();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float4 pg = sm.page[slot][x / 16 + h];
+            const float4 pg = page[x / 16 + h];
             // a scale is positive, or 0 with pg.z = -infinity: masked scores must not meet the 0
             const float f1 = fmaxf(qscale * pg.y, 1e-37f), o1 = pg.z - ref;
             const float2 f = make_float2(f1, f1), off = make_float2(o1, o1);
@@ -387,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             }
             l = fmaf(sum.x + sum.y, pg.w, l);
           }
-          tmem_st16(s_at + x / 2, w);
+          tmem_st16(s_at + hf * kHalf + x / 2, w);
         }
         tmem_st_wait();
         // every phase of o_done is waited for in turn; the product of this tile
@@ -409,15 +436,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       if (it.valid()) row = load_q(it.u);
       mbar_wait(&sm.o_done, (c - 1) & 1, wg, 64);
       tc_fence_after();
+      softmax_sync();  // swap has been read
+      sm.swap[hf][r128] = l;
+      softmax_sync();
+      l = sm.swap[0][r128] + sm.swap[1][r128];
       const bool alone = t0 == 0 && t1 == u.nt;
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
       const long long tr = u.row0 + (long long)was.i, lse_at = tr * p.Hq + was.hq;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + tr * p.out_tok_stride + was.hq * p.out_head_stride;
       float* slot = p.work + ((long long)blockIdx.x * 2 + (t0 == 0)) * (kM * (D + 2));
 #pragma unroll 1
-      for (int x = 0; x < D / 32; ++x) {
+      for (int x = hf * (D / 2); x < (hf + 1) * (D / 2); x += 32) {
         uint32_t o[32];
-        tmem_ld32(lanes + kColO + 32 * x, o);
+        tmem_ld32(lanes + kColO + x, o);
         tmem_ld_wait();
         if (in && alone) {
 #pragma unroll
@@ -426,20 +457,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
 #pragma unroll
             for (int z = 0; z < 4; ++z)
               w[z] = pack_bf16x2(__uint_as_float(o[y + 2 * z]) * inv, __uint_as_float(o[y + 2 * z + 1]) * inv);
-            *reinterpret_cast<uint4*>(dst + 32 * x + y) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + x + y) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else if (in) {
 #pragma unroll
           for (int y = 0; y < 32; y += 4)
-            *reinterpret_cast<uint4*>(slot + tid * D + 32 * x + y) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+            *reinterpret_cast<uint4*>(slot + r128 * D + x + y) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
         }
         __syncwarp();
       }
       tc_fence_before();
       if (alone) {
-        if (in && p.lse) p.lse[lse_at] = lse_of(m, l);
+        if (in && hf == 0 && p.lse) p.lse[lse_at] = lse_of(m, l);
       } else {
-        if (in) *reinterpret_cast<float2*>(slot + kM * D + 2 * tid) = make_float2(m, l);
+        if (in && hf == 0) *reinterpret_cast<float2*>(slot + kM * D + 2 * r128) = make_float2(m, l);
         __threadfence();
         const int c0 = (int)(((u.at + 1) * shares - 1) / total), c1 = (int)(((u.at + u.nt) * shares - 1) / total);
         softmax_sync();
@@ -452,44 +483,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         softmax_sync();
         if (sm.last && in) {
           float mx = -INFINITY, sum = 0.0f;
-          for (int x = c0; x <= c1; ++x) mx = fmaxf(mx, __ldcg(p.work + piece_at<D>(x, c0) + kM * D + 2 * tid));
+          for (int x = c0; x <= c1; ++x) mx = fmaxf(mx, __ldcg(p.work + piece_at<D>(x, c0) + kM * D + 2 * r128));
           const float ref = mx == -INFINITY ? 0.0f : mx;
           for (int x = c0; x <= c1; ++x) {
-            const float2 e = __ldcg(reinterpret_cast<const float2*>(p.work + piece_at<D>(x, c0) + kM * D + 2 * tid));
+            const float2 e = __ldcg(reinterpret_cast<const float2*>(p.work + piece_at<D>(x, c0) + kM * D + 2 * r128));
             sum += e.y * ex2(e.x - ref);
           }
           const float by = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll 1
-          for (int d = 0; d < D; d += 32) {
-            float acc[32] = {};
+          for (int d = hf * (D / 2); d < (hf + 1) * (D / 2); d += 16) {
+            float acc[16] = {};
 #pragma unroll 2
             for (int x = c0; x <= c1; ++x) {
               const float* from = p.work + piece_at<D>(x, c0);
-              float4 v[8];
+              float4 v[4];
 #pragma unroll
-              for (int y = 0; y < 8; ++y) v[y] = __ldcg(reinterpret_cast<const float4*>(from + tid * D + d) + y);
-              const float f = ex2(__ldcg(from + kM * D + 2 * tid) - ref);
+              for (int y = 0; y < 4; ++y) v[y] = __ldcg(reinterpret_cast<const float4*>(from + r128 * D + d) + y);
+              const float f = ex2(__ldcg(from + kM * D + 2 * r128) - ref);
 #pragma unroll
-              for (int y = 0; y < 8; ++y)
+              for (int y = 0; y < 4; ++y)
                 acc[4 * y] += f * v[y].x, acc[4 * y + 1] += f * v[y].y, acc[4 * y + 2] += f * v[y].z, acc[4 * y + 3] += f * v[y].w;
             }
 #pragma unroll
-            for (int y = 0; y < 32; y += 8)
+            for (int y = 0; y < 16; y += 8)
               *reinterpret_cast<uint4*>(dst + d + y) =
                   make_uint4(pack_bf16x2(acc[y] * by, acc[y + 1] * by), pack_bf16x2(acc[y + 2] * by, acc[y + 3] * by),
                              pack_bf16x2(acc[y + 4] * by, acc[y + 5] * by), pack_bf16x2(acc[y + 6] * by, acc[y + 7] * by));
           }
-          if (p.lse) p.lse[lse_at] = lse_of(mx, sum);
+          if (hf == 0 && p.lse) p.lse[lse_at] = lse_of(mx, sum);
         }
+        __syncwarp();
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < kSoft + 4) {
     // ------------------------------------------------------------ K codes -> fp16
     // Lane: 16 codes of a token (and the token's place among its warp's), such
     // that eight lanes in a row store to eight different chunks.
     constexpr int kSteps = kN * D / (128 * 16);           // 16-byte loads per thread
     constexpr int kStepTokens = kN / kSteps;
-    const int w = warp - 4, q = lane & 3;
+    const int w = warp - kSoft, q = lane & 3;
     const int panel = D == 128 ? (lane >> 3) & 1 : 0;
     const int tok = D == 128 ? w * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1) : w * 8 + (lane >> 2);
     const uint8_t* codes = p.k_codes + (tok & 15) * D + 64 * panel + 16 * q;
@@ -525,12 +557,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.k_full[kb]);
     }
-  } else if (warp < 12) {
+  } else if (warp < kSoft + 8) {
     // ------------------------------------------------------------ V codes -> fp16, transposed
     // Lane: 8 tokens x 4 columns, as eight 4-byte loads; four lanes share their
     // columns and take four token groups of 8 in a row.
     constexpr int kSteps = D / 32;                         // blocks of 32 tokens x 32 columns per warp
-    const int w = warp - 8, tl = lane & 3, dl = lane >> 2;
+    const int w = warp - kSoft - 4, tl = lane & 3, dl = lane >> 2;
     const int col = 32 * (w % (D / 32)) + 4 * dl, first = D == 128 ? 0 : 2 * (w >> 1);
     const uint8_t* codes = p.v_codes + (8 * (tl & 1)) * D + col;
     for (; it.valid(); it.next(p, G), ++c) {
@@ -576,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.v_full[vb]);
     }
-  } else if (warp == 12) {
+  } else if (warp == kMma) {
     // ------------------------------------------------------------ MMA issue
     constexpr uint32_t kPanelK = kN * 128, kPanelV = D * 128;
     const uint32_t idesc_s = idesc_f16(kM, kN), idesc_o = idesc_f16(kM, D);
@@ -614,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         if (elect_one()) {
 #pragma unroll
           for (int x = 0; x < kN / 16; ++x)
-            mma_ts_f16(tmem + kColO, tmem + kColS + b * kN + 8 * x, dv + (x / 4) * (kPanelV >> 4) + 2 * (x % 4), idesc_o,
+            mma_ts_f16(tmem + kColO, tmem + kColS + b * kN + (x / 4) * kHalf + 8 * (x % 4), dv + (x / 4) * (kPanelV >> 4) + 2 * (x % 4), idesc_o,
                        t > t0 || x > 0);
           tc_commit(&sm.v_empty[b]);
           tc_commit(&sm.o_done);
@@ -664,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kMma) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
