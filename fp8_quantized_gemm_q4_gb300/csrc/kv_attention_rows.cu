@@ -16,7 +16,7 @@
 //               took 2.5 times the MMAs' time)
 //   warps 8-11  K codes -> fp16        warps 12-15  V codes -> fp16, transposed
 //   warp 16     MMA issue: S(j + 1) = Q K^T goes ahead of O += P(j) V
-//   warp 17     page ids and scales of the next tiles
+//   warp 17     the next units, page ids and scales of the next tiles
 // The tiles of all units form one list that is cut into equal shares, one CTA
 // each; units cut between CTAs are joined by the last CTA to finish a piece.
 #include "kv_attention.cuh"
@@ -32,11 +32,19 @@ constexpr int kThreads = 18 * 32;
 constexpr int kHalf = kN / 2;     // columns of S a softmax thread has
 constexpr int kMinTiles = 2;      // least tiles worth a CTA of its own
 constexpr int kPageSlots = 8;     // tiles whose pages are known ahead
+constexpr int kUnitSlots = 4;     // units known ahead
 constexpr int kCounters = 1024;   // arrival counters at the head of the workspace
 constexpr int kTmemCols = 512;
 // Tensor memory columns: S twice (the weights of 64 tokens go into the first half of
 // the 64 columns that their scores had), O, Q
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384;
+
+// A unit as the roles read it; t0 == t1: the share is done
+struct UnitInfo {
+  int t0, t1, nt, len;     // its tiles within the share, all its tiles, cached tokens
+  int h, rt, row0, n;      // KV head, row tile; the request's first row and rows
+  long long at;            // its first tile's place in the list
+};
 
 template <int D>
 struct RowsSmem {
@@ -45,6 +53,8 @@ struct RowsSmem {
   float4 page[kPageSlots][kGroups];        // first row of codes (int, -1: none), K scale, log2 of V scale, 1 / V scale
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2];
   uint64_t page_full[kPageSlots], page_empty[kPageSlots], o_done, q_full, drain;
+  UnitInfo unit[kUnitSlots];
+  uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
   float swap[2][kM];                       // between the two threads of a row
   long long scan[kThreads / 32];
   long long start_at;
@@ -113,23 +123,6 @@ __device__ __forceinline__ void next_unit(const KvAttentionParams& p, int G, Uni
   }
   u.nt = unit_tiles(u.n, u.len, G, u.rt);
 }
-// The tiles of a share, one after the other
-struct Tiles {
-  Unit u;
-  int t, end;  // tile within the unit; the unit's end within the share
-  long long last;
-  __device__ __forceinline__ void open(long long first) {
-    t = (int)max(0ll, first - u.at);
-    end = (int)min((long long)u.nt, last - u.at);
-  }
-  __device__ __forceinline__ bool valid() const { return u.at + t < last; }
-  __device__ __forceinline__ void next(const KvAttentionParams& p, int G) {
-    if (++t < end) return;
-    next_unit(p, G, u);
-    open(u.at);
-  }
-};
-
 template <int D>
 __device__ __forceinline__ long long piece_at(int cta, int first_cta) {
   return ((long long)cta * 2 + (cta == first_cta)) * (kM * (D + 2));
@@ -173,6 +166,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
     for (int s = 0; s < kPageSlots; ++s) {
       mbar_init(&sm.page_full[s], 1);
       mbar_init(&sm.page_empty[s], kSoft + 8);
+    }
+    for (int s = 0; s < kUnitSlots; ++s) {
+      mbar_init(&sm.unit_full[s], 1);
+      mbar_init(&sm.unit_empty[s], kSoft + 8 + 1);
     }
     mbar_init(&sm.o_done, 1);
     mbar_init(&sm.q_full, kSoft);
@@ -253,21 +250,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
   __syncthreads();
   const uint32_t tmem = sm.tmem;
 
-  Tiles it;
-  if (works) {
-    it.u.b = sm.start[0];
-    it.u.h = sm.start[1];
-    it.u.rt = sm.start[2];
-    it.u.at = sm.start_at;
-    it.last = t_last;
-    load_request(p, G, it.u);
-    it.u.nt = unit_tiles(it.u.n, it.u.len, G, it.u.rt);
-    it.open(t_first);
-  } else {
-    it.u.at = it.last = 0;
-    it.t = 0;
-  }
   uint32_t c = 0;  // tiles of the share so far: ring places and phases follow from it in every role
+  uint32_t k = 0;  // units so far, likewise
+  // the next unit, for a whole warp; false after a wait that gave up
+  auto unit_open = [&](const UnitInfo*& u) {
+    const bool ok = mbar_wait(&sm.unit_full[k % kUnitSlots], (k / kUnitSlots) & 1, wg, 74);
+    u = &sm.unit[k % kUnitSlots];
+    return __all_sync(kFullMask, ok) != 0;
+  };
+  auto unit_close = [&] {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.unit_empty[k % kUnitSlots]);
+    ++k;
+  };
 
   if (warp < kSoft) {
     // ------------------------------------------------------------ softmax: two threads per row
@@ -279,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       float qscale;
     };
     // q to tensor memory, fp16 by a power of two
-    auto load_q = [&](const Unit& u) {
+    auto load_q = [&](const UnitInfo& u) {
       Row w;
       const long long r = (long long)u.rt * kM + r128;
       w.i = (int)(r / G), w.hq = u.h * G + (int)(r % G);
@@ -319,13 +314,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       return w;
     };
     Row row = {};
-    if (it.valid()) row = load_q(it.u);
-    while (it.valid()) {
-      const Unit u = it.u;
-      const int t0 = it.t, t1 = it.end;
+    const UnitInfo* u;
+    // the softmax warps go on or end together, whichever of them gave up
+    bool dead = softmax_any(!unit_open(u));
+    if (!dead && u->t0 < u->t1) row = load_q(*u);
+    while (!dead && u->t0 < u->t1) {
+      const int t0 = u->t0, t1 = u->t1;
       const bool in = row.in;
       const float qscale = row.qscale;
-      const int seen = in ? u.len - u.n + row.i + 1 : 0;
+      const int seen = in ? u->len - u->n + row.i + 1 : 0;
       float m = -INFINITY, l = 0.0f;  // l: of this thread's columns
       for (int t = t0; t < t1; ++t, ++c) {
         const uint32_t sb = c & 1, slot = c % kPageSlots;
@@ -395,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll 1
         for (int x = 0; x < kHalf; x += 32) {
-          uint32_t raw[32], w[16];
+          uint32_t raw[32];
           tmem_ld32(s_at + hf * kHalf + x, raw);
           tmem_ld_wait();
 #pragma unroll
@@ -405,16 +402,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             const float f1 = fmaxf(qscale * pg.y, 1e-37f), o1 = pg.z - ref;
             const float2 f = make_float2(f1, f1), off = make_float2(o1, o1);
             float2 sum = make_float2(0.0f, 0.0f);
+            uint32_t w[8];
 #pragma unroll
             for (int y = 0; y < 16; y += 2) {
               const float2 z = __ffma2_rn(make_float2(__uint_as_float(raw[16 * h + y]), __uint_as_float(raw[16 * h + y + 1])), f, off);
               const float2 e = make_float2(ex2(z.x), ex2(z.y));
               sum = __fadd2_rn(sum, e);
-              w[8 * h + y / 2] = pack_f16x2(e.x, e.y);
+              w[y / 2] = pack_f16x2(e.x, e.y);
             }
+            tmem_st8(s_at + hf * kHalf + x / 2 + 8 * h, w);
             l = fmaf(sum.x + sum.y, pg.w, l);
           }
-          tmem_st16(s_at + hf * kHalf + x / 2, w);
         }
         tmem_st_wait();
         // every phase of o_done is waited for in turn; the product of this tile
@@ -430,19 +428,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       // ---- the unit's rows.  Its scores are done: the next unit's q goes first,
       // so that the next scores run beside what follows.
       const Row was = row;
-      next_unit(p, G, it.u);
-      it.open(it.u.at);
-      __syncwarp();
-      if (it.valid()) row = load_q(it.u);
+      const int row0 = u->row0, nt = u->nt;
+      const long long at = u->at;
+      unit_close();
+      dead = softmax_any(!unit_open(u));
+      if (!dead && u->t0 < u->t1) row = load_q(*u);
       mbar_wait(&sm.o_done, (c - 1) & 1, wg, 64);
       tc_fence_after();
       softmax_sync();  // swap has been read
       sm.swap[hf][r128] = l;
       softmax_sync();
       l = sm.swap[0][r128] + sm.swap[1][r128];
-      const bool alone = t0 == 0 && t1 == u.nt;
+      const bool alone = t0 == 0 && t1 == nt;
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-      const long long tr = u.row0 + (long long)was.i, lse_at = tr * p.Hq + was.hq;
+      const long long tr = row0 + (long long)was.i, lse_at = tr * p.Hq + was.hq;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + tr * p.out_tok_stride + was.hq * p.out_head_stride;
       float* slot = p.work + ((long long)blockIdx.x * 2 + (t0 == 0)) * (kM * (D + 2));
 #pragma unroll 1
@@ -472,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       } else {
         if (in && hf == 0) *reinterpret_cast<float2*>(slot + kM * D + 2 * r128) = make_float2(m, l);
         __threadfence();
-        const int c0 = (int)(((u.at + 1) * shares - 1) / total), c1 = (int)(((u.at + u.nt) * shares - 1) / total);
+        const int c0 = (int)(((at + 1) * shares - 1) / total), c1 = (int)(((at + nt) * shares - 1) / total);
         softmax_sync();
         if (tid == 0) {
           const int old = atomicAdd(p.counters + c0, 1);
@@ -515,6 +514,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         __syncwarp();
       }
     }
+    if (dead && tid == 0 && works) {
+      // a wait gave up: the pieces that were not written count as arrived, so
+      // that the counters are zero again for the next call
+      Unit w = {};
+      w.b = sm.start[0], w.h = sm.start[1], w.rt = sm.start[2], w.at = sm.start_at;
+      load_request(p, G, w);
+      w.nt = unit_tiles(w.n, w.len, G, w.rt);
+      for (uint32_t x = 0; w.at < t_last; ++x, next_unit(p, G, w)) {
+        if (x < k || (w.at >= t_first && w.at + w.nt <= t_last)) continue;
+        const int c0 = (int)(((w.at + 1) * shares - 1) / total), c1 = (int)(((w.at + w.nt) * shares - 1) / total);
+        if (atomicAdd(p.counters + c0, 1) == c1 - c0) p.counters[c0] = 0;
+      }
+    }
   } else if (warp < kSoft + 4) {
     // ------------------------------------------------------------ K codes -> fp16
     // Lane: 16 codes of a token (and the token's place among its warp's), such
@@ -525,10 +537,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
     const int panel = D == 128 ? (lane >> 3) & 1 : 0;
     const int tok = D == 128 ? w * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1) : w * 8 + (lane >> 2);
     const uint8_t* codes = p.k_codes + (tok & 15) * D + 64 * panel + 16 * q;
-    for (; it.valid(); it.next(p, G), ++c) {
+    for (;;) {
+      const UnitInfo* u;
+      if (!unit_open(u)) break;
+      const int t1 = u->t1, len = u->len;
+      int t = u->t0;
+      if (t == t1) break;
+      unit_close();
+    for (; t < t1; ++t, ++c) {
       const uint32_t kb = c & 1, slot = c % kPageSlots;
       mbar_wait(&sm.page_full[slot], (c / kPageSlots) & 1, wg, 65);
-      const int left = it.u.len - it.t * kN;  // tokens from the tile's first on
+      const int left = len - t * kN;  // tokens from the tile's first on
       uint4 raw[kSteps];
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
@@ -557,6 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.k_full[kb]);
     }
+    }
   } else if (warp < kSoft + 8) {
     // ------------------------------------------------------------ V codes -> fp16, transposed
     // Lane: 8 tokens x 4 columns, as eight 4-byte loads; four lanes share their
@@ -565,10 +585,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
     const int w = warp - kSoft - 4, tl = lane & 3, dl = lane >> 2;
     const int col = 32 * (w % (D / 32)) + 4 * dl, first = D == 128 ? 0 : 2 * (w >> 1);
     const uint8_t* codes = p.v_codes + (8 * (tl & 1)) * D + col;
-    for (; it.valid(); it.next(p, G), ++c) {
+    for (;;) {
+      const UnitInfo* u;
+      if (!unit_open(u)) break;
+      const int t1 = u->t1, len = u->len;
+      int t = u->t0;
+      if (t == t1) break;
+      unit_close();
+    for (; t < t1; ++t, ++c) {
       const uint32_t vb = c & 1, slot = c % kPageSlots;
       mbar_wait(&sm.page_full[slot], (c / kPageSlots) & 1, wg, 67);
-      const int left = it.u.len - it.t * kN;  // tokens from the tile's first on
+      const int left = len - t * kN;  // tokens from the tile's first on
       uint32_t raw[kSteps][8];
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
@@ -608,11 +635,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.v_full[vb]);
     }
+    }
   } else if (warp == kMma) {
     // ------------------------------------------------------------ MMA issue
     constexpr uint32_t kPanelK = kN * 128, kPanelV = D * 128;
     const uint32_t idesc_s = idesc_f16(kM, kN), idesc_o = idesc_f16(kM, D);
-    uint32_t unit = 0;
     bool ok = true;
     auto scores = [&](uint32_t c) {  // S(c) = Q K(c)^T
       const uint32_t b = c & 1;
@@ -629,9 +656,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       }
       __syncwarp();
     };
-    while (it.valid()) {
-      const int t0 = it.t, t1 = it.end;
-      ok = ok && mbar_wait_warp(&sm.q_full, unit & 1, wg, 70);
+    for (;;) {
+      const UnitInfo* u;
+      ok = unit_open(u) && ok;
+      if (!ok) break;
+      const int t0 = warp_bcast(u->t0), t1 = warp_bcast(u->t1);
+      if (t0 == t1) break;
+      ok = ok && mbar_wait_warp(&sm.q_full, k & 1, wg, 70);
       tc_fence_after();
       scores(c);
       for (int t = t0; t < t1; ++t, ++c) {
@@ -653,9 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         }
         __syncwarp();
       }
-      ++unit;
-      next_unit(p, G, it.u);
-      it.open(it.u.at);
+      unit_close();
     }
     if (elect_one()) {
       tc_commit(&sm.drain);
@@ -663,14 +692,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------ page ids and scales, four tiles at a time
-    while (it.valid()) {
-      const Unit u = it.u;
-      for (int t = it.t; t < it.end; t += 4) {
+    // ------------------------------------------------------------ units; page ids and scales, four tiles at a time
+    Unit u = {};
+    if (works) {
+      u.b = sm.start[0];
+      u.h = sm.start[1];
+      u.rt = sm.start[2];
+      u.at = sm.start_at;
+      load_request(p, G, u);
+      u.nt = unit_tiles(u.n, u.len, G, u.rt);
+    }
+    auto announce = [&](int t0, int t1) {
+      const uint32_t slot = k % kUnitSlots;
+      // a unit is never replaced before every role is done with it
+      const bool ok = mbar_wait(&sm.unit_empty[slot], ((k / kUnitSlots) & 1) ^ 1, wg, 75);
+      if (!__all_sync(kFullMask, ok)) return false;
+      if (lane == 0) {
+        sm.unit[slot] = UnitInfo{t0, t1, u.nt, u.len, u.h, u.rt, u.row0, u.n, u.at};
+        mbar_arrive(&sm.unit_full[slot]);
+      }
+      __syncwarp();
+      ++k;
+      return true;
+    };
+    bool ok = true;
+    while (works && u.at < t_last) {
+      const int t0 = (int)max(0ll, t_first - u.at), t1 = (int)min((long long)u.nt, t_last - u.at);
+      ok = announce(t0, t1);
+      if (!ok) break;
+      for (int t = t0; t < t1; t += 4) {
         const int j = lane & 7, tt = t + (lane >> 3), token = tt * kN + 16 * j;
         int first = -1;
         float ks = 0.0f, log_vs = -INFINITY, inv_vs = 0.0f;
-        if (tt < it.end && token < u.len) {
+        if (tt < t1 && token < u.len) {
           const int id = p.table[u.b * p.ld_table + (token >> p.page_shift)];
           if ((unsigned)id >= (unsigned)p.num_pages) {
             record_status(p.status, kStatusOffsets, 50);
@@ -682,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             inv_vs = 1.0f / vs;
           }
         }
-        for (int x = 0; x < 4 && t + x < it.end; ++x, ++c) {
+        for (int x = 0; x < 4 && t + x < t1; ++x, ++c) {
           const uint32_t slot = c % kPageSlots;
           mbar_wait(&sm.page_empty[slot], ((c / kPageSlots) & 1) ^ 1, wg, 73);
           if (lane >> 3 == x) sm.page[slot][j] = make_float4(__int_as_float(first), ks, log_vs, inv_vs);
@@ -690,9 +744,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
           if (lane == 0) mbar_arrive(&sm.page_full[slot]);
         }
       }
-      next_unit(p, G, it.u);
-      it.open(it.u.at);
+      next_unit(p, G, u);
     }
+    if (ok) announce(0, 0);
   }
   tc_fence_before();
   __syncthreads();
