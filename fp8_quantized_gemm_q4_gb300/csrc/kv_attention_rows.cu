@@ -4,8 +4,9 @@
 // A unit is 128 rows (row r = i * G + g: token i, head g of a KV head's group)
 // against its cached tokens in tiles of 128.  The codes are exact in fp16 but not
 // an operand type that fp16 may be multiplied with, so every tile is widened on
-// the way: warps read the codes from L2, convert them and write K and V^T to
-// shared memory as fp16 in the tensor core's 128-byte swizzled layout.  q and
+// the way: warps read the codes from L2, convert them and write K and V to shared
+// memory as fp16 in the tensor core's 128-byte swizzled layout, both as rows of
+// tokens (K-major for S = Q K^T, MN-major for O = P V).  q and
 // the softmax weights are A operands in tensor memory and cost no shared
 // memory traffic.  Per tile and SM: 1024 clocks of MMA, 512 of writing and 512 of
 // the MMAs' reading 64 KB, 500 of exponentials, so the pieces balance where each
@@ -49,10 +50,10 @@ struct UnitInfo {
 template <int D>
 struct RowsSmem {
   alignas(1024) uint8_t k[2][kN * D * 2];  // [D / 64][token][64 columns]
-  alignas(1024) uint8_t v[2][D * kN * 2];  // [token / 64][column][64 tokens]
+  alignas(1024) uint8_t v[2][kN * D * 2];  // the same of V
   float4 page[kPageSlots][kGroups];        // first row of codes (int, -1: none), K scale, log2 of V scale, 1 / V scale
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2];
-  uint64_t page_full[kPageSlots], page_empty[kPageSlots], o_done, q_full, drain;
+  uint64_t page_full[kPageSlots], page_empty[kPageSlots], o_done, unit_done, q_full, drain;
   UnitInfo unit[kUnitSlots];
   uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
   float swap[2][kM];                       // between the two threads of a row
@@ -63,8 +64,10 @@ struct RowsSmem {
   int abort_flag, last;
 };
 
-__device__ __forceinline__ uint32_t idesc_f16(int M, int N) {  // fp16 x fp16 -> fp32, both K-major
-  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+// fp16 x fp16 -> fp32; A K-major, B K-major or (mn) MN-major
+__device__ __forceinline__ uint32_t idesc_f16(int M, int N, bool mn) {
+  return (1u << 4) | (static_cast<uint32_t>(mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
 }
 // D[tmem] (+)= A[tmem] B[smem]^T
 __device__ __forceinline__ void mma_ts_f16(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
@@ -172,6 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       mbar_init(&sm.unit_empty[s], kSoft + 8 + 1);
     }
     mbar_init(&sm.o_done, 1);
+    mbar_init(&sm.unit_done, 1);
     mbar_init(&sm.q_full, kSoft);
     mbar_init(&sm.drain, 1);
     fence_barrier_init();
@@ -364,7 +368,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             mx = fmaxf(mx, fmaf(g, qscale * pg.y, pg.z));
           }
         }
-        bool waited = t == t0;  // o_done of the tile before: none, or not waited for yet
         if (softmax_any(mx > m + 8.0f)) {
           sm.swap[hf][r128] = mx;
           softmax_sync();
@@ -374,8 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
           m = up ? mx : m;
           l *= f;
           if (t > t0) {
+            // the product of the tile before; those further back were done before
+            // these scores, so the phase's parity says which one it is
             mbar_wait(&sm.o_done, (c - 1) & 1, wg, 62);
-            waited = true;
             tc_fence_after();
 #pragma unroll 1
             for (int x = hf * (D / 2); x < (hf + 1) * (D / 2); x += 32) {
@@ -415,9 +419,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
           }
         }
         tmem_st_wait();
-        // every phase of o_done is waited for in turn; the product of this tile
-        // could not begin before that of the last one anyway
-        if (!waited) mbar_wait(&sm.o_done, (c - 1) & 1, wg, 63);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -428,12 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       // ---- the unit's rows.  Its scores are done: the next unit's q goes first,
       // so that the next scores run beside what follows.
       const Row was = row;
+      const uint32_t unit = k;
       const int row0 = u->row0, nt = u->nt;
       const long long at = u->at;
       unit_close();
       dead = softmax_any(!unit_open(u));
       if (!dead && u->t0 < u->t1) row = load_q(*u);
-      mbar_wait(&sm.o_done, (c - 1) & 1, wg, 64);
+      mbar_wait(&sm.unit_done, unit & 1, wg, 64);
       tc_fence_after();
       softmax_sync();  // swap has been read
       sm.swap[hf][r128] = l;
@@ -527,119 +529,71 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         if (atomicAdd(p.counters + c0, 1) == c1 - c0) p.counters[c0] = 0;
       }
     }
-  } else if (warp < kSoft + 4) {
-    // ------------------------------------------------------------ K codes -> fp16
+  } else if (warp < kSoft + 8) {
+    // ------------------------------------------------------------ K (four warps) and V (four warps) codes -> fp16
     // Lane: 16 codes of a token (and the token's place among its warp's), such
-    // that eight lanes in a row store to eight different chunks.
+    // that eight lanes in a row store to eight different chunks.  The codes of
+    // a tile are read while those of the tile before are converted.
     constexpr int kSteps = kN * D / (128 * 16);           // 16-byte loads per thread
     constexpr int kStepTokens = kN / kSteps;
-    const int w = warp - kSoft, q = lane & 3;
+    const bool is_v = warp >= kSoft + 4;
+    const int w = warp & 3, q = lane & 3;
     const int panel = D == 128 ? (lane >> 3) & 1 : 0;
     const int tok = D == 128 ? w * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1) : w * 8 + (lane >> 2);
-    const uint8_t* codes = p.k_codes + (tok & 15) * D + 64 * panel + 16 * q;
+    const uint8_t* codes = (is_v ? p.v_codes : p.k_codes) + (tok & 15) * D + 64 * panel + 16 * q;
+    const uint32_t base = smem_u32(is_v ? sm.v[0] : sm.k[0]) + panel * (kN * 128) + tok * 128;
+    const uint32_t at0 = base + (((2 * q) ^ (tok & 7)) << 4), at1 = base + (((2 * q + 1) ^ (tok & 7)) << 4);
+    uint64_t* full = is_v ? sm.v_full : sm.k_full;
+    uint64_t* empty = is_v ? sm.v_empty : sm.k_empty;
     for (;;) {
       const UnitInfo* u;
       if (!unit_open(u)) break;
-      const int t1 = u->t1, len = u->len;
-      int t = u->t0;
-      if (t == t1) break;
+      const int t0 = u->t0, t1 = u->t1, len = u->len;
+      if (t0 == t1) break;
       unit_close();
-    for (; t < t1; ++t, ++c) {
-      const uint32_t kb = c & 1, slot = c % kPageSlots;
-      mbar_wait(&sm.page_full[slot], (c / kPageSlots) & 1, wg, 65);
-      const int left = len - t * kN;  // tokens from the tile's first on
       uint4 raw[kSteps];
+      auto load = [&](int t, uint32_t c) {
+        const uint32_t slot = c % kPageSlots;
+        mbar_wait(&sm.page_full[slot], (c / kPageSlots) & 1, wg, 65);
+        const int left = len - t * kN;  // tokens from the tile's first on
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int x = s * kStepTokens + tok, first = __float_as_int(sm.page[slot][x >> 4].x);
-        raw[s] = make_uint4(0, 0, 0, 0);
-        if (first >= 0 && x < left) raw[s] = __ldg(reinterpret_cast<const uint4*>(codes + (long long)first * D));
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.page_empty[slot]);
-      mbar_wait(&sm.k_empty[kb], ((c >> 1) & 1) ^ 1, wg, 66);
-      const uint32_t base = smem_u32(sm.k[kb]) + panel * (kN * 128) + tok * 128;
-      const uint32_t at0 = base + (((2 * q) ^ (tok & 7)) << 4), at1 = base + (((2 * q + 1) ^ (tok & 7)) << 4);
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const uint32_t in[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
-        uint32_t h[8];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          h[2 * y] = e4m3x2_to_f16x2((uint16_t)in[y]);
-          h[2 * y + 1] = e4m3x2_to_f16x2((uint16_t)(in[y] >> 16));
+        for (int s = 0; s < kSteps; ++s) {
+          const int x = s * kStepTokens + tok, first = __float_as_int(sm.page[slot][x >> 4].x);
+          raw[s] = make_uint4(0, 0, 0, 0);
+          if (first >= 0 && x < left) raw[s] = __ldg(reinterpret_cast<const uint4*>(codes + (long long)first * D));
         }
-        st_shared_v4(at0 + s * (kStepTokens * 128), h[0], h[1], h[2], h[3]);
-        st_shared_v4(at1 + s * (kStepTokens * 128), h[4], h[5], h[6], h[7]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.k_full[kb]);
-    }
-    }
-  } else if (warp < kSoft + 8) {
-    // ------------------------------------------------------------ V codes -> fp16, transposed
-    // Lane: 8 tokens x 4 columns, as eight 4-byte loads; four lanes share their
-    // columns and take four token groups of 8 in a row.
-    constexpr int kSteps = D / 32;                         // blocks of 32 tokens x 32 columns per warp
-    const int w = warp - kSoft - 4, tl = lane & 3, dl = lane >> 2;
-    const int col = 32 * (w % (D / 32)) + 4 * dl, first = D == 128 ? 0 : 2 * (w >> 1);
-    const uint8_t* codes = p.v_codes + (8 * (tl & 1)) * D + col;
-    for (;;) {
-      const UnitInfo* u;
-      if (!unit_open(u)) break;
-      const int t1 = u->t1, len = u->len;
-      int t = u->t0;
-      if (t == t1) break;
-      unit_close();
-    for (; t < t1; ++t, ++c) {
-      const uint32_t vb = c & 1, slot = c % kPageSlots;
-      mbar_wait(&sm.page_full[slot], (c / kPageSlots) & 1, wg, 67);
-      const int left = len - t * kN;  // tokens from the tile's first on
-      uint32_t raw[kSteps][8];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.page_empty[slot]);
+      };
+      load(t0, c);
+      for (int t = t0; t < t1; ++t, ++c) {
+        uint4 now[kSteps];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int x = 32 * (first + s) + 8 * tl, page_row = __float_as_int(sm.page[slot][x >> 4].x);
-        const uint8_t* v = codes + (long long)page_row * D;
-        if (page_row >= 0 && x + 8 <= left) {
+        for (int s = 0; s < kSteps; ++s) now[s] = raw[s];
+        if (t + 1 < t1) load(t + 1, c + 1);
+        const uint32_t b = c & 1, to = b * (kN * D * 2);
+        mbar_wait(&empty[b], ((c >> 1) & 1) ^ 1, wg, 66);
 #pragma unroll
-          for (int y = 0; y < 8; ++y) raw[s][y] = __ldg(reinterpret_cast<const uint32_t*>(v + y * D));
-        } else {
+        for (int s = 0; s < kSteps; ++s) {
+          const uint32_t in[4] = {now[s].x, now[s].y, now[s].z, now[s].w};
+          uint32_t h[8];
 #pragma unroll
-          for (int y = 0; y < 8; ++y)
-            raw[s][y] = page_row >= 0 && x + y < left ? __ldg(reinterpret_cast<const uint32_t*>(v + y * D)) : 0u;
+          for (int y = 0; y < 4; ++y) {
+            h[2 * y] = e4m3x2_to_f16x2((uint16_t)in[y]);
+            h[2 * y + 1] = e4m3x2_to_f16x2((uint16_t)(in[y] >> 16));
+          }
+          st_shared_v4(at0 + to + s * (kStepTokens * 128), h[0], h[1], h[2], h[3]);
+          st_shared_v4(at1 + to + s * (kStepTokens * 128), h[4], h[5], h[6], h[7]);
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[b]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.page_empty[slot]);
-      mbar_wait(&sm.v_empty[vb], ((c >> 1) & 1) ^ 1, wg, 68);
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int block = first + s, chunk = (block & 1) * 4 + tl;
-        const uint32_t base = smem_u32(sm.v[vb]) + (block >> 1) * (D * 128);
-        uint32_t h[4][4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {  // tokens 2 y, 2 y + 1: columns 0, 1 and 2, 3 in pairs of tokens
-          const uint32_t a = __byte_perm(raw[s][2 * y], raw[s][2 * y + 1], 0x5140);
-          const uint32_t b = __byte_perm(raw[s][2 * y], raw[s][2 * y + 1], 0x7362);
-          h[0][y] = e4m3x2_to_f16x2((uint16_t)a);
-          h[1][y] = e4m3x2_to_f16x2((uint16_t)(a >> 16));
-          h[2][y] = e4m3x2_to_f16x2((uint16_t)b);
-          h[3][y] = e4m3x2_to_f16x2((uint16_t)(b >> 16));
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          st_shared_v4(base + (col + e) * 128 + ((chunk ^ ((col + e) & 7)) << 4), h[e][0], h[e][1], h[e][2], h[e][3]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.v_full[vb]);
-    }
     }
   } else if (warp == kMma) {
     // ------------------------------------------------------------ MMA issue
-    constexpr uint32_t kPanelK = kN * 128, kPanelV = D * 128;
-    const uint32_t idesc_s = idesc_f16(kM, kN), idesc_o = idesc_f16(kM, D);
+    constexpr uint32_t kPanel = kN * 128;  // 64 columns of a tile
+    const uint32_t idesc_s = idesc_f16(kM, kN, false), idesc_o = idesc_f16(kM, D, true);
     bool ok = true;
     auto scores = [&](uint32_t c) {  // S(c) = Q K(c)^T
       const uint32_t b = c & 1;
@@ -650,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       if (elect_one()) {
 #pragma unroll
         for (int x = 0; x < D / 16; ++x)
-          mma_ts_f16(tmem + kColS + b * kN, tmem + kColQ + 8 * x, dk + (x / 4) * (kPanelK >> 4) + 2 * (x % 4), idesc_s, x > 0);
+          mma_ts_f16(tmem + kColS + b * kN, tmem + kColQ + 8 * x, dk + (x / 4) * (kPanel >> 4) + 2 * (x % 4), idesc_s, x > 0);
         tc_commit(&sm.k_empty[b]);
         tc_commit(&sm.s_full[b]);
       }
@@ -673,14 +627,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         ok = ok && mbar_wait_warp(&sm.p_full[b], (c >> 1) & 1, wg, 72);
         if (!ok) continue;
         tc_fence_after();
-        const uint64_t dv = smem_desc(smem_u32(sm.v[b]), 16, 1024, kLayoutSw128);
+        // 64 columns a panel, 8 tokens 1024 bytes
+        const uint64_t dv = smem_desc(smem_u32(sm.v[b]), kPanel, 1024, kLayoutSw128);
         if (elect_one()) {
 #pragma unroll
           for (int x = 0; x < kN / 16; ++x)
-            mma_ts_f16(tmem + kColO, tmem + kColS + b * kN + (x / 4) * kHalf + 8 * (x % 4), dv + (x / 4) * (kPanelV >> 4) + 2 * (x % 4), idesc_o,
+            mma_ts_f16(tmem + kColO, tmem + kColS + b * kN + (x / 4) * kHalf + 8 * (x % 4), dv + x * (16 * 128 >> 4), idesc_o,
                        t > t0 || x > 0);
           tc_commit(&sm.v_empty[b]);
           tc_commit(&sm.o_done);
+          if (t + 1 == t1) tc_commit(&sm.unit_done);
         }
         __syncwarp();
       }
@@ -758,8 +714,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
 
 template <int D>
 cudaError_t launch(const KvAttentionLaunch& L, cudaStream_t stream) {
-  // more than half of an SM's shared memory: one CTA an SM, as tensor memory has it
-  constexpr int kNeed = (int)sizeof(RowsSmem<D>) + 1024, kSmem = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
+  // all of an SM's shared memory: one CTA an SM, as tensor memory has it
+  constexpr int kSmem = 227 * 1024;
+  static_assert(sizeof(RowsSmem<D>) + 1024 <= kSmem, "shared memory");
   static const cudaError_t attr =
       cudaFuncSetAttribute(kv_attention_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (attr != cudaSuccess) return attr;
