@@ -202,6 +202,12 @@ cudaError_t launch_kv_release(const KvReleaseParams& p, cudaStream_t stream) {
 // subnormals.
 // ---------------------------------------------------------------------------
 constexpr int kAppendWarps = 4;
+constexpr int kAppendThreads = kAppendWarps * 32;
+// Rows from which a CTA takes a page's worth of rows instead of four.  Four rows
+// suit decode steps (64 rows, 8 heads: the launch and four dependent reads are all
+// there is); a prompt of 16384 rows leaves 15 of 16 such CTAs without work (80 us
+// against 20 us).
+constexpr int kAppendWideRows = 2048;
 
 // log2 of the scale for this amax (>= 0)
 __device__ __forceinline__ int scale_exp(float amax) {
@@ -237,97 +243,181 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
-template <bool kBf16, int D>
-__global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes a row, rows a pass
-  const int lane = threadIdx.x & 31, row = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
-  const int h = blockIdx.y >> 1, which = blockIdx.y & 1;
-  if (row >= p.T) return;
-  const int page = 1 << p.page_shift;
-  const int slot = p.slots[row];
-  if (slot < 0) return;
-  const int id = slot >> p.page_shift, off = slot & (page - 1);
-  if (id >= p.num_pages) {
-    if (lane == 0) record_status(p.status, kStatusOffsets, 45);
-    return;
-  }
-  if (row > 0 && off > 0 && p.slots[row - 1] == slot - 1) return;  // inside a run
-  // the run's length: slots ascend by one up to the page's end
-  int n = 1;
-  for (; n < page - off && row + n < p.T; n += 32) {
-    const int i = n + lane;
-    const bool in = i < page - off && row + i < p.T && p.slots[row + i] == slot + i;
-    const unsigned m = __ballot_sync(kFullMask, in);
-    if (m != kFullMask) {
-      n += __ffs(~m) - 1;
-      break;
-    }
-  }
-  n = min(n, page - off);
-  const void* x = p.x[which];
-  const long long ts = p.tok_stride[which];
-  const long long x0 = row * ts + h * p.head_stride[which] + (lane % kLanes) * 8;
-  float amax = 0.0f;
-  for (int r = lane / kLanes; r < n; r += kRows) {
+// The new scale of a run, and where it grows the page's earlier codes rounded
+// again to it: by `threads` threads, of which this is the t-th.  Returns the
+// scale; old is the page's (read by the caller, used if off > 0).
+template <int D>
+__device__ __forceinline__ float page_scale(uint8_t* codes, int off, float amax, float old, int t, int threads) {
+  const float s = exp2_int(scale_exp(amax));
+  if (off == 0) return s;
+  if (s <= old) return old;
+  const float ratio = old / s;
+  for (int x = t; x < off * (D / 8); x += threads) {
+    uint2* at = reinterpret_cast<uint2*>(codes) + x;
+    const uint2 w = *at;
+    const uint32_t in[2] = {w.x, w.y};
     float v[8];
-    load8<kBf16>(x, x0 + r * ts, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-  }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, d));
-  float s = exp2_int(scale_exp(amax));
-  float* scale = p.scales[which] + (long long)id * p.Hkv + h;
-  uint8_t* codes = p.codes[which] + (((long long)id * p.Hkv + h) << p.page_shift) * D + (lane % kLanes) * 8;
-  if (off > 0) {
-    const float old = *scale;
-    if (s > old) {
-      const float ratio = old / s;
-      for (int r = lane / kLanes; r < off; r += kRows) {
-        uint2* at = reinterpret_cast<uint2*>(codes + r * D);
-        const uint2 w = *at;
-        const uint32_t in[2] = {w.x, w.y};
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)(in[i >> 1] >> (16 * (i & 1))));
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-          v[2 * i] = f.x, v[2 * i + 1] = f.y;
-        }
-        *at = codes8(v, ratio);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)(in[i >> 1] >> (16 * (i & 1))));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+      v[2 * i] = f.x, v[2 * i + 1] = f.y;
     }
-    s = fmaxf(s, old);
+    *at = codes8(v, ratio);
   }
-  const float inv = 1.0f / s;
-  for (int r = lane / kLanes; r < n; r += kRows) {
-    float v[8];
-    load8<kBf16>(x, x0 + r * ts, v);
-    *reinterpret_cast<uint2*>(codes + (off + r) * D) = codes8(v, inv);
-  }
-  __syncwarp();
-  if (lane == 0) *scale = s;
+  return s;
 }
 
-template <bool kBf16>
+// A run of n rows from row `row` on, into page `id` at place off, by a group of
+// kThreads threads (a warp or the CTA); `reduce` gives every thread the largest
+// of their values.  What a thread reads stays in registers, up to kKeep times 8
+// elements; a longer run's rest is read again.
+template <bool kBf16, int D, int kThreads, typename Reduce>
+__device__ __forceinline__ void append_run(const KvAppendParams& p, int which, int h, int row, int n, int id, int off,
+                                           int t, Reduce reduce) {
+  constexpr int kKeep = kBf16 ? 8 : 4, kVecs = D / 8;
+  const long long page = (long long)id * p.Hkv + h;
+  const long long ts = p.tok_stride[which];
+  const long long x0 = row * ts + h * p.head_stride[which];
+  float* scale = p.scales[which] + page;
+  uint8_t* codes = p.codes[which] + (page << p.page_shift) * D;
+  const float old = off > 0 ? *scale : 0.0f;
+  const int total = n * kVecs;
+  float kept[kKeep][8];
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    const int x = i * kThreads + t;
+    if (x < total) {
+      load8<kBf16>(p.x[which], x0 + (x / kVecs) * ts + (x % kVecs) * 8, kept[i]);
+    } else {
+#pragma unroll
+      for (int y = 0; y < 8; ++y) kept[i][y] = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i)
+#pragma unroll
+    for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fabsf(kept[i][y]));
+  for (int x = kKeep * kThreads + t; x < total; x += kThreads) {
+    float v[8];
+    load8<kBf16>(p.x[which], x0 + (x / kVecs) * ts + (x % kVecs) * 8, v);
+#pragma unroll
+    for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fabsf(v[y]));
+  }
+  amax = reduce(amax);
+  const float s = page_scale<D>(codes, off, amax, old, t, kThreads);
+  const float inv = 1.0f / s;
+  uint2* out = reinterpret_cast<uint2*>(codes) + off * kVecs;
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    const int x = i * kThreads + t;
+    if (x < total) out[x] = codes8(kept[i], inv);
+  }
+  for (int x = kKeep * kThreads + t; x < total; x += kThreads) {
+    float v[8];
+    load8<kBf16>(p.x[which], x0 + (x / kVecs) * ts + (x % kVecs) * 8, v);
+    out[x] = codes8(v, inv);
+  }
+  if constexpr (kThreads == 32) __syncwarp();  // a CTA's reduce() has a barrier: the old scale has been read by all
+  if (t == 0) *scale = s;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, d));
+  return v;
+}
+__device__ __forceinline__ bool slot_ok(const KvAppendParams& p, int slot) {
+  if (slot < 0) return false;
+  if ((slot >> p.page_shift) < p.num_pages) return true;
+  record_status(p.status, kStatusOffsets, 45);
+  return false;
+}
+
+// A warp per row that begins a run.
+template <bool kBf16, int D>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, row = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  if (row >= p.T) return;
+  const int page = 1 << p.page_shift;
+  // lane i has the slot of row - 1 + i: whether the row begins a run, and its length
+  const int near = row - 1 + lane;
+  const int mine = near >= 0 && near < p.T ? p.slots[near] : -1;
+  const int slot = __shfl_sync(kFullMask, mine, 1), before = __shfl_sync(kFullMask, mine, 0);
+  const int off = slot & (page - 1);
+  if (slot < 0 || (off > 0 && before == slot - 1)) return;
+  if (!slot_ok(p, slot)) return;
+  const unsigned run = __ballot_sync(kFullMask, lane == 0 || (lane - 1 < page - off && mine == slot + lane - 1));
+  int n = run == kFullMask ? 31 : __ffs(~run) - 2;
+  if (n == 31)
+    while (n < page - off && row + n < p.T && p.slots[row + n] == slot + n) ++n;
+  append_run<kBf16, D, 32>(p, blockIdx.y & 1, blockIdx.y >> 1, row, n, slot >> p.page_shift, off, lane, warp_max);
+}
+
+// A CTA for a page's worth of rows: it finds the runs that begin there; long ones
+// are done by all warps together, runs of up to four rows by a warp each.
+template <bool kBf16, int D>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_wide_kernel(const __grid_constant__ KvAppendParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ int slots[128 + 128 + 1];  // of the rows from first - 1 on, as far as a run can go
+  __shared__ float maxima[2][kAppendWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int page = 1 << p.page_shift, first = blockIdx.x << p.page_shift;
+  const int rows = min(page, p.T - first);
+  for (int i = tid; i < 2 * page + 1; i += kAppendThreads) {
+    const int r = first - 1 + i;
+    slots[i] = r >= 0 && r < p.T ? p.slots[r] : -1;
+  }
+  __syncthreads();
+  const int which = blockIdx.y & 1, h = blockIdx.y >> 1;
+  int turn = 0, shorts = 0;
+  for (int i = 0; i < rows; ++i) {
+    const int slot = slots[i + 1], off = slot & (page - 1);
+    if (slot < 0 || (off > 0 && slots[i] == slot - 1)) continue;
+    int n = 0;  // the run's length, 32 rows at a time
+    for (unsigned m = kFullMask; m == kFullMask && n < page - off; n += m == kFullMask ? 32 : __ffs(~m) - 1)
+      m = __ballot_sync(kFullMask, n + lane < page - off && slots[i + 1 + n + lane] == slot + n + lane);
+    if (n <= 4) {
+      if ((shorts++ & (kAppendWarps - 1)) == warp && slot_ok(p, slot))
+        append_run<kBf16, D, 32>(p, which, h, first + i, n, slot >> p.page_shift, off, lane, warp_max);
+    } else if (slot_ok(p, slot)) {
+      append_run<kBf16, D, kAppendThreads>(p, which, h, first + i, n, slot >> p.page_shift, off, tid, [&](float v) {
+        v = warp_max(v);
+        if (lane == 0) maxima[turn][warp] = v;
+        __syncthreads();
+        v = fmaxf(fmaxf(maxima[turn][0], maxima[turn][1]), fmaxf(maxima[turn][2], maxima[turn][3]));
+        return v;
+      });
+      turn ^= 1;
+    }
+    i += n - 1;
+  }
+}
+
+template <bool kBf16, int D>
 static cudaError_t launch_append(const KvAppendParams& p, cudaStream_t stream) {
+  const bool wide = p.T >= kAppendWideRows;
+  const int rows = wide ? 1 << p.page_shift : kAppendWarps;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.T + kAppendWarps - 1) / kAppendWarps), (unsigned)(2 * p.Hkv), 1);
-  cfg.blockDim = dim3(kAppendWarps * 32, 1, 1);
+  cfg.gridDim = dim3((unsigned)((p.T + rows - 1) / rows), (unsigned)(2 * p.Hkv), 1);
+  cfg.blockDim = dim3(kAppendThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return p.D == 64 ? cudaLaunchKernelEx(&cfg, kv_append_kernel<kBf16, 64>, p)
-                   : cudaLaunchKernelEx(&cfg, kv_append_kernel<kBf16, 128>, p);
+  return wide ? cudaLaunchKernelEx(&cfg, kv_append_wide_kernel<kBf16, D>, p)
+              : cudaLaunchKernelEx(&cfg, kv_append_kernel<kBf16, D>, p);
 }
 
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream) {
-  return p.x_bf16 ? launch_append<true>(p, stream) : launch_append<false>(p, stream);
+  if (p.x_bf16) return p.D == 64 ? launch_append<true, 64>(p, stream) : launch_append<true, 128>(p, stream);
+  return p.D == 64 ? launch_append<false, 64>(p, stream) : launch_append<false, 128>(p, stream);
 }
 
 }  // namespace bsk
