@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import NamedTuple
 
@@ -55,29 +56,10 @@ class GemmArgs(ctypes.Structure):
     ]
 
 
-class KvAppendArgs(ctypes.Structure):
-    _fields_ = [
-        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int), ("T", ctypes.c_int64),
-        ("Hkv", ctypes.c_int), ("D", ctypes.c_int), ("k_token_stride", ctypes.c_int64),
-        ("k_head_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
-        ("slots", ctypes.c_void_p), ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
-        ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
-        ("page_size", ctypes.c_int),
-    ]
-
-
-class KvAttentionArgs(ctypes.Structure):
-    _fields_ = [
-        ("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
-        ("out", ctypes.c_void_p), ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
-        ("lse", ctypes.c_void_p), ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
-        ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
-        ("page_size", ctypes.c_int), ("block_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64),
-        ("max_pages", ctypes.c_int), ("cu_q", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("B", ctypes.c_int),
-        ("T", ctypes.c_int64), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
-        ("max_q_len", ctypes.c_int), ("softmax_scale", ctypes.c_float), ("wait_timeout_us", ctypes.c_int),
-        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
-    ]
+# bs_kv_append_args and bs_kv_attention_args, packed in native layout: building
+# a ctypes.Structure of as many fields takes three times as long.
+_KV_APPEND_ARGS = struct.Struct("PPiqiiqqqqPPPPPqi4x")
+_KV_ATTENTION_ARGS = struct.Struct("PqqPqqPPPPPqiPqiPPiqiiiifiPN")
 
 
 # Per-call kernel choices of bs_gemm_args (0 = the library's default), see
@@ -177,11 +159,11 @@ def load(path: str | None = None):
         lib.bs_kv_release.restype = I
         lib.bs_kv_release.argtypes = [P, P, I, P, I64, I, P, P, I, I, P]
         lib.bs_kv_append.restype = I
-        lib.bs_kv_append.argtypes = [ctypes.POINTER(KvAppendArgs), P]
+        lib.bs_kv_append.argtypes = [ctypes.c_char_p, P]   # the packed struct
         lib.bs_kv_attention_workspace_bytes.restype = SZ
-        lib.bs_kv_attention_workspace_bytes.argtypes = [ctypes.POINTER(KvAttentionArgs)]
+        lib.bs_kv_attention_workspace_bytes.argtypes = [ctypes.c_char_p]
         lib.bs_kv_attention.restype = I
-        lib.bs_kv_attention.argtypes = [ctypes.POINTER(KvAttentionArgs), P]
+        lib.bs_kv_attention.argtypes = [ctypes.c_char_p, P]
         lib.bs_fp4_matvec.restype = I
         lib.bs_fp4_matvec.argtypes = [P, I64, I, P, P, I64, I64, F, P, P, P, I, I64, P]
         lib.bs_get_device_status.restype = I
@@ -575,8 +557,9 @@ class KVCache(NamedTuple):
                    torch.ones(shape[:2], dtype=torch.float32, device=device))
 
 
-# Short names: a module lookup of torch.int32 and the like costs as much as
-# the check itself, and these calls are as small as a launch.
+# Short names, identities instead of comparisons, one attribute read each: these
+# calls launch kernels of a few microseconds, and their checks cost as much as
+# the launch if they are written at leisure.
 _F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
 
 
@@ -587,7 +570,7 @@ def _check_kv_cache(cache):
     shape = k.shape
     if len(shape) != 4 or v.shape != shape or ks.shape != shape[:2] or vs.shape != shape[:2]:
         raise ValueError("a KV cache is codes [pages, Hkv, page_size, D] and scales [pages, Hkv], twice")
-    if k.dtype != _U8 or v.dtype != _U8 or ks.dtype != _F32 or vs.dtype != _F32:
+    if k.dtype is not _U8 or v.dtype is not _U8 or ks.dtype is not _F32 or vs.dtype is not _F32:
         raise TypeError("KV cache codes are uint8 (e4m3), scales float32")
     if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
         raise ValueError("KV cache buffers must be contiguous")
@@ -596,14 +579,14 @@ def _check_kv_cache(cache):
 
 def _ints(name, *tensors):
     for t in tensors:
-        if t.dtype != _I32 or not t.is_contiguous():
+        if t.dtype is not _I32 or not t.is_contiguous():
             raise TypeError(f"{name}: lengths, tables and slots are contiguous int32 tensors")
 
 
 def _check_table(name, table, B):
     """(row stride, width) of a block table of B requests."""
     shape, stride = table.shape, table.stride()
-    if table.dtype != _I32 or len(shape) != 2 or stride[1] != 1:
+    if table.dtype is not _I32 or len(shape) != 2 or stride[1] != 1:
         raise TypeError(f"{name}: block_table is an int32 [B, max_pages] tensor with contiguous rows")
     if shape[0] != B:
         raise ValueError(f"{name}: block_table has {shape[0]} rows for {B} requests")
@@ -652,20 +635,25 @@ def kv_append(k, v, slots, cache, stream=None):
     """Quantize new keys and values [T, Hkv, D] (fp32 or bf16, any token and
     head strides) into their slots of the 8-bit cache, in place."""
     kc, vc, ks, vs, (pages, Hkv, page, D) = _check_kv_cache(cache)
+    shape = k.shape
     T = slots.numel()
-    shape = (T, Hkv, D)
-    if k.shape != shape or v.shape != shape:
+    if shape != (T, Hkv, D) or v.shape != shape:
         raise ValueError(f"kv_append: k and v are [{T}, {Hkv}, {D}] for these slots and this cache")
     (kt, kh, kd), (vt, vh, vd) = k.stride(), v.stride()
     dt = k.dtype
-    if kd != 1 or vd != 1 or v.dtype != dt:
+    if kd != 1 or vd != 1 or v.dtype is not dt:
         raise ValueError("kv_append: k and v have one type and contiguous rows of D")
-    if dt != _BF16 and dt != _F32:
+    if dt is not _BF16 and dt is not _F32:
         raise TypeError(f"unsupported dtype {dt}")
-    _ints("kv_append", slots)
-    a = KvAppendArgs(k.data_ptr(), v.data_ptr(), DTYPE_BF16 if dt == _BF16 else DTYPE_F32, T, Hkv, D, kt, kh, vt, vh,
-                     slots.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, page)
+    if slots.dtype is not _I32 or not slots.is_contiguous():
+        raise TypeError("kv_append: slots is a contiguous int32 tensor")
+    a = _KV_APPEND_ARGS.pack(k.data_ptr(), v.data_ptr(), DTYPE_BF16 if dt is _BF16 else DTYPE_F32, T, Hkv, D, kt, kh,
+                             vt, vh, slots.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+                             pages, page)
     _check((_lib or load()).bs_kv_append(a, _stream(stream)))
+
+
+_kv_workspace_bytes: dict = {}   # (device, D, only few rows): they do not depend on anything else
 
 
 def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_scale: float | None = None, out=None,
@@ -677,35 +665,42 @@ def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_s
     shape = q.shape
     if out is None:
         out = torch.empty(shape, dtype=_BF16, device=q.device)
-    if q.dtype != _BF16 or out.dtype != _BF16:
+    if q.dtype is not _BF16 or out.dtype is not _BF16:
         raise TypeError("kv_attention: q and out are bfloat16")
     if len(shape) != 3 or shape[2] != D or out.shape != shape:
         raise ValueError(f"kv_attention: q and out are [T, Hq, {D}]")
+    T, Hq, _ = shape
     (qt, qh, qd), (ot, oh, od) = q.stride(), out.stride()
     if qd != 1 or od != 1:
         raise ValueError("kv_attention: rows of q and out are contiguous")
-    T, Hq = shape[0], shape[1]
     B = kv_lens.numel()
     ld, width = _check_table("kv_attention", block_table, B)
     if cu_q.numel() != B + 1:
         raise ValueError("kv_attention: cu_q is [B + 1] and kv_lens [B]")
-    _ints("kv_attention", cu_q, kv_lens)
-    if lse is not None and (lse.dtype != _F32 or lse.shape != shape[:2] or not lse.is_contiguous()):
-        raise ValueError("kv_attention: lse is a contiguous float32 [T, Hq] tensor")
-    a = KvAttentionArgs(q.data_ptr(), qt, qh, out.data_ptr(), ot, oh, None if lse is None else lse.data_ptr(),
-                        kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, page,
-                        block_table.data_ptr(), ld, width, cu_q.data_ptr(), kv_lens.data_ptr(), B, T, Hq, Hkv, D,
-                        max_q_len, D ** -0.5 if softmax_scale is None else softmax_scale)
-    opts = getattr(_tls, "opts", None)
-    if opts:
-        a.wait_timeout_us = opts.get("wait_timeout_us", 0)
-    lib = _lib or load()
+    if cu_q.dtype is not _I32 or kv_lens.dtype is not _I32 or not cu_q.is_contiguous() or not kv_lens.is_contiguous():
+        raise TypeError("kv_attention: cu_q and kv_lens are contiguous int32 tensors")
+    if lse is None:
+        lse_ptr = 0
+    else:
+        if lse.dtype is not _F32 or lse.shape != (T, Hq) or not lse.is_contiguous():
+            raise ValueError("kv_attention: lse is a contiguous float32 [T, Hq] tensor")
+        lse_ptr = lse.data_ptr()
     handle = _stream(stream)
-    nbytes = lib.bs_kv_attention_workspace_bytes(a)
-    if nbytes:
+    opts = getattr(_tls, "opts", None)
+    args = (q.data_ptr(), qt, qh, out.data_ptr(), ot, oh, lse_ptr, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(),
+            vs.data_ptr(), pages, page, block_table.data_ptr(), ld, width, cu_q.data_ptr(), kv_lens.data_ptr(), B, T,
+            Hq, Hkv, D, max_q_len, D ** -0.5 if softmax_scale is None else softmax_scale,
+            opts.get("wait_timeout_us", 0) if opts else 0)
+    lib = _lib or load()
+    dev = q.get_device()
+    key = (dev, D, (max_q_len or T) * Hq <= 16 * Hkv)
+    nbytes = _kv_workspace_bytes.get(key)
+    if nbytes is None:
+        nbytes = _kv_workspace_bytes[key] = int(lib.bs_kv_attention_workspace_bytes(_KV_ATTENTION_ARGS.pack(*args, 0, 0)))
+    ws = _workspaces.get((dev, handle))
+    if ws is None or ws.numel() < nbytes:
         ws = _workspace_of(q.device, handle, nbytes)
-        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
-    _check(lib.bs_kv_attention(a, handle))
+    _check(lib.bs_kv_attention(_KV_ATTENTION_ARGS.pack(*args, ws.data_ptr(), nbytes), handle))
     return out
 
 
@@ -716,15 +711,15 @@ def matvec_fp4(x, codes, sf, out_dtype=torch.bfloat16, alpha: float = 1.0, bias=
     Y = alpha tensor_scale x W^T + bias, x left unquantized."""
     (M, K), (N, half) = x.shape, codes.shape
     ldx, one = x.stride()
-    if x.dtype != _BF16 or one != 1:
+    if x.dtype is not _BF16 or one != 1:
         raise TypeError("matvec_fp4: x is a bfloat16 [M, K] tensor with contiguous rows")
-    if codes.dtype != _U8 or half * 2 != K or not codes.is_contiguous():
+    if codes.dtype is not _U8 or half * 2 != K or not codes.is_contiguous():
         raise ValueError(f"matvec_fp4: codes are contiguous uint8 [N, {K // 2}]")
-    if sf.dtype != _U8 or sf.numel() < (N + 127) // 128 * 128 * (K // 16):
+    if sf.dtype is not _U8 or sf.numel() < (N + 127) // 128 * 128 * (K // 16):
         raise ValueError("matvec_fp4: sf are the uint8 scales of [N, K], bs_sf_bytes(N, K) of them")
-    if bias is not None and (bias.dtype != _BF16 or bias.numel() != N or not bias.is_contiguous()):
+    if bias is not None and (bias.dtype is not _BF16 or bias.numel() != N or not bias.is_contiguous()):
         raise ValueError("matvec_fp4: bias is a contiguous bfloat16 [N] tensor")
-    if tensor_scale is not None and tensor_scale.dtype != _F32:
+    if tensor_scale is not None and tensor_scale.dtype is not _F32:
         raise TypeError("matvec_fp4: tensor_scale is a float32 tensor")
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=x.device)

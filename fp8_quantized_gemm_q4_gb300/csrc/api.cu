@@ -1153,7 +1153,8 @@ bs_status bs_kv_append(const bs_kv_append_args* a, bs_stream_t stream) {
   if (a->T < 0 || a->T > INT32_MAX) return fail(BS_ERR_INVALID, "kv_append: T=%lld", (long long)a->T);
   if (a->dtype != BS_DTYPE_F32 && a->dtype != BS_DTYPE_BF16)
     return fail(BS_ERR_INVALID, "kv_append: dtype %d", a->dtype);
-  if (2 * (int64_t)a->Hkv > 65535) return fail(BS_ERR_UNSUPPORTED, "kv_append: Hkv=%d", a->Hkv);
+  if (a->Hkv > 16384 || (a->T + 3) / 4 * 2 * a->Hkv > INT32_MAX)  // the launch grid
+    return fail(BS_ERR_UNSUPPORTED, "kv_append: T=%lld rows of Hkv=%d heads in one call", (long long)a->T, a->Hkv);
   if (a->T == 0) return BS_OK;
   if (!a->k || !a->v || !a->slots || !a->k_codes || !a->v_codes || !a->k_scales || !a->v_scales)
     return fail(BS_ERR_INVALID, "kv_append: null pointer");

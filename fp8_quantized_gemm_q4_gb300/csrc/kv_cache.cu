@@ -203,11 +203,10 @@ cudaError_t launch_kv_release(const KvReleaseParams& p, cudaStream_t stream) {
 // ---------------------------------------------------------------------------
 constexpr int kAppendWarps = 4;
 constexpr int kAppendThreads = kAppendWarps * 32;
-// Rows from which a CTA takes a page's worth of rows instead of four.  Four rows
-// suit decode steps (64 rows, 8 heads: the launch and four dependent reads are all
-// there is); a prompt of 16384 rows leaves 15 of 16 such CTAs without work (80 us
-// against 20 us).
-constexpr int kAppendWideRows = 2048;
+// Rows from which a warp takes 16 rows instead of one.  One suits decode steps (64
+// rows, 8 heads: the launch and three dependent reads are all there is); a prompt
+// of 16384 rows on 64-token pages leaves 63 of 64 such warps without work (80 us).
+constexpr int kAppendWideRows = 2048, kWideRows = 16;
 
 // log2 of the scale for this amax (>= 0)
 __device__ __forceinline__ int scale_exp(float amax) {
@@ -219,108 +218,68 @@ __device__ __forceinline__ int scale_exp(float amax) {
 }
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// Eight elements of a row as floats
+// Eight elements of a row, as they lie in memory
 template <bool kBf16>
-__device__ __forceinline__ void load8(const void* x, long long at, float (&v)[8]) {
-  if constexpr (kBf16) {
-    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) + at);
-    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+struct Eight {
+  uint32_t w[kBf16 ? 4 : 8];
+  __device__ __forceinline__ void load(const void* x, long long at) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(x) + at * (kBf16 ? 2 : 4));
+#pragma unroll
+    for (int i = 0; i < (kBf16 ? 1 : 2); ++i) {
+      const uint4 v = p[i];
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  }
+  __device__ __forceinline__ float value(int i) const {
+    if constexpr (kBf16) return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    return __uint_as_float(w[i]);
+  }
+  __device__ __forceinline__ float amax() const {
+    if constexpr (kBf16) {  // in pairs: a maximum of bf16 values is one of them
+      __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
+#pragma unroll
+      for (int i = 1; i < 4; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+      return fmaxf(__low2float(m), __high2float(m));
+    } else {
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(__uint_as_float(w[i])));
+      return m;
+    }
+  }
+  __device__ __forceinline__ uint2 codes(float inv) const {
+    uint32_t h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(a[i] << 16);
-      v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+      const float2 v = __fmul2_rn(make_float2(value(2 * i), value(2 * i + 1)), make_float2(inv, inv));
+      h[i] = f32x2_to_e4m3x2(v.x, v.y);
     }
-  } else {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-    const float4 a = f[0], b = f[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
   }
-}
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
-  uint32_t h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = f32x2_to_e4m3x2(v[2 * i] * inv, v[2 * i + 1] * inv);
-  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-}
+};
 
 // The new scale of a run, and where it grows the page's earlier codes rounded
-// again to it: by `threads` threads, of which this is the t-th.  Returns the
-// scale; old is the page's (read by the caller, used if off > 0).
+// again to it, by a warp.  Returns the scale; old is the page's (used if off > 0).
 template <int D>
-__device__ __forceinline__ float page_scale(uint8_t* codes, int off, float amax, float old, int t, int threads) {
+__device__ __forceinline__ float page_scale(uint8_t* codes, int off, float amax, float old, int lane) {
   const float s = exp2_int(scale_exp(amax));
   if (off == 0) return s;
   if (s <= old) return old;
   const float ratio = old / s;
-  for (int x = t; x < off * (D / 8); x += threads) {
+  for (int x = lane; x < off * (D / 8); x += 32) {
     uint2* at = reinterpret_cast<uint2*>(codes) + x;
     const uint2 w = *at;
     const uint32_t in[2] = {w.x, w.y};
-    float v[8];
+    uint32_t h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t h2 = e4m3x2_to_f16x2((uint16_t)(in[i >> 1] >> (16 * (i & 1))));
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+      h[i] = f32x2_to_e4m3x2(f.x * ratio, f.y * ratio);
     }
-    *at = codes8(v, ratio);
+    *at = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
   }
   return s;
-}
-
-// A run of n rows from row `row` on, into page `id` at place off, by a group of
-// kThreads threads (a warp or the CTA); `reduce` gives every thread the largest
-// of their values.  What a thread reads stays in registers, up to kKeep times 8
-// elements; a longer run's rest is read again.
-template <bool kBf16, int D, int kThreads, typename Reduce>
-__device__ __forceinline__ void append_run(const KvAppendParams& p, int which, int h, int row, int n, int id, int off,
-                                           int t, Reduce reduce) {
-  constexpr int kKeep = kBf16 ? 8 : 4, kVecs = D / 8;
-  const long long page = (long long)id * p.Hkv + h;
-  const long long ts = p.tok_stride[which];
-  const long long x0 = row * ts + h * p.head_stride[which];
-  float* scale = p.scales[which] + page;
-  uint8_t* codes = p.codes[which] + (page << p.page_shift) * D;
-  const float old = off > 0 ? *scale : 0.0f;
-  const int total = n * kVecs;
-  float kept[kKeep][8];
-  float amax = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kKeep; ++i) {
-    const int x = i * kThreads + t;
-    if (x < total) {
-      load8<kBf16>(p.x[which], x0 + (x / kVecs) * ts + (x % kVecs) * 8, kept[i]);
-    } else {
-#pragma unroll
-      for (int y = 0; y < 8; ++y) kept[i][y] = 0.0f;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kKeep; ++i)
-#pragma unroll
-    for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fabsf(kept[i][y]));
-  for (int x = kKeep * kThreads + t; x < total; x += kThreads) {
-    float v[8];
-    load8<kBf16>(p.x[which], x0 + (x / kVecs) * ts + (x % kVecs) * 8, v);
-#pragma unroll
-    for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fabsf(v[y]));
-  }
-  amax = reduce(amax);
-  const float s = page_scale<D>(codes, off, amax, old, t, kThreads);
-  const float inv = 1.0f / s;
-  uint2* out = reinterpret_cast<uint2*>(codes) + off * kVecs;
-#pragma unroll
-  for (int i = 0; i < kKeep; ++i) {
-    const int x = i * kThreads + t;
-    if (x < total) out[x] = codes8(kept[i], inv);
-  }
-  for (int x = kKeep * kThreads + t; x < total; x += kThreads) {
-    float v[8];
-    load8<kBf16>(p.x[which], x0 + (x / kVecs) * ts + (x % kVecs) * 8, v);
-    out[x] = codes8(v, inv);
-  }
-  if constexpr (kThreads == 32) __syncwarp();  // a CTA's reduce() has a barrier: the old scale has been read by all
-  if (t == 0) *scale = s;
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -335,12 +294,58 @@ __device__ __forceinline__ bool slot_ok(const KvAppendParams& p, int slot) {
   return false;
 }
 
+// A run of n rows from row `row` on, into page `id` at place off, by a warp.  What
+// a lane reads stays in its registers, up to kKeep times 8 elements; a longer
+// run's rest is read again.
+template <bool kBf16, int D, int kKeep>
+__device__ __forceinline__ void append_run(const KvAppendParams& p, int which, int h, int row, int n, int id, int off,
+                                           int lane) {
+  constexpr int kVecs = D / 8, kPass = 32 / kVecs;  // lanes a row, rows a pass
+  const long long page = (long long)id * p.Hkv + h;
+  const long long step = p.tok_stride[which] * kPass;
+  const int r0 = lane / kVecs, col = lane % kVecs;
+  long long at = (row + r0) * p.tok_stride[which] + h * p.head_stride[which] + col * 8;
+  const long long again = at + kKeep * step;
+  float* scale = p.scales[which] + page;
+  uint8_t* codes = p.codes[which] + (page << p.page_shift) * D;
+  const float old = off > 0 ? *scale : 0.0f;
+  Eight<kBf16> kept[kKeep], more;
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i, at += step)
+    if (r0 + i * kPass < n) kept[i].load(p.x[which], at);
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i)
+    if (r0 + i * kPass < n) amax = fmaxf(amax, kept[i].amax());
+  for (int i = kKeep; r0 + i * kPass < n; ++i, at += step) {
+    more.load(p.x[which], at);
+    amax = fmaxf(amax, more.amax());
+  }
+  __syncwarp();
+  amax = warp_max(amax);
+  const float s = page_scale<D>(codes, off, amax, old, lane);
+  const float inv = 1.0f / s;
+  uint2* out = reinterpret_cast<uint2*>(codes) + (off + r0) * kVecs + col;
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i)
+    if (r0 + i * kPass < n) out[i * 32] = kept[i].codes(inv);
+  at = again;
+  for (int i = kKeep; r0 + i * kPass < n; ++i, at += step) {
+    more.load(p.x[which], at);
+    out[i * 32] = more.codes(inv);
+  }
+  __syncwarp();  // the old scale has been read by all
+  if (lane == 0) *scale = s;
+}
+
 // A warp per row that begins a run.
 template <bool kBf16, int D>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, row = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const unsigned block = blockIdx.x / (2 * p.Hkv), head = blockIdx.x % (2 * p.Hkv);
+  const int row = block * kAppendWarps + (threadIdx.x >> 5);
   if (row >= p.T) return;
   const int page = 1 << p.page_shift;
   // lane i has the slot of row - 1 + i: whether the row begins a run, and its length
@@ -354,56 +359,60 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
   int n = run == kFullMask ? 31 : __ffs(~run) - 2;
   if (n == 31)
     while (n < page - off && row + n < p.T && p.slots[row + n] == slot + n) ++n;
-  append_run<kBf16, D, 32>(p, blockIdx.y & 1, blockIdx.y >> 1, row, n, slot >> p.page_shift, off, lane, warp_max);
+  append_run<kBf16, D, 4>(p, head / p.Hkv, head % p.Hkv, row, n, slot >> p.page_shift, off, lane);
 }
 
-// A CTA for a page's worth of rows: it finds the runs that begin there; long ones
-// are done by all warps together, runs of up to four rows by a warp each.
+// A warp for the runs that begin in 16 rows; the CTA's four warps take four heads
+// of the same rows.
 template <bool kBf16, int D>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_wide_kernel(const __grid_constant__ KvAppendParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ int slots[128 + 128 + 1];  // of the rows from first - 1 on, as far as a run can go
-  __shared__ float maxima[2][kAppendWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int page = 1 << p.page_shift, first = blockIdx.x << p.page_shift;
-  const int rows = min(page, p.T - first);
-  for (int i = tid; i < 2 * page + 1; i += kAppendThreads) {
-    const int r = first - 1 + i;
-    slots[i] = r >= 0 && r < p.T ? p.slots[r] : -1;
+  constexpr int kWords = 5;  // 32 rows each, from first - 1 on: as far as a run can go
+  const int lane = threadIdx.x & 31, heads = 2 * p.Hkv, groups = (heads + kAppendWarps - 1) / kAppendWarps;
+  const int first = (int)(blockIdx.x / groups) * kWideRows;
+  const int head = (int)(blockIdx.x % groups) * kAppendWarps + (threadIdx.x >> 5);
+  if (head >= heads) return;
+  const int page = 1 << p.page_shift;
+  int slot[kWords];
+  unsigned inside[kWords + 1];  // rows that carry on the run of the row before
+#pragma unroll
+  for (int j = 0; j < kWords; ++j) {
+    const int r = first - 1 + 32 * j + lane;
+    slot[j] = r >= 0 && r < p.T ? p.slots[r] : -1;
   }
-  __syncthreads();
-  const int which = blockIdx.y & 1, h = blockIdx.y >> 1;
-  int turn = 0, shorts = 0;
-  for (int i = 0; i < rows; ++i) {
-    const int slot = slots[i + 1], off = slot & (page - 1);
-    if (slot < 0 || (off > 0 && slots[i] == slot - 1)) continue;
-    int n = 0;  // the run's length, 32 rows at a time
-    for (unsigned m = kFullMask; m == kFullMask && n < page - off; n += m == kFullMask ? 32 : __ffs(~m) - 1)
-      m = __ballot_sync(kFullMask, n + lane < page - off && slots[i + 1 + n + lane] == slot + n + lane);
-    if (n <= 4) {
-      if ((shorts++ & (kAppendWarps - 1)) == warp && slot_ok(p, slot))
-        append_run<kBf16, D, 32>(p, which, h, first + i, n, slot >> p.page_shift, off, lane, warp_max);
-    } else if (slot_ok(p, slot)) {
-      append_run<kBf16, D, kAppendThreads>(p, which, h, first + i, n, slot >> p.page_shift, off, tid, [&](float v) {
-        v = warp_max(v);
-        if (lane == 0) maxima[turn][warp] = v;
-        __syncthreads();
-        v = fmaxf(fmaxf(maxima[turn][0], maxima[turn][1]), fmaxf(maxima[turn][2], maxima[turn][3]));
-        return v;
-      });
-      turn ^= 1;
+#pragma unroll
+  for (int j = 0; j < kWords; ++j) {
+    int before = __shfl_up_sync(kFullMask, slot[j], 1);
+    const int last = j ? __shfl_sync(kFullMask, slot[j ? j - 1 : 0], 31) : -1;
+    if (lane == 0) before = last;
+    inside[j] = __ballot_sync(kFullMask, (slot[j] & (page - 1)) > 0 && slot[j] == before + 1 && before >= 0);
+  }
+  inside[kWords] = 0;
+  const unsigned begins = __ballot_sync(kFullMask, slot[0] >= 0) & ~inside[0] & ((1u << (kWideRows + 1)) - 2);
+  for (unsigned todo = begins; todo; todo &= todo - 1) {
+    const int i = __ffs(todo) - 1, mine = __shfl_sync(kFullMask, slot[0], i);
+    if (!slot_ok(p, mine)) continue;
+    int n = 1;
+    bool on = true;
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+      const unsigned w = __funnelshift_r(inside[j], inside[j + 1], i + 1);
+      if (on) n += w == kFullMask ? 32 : __ffs(~w) - 1;
+      on &= w == kFullMask;
     }
-    i += n - 1;
+    append_run<kBf16, D, kBf16 ? 32 : 16>(p, head / p.Hkv, head % p.Hkv, first - 1 + i, n, mine >> p.page_shift,
+                                          mine & (page - 1), lane);
   }
 }
 
 template <bool kBf16, int D>
 static cudaError_t launch_append(const KvAppendParams& p, cudaStream_t stream) {
   const bool wide = p.T >= kAppendWideRows;
-  const int rows = wide ? 1 << p.page_shift : kAppendWarps;
+  const int rows = wide ? kWideRows : kAppendWarps, heads = wide ? (2 * p.Hkv + kAppendWarps - 1) / kAppendWarps : 2 * p.Hkv;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.T + rows - 1) / rows), (unsigned)(2 * p.Hkv), 1);
+  // the heads of the same rows side by side: together they read whole rows
+  cfg.gridDim = dim3((unsigned)(((long long)p.T + rows - 1) / rows * heads), 1, 1);
   cfg.blockDim = dim3(kAppendThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr;

@@ -56,11 +56,13 @@ def test_append_refusals(bs):
     lib = bs.load()
     assert lib.bs_kv_append(None, None) == bs.BS_ERR_INVALID
 
+    names = "k v dtype T Hkv D k_token_stride k_head_stride v_token_stride v_head_stride slots k_codes v_codes k_scales " \
+            "v_scales num_pages page_size".split()
+    good = dict(zip(names, (F, F, 1, 10, 8, 128, 1024, 128, 1024, 128, F, F, F, F, F, 100, 64)))
+
     def call(**kw):
-        a = bs.KvAppendArgs(F, F, 1, 10, 8, 128, 1024, 128, 1024, 128, F, F, F, F, F, 100, 64)
-        for k, v in kw.items():
-            setattr(a, k, v)
-        return lib.bs_kv_append(ctypes.byref(a), None)
+        a = {k: v or 0 for k, v in {**good, **kw}.items()}
+        return lib.bs_kv_append(bs._KV_APPEND_ARGS.pack(*a.values()), None)
 
     assert call(D=96) == bs.BS_ERR_UNSUPPORTED
     assert call(page_size=24) == bs.BS_ERR_UNSUPPORTED
@@ -81,12 +83,15 @@ def test_attention_refusals(bs):
     lib = bs.load()
     assert lib.bs_kv_attention(None, None) == bs.BS_ERR_INVALID
 
+    names = "q q_token_stride q_head_stride out out_token_stride out_head_stride lse k_codes v_codes k_scales v_scales " \
+            "num_pages page_size block_table ld_table max_pages cu_q kv_lens B T Hq Hkv D max_q_len softmax_scale " \
+            "wait_timeout_us workspace workspace_bytes".split()
+    good = dict(zip(names, (F, 4096, 128, F, 4096, 128, F, F, F, F, F, 100, 64, F, 8, 8, F, F, 4, 4, 32, 8, 128, 1, 0.1, 0,
+                            0, 0)))
+
     def call(**kw):
-        a = bs.KvAttentionArgs(F, 4096, 128, F, 4096, 128, F, F, F, F, F, 100, 64, F, 8, 8, F, F, 4, 4, 32, 8, 128, 1,
-                               0.1, 0, None, 0)
-        for k, v in kw.items():
-            setattr(a, k, v)
-        return lib.bs_kv_attention(ctypes.byref(a), None)
+        a = {k: v or 0 for k, v in {**good, **kw}.items()}
+        return lib.bs_kv_attention(bs._KV_ATTENTION_ARGS.pack(*a.values()), None)
 
     assert call(D=256) == bs.BS_ERR_UNSUPPORTED
     assert call(page_size=0) == bs.BS_ERR_UNSUPPORTED
