@@ -1287,6 +1287,7 @@ bs_status bs_fp4_matvec(const void* x, int64_t ldx, int M, const uint8_t* codes,
   if (out_dtype != BS_DTYPE_F32 && out_dtype != BS_DTYPE_BF16)
     return fail(BS_ERR_INVALID, "fp4_matvec: out_dtype %d", out_dtype);
   if (M > 16) return fail(BS_ERR_UNSUPPORTED, "fp4_matvec: M=%d above 16 (bs_gemm takes more rows)", M);
+  if (K > 1 << 22) return fail(BS_ERR_UNSUPPORTED, "fp4_matvec: K=%lld above 2^22", (long long)K);
   if (K % 64) return fail(BS_ERR_ALIGN, "fp4_matvec: K=%lld not a multiple of 64", (long long)K);
   if (M == 0 || N == 0) return BS_OK;
   if (!x || !codes || !sf || !out) return fail(BS_ERR_INVALID, "fp4_matvec: null pointer");

@@ -661,7 +661,7 @@ bs_status bs_kv_attention(const bs_kv_attention_args *args, bs_stream_t stream);
  * quantization of x, fp32 accumulation.
  *
  *   x       bf16 [M, ldx], 16-byte aligned, ldx % 8 == 0; 0 <= M <= 16
- *   N, K    any N >= 0; K % 64 == 0
+ *   N, K    any N >= 0; K % 64 == 0, K <= 2^22
  *   tensor_scale device fp32 scalar or NULL (= 1); bias bf16 [N] or NULL
  *   out     fp32 or bf16 [M, ldo], aligned to its elements, ldo >= N
  * ------------------------------------------------------------------------- */

@@ -56,6 +56,14 @@ def test_sizes(cuda_lib, M, N, K):
     run(cuda_lib, M, N, K, out_dtype=torch.bfloat16, bias=True, two_level=True)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 19457, 64), (8, 24323, 192), (9, 25000, 576), (16, 29185, 640), (2, 50001, 64),
+                                   (16, 49153, 192), (13, 130, 4160), (3, 1, 4224), (16, 2049, 8256)])
+def test_many_tiles_or_long_rows(cuda_lib, M, N, K):
+    """One to five tiles a warp, several blocks of tiles, K that ends inside a
+    chunk or before some warps' first chunk."""
+    run(cuda_lib, M, N, K, ldx=8, ldo=1)
+
+
 @pytest.mark.parametrize("M", [1, 4, 16])
 def test_epilogue_and_strides(cuda_lib, M):
     for dt in (torch.float32, torch.bfloat16):
