@@ -1,0 +1,82 @@
+"""One layer's attention in serving: FP4 projections around an 8-bit paged cache.
+
+Order of a step, for requests that each bring some new tokens (a prompt, one
+token, a few drafted ones, or none):
+
+  1. bs_kv_plan       pages for the new tokens from the free list, their slots
+  2. bs_fp4_matvec    q, k and v of the new tokens in one product with the
+                      concatenated FP4 weights, x left in bf16 (at most 16
+                      tokens; more go through q4_quantize and bs_gemm with the
+                      same weights)
+  3. bs_kv_append     k and v, read where the product left them, to 8 bits in
+                      their slots
+  4. bs_kv_attention  q over each request's cached tokens, causal
+  5. bs_fp4_matvec    the output projection (or q4_quantize and bs_gemm)
+
+bs_kv_release gives the pages of finished requests back.  Lengths, tables and
+the free list stay on the device and nothing synchronises the host, so a step of
+fixed shape can be captured in a CUDA graph and replayed.
+
+The kernels are the library's; this module holds the buffers and calls them in
+order.  No rotation or normalisation is applied to q and k.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import KVCache, gemm_fp4, kv_append, kv_attention, kv_plan, kv_release, matvec_fp4, q4_quantize
+
+MATVEC_ROWS = 16   # the most rows that bs_fp4_matvec takes
+
+
+def fp4_linear(x, codes, sf, out=None):
+    """x bf16 [T, K] times FP4 weights (codes [N, K/2] and scales of q4_quantize)."""
+    if x.shape[0] <= MATVEC_ROWS:
+        return matvec_fp4(x, codes, sf, out=out)
+    xc, xsf, _ = q4_quantize(x)
+    return gemm_fp4(xc, xsf, codes, sf, x.shape[1], out=out)
+
+
+class DecodeAttention:
+    """Attention of one layer over requests 0 .. B - 1.
+
+    w_qkv, w_out    (codes, scales) of q4_quantize for bf16 weights
+                    [(Hq + 2 Hkv) D, hidden] (rows of q, then k, then v) and
+                    [hidden, Hq D]
+    lens            int32 [B], the cached tokens of each request (device)
+    n_free          int32 [1], the pages left (device)
+    """
+
+    def __init__(self, w_qkv, w_out, Hq: int, Hkv: int, D: int, requests: int, num_pages: int, page_size: int,
+                 max_pages: int):
+        rows = (Hq + 2 * Hkv) * D
+        if w_qkv[0].shape[0] != rows or w_out[0].shape[1] * 2 != Hq * D:
+            raise ValueError(f"DecodeAttention: w_qkv has {rows} rows and w_out {Hq * D} columns")
+        dev = w_qkv[0].device
+        self.w_qkv, self.w_out = w_qkv, w_out
+        self.Hq, self.Hkv, self.D, self.page_size = Hq, Hkv, D, page_size
+        self.cache = KVCache.empty(num_pages, Hkv, page_size, D, device=dev)
+        self.table = torch.full((requests, max_pages), -1, dtype=torch.int32, device=dev)
+        self.free = torch.arange(num_pages, dtype=torch.int32, device=dev)
+        self.n_free = torch.full((1,), num_pages, dtype=torch.int32, device=dev)
+        self.lens = torch.zeros(requests, dtype=torch.int32, device=dev)
+
+    def step(self, x, new_lens, max_new: int):
+        """x bf16 [T, hidden], the new tokens of request 0, then 1, ..;
+        new_lens int32 [B] on the device, their sum at most T, each at most
+        max_new.  Returns bf16 [T, hidden].  A request for which the pages do not
+        suffice gets zeros and keeps its length (device status BS_ERR_PAGES)."""
+        T, q_rows, kv_rows = x.shape[0], self.Hq * self.D, self.Hkv * self.D
+        cu, kv_lens, slots, left = kv_plan(self.lens, new_lens, self.table, self.free, self.n_free, self.page_size, T)
+        qkv = fp4_linear(x, *self.w_qkv)
+        q, k, v = qkv.split([q_rows, kv_rows, kv_rows], 1)
+        kv_append(k.view(T, self.Hkv, self.D), v.view(T, self.Hkv, self.D), slots, self.cache)
+        att = kv_attention(q.view(T, self.Hq, self.D), self.cache, self.table, cu, kv_lens, max_new)
+        self.n_free.copy_(left)
+        torch.maximum(self.lens, kv_lens, out=self.lens)
+        return fp4_linear(att.view(T, q_rows), *self.w_out)
+
+    def release(self, done):
+        """Give back the pages of the requests with done[b] != 0 (int32 [B])."""
+        kv_release(self.lens, done, self.table, self.free, self.n_free, self.page_size)
+        self.lens.masked_fill_(done != 0, 0)

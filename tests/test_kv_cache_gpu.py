@@ -162,6 +162,45 @@ def test_append(cuda_lib, H, D, page, dt, kind):
     assert bs.device_status()[0] == bs.BS_OK
 
 
+@pytest.mark.parametrize("H,D,page,dt", [(1, 128, 128, torch.bfloat16), (3, 64, 128, torch.float32),
+                                         (2, 128, 64, torch.float32), (5, 64, 16, torch.bfloat16),
+                                         (2, 128, 32, torch.bfloat16), (1, 64, 64, torch.bfloat16)])
+def test_append_long(cuda_lib, H, D, page, dt):
+    """Calls of thousands of rows: whole pages, pages that begin late and end
+    early, single tokens, rows to skip, at every offset to the groups of rows that
+    a warp looks at."""
+    bs = cuda_lib
+    rng = random.Random(page + D)
+    gen = torch.Generator(device=DEV).manual_seed(H + D + page)
+    slots, pages = [], 0
+    kinds = [("whole", 5 * page), ("single", 40), ("part", 12), ("whole", 2 * page + 1), ("skip", 37), ("part", 9)]
+    while len(slots) < 2100:
+        kind, n = kinds[rng.randrange(len(kinds))]
+        if kind == "skip":
+            slots += [-1] * rng.randrange(1, n)
+        elif kind == "whole":
+            first = pages * page + rng.choice([0, 0, 1, page - 1])
+            slots += range(first, first + n)
+            pages += n // page + 2
+        else:
+            for _ in range(n):
+                m = 1 if kind == "single" else rng.randrange(1, page + 1)
+                off = rng.randrange(0, page - m + 1)
+                slots += range(pages * page + off, pages * page + off + m)
+                pages += 1
+    T = len(slots)
+    # pages anywhere in the cache; inside a request they follow one another in the rows only
+    ids = list(range(pages))
+    rng.shuffle(ids)
+    slots = [s if s < 0 else ids[s // page] * page + s % page for s in slots]
+    cache = make_cache(bs, gen, pages, H, page, D)
+    qkv = torch.randn((T, 3 * H, D), device=DEV, generator=gen)
+    qkv *= torch.exp2(torch.randint(-6, 7, (T, 1, 1), device=DEV, generator=gen).float())
+    qkv = qkv.to(dt)
+    check_append(bs, qkv[:, H:2 * H], qkv[:, 2 * H:], slots, cache, page)
+    assert bs.device_status()[0] == bs.BS_OK
+
+
 def test_append_extremes(cuda_lib):
     """Amax exactly at, next to and far from 448 * 2^e; zero rows; the clamped ends of the scale range."""
     bs = cuda_lib
