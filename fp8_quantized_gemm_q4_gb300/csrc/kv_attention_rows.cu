@@ -11,13 +11,22 @@
 // memory traffic.  Per tile and SM: 1024 clocks of MMA, 512 of writing and 512 of
 // the MMAs' reading 64 KB, 500 of exponentials, so the pieces balance where each
 // runs beside the others:
-//   warps 0-7   softmax, two threads per row, each half of the columns: S from
-//               tensor memory, weights back into S's place, the running (m, l),
-//               rare rescaling of O (with one thread per row the softmax alone
-//               took 2.5 times the MMAs' time)
-//   warps 8-11  K codes -> fp16        warps 12-15  V codes -> fp16, transposed
-//   warp 16     MMA issue: S(j + 1) = Q K^T goes ahead of O += P(j) V
-//   warp 17     the next units, page ids and scales of the next tiles
+//   warps 0-15   softmax, four threads per row, each a quarter of the columns: S
+//                from tensor memory once, weights back into S's place, the running
+//                (m, l), rare rescaling of O
+//   warps 16-19  K codes -> fp16        warps 20-23  V codes -> fp16
+//   warp 24      MMA issue: S(j + 1) = Q K^T goes ahead of O += P(j) V
+//   warp 25      the next units, page ids and scales of the next tiles
+// What bounds it: the softmax of a tile, whose steps follow one another (S, the
+// maximum, the vote on the reference, the exponentials, the store) and whose
+// warps have 1480 issue slots of about 2900 clocks a tile with the converters.
+// B = 2, 2048 rows x 32 heads over 4000 to 8000 tokens, D = 128: 289 us (773 TFLOP/s);
+// with two threads per row 303 us, with one 2.5 times the MMAs' time.  Also built and
+// measured: two groups of warps on alternate tiles, each with an O of its own and
+// Q in shared memory (303 us: both operands of Q K^T from shared memory take all of
+// its bandwidth), with one O and a reference settled in turn (324 us: P in S's place
+// holds the next scores back), and with columns of its own for P (443 us: there
+// is room for one P only).
 // The tiles of all units form one list that is cut into equal shares, one CTA
 // each; units cut between CTAs are joined by the last CTA to finish a piece.
 #include "kv_attention.cuh"
@@ -28,16 +37,16 @@ namespace {
 constexpr int kM = 128;           // rows of a unit
 constexpr int kN = 128;           // cached tokens of a tile
 constexpr int kGroups = kN / 16;  // groups of 16 tokens: each lies in one page
-constexpr int kSoft = 8, kMma = 16;  // softmax warps, the MMA warp
-constexpr int kThreads = 18 * 32;
-constexpr int kHalf = kN / 2;     // columns of S a softmax thread has
+constexpr int kSoft = 16, kMma = kSoft + 8;  // softmax warps, the MMA warp
+constexpr int kThreads = (kMma + 2) * 32;
+constexpr int kOwn = kN / 4;      // columns of S a softmax thread has
 constexpr int kMinTiles = 2;      // least tiles worth a CTA of its own
 constexpr int kPageSlots = 8;     // tiles whose pages are known ahead
 constexpr int kUnitSlots = 4;     // units known ahead
 constexpr int kCounters = 1024;   // arrival counters at the head of the workspace
 constexpr int kTmemCols = 512;
-// Tensor memory columns: S twice (the weights of 64 tokens go into the first half of
-// the 64 columns that their scores had), O, Q
+// Tensor memory columns: S twice (the weights of 32 tokens go into the first half of
+// the 32 columns that their scores had), O, Q
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384;
 
 // A unit as the roles read it; t0 == t1: the share is done
@@ -56,7 +65,7 @@ struct RowsSmem {
   uint64_t page_full[kPageSlots], page_empty[kPageSlots], o_done, unit_done, q_full, drain;
   UnitInfo unit[kUnitSlots];
   uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
-  float swap[2][kM];                       // between the two threads of a row
+  float swap[4][kM];                       // between the four threads of a row
   long long scan[kThreads / 32];
   long long start_at;
   int start[3];
@@ -76,14 +85,6 @@ __device__ __forceinline__ void mma_ts_f16(uint32_t d, uint32_t a, uint64_t bdes
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
       "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
@@ -269,47 +270,47 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
   };
 
   if (warp < kSoft) {
-    // ------------------------------------------------------------ softmax: two threads per row
+    // ------------------------------------------------------------ softmax: four threads per row
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const int hf = warp >> 2, r128 = tid & (kM - 1);  // half of the columns, row of the unit
+    const int part = warp >> 2, r128 = tid & (kM - 1);  // quarter of the columns, row of the unit
     struct Row {
       int i, hq;     // token, query head
       bool in;
       float qscale;
     };
-    // q to tensor memory, fp16 by a power of two
+    // q to tensor memory, fp16 by a power of two; the scores of the unit before are done by the second barrier
     auto load_q = [&](const UnitInfo& u) {
       Row w;
       const long long r = (long long)u.rt * kM + r128;
       w.i = (int)(r / G), w.hq = u.h * G + (int)(r % G);
       w.in = r < (long long)u.n * G && u.row0 + w.i < p.T;
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (u.row0 + (long long)w.i) * p.q_tok_stride +
-                               w.hq * p.q_head_stride + hf * (D / 2);
-      uint4 v[D / 16];
+                               w.hq * p.q_head_stride + part * (D / 4);
+      uint4 v[D / 32];
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) v[x] = w.in ? __ldg(reinterpret_cast<const uint4*>(q) + x) : make_uint4(0, 0, 0, 0);
+      for (int x = 0; x < D / 32; ++x) v[x] = w.in ? __ldg(reinterpret_cast<const uint4*>(q) + x) : make_uint4(0, 0, 0, 0);
       float amax = 0.0f;
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
+      for (int x = 0; x < D / 32; ++x) {
         const uint32_t y[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
 #pragma unroll
         for (int z = 0; z < 4; ++z)
           amax = max3(amax, fabsf(__uint_as_float(y[z] << 16)), fabsf(__uint_as_float(y[z] & 0xffff0000u)));
       }
       softmax_sync();  // what was in swap has been read
-      sm.swap[hf][r128] = amax;
+      sm.swap[part][r128] = amax;
       softmax_sync();
-      const int up = fp16_up(fmaxf(sm.swap[0][r128], sm.swap[1][r128]));
+      const int up = fp16_up(fmaxf(fmaxf(sm.swap[0][r128], sm.swap[1][r128]), fmaxf(sm.swap[2][r128], sm.swap[3][r128])));
       const float mul = exp2i(up);
       w.qscale = exp2i(-up) * p.scale_log2;
 #pragma unroll
-      for (int x = 0; x < D / 16; x += 2) {
+      for (int x = 0; x < D / 32; x += 2) {
         const uint32_t y[8] = {v[x].x, v[x].y, v[x].z, v[x].w, v[x + 1].x, v[x + 1].y, v[x + 1].z, v[x + 1].w};
         uint32_t h[8];
 #pragma unroll
         for (int z = 0; z < 8; ++z)
           h[z] = pack_f16x2(__uint_as_float(y[z] << 16) * mul, __uint_as_float(y[z] & 0xffff0000u) * mul);
-        tmem_st8(lanes + kColQ + hf * (D / 4) + 4 * x, h);
+        tmem_st8(lanes + kColQ + part * (D / 8) + 4 * x, h);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -327,51 +328,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       const bool in = row.in;
       const float qscale = row.qscale;
       const int seen = in ? u->len - u->n + row.i + 1 : 0;
-      float m = -INFINITY, l = 0.0f;  // l: of this thread's columns
+      float m = -INFINITY, l = 0.0f;  // the row's reference; the sum of this thread's weights
       for (int t = t0; t < t1; ++t, ++c) {
         const uint32_t sb = c & 1, slot = c % kPageSlots;
         mbar_wait(&sm.page_full[slot], (c / kPageSlots) & 1, wg, 60);
         mbar_wait(&sm.s_full[sb], (c >> 1) & 1, wg, 61);
         tc_fence_after();
-        const uint32_t s_at = lanes + kColS + sb * kN;
-        const int limit = seen - t * kN - hf * kHalf;  // of its columns, those that this row sees
-        const float4* page = &sm.page[slot][hf * (kGroups / 2)];
-        // The loops over S stay rolled and short: unrolled, the softmax warps
-        // waited for instructions most of the time.
-        if (__any_sync(kFullMask, limit < kHalf)) {
-#pragma unroll 1
-          for (int x = 0; x < kHalf; x += 16) {
-            uint32_t raw[16];
-            tmem_ld16(s_at + hf * kHalf + x, raw);
-            tmem_ld_wait();
+        const uint32_t s_at = lanes + kColS + sb * kN + part * kOwn;
+        const int limit = seen - t * kN - part * kOwn;  // of its columns, those that this row sees
+        const float4* page = &sm.page[slot][part * (kGroups / 4)];
+        uint32_t raw[kOwn];
+        tmem_ld32(s_at, raw);
+        tmem_ld_wait();
+        if (limit < kOwn) {
 #pragma unroll
-            for (int y = 0; y < 16; ++y)
-              if (x + y >= limit) raw[y] = __float_as_uint(-INFINITY);
-            tmem_st16(s_at + hf * kHalf + x, raw);
-          }
-          tmem_st_wait();
+          for (int y = 0; y < kOwn; ++y)
+            if (y >= limit) raw[y] = __float_as_uint(-INFINITY);
         }
         float mx = -INFINITY;
-#pragma unroll 1
-        for (int x = 0; x < kHalf; x += 32) {
-          uint32_t raw[32];
-          tmem_ld32(s_at + hf * kHalf + x, raw);
-          tmem_ld_wait();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float4 pg = page[x / 16 + h];
-            float g = __uint_as_float(raw[16 * h]);
+        for (int h = 0; h < kOwn / 16; ++h) {
+          const float4 pg = page[h];
+          float g = __uint_as_float(raw[16 * h]);
 #pragma unroll
-            for (int y = 1; y < 15; y += 2)
-              g = max3(g, __uint_as_float(raw[16 * h + y]), __uint_as_float(raw[16 * h + y + 1]));
-            g = fmaxf(g, __uint_as_float(raw[16 * h + 15]));
-            mx = fmaxf(mx, fmaf(g, qscale * pg.y, pg.z));
-          }
+          for (int y = 1; y < 15; y += 2)
+            g = max3(g, __uint_as_float(raw[16 * h + y]), __uint_as_float(raw[16 * h + y + 1]));
+          g = fmaxf(g, __uint_as_float(raw[16 * h + 15]));
+          mx = fmaxf(mx, fmaf(g, qscale * pg.y, pg.z));
         }
         if (softmax_any(mx > m + 8.0f)) {
-          sm.swap[hf][r128] = mx;
+          sm.swap[part][r128] = mx;
           softmax_sync();
-          mx = fmaxf(sm.swap[0][r128], sm.swap[1][r128]);
+          mx = fmaxf(fmaxf(sm.swap[0][r128], sm.swap[1][r128]), fmaxf(sm.swap[2][r128], sm.swap[3][r128]));
           const bool up = mx > m + 8.0f;
           const float f = up ? ex2(m - mx) : 1.0f;
           m = up ? mx : m;
@@ -382,41 +370,34 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             mbar_wait(&sm.o_done, (c - 1) & 1, wg, 62);
             tc_fence_after();
 #pragma unroll 1
-            for (int x = hf * (D / 2); x < (hf + 1) * (D / 2); x += 32) {
-              uint32_t o[32];
-              tmem_ld32(lanes + kColO + x, o);
+            for (int x = part * (D / 4); x < (part + 1) * (D / 4); x += 8) {
+              uint32_t o[8];
+              tmem_ld8(lanes + kColO + x, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-              tmem_st16(lanes + kColO + x, o);
-              tmem_st16(lanes + kColO + x + 16, o + 16);
+              for (int y = 0; y < 8; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tmem_st8(lanes + kColO + x, o);
             }
           }
         }
         const float ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll 1
-        for (int x = 0; x < kHalf; x += 32) {
-          uint32_t raw[32];
-          tmem_ld32(s_at + hf * kHalf + x, raw);
-          tmem_ld_wait();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float4 pg = page[x / 16 + h];
-            // a scale is positive, or 0 with pg.z = -infinity: masked scores must not meet the 0
-            const float f1 = fmaxf(qscale * pg.y, 1e-37f), o1 = pg.z - ref;
-            const float2 f = make_float2(f1, f1), off = make_float2(o1, o1);
-            float2 sum = make_float2(0.0f, 0.0f);
-            uint32_t w[8];
+        for (int h = 0; h < kOwn / 16; ++h) {
+          const float4 pg = page[h];
+          // a scale is positive, or 0 with pg.z = -infinity: masked scores must not meet the 0
+          const float f1 = fmaxf(qscale * pg.y, 1e-37f), o1 = pg.z - ref;
+          const float2 f = make_float2(f1, f1), off = make_float2(o1, o1);
+          float2 sum = make_float2(0.0f, 0.0f);
+          uint32_t w[8];
 #pragma unroll
-            for (int y = 0; y < 16; y += 2) {
-              const float2 z = __ffma2_rn(make_float2(__uint_as_float(raw[16 * h + y]), __uint_as_float(raw[16 * h + y + 1])), f, off);
-              const float2 e = make_float2(ex2(z.x), ex2(z.y));
-              sum = __fadd2_rn(sum, e);
-              w[y / 2] = pack_f16x2(e.x, e.y);
-            }
-            tmem_st8(s_at + hf * kHalf + x / 2 + 8 * h, w);
-            l = fmaf(sum.x + sum.y, pg.w, l);
+          for (int y = 0; y < 16; y += 2) {
+            const float2 z = __ffma2_rn(make_float2(__uint_as_float(raw[16 * h + y]), __uint_as_float(raw[16 * h + y + 1])), f, off);
+            const float2 e = make_float2(ex2(z.x), ex2(z.y));
+            sum = __fadd2_rn(sum, e);
+            w[y / 2] = pack_f16x2(e.x, e.y);
           }
+          tmem_st8(s_at + 8 * h, w);
+          l = fmaf(sum.x + sum.y, pg.w, l);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -438,40 +419,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       mbar_wait(&sm.unit_done, unit & 1, wg, 64);
       tc_fence_after();
       softmax_sync();  // swap has been read
-      sm.swap[hf][r128] = l;
+      sm.swap[part][r128] = l;
       softmax_sync();
-      l = sm.swap[0][r128] + sm.swap[1][r128];
+      l = (sm.swap[0][r128] + sm.swap[1][r128]) + (sm.swap[2][r128] + sm.swap[3][r128]);
       const bool alone = t0 == 0 && t1 == nt;
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const float inv = !alone ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
       const long long tr = row0 + (long long)was.i, lse_at = tr * p.Hq + was.hq;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + tr * p.out_tok_stride + was.hq * p.out_head_stride;
       float* slot = p.work + ((long long)blockIdx.x * 2 + (t0 == 0)) * (kM * (D + 2));
 #pragma unroll 1
-      for (int x = hf * (D / 2); x < (hf + 1) * (D / 2); x += 32) {
-        uint32_t o[32];
-        tmem_ld32(lanes + kColO + x, o);
+      for (int x = part * (D / 4); x < (part + 1) * (D / 4); x += 16) {
+        uint32_t o[16];
+        tmem_ld16(lanes + kColO + x, o);
         tmem_ld_wait();
+#pragma unroll
+        for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * inv);
         if (in && alone) {
 #pragma unroll
-          for (int y = 0; y < 32; y += 8) {
+          for (int y = 0; y < 16; y += 8) {
             uint32_t w[4];
 #pragma unroll
-            for (int z = 0; z < 4; ++z)
-              w[z] = pack_bf16x2(__uint_as_float(o[y + 2 * z]) * inv, __uint_as_float(o[y + 2 * z + 1]) * inv);
+            for (int z = 0; z < 4; ++z) w[z] = pack_bf16x2(__uint_as_float(o[y + 2 * z]), __uint_as_float(o[y + 2 * z + 1]));
             *reinterpret_cast<uint4*>(dst + x + y) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else if (in) {
 #pragma unroll
-          for (int y = 0; y < 32; y += 4)
+          for (int y = 0; y < 16; y += 4)
             *reinterpret_cast<uint4*>(slot + r128 * D + x + y) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
         }
         __syncwarp();
       }
       tc_fence_before();
+      softmax_sync();  // O has been read by all: the next unit's products may come
       if (alone) {
-        if (in && hf == 0 && p.lse) p.lse[lse_at] = lse_of(m, l);
+        if (in && part == 0 && p.lse) p.lse[lse_at] = lse_of(m, l);
       } else {
-        if (in && hf == 0) *reinterpret_cast<float2*>(slot + kM * D + 2 * r128) = make_float2(m, l);
+        if (in && part == 0) *reinterpret_cast<float2*>(slot + kM * D + 2 * r128) = make_float2(m, l);
         __threadfence();
         const int c0 = (int)(((at + 1) * shares - 1) / total), c1 = (int)(((at + nt) * shares - 1) / total);
         softmax_sync();
@@ -492,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
           }
           const float by = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll 1
-          for (int d = hf * (D / 2); d < (hf + 1) * (D / 2); d += 16) {
+          for (int d = part * (D / 4); d < (part + 1) * (D / 4); d += 16) {
             float acc[16] = {};
 #pragma unroll 2
             for (int x = c0; x <= c1; ++x) {
@@ -511,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                   make_uint4(pack_bf16x2(acc[y] * by, acc[y + 1] * by), pack_bf16x2(acc[y + 2] * by, acc[y + 3] * by),
                              pack_bf16x2(acc[y + 4] * by, acc[y + 5] * by), pack_bf16x2(acc[y + 6] * by, acc[y + 7] * by));
           }
-          if (hf == 0 && p.lse) p.lse[lse_at] = lse_of(mx, sum);
+          if (part == 0 && p.lse) p.lse[lse_at] = lse_of(mx, sum);
         }
         __syncwarp();
       }
@@ -552,30 +535,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       if (t0 == t1) break;
       unit_close();
       uint4 raw[kSteps];
-      auto load = [&](int t, uint32_t c) {
-        const uint32_t slot = c % kPageSlots;
-        mbar_wait(&sm.page_full[slot], (c / kPageSlots) & 1, wg, 65);
-        const int left = len - t * kN;  // tokens from the tile's first on
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          const int x = s * kStepTokens + tok, first = __float_as_int(sm.page[slot][x >> 4].x);
-          raw[s] = make_uint4(0, 0, 0, 0);
-          if (first >= 0 && x < left) raw[s] = __ldg(reinterpret_cast<const uint4*>(codes + (long long)first * D));
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.page_empty[slot]);
+      auto load = [&](uint4& r, int s, int left, const float4* page) {
+        const int x = s * kStepTokens + tok, first = __float_as_int(page[x >> 4].x);
+        r = make_uint4(0, 0, 0, 0);
+        if (first >= 0 && x < left) r = __ldg(reinterpret_cast<const uint4*>(codes + (long long)first * D));
       };
-      load(t0, c);
-      for (int t = t0; t < t1; ++t, ++c) {
-        uint4 now[kSteps];
+      auto page_open = [&](uint32_t c) {
+        mbar_wait(&sm.page_full[c % kPageSlots], (c / kPageSlots) & 1, wg, 65);
+        return sm.page[c % kPageSlots];
+      };
+      auto page_close = [&](uint32_t c) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.page_empty[c % kPageSlots]);
+      };
+      const float4* page = page_open(c);
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) now[s] = raw[s];
-        if (t + 1 < t1) load(t + 1, c + 1);
+      for (int s = 0; s < kSteps; ++s) load(raw[s], s, len - t0 * kN, page);
+      page_close(c);
+      for (int t = t0; t < t1; ++t, ++c) {
+        const bool more = t + 1 < t1;
+        if (more) page = page_open(c + 1);
         const uint32_t b = c & 1, to = b * (kN * D * 2);
         mbar_wait(&empty[b], ((c >> 1) & 1) ^ 1, wg, 66);
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-          const uint32_t in[4] = {now[s].x, now[s].y, now[s].z, now[s].w};
+          const uint32_t in[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
           uint32_t h[8];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
@@ -584,10 +568,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
           }
           st_shared_v4(at0 + to + s * (kStepTokens * 128), h[0], h[1], h[2], h[3]);
           st_shared_v4(at1 + to + s * (kStepTokens * 128), h[4], h[5], h[6], h[7]);
+          if (more) load(raw[s], s, len - (t + 1) * kN, page);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[b]);
+        if (more) page_close(c + 1);
       }
     }
   } else if (warp == kMma) {
@@ -632,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         if (elect_one()) {
 #pragma unroll
           for (int x = 0; x < kN / 16; ++x)
-            mma_ts_f16(tmem + kColO, tmem + kColS + b * kN + (x / 4) * kHalf + 8 * (x % 4), dv + x * (16 * 128 >> 4), idesc_o,
+            mma_ts_f16(tmem + kColO, tmem + kColS + b * kN + (x / 2) * kOwn + 8 * (x % 2), dv + x * (16 * 128 >> 4), idesc_o,
                        t > t0 || x > 0);
           tc_commit(&sm.v_empty[b]);
           tc_commit(&sm.o_done);
