@@ -136,19 +136,23 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
+// all softmax warps: barrier 1; the four with the same 32 rows: barriers 2 to 5
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft * 32) : "memory"); }
-__device__ __forceinline__ bool softmax_any(bool x) {
+__device__ __forceinline__ void rows_sync(int rows) { asm volatile("bar.sync %0, 128;" ::"r"(2 + rows) : "memory"); }
+__device__ __forceinline__ bool any_of(int bar, int threads, bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 1, %2, p;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\t"
       "selp.b32 %0, 1, 0, q;\n\t}\n"
       : "=r"(r)
-      : "r"((uint32_t)x), "n"(kSoft * 32)
+      : "r"(bar), "r"(threads), "r"((uint32_t)x)
       : "memory");
   return r != 0;
 }
+__device__ __forceinline__ bool softmax_any(bool x) { return any_of(1, kSoft * 32, x); }
+__device__ __forceinline__ bool rows_any(int rows, bool x) { return any_of(2 + rows, 128, x); }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __grid_constant__ KvAttentionParams p) {
@@ -272,13 +276,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
   if (warp < kSoft) {
     // ------------------------------------------------------------ softmax: four threads per row
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const int part = warp >> 2, r128 = tid & (kM - 1);  // quarter of the columns, row of the unit
+    // quarter of the columns, of the rows, row of the unit
+    const int part = warp >> 2, rows = warp & 3, r128 = tid & (kM - 1);
     struct Row {
       int i, hq;     // token, query head
       bool in;
       float qscale;
     };
-    // q to tensor memory, fp16 by a power of two; the scores of the unit before are done by the second barrier
+    // q to tensor memory, fp16 by a power of two; the scores of the unit before are done
     auto load_q = [&](const UnitInfo& u) {
       Row w;
       const long long r = (long long)u.rt * kM + r128;
@@ -297,9 +302,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         for (int z = 0; z < 4; ++z)
           amax = max3(amax, fabsf(__uint_as_float(y[z] << 16)), fabsf(__uint_as_float(y[z] & 0xffff0000u)));
       }
-      softmax_sync();  // what was in swap has been read
+      rows_sync(rows);  // what was in swap has been read
       sm.swap[part][r128] = amax;
-      softmax_sync();
+      rows_sync(rows);
       const int up = fp16_up(fmaxf(fmaxf(sm.swap[0][r128], sm.swap[1][r128]), fmaxf(sm.swap[2][r128], sm.swap[3][r128])));
       const float mul = exp2i(up);
       w.qscale = exp2i(-up) * p.scale_log2;
@@ -331,8 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       float m = -INFINITY, l = 0.0f;  // the row's reference; the sum of this thread's weights
       for (int t = t0; t < t1; ++t, ++c) {
         const uint32_t sb = c & 1, slot = c % kPageSlots;
-        mbar_wait(&sm.page_full[slot], (c / kPageSlots) & 1, wg, 60);
         mbar_wait(&sm.s_full[sb], (c >> 1) & 1, wg, 61);
+        mbar_wait(&sm.page_full[slot], (c / kPageSlots) & 1, wg, 60);
         tc_fence_after();
         const uint32_t s_at = lanes + kColS + sb * kN + part * kOwn;
         const int limit = seen - t * kN - part * kOwn;  // of its columns, those that this row sees
@@ -356,9 +361,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
           g = fmaxf(g, __uint_as_float(raw[16 * h + 15]));
           mx = fmaxf(mx, fmaf(g, qscale * pg.y, pg.z));
         }
-        if (softmax_any(mx > m + 8.0f)) {
+        if (rows_any(rows, mx > m + 8.0f)) {
           sm.swap[part][r128] = mx;
-          softmax_sync();
+          rows_sync(rows);
           mx = fmaxf(fmaxf(sm.swap[0][r128], sm.swap[1][r128]), fmaxf(sm.swap[2][r128], sm.swap[3][r128]));
           const bool up = mx > m + 8.0f;
           const float f = up ? ex2(m - mx) : 1.0f;
@@ -418,9 +423,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       if (!dead && u->t0 < u->t1) row = load_q(*u);
       mbar_wait(&sm.unit_done, unit & 1, wg, 64);
       tc_fence_after();
-      softmax_sync();  // swap has been read
+      rows_sync(rows);  // swap has been read
       sm.swap[part][r128] = l;
-      softmax_sync();
+      rows_sync(rows);
       l = (sm.swap[0][r128] + sm.swap[1][r128]) + (sm.swap[2][r128] + sm.swap[3][r128]);
       const bool alone = t0 == 0 && t1 == nt;
       const float inv = !alone ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
@@ -450,7 +455,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         __syncwarp();
       }
       tc_fence_before();
-      softmax_sync();  // O has been read by all: the next unit's products may come
       if (alone) {
         if (in && part == 0 && p.lse) p.lse[lse_at] = lse_of(m, l);
       } else {
@@ -563,8 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
           uint32_t h[8];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            h[2 * y] = e4m3x2_to_f16x2((uint16_t)in[y]);
-            h[2 * y + 1] = e4m3x2_to_f16x2((uint16_t)(in[y] >> 16));
+            e4m3x4_to_f16(in[y], h[2 * y], h[2 * y + 1]);
           }
           st_shared_v4(at0 + to + s * (kStepTokens * 128), h[0], h[1], h[2], h[3]);
           st_shared_v4(at1 + to + s * (kStepTokens * 128), h[4], h[5], h[6], h[7]);
