@@ -557,8 +557,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
     }
     k_done = k_end;
   }
-  // after a wait that gave up: copies in flight land before the CTA's memory goes
-  if (warp == kWarps && dead)
+  // after a wait that gave up, the producer's or a consumer's: copies in flight
+  // land before the CTA's memory goes
+  __syncthreads();
+  if (warp == kWarps && *wg.abort_flag)
     for (uint32_t k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
       mbar_drain(&sm.full[k % kStages], (k / kStages) & 1, 100000000ull);
 }

@@ -186,6 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
     fence_barrier_init();
     sm.abort_flag = 0;
   }
+  // whoever goes on after a wait that gave up finds no page here, or an old one
+  if (tid < kPageSlots * kGroups) sm.page[tid / kGroups][tid % kGroups].x = __int_as_float(-1);
   if (warp == kMma) {
     tmem_alloc(&sm.tmem, kTmemCols);
     tmem_relinquish();

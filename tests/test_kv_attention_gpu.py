@@ -233,6 +233,49 @@ def test_cache_past_32_bits(cuda_lib):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("q_lens,sites", [([1, 2, 1], {51, 52}), ([140, 90, 33], set(range(60, 77)))], ids=["few", "many"])
+def test_waits_that_run_out(cuda_lib, q_lens, sites):
+    """With a wait limit of 1 us the kernels end by themselves, either with a right
+    result or with the status that says otherwise, and leave the workspace as the
+    next call needs it.  The first scores of many rows take longer than that; the
+    copies that few rows wait for may not."""
+    bs = cuda_lib
+    kv = [3000, 700, 2100]
+    q, cache, table, cu = build(bs, 23, kv, q_lens, 16, 4, 128, 64)
+    args = (q, cache, i32(table), i32(cu), i32(kv), max(q_lens))
+    bs.clear_device_status()
+    want = bs.kv_attention(*args)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with bs.kernel_options(wait_timeout_us=1):
+            got = bs.kv_attention(*args)
+        torch.cuda.synchronize()
+        st, detail = bs.device_status()
+        if st == bs.BS_OK and max(q_lens) < 10:
+            assert torch.equal(got, want)
+        else:
+            assert st == bs.BS_ERR_TIMEOUT and (detail >> 8) in sites, (st, hex(detail))
+        bs.clear_device_status()
+        assert torch.equal(bs.kv_attention(*args), want)
+        assert bs.device_status()[0] == bs.BS_OK
+
+
+def test_workspace_shared_with_a_gemm(cuda_lib):
+    """A decode GEMM (stream-K) and attention of either kind in turn on one stream."""
+    bs = cuda_lib
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    x, w = (torch.randn(n, 2048, device=DEV, generator=gen).to(torch.bfloat16) for n in (16, 640))
+    (xc, xs, _), (wc, ws, _) = bs.q4_quantize(x), bs.q4_quantize(w)
+    calls = [lambda: bs.gemm_fp4(xc, xs, wc, ws, 2048)]
+    for q_lens in ([1, 1], [77, 40]):
+        q, cache, table, cu = build(bs, 31, [2500, 900], q_lens, 16, 4, 128, 64)
+        calls.append(lambda a=(q, cache, i32(table), i32(cu), i32([2500, 900]), max(q_lens)): bs.kv_attention(*a))
+    want = [f() for f in calls]
+    for order in ([0, 1, 2], [2, 0, 1], [1, 1, 0], [2, 2, 0]):
+        for i in order:
+            assert torch.equal(calls[i](), want[i])
+
+
 def test_empty_calls(cuda_lib):
     bs = cuda_lib
     q, cache, table, cu = build(bs, 37, [50], [2], 4, 2, 64, 16)
