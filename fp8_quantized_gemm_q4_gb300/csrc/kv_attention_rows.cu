@@ -20,8 +20,8 @@
 // What bounds it: the softmax of a tile, whose steps follow one another (S, the
 // maximum, the vote on the reference, the exponentials, the store) and whose
 // warps have 1480 issue slots of about 2900 clocks a tile with the converters.
-// B = 2, 2048 rows x 32 heads over 4000 to 8000 tokens, D = 128: 289 us (773 TFLOP/s);
-// with two threads per row 303 us, with one 2.5 times the MMAs' time.  Also built and
+// B = 2, 2048 rows x 32 heads over 4000 to 8000 tokens, D = 128: 276 us (808 TFLOP/s);
+// before the pieces' layout below 287, with two threads per row 303, with one 2.5 times the MMAs' time.  Also built and
 // measured: two groups of warps on alternate tiles, each with an O of its own and
 // Q in shared memory (303 us: both operands of Q K^T from shared memory take all of
 // its bandwidth), with one O and a reference settled in turn (324 us: P in S's place
@@ -40,7 +40,10 @@ constexpr int kGroups = kN / 16;  // groups of 16 tokens: each lies in one page
 constexpr int kSoft = 16, kMma = kSoft + 8;  // softmax warps, the MMA warp
 constexpr int kThreads = (kMma + 2) * 32;
 constexpr int kOwn = kN / 4;      // columns of S a softmax thread has
-constexpr int kMinTiles = 2;      // least tiles worth a CTA of its own
+// Least tiles worth a CTA of its own: a unit's pieces are joined by one CTA, which
+// takes about 0.7 us a piece (of 64 rows x 4 heads over 6000 tokens: 58 us with 2
+// tiles a CTA, 32 with 4, 30 with 6, 34 with 12; over 2000 tokens 25, 25, 27, 37).
+constexpr int kMinTiles = 4;
 constexpr int kPageSlots = 8;     // tiles whose pages are known ahead
 constexpr int kUnitSlots = 4;     // units known ahead
 constexpr int kCounters = 1024;   // arrival counters at the head of the workspace
@@ -452,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         } else if (in) {
 #pragma unroll
           for (int y = 0; y < 16; y += 4)
-            *reinterpret_cast<uint4*>(slot + r128 * D + x + y) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+            *reinterpret_cast<uint4*>(slot + (x + y) * kM + r128 * 4) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
         }
         __syncwarp();
       }
@@ -481,24 +484,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
           }
           const float by = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll 1
-          for (int d = part * (D / 4); d < (part + 1) * (D / 4); d += 16) {
-            float acc[16] = {};
-#pragma unroll 2
+          for (int d = part * (D / 4); d < (part + 1) * (D / 4); d += 8) {
+            float acc[8] = {};
+#pragma unroll 4
             for (int x = c0; x <= c1; ++x) {
               const float* from = p.work + piece_at<D>(x, c0);
-              float4 v[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y) v[y] = __ldcg(reinterpret_cast<const float4*>(from + r128 * D + d) + y);
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(from + d * kM + r128 * 4));
+              const float4 w = __ldcg(reinterpret_cast<const float4*>(from + (d + 4) * kM + r128 * 4));
               const float f = ex2(__ldcg(from + kM * D + 2 * r128) - ref);
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                acc[4 * y] += f * v[y].x, acc[4 * y + 1] += f * v[y].y, acc[4 * y + 2] += f * v[y].z, acc[4 * y + 3] += f * v[y].w;
+              acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
+              acc[4] += f * w.x, acc[5] += f * w.y, acc[6] += f * w.z, acc[7] += f * w.w;
             }
-#pragma unroll
-            for (int y = 0; y < 16; y += 8)
-              *reinterpret_cast<uint4*>(dst + d + y) =
-                  make_uint4(pack_bf16x2(acc[y] * by, acc[y + 1] * by), pack_bf16x2(acc[y + 2] * by, acc[y + 3] * by),
-                             pack_bf16x2(acc[y + 4] * by, acc[y + 5] * by), pack_bf16x2(acc[y + 6] * by, acc[y + 7] * by));
+            *reinterpret_cast<uint4*>(dst + d) = make_uint4(pack_bf16x2(acc[0] * by, acc[1] * by), pack_bf16x2(acc[2] * by, acc[3] * by),
+                                                            pack_bf16x2(acc[4] * by, acc[5] * by), pack_bf16x2(acc[6] * by, acc[7] * by));
           }
           if (part == 0 && p.lse) p.lse[lse_at] = lse_of(mx, sum);
         }

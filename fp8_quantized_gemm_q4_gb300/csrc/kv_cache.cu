@@ -203,10 +203,13 @@ cudaError_t launch_kv_release(const KvReleaseParams& p, cudaStream_t stream) {
 // ---------------------------------------------------------------------------
 constexpr int kAppendWarps = 4;
 constexpr int kAppendThreads = kAppendWarps * 32;
-// Rows from which a warp takes 16 rows instead of one.  One suits decode steps (64
-// rows, 8 heads: the launch and three dependent reads are all there is); a prompt
-// of 16384 rows on 64-token pages leaves 63 of 64 such warps without work (80 us).
-constexpr int kAppendWideRows = 2048, kWideRows = 16;
+// Rows from which a warp takes 16 rows instead of one, and the runs among them one
+// after the other.  us, one row / 16 rows a warp (8 heads, D = 128, bf16):
+//   prompts on 64-token pages, 16384 rows   80 / 22   1900 rows  14.5 / 8   512 rows  8.7 / 8
+//   single tokens               4000 rows   19 / 44   2048 rows    11 / 29    64 rows  2.2 / 15
+// How the rows fall into pages is known on the device only; calls of thousands of
+// rows hold prompts, calls of hundreds are decode steps.
+constexpr int kAppendWideRows = 2048, kWideRows = 16, kShort = 4;
 
 // log2 of the scale for this amax (>= 0)
 __device__ __forceinline__ int scale_exp(float amax) {
@@ -365,7 +368,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
 // A warp for the runs that begin in 16 rows; the CTA's four warps take four heads
 // of the same rows.
 template <bool kBf16, int D>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_wide_kernel(const __grid_constant__ KvAppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 3) kv_append_wide_kernel(const __grid_constant__ KvAppendParams p) {
   griddep_wait();
   griddep_launch_dependents();
   constexpr int kWords = 5;  // 32 rows each, from first - 1 on: as far as a run can go
@@ -401,8 +404,13 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_wide_kernel(const __
       if (on) n += w == kFullMask ? 32 : __ffs(~w) - 1;
       on &= w == kFullMask;
     }
-    append_run<kBf16, D, kBf16 ? 32 : 16>(p, head / p.Hkv, head % p.Hkv, first - 1 + i, n, mine >> p.page_shift,
-                                          mine & (page - 1), lane);
+    // a short run passes through little code, a page's worth stays in registers
+    if (n <= kShort)
+      append_run<kBf16, D, kShort / (256 / D)>(p, head / p.Hkv, head % p.Hkv, first - 1 + i, n, mine >> p.page_shift,
+                                               mine & (page - 1), lane);
+    else
+      append_run<kBf16, D, kBf16 ? 32 : 16>(p, head / p.Hkv, head % p.Hkv, first - 1 + i, n, mine >> p.page_shift,
+                                            mine & (page - 1), lane);
   }
 }
 
