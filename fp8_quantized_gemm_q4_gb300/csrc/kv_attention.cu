@@ -352,6 +352,16 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
             const uint4 v = g < R ? *reinterpret_cast<const uint4*>(q + 64 * (x >> 1) + 8 * (x & 1)) : make_uint4(0, 0, 0, 0);
             w[4 * x] = v.x, w[4 * x + 1] = v.y, w[4 * x + 2] = v.z, w[4 * x + 3] = v.w;
           }
+          // the next unit's q on its way to L1 meanwhile
+          if (im + 1 < kItems && sm.end[im + 1]) {
+            const int4 ni = sm.item[im + 1], nr = sm.rows[im + 1];
+            const int rn = ni.z + g;
+            if (rn < nr.z * G && c < kQ) {
+              const __nv_bfloat16* qn = static_cast<const __nv_bfloat16*>(p.q) + (nr.x + rn / G) * p.q_tok_stride +
+                                        (ni.y * G + rn % G) * p.q_head_stride + 64 * c;
+              asm volatile("prefetch.global.L1 [%0];" ::"l"(qn));
+            }
+          }
           float amax = 0.0f;
 #pragma unroll
           for (int x = 0; x < 8 * kQ; ++x)
