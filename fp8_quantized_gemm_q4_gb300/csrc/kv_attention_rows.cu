@@ -104,7 +104,7 @@ struct Unit {
   int nt;                    // tiles
   long long at;              // the first one's place in the list
 };
-__device__ __forceinline__ bool takes(int n, int G) { return n > 0 && (long long)n * G > kFewRows; }
+__device__ __forceinline__ bool takes(const KvAttentionParams& p, int n, int G) { return n > 0 && (long long)n * G > p.few_rows; }
 // Tiles that the unit's last row sees (one at least)
 __device__ __forceinline__ int unit_tiles(int n, int len, int G, int rt) {
   const int last = (int)min((long long)n - 1, ((long long)rt * kM + kM - 1) / G);
@@ -123,7 +123,7 @@ __device__ __forceinline__ void next_unit(const KvAttentionParams& p, int G, Uni
     if (++u.h == p.Hkv) {
       u.h = 0;
       while (++u.b < p.B)
-        if (takes(p.cu_q[u.b + 1] - p.cu_q[u.b], G)) break;
+        if (takes(p, p.cu_q[u.b + 1] - p.cu_q[u.b], G)) break;
       if (u.b >= p.B) return;  // the list ends here, and so does the last share
       load_request(p, G, u);
     }
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   auto request_tiles = [&](int b) {  // of one KV head
     const int n = p.cu_q[b + 1] - p.cu_q[b];
-    if (!takes(n, G)) return 0ll;
+    if (!takes(p, n, G)) return 0ll;
     const int len = cached(p, b);
     const int rts = (int)(((long long)n * G + kM - 1) / kM);
     long long x = 0;

@@ -19,7 +19,9 @@ namespace bsk {
 // all lengths (a few kB from L2) and then handles its own rows of the slot
 // map and its own share of the taken pages, so one launch does and nothing
 // waits on another CTA: slots read the table only below `before`, the table is
-// written only from `before` on.
+// written only from `before` on.  Its bytes are nothing (1024 requests and 20000
+// rows: 0.2 MB); the launch and two dependent reads bound it: 4.1 us for 64
+// requests, 5.2 us for 1024.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 
@@ -199,7 +201,10 @@ cudaError_t launch_kv_release(const KvReleaseParams& p, cudaStream_t stream) {
 // the larger of that and the page's scale, and where the scale grows the
 // page's earlier codes are rounded again to it.  Powers of two: a quotient by
 // one is exact, and re-rounding changes only codes that fall among e4m3's
-// subnormals.
+// subnormals.  Every element is read once and stays in registers between the
+// maximum and the codes.  64 tokens of 8 heads: 2.3 us (launch and three dependent
+// reads); 16384 tokens, 100 MB: 21.5 us, 0.69 of HBM (bound by the conversion's
+// instructions, 12 warps an SM with what they keep).
 // ---------------------------------------------------------------------------
 constexpr int kAppendWarps = 4;
 constexpr int kAppendThreads = kAppendWarps * 32;

@@ -163,6 +163,39 @@ def test_nan_where_masked(cuda_lib, q_lens, kv_lens):
     assert torch.equal(a, b) and torch.equal(la, lse)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(16, 2, 128, 64), (24, 8, 64, 16)])
+def test_edges_in_a_large_call(cuda_lib, Hq, Hkv, D, page):
+    """Sharp, flat and far apart scores, NaN where nobody looks, ids outside the pool,
+    rows that see nothing, in a call of thousands of rows."""
+    bs = cuda_lib
+    q_lens, kv_lens = [200, 2, 1, 40, 90], [700, 70, 1, 17, 0]
+    for spread, scale in ((30.0, 0.5), (1e-3, 1e-3), (1.0, None)):
+        q, cache, table, cu = build(bs, 41, kv_lens, q_lens, Hq, Hkv, D, page, spread=spread)
+        check(bs, q, cache, table, cu, kv_lens, page, scale=scale)
+    cache.v_scale.copy_(torch.exp2(torch.randint(-30, 21, cache.v_scale.shape, device=DEV).float()))
+    a, la = check(bs, q, cache, table, cu, kv_lens, page)
+    owned = {i for r in table for i in r if i >= 0}
+    for codes in (cache.k, cache.v):
+        for r, m in zip(table, kv_lens):
+            if m % page:
+                codes[r[m // page], :, m % page:] = 0x7f
+    ghosts = [i for i in range(cache.k.shape[0]) if i not in owned]
+    cache.k[ghosts] = 0xff
+    cache.v[ghosts] = 0x7f
+    cache.k_scale[ghosts] = math.nan
+    cache.v_scale[ghosts] = math.inf
+    lse = torch.empty_like(la)
+    b = bs.kv_attention(q, cache, i32(table), i32(cu), i32(kv_lens), max(q_lens), lse=lse)
+    assert torch.equal(a, b) and torch.equal(la, lse)
+    for bad in (-1, cache.k.shape[0], 2 ** 31 - 1):
+        t = [list(r) for r in table]
+        t[0][1] = bad
+        bs.clear_device_status()
+        bs.kv_attention(q, cache, i32(t), i32(cu), i32(kv_lens), max(q_lens))
+        assert bs.device_status()[0] == bs.BS_ERR_OFFSETS
+    bs.clear_device_status()
+
+
 def test_strides_and_streams(cuda_lib):
     """q and out as slices, [H, T, D] in memory, on a stream of their own."""
     kv, ql = [400, 33, 64], [1, 5, 1]
