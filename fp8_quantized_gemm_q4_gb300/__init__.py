@@ -58,6 +58,8 @@ class GemmArgs(ctypes.Structure):
 
 # bs_kv_append_args and bs_kv_attention_args, packed in native layout: building
 # a ctypes.Structure of as many fields takes three times as long.
+_KV_PLAN_ARGS = struct.Struct("PPiPqiPPiiqPPPP")
+_FP4_MATVEC_ARGS = struct.Struct("PqiPPqqfPPPiq")
 _KV_APPEND_ARGS = struct.Struct("PPiqiiqqqqPPPPPqi4x")
 _KV_ATTENTION_ARGS = struct.Struct("PqqPqqPPPPPqiPqiPPiqiiiifiPN")
 
@@ -155,17 +157,17 @@ def load(path: str | None = None):
         lib.bs_moe_combine.restype = I
         lib.bs_moe_combine.argtypes = [P, I64, P, I64, I64, I, I64, P, P, I64, P]
         lib.bs_kv_plan.restype = I
-        lib.bs_kv_plan.argtypes = [P, P, I, P, I64, I, P, P, I, I, I64, P, P, P, P, P]
+        lib.bs_kv_plan.argtypes = [ctypes.c_char_p, P]   # the packed structs
         lib.bs_kv_release.restype = I
         lib.bs_kv_release.argtypes = [P, P, I, P, I64, I, P, P, I, I, P]
         lib.bs_kv_append.restype = I
-        lib.bs_kv_append.argtypes = [ctypes.c_char_p, P]   # the packed struct
+        lib.bs_kv_append.argtypes = [ctypes.c_char_p, P]
         lib.bs_kv_attention_workspace_bytes.restype = SZ
         lib.bs_kv_attention_workspace_bytes.argtypes = [ctypes.c_char_p]
         lib.bs_kv_attention.restype = I
         lib.bs_kv_attention.argtypes = [ctypes.c_char_p, P]
         lib.bs_fp4_matvec.restype = I
-        lib.bs_fp4_matvec.argtypes = [P, I64, I, P, P, I64, I64, F, P, P, P, I, I64, P]
+        lib.bs_fp4_matvec.argtypes = [ctypes.c_char_p, P]
         lib.bs_get_device_status.restype = I
         lib.bs_get_device_status.argtypes = [ctypes.POINTER(I)]
         lib.bs_clear_device_status.restype = I
@@ -611,10 +613,10 @@ def kv_plan(seq_lens, new_lens, block_table, free_pages, n_free, page_size: int,
     ld, width = _check_table("kv_plan", block_table, B)
     if cu.numel() < B + 1 or kv.numel() < B or slots.numel() < total_new:
         raise ValueError("kv_plan: outputs are [B + 1], [B], [total_new] and [1]")
-    _check((_lib or load()).bs_kv_plan(
-        seq_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(), ld, width, free_pages.data_ptr(),
-        n_free.data_ptr(), free_pages.numel(), page_size, total_new, cu.data_ptr(), kv.data_ptr(), slots.data_ptr(),
-        left.data_ptr(), _stream(stream)))
+    a = _KV_PLAN_ARGS.pack(seq_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(), ld, width,
+                           free_pages.data_ptr(), n_free.data_ptr(), free_pages.numel(), page_size, total_new,
+                           cu.data_ptr(), kv.data_ptr(), slots.data_ptr(), left.data_ptr())
+    _check((_lib or load()).bs_kv_plan(a, _stream(stream)))
     return out
 
 
@@ -728,10 +730,10 @@ def matvec_fp4(x, codes, sf, out_dtype=torch.bfloat16, alpha: float = 1.0, bias=
         raise ValueError(f"matvec_fp4: out is [{M}, {N}] with contiguous rows")
     if M <= 1:
         ldx, ldo = K, N   # the stride of a single row means nothing
-    _check((_lib or load()).bs_fp4_matvec(
-        x.data_ptr(), ldx, M, codes.data_ptr(), sf.data_ptr(), N, K, alpha,
-        None if tensor_scale is None else tensor_scale.data_ptr(), None if bias is None else bias.data_ptr(),
-        out.data_ptr(), _dt(out), ldo, _stream(stream)))
+    a = _FP4_MATVEC_ARGS.pack(x.data_ptr(), ldx, M, codes.data_ptr(), sf.data_ptr(), N, K, alpha,
+                              0 if tensor_scale is None else tensor_scale.data_ptr(),
+                              0 if bias is None else bias.data_ptr(), out.data_ptr(), _dt(out), ldo)
+    _check((_lib or load()).bs_fp4_matvec(a, _stream(stream)))
     return out
 
 

@@ -1060,10 +1060,10 @@ static int kv_page_shift(int page_size) {
 
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-bs_status bs_kv_plan(const int32_t* seq_lens, const int32_t* new_lens, int B, int32_t* block_table, int64_t ld_table,
-                     int max_pages, const int32_t* free_pages, const int32_t* n_free, int free_capacity,
-                     int page_size, int64_t T, int32_t* cu_new, int32_t* kv_lens, int32_t* slots,
-                     int32_t* n_free_out, bs_stream_t stream) {
+bs_status bs_kv_plan(const bs_kv_plan_args* a, bs_stream_t stream) {
+  if (!a) return fail(BS_ERR_INVALID, "kv_plan: null arguments");
+  const auto& [seq_lens, new_lens, B, block_table, ld_table, max_pages, free_pages, n_free, free_capacity, page_size, T,
+               cu_new, kv_lens, slots, n_free_out] = *a;
   if (B < 0 || T < 0 || T > INT32_MAX || max_pages < 0 || free_capacity < 0)
     return fail(BS_ERR_INVALID, "kv_plan: B=%d T=%lld max_pages=%d free_capacity=%d", B, (long long)T, max_pages,
                 free_capacity);
@@ -1280,9 +1280,9 @@ bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
   return BS_OK;
 }
 
-bs_status bs_fp4_matvec(const void* x, int64_t ldx, int M, const uint8_t* codes, const uint8_t* sf, int64_t N, int64_t K,
-                        float alpha, const float* tensor_scale, const void* bias, void* out, int out_dtype, int64_t ldo,
-                        bs_stream_t stream) {
+bs_status bs_fp4_matvec(const bs_fp4_matvec_args* a, bs_stream_t stream) {
+  if (!a) return fail(BS_ERR_INVALID, "fp4_matvec: null arguments");
+  const auto& [x, ldx, M, codes, sf, N, K, alpha, tensor_scale, bias, out, out_dtype, ldo] = *a;
   if (M < 0 || N < 0 || K <= 0 || N > INT32_MAX - 255 || K > INT32_MAX - 255)
     return fail(BS_ERR_INVALID, "fp4_matvec: M=%d N=%lld K=%lld", M, (long long)N, (long long)K);
   if (out_dtype != BS_DTYPE_F32 && out_dtype != BS_DTYPE_BF16)

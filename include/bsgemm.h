@@ -559,10 +559,18 @@ bs_status bs_moe_combine(const float *rows, int64_t ld_rows, const int32_t *pair
  * their number, and their table entries become -1.  The caller then gives the
  * request length 0.
  * ------------------------------------------------------------------------- */
-bs_status bs_kv_plan(const int32_t *seq_lens, const int32_t *new_lens, int B, int32_t *block_table, int64_t ld_table,
-                     int max_pages, const int32_t *free_pages, const int32_t *n_free, int free_capacity,
-                     int page_size, int64_t T, int32_t *cu_new, int32_t *kv_lens, int32_t *slots,
-                     int32_t *n_free_out, bs_stream_t stream);
+typedef struct {
+    const int32_t *seq_lens, *new_lens;
+    int B;
+    int32_t *block_table;
+    int64_t ld_table;
+    int max_pages;
+    const int32_t *free_pages, *n_free;
+    int free_capacity, page_size;
+    int64_t T;
+    int32_t *cu_new, *kv_lens, *slots, *n_free_out;
+} bs_kv_plan_args;
+bs_status bs_kv_plan(const bs_kv_plan_args *args, bs_stream_t stream);
 bs_status bs_kv_release(const int32_t *lens, const int32_t *done, int B, int32_t *block_table, int64_t ld_table,
                         int max_pages, int32_t *free_pages, int32_t *n_free, int free_capacity, int page_size,
                         bs_stream_t stream);
@@ -665,9 +673,20 @@ bs_status bs_kv_attention(const bs_kv_attention_args *args, bs_stream_t stream);
  *   tensor_scale device fp32 scalar or NULL (= 1); bias bf16 [N] or NULL
  *   out     fp32 or bf16 [M, ldo], aligned to its elements, ldo >= N
  * ------------------------------------------------------------------------- */
-bs_status bs_fp4_matvec(const void *x, int64_t ldx, int M, const uint8_t *codes, const uint8_t *sf, int64_t N,
-                        int64_t K, float alpha, const float *tensor_scale, const void *bias, void *out,
-                        int out_dtype, int64_t ldo, bs_stream_t stream);
+typedef struct {
+    const void *x;
+    int64_t ldx;
+    int M;
+    const uint8_t *codes, *sf;
+    int64_t N, K;
+    float alpha;
+    const float *tensor_scale;
+    const void *bias;
+    void *out;
+    int out_dtype;           /* bs_dtype */
+    int64_t ldo;
+} bs_fp4_matvec_args;
+bs_status bs_fp4_matvec(const bs_fp4_matvec_args *args, bs_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Status.

@@ -23,13 +23,15 @@ F = 1 << 20          # never dereferenced: validation fails first
 
 def test_plan_refusals(bs):
     f = bs.load().bs_kv_plan
-    good = [F, F + 64, 4, F + 128, 8, 8, F, F + 256, 32, 64, 10, F, F + 512, F, F + 1024, None]
+    good = [F, F + 64, 4, F + 128, 8, 8, F, F + 256, 32, 64, 10, F, F + 512, F, F + 1024]
 
     def call(**kw):
         a = list(good)
         for i, v in kw.items():
-            a[int(i[1:])] = v
-        return f(*a)
+            a[int(i[1:])] = v or 0
+        return f(bs._KV_PLAN_ARGS.pack(*a), None)
+
+    assert f(None, None) == bs.BS_ERR_INVALID
 
     assert call(a2=-1) == bs.BS_ERR_INVALID
     assert call(a2=8193) == bs.BS_ERR_UNSUPPORTED
@@ -116,13 +118,15 @@ def test_attention_refusals(bs):
 
 def test_matvec_refusals(bs):
     f = bs.load().bs_fp4_matvec
-    good = [F, 256, 4, F, F, 100, 256, 1.0, None, None, F, 1, 100, None]
+    good = [F, 256, 4, F, F, 100, 256, 1.0, 0, 0, F, 1, 100]
 
     def call(**kw):
         a = list(good)
         for i, v in kw.items():
-            a[int(i[1:])] = v
-        return f(*a)
+            a[int(i[1:])] = v or 0
+        return f(bs._FP4_MATVEC_ARGS.pack(*a), None)
+
+    assert f(None, None) == bs.BS_ERR_INVALID
 
     assert call(a2=17) == bs.BS_ERR_UNSUPPORTED
     assert call(a2=-1) == bs.BS_ERR_INVALID
