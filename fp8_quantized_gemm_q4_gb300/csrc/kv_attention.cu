@@ -90,7 +90,7 @@ __device__ __forceinline__ void softmax_step(float (&u)[4], float inv_sv, float 
 // ---------------------------------------------------------------------------
 // Requests with at most few_rows rows per KV head (decode, drafts): bound by the
 // cache stream.  Work is a list of (request, head, 8 rows) units of 64-token
-// tiles, cut into equal contiguous shares, whatever the lengths.  Three CTAs an
+// tiles, cut into contiguous shares of equal cost, whatever the lengths.  Three CTAs an
 // SM take one each: a producer warp keeps 64 KB of codes in flight with TMA copies
 // page by page, four consumer warps take 16 tokens of a tile each, and while one
 // CTA joins the warps' results of a unit, the other two stream (one CTA with 12
@@ -99,15 +99,18 @@ __device__ __forceinline__ void softmax_step(float (&u)[4], float inv_sv, float 
 // S^T = K Q^T, O^T = V^T P^T; a group of 4 or 8 query heads fills N, where it would
 // leave half of M = 16 empty.  More than 8 rows are units of their own beside the
 // first, whose tiles they find in L2.
-// 64 requests of 500 to 16000 tokens, 32 heads over 8, D = 128 (604 MB): 107 us, 0.82
-// of HBM; the rest is CTAs that end at different times.  63 drafted tokens of 16
-// requests, 16 heads, D = 64, 16-token pages (60 MB): 24.6 us, bound by what a unit costs
-// beside its tiles (q, the join of the warps, its piece); one token over 1000: 9.3 us,
-// a chain of dependent reads.
+// 64 requests of 500 to 16000 tokens, 32 heads over 8, D = 128 (604 MB): 105 us, 0.85
+// of HBM.  63 drafted tokens of 16 requests, 16 heads, D = 64, 16-token pages (60 MB):
+// 23 us, bound by what a unit costs beside its tiles (q, the join of the warps, its
+// piece); one token over 1000: 10 us, a chain of dependent reads.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 64;          // cached tokens per stage
 constexpr int kItems = 32;         // units listed at a time
-constexpr int kMinTiles = 2;       // least tiles worth a CTA of its own
+constexpr int kMinTiles = 2;       // least cost worth a CTA of its own
+// What a unit costs beside its tiles (q, the join of the warps, a piece), in tiles.
+// us with 0 / 2 / 4 / 10: 64 decode requests 107.6 / 106.1 / 105.5 / 106, drafts over 16
+// heads 24.8 / 23.3 / 22.9 / 23.9, 64 requests of 30 to 14000 tokens 20.6 / 17.4 / 16.6 / 16.7
+constexpr int kUnitTiles = 4;
 constexpr int kCounters = 1024;    // arrival counters at the head of the workspace
 constexpr int kFewWarps = 4;       // consumers; one more warp produces
 constexpr int kFewThreads = kFewWarps * 32 + 32;
@@ -130,6 +133,7 @@ struct FewSmem {
   uint64_t full[kStages], empty[kStages];
   int2 scan[kFewThreads / 32];
   long long first_unit;      // of this share, counted over requests with tiles
+  long long bound[2];        // its first tile in the list, the next share's
   int abort_flag, last;
 };
 
@@ -139,6 +143,11 @@ struct FewSmem {
 // the call's, so that its result does not depend on the bound that the call gives.
 __device__ __forceinline__ int few_tiles(const KvAttentionParams& p, int n, int len, int G) {
   return n <= 0 || (long long)n * G > p.few_rows ? 0 : max(1, (len + kTile - 1) / kTile);
+}
+
+// a / b for a >= 0 and b > 0: 64-bit division only where it takes one
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
 
 // A piece of a unit that is cut between CTAs: partial sums [8][D], then (m, l) of
@@ -201,30 +210,37 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
   }
   if (lane == 31) sm.scan[warp] = incl;
   __syncthreads();
-  int2 before = make_int2(incl.x - mine.x, incl.y - mine.y);
-  int sum = 0;
+  int2 before = make_int2(incl.x - mine.x, incl.y - mine.y), sum = make_int2(0, 0);
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     const int2 v = sm.scan[w];
     if (w < warp) before.x += v.x, before.y += v.y;
-    sum += v.x;
+    sum.x += v.x, sum.y += v.y;
   }
-  const long long total = (long long)sum * p.Hkv;
-  const int shares = (int)min((long long)gridDim.x, (total + kMinTiles - 1) / kMinTiles);
+  // Shares are equal in cost: a unit costs kUnitTiles beside its tiles.  Tile i of
+  // the unit that is the u-th of the list and has x tiles before it stands at
+  // x + u kUnitTiles + kUnitTiles + i on the axis of costs.
+  const long long total = (long long)sum.x * p.Hkv, cost = total + (long long)sum.y * p.Hkv * kUnitTiles;
+  const int shares = (int)min((long long)gridDim.x, (cost + kMinTiles - 1) / kMinTiles);
   if ((int)blockIdx.x >= shares) return;
-  const long long t_first = total * blockIdx.x / shares;
-  const int tiles = (int)(total * (blockIdx.x + 1) / shares - t_first);  // of this share
   const long long own_at = (long long)before.x * p.Hkv;
-  if (t_first >= own_at && t_first < own_at + (long long)mine.x * p.Hkv) {
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e) {  // the share's first tile and the next one's
+    const long long c = quotient(cost * (blockIdx.x + e), shares);
     long long at = own_at, units = (long long)before.y * p.Hkv;
+    const long long from = at + units * kUnitTiles;
+    if (c < from || c >= from + (long long)mine.x * p.Hkv + (long long)mine.y * p.Hkv * kUnitTiles) continue;
     for (int b = b0; b < b1; ++b) {
       int n = n_own, len = len_own;
       if (per > 1) n = p.cu_q[b + 1] - p.cu_q[b], len = cached(p, b);
       const int nt = few_tiles(p, n, len, G);
       if (!nt) continue;
       const int u = p.Hkv * ((n * G + 7) / 8);
-      if (t_first < at + (long long)nt * u) {
-        sm.first_unit = units + (int)((t_first - at) / nt);
+      const long long off = c - (at + units * kUnitTiles);
+      if (off < (long long)(nt + kUnitTiles) * u) {
+        const long long i = quotient(off, nt + kUnitTiles);
+        if (e == 0) sm.first_unit = units + i;
+        sm.bound[e] = at + i * nt + max(0ll, off - i * (nt + kUnitTiles) - kUnitTiles);
         break;
       }
       at += (long long)nt * u;
@@ -232,6 +248,9 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
     }
   }
   __syncthreads();
+  const long long t_first = sm.bound[0];
+  // of this share; none if it is all beside the tiles
+  const int tiles = (int)(((int)blockIdx.x + 1 < shares ? sm.bound[1] : total) - t_first);
 
   bool dead = false;  // producer: a wait gave up, nothing more is copied
   uint32_t issued = 0;
@@ -532,8 +551,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
         }
         __threadfence();
         // the shares that hold the unit's first and last tile
-        const long long first = t_first + begin;
-        const int c0 = (int)(((first + 1) * shares - 1) / total), c1 = (int)(((first + nt) * shares - 1) / total);
+        const long long first = t_first + begin + (base + im + 1) * kUnitTiles;  // on the axis of costs
+        const int c0 = (int)quotient((first + 1) * shares - 1, cost), c1 = (int)quotient((first + nt) * shares - 1, cost);
         consumer_sync();
         if (tid == 0) {
           const int old = atomicAdd(p.counters + c0, 1);
