@@ -655,7 +655,20 @@ def kv_append(k, v, slots, cache, stream=None):
     _check((_lib or load()).bs_kv_append(a, _stream(stream)))
 
 
-_kv_workspace_bytes: dict = {}   # (device, D, only few rows): they do not depend on anything else
+_kv_workspace_sizes: dict = {}   # (device, D) -> bytes
+
+
+def _kv_workspace_bytes(lib, dev: int, D: int) -> int:
+    """Workspace of any kv_attention call of heads of D on this device: the
+    library's answer for a long call, no bound known, which is its largest.  0,
+    which is not kept, where the library has no answer (and refuses the call)."""
+    nbytes = _kv_workspace_sizes.get((dev, D))
+    if nbytes is None:
+        a = _KV_ATTENTION_ARGS.pack(*(0,) * 19, 1 << 20, 1, 1, D, *(0,) * 5)   # T, Hq, Hkv, D
+        nbytes = int(lib.bs_kv_attention_workspace_bytes(a))
+        if nbytes:
+            _kv_workspace_sizes[(dev, D)] = nbytes
+    return nbytes
 
 
 def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_scale: float | None = None, out=None,
@@ -695,10 +708,7 @@ def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_s
             opts.get("wait_timeout_us", 0) if opts else 0)
     lib = _lib or load()
     dev = q.get_device()
-    key = (dev, D, (max_q_len or T) * Hq <= (128 if T * Hq <= 2048 else 16) * Hkv)
-    nbytes = _kv_workspace_bytes.get(key)
-    if nbytes is None:
-        nbytes = _kv_workspace_bytes[key] = int(lib.bs_kv_attention_workspace_bytes(_KV_ATTENTION_ARGS.pack(*args, 0, 0)))
+    nbytes = _kv_workspace_bytes(lib, dev, D)
     ws = _workspaces.get((dev, handle))
     if ws is None or ws.numel() < nbytes:
         ws = _workspace_of(q.device, handle, nbytes)
