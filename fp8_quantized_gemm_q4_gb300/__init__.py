@@ -345,10 +345,14 @@ def gemm_fp4(a, sfa, b, sfb, K: int, out_dtype=torch.bfloat16, alpha: float = 1.
     return out
 
 
-# Workspaces of the FP8 stream-K schedule, one per (device, stream): calls on
-# one stream run in order, so they may share it; the library leaves it zeroed
-# where the next call reads it.
+# Workspaces of calls that bring none of their own (stream-K GEMMs, attention), one
+# per (device, stream): calls on one stream run in order, so they may share it;
+# the library leaves it zeroed where the next call reads it.  A CUDA graph keeps
+# the address that it was captured with, so a buffer that a larger one replaces
+# stays; sizes at least double, which bounds what all of them take by twice the last.
+# Graphs captured on one stream share its buffer and must not overlap.
 _workspaces: dict = {}
+_outgrown: list = []
 
 
 def _workspace(device, stream, nbytes: int):
@@ -363,9 +367,16 @@ def _workspace_of(device, handle: int, nbytes: int):
         s = torch.cuda.current_stream(device)
         if s.cuda_stream != handle:
             s = torch.cuda.ExternalStream(handle, device=device)
+        size = max(nbytes, 256, 2 * ws.numel() if ws is not None else 0)
         with torch.cuda.stream(s):
-            ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-        _workspaces[key] = ws
+            new = torch.zeros(size, dtype=torch.uint8, device=device)
+            if torch.cuda.is_current_stream_capturing():
+                # the graph's own memory, zeroed when the graph runs and not
+                # before: for this call alone
+                return new
+        if ws is not None:
+            _outgrown.append(ws)
+        _workspaces[key] = ws = new
     return ws
 
 

@@ -53,3 +53,61 @@ def test_one_size_serves_every_call(cuda_lib, D):
     for T, Hq, Hkv, most in ((1, 8, 8, 1), (64, 32, 8, 1), (4096, 32, 8, 4096), (5000, 64, 1, 3), (300, 8, 1, 300)):
         a = bs._KV_ATTENTION_ARGS.pack(*(0,) * 19, T, Hq, Hkv, D, most, *(0,) * 4)
         assert 0 < int(lib.bs_kv_attention_workspace_bytes(a)) <= kept
+
+
+def graph_of(call, stream):
+    g = torch.cuda.CUDAGraph()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=stream):
+        out = call()
+    return g, out
+
+
+def test_replay_after_the_buffer_grew(cuda_lib, monkeypatch):
+    """Captured with the stream's buffer, which a later call then replaces by a
+    larger one; memory allocated since is filled with junk before the replays."""
+    bs = cuda_lib
+    monkeypatch.setattr(bs, "_workspaces", {})
+    side = torch.cuda.Stream()
+    small, large = case(bs, [5000, 900], [1, 1], D=64), case(bs, [3000, 700], [150, 90])
+    want = bs.kv_attention(*small).clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        bs.kv_attention(*small)
+    g, out = graph_of(lambda: bs.kv_attention(*small), side)
+    before = bs._workspaces[(out.get_device(), side.cuda_stream)]
+    with torch.cuda.stream(side):
+        wide = bs.kv_attention(*large)
+    torch.cuda.synchronize()
+    assert bs._workspaces[(out.get_device(), side.cuda_stream)] is not before
+    del before
+    junk = [torch.full((1 << 20,), 0x5a, dtype=torch.uint8, device=DEV) for _ in range(64)]
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert all(bool((x == 0x5a).all()) for x in junk)
+    assert torch.equal(wide, bs.kv_attention(*large))
+
+
+def test_capture_without_a_first_call(cuda_lib, monkeypatch):
+    """Two graphs captured on a stream that has no buffer yet, the second replayed
+    first, with calls on the stream between them."""
+    bs = cuda_lib
+    monkeypatch.setattr(bs, "_workspaces", {})
+    side = torch.cuda.Stream()
+    few, many = case(bs, [5000, 900], [1, 1]), case(bs, [3000, 700], [150, 90])
+    want = [bs.kv_attention(*few).clone(), bs.kv_attention(*many).clone()]
+    torch.cuda.synchronize()
+    g0, out0 = graph_of(lambda: [bs.kv_attention(*few), bs.kv_attention(*few)], side)
+    g1, out1 = graph_of(lambda: bs.kv_attention(*many), side)
+    with torch.cuda.stream(side):
+        eager = bs.kv_attention(*few)
+    torch.cuda.synchronize()
+    assert torch.equal(eager, want[0])
+    for g in (g1, g0, g0, g1, g0):
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want[0]) for o in out0) or g is g1
+        assert torch.equal(out1, want[1])
