@@ -23,7 +23,7 @@ from ._build import LIB as _LIB_PATH
 
 __all__ = [
     "load", "sf_bytes", "sf_offset", "q4_quantize", "tensor_amax", "q4_quantize_two_level", "fp4_gather_rows", "fp8_gather_rows", "q8_quantize", "gemm_fp4", "gemm_fp8", "gemm_fp8_multi", "gemm_fp4_multi",
-    "grouped_gemm_fp4", "grouped_gemm_fp4_swiglu_q4", "grouped_gemm_fp8", "moe_router_topk", "moe_dispatch", "moe_finalize", "moe_combine", "moe_rows_bound", "kv_plan", "kv_release", "kv_append", "kv_attention", "matvec_fp4", "KVCache", "device_status",
+    "grouped_gemm_fp4", "grouped_gemm_fp4_swiglu_q4", "grouped_gemm_fp8", "moe_router_topk", "moe_dispatch", "moe_finalize", "moe_combine", "moe_rows_bound", "kv_plan", "kv_release", "kv_append", "kv_attention", "kv_attention_workspace", "matvec_fp4", "KVCache", "device_status",
     "clear_device_status", "BSError", "EPI_STORE", "EPI_SWIGLU", "EPI_COMBINE", "EPI_ROWS", "kernel_options",
     "current_kernel_options", "FP4_ONE_CTA", "FP4_PAIR",
 ]
@@ -682,11 +682,23 @@ def _kv_workspace_bytes(lib, dev: int, D: int) -> int:
     return nbytes
 
 
+def kv_attention_workspace(D: int, device=None):
+    """A zeroed workspace for kv_attention calls with heads of D that run one
+    after the other, whatever their lengths."""
+    device = torch.device("cuda" if device is None else device)
+    with torch.cuda.device(device):
+        nbytes = _kv_workspace_bytes(_lib or load(), torch.cuda.current_device(), D)
+    if not nbytes:
+        raise ValueError(f"kv_attention_workspace: no kernel for heads of {D}")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
 def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_scale: float | None = None, out=None,
-                 lse=None, stream=None):
+                 lse=None, workspace=None, stream=None):
     """Causal attention of new tokens q bf16 [T, Hq, D] over the 8-bit cache
     (their own keys and values appended first).  ``lse`` (fp32 [T, Hq], natural
-    log) is filled if given.  Returns out bf16 [T, Hq, D]."""
+    log) is filled if given.  ``workspace`` from kv_attention_workspace, or the
+    stream's own if None.  Returns out bf16 [T, Hq, D]."""
     kc, vc, ks, vs, (pages, Hkv, page, D) = _check_kv_cache(cache)
     shape = q.shape
     if out is None:
@@ -719,10 +731,15 @@ def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_s
             opts.get("wait_timeout_us", 0) if opts else 0)
     lib = _lib or load()
     dev = q.get_device()
-    nbytes = _kv_workspace_bytes(lib, dev, D)
-    ws = _workspaces.get((dev, handle))
-    if ws is None or ws.numel() < nbytes:
-        ws = _workspace_of(q.device, handle, nbytes)
+    if workspace is not None:
+        if workspace.dtype is not _U8 or not workspace.is_contiguous():
+            raise TypeError("kv_attention: workspace is a contiguous uint8 tensor of kv_attention_workspace")
+        ws, nbytes = workspace, workspace.numel()
+    else:
+        nbytes = _kv_workspace_bytes(lib, dev, D)
+        ws = _workspaces.get((dev, handle))
+        if ws is None or ws.numel() < nbytes:
+            ws = _workspace_of(q.device, handle, nbytes)
     _check(lib.bs_kv_attention(_KV_ATTENTION_ARGS.pack(*args, ws.data_ptr(), nbytes), handle))
     return out
 

@@ -15,7 +15,10 @@ token, a few drafted ones, or none):
 
 bs_kv_release gives the pages of finished requests back.  Lengths, tables and
 the free list stay on the device and nothing synchronises the host, so a step of
-fixed shape can be captured in a CUDA graph and replayed.
+fixed shape can be captured in a CUDA graph and replayed, between steps of any
+other shape: the attention's scratch belongs to the layer.  (A step of 17 to 32
+tokens also uses the stream's workspace of bs_gemm: run one such step on the
+capture stream first, or each replay zeroes one of its own.)
 
 The kernels are the library's; this module holds the buffers and calls them in
 order.  No rotation or normalisation is applied to q and k.
@@ -24,7 +27,8 @@ from __future__ import annotations
 
 import torch
 
-from . import KVCache, gemm_fp4, kv_append, kv_attention, kv_plan, kv_release, matvec_fp4, q4_quantize
+from . import (KVCache, gemm_fp4, kv_append, kv_attention, kv_attention_workspace, kv_plan, kv_release, matvec_fp4,
+               q4_quantize)
 
 MATVEC_ROWS = 16   # the most rows that bs_fp4_matvec takes
 
@@ -60,6 +64,7 @@ class DecodeAttention:
         self.free = torch.arange(num_pages, dtype=torch.int32, device=dev)
         self.n_free = torch.full((1,), num_pages, dtype=torch.int32, device=dev)
         self.lens = torch.zeros(requests, dtype=torch.int32, device=dev)
+        self.workspace = kv_attention_workspace(D, dev)
 
     def step(self, x, new_lens, max_new: int):
         """x bf16 [T, hidden], the new tokens of request 0, then 1, ..;
@@ -71,7 +76,8 @@ class DecodeAttention:
         qkv = fp4_linear(x, *self.w_qkv)
         q, k, v = qkv.split([q_rows, kv_rows, kv_rows], 1)
         kv_append(k.view(T, self.Hkv, self.D), v.view(T, self.Hkv, self.D), slots, self.cache)
-        att = kv_attention(q.view(T, self.Hq, self.D), self.cache, self.table, cu, kv_lens, max_new)
+        att = kv_attention(q.view(T, self.Hq, self.D), self.cache, self.table, cu, kv_lens, max_new,
+                           workspace=self.workspace)
         self.n_free.copy_(left)
         torch.maximum(self.lens, kv_lens, out=self.lens)
         return fp4_linear(att.view(T, q_rows), *self.w_out)
