@@ -194,13 +194,14 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
   int row0_own = 0, n_own = 0, len_own = 0;  // of the last of them: all there is while B <= threads
   int2 mine = make_int2(0, 0);
   for (int b = b0; b < b1; ++b) {
-    row0_own = p.cu_q[b];
-    n_own = p.cu_q[b + 1] - row0_own;
+    const Rows own = rows_of(p, b);
+    row0_own = own.row0, n_own = own.n;
     len_own = cached(p, b);
     const int nt = few_tiles(p, n_own, len_own, G), rt = nt ? (n_own * G + 7) / 8 : 0;
     mine.x += nt * rt;
     mine.y += rt;
     if ((long long)n_own * G > p.most_rows) record_status(p.status, kStatusOffsets, 53);
+    if (own.bad) record_status(p.status, kStatusOffsets, 54);
   }
   int2 incl = mine;
 #pragma unroll
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
     if (c < from || c >= from + (long long)mine.x * p.Hkv + (long long)mine.y * p.Hkv * kUnitTiles) continue;
     for (int b = b0; b < b1; ++b) {
       int n = n_own, len = len_own;
-      if (per > 1) n = p.cu_q[b + 1] - p.cu_q[b], len = cached(p, b);
+      if (per > 1) n = rows_of(p, b).n, len = cached(p, b);
       const int nt = few_tiles(p, n, len, G);
       if (!nt) continue;
       const int u = p.Hkv * ((n * G + 7) / 8);
@@ -266,7 +267,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
       long long at = own_at, units = (long long)before.y * p.Hkv;
       for (int b = b0; b < b1 && units < base + kItems && at < t_first + tiles; ++b) {
         int row0 = row0_own, n = n_own, len = len_own;
-        if (per > 1) row0 = p.cu_q[b], n = p.cu_q[b + 1] - row0, len = cached(p, b);
+        if (per > 1) {
+          const Rows r = rows_of(p, b);
+          row0 = r.row0, n = r.n, len = cached(p, b);
+        }
         const int nt = few_tiles(p, n, len, G);
         if (!nt) continue;
         const int rt = (n * G + 7) / 8, u = p.Hkv * rt;

@@ -26,6 +26,18 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
+// A request's rows: the first, how many, and how many of them the call has (row < T).
+// Offsets that do not ascend from 0 give none, and work never goes past T.
+struct Rows {
+  int row0, n, in;
+  bool bad;  // offsets that break the contract
+};
+__device__ __forceinline__ Rows rows_of(const KvAttentionParams& p, int b) {
+  const int r0 = p.cu_q[b], r1 = p.cu_q[b + 1];
+  const int n = r0 < 0 || r1 <= r0 ? 0 : r1 - r0;
+  return {r0, n, n ? max(0, min(n, p.T - r0)) : 0, r0 < 0 || r1 < r0 || r1 > p.T};
+}
+
 // Cached tokens of a request, as far as its table row can name them.
 __device__ __forceinline__ int cached(const KvAttentionParams& p, int b) {
   return min(max(p.kv_lens[b], 0), p.max_pages << p.page_shift);

@@ -104,17 +104,21 @@ struct Unit {
   int nt;                    // tiles
   long long at;              // the first one's place in the list
 };
-__device__ __forceinline__ bool takes(const KvAttentionParams& p, int n, int G) { return n > 0 && (long long)n * G > p.few_rows; }
+__device__ __forceinline__ bool takes(const KvAttentionParams& p, const Rows& r, int G) {
+  return r.in > 0 && (long long)r.n * G > p.few_rows;
+}
+__device__ __forceinline__ int row_tiles(const Rows& r, int G) { return (int)(((long long)r.in * G + kM - 1) / kM); }
 // Tiles that the unit's last row sees (one at least)
 __device__ __forceinline__ int unit_tiles(int n, int len, int G, int rt) {
   const int last = (int)min((long long)n - 1, ((long long)rt * kM + kM - 1) / G);
   return max(1, (len - n + last + 1 + kN - 1) / kN);
 }
 __device__ __forceinline__ void load_request(const KvAttentionParams& p, int G, Unit& u) {
-  u.row0 = p.cu_q[u.b];
-  u.n = p.cu_q[u.b + 1] - u.row0;
+  const Rows r = rows_of(p, u.b);
+  u.row0 = r.row0;
+  u.n = r.n;
   u.len = cached(p, u.b);
-  u.rts = (int)(((long long)u.n * G + kM - 1) / kM);
+  u.rts = row_tiles(r, G);
 }
 __device__ __forceinline__ void next_unit(const KvAttentionParams& p, int G, Unit& u) {
   u.at += u.nt;
@@ -123,7 +127,7 @@ __device__ __forceinline__ void next_unit(const KvAttentionParams& p, int G, Uni
     if (++u.h == p.Hkv) {
       u.h = 0;
       while (++u.b < p.B)
-        if (takes(p, p.cu_q[u.b + 1] - p.cu_q[u.b], G)) break;
+        if (takes(p, rows_of(p, u.b), G)) break;
       if (u.b >= p.B) return;  // the list ends here, and so does the last share
       load_request(p, G, u);
     }
@@ -204,18 +208,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   auto request_tiles = [&](int b) {  // of one KV head
-    const int n = p.cu_q[b + 1] - p.cu_q[b];
-    if (!takes(p, n, G)) return 0ll;
-    const int len = cached(p, b);
-    const int rts = (int)(((long long)n * G + kM - 1) / kM);
+    const Rows r = rows_of(p, b);
+    if (!takes(p, r, G)) return 0ll;
+    const int len = cached(p, b), rts = row_tiles(r, G);
     long long x = 0;
-    for (int rt = 0; rt < rts; ++rt) x += unit_tiles(n, len, G, rt);
+    for (int rt = 0; rt < rts; ++rt) x += unit_tiles(r.n, len, G, rt);
     return x;
   };
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
     mine += request_tiles(b);
-    if ((long long)(p.cu_q[b + 1] - p.cu_q[b]) * G > p.most_rows) record_status(p.status, kStatusOffsets, 53);
+    const Rows r = rows_of(p, b);
+    if ((long long)r.n * G > p.most_rows) record_status(p.status, kStatusOffsets, 53);
+    if (r.bad) record_status(p.status, kStatusOffsets, 54);
   }
   long long incl = mine;
 #pragma unroll
@@ -245,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       if (x && t_first < at + x * p.Hkv) {
         const int h = (int)((t_first - at) / x);
         at += h * x;
-        const int n = p.cu_q[b + 1] - p.cu_q[b], len = cached(p, b);
+        const int n = rows_of(p, b).n, len = cached(p, b);
         int rt = 0;
         for (;; ++rt) {
           const int nt = unit_tiles(n, len, G, rt);
@@ -337,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       const int t0 = u->t0, t1 = u->t1;
       const bool in = row.in;
       const float qscale = row.qscale;
-      const int seen = in ? u->len - u->n + row.i + 1 : 0;
+      const int seen = in ? max(0, u->len - u->n + row.i + 1) : 0;
       float m = -INFINITY, l = 0.0f;  // the row's reference; the sum of this thread's weights
       for (int t = t0; t < t1; ++t, ++c) {
         const uint32_t sb = c & 1, slot = c % kPageSlots;
