@@ -590,6 +590,11 @@ def _check_kv_cache(cache):
     return k, v, ks, vs, shape
 
 
+def _not_on_gpu(name):
+    """The calls hand addresses to kernels: a tensor elsewhere is refused before that."""
+    raise ValueError(f"{name}: every tensor is on the GPU")
+
+
 def _ints(name, *tensors):
     for t in tensors:
         if t.dtype is not _I32 or not t.is_contiguous():
@@ -624,6 +629,9 @@ def kv_plan(seq_lens, new_lens, block_table, free_pages, n_free, page_size: int,
     ld, width = _check_table("kv_plan", block_table, B)
     if cu.numel() < B + 1 or kv.numel() < B or slots.numel() < total_new:
         raise ValueError("kv_plan: outputs are [B + 1], [B], [total_new] and [1]")
+    if not (seq_lens.is_cuda and new_lens.is_cuda and block_table.is_cuda and free_pages.is_cuda and n_free.is_cuda
+            and cu.is_cuda and kv.is_cuda and slots.is_cuda and left.is_cuda):
+        _not_on_gpu("kv_plan")
     a = _KV_PLAN_ARGS.pack(seq_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(), ld, width,
                            free_pages.data_ptr(), n_free.data_ptr(), free_pages.numel(), page_size, total_new,
                            cu.data_ptr(), kv.data_ptr(), slots.data_ptr(), left.data_ptr())
@@ -639,6 +647,8 @@ def kv_release(lens, done, block_table, free_pages, n_free, page_size: int, stre
     if done.numel() != B:
         raise ValueError("kv_release: lens and done differ in the number of requests")
     ld, width = _check_table("kv_release", block_table, B)
+    if not (lens.is_cuda and done.is_cuda and block_table.is_cuda and free_pages.is_cuda and n_free.is_cuda):
+        _not_on_gpu("kv_release")
     _check((_lib or load()).bs_kv_release(
         lens.data_ptr(), done.data_ptr(), B, block_table.data_ptr(), ld, width, free_pages.data_ptr(),
         n_free.data_ptr(), free_pages.numel(), page_size, _stream(stream)))
@@ -660,6 +670,8 @@ def kv_append(k, v, slots, cache, stream=None):
         raise TypeError(f"unsupported dtype {dt}")
     if slots.dtype is not _I32 or not slots.is_contiguous():
         raise TypeError("kv_append: slots is a contiguous int32 tensor")
+    if not (k.is_cuda and v.is_cuda and slots.is_cuda and kc.is_cuda and vc.is_cuda and ks.is_cuda and vs.is_cuda):
+        _not_on_gpu("kv_append")
     a = _KV_APPEND_ARGS.pack(k.data_ptr(), v.data_ptr(), DTYPE_BF16 if dt is _BF16 else DTYPE_F32, T, Hkv, D, kt, kh,
                              vt, vh, slots.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(),
                              pages, page)
@@ -722,7 +734,17 @@ def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_s
     else:
         if lse.dtype is not _F32 or lse.shape != (T, Hq) or not lse.is_contiguous():
             raise ValueError("kv_attention: lse is a contiguous float32 [T, Hq] tensor")
+        if not lse.is_cuda:
+            _not_on_gpu("kv_attention")
         lse_ptr = lse.data_ptr()
+    if workspace is not None:
+        if workspace.dtype is not _U8 or not workspace.is_contiguous():
+            raise TypeError("kv_attention: workspace is a contiguous uint8 tensor of kv_attention_workspace")
+        if not workspace.is_cuda:
+            _not_on_gpu("kv_attention")
+    if not (q.is_cuda and out.is_cuda and kc.is_cuda and vc.is_cuda and ks.is_cuda and vs.is_cuda and block_table.is_cuda
+            and cu_q.is_cuda and kv_lens.is_cuda):
+        _not_on_gpu("kv_attention")
     handle = _stream(stream)
     opts = getattr(_tls, "opts", None)
     args = (q.data_ptr(), qt, qh, out.data_ptr(), ot, oh, lse_ptr, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(),
@@ -732,8 +754,6 @@ def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_s
     lib = _lib or load()
     dev = q.get_device()
     if workspace is not None:
-        if workspace.dtype is not _U8 or not workspace.is_contiguous():
-            raise TypeError("kv_attention: workspace is a contiguous uint8 tensor of kv_attention_workspace")
         ws, nbytes = workspace, workspace.numel()
     else:
         nbytes = _kv_workspace_bytes(lib, dev, D)
@@ -766,6 +786,9 @@ def matvec_fp4(x, codes, sf, out_dtype=torch.bfloat16, alpha: float = 1.0, bias=
     ldo, one = out.stride()
     if out.shape != (M, N) or one != 1:
         raise ValueError(f"matvec_fp4: out is [{M}, {N}] with contiguous rows")
+    if not (x.is_cuda and codes.is_cuda and sf.is_cuda and out.is_cuda and (bias is None or bias.is_cuda)
+            and (tensor_scale is None or tensor_scale.is_cuda)):
+        _not_on_gpu("matvec_fp4")
     if M <= 1:
         ldx, ldo = K, N   # the stride of a single row means nothing
     a = _FP4_MATVEC_ARGS.pack(x.data_ptr(), ldx, M, codes.data_ptr(), sf.data_ptr(), N, K, alpha,
