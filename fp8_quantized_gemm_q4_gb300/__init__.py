@@ -627,8 +627,10 @@ def kv_plan(seq_lens, new_lens, block_table, free_pages, n_free, page_size: int,
     if new_lens.numel() != B:
         raise ValueError("kv_plan: seq_lens and new_lens differ in the number of requests")
     ld, width = _check_table("kv_plan", block_table, B)
-    if cu.numel() < B + 1 or kv.numel() < B or slots.numel() < total_new:
+    if cu.numel() < B + 1 or kv.numel() < B or slots.numel() < total_new or left.numel() < 1:
         raise ValueError("kv_plan: outputs are [B + 1], [B], [total_new] and [1]")
+    if n_free.numel() != 1:
+        raise ValueError("kv_plan: n_free is an int32 tensor of one element")
     if not (seq_lens.is_cuda and new_lens.is_cuda and block_table.is_cuda and free_pages.is_cuda and n_free.is_cuda
             and cu.is_cuda and kv.is_cuda and slots.is_cuda and left.is_cuda):
         _not_on_gpu("kv_plan")
@@ -646,6 +648,8 @@ def kv_release(lens, done, block_table, free_pages, n_free, page_size: int, stre
     B = lens.numel()
     if done.numel() != B:
         raise ValueError("kv_release: lens and done differ in the number of requests")
+    if n_free.numel() != 1:
+        raise ValueError("kv_release: n_free is an int32 tensor of one element")
     ld, width = _check_table("kv_release", block_table, B)
     if not (lens.is_cuda and done.is_cuda and block_table.is_cuda and free_pages.is_cuda and n_free.is_cuda):
         _not_on_gpu("kv_release")
@@ -775,12 +779,12 @@ def matvec_fp4(x, codes, sf, out_dtype=torch.bfloat16, alpha: float = 1.0, bias=
         raise TypeError("matvec_fp4: x is a bfloat16 [M, K] tensor with contiguous rows")
     if codes.dtype is not _U8 or half * 2 != K or not codes.is_contiguous():
         raise ValueError(f"matvec_fp4: codes are contiguous uint8 [N, {K // 2}]")
-    if sf.dtype is not _U8 or sf.numel() < (N + 127) // 128 * 128 * (K // 16):
-        raise ValueError("matvec_fp4: sf are the uint8 scales of [N, K], bs_sf_bytes(N, K) of them")
+    if sf.dtype is not _U8 or sf.numel() < (N + 127) // 128 * 128 * (K // 16) or not sf.is_contiguous():
+        raise ValueError("matvec_fp4: sf are the uint8 scales of [N, K], bs_sf_bytes(N, K) of them, contiguous")
     if bias is not None and (bias.dtype is not _BF16 or bias.numel() != N or not bias.is_contiguous()):
         raise ValueError("matvec_fp4: bias is a contiguous bfloat16 [N] tensor")
-    if tensor_scale is not None and tensor_scale.dtype is not _F32:
-        raise TypeError("matvec_fp4: tensor_scale is a float32 tensor")
+    if tensor_scale is not None and (tensor_scale.dtype is not _F32 or tensor_scale.numel() != 1):
+        raise TypeError("matvec_fp4: tensor_scale is a float32 tensor of one element")
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=x.device)
     ldo, one = out.stride()

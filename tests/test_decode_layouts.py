@@ -1,0 +1,43 @@
+"""Sizes and layouts that the binding of the decode-step calls hands on as bare
+addresses: what is too small or laid out otherwise is refused (no GPU needed: a
+call that went on would reach the stand-ins)."""
+import pytest
+import torch
+
+
+@pytest.fixture
+def bs(monkeypatch):
+    import fp8_quantized_gemm_q4_gb300 as bs
+
+    def reached(*args):
+        raise AssertionError("the call went on")
+
+    monkeypatch.setattr(bs, "_stream", reached)
+    monkeypatch.setattr(bs, "_not_on_gpu", reached)
+    monkeypatch.setattr(bs, "_lib", object())
+    return bs
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def test_sizes_and_layouts(bs):
+    w, x = torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(2, 64).bfloat16()
+    sf = torch.zeros(512, dtype=torch.uint8)
+    with pytest.raises(AssertionError):
+        bs.matvec_fp4(x, w, sf, tensor_scale=torch.ones(1))
+    with pytest.raises(ValueError):                       # every second byte
+        bs.matvec_fp4(x, w, torch.zeros(1024, dtype=torch.uint8)[::2])
+    for ts in (torch.ones(0), torch.ones(2)):
+        with pytest.raises(TypeError):
+            bs.matvec_fp4(x, w, sf, tensor_scale=ts)
+    out = (i32(3), i32(2), i32(4), i32(1))
+    with pytest.raises(AssertionError):
+        bs.kv_plan(i32(2), i32(2), i32(2, 3), i32(9), i32(1), 16, 4, out=out)
+    with pytest.raises(ValueError):
+        bs.kv_plan(i32(2), i32(2), i32(2, 3), i32(9), i32(0), 16, 4, out=out)
+    with pytest.raises(ValueError):
+        bs.kv_plan(i32(2), i32(2), i32(2, 3), i32(9), i32(1), 16, 4, out=(*out[:3], i32(0)))
+    with pytest.raises(ValueError):
+        bs.kv_release(i32(2), i32(2), i32(2, 3), i32(9), i32(0), 16)
