@@ -38,6 +38,16 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), unsigned grid, unsigned block,
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
+// launch_kernel for a kernel that needs more dynamic shared memory than 48 KB: the
+// limit belongs to the function in one context, so it is set with each launch.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_kernel_smem(void (*kern)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                               Args&&... args) {
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, grid, block, smem, stream, 1, std::forward<Args>(args)...);
+}
+
 enum { kEpiStore = 0, kEpiSwiglu = 1, kEpiCombine = 2, kEpiRows = 3, kEpiSwigluQ4 = 4 };
 // SWIGLU and SWIGLU_Q4 share the tile map (gate / up column blocks); Q4 then
 // quantizes h in the epilogue instead of storing it.

@@ -606,11 +606,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
 template <int D>
 cudaError_t launch_few(const KvAttentionLaunch& L, cudaStream_t stream) {
   constexpr int kSmem = (int)sizeof(FewSmem<D>) + 1024;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(kv_attention_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (attr != cudaSuccess) return attr;
-  return launch_kernel(kv_attention_few_kernel<D>, (unsigned)L.few_grid, kFewThreads, kSmem, stream, 1, L.tm_k, L.tm_v,
-                       L.p);
+  return launch_kernel_smem(kv_attention_few_kernel<D>, (unsigned)L.few_grid, kFewThreads, kSmem, stream, L.tm_k, L.tm_v,
+                            L.p);
 }
 
 }  // namespace

@@ -711,10 +711,7 @@ cudaError_t launch(const KvAttentionLaunch& L, cudaStream_t stream) {
   // all of an SM's shared memory: one CTA an SM, as tensor memory has it
   constexpr int kSmem = 227 * 1024;
   static_assert(sizeof(RowsSmem<D>) + 1024 <= kSmem, "shared memory");
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(kv_attention_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (attr != cudaSuccess) return attr;
-  return launch_kernel(kv_attention_rows_kernel<D>, (unsigned)L.rows_grid, kThreads, kSmem, stream, 1, L.p);
+  return launch_kernel_smem(kv_attention_rows_kernel<D>, (unsigned)L.rows_grid, kThreads, kSmem, stream, L.p);
 }
 
 }  // namespace

@@ -142,12 +142,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
 
 cudaError_t launch_kv_plan(const KvPlanParams& p, cudaStream_t stream) {
   const size_t smem = (size_t)(3 * p.B + 1) * sizeof(int);
-  static const cudaError_t attr = cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       (3 * kKvPlanMaxB + 1) * (int)sizeof(int));
-  if (attr != cudaSuccess) return attr;
   const long long ctas = ((long long)p.T + kPlanThreads - 1) / kPlanThreads;
   const unsigned grid = (unsigned)(ctas < 1 ? 1 : ctas > 148 ? 148 : ctas);
-  return launch_kernel(kv_plan_kernel, grid, kPlanThreads, smem, stream, 1, p);
+  return smem <= 48000 ? launch_kernel(kv_plan_kernel, grid, kPlanThreads, smem, stream, 1, p)
+                       : launch_kernel_smem(kv_plan_kernel, grid, kPlanThreads, smem, stream, p);
 }
 
 // ---------------------------------------------------------------------------

@@ -518,21 +518,15 @@ template <int NT>
 cudaError_t launch_many(const Fp4MatvecParams& p, int sms, cudaStream_t stream) {
   constexpr int kBytes = (int)sizeof(ManySmem<NT>);
   static_assert(kBytes <= 227 * 1024 && kKp * 4 * NT * (16 * kRg * kOwn + 4) * 8 <= (int)sizeof(ManySmem<NT>::ring), "shared memory");
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(fp4_matvec_many_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
-  if (attr != cudaSuccess) return attr;
   const int tiles = (p.N + 127) / 128 * 8;
-  return launch_kernel(fp4_matvec_many_kernel<NT>, (unsigned)(tiles < sms ? tiles : sms), kThreads, kBytes, stream, 1, p,
-                       tiles);
+  return launch_kernel_smem(fp4_matvec_many_kernel<NT>, (unsigned)(tiles < sms ? tiles : sms), kThreads, kBytes, stream, p,
+                            tiles);
 }
 
 template <int NT>
 cudaError_t launch_few(const Fp4MatvecParams& p, int sms, cudaStream_t stream) {
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(fp4_matvec_few_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (attr != cudaSuccess) return attr;
   const int tiles = (p.N + 127) / 128 * 8;
-  return launch_kernel(fp4_matvec_few_kernel<NT>, (unsigned)(tiles < sms ? tiles : sms), kThreads, kSmem, stream, 1, p, tiles);
+  return launch_kernel_smem(fp4_matvec_few_kernel<NT>, (unsigned)(tiles < sms ? tiles : sms), kThreads, kSmem, stream, p, tiles);
 }
 
 }  // namespace
