@@ -23,7 +23,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 // natural log of the softmax sum 2^m l
 __device__ __forceinline__ float lse_of(float m, float l) {
-  return l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;  // NaN sums stay NaN
 }
 
 // A request's rows: the first, how many, and how many of them the call has (row < T).
