@@ -54,6 +54,30 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   return r;
 }
 
+// NaN codes among the first cnt of 16 tokens of V that some row does not see: a
+// weight of 0 would spread them, so they become 0 in shared memory.  The lane's
+// accumulators whose row does see one are returned: bit 4 a + 2 i + e for column
+// 16 a + 2 g + i and the row that sees `seen[e]` of the 16.  Called by a whole
+// warp; out of line, for calls that meet none.
+template <int D>
+__device__ __noinline__ uint32_t take_nan(uint8_t* vt, int cnt, int seen0, int seen1, int lane) {
+  uint32_t hit = 0;
+  for (int tok = 0; tok < cnt; ++tok)
+#pragma unroll 1
+    for (int a = 0; a < D / 16; ++a)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if ((vt[code_at<D>(tok, a) + 2 * (lane >> 2) + i] & 0x7f) == 0x7f)
+          hit |= (tok < seen0 ? 1u : 0u) << (4 * a + 2 * i) | (tok < seen1 ? 2u : 0u) << (4 * a + 2 * i);
+  __syncwarp();
+  for (int x = lane; x < cnt * (D / 4); x += 32) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(vt + code_at<D>(x / (D / 4), x % (D / 4) / 4)) + x % 4;
+    *w = without(*w, nan_codes(*w));
+  }
+  __syncwarp();
+  return hit;
+}
+
 // One step of the online softmax over 16 tokens for 8 rows.  u[e]: logit of
 // row 2 c + e % 2 for token place g + 8 (e / 2).  Returns the weights as the B
 // fragment (places on k) of the product with V.
@@ -428,6 +452,23 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
                 *reinterpret_cast<uint4*>(vt + code_at<D>(x / (D / 16), x % (D / 16))) = make_uint4(0, 0, 0, 0);
               __syncwarp();
             }
+            const int tok0 = (tile - begin) * kTile + warp * 16;
+            if (tok0 + cnt > all_seen) {
+              uint32_t any = 0;
+              for (int x = lane; x < cnt * (D / 16); x += 32) {
+                const uint4 w = *reinterpret_cast<const uint4*>(vt + code_at<D>(x / (D / 16), x % (D / 16)));
+                any |= nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w);
+              }
+              if (__any_sync(kFullMask, any)) {
+                const uint32_t hit = take_nan<D>(vt, cnt, seen[0] - tok0, seen[1] - tok0, lane);
+#pragma unroll
+                for (int a = 0; a < D / 16; ++a)
+#pragma unroll
+                  for (int x = 0; x < 4; ++x)
+                    if (hit >> (4 * a + x) & 1) o[a][x] = __int_as_float(0x7fffffff);
+                __syncwarp();
+              }
+            }
             float u[4] = {}, u2[4] = {};  // two chains of products
             {
               const int tok = token_of<D>(g);
@@ -444,7 +485,6 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
                 }
               }
             }
-            const int tok0 = (tile - begin) * kTile + warp * 16;
             const float f[2] = {qscale[0] * sc.x, qscale[1] * sc.x};
 #pragma unroll
             for (int e = 0; e < 4; ++e) u[e] = fmaf(u[e] + u2[e], f[e & 1], sc.y);
@@ -472,7 +512,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
                 mma_f16(o[2 * a + x], va, pb[0], pb[1]);
               }
             }
-            if (cnt < 16) fence_proxy_async_smem();  // the zeros, before the next copy into this stage
+            if (cnt < 16 || tok0 + cnt > all_seen) fence_proxy_async_smem();  // the zeros, before the next copy into this stage
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.empty[stage]);

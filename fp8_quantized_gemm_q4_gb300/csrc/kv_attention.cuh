@@ -21,6 +21,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// 0x80 in every byte of w that is a NaN code (0x7f or 0xff)
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+// w with the codes marked by n at 0
+__device__ __forceinline__ uint32_t without(uint32_t w, uint32_t n) { return w & ~((n >> 7) * 0xffu); }
+
 // natural log of the softmax sum 2^m l
 __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;  // NaN sums stay NaN

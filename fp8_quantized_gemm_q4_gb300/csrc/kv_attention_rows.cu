@@ -55,6 +55,7 @@ constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384;
 // A unit as the roles read it; t0 == t1: the share is done
 struct UnitInfo {
   int t0, t1, nt, len;     // its tiles within the share, all its tiles, cached tokens
+  int b;                   // request
   int h, rt, row0, n;      // KV head, row tile; the request's first row and rows
   long long at;            // its first tile's place in the list
 };
@@ -69,9 +70,16 @@ struct RowsSmem {
   UnitInfo unit[kUnitSlots];
   uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
   float swap[4][kM];                       // between the four threads of a row
+  // of the unit of that number modulo 8, if NaN codes of V were taken out where not every row
+  // sees them: the number + 1, request, KV head, the first token of such tiles
+  int4 nan_unit[8];
   long long scan[kThreads / 32];
   long long start_at;
   int start[3];
+  // tiles in the list and CTAs that share them, for the joins: in registers through
+  // the tiles they cost the softmax its room there (287 us, not 265, for the prompts above)
+  long long total;
+  int shares;
   uint32_t tmem;
   int abort_flag, last;
 };
@@ -143,6 +151,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
+// NaN into the columns part * D / 4 .. of a row whose tokens from .. to - 1 hold NaN
+// codes of V there, in the output (dst) or the unit's piece.  Out of line, for units
+// that meet none.
+template <int D>
+__device__ __noinline__ void put_nan(const KvAttentionParams& p, int b, int h, int part, int from, int to,
+                                     __nv_bfloat16* dst, float* piece) {
+  for (int x = from; x < to; ++x) {
+    const int id = p.table[b * p.ld_table + (x >> p.page_shift)];
+    if ((unsigned)id >= (unsigned)p.num_pages) continue;
+    const uint8_t* code =
+        p.v_codes + ((((long long)id * p.Hkv + h) << p.page_shift) + (x & ((1 << p.page_shift) - 1))) * D;
+    for (int d = part * (D / 4); d < (part + 1) * (D / 4); ++d)
+      if ((code[d] & 0x7f) == 0x7f) {
+        if (dst)
+          dst[d] = __ushort_as_bfloat16(0x7fff);
+        else
+          piece[(d & ~3) * kM + (d & 3)] = __int_as_float(0x7fffffff);
+      }
+  }
+}
+
 // all softmax warps: barrier 1; the four with the same 32 rows: barriers 2 to 5
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft * 32) : "memory"); }
 __device__ __forceinline__ void rows_sync(int rows) { asm volatile("bar.sync %0, 128;" ::"r"(2 + rows) : "memory"); }
@@ -193,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
     fence_barrier_init();
     sm.abort_flag = 0;
   }
+  if (tid < 8) sm.nan_unit[tid] = make_int4(0, 0, 0, 0);
   // whoever goes on after a wait that gave up finds no page here, or an old one
   if (tid < kPageSlots * kGroups) sm.page[tid / kGroups][tid % kGroups].x = __int_as_float(-1);
   if (warp == kMma) {
@@ -240,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
   total *= p.Hkv;
   before *= p.Hkv;
   const int shares = (int)min((long long)gridDim.x, (total + kMinTiles - 1) / kMinTiles);
+  if (tid == 0) sm.total = total, sm.shares = shares;
   const bool works = (int)blockIdx.x < shares;
   const long long t_first = works ? total * blockIdx.x / shares : 0;
   const long long t_last = works ? total * (blockIdx.x + 1) / shares : 0;
@@ -465,12 +496,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         __syncwarp();
       }
       tc_fence_before();
+      if (sm.nan_unit[unit & 7].x == (int)unit + 1) {
+        const int4 bad = sm.nan_unit[unit & 7];
+        if (in) put_nan<D>(p, bad.y, bad.z, part, max(bad.w, t0 * kN), min(seen, t1 * kN), alone ? dst : nullptr, slot + r128 * 4);
+        __syncwarp();
+      }
       if (alone) {
         if (in && part == 0 && p.lse) p.lse[lse_at] = lse_of(m, l);
       } else {
         if (in && part == 0) *reinterpret_cast<float2*>(slot + kM * D + 2 * r128) = make_float2(m, l);
         __threadfence();
-        const int c0 = (int)(((at + 1) * shares - 1) / total), c1 = (int)(((at + nt) * shares - 1) / total);
+        const long long all = sm.total;
+        const int c0 = (int)(((at + 1) * sm.shares - 1) / all), c1 = (int)(((at + nt) * sm.shares - 1) / all);
         softmax_sync();
         if (tid == 0) {
           const int old = atomicAdd(p.counters + c0, 1);
@@ -517,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       w.nt = unit_tiles(w.n, w.len, G, w.rt);
       for (uint32_t x = 0; w.at < t_last; ++x, next_unit(p, G, w)) {
         if (x < k || (w.at >= t_first && w.at + w.nt <= t_last)) continue;
-        const int c0 = (int)(((w.at + 1) * shares - 1) / total), c1 = (int)(((w.at + w.nt) * shares - 1) / total);
+        const int c0 = (int)(((w.at + 1) * sm.shares - 1) / sm.total), c1 = (int)(((w.at + w.nt) * sm.shares - 1) / sm.total);
         if (atomicAdd(p.counters + c0, 1) == c1 - c0) p.counters[c0] = 0;
       }
     }
@@ -542,6 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       if (!unit_open(u)) break;
       const int t0 = u->t0, t1 = u->t1, len = u->len;
       if (t0 == t1) break;
+      // from this token on, some row of the unit does not see V: a NaN code there
+      // would reach that row with a weight of 0.  Tiles with such tokens go without
+      // theirs, and the rows that see one get the NaN at the end.
+      const int hidden = max(0, len - u->n + (int)((long long)u->rt * kM / G) + 1);
+      const int4 bad = make_int4((int)k + 1, u->b, u->h, hidden / kN * kN);
       unit_close();
       uint4 raw[kSteps];
       auto load = [&](uint4& r, int s, int left, const float4* page) {
@@ -565,6 +607,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         const bool more = t + 1 < t1;
         if (more) page = page_open(c + 1);
         const uint32_t b = c & 1, to = b * (kN * D * 2);
+        if (is_v && (t + 1) * kN > hidden) {
+          uint32_t any = 0;
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) {
+            const uint4 n = make_uint4(nan_codes(raw[s].x), nan_codes(raw[s].y), nan_codes(raw[s].z), nan_codes(raw[s].w));
+            any |= n.x | n.y | n.z | n.w;
+            raw[s] = make_uint4(without(raw[s].x, n.x), without(raw[s].y, n.y), without(raw[s].z, n.z), without(raw[s].w, n.w));
+          }
+          if (any) sm.nan_unit[(bad.x - 1) & 7] = bad;
+        }
         mbar_wait(&empty[b], ((c >> 1) & 1) ^ 1, wg, 66);
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
@@ -658,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       const bool ok = mbar_wait(&sm.unit_empty[slot], ((k / kUnitSlots) & 1) ^ 1, wg, 75);
       if (!__all_sync(kFullMask, ok)) return false;
       if (lane == 0) {
-        sm.unit[slot] = UnitInfo{t0, t1, u.nt, u.len, u.h, u.rt, u.row0, u.n, u.at};
+        sm.unit[slot] = UnitInfo{t0, t1, u.nt, u.len, u.b, u.h, u.rt, u.row0, u.n, u.at};
         mbar_arrive(&sm.unit_full[slot]);
       }
       __syncwarp();

@@ -616,7 +616,8 @@ bs_status bs_kv_append(const bs_kv_append_args *args, bs_stream_t stream);
  * 0 .. kv_lens[b] - n + i (append first: the new tokens are in the cache):
  *     s_t = softmax_scale * q . K_t,  lse = log sum_t exp(s_t),
  *     out = sum_t exp(s_t - lse) V_t
- * A row that sees no token gets out 0 and lse -infinity.  Sums are fp32; the
+ * A row that sees no token gets out 0 and lse -infinity.  NaN codes reach the rows
+ * that see their token only: of K, the whole row; of V, its column.  Sums are fp32; the
  * products take q scaled by a power of two per row as fp16 (exact for every
  * element within 2^-29 of the row's largest) and the weights exp(s - max)
  * rounded to fp16.
