@@ -224,8 +224,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
     const int nt = few_tiles(p, n_own, len_own, G), rt = nt ? (n_own * G + 7) / 8 : 0;
     mine.x += nt * rt;
     mine.y += rt;
-    if ((long long)n_own * G > p.most_rows) record_status(p.status, kStatusOffsets, 53);
-    if (own.bad) record_status(p.status, kStatusOffsets, 54);
+    // one CTA tells: the check in all of them cost a call of prompts, whose other kernel
+    // waits for this one to end, 11 of 276 us
+    if (blockIdx.x == 0 && ((long long)n_own * G > p.most_rows || own.bad || length_bad(p, b)))
+      record_status(p.status, kStatusOffsets, 53);
   }
   int2 incl = mine;
 #pragma unroll

@@ -43,8 +43,12 @@ __device__ __forceinline__ Rows rows_of(const KvAttentionParams& p, int b) {
   return {r0, n, n ? max(0, min(n, p.T - r0)) : 0, r0 < 0 || r1 < r0 || r1 > p.T};
 }
 
-// Cached tokens of a request, as far as its table row can name them.
+// Cached tokens of a request, as far as its table row can name them; a length beyond
+// that, or a negative one, is the status's to tell.
 __device__ __forceinline__ int cached(const KvAttentionParams& p, int b) {
   return min(max(p.kv_lens[b], 0), p.max_pages << p.page_shift);
+}
+__device__ __forceinline__ bool length_bad(const KvAttentionParams& p, int b) {
+  return (unsigned)p.kv_lens[b] > (unsigned)(p.max_pages << p.page_shift);
 }
 }  // namespace bsk

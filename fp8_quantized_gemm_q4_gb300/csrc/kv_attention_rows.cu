@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
     mine += request_tiles(b);
     const Rows r = rows_of(p, b);
     if ((long long)r.n * G > p.most_rows) record_status(p.status, kStatusOffsets, 53);
-    if (r.bad) record_status(p.status, kStatusOffsets, 54);
+    if (r.bad || length_bad(p, b)) record_status(p.status, kStatusOffsets, 54);
   }
   long long incl = mine;
 #pragma unroll

@@ -628,7 +628,9 @@ bs_status bs_kv_append(const bs_kv_append_args *args, bs_stream_t stream);
  *   cu_q, kv_lens  int32 [B + 1] / [B]; cu_q[0] == 0, ascending, cu_q[B] <= T;
  *              rows from cu_q[B] on are not written.  Offsets that are negative,
  *              descend or pass T set BS_ERR_OFFSETS: no row outside [0, T) is
- *              touched, a request with a negative or descending pair has no rows
+ *              touched, a request with a negative or descending pair has no rows.
+ *              So does a length below 0 (taken as 0) or above max_pages * page_size
+ *              (taken as that)
  *   max_q_len  an upper bound of the rows of a request (0: no bound known, T)
  *   block_table int32 [B, ld_table]; an id outside [0, num_pages) on a seen
  *              page sets BS_ERR_OFFSETS, the page is left out

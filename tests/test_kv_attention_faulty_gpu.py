@@ -39,3 +39,21 @@ def test_offsets(cuda_lib, Hq, Hkv, D, T, kind):
     # and the workspace is as the next call needs it
     assert torch.equal(bs.kv_attention(q, cache, i32(table), i32(good), i32(kv), 0), want)
     assert bs.device_status()[0] == bs.BS_OK
+
+
+@pytest.mark.parametrize("q_lens", [[1, 2], [150, 40]])
+def test_lengths(cuda_lib, q_lens):
+    """A length that the table cannot hold, or a negative one, sets the status (the
+    first is cut to the table's, the second counts as 0); the longest it can hold does not."""
+    bs = cuda_lib
+    q, cache, table, cu = build(bs, 9, [320, 100], q_lens, 16, 2, 64, 64)
+    t = i32([r[:5] for r in table])
+    for kv, same, status in (([320, 100], None, bs.BS_OK), ([321, 100], [320, 100], bs.BS_ERR_OFFSETS),
+                             ([(1 << 31) - 1, 100], [320, 100], bs.BS_ERR_OFFSETS), ([320, -1], [320, 0], bs.BS_ERR_OFFSETS),
+                             ([-(1 << 31), 100], [0, 100], bs.BS_ERR_OFFSETS)):
+        bs.clear_device_status()
+        out = bs.kv_attention(q, cache, t, i32(cu), i32(kv), 0)
+        assert bs.device_status()[0] == status, kv
+        if same:
+            assert torch.equal(out, bs.kv_attention(q, cache, t, i32(cu), i32(same), 0))
+    bs.clear_device_status()
