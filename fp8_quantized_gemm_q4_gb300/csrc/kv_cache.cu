@@ -240,18 +240,23 @@ struct Eight {
     if constexpr (kBf16) return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
     return __uint_as_float(w[i]);
   }
-  __device__ __forceinline__ float amax() const {
-    if constexpr (kBf16) {  // in pairs: a maximum of bf16 values is one of them
-      __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
+  // Running maximum of the finite magnitudes' bits, bf16 in pairs.  (One infinity's
+  // scale would take all that the page holds to 0.)  Bits one step of the exponent
+  // up keep their order as signed integers, and the non-finite ones turn negative.
+  static constexpr uint32_t kUp = kBf16 ? 0x00800080u : 0x00800000u;
+  __device__ __forceinline__ void amax(uint32_t& m) const {
 #pragma unroll
-      for (int i = 1; i < 4; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
-      return fmaxf(__low2float(m), __high2float(m));
-    } else {
-      float m = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(__uint_as_float(w[i])));
-      return m;
+    for (int i = 0; i < (kBf16 ? 4 : 8); ++i) {
+      if constexpr (kBf16)
+        m = __vmaxs2(m, (w[i] & 0x7fff7fffu) + kUp);
+      else
+        m = max((int)m, (int)((w[i] & 0x7fffffffu) + kUp));
     }
+  }
+  // of a warp's lanes, as fp32
+  static __device__ __forceinline__ float amax_of(uint32_t m) {
+    if constexpr (kBf16) m = max((int)(m << 16), (int)(m & 0xffff0000u));
+    return __uint_as_float((uint32_t)__reduce_max_sync(kFullMask, (int)m) - 0x00800000u);
   }
   __device__ __forceinline__ uint2 codes(float inv) const {
     uint32_t h[4];
@@ -288,11 +293,6 @@ __device__ __forceinline__ float page_scale(uint8_t* codes, int off, float amax,
   return s;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, d));
-  return v;
-}
 __device__ __forceinline__ bool slot_ok(const KvAppendParams& p, int slot) {
   if (slot < 0) return false;
   if ((slot >> p.page_shift) < p.num_pages) return true;
@@ -316,20 +316,19 @@ __device__ __forceinline__ void append_run(const KvAppendParams& p, int which, i
   uint8_t* codes = p.codes[which] + (page << p.page_shift) * D;
   const float old = off > 0 ? *scale : 0.0f;
   Eight<kBf16> kept[kKeep], more;
-  float amax = 0.0f;
+  uint32_t top = Eight<kBf16>::kUp;
 #pragma unroll
   for (int i = 0; i < kKeep; ++i, at += step)
     if (r0 + i * kPass < n) kept[i].load(p.x[which], at);
 #pragma unroll
   for (int i = 0; i < kKeep; ++i)
-    if (r0 + i * kPass < n) amax = fmaxf(amax, kept[i].amax());
+    if (r0 + i * kPass < n) kept[i].amax(top);
   for (int i = kKeep; r0 + i * kPass < n; ++i, at += step) {
     more.load(p.x[which], at);
-    amax = fmaxf(amax, more.amax());
+    more.amax(top);
   }
   __syncwarp();
-  amax = warp_max(amax);
-  const float s = page_scale<D>(codes, off, amax, old, lane);
+  const float s = page_scale<D>(codes, off, Eight<kBf16>::amax_of(top), old, lane);
   const float inv = 1.0f / s;
   uint2* out = reinterpret_cast<uint2*>(codes) + (off + r0) * kVecs + col;
 #pragma unroll

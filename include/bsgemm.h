@@ -586,7 +586,8 @@ bs_status bs_kv_release(const int32_t *lens, const int32_t *done, int B, int32_t
  *     e4m3_rn(code * old scale / s)
  *     code = e4m3_rn_satfinite(x / s)
  * Dividing by a power of two is exact, and growing a scale changes only codes
- * that fall among e4m3's subnormals.
+ * that fall among e4m3's subnormals.  amax is that of the finite values: a NaN
+ * becomes a NaN code, an infinity the code of +-448.
  *
  *   k, v       [T, Hkv, D] fp32 or bf16 (dtype) with strides in elements; D is
  *              contiguous, strides are multiples of 8, pointers 16-byte aligned
