@@ -174,18 +174,44 @@ __global__ void __launch_bounds__(kPlanThreads) kv_release_kernel(const __grid_c
     sum += block;
   }
   __syncthreads();
-  const int room = p.capacity - n_free;
-  const int total = (int)min(sum, (long long)room);
-  for (int e = tid; e < total; e += kPlanThreads) {
-    const int b = upper_bound(ends, p.B, e);
-    int* entry = p.table + b * p.ld_table + (e - (b ? ends[b - 1] : 0));
-    p.free_pages[n_free + e] = *entry;
-    *entry = -1;
+  const int entries = (int)min(sum, (long long)INT_MAX);
+  int at = n_free;  // where the next page goes
+  constexpr int kEach = 4;  // entries a thread has on their way
+  for (int base = 0; base < entries; base += kEach * kPlanThreads) {
+    int* entry[kEach];
+    int id[kEach];
+    bool missing = false;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int e = base + i * kPlanThreads + tid;
+      id[i] = -1;
+      if (e >= entries) continue;
+      const int b = upper_bound(ends, p.B, e);
+      entry[i] = p.table + b * p.ld_table + (e - (b ? ends[b - 1] : 0));
+      id[i] = *entry[i];
+      missing |= id[i] < 0;
+    }
+    // a page given back before, or a length that the table does not have
+    if (missing) record_status(p.status, kStatusOffsets, 46);
+    const bool gaps = __syncthreads_or(missing);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      long long rank = tid, unused = 0, here = min(entries - base - i * kPlanThreads, kPlanThreads), unused_here;
+      if (here <= 0) break;
+      if (gaps) {
+        rank = id[i] >= 0;
+        block_scan2(rank, unused, here, unused_here);
+        --rank;
+      }
+      if (id[i] >= 0 && at + rank < p.capacity) {
+        p.free_pages[at + rank] = id[i];
+        *entry[i] = -1;
+      }
+      if (at + here > p.capacity && tid == 0) record_status(p.status, kStatusPages, 44);
+      at = (int)min(at + here, (long long)p.capacity);
+    }
   }
-  if (tid == 0) {
-    *p.n_free = n_free + total;
-    if (sum > room) record_status(p.status, kStatusPages, 44);
-  }
+  if (tid == 0) *p.n_free = at;
 }
 
 cudaError_t launch_kv_release(const KvReleaseParams& p, cudaStream_t stream) {

@@ -557,7 +557,9 @@ bs_status bs_moe_combine(const float *rows, int64_t ld_rows, const int32_t *pair
  * bs_kv_release -- the pages of finished requests (done[b] != 0; lens[b]
  * tokens) are put on the end of free_pages, in request order, *n_free grows by
  * their number, and their table entries become -1.  The caller then gives the
- * request length 0.
+ * request length 0.  A negative entry (a page given back before) is left out and
+ * sets BS_ERR_OFFSETS; pages for which free_pages has no room stay in the table
+ * and set BS_ERR_PAGES.
  * ------------------------------------------------------------------------- */
 typedef struct {
     const int32_t *seq_lens, *new_lens;
