@@ -34,9 +34,17 @@ MATVEC_ROWS = 16   # the most rows that bs_fp4_matvec takes
 
 
 def fp4_linear(x, codes, sf, out=None):
-    """x bf16 [T, K] times FP4 weights (codes [N, K/2] and scales of q4_quantize)."""
+    """x bf16 [T, K] times FP4 weights (codes [N, K/2] and scales of q4_quantize).
+    bs_gemm takes N in multiples of 128; other weights are multiplied 16 rows of x
+    at a time."""
     if x.shape[0] <= MATVEC_ROWS:
         return matvec_fp4(x, codes, sf, out=out)
+    if codes.shape[0] % 128:
+        if out is None:
+            out = torch.empty((x.shape[0], codes.shape[0]), dtype=torch.bfloat16, device=x.device)
+        for at in range(0, x.shape[0], MATVEC_ROWS):
+            matvec_fp4(x[at:at + MATVEC_ROWS], codes, sf, out=out[at:at + MATVEC_ROWS])
+        return out
     xc, xsf, _ = q4_quantize(x)
     return gemm_fp4(xc, xsf, codes, sf, x.shape[1], out=out)
 

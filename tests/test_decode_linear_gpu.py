@@ -1,0 +1,53 @@
+"""The products around the attention of DecodeAttention."""
+import pytest
+import torch
+
+from tests import decode_reference as ref
+from tests.test_decode_step_gpu import i32
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def weights(bs, N, K, gen):
+    codes, sf, _ = bs.q4_quantize((torch.randn(N, K, device=DEV, generator=gen) * 0.05).to(torch.bfloat16))
+    return codes, sf
+
+
+def off(y, x, w, scale=1.0):
+    """Largest |y - x W^T| over its bound: fp32 sums over K, terms of x below 2^-29 of the row's largest, bf16 output."""
+    N, K = w[0].shape[0], w[0].shape[1] * 2
+    W = ref.fp4_weights(*w[:2], N, K).to(DEV) * scale
+    want, S = x.double() @ W.T, x.double().abs() @ W.abs().T
+    low = 2.0 ** -39 * K * x.double().abs().amax(1, keepdim=True) * W.abs().amax(1)[None]
+    bound = (K + 8) * 2.0 ** -24 * S + low + 2.0 ** -8 * want.abs()
+    return float(((y.double() - want).abs() / bound).max())
+
+
+@pytest.mark.parametrize("T", [1, 16, 17, 45])
+@pytest.mark.parametrize("N,K", [(320, 192), (129, 256)])
+def test_any_number_of_columns(cuda_lib, T, N, K):
+    """Weights whose rows are no multiple of 128, for any number of tokens."""
+    from fp8_quantized_gemm_q4_gb300.decode import fp4_linear
+    gen = torch.Generator(device=DEV).manual_seed(T + N)
+    w = weights(cuda_lib, N, K, gen)
+    x = torch.randn(T, K, device=DEV, generator=gen).to(torch.bfloat16)
+    assert off(fp4_linear(x, *w), x, w) <= 1
+    out = torch.full((T, N), 9.0, dtype=torch.bfloat16, device=DEV)
+    assert torch.equal(fp4_linear(x, *w, out=out), fp4_linear(x, *w)) and bool((out != 9.0).any())
+
+
+def test_layer_of_odd_width(cuda_lib):
+    """An odd number of heads of 64 and a hidden size of 192: prompts and single tokens."""
+    bs = cuda_lib
+    from fp8_quantized_gemm_q4_gb300.decode import DecodeAttention
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    Hq, Hkv, D, hidden = 3, 1, 64, 192
+    a = DecodeAttention(weights(bs, (Hq + 2 * Hkv) * D, hidden, gen), weights(bs, hidden, Hq * D, gen), Hq, Hkv, D, 2, 8,
+                        16, 4)
+    bs.clear_device_status()
+    prompt = torch.randn(50, hidden, device=DEV, generator=gen).to(torch.bfloat16)
+    y = a.step(prompt, i32([30, 20]), 30)
+    assert y.shape == (50, hidden) and bool(y.isfinite().all()) and a.lens.tolist() == [30, 20]
+    y = a.step(prompt[:2], i32([1, 1]), 1)
+    assert bool(y.isfinite().all()) and a.lens.tolist() == [31, 21] and bs.device_status()[0] == bs.BS_OK
