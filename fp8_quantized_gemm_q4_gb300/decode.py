@@ -33,26 +33,27 @@ from . import (KVCache, gemm_fp4, kv_append, kv_attention, kv_attention_workspac
 MATVEC_ROWS = 16   # the most rows that bs_fp4_matvec takes
 
 
-def fp4_linear(x, codes, sf, out=None):
-    """x bf16 [T, K] times FP4 weights (codes [N, K/2] and scales of q4_quantize).
-    bs_gemm takes N in multiples of 128; other weights are multiplied 16 rows of x
+def fp4_linear(x, codes, sf, out=None, tensor_scale=None):
+    """x bf16 [T, K] times FP4 weights (codes [N, K/2] and scales of q4_quantize, or
+    with ``tensor_scale`` of q4_quantize_two_level).  bs_gemm takes N in multiples of 128; other weights are multiplied 16 rows of x
     at a time."""
     if x.shape[0] <= MATVEC_ROWS:
-        return matvec_fp4(x, codes, sf, out=out)
+        return matvec_fp4(x, codes, sf, out=out, tensor_scale=tensor_scale)
     if codes.shape[0] % 128:
         if out is None:
             out = torch.empty((x.shape[0], codes.shape[0]), dtype=torch.bfloat16, device=x.device)
         for at in range(0, x.shape[0], MATVEC_ROWS):
-            matvec_fp4(x[at:at + MATVEC_ROWS], codes, sf, out=out[at:at + MATVEC_ROWS])
+            matvec_fp4(x[at:at + MATVEC_ROWS], codes, sf, out=out[at:at + MATVEC_ROWS], tensor_scale=tensor_scale)
         return out
     xc, xsf, _ = q4_quantize(x)
-    return gemm_fp4(xc, xsf, codes, sf, x.shape[1], out=out)
+    return gemm_fp4(xc, xsf, codes, sf, x.shape[1], out=out, b_tensor_scale=tensor_scale)
 
 
 class DecodeAttention:
     """Attention of one layer over requests 0 .. B - 1.
 
-    w_qkv, w_out    (codes, scales) of q4_quantize for bf16 weights
+    w_qkv, w_out    (codes, scales) of q4_quantize, or (codes, scales, tensor scale)
+                    of q4_quantize_two_level, for bf16 weights
                     [(Hq + 2 Hkv) D, hidden] (rows of q, then k, then v) and
                     [hidden, Hq D]
     lens            int32 [B], the cached tokens of each request (device)
@@ -74,6 +75,11 @@ class DecodeAttention:
         self.lens = torch.zeros(requests, dtype=torch.int32, device=dev)
         self.workspace = kv_attention_workspace(D, dev)
 
+    @staticmethod
+    def _linear(x, weight):
+        codes, sf, *scale = weight
+        return fp4_linear(x, codes, sf, tensor_scale=scale[0] if scale else None)
+
     def step(self, x, new_lens, max_new: int):
         """x bf16 [T, hidden], the new tokens of request 0, then 1, ..;
         new_lens int32 [B] on the device, their sum at most T, each at most
@@ -81,14 +87,14 @@ class DecodeAttention:
         suffice gets zeros and keeps its length (device status BS_ERR_PAGES)."""
         T, q_rows, kv_rows = x.shape[0], self.Hq * self.D, self.Hkv * self.D
         cu, kv_lens, slots, left = kv_plan(self.lens, new_lens, self.table, self.free, self.n_free, self.page_size, T)
-        qkv = fp4_linear(x, *self.w_qkv)
+        qkv = self._linear(x, self.w_qkv)
         q, k, v = qkv.split([q_rows, kv_rows, kv_rows], 1)
         kv_append(k.view(T, self.Hkv, self.D), v.view(T, self.Hkv, self.D), slots, self.cache)
         att = kv_attention(q.view(T, self.Hq, self.D), self.cache, self.table, cu, kv_lens, max_new,
                            workspace=self.workspace)
         self.n_free.copy_(left)
         torch.maximum(self.lens, kv_lens, out=self.lens)
-        return fp4_linear(att.view(T, q_rows), *self.w_out)
+        return self._linear(att.view(T, q_rows), self.w_out)
 
     def release(self, done):
         """Give back the pages of the requests with done[b] != 0 (int32 [B])."""

@@ -51,3 +51,36 @@ def test_layer_of_odd_width(cuda_lib):
     assert y.shape == (50, hidden) and bool(y.isfinite().all()) and a.lens.tolist() == [30, 20]
     y = a.step(prompt[:2], i32([1, 1]), 1)
     assert bool(y.isfinite().all()) and a.lens.tolist() == [31, 21] and bs.device_status()[0] == bs.BS_OK
+
+
+def test_two_level_weights(cuda_lib):
+    """Weights of q4_quantize_two_level, as it returns them, for few and many tokens and in a layer."""
+    bs = cuda_lib
+    from fp8_quantized_gemm_q4_gb300.decode import DecodeAttention, fp4_linear
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    Hq, Hkv, D, hidden = 4, 2, 64, 256
+    raw = [(torch.randn(n, k, device=DEV, generator=gen) * 2.0 ** -9).to(torch.bfloat16)
+           for n, k in (((Hq + 2 * Hkv) * D, hidden), (hidden, Hq * D))]
+    two = [bs.q4_quantize_two_level(w) for w in raw]
+    x = torch.randn(40, hidden, device=DEV, generator=gen).to(torch.bfloat16)
+    codes, sf, ts = two[0]
+    assert float(ts) != 1.0
+    assert off(fp4_linear(x[:9], codes, sf, tensor_scale=ts), x[:9], two[0], float(ts)) <= 1
+    # a power of two on the product is exact: few tokens and many against the same without it
+    for n in (9, 40):
+        plain = fp4_linear(x[:n], codes, sf)
+        assert torch.equal(fp4_linear(x[:n], codes, sf, tensor_scale=ts), plain * ts.to(torch.bfloat16))
+    a = DecodeAttention(*two, Hq, Hkv, D, 2, 12, 16, 6)
+    bs.clear_device_status()
+    y = a.step(x[:13], i32([9, 4]), 9)
+    q, k, v = fp4_linear(x[:13], codes, sf, tensor_scale=ts).split([Hq * D, Hkv * D, Hkv * D], 1)
+    table = ref.e4m3_table().to(DEV)
+    kk, vv = (table[c.long()] * s.double()[..., None, None] for c, s in ((a.cache.k, a.cache.k_scale), (a.cache.v, a.cache.v_scale)))
+    o, _, A, S = ref.attention(q.reshape(13, Hq, D).double(), kk, vv, a.table.tolist(), [0, 9, 13], [9, 4], 16, D ** -0.5)
+    do = 2.0 ** -8 * o.abs() + (2.0 ** -11 + (D + 16) * 2.0 ** -23 * S[..., None]) * A + 9 * 2.0 ** -25 * 448 * float(a.cache.v_scale.max())
+    W = ref.fp4_weights(*two[1][:2], hidden, Hq * D).to(DEV) * float(two[1][2])
+    o, do = o.reshape(13, -1), do.reshape(13, -1)
+    bound = (do + (Hq * D + 8) * 2.0 ** -24 * (o.abs() + do)) @ W.abs().T * (1 + 2.0 ** -8) + 2.0 ** -8 * (o @ W.T).abs() + 1e-30
+    assert bool(((y.double() - o @ W.T).abs() <= bound).all())
+    y = a.step(x, i32([20, 20]), 20)     # more than 16 tokens
+    assert bool(y.isfinite().all()) and a.lens.tolist() == [29, 24] and bs.device_status()[0] == bs.BS_OK
