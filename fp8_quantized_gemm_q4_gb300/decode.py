@@ -7,7 +7,7 @@ token, a few drafted ones, or none):
   2. bs_fp4_matvec    q, k and v of the new tokens in one product with the
                       concatenated FP4 weights, x left in bf16 (at most 16
                       tokens; more go through q4_quantize and bs_gemm with the
-                      same weights)
+                      same weights, unless ``activations`` says otherwise)
   3. bs_kv_append     k and v, read where the product left them, to 8 bits in
                       their slots
   4. bs_kv_attention  q over each request's cached tokens, causal
@@ -33,20 +33,31 @@ from . import (KVCache, gemm_fp4, kv_append, kv_attention, kv_attention_workspac
 MATVEC_ROWS = 16   # the most rows that bs_fp4_matvec takes
 
 
-def fp4_linear(x, codes, sf, out=None, tensor_scale=None):
+def fp4_linear(x, codes, sf, out=None, tensor_scale=None, activations="auto"):
     """x bf16 [T, K] times FP4 weights (codes [N, K/2] and scales of q4_quantize, or
-    with ``tensor_scale`` of q4_quantize_two_level).  bs_gemm takes N in multiples of 128; other weights are multiplied 16 rows of x
-    at a time."""
-    if x.shape[0] <= MATVEC_ROWS:
+    with ``tensor_scale`` of q4_quantize_two_level).
+
+    activations  "bf16": x as it is, 16 rows at a time, so that a row's result does
+                 not depend on how many are beside it; "fp4": x quantized, whatever
+                 their number; "auto": bf16 up to 16 rows, FP4 from 17 on, the
+                 faster for each, at the price of x's rounding to FP4 for the
+                 rows of a larger call.  bs_gemm takes N in multiples of 128: other
+                 weights always meet x in bf16 (and "fp4" is refused)."""
+    T, N = x.shape[0], codes.shape[0]
+    if activations not in ("auto", "bf16", "fp4"):
+        raise ValueError(f"activations are auto, bf16 or fp4, not {activations!r}")
+    if activations == "fp4" and N % 128:
+        raise ValueError(f"fp4 activations: {N} columns are no multiple of 128")
+    if activations == "fp4" or (activations == "auto" and T > MATVEC_ROWS and N % 128 == 0):
+        xc, xsf, _ = q4_quantize(x)
+        return gemm_fp4(xc, xsf, codes, sf, x.shape[1], out=out, b_tensor_scale=tensor_scale)
+    if T <= MATVEC_ROWS:
         return matvec_fp4(x, codes, sf, out=out, tensor_scale=tensor_scale)
-    if codes.shape[0] % 128:
-        if out is None:
-            out = torch.empty((x.shape[0], codes.shape[0]), dtype=torch.bfloat16, device=x.device)
-        for at in range(0, x.shape[0], MATVEC_ROWS):
-            matvec_fp4(x[at:at + MATVEC_ROWS], codes, sf, out=out[at:at + MATVEC_ROWS], tensor_scale=tensor_scale)
-        return out
-    xc, xsf, _ = q4_quantize(x)
-    return gemm_fp4(xc, xsf, codes, sf, x.shape[1], out=out, b_tensor_scale=tensor_scale)
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+    for at in range(0, T, MATVEC_ROWS):
+        matvec_fp4(x[at:at + MATVEC_ROWS], codes, sf, out=out[at:at + MATVEC_ROWS], tensor_scale=tensor_scale)
+    return out
 
 
 class DecodeAttention:
@@ -56,16 +67,24 @@ class DecodeAttention:
                     of q4_quantize_two_level, for bf16 weights
                     [(Hq + 2 Hkv) D, hidden] (rows of q, then k, then v) and
                     [hidden, Hq D]
+    activations     of the two products, as fp4_linear takes them.  With "auto" the
+                    same token gets coarser q, k, v and output in a step of 17
+                    tokens and more than in a smaller one
     lens            int32 [B], the cached tokens of each request (device)
     n_free          int32 [1], the pages left (device)
     """
 
     def __init__(self, w_qkv, w_out, Hq: int, Hkv: int, D: int, requests: int, num_pages: int, page_size: int,
-                 max_pages: int):
+                 max_pages: int, activations: str = "auto"):
         rows = (Hq + 2 * Hkv) * D
         if w_qkv[0].shape[0] != rows or w_out[0].shape[1] * 2 != Hq * D:
             raise ValueError(f"DecodeAttention: w_qkv has {rows} rows and w_out {Hq * D} columns")
+        if activations not in ("auto", "bf16", "fp4"):
+            raise ValueError(f"DecodeAttention: activations are auto, bf16 or fp4, not {activations!r}")
+        if activations == "fp4" and (rows % 128 or w_out[0].shape[0] % 128):
+            raise ValueError("DecodeAttention: fp4 activations need weights whose rows are multiples of 128")
         dev = w_qkv[0].device
+        self.activations = activations
         self.w_qkv, self.w_out = w_qkv, w_out
         self.Hq, self.Hkv, self.D, self.page_size = Hq, Hkv, D, page_size
         self.cache = KVCache.empty(num_pages, Hkv, page_size, D, device=dev)
@@ -75,10 +94,9 @@ class DecodeAttention:
         self.lens = torch.zeros(requests, dtype=torch.int32, device=dev)
         self.workspace = kv_attention_workspace(D, dev)
 
-    @staticmethod
-    def _linear(x, weight):
+    def _linear(self, x, weight):
         codes, sf, *scale = weight
-        return fp4_linear(x, codes, sf, tensor_scale=scale[0] if scale else None)
+        return fp4_linear(x, codes, sf, tensor_scale=scale[0] if scale else None, activations=self.activations)
 
     def step(self, x, new_lens, max_new: int):
         """x bf16 [T, hidden], the new tokens of request 0, then 1, ..;

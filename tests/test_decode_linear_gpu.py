@@ -84,3 +84,57 @@ def test_two_level_weights(cuda_lib):
     assert bool(((y.double() - o @ W.T).abs() <= bound).all())
     y = a.step(x, i32([20, 20]), 20)     # more than 16 tokens
     assert bool(y.isfinite().all()) and a.lens.tolist() == [29, 24] and bs.device_status()[0] == bs.BS_OK
+
+
+@pytest.mark.parametrize("N,K", [(512, 256), (1024, 4160)])
+def test_activations(cuda_lib, N, K):
+    """Which rows of x are quantized is the caller's choice: "bf16" and "fp4" give a
+    row the same result among few rows and many, "auto" is the one up to 16 rows and the
+    other from 17 on, and those differ by far more than either's own error."""
+    bs = cuda_lib
+    from fp8_quantized_gemm_q4_gb300.decode import fp4_linear
+    gen = torch.Generator(device=DEV).manual_seed(N)
+    w = weights(bs, N, K, gen)
+    x = torch.randn(40, K, device=DEV, generator=gen).to(torch.bfloat16)
+    xc, xsf, _ = bs.q4_quantize(x)
+    rounded = ref.fp4_weights(xc, xsf, 40, K).to(DEV)
+    full = {mode: fp4_linear(x, *w, activations=mode) for mode in ("bf16", "fp4", "auto")}
+    assert off(full["bf16"], x, w) <= 1 and off(full["fp4"], rounded, w) <= 1
+    assert off(full["fp4"], x, w) > 10 and torch.equal(full["auto"], full["fp4"])
+    for n in (1, 3, 8, 16, 17, 33):
+        assert torch.equal(fp4_linear(x[:n], *w, activations="bf16"), full["bf16"][:n])
+        assert off(fp4_linear(x[:n], *w, activations="fp4"), rounded[:n], w) <= 1
+        assert torch.equal(fp4_linear(x[:n], *w), fp4_linear(x[:n], *w, activations="bf16" if n <= 16 else "fp4"))
+
+
+def test_a_token_alone_and_in_a_batch(cuda_lib):
+    """With bf16 activations, the step of request 0 is the same whether two requests run or 20."""
+    bs = cuda_lib
+    from fp8_quantized_gemm_q4_gb300.decode import DecodeAttention
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    Hq, Hkv, D, hidden = 8, 2, 64, 256
+    w = weights(bs, (Hq + 2 * Hkv) * D, hidden, gen), weights(bs, hidden, Hq * D, gen)
+    prompt = torch.randn(20, 5, hidden, device=DEV, generator=gen).to(torch.bfloat16)
+    caches = []
+    for B in (2, 20):
+        a = DecodeAttention(*w, Hq, Hkv, D, B, 64, 16, 3, activations="bf16")
+        a.step(prompt[:B].reshape(-1, hidden), i32([5] * B), 5)
+        a.step(prompt[:B, 0], i32([1] * B), 1)
+        caches.append([(c[int(a.table[0, 0])], s[int(a.table[0, 0])]) for c, s in ((a.cache.k, a.cache.k_scale), (a.cache.v, a.cache.v_scale))])
+    for (c0, s0), (c1, s1) in zip(*caches):
+        assert torch.equal(c0, c1) and torch.equal(s0, s1)
+
+
+def test_refusals(cuda_lib):
+    bs = cuda_lib
+    from fp8_quantized_gemm_q4_gb300.decode import DecodeAttention, fp4_linear
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    w = weights(bs, 320, 192, gen)
+    x = torch.zeros(3, 192, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError):
+        fp4_linear(x, *w, activations="fp4")
+    with pytest.raises(ValueError):
+        fp4_linear(x, *w, activations="fp8")
+    for mode in ("fp4", "bf8"):
+        with pytest.raises(ValueError):
+            DecodeAttention(w, weights(bs, 192, 192, gen), 3, 1, 64, 2, 8, 16, 4, activations=mode)
