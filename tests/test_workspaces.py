@@ -56,3 +56,13 @@ def test_made_in_a_capture(bs):
     c = bs.get(5000)
     bs.state.capturing = False
     assert c.numel() >= 5000 and bs.get(1000) is b
+
+
+def test_stream_handle_without_the_raw_one(monkeypatch):
+    """A torch without the function that gives the bare handle."""
+    import fp8_quantized_gemm_q4_gb300 as bs
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(bs, "_raw_stream", None, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: types.SimpleNamespace(cuda_stream=11))
+    assert bs._stream() == 11
+    assert bs._stream(types.SimpleNamespace(cuda_stream=5)) == 5
