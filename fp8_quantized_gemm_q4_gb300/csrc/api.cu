@@ -1210,8 +1210,8 @@ bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
   if (!(a->softmax_scale > 0.0f)) return fail(BS_ERR_INVALID, "kv_attention: softmax_scale=%g", (double)a->softmax_scale);
   if (a->wait_timeout_us < 0) return fail(BS_ERR_INVALID, "kv_attention: wait_timeout_us=%d", a->wait_timeout_us);
   if (a->ld_table < a->max_pages) return fail(BS_ERR_INVALID, "kv_attention: ld_table=%lld below max_pages", (long long)a->ld_table);
-  if ((int64_t)a->max_pages * a->page_size > INT32_MAX)
-    return fail(BS_ERR_INVALID, "kv_attention: max_pages=%d pages of %d tokens pass 2^31", a->max_pages, a->page_size);
+  if ((int64_t)a->max_pages * a->page_size > INT32_MAX - 127)  // lengths are rounded up to tiles in 32 bits
+    return fail(BS_ERR_INVALID, "kv_attention: max_pages=%d pages of %d tokens pass 2^31 - 128", a->max_pages, a->page_size);
   if (a->T == 0 || a->B == 0) return BS_OK;
   if (!a->q || !a->out || !a->cu_q || !a->kv_lens || (a->max_pages > 0 && !a->block_table) ||
       (a->num_pages > 0 && (!a->k_codes || !a->v_codes || !a->k_scales || !a->v_scales)))

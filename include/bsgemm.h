@@ -636,7 +636,8 @@ bs_status bs_kv_append(const bs_kv_append_args *args, bs_stream_t stream);
  *              (taken as that)
  *   max_q_len  an upper bound of the rows of a request (0: no bound known, T)
  *   block_table int32 [B, ld_table]; an id outside [0, num_pages) on a seen
- *              page sets BS_ERR_OFFSETS, the page is left out
+ *              page sets BS_ERR_OFFSETS, the page is left out;
+ *              max_pages * page_size <= 2^31 - 128
  *   softmax_scale > 0
  *   workspace  device scratch of bs_kv_attention_workspace_bytes(args) bytes,
  *              with the conventions of bs_gemm_args.workspace (one buffer may

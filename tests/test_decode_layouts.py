@@ -41,3 +41,21 @@ def test_sizes_and_layouts(bs):
         bs.kv_plan(i32(2), i32(2), i32(2, 3), i32(9), i32(1), 16, 4, out=(*out[:3], i32(0)))
     with pytest.raises(ValueError):
         bs.kv_release(i32(2), i32(2), i32(2, 3), i32(9), i32(0), 16)
+
+
+def test_longest_table():
+    """Lengths that pass 2^31 when they are rounded up to a tile are refused (host side; nothing is launched)."""
+    import __graft_entry__
+    __graft_entry__.build()
+    import fp8_quantized_gemm_q4_gb300 as bs
+    F = 1 << 20
+
+    def call(max_pages, page):
+        return bs.load().bs_kv_attention(bs._KV_ATTENTION_ARGS.pack(
+            F, 4096, 128, F, 4096, 128, F, F, F, F, F, 100, page, F, max_pages, max_pages, F, F, 0, 4, 32, 8, 128, 1, 0.1, 0,
+            0, 0), None)
+
+    for page in (16, 32, 64, 128):
+        most = ((1 << 31) - 128) // page
+        assert call(most, page) == bs.BS_OK                 # no requests: nothing to do
+        assert call(most + 1, page) == bs.BS_ERR_INVALID
