@@ -716,7 +716,7 @@ def kv_attention_workspace(D: int, device=None):
 
 
 def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_scale: float | None = None, out=None,
-                 lse=None, workspace=None, stream=None):
+                 lse=None, stream=None, workspace=None):
     """Causal attention of new tokens q bf16 [T, Hq, D] over the 8-bit cache
     (their own keys and values appended first).  ``lse`` (fp32 [T, Hq], natural
     log) is filled if given.  ``workspace`` from kv_attention_workspace, or the

@@ -59,3 +59,20 @@ def test_longest_table():
         most = ((1 << 31) - 128) // page
         assert call(most, page) == bs.BS_OK                 # no requests: nothing to do
         assert call(most + 1, page) == bs.BS_ERR_INVALID
+
+
+def test_arguments_by_position():
+    """What calls pass by position stays where it was; later arguments are added at the end."""
+    import inspect
+
+    import fp8_quantized_gemm_q4_gb300 as bs
+    from fp8_quantized_gemm_q4_gb300 import decode
+
+    def names(f):
+        return list(inspect.signature(f).parameters)
+
+    assert names(bs.kv_attention)[:10] == ["q", "cache", "block_table", "cu_q", "kv_lens", "max_q_len", "softmax_scale", "out",
+                                           "lse", "stream"]
+    assert names(decode.fp4_linear)[:4] == ["x", "codes", "sf", "out"]
+    assert names(decode.DecodeAttention)[:9] == ["w_qkv", "w_out", "Hq", "Hkv", "D", "requests", "num_pages", "page_size",
+                                                 "max_pages"]
