@@ -351,7 +351,7 @@ struct KvAttentionParams {
 };
 struct KvAttentionLaunch {
   KvAttentionParams p;
-  CUtensorMap tm_k, tm_v; // codes [pages * Hkv * page, D], box kv_attention_box rows x D
+  CUtensorMap tm_k, tm_v; // codes as rows of 128 bytes, box kv_attention_box tokens
   int few_grid, rows_grid;
 };
 int kv_attention_few_grid(int sms);

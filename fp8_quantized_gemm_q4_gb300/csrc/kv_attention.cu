@@ -125,8 +125,9 @@ __device__ __forceinline__ void softmax_step(float (&u)[4], float inv_sv, float 
 // first, whose tiles they find in L2.
 // 64 requests of 500 to 16000 tokens, 32 heads over 8, D = 128 (604 MB): 105 us, 0.85
 // of HBM.  63 drafted tokens of 16 requests, 16 heads, D = 64, 16-token pages (60 MB):
-// 23 us, bound by what a unit costs beside its tiles (q, the join of the warps, its
-// piece); one token over 1000: 10 us, a chain of dependent reads.
+// 24 us, bound by what a unit costs beside its tiles (q, the join of the warps, its
+// piece); one token over 1000: 10 us, a chain of dependent reads.  Three CTAs an SM
+// leave 128 registers a thread, of which 16 to 20 bytes are spilled.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 64;          // cached tokens per stage
 constexpr int kItems = 32;         // units listed at a time

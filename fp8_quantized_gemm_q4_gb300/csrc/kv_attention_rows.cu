@@ -19,9 +19,10 @@
 //   warp 25      the next units, page ids and scales of the next tiles
 // What bounds it: the softmax of a tile, whose steps follow one another (S, the
 // maximum, the vote on the reference, the exponentials, the store) and whose
-// warps have 1480 issue slots of about 2900 clocks a tile with the converters.
-// B = 2, 2048 rows x 32 heads over 4000 to 8000 tokens, D = 128: 276 us (808 TFLOP/s);
-// before the pieces' layout below 287, with two threads per row 303, with one 2.5 times the MMAs' time.  Also built and
+// warps have 1540 issue slots of about 2800 clocks a tile with the converters.  832
+// threads leave 72 registers each, 20 bytes of which are spilled.
+// B = 2, 2048 rows x 32 heads over 4000 to 8000 tokens, D = 128: 265 us (840 TFLOP/s); the
+// same with D = 64, half the MMAs: 225.  With two threads per row 303, with one 2.5 times the MMAs' time.  Also built and
 // measured: two groups of warps on alternate tiles, each with an O of its own and
 // Q in shared memory (303 us: both operands of Q K^T from shared memory take all of
 // its bandwidth), with one O and a reference settled in turn (324 us: P in S's place

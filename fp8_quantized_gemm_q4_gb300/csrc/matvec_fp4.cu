@@ -7,7 +7,7 @@
 // scale has at most 6 significant bits and lies in [2^-10, 2688], so it is
 // exact in fp16; x is brought to fp16 by a power of two per row that puts the
 // largest element in [2^14, 2^15): exact for every element within 2^-29 of it,
-// and 2^-40 of it is the error of the others.  The products go through mma.sync
+// and 2^-39 of it bounds the error of the others.  The products go through mma.sync
 // m16n8k16 with 16 weight rows on its M and 8 (or 2 x 8) x rows on its N,
 // accumulated in fp32.  With so few rows tcgen05 has nothing to gain: its
 // M = 128 tile takes the same 64 clocks per 16 of K for 16 columns as for 128,
@@ -35,7 +35,11 @@
 //   M = 4,  N = 10000, K = 4096 (4)  10.2 / 12.6   M = 16, 7168 x 4096 (3)     11.8 / 12.8
 //   M = 8,  N = 20000, K = 4096 (8)  16.0 / 15.5   M = 16, 28672 x 4096 (12)   26.1 / 22.8
 //   M = 8,  N = 40960, K = 7168 (17)   53 / 35     M = 16, 40960 x 7168 (17)     73 / 48
-// So: many from 8 tiles per SM on, and for K above 4096.
+// So: many from 8 tiles per SM on, and for K above 4096.  At 16 rows neither HBM
+// (0.48), the issue slots (0.47) nor the tensor pipe (0.33) is full: four warps a
+// scheduler wait for their own chains from ring to product.  Registers are at their
+// limit of 128; 144 bytes a thread are spilled in the first kernel at 9 to 16 rows, 36
+// in the second.
 #include "kernels.h"
 #include "ptx.cuh"
 

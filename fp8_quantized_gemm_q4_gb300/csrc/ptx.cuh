@@ -436,8 +436,7 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t code) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(in));
   return __half2float(__ushort_as_half(static_cast<unsigned short>(h2 & 0xFFFFu)));
 }
-// The two e4m3 codes of a 16-bit word / the two E2M1 codes of a byte as fp16
-// (exact: both formats are subsets of fp16), low code in the low half.
+// The two e4m3 codes of a 16-bit word as fp16 (exact), low code in the low half.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t codes) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(codes));
@@ -451,15 +450,6 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t
       "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}\n"
       : "=r"(lo), "=r"(hi)
       : "r"(w));
-}
-__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t}\n"
-      : "=r"(r)
-      : "r"(byte));
-  return r;
 }
 // Eight fp32 values to eight E2M1 codes packed in a word, element i in
 // nibble i (bits 4i..4i+3).

@@ -101,8 +101,9 @@ class DecodeAttention:
     def step(self, x, new_lens, max_new: int):
         """x bf16 [T, hidden], the new tokens of request 0, then 1, ..;
         new_lens int32 [B] on the device, their sum at most T, each at most
-        max_new.  Returns bf16 [T, hidden].  A request for which the pages do not
-        suffice gets zeros and keeps its length (device status BS_ERR_PAGES)."""
+        max_new.  Returns bf16 [T, hidden]; rows past the sum of new_lens hold
+        nothing of use.  A request for which the pages do not suffice gets zeros
+        and keeps its length (device status BS_ERR_PAGES)."""
         T, q_rows, kv_rows = x.shape[0], self.Hq * self.D, self.Hkv * self.D
         cu, kv_lens, slots, left = kv_plan(self.lens, new_lens, self.table, self.free, self.n_free, self.page_size, T)
         qkv = self._linear(x, self.w_qkv)

@@ -579,9 +579,10 @@ bs_status bs_kv_release(const int32_t *lens, const int32_t *done, int B, int32_t
 
 /* ---------------------------------------------------------------------------
  * bs_kv_append -- quantize new keys and values into their slots.
- * The rows that go into one page follow one another with ascending slots (as
- * bs_kv_plan gives them); amax is taken over those rows and D, per head, for
- * keys and values apart:
+ * The rows that go into one page follow one another with consecutive slots (as
+ * bs_kv_plan gives them; a page that a call names twice apart, with a gap or a
+ * skipped row between, gets one part's scale and codes rounded to either's);
+ * amax is taken over those rows and D, per head, for keys and values apart:
  *     s    = the smallest power of two in [2^-32, 2^64] with amax <= 448 s
  *     if the first of the rows is not the page's first token: s = max(s, the
  *     page's scale), and where s grew, the page's earlier codes become
@@ -634,14 +635,17 @@ bs_status bs_kv_append(const bs_kv_append_args *args, bs_stream_t stream);
  *              touched, a request with a negative or descending pair has no rows.
  *              So does a length below 0 (taken as 0) or above max_pages * page_size
  *              (taken as that)
- *   max_q_len  an upper bound of the rows of a request (0: no bound known, T)
+ *   max_q_len  an upper bound of the rows of a request (0: no bound known, T); a
+ *              request with more sets BS_ERR_OFFSETS, and its rows may not be written
  *   block_table int32 [B, ld_table]; an id outside [0, num_pages) on a seen
  *              page sets BS_ERR_OFFSETS, the page is left out;
  *              max_pages * page_size <= 2^31 - 128
  *   softmax_scale > 0
  *   workspace  device scratch of bs_kv_attention_workspace_bytes(args) bytes,
  *              with the conventions of bs_gemm_args.workspace (one buffer may
- *              serve both)
+ *              serve both).  The size depends on D and on whether a request may
+ *              have many rows; it is largest for T = 2^20, Hq = Hkv = 1,
+ *              max_q_len = 0, which serves every call of that D
  * ------------------------------------------------------------------------- */
 typedef struct {
     const void *q;
