@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "bsgemm.h"
+#include "decode.h"
 #include "kernels.h"
 
 static_assert(BS_MOE_DISPATCH_NOALLOC_MAX_BYTES == bsk::kNoAllocDispatchScratchBytes,

@@ -1,7 +1,7 @@
 // kv_attention.cuh -- what the two attention kernels over the 8-bit cache share.
 #pragma once
-#include "kernels.h"
-#include "ptx.cuh"
+#include "decode.cuh"
+#include "decode.h"
 
 namespace bsk {
 

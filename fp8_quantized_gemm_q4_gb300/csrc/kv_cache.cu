@@ -6,8 +6,8 @@
 // one fp32 power-of-two scale per (page, KV head).
 #include <limits.h>
 
-#include "kernels.h"
-#include "ptx.cuh"
+#include "decode.cuh"
+#include "decode.h"
 
 namespace bsk {
 

@@ -40,8 +40,8 @@
 // scheduler wait for their own chains from ring to product.  Registers are at their
 // limit of 128; 144 bytes a thread are spilled in the first kernel at 9 to 16 rows, 36
 // in the second.
-#include "kernels.h"
-#include "ptx.cuh"
+#include "decode.cuh"
+#include "decode.h"
 
 namespace bsk {
 namespace {

@@ -10,7 +10,6 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -19,7 +18,6 @@ namespace bsk {
 // Device status word codes (mirror bs_status in bsgemm.h).
 constexpr int kStatusTimeout = 5;
 constexpr int kStatusOffsets = 6;
-constexpr int kStatusPages = 7;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -435,21 +433,6 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t code) {
   uint16_t in = static_cast<uint16_t>(code & 0xFFu);
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(in));
   return __half2float(__ushort_as_half(static_cast<unsigned short>(h2 & 0xFFFFu)));
-}
-// The two e4m3 codes of a 16-bit word as fp16 (exact), low code in the low half.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t codes) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(codes));
-  return r;
-}
-// Four bytes of e4m3 as two f16x2
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\t"
-      "mov.b32 {a, b}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}\n"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
 }
 // Eight fp32 values to eight E2M1 codes packed in a word, element i in
 // nibble i (bits 4i..4i+3).
