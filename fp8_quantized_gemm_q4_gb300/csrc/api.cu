@@ -1078,11 +1078,13 @@ bs_status bs_kv_plan(const bs_kv_plan_args* a, bs_stream_t stream) {
   if (ld_table < max_pages) return fail(BS_ERR_INVALID, "kv_plan: ld_table=%lld below max_pages", (long long)ld_table);
   if ((int64_t)max_pages * page_size > INT32_MAX)
     return fail(BS_ERR_INVALID, "kv_plan: max_pages=%d pages of %d tokens pass 2^31", max_pages, page_size);
-  if (n_free_out == n_free || kv_lens == seq_lens || kv_lens == new_lens)
-    return fail(BS_ERR_INVALID, "kv_plan: n_free_out / kv_lens must not be an input buffer");
   if (!aligned4(seq_lens) || !aligned4(new_lens) || !aligned4(block_table) || !aligned4(free_pages) ||
       !aligned4(n_free) || !aligned4(cu_new) || !aligned4(kv_lens) || !aligned4(slots) || !aligned4(n_free_out))
     return fail(BS_ERR_ALIGN, "kv_plan: buffers must be 4-byte aligned");
+  // every CTA reads the inputs, while others write these
+  for (const int32_t* out : {cu_new, kv_lens, slots, n_free_out})
+    for (const int32_t* in : {seq_lens, new_lens, free_pages, n_free})
+      if (out && out == in) return fail(BS_ERR_INVALID, "kv_plan: an output buffer is an input buffer");
   if (!device_info(&p.status, nullptr)) return fail(BS_ERR_CUDA, "no current device");
   p.seq_lens = seq_lens;
   p.new_lens = new_lens;

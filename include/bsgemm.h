@@ -550,7 +550,7 @@ bs_status bs_moe_combine(const float *rows, int64_t ld_rows, const int32_t *pair
  *   free_pages  int32 [free_capacity]; n_free device int32 (clamped to
  *               [0, free_capacity])
  *   T           entries of slots; cu_new[B] > T sets BS_ERR_OFFSETS
- *   n_free_out, kv_lens must not be input buffers (BS_ERR_INVALID)
+ *   cu_new, kv_lens, slots and n_free_out must not be input buffers (BS_ERR_INVALID)
  * Negative lengths, or more pages than max_pages, set BS_ERR_OFFSETS; such a
  * request takes no pages and gets kv_lens 0 and slots -1.
  *

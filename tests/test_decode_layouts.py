@@ -76,3 +76,18 @@ def test_arguments_by_position():
     assert names(decode.fp4_linear)[:4] == ["x", "codes", "sf", "out"]
     assert names(decode.DecodeAttention)[:9] == ["w_qkv", "w_out", "Hq", "Hkv", "D", "requests", "num_pages", "page_size",
                                                  "max_pages"]
+
+
+def test_plan_outputs_apart_from_inputs():
+    """An output of kv_plan at the address of an input that all its CTAs read is refused (host side)."""
+    import __graft_entry__
+    __graft_entry__.build()
+    import fp8_quantized_gemm_q4_gb300 as bs
+    F = 1 << 20
+    #        seq  new       B table    ld w free      n_free   cap page T  cu        kv        slots     left
+    good = [F, F + 64, 4, F + 128, 8, 8, F + 192, F + 256, 32, 64, 10, F + 320, F + 512, F + 640, F + 1024]
+    for out in (11, 12, 13, 14):
+        for src in (0, 1, 6, 7):
+            a = list(good)
+            a[out] = a[src]
+            assert bs.load().bs_kv_plan(bs._KV_PLAN_ARGS.pack(*a), None) == bs.BS_ERR_INVALID, (out, src)
