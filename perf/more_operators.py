@@ -224,8 +224,7 @@ def _own(op, s):
     import fp8_quantized_gemm_q4_gb300 as bs
     c = s["c"]
     if op == "adapters":
-        return bs.lora_add(s["x"], s["y"], s["a"], s["b"], s["cu"], s["which"], s["max_rows"], scales=s["scale"],
-                           out=s["out"])
+        return bs.lora_add(s["x"], s["y"], s["a"], s["b"], s["cu"], s["which"], scales=s["scale"], out=s["out"])
     if op == "attention4":
         cache = bs.KVCacheFP4(*s["cache"])
         bs.kv_attention(s["q"], cache, s["table"], s["cu"], s["kv"], s["max_q"], out=s["out"], lse=s["lse"])
