@@ -23,7 +23,7 @@ from ._build import LIB as _LIB_PATH
 
 __all__ = [
     "load", "sf_bytes", "sf_offset", "q4_quantize", "tensor_amax", "q4_quantize_two_level", "fp4_gather_rows", "fp8_gather_rows", "q8_quantize", "gemm_fp4", "gemm_fp8", "gemm_fp8_multi", "gemm_fp4_multi",
-    "grouped_gemm_fp4", "grouped_gemm_fp4_swiglu_q4", "grouped_gemm_fp8", "moe_router_topk", "moe_dispatch", "moe_finalize", "moe_combine", "moe_rows_bound", "kv_plan", "kv_release", "kv_append", "kv_attention", "kv_attention_workspace", "matvec_fp4", "KVCache", "device_status",
+    "grouped_gemm_fp4", "grouped_gemm_fp4_swiglu_q4", "grouped_gemm_fp8", "moe_router_topk", "moe_dispatch", "moe_finalize", "moe_combine", "moe_rows_bound", "kv_plan", "kv_release", "kv_append", "kv_append_rotary", "kv_gather", "kv_attention", "kv_attention_workspace", "matvec_fp4", "lora_add", "rotary_angles", "KVCache", "KVCacheFP4", "device_status",
     "clear_device_status", "BSError", "EPI_STORE", "EPI_SWIGLU", "EPI_COMBINE", "EPI_ROWS", "kernel_options",
     "current_kernel_options", "FP4_ONE_CTA", "FP4_PAIR",
 ]
@@ -62,6 +62,9 @@ _KV_PLAN_ARGS = struct.Struct("PPiPqiPPiiqPPPP")
 _FP4_MATVEC_ARGS = struct.Struct("PqiPPqqfPPPiq")
 _KV_APPEND_ARGS = struct.Struct("PPiqiiqqqqPPPPPqi4x")
 _KV_ATTENTION_ARGS = struct.Struct("PqqPqqPPPPPqiPqiPPiqiiiifiPN")
+_KV_APPEND_ROTARY_ARGS = struct.Struct("PqqPqqPPiiiiqqqqqPPPqiiiiPPPPq")
+_KV_GATHER_ARGS = struct.Struct("PqiiPPqqqqiiPPPPq")
+_LORA_ARGS = struct.Struct("PqPPPPPPqPqiiqqqiiPN")
 
 
 # Per-call kernel choices of bs_gemm_args (0 = the library's default), see
@@ -166,6 +169,16 @@ def load(path: str | None = None):
         lib.bs_kv_attention_workspace_bytes.argtypes = [ctypes.c_char_p]
         lib.bs_kv_attention.restype = I
         lib.bs_kv_attention.argtypes = [ctypes.c_char_p, P]
+        lib.bs_kv_attention_fp4.restype = I
+        lib.bs_kv_attention_fp4.argtypes = [ctypes.c_char_p, P, P, P]
+        lib.bs_kv_append_rotary.restype = I
+        lib.bs_kv_append_rotary.argtypes = [ctypes.c_char_p, P]
+        lib.bs_kv_gather.restype = I
+        lib.bs_kv_gather.argtypes = [ctypes.c_char_p, P]
+        lib.bs_lora_workspace_bytes.restype = SZ
+        lib.bs_lora_workspace_bytes.argtypes = [ctypes.c_char_p]
+        lib.bs_lora_add.restype = I
+        lib.bs_lora_add.argtypes = [ctypes.c_char_p, P]
         lib.bs_fp4_matvec.restype = I
         lib.bs_fp4_matvec.argtypes = [ctypes.c_char_p, P]
         lib.bs_get_device_status.restype = I
@@ -576,6 +589,22 @@ class KVCache(NamedTuple):
                    torch.ones(shape[:2], dtype=torch.float32, device=device))
 
 
+class KVCacheFP4(NamedTuple):
+    """One layer's 4-bit paged cache: E2M1 codes uint8 [pages, Hkv, page_size,
+    D / 2] (two a byte) and e4m3 scales uint8 [pages, Hkv, page_size, D / 16] of
+    keys and values."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    @classmethod
+    def empty(cls, num_pages: int, Hkv: int, page_size: int, D: int, device="cuda") -> "KVCacheFP4":
+        shape = (num_pages, Hkv, page_size)
+        return cls(*(torch.zeros((*shape, n), dtype=torch.uint8, device=device)
+                     for n in (D // 2, D // 2, D // 16, D // 16)))
+
+
 # Short names, identities instead of comparisons, one attribute read each: these
 # calls launch kernels of a few microseconds, and their checks cost as much as
 # the launch if they are written at leisure.
@@ -594,6 +623,39 @@ def _check_kv_cache(cache):
     if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
         raise ValueError("KV cache buffers must be contiguous")
     return k, v, ks, vs, shape
+
+
+def _check_kv_cache_fp4(cache):
+    """(k, v, k_scale, v_scale, shape with D) of a KVCacheFP4, checked for type and layout."""
+    k, v, ks, vs = cache
+    shape, groups = k.shape, ks.shape
+    if len(shape) != 4 or v.shape != shape or vs.shape != groups or groups != (*shape[:3], shape[3] // 8):
+        raise ValueError("a 4-bit KV cache is codes [pages, Hkv, page_size, D / 2] and scales [.., D / 16], twice")
+    if k.dtype is not _U8 or v.dtype is not _U8 or ks.dtype is not _U8 or vs.dtype is not _U8:
+        raise TypeError("4-bit KV cache codes and scales are uint8 (E2M1 pairs, e4m3)")
+    if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+        raise ValueError("KV cache buffers must be contiguous")
+    return k, v, ks, vs, (shape[0], shape[1], shape[2], 2 * shape[3])
+
+
+def _placed(name, *tensors):
+    """Refuses tensors that are not on the current GPU, whose stream the call goes to."""
+    here = None
+    for t in tensors:
+        if not t.is_cuda:
+            _not_on_gpu(name)
+        if here is None:
+            here = _device()
+        if t.get_device() != here:
+            raise ValueError(f"{name}: every tensor is on the current GPU (cuda:{here})")
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor of the stream that the call goes to: memory of another stream's may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _not_on_gpu(name):
@@ -666,7 +728,10 @@ def kv_release(lens, done, block_table, free_pages, n_free, page_size: int, stre
 
 def kv_append(k, v, slots, cache, stream=None):
     """Quantize new keys and values [T, Hkv, D] (fp32 or bf16, any token and
-    head strides) into their slots of the 8-bit cache, in place."""
+    head strides) into their slots of the cache (KVCache or KVCacheFP4), in place."""
+    if type(cache) is KVCacheFP4:
+        kv_append_rotary(None, k, v, slots, None, None, cache, stream=stream)
+        return
     kc, vc, ks, vs, (pages, Hkv, page, D) = _check_kv_cache(cache)
     shape = k.shape
     T = slots.numel()
@@ -686,6 +751,98 @@ def kv_append(k, v, slots, cache, stream=None):
                              vt, vh, slots.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(),
                              pages, page)
     _check((_lib or load()).bs_kv_append(a, _stream(stream)))
+
+
+def rotary_angles(max_positions: int, rotary_dim: int, base: float = 10000.0, device="cuda"):
+    """The table that kv_append_rotary reads: cos, then sin, of position *
+    base^(-2 i / rotary_dim), i < rotary_dim / 2, in fp32 (computed in 64 bits)."""
+    f = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device) / rotary_dim)
+    a = torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] * f
+    return torch.cat([a.cos(), a.sin()], 1).float()
+
+
+def kv_append_rotary(q, k, v, slots, positions, angles, cache, q_out=None, interleaved: bool = False, stream=None):
+    """New keys and values [T, Hkv, D] into their slots of the cache (KVCache or
+    KVCacheFP4), in place, and new queries [T, Hq, D] to bf16, queries and keys
+    rotated by the angles (fp32 [max_positions, R], see rotary_angles) of their
+    positions (int32 [T]): pairs i, i + R / 2, or 2 i, 2 i + 1 if ``interleaved``.
+    ``q`` None: keys and values only; ``angles`` None: no rotation.  ``q_out`` may be
+    ``q`` (bf16).  Rows with a negative slot are skipped.  Returns q_out."""
+    fp4 = type(cache) is KVCacheFP4
+    kc, vc, ks, vs, (pages, Hkv, page, D) = (_check_kv_cache_fp4 if fp4 else _check_kv_cache)(cache)
+    shape = k.shape
+    T = slots.numel()
+    if shape != (T, Hkv, D) or v.shape != shape:
+        raise ValueError(f"kv_append_rotary: k and v are [{T}, {Hkv}, {D}] for these slots and this cache")
+    (kt, kh, kd), (vt, vh, vd) = k.stride(), v.stride()
+    dt = k.dtype
+    if kd != 1 or vd != 1 or v.dtype is not dt:
+        raise ValueError("kv_append_rotary: q, k and v have one type and contiguous rows of D")
+    if dt is not _BF16 and dt is not _F32:
+        raise TypeError(f"unsupported dtype {dt}")
+    if slots.dtype is not _I32 or not slots.is_contiguous():
+        raise TypeError("kv_append_rotary: slots is a contiguous int32 tensor")
+    placed = [k, v, slots, kc, vc, ks, vs]
+    if q is None:
+        query = (0, 0, 0, 0, 0, 0)
+        Hq = 0
+        if q_out is not None:
+            raise ValueError("kv_append_rotary: q_out without q")
+    else:
+        if q_out is None:
+            q_out = _empty(q.shape, _BF16, q.device, stream)
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q_out.shape != q.shape:
+            raise ValueError(f"kv_append_rotary: q and q_out are [{T}, Hq, {D}]")
+        Hq = q.shape[1]
+        (qt, qh, qd), (ot, oh, od) = q.stride(), q_out.stride()
+        if qd != 1 or od != 1 or q.dtype is not dt:
+            raise ValueError("kv_append_rotary: q, k and v have one type and contiguous rows of D")
+        if q_out.dtype is not _BF16:
+            raise TypeError("kv_append_rotary: q_out is bfloat16")
+        query = (q.data_ptr(), qt, qh, q_out.data_ptr(), ot, oh)
+        placed += (q, q_out)
+    if angles is None:
+        turn = (0, 0, 0, 0)
+    else:
+        if angles.dtype is not _F32 or angles.dim() != 2 or not angles.is_contiguous():
+            raise TypeError("kv_append_rotary: angles is a contiguous float32 [max_positions, R] tensor")
+        if positions is None or positions.dtype is not _I32 or positions.numel() != T or not positions.is_contiguous():
+            raise TypeError(f"kv_append_rotary: positions is a contiguous int32 tensor of {T}")
+        turn = (positions.data_ptr(), angles.data_ptr(), angles.shape[0], angles.shape[1])
+        placed += (positions, angles)
+    _placed("kv_append_rotary", *placed)
+    at, table, rows, R = turn
+    a = _KV_APPEND_ROTARY_ARGS.pack(*query, k.data_ptr(), v.data_ptr(), DTYPE_BF16 if dt is _BF16 else DTYPE_F32, Hq,
+                                    Hkv, D, T, kt, kh, vt, vh, slots.data_ptr(), at, table, rows, R,
+                                    1 if interleaved else 0, FMT_FP4 if fp4 else FMT_FP8, page, kc.data_ptr(),
+                                    vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages)
+    _check((_lib or load()).bs_kv_append_rotary(a, _stream(stream)))
+    return q_out
+
+
+def kv_gather(cache, slots, out=None, stream=None):
+    """The rows of the cache (KVCache or KVCacheFP4) at these slots as bf16: (k, v),
+    [T, Hkv, D] each.  Rows of negative slots are left as they were (whatever a new
+    tensor holds, without ``out``)."""
+    fp4 = type(cache) is KVCacheFP4
+    kc, vc, ks, vs, (pages, Hkv, page, D) = (_check_kv_cache_fp4 if fp4 else _check_kv_cache)(cache)
+    if slots.dtype is not _I32 or not slots.is_contiguous():
+        raise TypeError("kv_gather: slots is a contiguous int32 tensor")
+    shape = (slots.numel(), Hkv, D)
+    if out is None:
+        out = (_empty(shape, _BF16, kc.device, stream), _empty(shape, _BF16, kc.device, stream))
+    k, v = out
+    (kt, kh, kd), (vt, vh, vd) = k.stride(), v.stride()
+    if k.shape != shape or v.shape != shape or kd != 1 or vd != 1:
+        raise ValueError(f"kv_gather: k and v are {list(shape)} with contiguous rows of D")
+    if k.dtype is not _BF16 or v.dtype is not _BF16:
+        raise TypeError("kv_gather: k and v are bfloat16")
+    _placed("kv_gather", slots, kc, vc, ks, vs, k, v)
+    a = _KV_GATHER_ARGS.pack(slots.data_ptr(), shape[0], Hkv, D, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh,
+                             FMT_FP4 if fp4 else FMT_FP8, page, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(),
+                             vs.data_ptr(), pages)
+    _check((_lib or load()).bs_kv_gather(a, _stream(stream)))
+    return k, v
 
 
 _kv_workspace_sizes: dict = {}   # (device, D) -> bytes
@@ -717,11 +874,12 @@ def kv_attention_workspace(D: int, device=None):
 
 def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_scale: float | None = None, out=None,
                  lse=None, stream=None, workspace=None):
-    """Causal attention of new tokens q bf16 [T, Hq, D] over the 8-bit cache
-    (their own keys and values appended first).  ``lse`` (fp32 [T, Hq], natural
+    """Causal attention of new tokens q bf16 [T, Hq, D] over the cache, KVCache or
+    KVCacheFP4 (their own keys and values appended first).  ``lse`` (fp32 [T, Hq], natural
     log) is filled if given.  ``workspace`` from kv_attention_workspace, or the
     stream's own if None.  Returns out bf16 [T, Hq, D]."""
-    kc, vc, ks, vs, (pages, Hkv, page, D) = _check_kv_cache(cache)
+    fp4 = type(cache) is KVCacheFP4
+    kc, vc, ks, vs, (pages, Hkv, page, D) = _check_kv_cache_fp4(cache) if fp4 else _check_kv_cache(cache)
     shape = q.shape
     if out is None:
         out = torch.empty(shape, dtype=_BF16, device=q.device)
@@ -770,7 +928,11 @@ def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_s
         ws = _workspaces.get((dev, handle))
         if ws is None or ws.numel() < nbytes:
             ws = _workspace_of(q.device, handle, nbytes)
-    _check(lib.bs_kv_attention(_KV_ATTENTION_ARGS.pack(*args, ws.data_ptr(), nbytes), handle))
+    packed = _KV_ATTENTION_ARGS.pack(*args, ws.data_ptr(), nbytes)
+    if fp4:
+        _check(lib.bs_kv_attention_fp4(packed, ks.data_ptr(), vs.data_ptr(), handle))
+    else:
+        _check(lib.bs_kv_attention(packed, handle))
     return out
 
 
@@ -805,6 +967,46 @@ def matvec_fp4(x, codes, sf, out_dtype=torch.bfloat16, alpha: float = 1.0, bias=
                               0 if tensor_scale is None else tensor_scale.data_ptr(),
                               0 if bias is None else bias.data_ptr(), out.data_ptr(), _dt(out), ldo)
     _check((_lib or load()).bs_fp4_matvec(a, _stream(stream)))
+    return out
+
+
+def lora_add(x, y, a, b, cu_rows, which, scales=None, out=None, stream=None):
+    """y + scale x A^T B^T with the low-rank adapter of each request, beside a
+    projection y [T, N] (bf16 or fp32) of x bf16 [T, K] that all share.  ``a`` bf16
+    [adapters, r, K], ``b`` bf16 [adapters, N, r], ``scales`` fp32 [adapters] or None
+    (1); request b has the rows cu_rows[b] .. cu_rows[b + 1] - 1 (int32 [B + 1], as
+    kv_plan gives them) and the adapter which[b] (int32 [B]; negative: none).  ``out``
+    may be ``y``; rows from cu_rows[B] on are not written.  Returns out."""
+    if x.dim() != 2 or y.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("lora_add: x [T, K], y [T, N], a [adapters, r, K], b [adapters, N, r]")
+    (T, K), N, (n, r, _) = x.shape, y.shape[1], a.shape
+    if out is None:
+        out = _empty(y.shape, y.dtype, y.device, stream)
+    if y.shape[0] != T or a.shape[2] != K or b.shape != (n, N, r) or out.shape != y.shape:
+        raise ValueError("lora_add: x [T, K], y and out [T, N], a [adapters, r, K], b [adapters, N, r]")
+    if x.dtype is not _BF16 or a.dtype is not _BF16 or b.dtype is not _BF16:
+        raise TypeError("lora_add: x, a and b are bfloat16")
+    if out.dtype is not y.dtype:
+        raise TypeError("lora_add: y and out have one type")
+    (ldx, x1), (ldy, y1), (ldo, o1) = x.stride(), y.stride(), out.stride()
+    if x1 != 1 or y1 != 1 or o1 != 1 or not a.is_contiguous() or not b.is_contiguous():
+        raise ValueError("lora_add: rows of x, y and out, and all of a and b, are contiguous")
+    _ints("lora_add", cu_rows, which)
+    B = which.numel()
+    if cu_rows.numel() != B + 1:
+        raise ValueError("lora_add: cu_rows is [B + 1] and which [B]")
+    placed = (x, y, a, b, cu_rows, which, out)
+    if scales is not None:
+        if scales.dtype is not _F32 or scales.numel() != n or not scales.is_contiguous():
+            raise TypeError(f"lora_add: scales is a contiguous float32 tensor of {n}")
+        placed += (scales,)
+    _placed("lora_add", *placed)
+    lib = _lib or load()
+    args = (x.data_ptr(), ldx, a.data_ptr(), b.data_ptr(), 0 if scales is None else scales.data_ptr(),
+            cu_rows.data_ptr(), which.data_ptr(), y.data_ptr(), ldy, out.data_ptr(), ldo, _dt(y), B, T, K, N, r, n)
+    nbytes = int(lib.bs_lora_workspace_bytes(_LORA_ARGS.pack(*args, 0, 0)))
+    ws = _empty(max(nbytes, 16), _U8, x.device, stream)
+    _check(lib.bs_lora_add(_LORA_ARGS.pack(*args, ws.data_ptr(), nbytes), _stream(stream)))
     return out
 
 

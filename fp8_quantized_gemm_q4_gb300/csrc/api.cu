@@ -1201,8 +1201,9 @@ size_t bs_kv_attention_workspace_bytes(const bs_kv_attention_args* a) {
   return kStreamKCounterBytes + (many && rows > few ? rows : few);
 }
 
-bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
-  if (!a) return fail(BS_ERR_INVALID, "kv_attention: null arguments");
+// Over the 8-bit cache, or (fp4) the 4-bit one with these scales.
+static bs_status kv_attention(const bs_kv_attention_args* a, bool fp4, const void* k_scales, const void* v_scales,
+                              bs_stream_t stream) {
   bs_status st = check_kv_cache("kv_attention", a->Hkv, a->D, a->num_pages, a->page_size);
   if (st != BS_OK) return st;
   if (a->T < 0 || a->T > INT32_MAX || a->B < 0 || a->max_q_len < 0 || a->max_pages < 0)
@@ -1217,16 +1218,18 @@ bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
     return fail(BS_ERR_INVALID, "kv_attention: max_pages=%d pages of %d tokens pass 2^31 - 128", a->max_pages, a->page_size);
   if (a->T == 0 || a->B == 0) return BS_OK;
   if (!a->q || !a->out || !a->cu_q || !a->kv_lens || (a->max_pages > 0 && !a->block_table) ||
-      (a->num_pages > 0 && (!a->k_codes || !a->v_codes || !a->k_scales || !a->v_scales)))
+      (a->num_pages > 0 && (!a->k_codes || !a->v_codes || !k_scales || !v_scales)))
     return fail(BS_ERR_INVALID, "kv_attention: null pointer");
   int64_t strides = 0;  // those of an axis of length 1 mean nothing
   if (a->T > 1) strides |= a->q_token_stride | a->out_token_stride;
   if (a->Hq > 1) strides |= a->q_head_stride | a->out_head_stride;
   if (strides % 8 || !aligned16(a->q) ||
-      !aligned16(a->out) || !aligned16(a->k_codes) || !aligned16(a->v_codes) || !aligned4(a->k_scales) ||
-      !aligned4(a->v_scales) || !aligned4(a->block_table) || !aligned4(a->cu_q) || !aligned4(a->kv_lens) ||
+      !aligned16(a->out) || !aligned16(a->k_codes) || !aligned16(a->v_codes) || !aligned4(k_scales) ||
+      !aligned4(v_scales) || !aligned4(a->block_table) || !aligned4(a->cu_q) || !aligned4(a->kv_lens) ||
       !aligned4(a->lse))
     return fail(BS_ERR_ALIGN, "kv_attention: q, out and codes must be 16-byte aligned, strides multiples of 8 elements");
+  if (fp4 && (!aligned16(k_scales) || !aligned16(v_scales)))
+    return fail(BS_ERR_ALIGN, "kv_attention: the scales of a 4-bit cache must be 16-byte aligned");
   bsk::KvAttentionLaunch L;
   memset(&L, 0, sizeof L);
   bsk::KvAttentionParams& p = L.p;
@@ -1237,9 +1240,10 @@ bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
     return fail(BS_ERR_INVALID, "kv_attention: workspace of %zu bytes, %zu needed", a->workspace ? a->workspace_bytes : 0, need);
   if (!aligned16(a->workspace)) return fail(BS_ERR_ALIGN, "kv_attention: workspace must be 16-byte aligned");
   if (a->num_pages > 0) {
-    // rows of 128 bytes: one token, or two of D = 64
-    const uint64_t rows = (uint64_t)a->num_pages * a->Hkv * a->page_size * a->D / 128;
-    const uint32_t box = (uint32_t)(bsk::kv_attention_box(a->page_size) * a->D / 128);
+    // rows of 128 bytes: one token, or two of D = 64; twice as many of 4 bits
+    const int bytes = fp4 ? a->D / 2 : a->D;
+    const uint64_t rows = (uint64_t)a->num_pages * a->Hkv * a->page_size * bytes / 128;
+    const uint32_t box = (uint32_t)(bsk::kv_attention_box(a->page_size) * bytes / 128);
     st = make_map(&L.tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a->k_codes, 128, rows, 128, 128, box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (st == BS_OK)
       st = make_map(&L.tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a->v_codes, 128, rows, 128, 128, box, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -1256,8 +1260,8 @@ bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
   p.lse = a->lse;
   p.k_codes = a->k_codes;
   p.v_codes = a->v_codes;
-  p.k_scales = a->k_scales;
-  p.v_scales = a->v_scales;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
   p.table = a->block_table;
   p.ld_table = a->ld_table;
   p.max_pages = a->max_pages;
@@ -1278,8 +1282,199 @@ bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
   p.counters = static_cast<int*>(a->workspace);
   p.work = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + kStreamKCounterBytes);
   p.wait_ns = wait_ns_of(a->wait_timeout_us);
-  cudaError_t e = bsk::launch_kv_attention(L, reinterpret_cast<cudaStream_t>(stream));
+  const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = fp4 ? bsk::launch_kv_attention_fp4(L, on) : bsk::launch_kv_attention(L, on);
   if (e != cudaSuccess) return cuda_fail(e, "kv_attention launch");
+  return BS_OK;
+}
+
+bs_status bs_kv_attention(const bs_kv_attention_args* a, bs_stream_t stream) {
+  if (!a) return fail(BS_ERR_INVALID, "kv_attention: null arguments");
+  return kv_attention(a, false, a->k_scales, a->v_scales, stream);
+}
+
+bs_status bs_kv_attention_fp4(const bs_kv_attention_args* a, const uint8_t* k_scales, const uint8_t* v_scales,
+                              bs_stream_t stream) {
+  if (!a) return fail(BS_ERR_INVALID, "kv_attention: null arguments");
+  return kv_attention(a, true, k_scales, v_scales, stream);
+}
+
+bs_status bs_kv_append_rotary(const bs_kv_append_rotary_args* a, bs_stream_t stream) {
+  if (!a) return fail(BS_ERR_INVALID, "kv_append_rotary: null arguments");
+  bs_status st = check_kv_cache("kv_append_rotary", a->Hkv, a->D, a->num_pages, a->page_size);
+  if (st != BS_OK) return st;
+  if (a->T < 0 || a->T > INT32_MAX || a->Hq < 0)
+    return fail(BS_ERR_INVALID, "kv_append_rotary: T=%lld Hq=%d", (long long)a->T, a->Hq);
+  if (a->dtype != BS_DTYPE_F32 && a->dtype != BS_DTYPE_BF16)
+    return fail(BS_ERR_INVALID, "kv_append_rotary: dtype %d", a->dtype);
+  if (a->cache_format != BS_FMT_FP8 && a->cache_format != BS_FMT_FP4)
+    return fail(BS_ERR_INVALID, "kv_append_rotary: cache_format %d", a->cache_format);
+  if (a->rotary_dim < 0 || a->rotary_dim > a->D || a->rotary_dim % 16)
+    return fail(BS_ERR_INVALID, "kv_append_rotary: rotary_dim=%d not a multiple of 16 up to D=%d", a->rotary_dim, a->D);
+  if (a->rotary_dim > 0 && (a->max_positions <= 0 || a->max_positions > INT32_MAX))
+    return fail(BS_ERR_INVALID, "kv_append_rotary: max_positions=%lld", (long long)a->max_positions);
+  if (a->Hkv > 16384 || a->Hq > 65535 || (a->T + 3) / 4 * (2 * (int64_t)a->Hkv + a->Hq + 1) > INT32_MAX)  // the launch grid
+    return fail(BS_ERR_UNSUPPORTED, "kv_append_rotary: T=%lld rows of Hq=%d and Hkv=%d heads in one call", (long long)a->T,
+                a->Hq, a->Hkv);
+  if (a->T == 0) return BS_OK;
+  if (!a->k || !a->v || !a->slots || !a->k_codes || !a->v_codes || !a->k_scales || !a->v_scales ||
+      (a->Hq > 0 && (!a->q || !a->q_out)) || (a->rotary_dim > 0 && (!a->positions || !a->angles)))
+    return fail(BS_ERR_INVALID, "kv_append_rotary: null pointer");
+  int64_t strides = 0;  // those of an axis of length 1 mean nothing
+  if (a->T > 1) strides |= a->k_token_stride | a->v_token_stride;
+  if (a->Hkv > 1) strides |= a->k_head_stride | a->v_head_stride;
+  if (a->Hq > 0 && a->T > 1) strides |= a->q_token_stride | a->q_out_token_stride;
+  if (a->Hq > 1) strides |= a->q_head_stride | a->q_out_head_stride;
+  const bool fp4 = a->cache_format == BS_FMT_FP4;
+  if (strides % 8 || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->k_codes) || !aligned16(a->v_codes) ||
+      (a->Hq > 0 && (!aligned16(a->q) || !aligned16(a->q_out))) || (a->rotary_dim > 0 && !aligned16(a->angles)) ||
+      !aligned4(a->k_scales) || !aligned4(a->v_scales) || !aligned4(a->slots) || !aligned4(a->positions))
+    return fail(BS_ERR_ALIGN, "kv_append_rotary: q, k, v, q_out, angles and codes must be 16-byte aligned, strides multiples of 8 elements");
+  // a row in place is read before it is written, any other order of rows is not
+  if (a->Hq > 0 && a->q == a->q_out &&
+      (a->dtype != BS_DTYPE_BF16 || (a->T > 1 && a->q_token_stride != a->q_out_token_stride) ||
+       (a->Hq > 1 && a->q_head_stride != a->q_out_head_stride)))
+    return fail(BS_ERR_INVALID, "kv_append_rotary: q_out in q's place needs bf16 and the same strides");
+  bsk::KvRotaryParams p = {};
+  if (!device_info(&p.status, nullptr)) return fail(BS_ERR_CUDA, "no current device");
+  p.q = a->q;
+  p.q_tok_stride = a->q_token_stride;
+  p.q_head_stride = a->q_head_stride;
+  p.q_out = a->q_out;
+  p.qo_tok_stride = a->q_out_token_stride;
+  p.qo_head_stride = a->q_out_head_stride;
+  p.x[0] = a->k;
+  p.x[1] = a->v;
+  p.tok_stride[0] = a->k_token_stride;
+  p.tok_stride[1] = a->v_token_stride;
+  p.head_stride[0] = a->k_head_stride;
+  p.head_stride[1] = a->v_head_stride;
+  p.slots = a->slots;
+  p.positions = a->positions;
+  p.angles = a->angles;
+  p.max_positions = (int)a->max_positions;
+  p.rot = a->rotary_dim;
+  p.interleaved = a->interleaved != 0;
+  p.codes[0] = a->k_codes;
+  p.codes[1] = a->v_codes;
+  p.scales[0] = a->k_scales;
+  p.scales[1] = a->v_scales;
+  p.fp4 = fp4;
+  p.T = (int)a->T;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  p.D = a->D;
+  p.num_pages = (int)a->num_pages;
+  p.page_shift = kv_page_shift(a->page_size);
+  p.x_bf16 = a->dtype == BS_DTYPE_BF16;
+  cudaError_t e = bsk::launch_kv_append_rotary(p, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_append_rotary launch");
+  return BS_OK;
+}
+
+bs_status bs_kv_gather(const bs_kv_gather_args* a, bs_stream_t stream) {
+  if (!a) return fail(BS_ERR_INVALID, "kv_gather: null arguments");
+  bs_status st = check_kv_cache("kv_gather", a->Hkv, a->D, a->num_pages, a->page_size);
+  if (st != BS_OK) return st;
+  if (a->T < 0 || a->T > INT32_MAX) return fail(BS_ERR_INVALID, "kv_gather: T=%lld", (long long)a->T);
+  if (a->cache_format != BS_FMT_FP8 && a->cache_format != BS_FMT_FP4)
+    return fail(BS_ERR_INVALID, "kv_gather: cache_format %d", a->cache_format);
+  if (a->Hkv > 16384 || a->T * a->Hkv > INT32_MAX)  // the launch grid
+    return fail(BS_ERR_UNSUPPORTED, "kv_gather: T=%lld rows of Hkv=%d heads in one call", (long long)a->T, a->Hkv);
+  if (a->T == 0) return BS_OK;
+  if (!a->slots || !a->k || !a->v || !a->k_codes || !a->v_codes || !a->k_scales || !a->v_scales)
+    return fail(BS_ERR_INVALID, "kv_gather: null pointer");
+  int64_t strides = 0;  // those of an axis of length 1 mean nothing
+  if (a->T > 1) strides |= a->k_token_stride | a->v_token_stride;
+  if (a->Hkv > 1) strides |= a->k_head_stride | a->v_head_stride;
+  if (strides % 8 || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->k_codes) || !aligned16(a->v_codes) ||
+      !aligned4(a->k_scales) || !aligned4(a->v_scales) || !aligned4(a->slots))
+    return fail(BS_ERR_ALIGN, "kv_gather: k, v and codes must be 16-byte aligned, strides multiples of 8 elements");
+  bsk::KvGatherParams p = {};
+  if (!device_info(&p.status, nullptr)) return fail(BS_ERR_CUDA, "no current device");
+  p.codes[0] = a->k_codes;
+  p.codes[1] = a->v_codes;
+  p.scales[0] = a->k_scales;
+  p.scales[1] = a->v_scales;
+  p.fp4 = a->cache_format == BS_FMT_FP4;
+  p.slots = a->slots;
+  p.out[0] = a->k;
+  p.out[1] = a->v;
+  p.out_tok_stride[0] = a->k_token_stride;
+  p.out_tok_stride[1] = a->v_token_stride;
+  p.out_head_stride[0] = a->k_head_stride;
+  p.out_head_stride[1] = a->v_head_stride;
+  p.T = (int)a->T;
+  p.Hkv = a->Hkv;
+  p.D = a->D;
+  p.num_pages = (int)a->num_pages;
+  p.page_shift = kv_page_shift(a->page_size);
+  cudaError_t e = bsk::launch_kv_gather(p, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_gather launch");
+  return BS_OK;
+}
+
+// Sizes of a bs_lora_add call, as far as its workspace depends on them.
+static bs_status check_lora(const bs_lora_args* a) {
+  if (a->T < 0 || a->T > INT32_MAX || a->B < 0 || a->N < 0 || a->N > INT32_MAX - 255 || a->K <= 0 || a->adapters < 0)
+    return fail(BS_ERR_INVALID, "lora_add: T=%lld B=%d K=%lld N=%lld adapters=%d", (long long)a->T, a->B, (long long)a->K,
+                (long long)a->N, a->adapters);
+  if (a->r <= 0 || a->r > 128 || a->r % 8) return fail(BS_ERR_UNSUPPORTED, "lora_add: rank %d not a multiple of 8 up to 128", a->r);
+  if (a->K % 8 || a->N % 8) return fail(BS_ERR_ALIGN, "lora_add: K=%lld or N=%lld not a multiple of 8", (long long)a->K, (long long)a->N);
+  if (a->K > 1 << 22 || a->B > 8192) return fail(BS_ERR_UNSUPPORTED, "lora_add: K=%lld above 2^22 or B=%d above 8192", (long long)a->K, a->B);
+  return BS_OK;
+}
+
+size_t bs_lora_workspace_bytes(const bs_lora_args* a) {
+  int sms = 0;
+  if (!a || check_lora(a) != BS_OK || !device_info(nullptr, &sms)) return 0;
+  return bsk::lora_workspace_bytes((int)a->T, a->B, (int)a->K, (int)a->N, a->r, sms);
+}
+
+bs_status bs_lora_add(const bs_lora_args* a, bs_stream_t stream) {
+  if (!a) return fail(BS_ERR_INVALID, "lora_add: null arguments");
+  if (a->dtype != BS_DTYPE_F32 && a->dtype != BS_DTYPE_BF16) return fail(BS_ERR_INVALID, "lora_add: dtype %d", a->dtype);
+  bs_status st = check_lora(a);
+  if (st != BS_OK) return st;
+  if (a->T == 0 || a->B == 0 || a->N == 0) return BS_OK;
+  if (!a->x || !a->y || !a->out || !a->cu_rows || !a->which || (a->adapters > 0 && (!a->a || !a->b)))
+    return fail(BS_ERR_INVALID, "lora_add: null pointer");
+  if (a->T > 1 && (a->ldx < a->K || a->ldy < a->N || a->ldo < a->N))
+    return fail(BS_ERR_INVALID, "lora_add: ldx=%lld / ldy=%lld / ldo=%lld below K / N", (long long)a->ldx, (long long)a->ldy,
+                (long long)a->ldo);
+  const int64_t strides = a->T > 1 ? a->ldx | a->ldy | a->ldo : 0;
+  if (strides % 8 || !aligned16(a->x) || !aligned16(a->a) || !aligned16(a->b) || !aligned16(a->y) || !aligned16(a->out) ||
+      !aligned4(a->scales) || !aligned4(a->cu_rows) || !aligned4(a->which))
+    return fail(BS_ERR_ALIGN, "lora_add: x, a, b, y and out must be 16-byte aligned, row strides multiples of 8");
+  if (a->out == a->y && a->T > 1 && a->ldo != a->ldy) return fail(BS_ERR_INVALID, "lora_add: out in y's place needs its stride");
+  int sms = 0;
+  bsk::LoraParams p = {};
+  if (!device_info(&p.status, &sms)) return fail(BS_ERR_CUDA, "no current device");
+  const size_t need = bsk::lora_workspace_bytes((int)a->T, a->B, (int)a->K, (int)a->N, a->r, sms);
+  if (!a->workspace || a->workspace_bytes < need)
+    return fail(BS_ERR_INVALID, "lora_add: workspace of %zu bytes, %zu needed", a->workspace ? a->workspace_bytes : 0, need);
+  if (!aligned16(a->workspace)) return fail(BS_ERR_ALIGN, "lora_add: workspace must be 16-byte aligned");
+  p.x = a->x;
+  p.ldx = a->ldx;
+  p.a = a->a;
+  p.b = a->b;
+  p.scales = a->scales;
+  p.cu = a->cu_rows;
+  p.which = a->which;
+  p.y = a->y;
+  p.ldy = a->ldy;
+  p.out = a->out;
+  p.ldo = a->ldo;
+  p.bf16 = a->dtype == BS_DTYPE_BF16;
+  p.T = (int)a->T;
+  p.B = a->B;
+  p.K = (int)a->K;
+  p.N = (int)a->N;
+  p.r = a->r;
+  p.adapters = a->adapters;
+  p.work = static_cast<float*>(a->workspace);
+  cudaError_t e = bsk::launch_lora(p, sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "lora_add launch");
   return BS_OK;
 }
 

@@ -63,6 +63,40 @@ struct KvAppendParams {
 };
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream);
 
+// New keys, values and queries with the rotation on the way (kv_append_rotary.cu)
+struct KvRotaryParams {
+  const void* q;          // [T, Hq, D]
+  long long q_tok_stride, q_head_stride;  // elements
+  void* q_out;            // bf16 [T, Hq, D]
+  long long qo_tok_stride, qo_head_stride;
+  const void* x[2];       // keys, values
+  long long tok_stride[2], head_stride[2];
+  const int* slots;       // [T]
+  const int* positions;   // [T]
+  const float* angles;    // [max_positions, rot]: cosines, then sines
+  int max_positions, rot, interleaved;
+  uint8_t* codes[2];      // [pages, Hkv, page, D] e4m3, or [.., D / 2] E2M1 pairs
+  void* scales[2];        // fp32 [pages, Hkv], or e4m3 [pages, Hkv, page, D / 16]
+  int fp4;
+  int T, Hq, Hkv, D;
+  int num_pages, page_shift;
+  int x_bf16;             // type of q, k and v
+  int* status;
+};
+cudaError_t launch_kv_append_rotary(const KvRotaryParams& p, cudaStream_t stream);
+struct KvGatherParams {
+  const uint8_t* codes[2];
+  const void* scales[2];
+  int fp4;
+  const int* slots;       // [T]
+  void* out[2];           // bf16 [T, Hkv, D]
+  long long out_tok_stride[2], out_head_stride[2];
+  int T, Hkv, D;
+  int num_pages, page_shift;
+  int* status;
+};
+cudaError_t launch_kv_gather(const KvGatherParams& p, cudaStream_t stream);
+
 // Attention over the paged 8-bit cache (kv_attention.cu)
 // Most rows (new tokens x heads of a group) per KV head of a request for the
 // few-rows kernel; kv_attention_rows.cu takes the others.  A call whose rows do not
@@ -81,8 +115,8 @@ struct KvAttentionParams {
   float* lse;             // [T, Hq] or null
   const uint8_t* k_codes;
   const uint8_t* v_codes;
-  const float* k_scales;
-  const float* v_scales;
+  const void* k_scales;   // fp32 [pages, Hkv]; 4-bit cache: e4m3 [pages, Hkv, page, D / 16]
+  const void* v_scales;
   const int* table;       // [B, ld_table]
   long long ld_table;
   int max_pages;
@@ -111,6 +145,8 @@ int kv_attention_rows_grid(int sms);
 size_t kv_attention_rows_piece_bytes(int D);
 cudaError_t launch_kv_attention_rows(const KvAttentionLaunch& L, cudaStream_t stream);
 cudaError_t launch_kv_attention(const KvAttentionLaunch& L, cudaStream_t stream);
+// the same over the 4-bit cache: k_scales and v_scales are e4m3 [pages, Hkv, page, D / 16]
+cudaError_t launch_kv_attention_fp4(const KvAttentionLaunch& L, cudaStream_t stream);
 
 // Few bf16 rows times FP4 weights (matvec_fp4.cu)
 struct Fp4MatvecParams {
@@ -127,5 +163,26 @@ struct Fp4MatvecParams {
   long long ldo;
 };
 cudaError_t launch_fp4_matvec(const Fp4MatvecParams& p, int sms, cudaStream_t stream);
+
+// Low-rank adapters of many requests (lora.cu)
+struct LoraParams {
+  const void* x;          // bf16 [T, ldx]
+  long long ldx;
+  const void* a;          // bf16 [adapters, r, K]
+  const void* b;          // bf16 [adapters, N, r]
+  const float* scales;    // [adapters] or null
+  const int* cu;          // [B + 1]
+  const int* which;       // [B]
+  const void* y;          // [T, ldy]
+  long long ldy;
+  void* out;              // [T, ldo]
+  long long ldo;
+  int bf16;               // type of y and out
+  int T, B, K, N, r, adapters;
+  float* work;
+  int* status;
+};
+size_t lora_workspace_bytes(int T, int B, int K, int N, int r, int sms);
+cudaError_t launch_lora(const LoraParams& p, int sms, cudaStream_t stream);
 
 }  // namespace bsk

@@ -348,8 +348,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
           x.cnt = 0;
           return;
         }
-        x.ks = p.k_scales[(long long)x.id * p.Hkv + x.h];
-        x.vs = p.v_scales[(long long)x.id * p.Hkv + x.h];
+        x.ks = static_cast<const float*>(p.k_scales)[(long long)x.id * p.Hkv + x.h];
+        x.vs = static_cast<const float*>(p.v_scales)[(long long)x.id * p.Hkv + x.h];
       };
       Group now = find(k_done), next = find(k_done + 8);
       scales(now);

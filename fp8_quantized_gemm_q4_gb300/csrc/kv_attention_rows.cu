@@ -733,8 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             record_status(p.status, kStatusOffsets, 50);
           } else {
             first = (int)((((long long)id * p.Hkv + u.h) << p.page_shift) + (token & ((1 << p.page_shift) - 1)));
-            ks = p.k_scales[(long long)id * p.Hkv + u.h];
-            const float vs = p.v_scales[(long long)id * p.Hkv + u.h];
+            ks = static_cast<const float*>(p.k_scales)[(long long)id * p.Hkv + u.h];
+            const float vs = static_cast<const float*>(p.v_scales)[(long long)id * p.Hkv + u.h];
             log_vs = log2f(vs);
             inv_vs = 1.0f / vs;
           }

@@ -675,6 +675,94 @@ size_t bs_kv_attention_workspace_bytes(const bs_kv_attention_args *args);
 bs_status bs_kv_attention(const bs_kv_attention_args *args, bs_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * The 4-bit paged cache: E2M1 codes and e4m3 scales for 16 elements of a token,
+ *   k_codes, v_codes   [num_pages, Hkv, page_size, D / 2], element 2 j of a token
+ *                      in the low nibble of byte j
+ *   k_scales, v_scales e4m3 [num_pages, Hkv, page_size, D / 16]
+ * 9/16 byte an element; element d stands for code * scale[d / 16].  Pages, block
+ * tables and slots are those of the 8-bit cache (bs_kv_plan, bs_kv_release).
+ *
+ * bs_kv_attention_fp4 -- bs_kv_attention over that cache.  args are bs_kv_attention's,
+ * with the 4-bit codes; args->k_scales and v_scales are not used, these are (16-byte
+ * aligned).  A NaN scale of K reaches the rows that see its token; of V, its 16
+ * columns of the rows that see its token.  Products and sums as there: a code times
+ * its scale is exact in fp16.
+ * ------------------------------------------------------------------------- */
+bs_status bs_kv_attention_fp4(const bs_kv_attention_args *args, const uint8_t *k_scales, const uint8_t *v_scales,
+                              bs_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * bs_kv_append_rotary -- new keys and values into their slots of either cache and
+ * queries to bf16, the position rotation applied on the way.  With R = rotary_dim, for
+ * i < R / 2, c = angles[position, i], s = angles[position, R / 2 + i] and the pairs
+ * (x1, x2) = (x[i], x[i + R / 2]), or (x[2 i], x[2 i + 1]) if interleaved:
+ *     y1 = fl(fl(x1 c) - fl(x2 s)),  y2 = fl(fl(x2 c) + fl(x1 s))   (fl: to fp32)
+ * on queries and keys; elements from R on, and values, stay as they are.
+ *   q_out   bf16_rn of the rotated queries
+ *   8 bits  (cache_format BS_FMT_FP8) as bs_kv_append, from the rotated keys
+ *   4 bits  (BS_FMT_FP4) for 16 elements: scale = e4m3_rn(fl(amax / 6)), at most 448,
+ *           code = e2m1_rn(fl(x / scale)), at most 6 (0 where the scale is 0).  amax is
+ *           that of the finite elements: an infinity takes the code of +-6, a NaN makes
+ *           its 16 elements NaN (scale 0x7f, codes 0).  Every row is for itself.
+ *
+ *   q, k, v    [T, Hq, D] and [T, Hkv, D] fp32 or bf16 (dtype) with strides in
+ *              elements; D contiguous, strides multiples of 8, pointers 16-byte
+ *              aligned.  Hq = 0: no queries
+ *   q_out      bf16 [T, Hq, D], likewise; may be q itself (bf16, the same strides), no
+ *              other overlap of outputs and inputs
+ *   slots      int32 [T]; a row with a negative slot is skipped, its query too; one
+ *              past the cache likewise, and sets BS_ERR_OFFSETS
+ *   positions  int32 [T]; one outside [0, max_positions) sets BS_ERR_OFFSETS and is
+ *              taken as the nearest
+ *   angles     fp32 [max_positions, rotary_dim], 16-byte aligned
+ *   rotary_dim a multiple of 16, 0 .. D; 0: no rotation (positions and angles unused)
+ *   k_scales, v_scales  fp32 or e4m3, as the format has them
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    const void *q;
+    int64_t q_token_stride, q_head_stride;
+    void *q_out;
+    int64_t q_out_token_stride, q_out_head_stride;
+    const void *k, *v;
+    int dtype;               /* bs_dtype of q, k and v */
+    int Hq, Hkv, D;
+    int64_t T;
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    const int32_t *slots, *positions;
+    const float *angles;
+    int64_t max_positions;
+    int rotary_dim, interleaved;
+    int cache_format;        /* bs_format */
+    int page_size;
+    uint8_t *k_codes, *v_codes;
+    void *k_scales, *v_scales;
+    int64_t num_pages;
+} bs_kv_append_rotary_args;
+bs_status bs_kv_append_rotary(const bs_kv_append_rotary_args *args, bs_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * bs_kv_gather -- rows of either cache as bf16: k[r, h], v[r, h] = code * scale
+ * (rounded to bf16; exact for a 4-bit cache and for power-of-two scales) of slot
+ * slots[r], to look at what a cache holds, or to move requests elsewhere.
+ *   slots      int32 [T]; a negative slot leaves its rows of k and v as they were, one
+ *              past the cache does too and sets BS_ERR_OFFSETS
+ *   k, v       bf16 [T, Hkv, D], strides in elements (multiples of 8), 16-byte aligned
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    const int32_t *slots;
+    int64_t T;
+    int Hkv, D;
+    void *k, *v;
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    int cache_format;        /* bs_format */
+    int page_size;
+    const uint8_t *k_codes, *v_codes;
+    const void *k_scales, *v_scales;
+    int64_t num_pages;
+} bs_kv_gather_args;
+bs_status bs_kv_gather(const bs_kv_gather_args *args, bs_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * bs_fp4_matvec -- 1 to 16 bf16 rows times FP4 weights:
  *     y[m, n] = alpha * tensor_scale * sum_k x[m, k] * e2m1[n, k] * sf[n, k/16] + bias[n]
  * The weights are those of bs_gemm (codes [N, K/2] and MMA-layout scales from
@@ -700,6 +788,49 @@ typedef struct {
     int64_t ldo;
 } bs_fp4_matvec_args;
 bs_status bs_fp4_matvec(const bs_fp4_matvec_args *args, bs_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * bs_lora_add -- low-rank adapters of many requests beside a projection that they
+ * share.  Rows cu_rows[b] .. cu_rows[b + 1] - 1 belong to request b, w = which[b]:
+ *     out[t] = y[t] + scales[w] (x[t] A_w^T) B_w^T        (y[t] where w < 0)
+ * Sums are fp32; x A^T enters the second product as a pair of bf16 (within 2^-16 of
+ * it); out is rounded once.
+ *
+ *   x          bf16 [T, ldx]
+ *   a, b       bf16 [adapters, r, K] and [adapters, N, r]
+ *   scales     fp32 [adapters] or NULL (= 1)
+ *   cu_rows    int32 [B + 1], as cu_q of bs_kv_attention: rows from cu_rows[B] on are
+ *              not written; offsets that are negative, descend or pass T set
+ *              BS_ERR_OFFSETS, no row outside [0, T) is touched, a request with a
+ *              negative or descending pair has no rows
+ *   which      int32 [B]; negative: no adapter; adapters and above: none either, and
+ *              sets BS_ERR_OFFSETS
+ *   y, out     fp32 or bf16 (dtype) [T, ldy], [T, ldo]; out may be y (same stride), no
+ *              other overlap
+ *   r          a multiple of 8, 8 .. 128; K and N multiples of 8, K <= 2^22, B <= 8192
+ *   all matrices 16-byte aligned, row strides multiples of 8 elements
+ *   workspace  device scratch of bs_lora_workspace_bytes(args) bytes, 16-byte aligned,
+ *              of this call alone until it has run; its contents do not matter
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    const void *x;
+    int64_t ldx;
+    const void *a, *b;
+    const float *scales;
+    const int32_t *cu_rows, *which;
+    const void *y;
+    int64_t ldy;
+    void *out;
+    int64_t ldo;
+    int dtype;               /* bs_dtype of y and out */
+    int B;
+    int64_t T, K, N;
+    int r, adapters;
+    void *workspace;
+    size_t workspace_bytes;
+} bs_lora_args;
+size_t bs_lora_workspace_bytes(const bs_lora_args *args);
+bs_status bs_lora_add(const bs_lora_args *args, bs_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Status.
