@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libbsgemm.so")
 SOURCES = ["api.cu", "quant.cu", "gemm_fp4.cu", "gemm_fp4_pair.cu", "gemm_fp4_decode.cu", "gemm_fp8.cu", "gemm_fp8_grouped.cu", "moe.cu", "kv_cache.cu", "kv_attention.cu", "kv_attention_rows.cu",
-           "matvec_fp4.cu", "kv_append_rotary.cu", "kv_attention_fp4.cu", "lora.cu"]
+           "matvec_fp4.cu", "kv_append_rotary.cu", "lora.cu"]
 HEADERS = ["ptx.cuh", "kernels.h", "decode.cuh", "decode.h", "kv_attention.cuh", "kv_cache.cuh", "budget.hpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

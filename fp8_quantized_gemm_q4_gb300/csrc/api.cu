@@ -1274,6 +1274,7 @@ static bs_status kv_attention(const bs_kv_attention_args* a, bool fp4, const voi
   p.D = a->D;
   p.num_pages = (int)a->num_pages;
   p.page_shift = kv_page_shift(a->page_size);
+  p.fp4 = fp4;
   p.scale_log2 = a->softmax_scale * 1.4426950408889634f;
   const int64_t most = a->max_q_len ? a->max_q_len : a->T;
   const int64_t most_rows = most * (a->Hq / a->Hkv);
@@ -1282,8 +1283,7 @@ static bs_status kv_attention(const bs_kv_attention_args* a, bool fp4, const voi
   p.counters = static_cast<int*>(a->workspace);
   p.work = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + kStreamKCounterBytes);
   p.wait_ns = wait_ns_of(a->wait_timeout_us);
-  const cudaStream_t on = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = fp4 ? bsk::launch_kv_attention_fp4(L, on) : bsk::launch_kv_attention(L, on);
+  cudaError_t e = bsk::launch_kv_attention(L, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv_attention launch");
   return BS_OK;
 }

@@ -124,6 +124,7 @@ struct KvAttentionParams {
   const int* kv_lens;     // [B]
   int B, T, Hq, Hkv, D;
   int num_pages, page_shift;
+  int fp4;                // the cache holds 4 bits
   float scale_log2;       // softmax scale * log2(e)
   int most_rows;          // bound of the rows per KV head of a request (at most 2^30)
   int few_rows;           // few_rows(T, Hq)
@@ -145,8 +146,6 @@ int kv_attention_rows_grid(int sms);
 size_t kv_attention_rows_piece_bytes(int D);
 cudaError_t launch_kv_attention_rows(const KvAttentionLaunch& L, cudaStream_t stream);
 cudaError_t launch_kv_attention(const KvAttentionLaunch& L, cudaStream_t stream);
-// the same over the 4-bit cache: k_scales and v_scales are e4m3 [pages, Hkv, page, D / 16]
-cudaError_t launch_kv_attention_fp4(const KvAttentionLaunch& L, cudaStream_t stream);
 
 // Few bf16 rows times FP4 weights (matvec_fp4.cu)
 struct Fp4MatvecParams {

@@ -32,13 +32,14 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t add
                : "r"(addr)
                : "memory");
 }
-// Shared memory of a tile as TMA writes it: rows of 128 bytes (one token, or two
-// for D = 64: rows of 64 bytes came in at half the rate), their 16-byte chunks
+// Shared memory of a tile as TMA writes it: rows of 128 bytes (one token of kBytes,
+// or two or four: rows of 64 bytes came in at half the rate), their 16-byte chunks
 // exchanged by the 128-byte swizzle.
-template <int D>
+template <int kBytes>
 __device__ __forceinline__ int code_at(int tok, int chunk) {
-  return D == 128 ? tok * 128 + ((chunk ^ (tok & 7)) << 4)
-                  : (tok >> 1) * 128 + (((((tok & 1) << 2) | chunk) ^ ((tok >> 1) & 7)) << 4);
+  if constexpr (kBytes == 128) return tok * 128 + ((chunk ^ (tok & 7)) << 4);
+  if constexpr (kBytes == 64) return (tok >> 1) * 128 + (((((tok & 1) << 2) | chunk) ^ ((tok >> 1) & 7)) << 4);
+  return (tok >> 2) * 128 + (((((tok & 3) << 1) | chunk) ^ ((tok >> 2) & 7)) << 4);
 }
 // Which of 8 tokens stands at place n of the MMA's token axis: any order does,
 // as long as scores, masks and V rows agree.  For D = 128 places 2 i, 2 i + 1
@@ -48,6 +49,16 @@ __device__ __forceinline__ int token_of(int n) {
   return D == 128 ? (n >> 1) | ((n & 1) << 2) : n;
 }
 
+__device__ __forceinline__ void store_floats(float4* at, float x, float y, float z, float w) { *at = make_float4(x, y, z, w); }
+__device__ __forceinline__ void store_floats(float2* at, float x, float y, float, float) { *at = make_float2(x, y); }
+__device__ __forceinline__ void add_floats(const float4* at, float& x, float& y, float& z, float& w) {
+  const float4 v = *at;
+  x += v.x, y += v.y, z += v.z, w += v.w;
+}
+__device__ __forceinline__ void add_floats(const float2* at, float& x, float& y, float&, float&) {
+  const float2 v = *at;
+  x += v.x, y += v.y;
+}
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
@@ -76,6 +87,40 @@ __device__ __noinline__ uint32_t take_nan(uint8_t* vt, int cnt, int seen0, int s
   }
   __syncwarp();
   return hit;
+}
+
+// The same of a 4-bit cache, where a NaN scale stands for a NaN in its 16 columns:
+// `scales` are those of V, the accumulators at bit 2 x + e: o[4 (x / 2) + j][2 (x % 2) + e]
+// for every j.
+template <int D>
+__device__ __noinline__ uint32_t take_nan_scales(uint8_t* scales, int cnt, int seen0, int seen1, int lane) {
+  uint32_t hit = 0;
+  for (int tok = 0; tok < cnt; ++tok)
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x)
+      if ((scales[tok * (D / 16) + 2 * x + (lane >> 4)] & 0x7f) == 0x7f)
+        hit |= (tok < seen0 ? 1u : 0u) << (2 * x) | (tok < seen1 ? 2u : 0u) << (2 * x);
+  __syncwarp();
+  for (int x = lane; x < cnt * (D / 16); x += 32)
+    if ((scales[x] & 0x7f) == 0x7f) scales[x] = 0;
+  __syncwarp();
+  return hit;
+}
+
+// Four columns of two tokens (a token in each half) as E2M1 codes to pairs of tokens:
+// column j as f16x2.  Pairs of nibbles of one column are brought side by side first.
+__device__ __forceinline__ void columns_to_f16(uint32_t w, uint32_t (&h)[4]) {
+  const uint32_t even = (w & 0x0f0fu) | ((w >> 12) & 0xf0f0u);
+  const uint32_t odd = ((w >> 4) & 0x0f0fu) | ((w >> 16) & 0xf0f0u);
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b1;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %5;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b1;\n\t}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(even), "r"(odd));
 }
 
 // One step of the online softmax over 16 tokens for 8 rows.  u[e]: logit of
@@ -141,14 +186,16 @@ constexpr int kFewWarps = 4;       // consumers; one more warp produces
 constexpr int kFewThreads = kFewWarps * 32 + 32;
 constexpr int kFewCtas = 3;        // an SM
 
-template <int D>
+template <int D, bool kFp4>
 struct FewSmem {
-  static constexpr int kStages = 512 / D;  // 64 KB of codes
-  static constexpr int kStageBytes = 2 * kTile * D;
+  static constexpr int kStages = kFp4 ? 896 / D : 512 / D;  // 64 KB of codes (and 4-bit scales)
+  static constexpr int kRow = kFp4 ? D / 2 : D;             // bytes of a token's codes
+  static constexpr int kStageBytes = 2 * kTile * kRow;
   alignas(1024) uint8_t kv[kStages][kStageBytes];  // K rows, then V rows
+  alignas(16) uint8_t scale[kFp4 ? kStages : 1][2][kFp4 ? kTile * D / 16 : 16];  // of K and V, 4 bits
   float red[kFewWarps / 2][8 * D];
   float2 ml[kFewWarps][8];
-  float4 group[kStages][4];  // per 16 tokens: K scale, log2 of V scale, 1 / V scale, valid tokens (int)
+  float4 group[kStages][4];  // per 16 tokens: K scale, log2 of V scale, 1 / V scale (8 bits), valid tokens (int)
   // units of this share: request, KV head, first of the 8 rows, cached tokens;
   // first row, rows (true), rows within T; the share's tile at which the unit
   // would begin, its end tile within the share (0: no unit)
@@ -184,17 +231,20 @@ __device__ __forceinline__ long long piece_at(int cta, int first_cta) {
 }
 // Place of column d of a row in a reduction buffer: 16-column windows and their
 // halves exchanged by row, so that the fragments' stores meet no bank twice.
-template <int D>
+// For 4 bits, whose fragments store four columns at a time, 4-column windows by row.
+template <int D, bool kFp4>
 __device__ __forceinline__ int red_at(int r, int d) {
+  if constexpr (kFp4) return r * D + (d ^ (((r >> 1) & 3) << 3));
   return r * D + ((((d >> 4) ^ ((r >> 1) & 1)) << 4) | ((d & 15) ^ (((r >> 2) & 1) << 3)));
 }
 
-template <int D>
+template <int D, bool kFp4>
 __global__ void __launch_bounds__(kFewThreads, kFewCtas)
     kv_attention_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                             const __grid_constant__ KvAttentionParams p) {
   extern __shared__ uint8_t smem_raw[];
-  using Smem = FewSmem<D>;
+  using Smem = FewSmem<D, kFp4>;
+  constexpr int kRow = Smem::kRow;
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr int kStages = Smem::kStages, kWarps = kFewWarps, kThreads = kFewThreads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -348,8 +398,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
           x.cnt = 0;
           return;
         }
-        x.ks = static_cast<const float*>(p.k_scales)[(long long)x.id * p.Hkv + x.h];
-        x.vs = static_cast<const float*>(p.v_scales)[(long long)x.id * p.Hkv + x.h];
+        if constexpr (!kFp4) {
+          x.ks = static_cast<const float*>(p.k_scales)[(long long)x.id * p.Hkv + x.h];
+          x.vs = static_cast<const float*>(p.v_scales)[(long long)x.id * p.Hkv + x.h];
+        }
       };
       Group now = find(k_done), next = find(k_done + 8);
       scales(now);
@@ -360,7 +412,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
         const bool copies = now.cnt > 0 && (16 * j) % box == 0;
         const unsigned copy_mask = __ballot_sync(kFullMask, copies);
         const long long token = (((long long)now.id * p.Hkv + now.h) << p.page_shift) + (now.tok & ((1 << p.page_shift) - 1));
-        const int row = (int)(token * D / 128);
+        const int row = (int)(token * kRow / 128);
         const int rounds = min(8, k_end - k0);
         float log_vs = 0.0f, inv_vs = 0.0f;
         for (int i = 0; i < rounds; ++i) {
@@ -368,14 +420,18 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
           dead |= __any_sync(kFullMask, !ok) != 0;
           if (!dead) {
             if (k == i && copies) {
-              tma_load_2d(&sm.kv[s][16 * j * D], &tm_k, &sm.full[s], 0, row);
-              tma_load_2d(&sm.kv[s][(kTile + 16 * j) * D], &tm_v, &sm.full[s], 0, row);
+              tma_load_2d(&sm.kv[s][16 * j * kRow], &tm_k, &sm.full[s], 0, row);
+              tma_load_2d(&sm.kv[s][(kTile + 16 * j) * kRow], &tm_v, &sm.full[s], 0, row);
+              if constexpr (kFp4) {
+                bulk_load(&sm.scale[s][0][j * D], static_cast<const uint8_t*>(p.k_scales) + token * (D / 16), box * D / 16, &sm.full[s]);
+                bulk_load(&sm.scale[s][1][j * D], static_cast<const uint8_t*>(p.v_scales) + token * (D / 16), box * D / 16, &sm.full[s]);
+              }
             }
-            if (i == 0) log_vs = log2f(now.vs), inv_vs = 1.0f / now.vs;  // the scales may still be on their way
+            if (!kFp4 && i == 0) log_vs = log2f(now.vs), inv_vs = 1.0f / now.vs;  // the scales may still be on their way
             if (k == i) sm.group[s][j] = make_float4(now.ks, log_vs, inv_vs, __int_as_float(now.cnt));
             __syncwarp();
             const int n = __popc((copy_mask >> (4 * i)) & 15u);
-            if (lane == 4 * i) mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(n * box * D * 2));
+            if (lane == 4 * i) mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(n * box * (kFp4 ? kRow + D / 16 : kRow) * 2));
             issued = k0 + i + 1;
           }
           if (++s == kStages) s = 0, ph ^= 1;
@@ -400,11 +456,12 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
         {
           const int r = r0 + g;
           const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (row0 + r / G) * p.q_tok_stride +
-                                   (h * G + r % G) * p.q_head_stride + 16 * c;
+                                   (h * G + r % G) * p.q_head_stride + (kFp4 ? D / 4 : 16) * c;
           uint32_t w[8 * kQ];
 #pragma unroll
           for (int x = 0; x < 2 * kQ; ++x) {
-            const uint4 v = g < R ? *reinterpret_cast<const uint4*>(q + 64 * (x >> 1) + 8 * (x & 1)) : make_uint4(0, 0, 0, 0);
+            const uint4 v = g < R ? *reinterpret_cast<const uint4*>(q + (kFp4 ? 8 * x : 64 * (x >> 1) + 8 * (x & 1)))
+                                  : make_uint4(0, 0, 0, 0);
             w[4 * x] = v.x, w[4 * x + 1] = v.y, w[4 * x + 2] = v.z, w[4 * x + 3] = v.w;
           }
           // the next unit's q on its way to L1 meanwhile
@@ -426,7 +483,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
           const int up = fp16_up(amax);
           const float mul = exp2i(up);
 #pragma unroll
-          for (int x = 0; x < 4 * kQ; ++x)  // k step x: columns 64 (x / 4) + 16 c + 4 (x % 4) .. + 3
+          for (int x = 0; x < 4 * kQ; ++x)  // k step x: columns 64 (x / 4) + 16 c + 4 (x % 4) .. + 3, or (4 bits) D / 4 c + 4 x .. + 3
 #pragma unroll
             for (int y = 0; y < 2; ++y)
               qb[x][y] = pack_f16x2(__uint_as_float(w[2 * x + y] << 16) * mul,
@@ -448,32 +505,81 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
           const float4 sc = sm.group[stage][warp];
           const int cnt = min(__float_as_int(sc.w), 16);  // after a wait that gave up, whatever lies here
           if (cnt > 0) {
-            uint8_t* kt = &sm.kv[stage][warp * 16 * D];
-            uint8_t* vt = kt + kTile * D;
-            if (cnt < 16) {  // codes behind the last token may stand for NaN
-              for (int x = cnt * (D / 16) + lane; x < D; x += 32)
-                *reinterpret_cast<uint4*>(vt + code_at<D>(x / (D / 16), x % (D / 16))) = make_uint4(0, 0, 0, 0);
+            uint8_t* kt = &sm.kv[stage][kFp4 ? 0 : warp * 16 * D];
+            uint8_t* vt = kt + kTile * kRow;
+            uint8_t* vs = kFp4 ? &sm.scale[stage][1][warp * D] : nullptr;  // of 4 bits: the scales of the warp's 16 tokens
+            if (cnt < 16) {  // what lies behind the last token may stand for NaN
+              if constexpr (kFp4) {
+                if (lane * 4 >= cnt * (D / 16) && lane < D / 4) *reinterpret_cast<uint32_t*>(vs + 4 * lane) = 0;
+              } else {
+                for (int x = cnt * (D / 16) + lane; x < D; x += 32)
+                  *reinterpret_cast<uint4*>(vt + code_at<D>(x / (D / 16), x % (D / 16))) = make_uint4(0, 0, 0, 0);
+              }
               __syncwarp();
             }
             const int tok0 = (tile - begin) * kTile + warp * 16;
             if (tok0 + cnt > all_seen) {
               uint32_t any = 0;
-              for (int x = lane; x < cnt * (D / 16); x += 32) {
-                const uint4 w = *reinterpret_cast<const uint4*>(vt + code_at<D>(x / (D / 16), x % (D / 16)));
-                any |= nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w);
+              if constexpr (kFp4) {
+                if (lane < D / 4) any = nan_codes(*reinterpret_cast<const uint32_t*>(vs + 4 * lane));
+              } else {
+                for (int x = lane; x < cnt * (D / 16); x += 32) {
+                  const uint4 w = *reinterpret_cast<const uint4*>(vt + code_at<D>(x / (D / 16), x % (D / 16)));
+                  any |= nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w);
+                }
               }
               if (__any_sync(kFullMask, any)) {
-                const uint32_t hit = take_nan<D>(vt, cnt, seen[0] - tok0, seen[1] - tok0, lane);
+                if constexpr (kFp4) {
+                  const uint32_t hit = take_nan_scales<D>(vs, cnt, seen[0] - tok0, seen[1] - tok0, lane);
 #pragma unroll
-                for (int a = 0; a < D / 16; ++a)
+                  for (int a = 0; a < D / 16; ++a)
 #pragma unroll
-                  for (int x = 0; x < 4; ++x)
-                    if (hit >> (4 * a + x) & 1) o[a][x] = __int_as_float(0x7fffffff);
+                    for (int x = 0; x < 4; ++x)
+                      if (hit >> (4 * (a >> 2) + x) & 1) o[a][x] = __int_as_float(0x7fffffff);
+                } else {
+                  const uint32_t hit = take_nan<D>(vt, cnt, seen[0] - tok0, seen[1] - tok0, lane);
+#pragma unroll
+                  for (int a = 0; a < D / 16; ++a)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                      if (hit >> (4 * a + x) & 1) o[a][x] = __int_as_float(0x7fffffff);
+                }
                 __syncwarp();
               }
             }
             float u[4] = {}, u2[4] = {};  // two chains of products
-            {
+            if constexpr (kFp4) {
+              // lane: D / 4 columns of tokens g and g + 8, one or two groups with a scale each
+              const uint8_t* ks = &sm.scale[stage][0][warp * D];
+              uint32_t wa[kQ * 2], wb[kQ * 2], sa, sb;
+              if constexpr (D == 128) {
+                const uint4 a = *reinterpret_cast<const uint4*>(kt + code_at<kRow>(warp * 16 + g, c));
+                const uint4 b = *reinterpret_cast<const uint4*>(kt + code_at<kRow>(warp * 16 + 8 + g, c));
+                wa[0] = a.x, wa[1] = a.y, wa[2] = a.z, wa[3] = a.w, wb[0] = b.x, wb[1] = b.y, wb[2] = b.z, wb[3] = b.w;
+                sa = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ks + 8 * g + 2 * c));
+                sb = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ks + 8 * (g + 8) + 2 * c));
+              } else {
+                const uint2 a = *reinterpret_cast<const uint2*>(kt + code_at<kRow>(warp * 16 + g, c >> 1) + 8 * (c & 1));
+                const uint2 b = *reinterpret_cast<const uint2*>(kt + code_at<kRow>(warp * 16 + 8 + g, c >> 1) + 8 * (c & 1));
+                wa[0] = a.x, wa[1] = a.y, wb[0] = b.x, wb[1] = b.y;
+                sa = e4m3x2_to_f16x2(ks[4 * g + c]);
+                sb = e4m3x2_to_f16x2(ks[4 * (g + 8) + c]);
+              }
+#pragma unroll
+              for (int y = 0; y < 2 * kQ; ++y) {
+                const uint32_t fa = __byte_perm(sa, 0, y < 2 ? 0x1010 : 0x3232), fb = __byte_perm(sb, 0, y < 2 ? 0x1010 : 0x3232);
+                uint32_t ka[4], kb[4];
+                e2m1x8_to_f16(wa[y], ka);
+                e2m1x8_to_f16(wb[y], kb);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const uint32_t f[4] = {hmul2(ka[2 * x], fa), hmul2(kb[2 * x], fb), hmul2(ka[2 * x + 1], fa), hmul2(kb[2 * x + 1], fb)};
+                  mma_f16(x ? u2 : u, f, qb[2 * y + x][0], qb[2 * y + x][1]);
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) u[e] = (u[e] + u2[e]) * qscale[e & 1];
+            } else {
               const int tok = token_of<D>(g);
 #pragma unroll
               for (int part = 0; part < kQ; ++part) {
@@ -487,32 +593,70 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
                   mma_f16(x & 1 ? u2 : u, ka, qb[4 * part + x][0], qb[4 * part + x][1]);
                 }
               }
-            }
-            const float f[2] = {qscale[0] * sc.x, qscale[1] * sc.x};
+              const float f[2] = {qscale[0] * sc.x, qscale[1] * sc.x};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) u[e] = fmaf(u[e] + u2[e], f[e & 1], sc.y);
+              for (int e = 0; e < 4; ++e) u[e] = fmaf(u[e] + u2[e], f[e & 1], sc.y);
+            }
             if (cnt < 16 || tok0 + 16 > all_seen) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const int tok = 8 * (e >> 1) + token_of<D>(g);
+                const int tok = 8 * (e >> 1) + (kFp4 ? g : token_of<D>(g));
                 if (tok >= cnt || tok0 + tok >= seen[e & 1]) u[e] = -INFINITY;
               }
             }
             uint32_t pb[2];
-            softmax_step<D / 16>(u, sc.z, m, l, o, pb);
+            softmax_step<D / 16>(u, kFp4 ? 1.0f : sc.z, m, l, o, pb);
+            if constexpr (kFp4) {
+              // scales of the pairs of tokens 2 c, 2 c + 1 and 8 more, of the groups 2 x + g / 4
+              uint32_t sv[D / 32][2];
+              const uint32_t pick = (lane >> 4) ? 0x7351 : 0x6240;
 #pragma unroll
-            for (int a = 0; a < D / 32; ++a) {
-              // lanes 8 i .. + 7 give the rows of matrix i: tokens 8 (i % 2) .. + 7 at 16-byte chunk 2 a + i / 2
-              uint32_t v[4];
-              const int tok = 8 * ((lane >> 3) & 1) + token_of<D>(lane & 7);
-              ldmatrix_x4_trans(v, smem_u32(vt + code_at<D>(tok, 2 * a + (lane >> 4))));
+              for (int t = 0; t < 2; ++t) {
+                uint32_t w[D / 64][2];  // four groups of the two tokens
+                if constexpr (D == 128) {
+                  const uint4 r = *reinterpret_cast<const uint4*>(vs + 8 * (2 * c + 8 * t));
+                  w[0][0] = r.x, w[1][0] = r.y, w[0][1] = r.z, w[1][1] = r.w;
+                } else {
+                  const uint2 r = *reinterpret_cast<const uint2*>(vs + 4 * (2 * c + 8 * t));
+                  w[0][0] = r.x, w[0][1] = r.y;
+                }
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                // a pair of codes (columns 2 g, 2 g + 1) of two tokens each: to pairs of tokens
-                const uint32_t w0 = __byte_perm(v[2 * x], 0, 0x3120), w1 = __byte_perm(v[2 * x + 1], 0, 0x3120);
-                const uint32_t va[4] = {e4m3x2_to_f16x2((uint16_t)w0), e4m3x2_to_f16x2((uint16_t)(w0 >> 16)),
-                                        e4m3x2_to_f16x2((uint16_t)w1), e4m3x2_to_f16x2((uint16_t)(w1 >> 16))};
-                mma_f16(o[2 * a + x], va, pb[0], pb[1]);
+                for (int a = 0; a < D / 64; ++a) {
+                  const uint32_t b = __byte_perm(w[a][0], w[a][1], pick);
+                  sv[2 * a][t] = e4m3x2_to_f16x2((uint16_t)b);
+                  sv[2 * a + 1][t] = e4m3x2_to_f16x2((uint16_t)(b >> 16));
+                }
+              }
+#pragma unroll
+              for (int a = 0; a < D / 64; ++a) {
+                // matrix i: tokens 8 (i % 2) .. + 7 at the 32 columns of chunk 2 a + i / 2, four of them
+                // (4 g .. + 3) and two tokens a register
+                uint32_t v[4], h[4][4];
+                ldmatrix_x4_trans(v, smem_u32(vt + code_at<kRow>(warp * 16 + (lane & 15), 2 * a + (lane >> 4))));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) columns_to_f16(v[i], h[i]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const uint32_t va[4] = {hmul2(h[0][x], sv[2 * a][0]), hmul2(h[2][x], sv[2 * a + 1][0]),
+                                          hmul2(h[1][x], sv[2 * a][1]), hmul2(h[3][x], sv[2 * a + 1][1])};
+                  mma_f16(o[4 * a + x], va, pb[0], pb[1]);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int a = 0; a < D / 32; ++a) {
+                // lanes 8 i .. + 7 give the rows of matrix i: tokens 8 (i % 2) .. + 7 at 16-byte chunk 2 a + i / 2
+                uint32_t v[4];
+                const int tok = 8 * ((lane >> 3) & 1) + token_of<D>(lane & 7);
+                ldmatrix_x4_trans(v, smem_u32(vt + code_at<D>(tok, 2 * a + (lane >> 4))));
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  // a pair of codes (columns 2 g, 2 g + 1) of two tokens each: to pairs of tokens
+                  const uint32_t w0 = __byte_perm(v[2 * x], 0, 0x3120), w1 = __byte_perm(v[2 * x + 1], 0, 0x3120);
+                  const uint32_t va[4] = {e4m3x2_to_f16x2((uint16_t)w0), e4m3x2_to_f16x2((uint16_t)(w0 >> 16)),
+                                          e4m3x2_to_f16x2((uint16_t)w1), e4m3x2_to_f16x2((uint16_t)(w1 >> 16))};
+                  mma_f16(o[2 * a + x], va, pb[0], pb[1]);
+                }
               }
             }
             if (cnt < 16 || tok0 + cnt > all_seen) fence_proxy_async_smem();  // the zeros, before the next copy into this stage
@@ -523,7 +667,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
         }
 
         // ---- the warps' (m, l, o) to one: o[a] holds columns 16 a + 2 g and + 1
-        // (e / 2) of rows 2 c and + 1 (e % 2)
+        // (e / 2) of rows 2 c and + 1 (e % 2); of 4 bits, columns 64 (a / 4) + 4 g + a % 4 and + 32
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -541,23 +685,31 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
           for (int a = 0; a < D / 16; ++a) o[a][e] *= f, o[a][2 + e] *= f;
         }
         float* buf = sm.red[warp % (kWarps / 2)];
-        auto put = [&] {
+        // the lane's columns, by as many as lie side by side
+        auto each = [&](auto&& f) {
+          if constexpr (kFp4) {
 #pragma unroll
-          for (int a = 0; a < D / 16; ++a)
+            for (int x = 0; x < D / 32; ++x)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              *reinterpret_cast<float2*>(buf + red_at<D>(2 * c + e, 16 * a + 2 * g)) = make_float2(o[a][e], o[a][2 + e]);
+              for (int e = 0; e < 2; ++e) {
+                float* at = buf + red_at<D, true>(2 * c + e, 32 * x + 4 * g);
+                const int a = 4 * (x >> 1), i = 2 * (x & 1) + e;
+                f(reinterpret_cast<float4*>(at), o[a][i], o[a + 1][i], o[a + 2][i], o[a + 3][i]);
+              }
+          } else {
+            float none = 0.0f;
+#pragma unroll
+            for (int a = 0; a < D / 16; ++a)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                f(reinterpret_cast<float2*>(buf + red_at<D, false>(2 * c + e, 16 * a + 2 * g)), o[a][e], o[a][2 + e], none, none);
+          }
         };
+        auto put = [&] { each([](auto* at, float x, float y, float z, float w) { store_floats(at, x, y, z, w); }); };
         if (warp >= kWarps / 2) put();
         consumer_sync();
         if (warp < kWarps / 2) {
-#pragma unroll
-          for (int a = 0; a < D / 16; ++a)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float2 add = *reinterpret_cast<const float2*>(buf + red_at<D>(2 * c + e, 16 * a + 2 * g));
-              o[a][e] += add.x, o[a][2 + e] += add.y;
-            }
+          each([](const auto* at, float& x, float& y, float& z, float& w) { add_floats(at, x, y, z, w); });
           put();
         }
         consumer_sync();
@@ -571,7 +723,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
           float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
           for (int w = 0; w < kWarps / 2; ++w) {
-            const float4 v = *reinterpret_cast<const float4*>(&sm.red[w][red_at<D>(r, d)]);
+            const float4 v = *reinterpret_cast<const float4*>(&sm.red[w][red_at<D, kFp4>(r, d)]);
             y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
           }
           float M = -INFINITY, L = 0.0f;
@@ -646,10 +798,11 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
       mbar_drain(&sm.full[k % kStages], (k / kStages) & 1, 100000000ull);
 }
 
-template <int D>
+template <int D, bool kFp4>
 cudaError_t launch_few(const KvAttentionLaunch& L, cudaStream_t stream) {
-  constexpr int kSmem = (int)sizeof(FewSmem<D>) + 1024;
-  return launch_kernel_smem(kv_attention_few_kernel<D>, (unsigned)L.few_grid, kFewThreads, kSmem, stream, L.tm_k, L.tm_v,
+  constexpr int kSmem = (int)sizeof(FewSmem<D, kFp4>) + 1024;
+  static_assert(kFewCtas * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
+  return launch_kernel_smem(kv_attention_few_kernel<D, kFp4>, (unsigned)L.few_grid, kFewThreads, kSmem, stream, L.tm_k, L.tm_v,
                             L.p);
 }
 
@@ -663,7 +816,8 @@ cudaError_t launch_kv_attention(const KvAttentionLaunch& L, cudaStream_t stream)
   const KvAttentionParams& p = L.p;
   const int G = p.Hq / p.Hkv;
   if (G <= p.few_rows) {
-    cudaError_t e = p.D == 64 ? launch_few<64>(L, stream) : launch_few<128>(L, stream);
+    cudaError_t e = p.fp4 ? (p.D == 64 ? launch_few<64, true>(L, stream) : launch_few<128, true>(L, stream))
+                          : (p.D == 64 ? launch_few<64, false>(L, stream) : launch_few<128, false>(L, stream));
     if (e != cudaSuccess) return e;
   }
   if (p.most_rows <= p.few_rows) return cudaSuccess;

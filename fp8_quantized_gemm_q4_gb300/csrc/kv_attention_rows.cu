@@ -65,7 +65,7 @@ template <int D>
 struct RowsSmem {
   alignas(1024) uint8_t k[2][kN * D * 2];  // [D / 64][token][64 columns]
   alignas(1024) uint8_t v[2][kN * D * 2];  // the same of V
-  float4 page[kPageSlots][kGroups];        // first row of codes (int, -1: none), K scale, log2 of V scale, 1 / V scale
+  float4 page[kPageSlots][kGroups];        // first row of codes (int, -1: none), K scale, log2 of V scale (4 bits: 0, of no page -infinity), 1 / V scale
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2];
   uint64_t page_full[kPageSlots], page_empty[kPageSlots], o_done, unit_done, q_full, drain;
   UnitInfo unit[kUnitSlots];
@@ -153,18 +153,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return y;
 }
 // NaN into the columns part * D / 4 .. of a row whose tokens from .. to - 1 hold NaN
-// codes of V there, in the output (dst) or the unit's piece.  Out of line, for units
-// that meet none.
-template <int D>
+// codes (4 bits: scales) of V there, in the output (dst) or the unit's piece.  Out of
+// line, for units that meet none.
+template <int D, bool kFp4>
 __device__ __noinline__ void put_nan(const KvAttentionParams& p, int b, int h, int part, int from, int to,
                                      __nv_bfloat16* dst, float* piece) {
   for (int x = from; x < to; ++x) {
     const int id = p.table[b * p.ld_table + (x >> p.page_shift)];
     if ((unsigned)id >= (unsigned)p.num_pages) continue;
-    const uint8_t* code =
-        p.v_codes + ((((long long)id * p.Hkv + h) << p.page_shift) + (x & ((1 << p.page_shift) - 1))) * D;
+    const long long token = (((long long)id * p.Hkv + h) << p.page_shift) + (x & ((1 << p.page_shift) - 1));
+    const uint8_t* code = kFp4 ? static_cast<const uint8_t*>(p.v_scales) + token * (D / 16) : p.v_codes + token * D;
     for (int d = part * (D / 4); d < (part + 1) * (D / 4); ++d)
-      if ((code[d] & 0x7f) == 0x7f) {
+      if ((code[kFp4 ? d / 16 : d] & 0x7f) == 0x7f) {
         if (dst)
           dst[d] = __ushort_as_bfloat16(0x7fff);
         else
@@ -191,7 +191,7 @@ __device__ __forceinline__ bool any_of(int bar, int threads, bool x) {
 __device__ __forceinline__ bool softmax_any(bool x) { return any_of(1, kSoft * 32, x); }
 __device__ __forceinline__ bool rows_any(int rows, bool x) { return any_of(2 + rows, 128, x); }
 
-template <int D>
+template <int D, bool kFp4>
 __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __grid_constant__ KvAttentionParams p) {
   extern __shared__ uint8_t smem_raw[];
   using Smem = RowsSmem<D>;
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         float mx = -INFINITY;
 #pragma unroll
         for (int h = 0; h < kOwn / 16; ++h) {
-          const float4 pg = page[h];
+          const float4 pg = kFp4 ? make_float4(0.0f, 1.0f, page[h].z, 1.0f) : page[h];
           float g = __uint_as_float(raw[16 * h]);
 #pragma unroll
           for (int y = 1; y < 15; y += 2)
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
         for (int h = 0; h < kOwn / 16; ++h) {
-          const float4 pg = page[h];
+          const float4 pg = kFp4 ? make_float4(0.0f, 1.0f, page[h].z, 1.0f) : page[h];
           // a scale is positive, or 0 with pg.z = -infinity: masked scores must not meet the 0
           const float f1 = fmaxf(qscale * pg.y, 1e-37f), o1 = pg.z - ref;
           const float2 f = make_float2(f1, f1), off = make_float2(o1, o1);
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       tc_fence_before();
       if (sm.nan_unit[unit & 7].x == (int)unit + 1) {
         const int4 bad = sm.nan_unit[unit & 7];
-        if (in) put_nan<D>(p, bad.y, bad.z, part, max(bad.w, t0 * kN), min(seen, t1 * kN), alone ? dst : nullptr, slot + r128 * 4);
+        if (in) put_nan<D, kFp4>(p, bad.y, bad.z, part, max(bad.w, t0 * kN), min(seen, t1 * kN), alone ? dst : nullptr, slot + r128 * 4);
         __syncwarp();
       }
       if (alone) {
@@ -564,15 +564,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
     // Lane: 16 codes of a token (and the token's place among its warp's), such
     // that eight lanes in a row store to eight different chunks.  The codes of
     // a tile are read while those of the tile before are converted.
-    constexpr int kSteps = kN * D / (128 * 16);           // 16-byte loads per thread
+    // Of 4 bits: 32 codes of a token and their two scales, stored as four chunks; eight
+    // lanes in a row have four tokens and two neighbours of each.
+    constexpr int kCodes = kFp4 ? 32 : 16;
+    constexpr int kSteps = kN * D / (128 * kCodes);       // 16-byte loads per thread
     constexpr int kStepTokens = kN / kSteps;
+    constexpr int kChunks = kCodes / 8;                   // 16-byte chunks that a load becomes
     const bool is_v = warp >= kSoft + 4;
-    const int w = warp & 3, q = lane & 3;
+    const int w = warp & 3, q = kFp4 ? lane & 1 : lane & 3;
     const int panel = D == 128 ? (lane >> 3) & 1 : 0;
-    const int tok = D == 128 ? w * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1) : w * 8 + (lane >> 2);
-    const uint8_t* codes = (is_v ? p.v_codes : p.k_codes) + (tok & 15) * D + 64 * panel + 16 * q;
+    const int tok = kFp4 ? (D == 128 ? w * 8 + (lane >> 4) * 4 + ((lane >> 1) & 3) : w * 16 + (lane >> 3) * 4 + ((lane >> 1) & 3))
+                    : D == 128 ? w * 4 + (lane >> 4) * 2 + ((lane >> 2) & 1) : w * 8 + (lane >> 2);
+    constexpr int kRow = kFp4 ? D / 2 : D;                // bytes of a token
+    const uint8_t* codes = (is_v ? p.v_codes : p.k_codes) + (tok & 15) * kRow + (kFp4 ? 32 : 64) * panel + 16 * q;
+    const uint8_t* scales = static_cast<const uint8_t*>(is_v ? p.v_scales : p.k_scales) + (tok & 15) * (D / 16) + 4 * panel + 2 * q;
     const uint32_t base = smem_u32(is_v ? sm.v[0] : sm.k[0]) + panel * (kN * 128) + tok * 128;
-    const uint32_t at0 = base + (((2 * q) ^ (tok & 7)) << 4), at1 = base + (((2 * q + 1) ^ (tok & 7)) << 4);
+    uint32_t at[kChunks];
+#pragma unroll
+    for (int x = 0; x < kChunks; ++x) at[x] = base + (((kChunks * q + x) ^ (tok & 7)) << 4);
     uint64_t* full = is_v ? sm.v_full : sm.k_full;
     uint64_t* empty = is_v ? sm.v_empty : sm.k_empty;
     for (;;) {
@@ -587,10 +596,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       const int4 bad = make_int4((int)k + 1, u->b, u->h, hidden / kN * kN);
       unit_close();
       uint4 raw[kSteps];
-      auto load = [&](uint4& r, int s, int left, const float4* page) {
+      uint16_t two[kFp4 ? kSteps : 1];  // scales
+      auto load = [&](int s, int left, const float4* page) {
         const int x = s * kStepTokens + tok, first = __float_as_int(page[x >> 4].x);
-        r = make_uint4(0, 0, 0, 0);
-        if (first >= 0 && x < left) r = __ldg(reinterpret_cast<const uint4*>(codes + (long long)first * D));
+        raw[s] = make_uint4(0, 0, 0, 0);
+        if constexpr (kFp4) two[s] = 0;
+        if (first >= 0 && x < left) {
+          raw[s] = __ldg(reinterpret_cast<const uint4*>(codes + (long long)first * kRow));
+          if constexpr (kFp4) two[s] = __ldg(reinterpret_cast<const uint16_t*>(scales + (long long)first * (D / 16)));
+        }
       };
       auto page_open = [&](uint32_t c) {
         mbar_wait(&sm.page_full[c % kPageSlots], (c / kPageSlots) & 1, wg, 65);
@@ -602,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       };
       const float4* page = page_open(c);
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) load(raw[s], s, len - t0 * kN, page);
+      for (int s = 0; s < kSteps; ++s) load(s, len - t0 * kN, page);
       page_close(c);
       for (int t = t0; t < t1; ++t, ++c) {
         const bool more = t + 1 < t1;
@@ -612,9 +626,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
           uint32_t any = 0;
 #pragma unroll
           for (int s = 0; s < kSteps; ++s) {
-            const uint4 n = make_uint4(nan_codes(raw[s].x), nan_codes(raw[s].y), nan_codes(raw[s].z), nan_codes(raw[s].w));
-            any |= n.x | n.y | n.z | n.w;
-            raw[s] = make_uint4(without(raw[s].x, n.x), without(raw[s].y, n.y), without(raw[s].z, n.z), without(raw[s].w, n.w));
+            if constexpr (kFp4) {
+              const uint32_t n = nan_codes(two[s]) & 0xffffu;
+              any |= n;
+              two[s] = (uint16_t)without(two[s], n);
+            } else {
+              const uint4 n = make_uint4(nan_codes(raw[s].x), nan_codes(raw[s].y), nan_codes(raw[s].z), nan_codes(raw[s].w));
+              any |= n.x | n.y | n.z | n.w;
+              raw[s] = make_uint4(without(raw[s].x, n.x), without(raw[s].y, n.y), without(raw[s].z, n.z), without(raw[s].w, n.w));
+            }
           }
           if (any) sm.nan_unit[(bad.x - 1) & 7] = bad;
         }
@@ -622,14 +642,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
           const uint32_t in[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
-          uint32_t h[8];
+          if constexpr (kFp4) {
+            const uint32_t sc = e4m3x2_to_f16x2(two[s]);
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            e4m3x4_to_f16(in[y], h[2 * y], h[2 * y + 1]);
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t f = __byte_perm(sc, 0, y < 2 ? 0x1010 : 0x3232);
+              uint32_t h[4];
+              e2m1x8_to_f16(in[y], h);
+              st_shared_v4(at[y] + to + s * (kStepTokens * 128), hmul2(h[0], f), hmul2(h[1], f), hmul2(h[2], f), hmul2(h[3], f));
+            }
+          } else {
+            uint32_t h[8];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              e4m3x4_to_f16(in[y], h[2 * y], h[2 * y + 1]);
+            }
+            st_shared_v4(at[0] + to + s * (kStepTokens * 128), h[0], h[1], h[2], h[3]);
+            st_shared_v4(at[1] + to + s * (kStepTokens * 128), h[4], h[5], h[6], h[7]);
           }
-          st_shared_v4(at0 + to + s * (kStepTokens * 128), h[0], h[1], h[2], h[3]);
-          st_shared_v4(at1 + to + s * (kStepTokens * 128), h[4], h[5], h[6], h[7]);
-          if (more) load(raw[s], s, len - (t + 1) * kN, page);
+          if (more) load(s, len - (t + 1) * kN, page);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -733,10 +764,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             record_status(p.status, kStatusOffsets, 50);
           } else {
             first = (int)((((long long)id * p.Hkv + u.h) << p.page_shift) + (token & ((1 << p.page_shift) - 1)));
-            ks = static_cast<const float*>(p.k_scales)[(long long)id * p.Hkv + u.h];
-            const float vs = static_cast<const float*>(p.v_scales)[(long long)id * p.Hkv + u.h];
-            log_vs = log2f(vs);
-            inv_vs = 1.0f / vs;
+            if constexpr (!kFp4) {
+              ks = static_cast<const float*>(p.k_scales)[(long long)id * p.Hkv + u.h];
+              const float vs = static_cast<const float*>(p.v_scales)[(long long)id * p.Hkv + u.h];
+              log_vs = log2f(vs);
+              inv_vs = 1.0f / vs;
+            } else {
+              log_vs = 0.0f;
+            }
           }
         }
         for (int x = 0; x < 4 && t + x < t1; ++x, ++c) {
@@ -759,12 +794,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
   }
 }
 
-template <int D>
+template <int D, bool kFp4>
 cudaError_t launch(const KvAttentionLaunch& L, cudaStream_t stream) {
   // all of an SM's shared memory: one CTA an SM, as tensor memory has it
   constexpr int kSmem = 227 * 1024;
   static_assert(sizeof(RowsSmem<D>) + 1024 <= kSmem, "shared memory");
-  return launch_kernel_smem(kv_attention_rows_kernel<D>, (unsigned)L.rows_grid, kThreads, kSmem, stream, L.p);
+  return launch_kernel_smem(kv_attention_rows_kernel<D, kFp4>, (unsigned)L.rows_grid, kThreads, kSmem, stream, L.p);
 }
 
 }  // namespace
@@ -773,7 +808,8 @@ int kv_attention_rows_grid(int sms) { return sms < kCounters ? sms : kCounters; 
 size_t kv_attention_rows_piece_bytes(int D) { return (size_t)2 * kM * (D + 2) * sizeof(float); }
 
 cudaError_t launch_kv_attention_rows(const KvAttentionLaunch& L, cudaStream_t stream) {
-  return L.p.D == 64 ? launch<64>(L, stream) : launch<128>(L, stream);
+  if (L.p.fp4) return L.p.D == 64 ? launch<64, true>(L, stream) : launch<128, true>(L, stream);
+  return L.p.D == 64 ? launch<64, false>(L, stream) : launch<128, false>(L, stream);
 }
 
 }  // namespace bsk
