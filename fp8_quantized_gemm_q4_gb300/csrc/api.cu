@@ -1243,7 +1243,7 @@ static bs_status kv_attention(const bs_kv_attention_args* a, bool fp4, const voi
     // rows of 128 bytes: one token, or two of D = 64; twice as many of 4 bits
     const int bytes = fp4 ? a->D / 2 : a->D;
     const uint64_t rows = (uint64_t)a->num_pages * a->Hkv * a->page_size * bytes / 128;
-    const uint32_t box = (uint32_t)(bsk::kv_attention_box(a->page_size) * bytes / 128);
+    const uint32_t box = (uint32_t)(bsk::kv_attention_box(a->page_size, fp4) * bytes / 128);
     st = make_map(&L.tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a->k_codes, 128, rows, 128, 128, box, CU_TENSOR_MAP_SWIZZLE_128B);
     if (st == BS_OK)
       st = make_map(&L.tm_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a->v_codes, 128, rows, 128, 128, box, CU_TENSOR_MAP_SWIZZLE_128B);

@@ -140,7 +140,7 @@ struct KvAttentionLaunch {
 };
 int kv_attention_few_grid(int sms);
 size_t kv_attention_piece_bytes(int D);  // per CTA of the few-rows grid
-int kv_attention_box(int page_size);
+int kv_attention_box(int page_size, bool fp4);
 // requests with more than few_rows rows per KV head (kv_attention_rows.cu)
 int kv_attention_rows_grid(int sms);
 size_t kv_attention_rows_piece_bytes(int D);

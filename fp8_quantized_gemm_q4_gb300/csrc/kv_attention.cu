@@ -19,6 +19,9 @@ namespace bsk {
 
 namespace {
 
+template <bool kFp4>
+constexpr int kTileOf = kFp4 ? 128 : 64;  // cached tokens per stage
+
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -107,22 +110,6 @@ __device__ __noinline__ uint32_t take_nan_scales(uint8_t* scales, int cnt, int s
   return hit;
 }
 
-// Four columns of two tokens (a token in each half) as E2M1 codes to pairs of tokens:
-// column j as f16x2.  Pairs of nibbles of one column are brought side by side first.
-__device__ __forceinline__ void columns_to_f16(uint32_t w, uint32_t (&h)[4]) {
-  const uint32_t even = (w & 0x0f0fu) | ((w >> 12) & 0xf0f0u);
-  const uint32_t odd = ((w >> 4) & 0x0f0fu) | ((w >> 16) & 0xf0f0u);
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b1;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %5;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b1;\n\t}\n"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(even), "r"(odd));
-}
-
 // One step of the online softmax over 16 tokens for 8 rows.  u[e]: logit of
 // row 2 c + e % 2 for token place g + 8 (e / 2).  Returns the weights as the B
 // fragment (places on k) of the product with V.
@@ -156,6 +143,202 @@ __device__ __forceinline__ void softmax_step(float (&u)[4], float inv_sv, float 
   }
 }
 
+// Places in shared memory of what a lane reads of the 32 tokens of a 4-bit tile that its
+// warp takes, from the stage's codes and the scales of those tokens on; [h]: 16 of them.
+template <int D>
+struct Fp4At {
+  uint32_t k[2][2], v[2][D / 64], ks, vs;
+  __device__ __forceinline__ Fp4At(int warp, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int tok = warp * 32 + 16 * h;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)  // D / 4 columns of tokens g and g + 8
+        k[h][i] = D == 128 ? code_at<64>(tok + 8 * i + g, c) : code_at<32>(tok + 8 * i + g, c >> 1) + 8 * (c & 1);
+#pragma unroll
+      for (int a = 0; a < D / 64; ++a)  // rows for ldmatrix: tokens 0 .. 15 at 16-byte chunk 2 a, then 2 a + 1
+        v[h][a] = kTileOf<true> * (D / 2) + code_at<D / 2>(tok + (lane & 15), 2 * a + (lane >> 4));
+    }
+    ks = g * (D / 16) + (D == 128 ? 2 : 1) * c;
+    vs = kTileOf<true> * (D / 16) + 2 * c * (D / 16);
+  }
+};
+constexpr float kNone = -3.0e38f;  // reference of a row that has seen no token
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint16_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return (uint16_t)v;
+}
+__device__ __forceinline__ uint16_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+
+// 32 tokens of a 4-bit tile for 8 rows: scores, a step of the online softmax (as
+// softmax_step, with the distance from the reference, score * qscale - m, in place of the
+// logit, and the rows' maxima looked for only where some distance passes 8), and the
+// product with V.  codes, scales: the stage's in shared memory; vs the same of V; cnt:
+// tokens that are there of each 16.
+template <int D>
+__device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_t* vs, const int (&cnt)[2], int tok0,
+                                         int all_seen, const int (&seen)[2], const float (&qscale)[2],
+                                         const uint32_t (&qb)[D / 16][2], float (&m)[2], float (&l)[2],
+                                         float (&o)[D / 16][4], const Fp4At<D>& at, int lane) {
+  const bool edge = min(cnt[0], cnt[1]) < 16 || tok0 + 32 > all_seen;
+  if (edge) {
+    // a NaN scale of V behind the last token, or where some row does not look
+    uint32_t any = 0;
+#pragma unroll
+    for (int x = lane; x < D / 2; x += 32) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(vs) + x;
+      const int tok = 4 * x / (D / 16);
+      if ((tok & 15) >= (tok < 16 ? cnt[0] : cnt[1])) *w = 0;
+      any |= nan_codes(*w);
+    }
+    __syncwarp();
+    if (__any_sync(kFullMask, any)) {
+      const uint32_t hit = take_nan_scales<D>(vs, 32, seen[0] - tok0, seen[1] - tok0, lane);
+#pragma unroll
+      for (int a = 0; a < D / 16; ++a)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (hit >> (4 * (a >> 2) + x) & 1) o[a][x] = __int_as_float(0x7fffffff);
+    }
+    __syncwarp();
+  }
+  float s[2][4] = {};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t wa[D / 32], wb[D / 32], sa, sb;
+    if constexpr (D == 128) {
+      const uint4 a = lds128(codes + at.k[h][0]), b = lds128(codes + at.k[h][1]);
+      wa[0] = a.x, wa[1] = a.y, wa[2] = a.z, wa[3] = a.w, wb[0] = b.x, wb[1] = b.y, wb[2] = b.z, wb[3] = b.w;
+      sa = e4m3x2_to_f16x2(lds16(scales + at.ks + 16 * h * (D / 16)));
+      sb = e4m3x2_to_f16x2(lds16(scales + at.ks + (16 * h + 8) * (D / 16)));
+    } else {
+      const uint2 a = lds64(codes + at.k[h][0]), b = lds64(codes + at.k[h][1]);
+      wa[0] = a.x, wa[1] = a.y, wb[0] = b.x, wb[1] = b.y;
+      sa = e4m3x2_to_f16x2(lds8(scales + at.ks + 16 * h * (D / 16)));
+      sb = e4m3x2_to_f16x2(lds8(scales + at.ks + (16 * h + 8) * (D / 16)));
+    }
+#pragma unroll
+    for (int y = 0; y < D / 32; ++y) {
+      const uint32_t fa = __byte_perm(sa, 0, y < 2 ? 0x1010 : 0x3232), fb = __byte_perm(sb, 0, y < 2 ? 0x1010 : 0x3232);
+      uint32_t ka[4], kb[4];
+      e2m1x8_to_f16(wa[y], ka);
+      e2m1x8_to_f16(wb[y], kb);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t f[4] = {hmul2(ka[2 * x], fa), hmul2(kb[2 * x], fb), hmul2(ka[2 * x + 1], fa), hmul2(kb[2 * x + 1], fb)};
+        mma_f16(s[h], f, qb[2 * y + x][0], qb[2 * y + x][1]);
+      }
+    }
+  }
+  if (edge) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int tok = 8 * (e >> 1) + (lane >> 2);
+        if (tok >= cnt[h] || tok0 + 16 * h + tok >= seen[e & 1]) s[h][e] = -INFINITY;
+      }
+  }
+  float z[2][4];
+  auto distances = [&] {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[h][e] = fmaf(s[h][e], qscale[e & 1], -m[e & 1]);
+  };
+  distances();
+  float far = fmaxf(fmaxf(z[0][0], z[0][1]), z[0][2]);
+  far = fmaxf(fmaxf(far, z[0][3]), z[1][0]);
+  far = fmaxf(fmaxf(far, z[1][1]), fmaxf(z[1][2], z[1][3]));
+  if (__any_sync(kFullMask, far > 8.0f)) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float mx = fmaxf(fmaxf(s[0][e], s[0][2 + e]), fmaxf(s[1][e], s[1][2 + e])) * qscale[e];
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, d));
+      const bool up = mx > m[e] + 8.0f;
+      const float f = up ? ex2(m[e] - mx) : 1.0f;
+      m[e] = up ? mx : m[e];
+      l[e] *= f;
+#pragma unroll
+      for (int a = 0; a < D / 16; ++a) o[a][e] *= f, o[a][2 + e] *= f;
+    }
+    distances();
+  }
+  uint32_t pb[2][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const float a = ex2(z[h][2 * t]), b = ex2(z[h][2 * t + 1]);
+      l[0] += a, l[1] += b;
+      pb[h][t] = movmatrix_trans(pack_f16x2(a, b));
+    }
+  const uint32_t pick = (lane >> 4) ? 0x7351 : 0x6240;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    // scales of the pairs of tokens 2 c, 2 c + 1 and 8 more, of the groups 2 x + g / 4
+    uint32_t sv[D / 32][2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      uint32_t w[D / 64][2];  // four groups of the two tokens
+      if constexpr (D == 128) {
+        const uint4 r = lds128(scales + at.vs + (16 * h + 8 * t) * (D / 16));
+        w[0][0] = r.x, w[1][0] = r.y, w[0][1] = r.z, w[1][1] = r.w;
+      } else {
+        const uint2 r = lds64(scales + at.vs + (16 * h + 8 * t) * (D / 16));
+        w[0][0] = r.x, w[0][1] = r.y;
+      }
+#pragma unroll
+      for (int a = 0; a < D / 64; ++a) {
+        const uint32_t b = __byte_perm(w[a][0], w[a][1], pick);
+        sv[2 * a][t] = e4m3x2_to_f16x2((uint16_t)b);
+        sv[2 * a + 1][t] = e4m3x2_to_f16x2((uint16_t)(b >> 16));
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < D / 64; ++a) {
+      // matrix i: tokens 8 (i % 2) .. + 7 at the 32 columns of chunk 2 a + i / 2; a register has four
+      // columns (4 g .. + 3) of two tokens, which become pairs of tokens after their conversion
+      uint32_t v[4], f[4][4];
+      ldmatrix_x4_trans(v, codes + at.v[h][a]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t e[4];
+        e2m1x8_to_f16(v[i], e);
+        f[i][0] = __byte_perm(e[0], e[2], 0x5410);
+        f[i][1] = __byte_perm(e[0], e[2], 0x7632);
+        f[i][2] = __byte_perm(e[1], e[3], 0x5410);
+        f[i][3] = __byte_perm(e[1], e[3], 0x7632);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t va[4] = {hmul2(f[0][x], sv[2 * a][0]), hmul2(f[2][x], sv[2 * a + 1][0]),
+                                hmul2(f[1][x], sv[2 * a][1]), hmul2(f[3][x], sv[2 * a + 1][1])};
+        mma_f16(o[4 * a + x], va, pb[h][0], pb[h][1]);
+      }
+    }
+  }
+  if (edge) fence_proxy_async_smem();  // the zeros, before the next copy into this stage
+}
+
 // ---------------------------------------------------------------------------
 // Requests with at most few_rows rows per KV head (decode, drafts): bound by the
 // cache stream.  Work is a list of (request, head, 8 rows) units of 64-token
@@ -174,13 +357,14 @@ __device__ __forceinline__ void softmax_step(float (&u)[4], float inv_sv, float 
 // piece); one token over 1000: 10 us, a chain of dependent reads.  Three CTAs an SM
 // leave 128 registers a thread, of which 16 to 20 bytes are spilled.
 // ---------------------------------------------------------------------------
-constexpr int kTile = 64;          // cached tokens per stage
 constexpr int kItems = 32;         // units listed at a time
-constexpr int kMinTiles = 2;       // least cost worth a CTA of its own
+template <bool kFp4>
+constexpr int kMinTilesOf = kFp4 ? 2 : 2;  // least cost worth a CTA of its own
 // What a unit costs beside its tiles (q, the join of the warps, a piece), in tiles.
 // us with 0 / 2 / 4 / 10: 64 decode requests 107.6 / 106.1 / 105.5 / 106, drafts over 16
 // heads 24.8 / 23.3 / 22.9 / 23.9, 64 requests of 30 to 14000 tokens 20.6 / 17.4 / 16.6 / 16.7
-constexpr int kUnitTiles = 4;
+template <bool kFp4>
+constexpr int kUnitTilesOf = kFp4 ? 2 : 4;
 constexpr int kCounters = 1024;    // arrival counters at the head of the workspace
 constexpr int kFewWarps = 4;       // consumers; one more warp produces
 constexpr int kFewThreads = kFewWarps * 32 + 32;
@@ -188,14 +372,15 @@ constexpr int kFewCtas = 3;        // an SM
 
 template <int D, bool kFp4>
 struct FewSmem {
-  static constexpr int kStages = kFp4 ? 896 / D : 512 / D;  // 64 KB of codes (and 4-bit scales)
+  static constexpr int kTile = kTileOf<kFp4>;
+  static constexpr int kStages = kFp4 ? 384 / D : 512 / D;  // 64 KB of codes, or 54 KB of them and scales
   static constexpr int kRow = kFp4 ? D / 2 : D;             // bytes of a token's codes
   static constexpr int kStageBytes = 2 * kTile * kRow;
   alignas(1024) uint8_t kv[kStages][kStageBytes];  // K rows, then V rows
   alignas(16) uint8_t scale[kFp4 ? kStages : 1][2][kFp4 ? kTile * D / 16 : 16];  // of K and V, 4 bits
   float red[kFewWarps / 2][8 * D];
   float2 ml[kFewWarps][8];
-  float4 group[kStages][4];  // per 16 tokens: K scale, log2 of V scale, 1 / V scale (8 bits), valid tokens (int)
+  float4 group[kStages][kTile / 16];  // per 16 tokens: K scale, log2 of V scale, 1 / V scale (8 bits), valid tokens (int)
   // units of this share: request, KV head, first of the 8 rows, cached tokens;
   // first row, rows (true), rows within T; the share's tile at which the unit
   // would begin, its end tile within the share (0: no unit)
@@ -213,6 +398,7 @@ struct FewSmem {
 // with more than few_rows per KV head, else one at least (rows that see nothing
 // are written too).  Which kernel serves a request follows from its own rows and
 // the call's, so that its result does not depend on the bound that the call gives.
+template <int kTile>
 __device__ __forceinline__ int few_tiles(const KvAttentionParams& p, int n, int len, int G) {
   return n <= 0 || (long long)n * G > p.few_rows ? 0 : max(1, (len + kTile - 1) / kTile);
 }
@@ -244,7 +430,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
                             const __grid_constant__ KvAttentionParams p) {
   extern __shared__ uint8_t smem_raw[];
   using Smem = FewSmem<D, kFp4>;
-  constexpr int kRow = Smem::kRow;
+  constexpr int kRow = Smem::kRow, kTile = Smem::kTile, kUnitTiles = kUnitTilesOf<kFp4>, kMinTiles = kMinTilesOf<kFp4>;
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr int kStages = Smem::kStages, kWarps = kFewWarps, kThreads = kFewThreads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -272,7 +458,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
     const Rows own = rows_of(p, b);
     row0_own = own.row0, n_own = own.n;
     len_own = cached(p, b);
-    const int nt = few_tiles(p, n_own, len_own, G), rt = nt ? (n_own * G + 7) / 8 : 0;
+    const int nt = few_tiles<kTile>(p, n_own, len_own, G), rt = nt ? (n_own * G + 7) / 8 : 0;
     mine.x += nt * rt;
     mine.y += rt;
     // one CTA tells: the check in all of them cost a call of prompts, whose other kernel
@@ -311,7 +497,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
     for (int b = b0; b < b1; ++b) {
       int n = n_own, len = len_own;
       if (per > 1) n = rows_of(p, b).n, len = cached(p, b);
-      const int nt = few_tiles(p, n, len, G);
+      const int nt = few_tiles<kTile>(p, n, len, G);
       if (!nt) continue;
       const int u = p.Hkv * ((n * G + 7) / 8);
       const long long off = c - (at + units * kUnitTiles);
@@ -348,7 +534,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
           const Rows r = rows_of(p, b);
           row0 = r.row0, n = r.n, len = cached(p, b);
         }
-        const int nt = few_tiles(p, n, len, G);
+        const int nt = few_tiles<kTile>(p, n, len, G);
         if (!nt) continue;
         const int rt = (n * G + 7) / 8, u = p.Hkv * rt;
         for (int h = (int)max(0ll, base - units); h < u && units + h < base + kItems; ++h) {
@@ -368,16 +554,17 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
     const int k_end = sm.end[kItems - 1] ? sm.end[kItems - 1] : tiles;  // where this list ends in the share
 
     if (warp == kWarps) {
-      // ---- producer: lane 4 k + j prepares group j (16 tokens) of the k-th of
-      // eight tiles, then each tile's copies go out as its stage frees.  Page
-      // ids are read two rounds of eight ahead and scales one, so that neither
+      // ---- producer: lane kGroups k + j prepares group j (16 tokens) of the k-th of
+      // kRound tiles, then each tile's copies go out as its stage frees.  Page
+      // ids are read two rounds ahead and scales one, so that neither
       // latency stands between two rounds.
+      constexpr int kGroups = kTile / 16, kRound = 32 / kGroups;
       struct Group {
         int id, tok, h, cnt;
         float ks, vs;
       };
       const int box = min(kTile, 1 << p.page_shift);  // tokens of a copy
-      const int k = lane >> 2, j = lane & 3;
+      const int k = lane / kGroups, j = lane % kGroups;
       int at_item = 0;  // this lane's unit: its tiles ascend
       auto find = [&](int k0) {
         Group x = {-1, 0, 0, 0, 0.0f, 1.0f};
@@ -403,17 +590,17 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
           x.vs = static_cast<const float*>(p.v_scales)[(long long)x.id * p.Hkv + x.h];
         }
       };
-      Group now = find(k_done), next = find(k_done + 8);
+      Group now = find(k_done), next = find(k_done + kRound);
       scales(now);
       uint32_t s = k_done % kStages, ph = (k_done / kStages) & 1;
-      for (int k0 = k_done; k0 < k_end; k0 += 8) {
+      for (int k0 = k_done; k0 < k_end; k0 += kRound) {
         scales(next);
-        const Group later = find(k0 + 16);
+        const Group later = find(k0 + 2 * kRound);
         const bool copies = now.cnt > 0 && (16 * j) % box == 0;
         const unsigned copy_mask = __ballot_sync(kFullMask, copies);
         const long long token = (((long long)now.id * p.Hkv + now.h) << p.page_shift) + (now.tok & ((1 << p.page_shift) - 1));
         const int row = (int)(token * kRow / 128);
-        const int rounds = min(8, k_end - k0);
+        const int rounds = min(kRound, k_end - k0);
         float log_vs = 0.0f, inv_vs = 0.0f;
         for (int i = 0; i < rounds; ++i) {
           const bool ok = mbar_wait(&sm.empty[s], ph ^ 1, wg, 51);
@@ -430,8 +617,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
             if (!kFp4 && i == 0) log_vs = log2f(now.vs), inv_vs = 1.0f / now.vs;  // the scales may still be on their way
             if (k == i) sm.group[s][j] = make_float4(now.ks, log_vs, inv_vs, __int_as_float(now.cnt));
             __syncwarp();
-            const int n = __popc((copy_mask >> (4 * i)) & 15u);
-            if (lane == 4 * i) mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(n * box * (kFp4 ? kRow + D / 16 : kRow) * 2));
+            const int n = __popc((copy_mask >> (kGroups * i)) & ((1u << kGroups) - 1));
+            if (lane == kGroups * i) mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(n * box * (kFp4 ? kRow + D / 16 : kRow) * 2));
             issued = k0 + i + 1;
           }
           if (++s == kStages) s = 0, ph ^= 1;
@@ -440,9 +627,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
         next = later;
       }
     } else {
-      // ---- consumers: warp w takes tokens 16 w .. + 15 of every tile
+      // ---- consumers: warp w takes tokens 16 w .. + 15 of every tile (of 4 bits 32 w .. + 31)
       const int g = lane >> 2, c = lane & 3;
       constexpr int kQ = D / 64;  // 64-wide parts of a row
+      const Fp4At<D> at(warp, lane);
       for (int im = 0; im < kItems; ++im) {
         const int end = sm.end[im];
         if (!end) break;
@@ -497,89 +685,48 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
         }
         const int all_seen = len - n + r0 / G + 1;  // tokens that every row sees
         float o[D / 16][4] = {};
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        float m[2], l[2] = {0.0f, 0.0f};  // reference and sum of weights of the two rows
+        m[0] = m[1] = kFp4 ? kNone : -INFINITY;
 
         const int begin = sm.begin[im];
         for (; tile < end; ++tile) {
           mbar_wait(&sm.full[stage], phase, wg, 52);
-          const float4 sc = sm.group[stage][warp];
-          const int cnt = min(__float_as_int(sc.w), 16);  // after a wait that gave up, whatever lies here
-          if (cnt > 0) {
-            uint8_t* kt = &sm.kv[stage][kFp4 ? 0 : warp * 16 * D];
-            uint8_t* vt = kt + kTile * kRow;
-            uint8_t* vs = kFp4 ? &sm.scale[stage][1][warp * D] : nullptr;  // of 4 bits: the scales of the warp's 16 tokens
-            if (cnt < 16) {  // what lies behind the last token may stand for NaN
-              if constexpr (kFp4) {
-                if (lane * 4 >= cnt * (D / 16) && lane < D / 4) *reinterpret_cast<uint32_t*>(vs + 4 * lane) = 0;
-              } else {
-                for (int x = cnt * (D / 16) + lane; x < D; x += 32)
-                  *reinterpret_cast<uint4*>(vt + code_at<D>(x / (D / 16), x % (D / 16))) = make_uint4(0, 0, 0, 0);
-              }
+          const float4 sc = sm.group[stage][kFp4 ? 2 * warp : warp];
+          // after a wait that gave up, whatever lies here
+          const int cnt = min(__float_as_int(sc.w), 16);
+          const int cnt2 = kFp4 ? min(max(__float_as_int(sm.group[stage][2 * warp + 1].w), 0), 16) : 0;
+          if (max(cnt, cnt2) <= 0) {
+          } else if constexpr (kFp4) {
+            const int there[2] = {max(cnt, 0), cnt2};
+            fp4_tile<D>(smem_u32(sm.kv[stage]), smem_u32(sm.scale[stage]) + warp * 2 * D, &sm.scale[stage][1][warp * 2 * D], there,
+                        (tile - begin) * kTile + warp * 32, all_seen, seen, qscale, qb, m, l, o, at, lane);
+          } else {
+            uint8_t* kt = &sm.kv[stage][warp * 16 * D];
+            uint8_t* vt = kt + kTile * D;
+            if (cnt < 16) {  // codes behind the last token may stand for NaN
+              for (int x = cnt * (D / 16) + lane; x < D; x += 32)
+                *reinterpret_cast<uint4*>(vt + code_at<D>(x / (D / 16), x % (D / 16))) = make_uint4(0, 0, 0, 0);
               __syncwarp();
             }
             const int tok0 = (tile - begin) * kTile + warp * 16;
             if (tok0 + cnt > all_seen) {
               uint32_t any = 0;
-              if constexpr (kFp4) {
-                if (lane < D / 4) any = nan_codes(*reinterpret_cast<const uint32_t*>(vs + 4 * lane));
-              } else {
-                for (int x = lane; x < cnt * (D / 16); x += 32) {
-                  const uint4 w = *reinterpret_cast<const uint4*>(vt + code_at<D>(x / (D / 16), x % (D / 16)));
-                  any |= nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w);
-                }
+              for (int x = lane; x < cnt * (D / 16); x += 32) {
+                const uint4 w = *reinterpret_cast<const uint4*>(vt + code_at<D>(x / (D / 16), x % (D / 16)));
+                any |= nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w);
               }
               if (__any_sync(kFullMask, any)) {
-                if constexpr (kFp4) {
-                  const uint32_t hit = take_nan_scales<D>(vs, cnt, seen[0] - tok0, seen[1] - tok0, lane);
+                const uint32_t hit = take_nan<D>(vt, cnt, seen[0] - tok0, seen[1] - tok0, lane);
 #pragma unroll
-                  for (int a = 0; a < D / 16; ++a)
+                for (int a = 0; a < D / 16; ++a)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                      if (hit >> (4 * (a >> 2) + x) & 1) o[a][x] = __int_as_float(0x7fffffff);
-                } else {
-                  const uint32_t hit = take_nan<D>(vt, cnt, seen[0] - tok0, seen[1] - tok0, lane);
-#pragma unroll
-                  for (int a = 0; a < D / 16; ++a)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                      if (hit >> (4 * a + x) & 1) o[a][x] = __int_as_float(0x7fffffff);
-                }
+                  for (int x = 0; x < 4; ++x)
+                    if (hit >> (4 * a + x) & 1) o[a][x] = __int_as_float(0x7fffffff);
                 __syncwarp();
               }
             }
             float u[4] = {}, u2[4] = {};  // two chains of products
-            if constexpr (kFp4) {
-              // lane: D / 4 columns of tokens g and g + 8, one or two groups with a scale each
-              const uint8_t* ks = &sm.scale[stage][0][warp * D];
-              uint32_t wa[kQ * 2], wb[kQ * 2], sa, sb;
-              if constexpr (D == 128) {
-                const uint4 a = *reinterpret_cast<const uint4*>(kt + code_at<kRow>(warp * 16 + g, c));
-                const uint4 b = *reinterpret_cast<const uint4*>(kt + code_at<kRow>(warp * 16 + 8 + g, c));
-                wa[0] = a.x, wa[1] = a.y, wa[2] = a.z, wa[3] = a.w, wb[0] = b.x, wb[1] = b.y, wb[2] = b.z, wb[3] = b.w;
-                sa = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ks + 8 * g + 2 * c));
-                sb = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ks + 8 * (g + 8) + 2 * c));
-              } else {
-                const uint2 a = *reinterpret_cast<const uint2*>(kt + code_at<kRow>(warp * 16 + g, c >> 1) + 8 * (c & 1));
-                const uint2 b = *reinterpret_cast<const uint2*>(kt + code_at<kRow>(warp * 16 + 8 + g, c >> 1) + 8 * (c & 1));
-                wa[0] = a.x, wa[1] = a.y, wb[0] = b.x, wb[1] = b.y;
-                sa = e4m3x2_to_f16x2(ks[4 * g + c]);
-                sb = e4m3x2_to_f16x2(ks[4 * (g + 8) + c]);
-              }
-#pragma unroll
-              for (int y = 0; y < 2 * kQ; ++y) {
-                const uint32_t fa = __byte_perm(sa, 0, y < 2 ? 0x1010 : 0x3232), fb = __byte_perm(sb, 0, y < 2 ? 0x1010 : 0x3232);
-                uint32_t ka[4], kb[4];
-                e2m1x8_to_f16(wa[y], ka);
-                e2m1x8_to_f16(wb[y], kb);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  const uint32_t f[4] = {hmul2(ka[2 * x], fa), hmul2(kb[2 * x], fb), hmul2(ka[2 * x + 1], fa), hmul2(kb[2 * x + 1], fb)};
-                  mma_f16(x ? u2 : u, f, qb[2 * y + x][0], qb[2 * y + x][1]);
-                }
-              }
-#pragma unroll
-              for (int e = 0; e < 4; ++e) u[e] = (u[e] + u2[e]) * qscale[e & 1];
-            } else {
+            {
               const int tok = token_of<D>(g);
 #pragma unroll
               for (int part = 0; part < kQ; ++part) {
@@ -593,70 +740,32 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
                   mma_f16(x & 1 ? u2 : u, ka, qb[4 * part + x][0], qb[4 * part + x][1]);
                 }
               }
-              const float f[2] = {qscale[0] * sc.x, qscale[1] * sc.x};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) u[e] = fmaf(u[e] + u2[e], f[e & 1], sc.y);
             }
+            const float f[2] = {qscale[0] * sc.x, qscale[1] * sc.x};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] = fmaf(u[e] + u2[e], f[e & 1], sc.y);
             if (cnt < 16 || tok0 + 16 > all_seen) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const int tok = 8 * (e >> 1) + (kFp4 ? g : token_of<D>(g));
+                const int tok = 8 * (e >> 1) + token_of<D>(g);
                 if (tok >= cnt || tok0 + tok >= seen[e & 1]) u[e] = -INFINITY;
               }
             }
             uint32_t pb[2];
-            softmax_step<D / 16>(u, kFp4 ? 1.0f : sc.z, m, l, o, pb);
-            if constexpr (kFp4) {
-              // scales of the pairs of tokens 2 c, 2 c + 1 and 8 more, of the groups 2 x + g / 4
-              uint32_t sv[D / 32][2];
-              const uint32_t pick = (lane >> 4) ? 0x7351 : 0x6240;
+            softmax_step<D / 16>(u, sc.z, m, l, o, pb);
 #pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                uint32_t w[D / 64][2];  // four groups of the two tokens
-                if constexpr (D == 128) {
-                  const uint4 r = *reinterpret_cast<const uint4*>(vs + 8 * (2 * c + 8 * t));
-                  w[0][0] = r.x, w[1][0] = r.y, w[0][1] = r.z, w[1][1] = r.w;
-                } else {
-                  const uint2 r = *reinterpret_cast<const uint2*>(vs + 4 * (2 * c + 8 * t));
-                  w[0][0] = r.x, w[0][1] = r.y;
-                }
+            for (int a = 0; a < D / 32; ++a) {
+              // lanes 8 i .. + 7 give the rows of matrix i: tokens 8 (i % 2) .. + 7 at 16-byte chunk 2 a + i / 2
+              uint32_t v[4];
+              const int tok = 8 * ((lane >> 3) & 1) + token_of<D>(lane & 7);
+              ldmatrix_x4_trans(v, smem_u32(vt + code_at<D>(tok, 2 * a + (lane >> 4))));
 #pragma unroll
-                for (int a = 0; a < D / 64; ++a) {
-                  const uint32_t b = __byte_perm(w[a][0], w[a][1], pick);
-                  sv[2 * a][t] = e4m3x2_to_f16x2((uint16_t)b);
-                  sv[2 * a + 1][t] = e4m3x2_to_f16x2((uint16_t)(b >> 16));
-                }
-              }
-#pragma unroll
-              for (int a = 0; a < D / 64; ++a) {
-                // matrix i: tokens 8 (i % 2) .. + 7 at the 32 columns of chunk 2 a + i / 2, four of them
-                // (4 g .. + 3) and two tokens a register
-                uint32_t v[4], h[4][4];
-                ldmatrix_x4_trans(v, smem_u32(vt + code_at<kRow>(warp * 16 + (lane & 15), 2 * a + (lane >> 4))));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) columns_to_f16(v[i], h[i]);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  const uint32_t va[4] = {hmul2(h[0][x], sv[2 * a][0]), hmul2(h[2][x], sv[2 * a + 1][0]),
-                                          hmul2(h[1][x], sv[2 * a][1]), hmul2(h[3][x], sv[2 * a + 1][1])};
-                  mma_f16(o[4 * a + x], va, pb[0], pb[1]);
-                }
-              }
-            } else {
-#pragma unroll
-              for (int a = 0; a < D / 32; ++a) {
-                // lanes 8 i .. + 7 give the rows of matrix i: tokens 8 (i % 2) .. + 7 at 16-byte chunk 2 a + i / 2
-                uint32_t v[4];
-                const int tok = 8 * ((lane >> 3) & 1) + token_of<D>(lane & 7);
-                ldmatrix_x4_trans(v, smem_u32(vt + code_at<D>(tok, 2 * a + (lane >> 4))));
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  // a pair of codes (columns 2 g, 2 g + 1) of two tokens each: to pairs of tokens
-                  const uint32_t w0 = __byte_perm(v[2 * x], 0, 0x3120), w1 = __byte_perm(v[2 * x + 1], 0, 0x3120);
-                  const uint32_t va[4] = {e4m3x2_to_f16x2((uint16_t)w0), e4m3x2_to_f16x2((uint16_t)(w0 >> 16)),
-                                          e4m3x2_to_f16x2((uint16_t)w1), e4m3x2_to_f16x2((uint16_t)(w1 >> 16))};
-                  mma_f16(o[2 * a + x], va, pb[0], pb[1]);
-                }
+              for (int x = 0; x < 2; ++x) {
+                // a pair of codes (columns 2 g, 2 g + 1) of two tokens each: to pairs of tokens
+                const uint32_t w0 = __byte_perm(v[2 * x], 0, 0x3120), w1 = __byte_perm(v[2 * x + 1], 0, 0x3120);
+                const uint32_t va[4] = {e4m3x2_to_f16x2((uint16_t)w0), e4m3x2_to_f16x2((uint16_t)(w0 >> 16)),
+                                        e4m3x2_to_f16x2((uint16_t)w1), e4m3x2_to_f16x2((uint16_t)(w1 >> 16))};
+                mma_f16(o[2 * a + x], va, pb[0], pb[1]);
               }
             }
             if (cnt < 16 || tok0 + cnt > all_seen) fence_proxy_async_smem();  // the zeros, before the next copy into this stage
@@ -666,6 +775,10 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
           if (++stage == kStages) stage = 0, phase ^= 1;
         }
 
+        if constexpr (kFp4) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) m[e] = m[e] == kNone ? -INFINITY : m[e];
+        }
         // ---- the warps' (m, l, o) to one: o[a] holds columns 16 a + 2 g and + 1
         // (e / 2) of rows 2 c and + 1 (e % 2); of 4 bits, columns 64 (a / 4) + 4 g + a % 4 and + 32
 #pragma unroll
@@ -810,7 +923,7 @@ cudaError_t launch_few(const KvAttentionLaunch& L, cudaStream_t stream) {
 
 int kv_attention_few_grid(int sms) { return kFewCtas * sms < kCounters ? kFewCtas * sms : kCounters; }
 size_t kv_attention_piece_bytes(int D) { return (size_t)2 * 8 * (D + 2) * sizeof(float); }
-int kv_attention_box(int page_size) { return min(page_size, kTile); }
+int kv_attention_box(int page_size, bool fp4) { return min(page_size, fp4 ? kTileOf<true> : kTileOf<false>); }
 
 cudaError_t launch_kv_attention(const KvAttentionLaunch& L, cudaStream_t stream) {
   const KvAttentionParams& p = L.p;
