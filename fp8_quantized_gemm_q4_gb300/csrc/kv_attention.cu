@@ -187,6 +187,26 @@ __device__ __forceinline__ uint16_t lds16(uint32_t a) {
   return v;
 }
 
+// Byte kByte of w, two E2M1 codes, as f16x2
+template <int kByte>
+__device__ __forceinline__ uint32_t e2m1x2_to_f16(uint32_t w) {
+  uint32_t r;
+  if constexpr (kByte == 0)
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t}\n" : "=r"(r) : "r"(w));
+  else if constexpr (kByte == 1)
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b1;\n\t}\n" : "=r"(r) : "r"(w));
+  else if constexpr (kByte == 2)
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b2;\n\t}\n" : "=r"(r) : "r"(w));
+  else
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b3;\n\t}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
 // 32 tokens of a 4-bit tile for 8 rows: scores, a step of the online softmax (as
 // softmax_step, with the distance from the reference, score * qscale - m, in place of the
 // logit, and the rows' maxima looked for only where some distance passes 8), and the
@@ -195,8 +215,8 @@ __device__ __forceinline__ uint16_t lds16(uint32_t a) {
 template <int D>
 __device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_t* vs, const int (&cnt)[2], int tok0,
                                          int all_seen, const int (&seen)[2], const float (&qscale)[2],
-                                         const uint32_t (&qb)[D / 16][2], float (&m)[2], float (&l)[2],
-                                         float (&o)[D / 16][4], const Fp4At<D>& at, int lane) {
+                                         uint32_t q, float (&m)[2], float (&l)[2], float (&o)[D / 16][4],
+                                         const Fp4At<D>& at, int lane) {
   const bool edge = min(cnt[0], cnt[1]) < 16 || tok0 + 32 > all_seen;
   if (edge) {
     // a NaN scale of V behind the last token, or where some row does not look
@@ -222,29 +242,31 @@ __device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_
   float s[2][4] = {};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t wa[D / 32], wb[D / 32], sa, sb;
-    if constexpr (D == 128) {
-      const uint4 a = lds128(codes + at.k[h][0]), b = lds128(codes + at.k[h][1]);
-      wa[0] = a.x, wa[1] = a.y, wa[2] = a.z, wa[3] = a.w, wb[0] = b.x, wb[1] = b.y, wb[2] = b.z, wb[3] = b.w;
-      sa = e4m3x2_to_f16x2(lds16(scales + at.ks + 16 * h * (D / 16)));
-      sb = e4m3x2_to_f16x2(lds16(scales + at.ks + (16 * h + 8) * (D / 16)));
-    } else {
-      const uint2 a = lds64(codes + at.k[h][0]), b = lds64(codes + at.k[h][1]);
-      wa[0] = a.x, wa[1] = a.y, wb[0] = b.x, wb[1] = b.y;
-      sa = e4m3x2_to_f16x2(lds8(scales + at.ks + 16 * h * (D / 16)));
-      sb = e4m3x2_to_f16x2(lds8(scales + at.ks + (16 * h + 8) * (D / 16)));
+    uint32_t w[2][D / 32], f[2];  // [i]: columns of token 16 h + 8 i + g, their one or two scales
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t at_scale = scales + at.ks + (16 * h + 8 * i) * (D / 16);
+      if constexpr (D == 128) {
+        const uint4 a = lds128(codes + at.k[h][i]);
+        w[i][0] = a.x, w[i][1] = a.y, w[i][2] = a.z, w[i][3] = a.w;
+        f[i] = e4m3x2_to_f16x2(lds16(at_scale));
+      } else {
+        const uint2 a = lds64(codes + at.k[h][i]);
+        w[i][0] = a.x, w[i][1] = a.y;
+        f[i] = e4m3x2_to_f16x2(lds8(at_scale));
+      }
     }
 #pragma unroll
     for (int y = 0; y < D / 32; ++y) {
-      const uint32_t fa = __byte_perm(sa, 0, y < 2 ? 0x1010 : 0x3232), fb = __byte_perm(sb, 0, y < 2 ? 0x1010 : 0x3232);
+      const uint4 b = lds128(q + y * 512);
+      const uint32_t fa = __byte_perm(f[0], 0, y < 2 ? 0x1010 : 0x3232), fb = __byte_perm(f[1], 0, y < 2 ? 0x1010 : 0x3232);
       uint32_t ka[4], kb[4];
-      e2m1x8_to_f16(wa[y], ka);
-      e2m1x8_to_f16(wb[y], kb);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint32_t f[4] = {hmul2(ka[2 * x], fa), hmul2(kb[2 * x], fb), hmul2(ka[2 * x + 1], fa), hmul2(kb[2 * x + 1], fb)};
-        mma_f16(s[h], f, qb[2 * y + x][0], qb[2 * y + x][1]);
-      }
+      e2m1x8_to_f16(w[0][y], ka);
+      e2m1x8_to_f16(w[1][y], kb);
+      const uint32_t lo[4] = {hmul2(ka[0], fa), hmul2(kb[0], fb), hmul2(ka[1], fa), hmul2(kb[1], fb)};
+      const uint32_t hi[4] = {hmul2(ka[2], fa), hmul2(kb[2], fb), hmul2(ka[3], fa), hmul2(kb[3], fb)};
+      mma_f16(s[h], lo, b.x, b.y);
+      mma_f16(s[h], hi, b.z, b.w);
     }
   }
   if (edge) {
@@ -293,49 +315,37 @@ __device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_
     }
   const uint32_t pick = (lane >> 4) ? 0x7351 : 0x6240;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    // scales of the pairs of tokens 2 c, 2 c + 1 and 8 more, of the groups 2 x + g / 4
-    uint32_t sv[D / 32][2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      uint32_t w[D / 64][2];  // four groups of the two tokens
-      if constexpr (D == 128) {
-        const uint4 r = lds128(scales + at.vs + (16 * h + 8 * t) * (D / 16));
-        w[0][0] = r.x, w[1][0] = r.y, w[0][1] = r.z, w[1][1] = r.w;
-      } else {
-        const uint2 r = lds64(scales + at.vs + (16 * h + 8 * t) * (D / 16));
-        w[0][0] = r.x, w[0][1] = r.y;
-      }
-#pragma unroll
-      for (int a = 0; a < D / 64; ++a) {
-        const uint32_t b = __byte_perm(w[a][0], w[a][1], pick);
-        sv[2 * a][t] = e4m3x2_to_f16x2((uint16_t)b);
-        sv[2 * a + 1][t] = e4m3x2_to_f16x2((uint16_t)(b >> 16));
-      }
-    }
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int a = 0; a < D / 64; ++a) {
+      // scales of the pairs of tokens 2 c, 2 c + 1 (and 8 more) for the group 4 a + g / 4 and the one two behind
+      uint32_t sv[2][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t from = scales + at.vs + (16 * h + 8 * t) * (D / 16) + 4 * a;
+        const uint32_t b = __byte_perm(lds32(from), lds32(from + D / 16), pick);
+        sv[0][t] = e4m3x2_to_f16x2((uint16_t)b);
+        sv[1][t] = e4m3x2_to_f16x2((uint16_t)(b >> 16));
+      }
       // matrix i: tokens 8 (i % 2) .. + 7 at the 32 columns of chunk 2 a + i / 2; a register has four
       // columns (4 g .. + 3) of two tokens, which become pairs of tokens after their conversion
-      uint32_t v[4], f[4][4];
+      uint32_t v[4];
       ldmatrix_x4_trans(v, codes + at.v[h][a]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t e[4];
-        e2m1x8_to_f16(v[i], e);
-        f[i][0] = __byte_perm(e[0], e[2], 0x5410);
-        f[i][1] = __byte_perm(e[0], e[2], 0x7632);
-        f[i][2] = __byte_perm(e[1], e[3], 0x5410);
-        f[i][3] = __byte_perm(e[1], e[3], 0x7632);
-      }
+      for (int x = 0; x < 2; ++x) {  // columns 2 x and 2 x + 1 of the four
+        uint32_t lo[4], hi[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint32_t va[4] = {hmul2(f[0][x], sv[2 * a][0]), hmul2(f[2][x], sv[2 * a + 1][0]),
-                                hmul2(f[1][x], sv[2 * a][1]), hmul2(f[3][x], sv[2 * a + 1][1])};
-        mma_f16(o[4 * a + x], va, pb[h][0], pb[h][1]);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t e = x ? e2m1x2_to_f16<1>(v[i]) : e2m1x2_to_f16<0>(v[i]);
+          const uint32_t f = x ? e2m1x2_to_f16<3>(v[i]) : e2m1x2_to_f16<2>(v[i]);
+          lo[i] = hmul2(__byte_perm(e, f, 0x5410), sv[i >> 1][i & 1]);
+          hi[i] = hmul2(__byte_perm(e, f, 0x7632), sv[i >> 1][i & 1]);
+        }
+        const uint32_t va[4] = {lo[0], lo[2], lo[1], lo[3]}, vb[4] = {hi[0], hi[2], hi[1], hi[3]};
+        mma_f16(o[4 * a + 2 * x], va, pb[h][0], pb[h][1]);
+        mma_f16(o[4 * a + 2 * x + 1], vb, pb[h][0], pb[h][1]);
       }
     }
-  }
   if (edge) fence_proxy_async_smem();  // the zeros, before the next copy into this stage
 }
 
@@ -378,6 +388,7 @@ struct FewSmem {
   static constexpr int kStageBytes = 2 * kTile * kRow;
   alignas(1024) uint8_t kv[kStages][kStageBytes];  // K rows, then V rows
   alignas(16) uint8_t scale[kFp4 ? kStages : 1][2][kFp4 ? kTile * D / 16 : 16];  // of K and V, 4 bits
+  uint4 q[kFp4 ? D / 32 : 1][kFp4 ? 32 : 1];  // of 4 bits: the unit's q as B fragments (in registers otherwise)
   float red[kFewWarps / 2][8 * D];
   float2 ml[kFewWarps][8];
   float4 group[kStages][kTile / 16];  // per 16 tokens: K scale, log2 of V scale, 1 / V scale (8 bits), valid tokens (int)
@@ -676,6 +687,12 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
             for (int y = 0; y < 2; ++y)
               qb[x][y] = pack_f16x2(__uint_as_float(w[2 * x + y] << 16) * mul,
                                     __uint_as_float(w[2 * x + y] & 0xffff0000u) * mul);
+          // the four warps write the same; none is at the unit after while another reads this one's
+          if constexpr (kFp4) {
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) sm.q[x][lane] = make_uint4(qb[2 * x][0], qb[2 * x][1], qb[2 * x + 1][0], qb[2 * x + 1][1]);
+            __syncwarp();
+          }
           const float undo = exp2i(-up) * p.scale_log2;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -699,7 +716,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
           } else if constexpr (kFp4) {
             const int there[2] = {max(cnt, 0), cnt2};
             fp4_tile<D>(smem_u32(sm.kv[stage]), smem_u32(sm.scale[stage]) + warp * 2 * D, &sm.scale[stage][1][warp * 2 * D], there,
-                        (tile - begin) * kTile + warp * 32, all_seen, seen, qscale, qb, m, l, o, at, lane);
+                        (tile - begin) * kTile + warp * 32, all_seen, seen, qscale, smem_u32(&sm.q[0][lane]), m, l, o, at, lane);
           } else {
             uint8_t* kt = &sm.kv[stage][warp * 16 * D];
             uint8_t* vt = kt + kTile * D;
