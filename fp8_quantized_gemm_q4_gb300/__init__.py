@@ -638,16 +638,9 @@ def _check_kv_cache_fp4(cache):
     return k, v, ks, vs, (shape[0], shape[1], shape[2], 2 * shape[3])
 
 
-def _placed(name, *tensors):
-    """Refuses tensors that are not on the current GPU, whose stream the call goes to."""
-    here = None
-    for t in tensors:
-        if not t.is_cuda:
-            _not_on_gpu(name)
-        if here is None:
-            here = _device()
-        if t.get_device() != here:
-            raise ValueError(f"{name}: every tensor is on the current GPU (cuda:{here})")
+def _misplaced(name):
+    """The calls hand addresses to kernels on the current GPU's stream: a tensor elsewhere is refused before that."""
+    raise ValueError(f"{name}: every tensor is on the current GPU")
 
 
 def _empty(shape, dtype, device, stream):
@@ -769,54 +762,59 @@ def kv_append_rotary(q, k, v, slots, positions, angles, cache, q_out=None, inter
     ``q`` None: keys and values only; ``angles`` None: no rotation.  ``q_out`` may be
     ``q`` (bf16).  Rows with a negative slot are skipped.  Returns q_out."""
     fp4 = type(cache) is KVCacheFP4
-    kc, vc, ks, vs, (pages, Hkv, page, D) = (_check_kv_cache_fp4 if fp4 else _check_kv_cache)(cache)
-    shape = k.shape
+    kc, vc, ks, vs, (pages, Hkv, page, D) = _check_kv_cache_fp4(cache) if fp4 else _check_kv_cache(cache)
     T = slots.numel()
-    if shape != (T, Hkv, D) or v.shape != shape:
-        raise ValueError(f"kv_append_rotary: k and v are [{T}, {Hkv}, {D}] for these slots and this cache")
-    (kt, kh, kd), (vt, vh, vd) = k.stride(), v.stride()
     dt = k.dtype
-    if kd != 1 or vd != 1 or v.dtype is not dt:
-        raise ValueError("kv_append_rotary: q, k and v have one type and contiguous rows of D")
+    if k.shape != (T, Hkv, D) or v.shape != k.shape:
+        raise ValueError(f"kv_append_rotary: k and v are [{T}, {Hkv}, {D}] for these slots and this cache")
     if dt is not _BF16 and dt is not _F32:
         raise TypeError(f"unsupported dtype {dt}")
+    (kt, kh, kd), (vt, vh, vd) = k.stride(), v.stride()
+    if kd != 1 or vd != 1 or v.dtype is not dt:
+        raise ValueError("kv_append_rotary: q, k and v have one type and contiguous rows of D")
     if slots.dtype is not _I32 or not slots.is_contiguous():
         raise TypeError("kv_append_rotary: slots is a contiguous int32 tensor")
-    placed = [k, v, slots, kc, vc, ks, vs]
+    here = k.get_device()
+    elsewhere = (here < 0 or v.get_device() != here or slots.get_device() != here or kc.get_device() != here
+                 or vc.get_device() != here or ks.get_device() != here or vs.get_device() != here)
     if q is None:
-        query = (0, 0, 0, 0, 0, 0)
-        Hq = 0
         if q_out is not None:
             raise ValueError("kv_append_rotary: q_out without q")
+        q_ptr = qt = qh = out_ptr = ot = oh = Hq = 0
     else:
+        shape = q.shape
         if q_out is None:
-            q_out = _empty(q.shape, _BF16, q.device, stream)
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q_out.shape != q.shape:
+            q_out = _empty(shape, _BF16, q.device, stream)
+        if len(shape) != 3 or shape[0] != T or shape[2] != D or q_out.shape != shape:
             raise ValueError(f"kv_append_rotary: q and q_out are [{T}, Hq, {D}]")
-        Hq = q.shape[1]
+        Hq = shape[1]
         (qt, qh, qd), (ot, oh, od) = q.stride(), q_out.stride()
         if qd != 1 or od != 1 or q.dtype is not dt:
             raise ValueError("kv_append_rotary: q, k and v have one type and contiguous rows of D")
         if q_out.dtype is not _BF16:
             raise TypeError("kv_append_rotary: q_out is bfloat16")
-        query = (q.data_ptr(), qt, qh, q_out.data_ptr(), ot, oh)
-        placed += (q, q_out)
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+        elsewhere = elsewhere or q.get_device() != here or q_out.get_device() != here
     if angles is None:
-        turn = (0, 0, 0, 0)
+        at_ptr = angles_ptr = rows = R = 0
     else:
         if angles.dtype is not _F32 or angles.dim() != 2 or not angles.is_contiguous():
             raise TypeError("kv_append_rotary: angles is a contiguous float32 [max_positions, R] tensor")
         if positions is None or positions.dtype is not _I32 or positions.numel() != T or not positions.is_contiguous():
             raise TypeError(f"kv_append_rotary: positions is a contiguous int32 tensor of {T}")
-        turn = (positions.data_ptr(), angles.data_ptr(), angles.shape[0], angles.shape[1])
-        placed += (positions, angles)
-    _placed("kv_append_rotary", *placed)
-    at, table, rows, R = turn
-    a = _KV_APPEND_ROTARY_ARGS.pack(*query, k.data_ptr(), v.data_ptr(), DTYPE_BF16 if dt is _BF16 else DTYPE_F32, Hq,
-                                    Hkv, D, T, kt, kh, vt, vh, slots.data_ptr(), at, table, rows, R,
-                                    1 if interleaved else 0, FMT_FP4 if fp4 else FMT_FP8, page, kc.data_ptr(),
-                                    vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages)
-    _check((_lib or load()).bs_kv_append_rotary(a, _stream(stream)))
+        rows, R = angles.shape
+        at_ptr, angles_ptr = positions.data_ptr(), angles.data_ptr()
+        elsewhere = elsewhere or positions.get_device() != here or angles.get_device() != here
+    if elsewhere or here != _device():
+        _misplaced("kv_append_rotary")
+    a = _KV_APPEND_ROTARY_ARGS.pack(q_ptr, qt, qh, out_ptr, ot, oh, k.data_ptr(), v.data_ptr(),
+                                    DTYPE_BF16 if dt is _BF16 else DTYPE_F32, Hq, Hkv, D, T, kt, kh, vt, vh,
+                                    slots.data_ptr(), at_ptr, angles_ptr, rows, R, 1 if interleaved else 0,
+                                    FMT_FP4 if fp4 else FMT_FP8, page, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(),
+                                    vs.data_ptr(), pages)
+    status = (_lib or load()).bs_kv_append_rotary(a, _stream(stream))
+    if status:
+        _check(status)
     return q_out
 
 
@@ -825,7 +823,7 @@ def kv_gather(cache, slots, out=None, stream=None):
     [T, Hkv, D] each.  Rows of negative slots are left as they were (whatever a new
     tensor holds, without ``out``)."""
     fp4 = type(cache) is KVCacheFP4
-    kc, vc, ks, vs, (pages, Hkv, page, D) = (_check_kv_cache_fp4 if fp4 else _check_kv_cache)(cache)
+    kc, vc, ks, vs, (pages, Hkv, page, D) = _check_kv_cache_fp4(cache) if fp4 else _check_kv_cache(cache)
     if slots.dtype is not _I32 or not slots.is_contiguous():
         raise TypeError("kv_gather: slots is a contiguous int32 tensor")
     shape = (slots.numel(), Hkv, D)
@@ -837,7 +835,10 @@ def kv_gather(cache, slots, out=None, stream=None):
         raise ValueError(f"kv_gather: k and v are {list(shape)} with contiguous rows of D")
     if k.dtype is not _BF16 or v.dtype is not _BF16:
         raise TypeError("kv_gather: k and v are bfloat16")
-    _placed("kv_gather", slots, kc, vc, ks, vs, k, v)
+    here = slots.get_device()
+    if (here < 0 or here != _device() or kc.get_device() != here or vc.get_device() != here or ks.get_device() != here
+            or vs.get_device() != here or k.get_device() != here or v.get_device() != here):
+        _misplaced("kv_gather")
     a = _KV_GATHER_ARGS.pack(slots.data_ptr(), shape[0], Hkv, D, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh,
                              FMT_FP4 if fp4 else FMT_FP8, page, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(),
                              vs.data_ptr(), pages)
@@ -995,12 +996,13 @@ def lora_add(x, y, a, b, cu_rows, which, scales=None, out=None, stream=None):
     B = which.numel()
     if cu_rows.numel() != B + 1:
         raise ValueError("lora_add: cu_rows is [B + 1] and which [B]")
-    placed = (x, y, a, b, cu_rows, which, out)
-    if scales is not None:
-        if scales.dtype is not _F32 or scales.numel() != n or not scales.is_contiguous():
-            raise TypeError(f"lora_add: scales is a contiguous float32 tensor of {n}")
-        placed += (scales,)
-    _placed("lora_add", *placed)
+    if scales is not None and (scales.dtype is not _F32 or scales.numel() != n or not scales.is_contiguous()):
+        raise TypeError(f"lora_add: scales is a contiguous float32 tensor of {n}")
+    here = x.get_device()
+    if (here < 0 or y.get_device() != here or a.get_device() != here or b.get_device() != here or out.get_device() != here
+            or cu_rows.get_device() != here or which.get_device() != here
+            or (scales is not None and scales.get_device() != here) or here != _device()):
+        _misplaced("lora_add")
     lib = _lib or load()
     args = (x.data_ptr(), ldx, a.data_ptr(), b.data_ptr(), 0 if scales is None else scales.data_ptr(),
             cu_rows.data_ptr(), which.data_ptr(), y.data_ptr(), ldy, out.data_ptr(), ldo, _dt(y), B, T, K, N, r, n)

@@ -81,6 +81,7 @@ struct KvRotaryParams {
   int T, Hq, Hkv, D;
   int num_pages, page_shift;
   int x_bf16;             // type of q, k and v
+  int heads, rows_each;   // the launch's choice: heads that a warp goes through, rows whose short runs it takes
   int* status;
 };
 cudaError_t launch_kv_append_rotary(const KvRotaryParams& p, cudaStream_t stream);

@@ -19,13 +19,17 @@
 namespace bsk {
 namespace {
 
-constexpr int kFp8 = 0, kFp8Wide = 1, kFp4 = 2;
-constexpr int kHeads = 4;  // heads of a token that a warp goes through
+// Heads of a token that a warp goes through: angles and places are worked out once for
+// them.  Two, all of whose elements are on their way at once, in a call that does not fill
+// the SMs with warps of eight (us, 2 / 8 heads, 32 + 16 heads, 4-bit cache with the rows
+// read back: 64 rows 4.6 / 8.3, 512 rows 8.0 / 9.4, 2047 rows 18 / 18).
+constexpr int kFewHeads = 2, kHeads = 8;
 
 template <int D>
 constexpr int kLanes = D / 16;  // lanes of a row
 template <int D>
 constexpr int kRows = 32 / kLanes<D>;  // rows of a warp's pass
+constexpr int kShort = 8;              // rows of a run that is a single warp's
 
 // A lane's two vectors of 8 elements of a row
 struct Pair {
@@ -36,30 +40,39 @@ __device__ __forceinline__ Pair vectors(const KvRotaryParams& p, int j) {
   return !p.interleaved && j < n ? Pair{j, j + n} : Pair{2 * j, 2 * j + 1};
 }
 
-// Eight elements as floats
+// A lane's sixteen elements of a row, as they lie in memory
 template <bool kBf16>
-__device__ __forceinline__ void load8(const void* x, long long at, float* v) {
-  const uint4* from = reinterpret_cast<const uint4*>(static_cast<const char*>(x) + at * (kBf16 ? 2 : 4));
-  if constexpr (kBf16) {
-    const uint4 w = *from;
-    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+struct Raw {
+  uint4 w[kBf16 ? 2 : 4];
+  __device__ __forceinline__ void load(const void* x, long long at, const Pair& v) {
+    constexpr int kEach = kBf16 ? 1 : 2;
+    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const char*>(x) + at * (kBf16 ? 2 : 4));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(in[i] << 16), v[2 * i + 1] = __uint_as_float(in[i] & 0xffff0000u);
-  } else {
-    const uint4 w = from[0], z = from[1];
-    v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y), v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
-    v[4] = __uint_as_float(z.x), v[5] = __uint_as_float(z.y), v[6] = __uint_as_float(z.z), v[7] = __uint_as_float(z.w);
+    for (int i = 0; i < kEach; ++i) w[i] = from[v.a * kEach + i], w[kEach + i] = from[v.b * kEach + i];
   }
-}
+  __device__ __forceinline__ void values(float (&v)[16]) const {
+#pragma unroll
+    for (int i = 0; i < (kBf16 ? 2 : 4); ++i) {
+      const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if constexpr (kBf16)
+          v[8 * i + 2 * x] = __uint_as_float(in[x] << 16), v[8 * i + 2 * x + 1] = __uint_as_float(in[x] & 0xffff0000u);
+        else
+          v[4 * i + x] = __uint_as_float(in[x]);
+      }
+    }
+  }
+};
 
 // The angles of a lane's eight pairs
 struct Turn {
   float c[8], s[8];
   bool on;
-  __device__ __forceinline__ void load(const KvRotaryParams& p, int row, int j) {
+  // of the row at this position (positions[row], read beside what else the row needs)
+  __device__ __forceinline__ void load(const KvRotaryParams& p, int at, int j) {
     on = j < p.rot >> 4;
     if (!on) return;
-    int at = p.positions[row];
     if ((unsigned)at >= (unsigned)p.max_positions) {
       record_status(p.status, kStatusOffsets, 47);
       at = min(max(at, 0), p.max_positions - 1);
@@ -116,38 +129,26 @@ __device__ __forceinline__ uint32_t codes4(const float* v, uint32_t scale) {
 }
 
 // Rows of a warp's pass: queries to bf16, or keys and values to 4 bits; up to kHeads
-// heads from `head` on, of kind 0 (q), 1 (k), 2 (v).
-template <bool kBf16, int D>
+// heads from `head` on, of kind 0 (q), 1 (k), 2 (v).  Everything that does not depend on
+// something read is asked for first: the heads' elements, slots, positions.
+template <bool kBf16, int D, bool kQ>
 __device__ __forceinline__ void flat_heads(const KvRotaryParams& p, int first, int kind, int head, int lane) {
-  const int j = lane % kLanes<D>, row = first + lane / kLanes<D>;
-  const int slot = row < p.T ? p.slots[row] : -1;
-  const bool ok = slot_ok(p, slot);
-  Turn turn;
-  turn.on = false;
-  if (ok && kind < 2) turn.load(p, row, j);
+  constexpr int kBatch = kBf16 ? 2 : 1;  // heads on their way
+  const int j = lane % kLanes<D>, row = min(first + lane / kLanes<D>, p.T - 1);
   const Pair at = vectors(p, j);
-  const int heads = min(kHeads, (kind ? p.Hkv : p.Hq) - head);
-  const void* x = kind ? p.x[kind - 1] : p.q;
-  const long long step = kind ? p.head_stride[kind - 1] : p.q_head_stride;
-  const long long from = row * (kind ? p.tok_stride[kind - 1] : p.q_tok_stride) + head * step;
-  float v[kHeads][16];
+  const int heads = min(p.heads, (kQ ? p.Hq : p.Hkv) - head), which = kQ ? 0 : kind - 1;
+  const void* x = kQ ? p.q : p.x[which];
+  const long long step = kQ ? p.q_head_stride : p.head_stride[which];
+  const long long from = row * (kQ ? p.q_tok_stride : p.tok_stride[which]) + head * step;
+  Raw<kBf16> raw[kBatch] = {};
+  const int slot_here = p.slots[row], position = kind < 2 && p.rot ? p.positions[row] : 0;
 #pragma unroll
-  for (int h = 0; h < kHeads; ++h)
-    if (ok && h < heads) {
-      load8<kBf16>(x, from + h * step + 8 * at.a, v[h]);
-      load8<kBf16>(x, from + h * step + 8 * at.b, v[h] + 8);
-    }
-  if (kind == 0) {
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.q_out) + row * p.qo_tok_stride + head * p.qo_head_stride;
-#pragma unroll
-    for (int h = 0; h < kHeads; ++h)
-      if (ok && h < heads) {
-        turn.apply(v[h], p.interleaved);
-        *reinterpret_cast<uint4*>(out + h * p.qo_head_stride + 8 * at.a) = to_bf16(v[h]);
-        *reinterpret_cast<uint4*>(out + h * p.qo_head_stride + 8 * at.b) = to_bf16(v[h] + 8);
-      }
-    return;
-  }
+  for (int h = 0; h < kBatch; ++h)
+    if (h < heads) raw[h].load(x, from + h * step, at);
+  const int slot = first + lane / kLanes<D> < p.T ? slot_here : -1;
+  const bool ok = slot_ok(p, slot);
+  Turn turn = {};
+  if (ok && kind < 2) turn.load(p, position, j);
   // who has the vector beside a, and the one beside b, in their groups of 16
   const int n = p.interleaved ? 0 : p.rot >> 4;
   auto owner = [&](int vec) { return vec < n ? vec : vec < 2 * n ? vec - n : vec >> 1; };
@@ -155,35 +156,51 @@ __device__ __forceinline__ void flat_heads(const KvRotaryParams& p, int first, i
   const int base = lane - j, oa = base + owner(at.a ^ 1), ob = base + owner(at.b ^ 1);
   const bool sa = second(at.a ^ 1), sb = second(at.b ^ 1);
   const long long line = ((((long long)(slot >> p.page_shift) * p.Hkv + head) << p.page_shift) + (slot & ((1 << p.page_shift) - 1)));
-  uint32_t* codes = reinterpret_cast<uint32_t*>(p.codes[kind - 1]);
-  uint8_t* scales = static_cast<uint8_t*>(p.scales[kind - 1]);
+#pragma unroll 1
+  for (int h0 = 0; h0 < heads; h0 += kBatch) {
+    if (h0) {
 #pragma unroll
-  for (int h = 0; h < kHeads; ++h) {
-    if (h >= heads) break;
-    uint32_t ma = 0, mb = 0;
-    if (ok) {
-      turn.apply(v[h], p.interleaved);
-      ma = amax8(v[h]), mb = amax8(v[h] + 8);
+      for (int h = 0; h < kBatch; ++h)
+        if (h0 + h < heads) raw[h].load(x, from + (h0 + h) * step, at);
     }
-    const uint32_t a0 = __shfl_sync(kFullMask, ma, oa), a1 = __shfl_sync(kFullMask, mb, oa);
-    const uint32_t b0 = __shfl_sync(kFullMask, ma, ob), b1 = __shfl_sync(kFullMask, mb, ob);
-    if (!ok) continue;
-    const uint32_t fa = scale4(max(ma, sa ? a1 : a0)), fb = scale4(max(mb, sb ? b1 : b0));
-    const long long to = line + ((long long)h << p.page_shift);
-    codes[to * (D / 8) + at.a] = codes4(v[h], fa);
-    codes[to * (D / 8) + at.b] = codes4(v[h] + 8, fb);
-    if (!(at.a & 1)) scales[to * (D / 16) + at.a / 2] = (uint8_t)fa;
-    if (!(at.b & 1)) scales[to * (D / 16) + at.b / 2] = (uint8_t)fb;
+#pragma unroll
+    for (int h = 0; h < kBatch; ++h) {
+      if (h0 + h >= heads) break;
+      float v[16];
+      raw[h].values(v);
+      turn.apply(v, p.interleaved);
+      if constexpr (kQ) {
+        if (!ok) continue;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.q_out) + row * p.qo_tok_stride + (head + h0 + h) * p.qo_head_stride;
+        *reinterpret_cast<uint4*>(out + 8 * at.a) = to_bf16(v);
+        *reinterpret_cast<uint4*>(out + 8 * at.b) = to_bf16(v + 8);
+      } else {
+        const uint32_t ma = amax8(v), mb = amax8(v + 8);
+        const uint32_t a0 = __shfl_sync(kFullMask, ma, oa), a1 = __shfl_sync(kFullMask, mb, oa);
+        const uint32_t b0 = __shfl_sync(kFullMask, ma, ob), b1 = __shfl_sync(kFullMask, mb, ob);
+        if (!ok) continue;
+        const uint32_t fa = scale4(max(ma, sa ? a1 : a0)), fb = scale4(max(mb, sb ? b1 : b0));
+        const long long to = line + ((long long)(h0 + h) << p.page_shift);
+        uint32_t* codes = reinterpret_cast<uint32_t*>(p.codes[which]) + to * (D / 8);
+        uint8_t* scales = static_cast<uint8_t*>(p.scales[which]) + to * (D / 16);
+        codes[at.a] = codes4(v, fa);
+        codes[at.b] = codes4(v + 8, fb);
+        if (!(at.a & 1)) scales[at.a / 2] = (uint8_t)fa;
+        if (!(at.b & 1)) scales[at.b / 2] = (uint8_t)fb;
+      }
+    }
   }
 }
 
 // A run of n rows from row `row` on into page `id` at place off, one head of the keys
-// (which = 0) or values, by kWarps warps (1, or all of the CTA); its rows up to kKeep
-// passes stay in registers between the maximum and the codes, the rest is read again.
-template <bool kBf16, int D, int kWarps, int kKeep>
+// (which = 0) or values, by a warp (n <= kShort) or by the kWarps warps of the CTA, whose
+// rows up to two passes stay in registers between the maximum and the codes and the rest
+// is read again.
+template <bool kBf16, int D, int kWarps>
 __device__ __forceinline__ void append_run(const KvRotaryParams& p, int which, int h, int row, int n, int id, int off,
                                            int thread) {
-  constexpr int kPass = kRows<D> * kWarps;
+  constexpr int kPass = kRows<D> * kWarps, kKeep = kWarps == 1 ? kShort / kPass : 2;
+  constexpr bool kRest = kWarps > 1;
   const int lane = thread & 31, j = lane % kLanes<D>, r0 = thread / kLanes<D>;
   const Pair at = vectors(p, j);
   const long long page = (long long)id * p.Hkv + h;
@@ -191,12 +208,12 @@ __device__ __forceinline__ void append_run(const KvRotaryParams& p, int which, i
   uint8_t* codes = p.codes[which] + (page << p.page_shift) * D;
   const float old = off > 0 ? *scale : 0.0f;
   auto get = [&](int r, float(&v)[16]) {
-    Turn turn;
-    turn.on = false;
-    if (which == 0) turn.load(p, row + r, j);
-    const long long from = (long long)(row + r) * p.tok_stride[which] + h * p.head_stride[which];
-    load8<kBf16>(p.x[which], from + 8 * at.a, v);
-    load8<kBf16>(p.x[which], from + 8 * at.b, v + 8);
+    Raw<kBf16> raw;
+    const int position = which == 0 && p.rot ? p.positions[row + r] : 0;
+    raw.load(p.x[which], (long long)(row + r) * p.tok_stride[which] + h * p.head_stride[which], at);
+    Turn turn = {};  // what is not set would be carried from run to run, and spilled
+    if (which == 0) turn.load(p, position, j);
+    raw.values(v);
     turn.apply(v, p.interleaved);
   };
   // running maximum of the finite magnitudes: bits one step of the exponent up keep
@@ -207,14 +224,15 @@ __device__ __forceinline__ void append_run(const KvRotaryParams& p, int which, i
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = max(top, (int)((__float_as_uint(v[i]) & 0x7fffffffu) + kUp));
   };
-  float kept[kKeep][16];
+  float kept[kKeep][16] = {};
 #pragma unroll
   for (int i = 0; i < kKeep; ++i)
     if (r0 + i * kPass < n) get(r0 + i * kPass, kept[i]);
 #pragma unroll
   for (int i = 0; i < kKeep; ++i)
     if (r0 + i * kPass < n) amax(kept[i]);
-  for (int r = r0 + kKeep * kPass; r < n; r += kPass) {
+#pragma unroll 1
+  for (int r = r0 + kKeep * kPass; kRest && r < n; r += kPass) {
     float v[16];
     get(r, v);
     amax(v);
@@ -243,7 +261,8 @@ __device__ __forceinline__ void append_run(const KvRotaryParams& p, int which, i
 #pragma unroll
   for (int i = 0; i < kKeep; ++i)
     if (r0 + i * kPass < n) put(r0 + i * kPass, kept[i]);
-  for (int r = r0 + kKeep * kPass; r < n; r += kPass) {
+#pragma unroll 1
+  for (int r = r0 + kKeep * kPass; kRest && r < n; r += kPass) {
     float v[16];
     get(r, v);
     put(r, v);
@@ -252,118 +271,126 @@ __device__ __forceinline__ void append_run(const KvRotaryParams& p, int which, i
   if (thread == 0) *scale = s;
 }
 
-// Row `row` as the head of a run: its slot and the rows that go with it, or 0.  A warp.
-__device__ __forceinline__ int run_at(const KvRotaryParams& p, int row, int lane, int& slot) {
+constexpr int kThreads = 128, kRunThreads = 256;
+constexpr int kWindow = 64;  // rows whose long runs a CTA takes
+// Rows whose short runs a warp takes, one after the other: 1, from 512 rows 4, from 4096 rows
+// 16 (us, 1 / 4 / 16: 64 single tokens 2.6 / 5.9 / 19, 512 of them 7.0 / 7.8 / 21, 1500 18 / 15 / 28,
+// 4096 54 / 45 / 51; prompts of 1024 rows 7.8 / 6.2 / 6.2, 4096 rows 34 / 27 / 25, 16384 rows
+// 121 / 91 / 83).  How the rows fall into pages is known on the device only.
+constexpr long long kManyWarps = 2432;  // 16 an SM
+
+// The runs of more than kShort rows that begin in the kWindow rows from `first` on, by a
+// warp, in any order; returns how many.
+__device__ __forceinline__ int list_runs(const KvRotaryParams& p, int first, int lane, int4* runs) {
+  constexpr int kWords = 6;  // 32 rows each, from first on: as far as a run can go
   const int page = 1 << p.page_shift;
-  // lane i has the slot of row - 1 + i
-  const int near = row - 1 + lane;
-  const int mine = near >= 0 && near < p.T ? p.slots[near] : -1;
-  slot = __shfl_sync(kFullMask, mine, 1);
-  const int before = __shfl_sync(kFullMask, mine, 0), off = slot & (page - 1);
-  if (slot < 0 || (off > 0 && before == slot - 1) || !slot_ok(p, slot)) return 0;
-  const unsigned run = __ballot_sync(kFullMask, lane == 0 || (lane - 1 < page - off && mine == slot + lane - 1));
-  int n = run == kFullMask ? 31 : __ffs(~run) - 2;
-  if (n == 31)
-    while (n < page - off && row + n < p.T && p.slots[row + n] == slot + n) ++n;
-  return n;
+  int slot[kWords];
+  unsigned inside[kWords + 1];  // rows that carry on the run of the row before
+  int last = first ? p.slots[first - 1] : -1;
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) {
+    const int r = first + 32 * w + lane;
+    slot[w] = r < p.T ? p.slots[r] : -1;
+  }
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) {
+    int before = __shfl_up_sync(kFullMask, slot[w], 1);
+    if (lane == 0) before = last;
+    last = __shfl_sync(kFullMask, slot[w], 31);
+    inside[w] = __ballot_sync(kFullMask, (slot[w] & (page - 1)) > 0 && slot[w] == before + 1 && before >= 0);
+  }
+  inside[kWords] = 0;
+  int count = 0;
+#pragma unroll
+  for (int e = 0; e < kWindow / 32; ++e) {
+    const int at = 32 * e + lane;
+    int n = 1;
+    bool on = slot[e] >= 0 && !(inside[e] >> lane & 1);
+#pragma unroll
+    for (int w = e; w < kWords; ++w) {  // the rows behind, a word from at + 1 on
+      const unsigned bits = lane == 31 ? inside[w + 1] : __funnelshift_r(inside[w], inside[w + 1], lane + 1);
+      if (on) n += bits == kFullMask ? 32 : __ffs(~bits) - 1;
+      on &= bits == kFullMask;
+    }
+    const int off = slot[e] & (page - 1);
+    const bool here = n > kShort && slot_ok(p, slot[e]);
+    const unsigned all = __ballot_sync(kFullMask, here);
+    if (here) runs[count + __popc(all & ((1u << lane) - 1))] = make_int4(first + at, min(n, page - off), slot[e] >> p.page_shift, off);
+    count += __popc(all);
+  }
+  return count;
 }
 
-constexpr int kThreads = 128, kWideThreads = 256;
-constexpr int kWindow = 64;  // rows whose runs a CTA of the wide form takes
-constexpr int kWideRows = 2048;
-
-template <bool kBf16, int D, int kFmt>
-__global__ void __launch_bounds__(kFmt == kFp8Wide ? kWideThreads : kThreads)
-    kv_append_rotary_kernel(const __grid_constant__ KvRotaryParams p, unsigned run_blocks) {
+template <bool kBf16, int D, bool kFp4>
+__global__ void __launch_bounds__(kFp4 ? kThreads : kRunThreads, kFp4 ? 7 : 4)
+    kv_append_rotary_kernel(const __grid_constant__ KvRotaryParams p, unsigned long_blocks, unsigned short_blocks) {
   griddep_wait();
   griddep_launch_dependents();
-  constexpr int kWarps = (kFmt == kFp8Wide ? kWideThreads : kThreads) / 32;
+  constexpr int kWarps = (kFp4 ? kThreads : kRunThreads) / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (kFmt != kFp4 && blockIdx.x < run_blocks) {
+  if (!kFp4 && blockIdx.x < long_blocks) {
     const unsigned block = blockIdx.x / (2 * p.Hkv), head = blockIdx.x % (2 * p.Hkv);
-    const int which = head / p.Hkv, h = head % p.Hkv, page = 1 << p.page_shift;
-    if constexpr (kFmt == kFp8) {
-      // a warp per row that begins a run
-      const int row = block * kWarps + warp;
-      if (row >= p.T) return;
-      int slot;
-      const int n = run_at(p, row, lane, slot);
-      if (n) append_run<kBf16, D, 1, 2>(p, which, h, row, n, slot >> p.page_shift, slot & (page - 1), lane);
-    } else {
-      // the runs that begin in a window of rows: short ones a warp each, others the CTA
-      constexpr int kWords = 6, kShort = 2 * kRows<D>;  // 32 rows a word, from first - 1 on
-      const int first = (int)block * kWindow;
-      int slot[kWords];
-      unsigned inside[kWords + 1];  // rows that carry on the run of the row before
-#pragma unroll
-      for (int w = 0; w < kWords; ++w) {
-        const int r = first - 1 + 32 * w + lane;
-        slot[w] = r >= 0 && r < p.T ? p.slots[r] : -1;
-      }
-      uint64_t begins = 0;
-#pragma unroll
-      for (int w = 0; w < kWords; ++w) {
-        int before = __shfl_up_sync(kFullMask, slot[w], 1);
-        const int last = w ? __shfl_sync(kFullMask, slot[w ? w - 1 : 0], 31) : -1;
-        if (lane == 0) before = last;
-        inside[w] = __ballot_sync(kFullMask, (slot[w] & (page - 1)) > 0 && slot[w] == before + 1 && before >= 0);
-        const unsigned begin = __ballot_sync(kFullMask, slot[w] >= 0) & ~inside[w];
-        // bit i: row first + i
-        if (w == 0) begins = begin >> 1;
-        if (w == 1) begins |= (uint64_t)begin << 31;
-        if (w == 2) begins |= (uint64_t)(begin & 1) << 63;
-      }
-      inside[kWords] = 0;
-      int turn = 0;
-      for (uint64_t todo = begins; todo; todo &= todo - 1) {
-        const int i = __ffsll((long long)todo);  // its place from first - 1 on
-        const int mine = __shfl_sync(kFullMask, i < 32 ? slot[0] : i < 64 ? slot[1] : slot[2], i & 31);
-        if (!slot_ok(p, mine)) continue;
-        int n = 1;
-        bool on = true;
-        const int whole = (i + 1) >> 5, rest = (i + 1) & 31;
-#pragma unroll
-        for (int w = 0; w < kWords; ++w) {
-          if (w < whole) continue;
-          const unsigned bits = __funnelshift_r(inside[w], inside[w + 1], rest);
-          if (on) n += bits == kFullMask ? 32 : __ffs(~bits) - 1;
-          on &= bits == kFullMask;
-        }
-        n = min(n, page - (mine & (page - 1)));
-        if (n <= kShort) {
-          if (turn++ % kWarps == warp)
-            append_run<kBf16, D, 1, 2>(p, which, h, first - 1 + i, n, mine >> p.page_shift, mine & (page - 1), lane);
-        } else {
-          append_run<kBf16, D, kWarps, 2>(p, which, h, first - 1 + i, n, mine >> p.page_shift, mine & (page - 1), threadIdx.x);
-        }
-      }
+    __shared__ int4 runs[kWindow / kShort];  // first row, rows, page, place in it
+    __shared__ int count;
+    if (warp == 0) {
+      const int n = list_runs(p, (int)block * kWindow, lane, runs);
+      if (lane == 0) count = n;
+    }
+    __syncthreads();
+    const int n = count;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i)
+      append_run<kBf16, D, kWarps>(p, head / p.Hkv, head % p.Hkv, runs[i].x, runs[i].y, runs[i].z, runs[i].w, threadIdx.x);
+    return;
+  }
+  if (!kFp4 && blockIdx.x < long_blocks + short_blocks) {
+    // lane i has the slot of row first - 1 + i
+    const unsigned task = (blockIdx.x - long_blocks) * kWarps + warp, head = task % (2 * p.Hkv);
+    const int first = (int)(task / (2 * p.Hkv)) * p.rows_each, page = 1 << p.page_shift, near = first - 1 + lane;
+    const int slot = near >= 0 && near < p.T ? p.slots[near] : -1;
+    int before = __shfl_up_sync(kFullMask, slot, 1);
+    if (lane == 0) before = -1;
+    const unsigned inside = __ballot_sync(kFullMask, (slot & (page - 1)) > 0 && slot == before + 1 && before >= 0);
+    unsigned todo = __ballot_sync(kFullMask, slot >= 0) & ~inside & (2u << p.rows_each) - 2;
+#pragma unroll 1
+    for (; todo; todo &= todo - 1) {
+      const int i = __ffs(todo) - 1, mine = __shfl_sync(kFullMask, slot, i), n = __ffs(~(inside >> (i + 1)));
+      if (n <= kShort && slot_ok(p, mine))
+        append_run<kBf16, D, 1>(p, head / p.Hkv, head % p.Hkv, first - 1 + i, n, mine >> p.page_shift, mine & (page - 1), lane);
     }
     return;
   }
-  const int cq = (p.Hq + kHeads - 1) / kHeads, ck = kFmt == kFp4 ? (p.Hkv + kHeads - 1) / kHeads : 0, parts = cq + 2 * ck;
-  const long long task = (long long)(blockIdx.x - run_blocks) * kWarps + warp;
+  const int cq = (p.Hq + p.heads - 1) / p.heads, ck = kFp4 ? (p.Hkv + p.heads - 1) / p.heads : 0, parts = cq + 2 * ck;
+  const long long task = (long long)(blockIdx.x - long_blocks - short_blocks) * kWarps + warp;
   const long long group = task / parts;
   const int part = (int)(task % parts);
   if (group * kRows<D> >= p.T) return;
   const int kind = part < cq ? 0 : part < cq + ck ? 1 : 2;
   const int chunk = kind == 0 ? part : part - cq - (kind - 1) * ck;
-  flat_heads<kBf16, D>(p, (int)(group * kRows<D>), kind, chunk * kHeads, lane);
+  if (!kFp4 || kind == 0)
+    flat_heads<kBf16, D, true>(p, (int)(group * kRows<D>), 0, chunk * p.heads, lane);
+  else
+    flat_heads<kBf16, D, false>(p, (int)(group * kRows<D>), kind, chunk * p.heads, lane);
 }
 
-template <bool kBf16, int D, int kFmt>
+template <bool kBf16, int D, bool kFp4>
 cudaError_t launch(const KvRotaryParams& p, cudaStream_t stream) {
-  constexpr int threads = kFmt == kFp8Wide ? kWideThreads : kThreads, warps = threads / 32;
-  const long long rows = kFmt == kFp8Wide ? kWindow : warps;
-  const long long runs = kFmt == kFp4 ? 0 : (p.T + rows - 1) / rows * 2 * p.Hkv;
-  const long long parts = (p.Hq + kHeads - 1) / kHeads + (kFmt == kFp4 ? (p.Hkv + kHeads - 1) / kHeads * 2 : 0);
-  const long long flat = ((p.T + kRows<D> - 1) / kRows<D> * parts + warps - 1) / warps;
-  return launch_kernel(kv_append_rotary_kernel<kBf16, D, kFmt>, (unsigned)(runs + flat), threads, 0, stream, 1, p,
-                       (unsigned)runs);
+  constexpr int threads = kFp4 ? kThreads : kRunThreads, warps = threads / 32;
+  KvRotaryParams q = p;
+  q.rows_each = p.T < 512 ? 1 : p.T < 4096 ? 4 : 16;
+  const long long longs = kFp4 ? 0 : ((long long)p.T + kWindow - 1) / kWindow * 2 * p.Hkv;
+  const long long shorts = kFp4 ? 0 : (((long long)p.T + q.rows_each - 1) / q.rows_each * 2 * p.Hkv + warps - 1) / warps;
+  const long long groups = (p.T + kRows<D> - 1) / kRows<D>;
+  auto flat = [&](int heads) {
+    return groups * ((p.Hq + heads - 1) / heads + (kFp4 ? (p.Hkv + heads - 1) / heads * 2 : 0));
+  };
+  q.heads = flat(kHeads) < kManyWarps ? kFewHeads : kHeads;
+  return launch_kernel(kv_append_rotary_kernel<kBf16, D, kFp4>, (unsigned)(longs + shorts + (flat(q.heads) + warps - 1) / warps), threads, 0, stream, 1, q, (unsigned)longs,
+                       (unsigned)shorts);
 }
 template <bool kBf16, int D>
 cudaError_t launch_fmt(const KvRotaryParams& p, cudaStream_t stream) {
-  if (p.fp4) return launch<kBf16, D, kFp4>(p, stream);
-  return p.T >= kWideRows ? launch<kBf16, D, kFp8Wide>(p, stream) : launch<kBf16, D, kFp8>(p, stream);
+  return p.fp4 ? launch<kBf16, D, true>(p, stream) : launch<kBf16, D, false>(p, stream);
 }
 
 // ---------------------------------------------------------------------------
