@@ -64,7 +64,7 @@ _KV_APPEND_ARGS = struct.Struct("PPiqiiqqqqPPPPPqi4x")
 _KV_ATTENTION_ARGS = struct.Struct("PqqPqqPPPPPqiPqiPPiqiiiifiPN")
 _KV_APPEND_ROTARY_ARGS = struct.Struct("PqqPqqPPiiiiqqqqqPPPqiiiiPPPPq")
 _KV_GATHER_ARGS = struct.Struct("PqiiPPqqqqiiPPPPq")
-_LORA_ARGS = struct.Struct("PqPPPPPPqPqiiqqqiiPN")
+_LORA_ARGS = struct.Struct("PqPPPPPPqPqiiqqqii")
 
 
 # Per-call kernel choices of bs_gemm_args (0 = the library's default), see
@@ -175,8 +175,6 @@ def load(path: str | None = None):
         lib.bs_kv_append_rotary.argtypes = [ctypes.c_char_p, P]
         lib.bs_kv_gather.restype = I
         lib.bs_kv_gather.argtypes = [ctypes.c_char_p, P]
-        lib.bs_lora_workspace_bytes.restype = SZ
-        lib.bs_lora_workspace_bytes.argtypes = [ctypes.c_char_p]
         lib.bs_lora_add.restype = I
         lib.bs_lora_add.argtypes = [ctypes.c_char_p, P]
         lib.bs_fp4_matvec.restype = I
@@ -1003,12 +1001,12 @@ def lora_add(x, y, a, b, cu_rows, which, scales=None, out=None, stream=None):
             or cu_rows.get_device() != here or which.get_device() != here
             or (scales is not None and scales.get_device() != here) or here != _device()):
         _misplaced("lora_add")
-    lib = _lib or load()
-    args = (x.data_ptr(), ldx, a.data_ptr(), b.data_ptr(), 0 if scales is None else scales.data_ptr(),
-            cu_rows.data_ptr(), which.data_ptr(), y.data_ptr(), ldy, out.data_ptr(), ldo, _dt(y), B, T, K, N, r, n)
-    nbytes = int(lib.bs_lora_workspace_bytes(_LORA_ARGS.pack(*args, 0, 0)))
-    ws = _empty(max(nbytes, 16), _U8, x.device, stream)
-    _check(lib.bs_lora_add(_LORA_ARGS.pack(*args, ws.data_ptr(), nbytes), _stream(stream)))
+    packed = _LORA_ARGS.pack(x.data_ptr(), ldx, a.data_ptr(), b.data_ptr(), 0 if scales is None else scales.data_ptr(),
+                             cu_rows.data_ptr(), which.data_ptr(), y.data_ptr(), ldy, out.data_ptr(), ldo, _dt(y), B, T,
+                             K, N, r, n)
+    status = (_lib or load()).bs_lora_add(packed, _stream(stream))
+    if status:
+        _check(status)
     return out
 
 

@@ -1414,21 +1414,15 @@ bs_status bs_kv_gather(const bs_kv_gather_args* a, bs_stream_t stream) {
   return BS_OK;
 }
 
-// Sizes of a bs_lora_add call, as far as its workspace depends on them.
+// Sizes of a bs_lora_add call.
 static bs_status check_lora(const bs_lora_args* a) {
-  if (a->T < 0 || a->T > INT32_MAX || a->B < 0 || a->N < 0 || a->N > INT32_MAX - 255 || a->K <= 0 || a->adapters < 0)
+  if (a->T < 0 || a->T > INT32_MAX - 255 || a->B < 0 || a->N < 0 || a->N > INT32_MAX - 255 || a->K <= 0 || a->adapters < 0)
     return fail(BS_ERR_INVALID, "lora_add: T=%lld B=%d K=%lld N=%lld adapters=%d", (long long)a->T, a->B, (long long)a->K,
                 (long long)a->N, a->adapters);
   if (a->r <= 0 || a->r > 128 || a->r % 8) return fail(BS_ERR_UNSUPPORTED, "lora_add: rank %d not a multiple of 8 up to 128", a->r);
   if (a->K % 8 || a->N % 8) return fail(BS_ERR_ALIGN, "lora_add: K=%lld or N=%lld not a multiple of 8", (long long)a->K, (long long)a->N);
   if (a->K > 1 << 22 || a->B > 8192) return fail(BS_ERR_UNSUPPORTED, "lora_add: K=%lld above 2^22 or B=%d above 8192", (long long)a->K, a->B);
   return BS_OK;
-}
-
-size_t bs_lora_workspace_bytes(const bs_lora_args* a) {
-  int sms = 0;
-  if (!a || check_lora(a) != BS_OK || !device_info(nullptr, &sms)) return 0;
-  return bsk::lora_workspace_bytes((int)a->T, a->B, (int)a->K, (int)a->N, a->r, sms);
 }
 
 bs_status bs_lora_add(const bs_lora_args* a, bs_stream_t stream) {
@@ -1450,10 +1444,6 @@ bs_status bs_lora_add(const bs_lora_args* a, bs_stream_t stream) {
   int sms = 0;
   bsk::LoraParams p = {};
   if (!device_info(&p.status, &sms)) return fail(BS_ERR_CUDA, "no current device");
-  const size_t need = bsk::lora_workspace_bytes((int)a->T, a->B, (int)a->K, (int)a->N, a->r, sms);
-  if (!a->workspace || a->workspace_bytes < need)
-    return fail(BS_ERR_INVALID, "lora_add: workspace of %zu bytes, %zu needed", a->workspace ? a->workspace_bytes : 0, need);
-  if (!aligned16(a->workspace)) return fail(BS_ERR_ALIGN, "lora_add: workspace must be 16-byte aligned");
   p.x = a->x;
   p.ldx = a->ldx;
   p.a = a->a;
@@ -1472,7 +1462,6 @@ bs_status bs_lora_add(const bs_lora_args* a, bs_stream_t stream) {
   p.N = (int)a->N;
   p.r = a->r;
   p.adapters = a->adapters;
-  p.work = static_cast<float*>(a->workspace);
   cudaError_t e = bsk::launch_lora(p, sms, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "lora_add launch");
   return BS_OK;

@@ -179,10 +179,8 @@ struct LoraParams {
   long long ldo;
   int bf16;               // type of y and out
   int T, B, K, N, r, adapters;
-  float* work;
   int* status;
 };
-size_t lora_workspace_bytes(int T, int B, int K, int N, int r, int sms);
 cudaError_t launch_lora(const LoraParams& p, int sms, cudaStream_t stream);
 
 }  // namespace bsk

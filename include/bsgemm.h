@@ -809,8 +809,6 @@ bs_status bs_fp4_matvec(const bs_fp4_matvec_args *args, bs_stream_t stream);
  *              other overlap
  *   r          a multiple of 8, 8 .. 128; K and N multiples of 8, K <= 2^22, B <= 8192
  *   all matrices 16-byte aligned, row strides multiples of 8 elements
- *   workspace  device scratch of bs_lora_workspace_bytes(args) bytes, 16-byte aligned,
- *              of this call alone until it has run; its contents do not matter
  * ------------------------------------------------------------------------- */
 typedef struct {
     const void *x;
@@ -826,10 +824,7 @@ typedef struct {
     int B;
     int64_t T, K, N;
     int r, adapters;
-    void *workspace;
-    size_t workspace_bytes;
 } bs_lora_args;
-size_t bs_lora_workspace_bytes(const bs_lora_args *args);
 bs_status bs_lora_add(const bs_lora_args *args, bs_stream_t stream);
 
 /* ---------------------------------------------------------------------------

@@ -88,11 +88,10 @@ def test_attention_refusals(bs):
 
 
 def test_lora_refusals(bs):
-    names = "x ldx a b scales cu_rows which y ldy out ldo dtype B T K N r adapters workspace workspace_bytes".split()
-    good = dict(zip(names, (F, 256, F, F, F, F, F, F, 512, 2 * F, 512, 1, 3, 10, 256, 512, 16, 4, F, 1 << 30)))
+    names = "x ldx a b scales cu_rows which y ldy out ldo dtype B T K N r adapters".split()
+    good = dict(zip(names, (F, 256, F, F, F, F, F, F, 512, 2 * F, 512, 1, 3, 10, 256, 512, 16, 4)))
     lib = bs.load()
     assert lib.bs_lora_add(None, None) == bs.BS_ERR_INVALID
-    assert lib.bs_lora_workspace_bytes(None) == 0
     call = caller(lib.bs_lora_add, bs._LORA_ARGS, good)
     for kw in (dict(T=-1), dict(T=1 << 31), dict(B=-1), dict(K=0), dict(N=-8), dict(adapters=-1), dict(dtype=3), dict(ldx=248),
                dict(ldy=504), dict(ldo=504), dict(out=F, ldo=1024)):
