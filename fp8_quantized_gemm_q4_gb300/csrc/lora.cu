@@ -1,16 +1,12 @@
 // lora.cu -- low-rank adapters of many requests beside a projection that they share:
 //   out = y + s_a (x A_a^T) B_a^T,  a = the adapter of the row's request.
 //
-// A tile is up to 16 or 64 rows of one request, and a cluster of CTAs takes it in one
-// launch: the CTAs share K, each warp brings a slice of x and of A to registers and
-// multiplies (mma.sync, 16 rows on M, ranks on N); the partial products t = x A^T meet in
-// distributed shared memory, where every CTA adds them in the same order; then the CTAs
-// share N.  t stays fp32 and enters the second product scaled and split into two bf16
-// (hi + lo, within 2^-17 of it; products with the bf16 B are exact, sums fp32).
-// Operands come as 16 consecutive bytes of a row a lane: a lane's k are 8 c .. + 7 of
-// every 32, the same for both operands, and its columns 8 c .. + 7 of 32, so that neither
-// weights nor outputs pass through shared memory.  What the second product reads of B and y
-// does not depend on t and is on its way before t is there.
+// A tile is up to 8 or 64 rows of one request, and a cluster of CTAs takes it in one
+// launch: the CTAs share K, and their partial products t = x A^T (mma.sync, rows on M,
+// ranks on N) meet in distributed shared memory, where every CTA adds them in the same
+// order; then the CTAs share N.  t stays fp32 and enters the second product scaled and
+// split into two bf16 (hi + lo, within 2^-17 of it; products with the bf16 B are exact,
+// sums fp32).
 #include "decode.h"
 #include "decode.cuh"
 
@@ -52,125 +48,179 @@ __device__ __forceinline__ Rows rows_of(const LoraParams& p, int b) {
   return {r0, r0 < 0 || r1 <= r0 ? 0 : max(0, min(r1, p.T) - r0), r0 < 0 || r1 < r0 || r1 > p.T || p.which[b] >= p.adapters};
 }
 
-// kBlocks: blocks of 16 rows of a tile (1 or 4); kRank: the ranks that there is room for
-template <int kBlocks, int kRank>
-struct Smem {
-  static constexpr int kRows = 16 * kBlocks;
-  static constexpr int kSplit = kWarps / kBlocks;  // warps that share a block's K
-  float part[kSplit][kRows][kRank];  // of the warps; [0]: of the CTA
-  __nv_bfloat16 t[2][kRows][kRank];  // hi, lo of the scaled t
-  long long scan[kWarps];
-  int4 tile;                         // first row, rows, adapter, whether there is one
+// The cluster's tile: requests in order, their rows in tiles of kRows.
+struct Tile {
+  int row0, rows, id;  // first row, rows, adapter (-1: none)
+  bool there;
 };
-
-template <int kBlocks, int kRank>
-__global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : 2) lora_kernel(const __grid_constant__ LoraParams p) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  using S = Smem<kBlocks, kRank>;
-  S& sm = *reinterpret_cast<S*>(smem_raw);
-  constexpr int kNT = kRank / 8, kKB = kRank / 32;  // tiles of 8 ranks, blocks of 32
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int size = (int)cluster_size(), rank = (int)cluster_ctarank();
-  const int tile = (int)(blockIdx.x / size);
-  griddep_wait();
-  griddep_launch_dependents();
-
-  // ---- the cluster's tile: requests in order, their rows in tiles of kRows
-  if (tid == 0) sm.tile = make_int4(0, 0, -1, 0);
-  {
-    const int per = (p.B + kThreads - 1) / kThreads, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    long long mine = 0;  // offsets that break the contract may claim rows twice
+template <int kRows>
+__device__ __forceinline__ Tile find_tile(const LoraParams& p, int tile, long long* scan, int4* found) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (p.B + kThreads - 1) / kThreads, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  if (tid == 0) *found = make_int4(0, 0, -1, 0);
+  long long mine = 0;  // offsets that break the contract may claim rows twice
+  for (int b = b0; b < b1; ++b) {
+    const Rows r = rows_of(p, b);
+    if (r.bad && blockIdx.x == 0) record_status(p.status, kStatusOffsets, 57);
+    mine += (r.n + kRows - 1) / kRows;
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long v = __shfl_up_sync(kFullMask, incl, d);
+    if (lane >= d) incl += v;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) before += w < warp ? scan[w] : 0;
+  if (tile >= before && tile < before + mine) {
     for (int b = b0; b < b1; ++b) {
       const Rows r = rows_of(p, b);
-      if (r.bad && blockIdx.x == 0) record_status(p.status, kStatusOffsets, 57);
-      mine += (r.n + S::kRows - 1) / S::kRows;
-    }
-    long long incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long v = __shfl_up_sync(kFullMask, incl, d);
-      if (lane >= d) incl += v;
-    }
-    if (lane == 31) sm.scan[warp] = incl;
-    __syncthreads();
-    long long before = incl - mine;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) before += w < warp ? sm.scan[w] : 0;
-    if (tile >= before && tile < before + mine) {
-      for (int b = b0; b < b1; ++b) {
-        const Rows r = rows_of(p, b);
-        const int n = (r.n + S::kRows - 1) / S::kRows;
-        const long long i = tile - before;
-        if (i < n) {
-          const int w = p.which[b];
-          const int at = (int)i * S::kRows;
-          sm.tile = make_int4(r.row0 + at, min(S::kRows, r.n - at), w >= p.adapters ? -1 : w, 1);
-          break;
-        }
-        before += n;
+      const int n = (r.n + kRows - 1) / kRows;
+      const long long i = tile - before;
+      if (i < n) {
+        const int w = p.which[b], at = (int)i * kRows;
+        *found = make_int4(r.row0 + at, min(kRows, r.n - at), w >= p.adapters ? -1 : w, 1);
+        break;
       }
-    }
-    __syncthreads();
-  }
-  const int row0 = sm.tile.x, rows = sm.tile.y, id = sm.tile.z;
-  if (!sm.tile.w) return;  // all CTAs of the cluster alike
-
-  const int es = p.bf16 ? 2 : 4;
-  const int chunks = (p.N + 31) / 32;  // of 32 columns, shared by the CTAs
-  const int c0 = (int)((long long)chunks * rank / size), c1 = (int)((long long)chunks * (rank + 1) / size);
-  if (id < 0) {
-    if (p.out == p.y) return;
-    const int n0 = c0 * 32, n1 = min(p.N, c1 * 32), vecs = (n1 - n0) * es / 16;
-    for (int x = tid; x < rows * vecs; x += kThreads) {
-      const long long row = row0 + x / vecs;
-      const int at = x % vecs;
-      const char* from = static_cast<const char*>(p.y) + (row * p.ldy + n0) * es;
-      reinterpret_cast<uint4*>(static_cast<char*>(p.out) + (row * p.ldo + n0) * es)[at] = reinterpret_cast<const uint4*>(from)[at];
-    }
-    return;
-  }
-
-  // ---- t = x A^T: a warp has a block of 16 rows and a share of K
-  const int block = warp % kBlocks, split = warp / kBlocks;
-  const bool works = 16 * block < rows;
-  const int ra = 16 * block + g, rb = ra + 8;  // this lane's rows of the tile
-  {
-    float acc[kNT][4] = {};
-    const int blocks = (p.K + 31) / 32, parts = size * S::kSplit, part = rank * S::kSplit + split;
-    const int k0 = (int)((long long)blocks * part / parts), k1 = (int)((long long)blocks * (part + 1) / parts);
-    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + (long long)row0 * p.ldx;
-    const __nv_bfloat16* a = static_cast<const __nv_bfloat16*>(p.a) + (long long)id * p.r * p.K;
-    if (works) {
-#pragma unroll 2
-      for (int k = k0; k < k1; ++k) {
-        const int at = 32 * k + 8 * c;
-        const bool in = at < p.K;
-        const uint4 xa = load16(x + ra * p.ldx + at, in && ra < rows), xb = load16(x + rb * p.ldx + at, in && rb < rows);
-        uint4 w[kNT];
-#pragma unroll
-        for (int n = 0; n < kNT; ++n) w[n] = load16(a + (long long)(8 * n + g) * p.K + at, in && 8 * n < p.r);
-        const uint32_t f0[4] = {xa.x, xb.x, xa.y, xb.y}, f1[4] = {xa.z, xb.z, xa.w, xb.w};
-#pragma unroll
-        for (int n = 0; n < kNT; ++n) {
-          if (8 * n >= p.r) break;
-          mma_bf16_16x8(acc[n], f0, w[n].x, w[n].y);
-          mma_bf16_16x8(acc[n], f1, w[n].z, w[n].w);
-        }
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < kNT; ++n) {
-      *reinterpret_cast<float2*>(&sm.part[split][ra][8 * n + 2 * c]) = make_float2(acc[n][0], acc[n][1]);
-      *reinterpret_cast<float2*>(&sm.part[split][rb][8 * n + 2 * c]) = make_float2(acc[n][2], acc[n][3]);
+      before += n;
     }
   }
   __syncthreads();
-  constexpr int kVecs = S::kRows * kRank / 4;  // of t
+  return {found->x, found->y, found->z, found->w != 0};
+}
+
+// Rows without an adapter: y to out, columns n0 .. n1 - 1
+__device__ __forceinline__ void copy_rows(const LoraParams& p, const Tile& t, int n0, int n1) {
+  if (p.out == p.y || n1 <= n0) return;
+  const int es = p.bf16 ? 2 : 4, vecs = (n1 - n0) * es / 16;
+  for (int x = threadIdx.x; x < t.rows * vecs; x += kThreads) {
+    const long long row = t.row0 + x / vecs;
+    const char* from = static_cast<const char*>(p.y) + (row * p.ldy + n0) * es;
+    reinterpret_cast<uint4*>(static_cast<char*>(p.out) + (row * p.ldo + n0) * es)[x % vecs] = reinterpret_cast<const uint4*>(from)[x % vecs];
+  }
+}
+
+// t of the cluster: the CTAs' sums (kVecs float4 at `sums` in each) added in order of rank,
+// scaled, as two bf16 at hi and lo
+template <int kVecs>
+__device__ __forceinline__ void gather_t(const LoraParams& p, int id, int size, const float* sums, __nv_bfloat16* hi, __nv_bfloat16* lo) {
+  const float scale = p.scales ? p.scales[id] : 1.0f;
+  const uint32_t mine = smem_u32(sums);
+  for (int x = threadIdx.x; x < kVecs; x += kThreads) {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int r = 0; r < size; ++r) {
+      const float4 e = ld_cluster(mapa_shared(mine + 16 * x, r));
+      v.x += e.x, v.y += e.y, v.z += e.z, v.w += e.w;
+    }
+    v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
+    const uint32_t h0 = pack_bf16x2(v.x, v.y), h1 = pack_bf16x2(v.z, v.w);
+    const uint32_t l0 = pack_bf16x2(v.x - __uint_as_float(h0 << 16), v.y - __uint_as_float(h0 & 0xffff0000u));
+    const uint32_t l1 = pack_bf16x2(v.z - __uint_as_float(h1 << 16), v.w - __uint_as_float(h1 & 0xffff0000u));
+    reinterpret_cast<uint2*>(hi)[x] = make_uint2(h0, h1);
+    reinterpret_cast<uint2*>(lo)[x] = make_uint2(l0, l1);
+  }
+}
+
+// Eight columns of a row of y: read, and written with the products added (accumulators e
+// and e + 1 of the four tiles of a chunk)
+struct Eight {
+  uint4 v[2];
+  __device__ __forceinline__ void load(const LoraParams& p, long long row, int n, bool in) {
+    const char* from = static_cast<const char*>(p.y) + (row * p.ldy + n) * (p.bf16 ? 2 : 4);
+    v[0] = load16(from, in);
+    if (!p.bf16) v[1] = load16(from + 16, in);
+  }
+  __device__ __forceinline__ void put(const LoraParams& p, long long row, int n, bool in, const float (&acc)[4][4], int e) const {
+    if (!in) return;
+    char* to = static_cast<char*>(p.out) + (row * p.ldo + n) * (p.bf16 ? 2 : 4);
+    if (p.bf16) {
+      const uint32_t o[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = pack_bf16x2(__uint_as_float(o[i] << 16) + acc[i][e], __uint_as_float(o[i] & 0xffff0000u) + acc[i][e + 1]);
+      *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        reinterpret_cast<float4*>(to)[i] =
+            make_float4(__uint_as_float(v[i].x) + acc[2 * i][e], __uint_as_float(v[i].y) + acc[2 * i][e + 1],
+                        __uint_as_float(v[i].z) + acc[2 * i + 1][e], __uint_as_float(v[i].w) + acc[2 * i + 1][e + 1]);
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Few rows a request: tiles of 8 rows.  Operands come as 16 consecutive bytes of a row a
+// lane: a lane's k are 8 c .. + 7 of every 32, the same for both operands, and its columns
+// 8 c .. + 7 of 32, so that neither weights nor outputs pass through shared memory.  What
+// the second product reads of B and y does not depend on t and is on its way before t is
+// there.
+// ---------------------------------------------------------------------------
+constexpr int kFewRows = 8;
+
+template <int kRank>
+struct FewSmem {
+  float part[kWarps][kFewRows][kRank];  // of the warps; [0]: of the CTA
+  __nv_bfloat16 t[2][kFewRows][kRank];  // hi, lo of the scaled t
+  long long scan[kWarps];
+  int4 tile;
+};
+
+template <int kRank>
+__global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : kRank > 32 ? 2 : 4) lora_few_kernel(const __grid_constant__ LoraParams p) {
+  __shared__ __align__(16) FewSmem<kRank> sm;
+  constexpr int kNT = kRank / 8, kKB = kRank / 32;  // tiles of 8 ranks, blocks of 32
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int size = (int)cluster_size(), rank = (int)cluster_ctarank();
+  griddep_wait();
+  griddep_launch_dependents();
+  const Tile tile = find_tile<kFewRows>(p, (int)(blockIdx.x / size), sm.scan, &sm.tile);
+  if (!tile.there) return;  // all CTAs of the cluster alike
+  const int chunks = (p.N + 31) / 32;  // of 32 columns, shared by the CTAs
+  const int c0 = (int)((long long)chunks * rank / size), c1 = (int)((long long)chunks * (rank + 1) / size);
+  if (tile.id < 0) {
+    copy_rows(p, tile, c0 * 32, min(p.N, c1 * 32));
+    return;
+  }
+  const bool row_in = g < tile.rows;
+  {
+    // ---- t = x A^T: the warps share the CTA's part of K
+    float acc[kNT][4] = {};
+    const int blocks = (p.K + 31) / 32, parts = size * kWarps, part = rank * kWarps + warp;
+    const int k0 = (int)((long long)blocks * part / parts), k1 = (int)((long long)blocks * (part + 1) / parts);
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + (tile.row0 + (long long)g) * p.ldx;
+    const __nv_bfloat16* a = static_cast<const __nv_bfloat16*>(p.a) + (long long)tile.id * p.r * p.K;
+#pragma unroll 2
+    for (int k = k0; k < k1; ++k) {
+      const int at = 32 * k + 8 * c;
+      const bool in = at < p.K;
+      const uint4 xa = load16(x + at, in && row_in);
+      uint4 w[kNT];
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) w[n] = load16(a + (long long)(8 * n + g) * p.K + at, in && 8 * n < p.r);
+      const uint32_t f0[4] = {xa.x, 0, xa.y, 0}, f1[4] = {xa.z, 0, xa.w, 0};
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        if (8 * n >= p.r) break;
+        mma_bf16_16x8(acc[n], f0, w[n].x, w[n].y);
+        mma_bf16_16x8(acc[n], f1, w[n].z, w[n].w);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) *reinterpret_cast<float2*>(&sm.part[warp][g][8 * n + 2 * c]) = make_float2(acc[n][0], acc[n][1]);
+  }
+  __syncthreads();
+  constexpr int kVecs = kFewRows * kRank / 4;  // of t
   for (int x = tid; x < kVecs; x += kThreads) {
     float4* at = reinterpret_cast<float4*>(&sm.part[0][0][0]) + x;
     float4 v = *at;
 #pragma unroll
-    for (int s = 1; s < S::kSplit; ++s) {
+    for (int s = 1; s < kWarps; ++s) {
       const float4 w = at[s * kVecs];
       v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
     }
@@ -179,11 +229,14 @@ __global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : 2) lora_kernel(cons
   __syncwarp();
   cluster_arrive();
 
-  // ---- out = y + t B^T: a warp has a block of 16 rows and every kSplit-th chunk of columns.
-  // Tile i of a chunk has the columns 8 (n / 2) + 2 i + n % 2, n = 0 .. 7.
-  const __nv_bfloat16* bw = static_cast<const __nv_bfloat16*>(p.b) + (long long)id * p.N * p.r;
+  // ---- out = y + t B^T: a warp has every eighth chunk of columns.  Tile i of a chunk has
+  // the columns 8 (n / 2) + 2 i + n % 2, n = 0 .. 7.
+  const __nv_bfloat16* bw = static_cast<const __nv_bfloat16*>(p.b) + (long long)tile.id * p.N * p.r;
+  const long long row = tile.row0 + (long long)g;
   uint4 w[4][kKB];
-  auto load_b = [&](int chunk) {
+  Eight y;
+  auto load = [&](int chunk) {
+    y.load(p, row, 32 * chunk + 8 * c, row_in && chunk < c1 && 32 * chunk + 8 * c < p.N);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int n = 32 * chunk + 8 * (g >> 1) + 2 * i + (g & 1);
@@ -192,113 +245,245 @@ __global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : 2) lora_kernel(cons
         w[i][k] = load16(bw + (long long)n * p.r + 32 * k + 8 * c, chunk < c1 && n < p.N && 32 * k + 8 * c < p.r);
     }
   };
-  int chunk = works ? c0 + split : c1;
-  load_b(chunk);
+  int chunk = c0 + warp;
+  load(chunk);
   __syncwarp();
   cluster_wait();
-  {
-    const float scale = p.scales ? p.scales[id] : 1.0f;
-    const uint32_t mine = smem_u32(&sm.part[0][0][0]);
-    for (int x = tid; x < kVecs; x += kThreads) {
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-      for (int r = 0; r < size; ++r) {
-        const float4 e = ld_cluster(mapa_shared(mine + 16 * x, r));
-        v.x += e.x, v.y += e.y, v.z += e.z, v.w += e.w;
-      }
-      v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
-      const uint32_t h0 = pack_bf16x2(v.x, v.y), h1 = pack_bf16x2(v.z, v.w);
-      const uint32_t l0 = pack_bf16x2(v.x - __uint_as_float(h0 << 16), v.y - __uint_as_float(h0 & 0xffff0000u));
-      const uint32_t l1 = pack_bf16x2(v.z - __uint_as_float(h1 << 16), v.w - __uint_as_float(h1 & 0xffff0000u));
-      reinterpret_cast<uint2*>(&sm.t[0][0][0])[x] = make_uint2(h0, h1);
-      reinterpret_cast<uint2*>(&sm.t[1][0][0])[x] = make_uint2(l0, l1);
-    }
-  }
+  gather_t<kVecs>(p, tile.id, size, &sm.part[0][0][0], &sm.t[0][0][0], &sm.t[1][0][0]);
   __syncthreads();
   cluster_arrive();  // this CTA has read the others' sums
-  if (works) {
-    uint4 ta[2][kKB], tb[2][kKB];
+  uint4 t[2][kKB];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int k = 0; k < kKB; ++k) t[h][k] = *reinterpret_cast<const uint4*>(&sm.t[h][g][32 * k + 8 * c]);
+#pragma unroll 1
+  for (; chunk < c1; chunk += kWarps) {
+    float acc[4][4] = {};
+#pragma unroll
+    for (int h = 1; h >= 0; --h)
 #pragma unroll
       for (int k = 0; k < kKB; ++k) {
-        ta[h][k] = *reinterpret_cast<const uint4*>(&sm.t[h][ra][32 * k + 8 * c]);
-        tb[h][k] = *reinterpret_cast<const uint4*>(&sm.t[h][rb][32 * k + 8 * c]);
-      }
-    const char* y = static_cast<const char*>(p.y);
-    char* out = static_cast<char*>(p.out);
-#pragma unroll 1
-    for (; chunk < c1; chunk += S::kSplit) {
-      const int n = 32 * chunk + 8 * c;
-      const bool ina = n < p.N && ra < rows, inb = n < p.N && rb < rows;
-      uint4 ya[2], yb[2];
+        const uint32_t f0[4] = {t[h][k].x, 0, t[h][k].y, 0}, f1[4] = {t[h][k].z, 0, t[h][k].w, 0};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        ya[i] = load16(y + ((row0 + ra) * p.ldy + n) * es + 16 * i, ina && (i == 0 || !p.bf16));
-        yb[i] = load16(y + ((row0 + rb) * p.ldy + n) * es + 16 * i, inb && (i == 0 || !p.bf16));
-      }
-      float acc[4][4] = {};
-#pragma unroll
-      for (int h = 1; h >= 0; --h)
-#pragma unroll
-        for (int k = 0; k < kKB; ++k) {
-          const uint32_t f0[4] = {ta[h][k].x, tb[h][k].x, ta[h][k].y, tb[h][k].y};
-          const uint32_t f1[4] = {ta[h][k].z, tb[h][k].z, ta[h][k].w, tb[h][k].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            mma_bf16_16x8(acc[i], f0, w[i][k].x, w[i][k].y);
-            mma_bf16_16x8(acc[i], f1, w[i][k].z, w[i][k].w);
-          }
+        for (int i = 0; i < 4; ++i) {
+          mma_bf16_16x8(acc[i], f0, w[i][k].x, w[i][k].y);
+          mma_bf16_16x8(acc[i], f1, w[i][k].z, w[i][k].w);
         }
-      load_b(chunk + S::kSplit);
-      auto put = [&](const uint4(&old)[2], long long row, int e, bool in) {
-        if (!in) return;
-        char* to = out + (row * p.ldo + n) * es;
-        if (p.bf16) {
-          const uint32_t o[4] = {old[0].x, old[0].y, old[0].z, old[0].w};
-          uint32_t v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[i] = pack_bf16x2(__uint_as_float(o[i] << 16) + acc[i][e], __uint_as_float(o[i] & 0xffff0000u) + acc[i][e + 1]);
-          *reinterpret_cast<uint4*>(to) = make_uint4(v[0], v[1], v[2], v[3]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            reinterpret_cast<float4*>(to)[i] =
-                make_float4(__uint_as_float(old[i].x) + acc[2 * i][e], __uint_as_float(old[i].y) + acc[2 * i][e + 1],
-                            __uint_as_float(old[i].z) + acc[2 * i + 1][e], __uint_as_float(old[i].w) + acc[2 * i + 1][e + 1]);
-        }
-      };
-      put(ya, row0 + ra, 0, ina);
-      put(yb, row0 + rb, 2, inb);
-    }
+      }
+    const Eight old = y;
+    load(chunk + kWarps);
+    old.put(p, row, 32 * chunk + 8 * c, row_in && 32 * chunk + 8 * c < p.N, acc, 0);
   }
   __syncwarp();
   cluster_wait();  // until the others have read this CTA's sums
 }
 
-template <int kBlocks, int kRank>
-cudaError_t launch(const LoraParams& p, int cluster, long long tiles, cudaStream_t stream) {
-  constexpr int kSmem = (int)sizeof(Smem<kBlocks, kRank>);
-  const cudaError_t e = cudaFuncSetAttribute(lora_kernel<kBlocks, kRank>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(lora_kernel<kBlocks, kRank>, (unsigned)(tiles * cluster), kThreads, kSmem, stream, cluster, p);
+// ---------------------------------------------------------------------------
+// Many rows a request: tiles of 64 rows.  x and A, then B, come through a ring of shared
+// memory with cp.async, so that the four warps that need a slice of weights read it from
+// L2 once; y goes from global memory to registers a chunk ahead.  Warps: a block of 16
+// rows and half the ranks, then half the columns of a chunk.
+// ---------------------------------------------------------------------------
+constexpr int kManyRows = 64, kSlice = 64;  // rows of a tile; K, or columns, of a stage
+constexpr int kStages = 4;
+
+template <int kRank>
+struct ManySmem {
+  static constexpr int kStageBytes = (kManyRows + kRank) * kSlice * 2;  // x and A; or B, which is smaller
+  alignas(128) uint8_t ring[kStages][kStageBytes];
+  float sum[kManyRows][kRank];           // the CTA's part of t
+  __nv_bfloat16 t[2][kManyRows][kRank];  // hi, lo of the scaled t
+  long long scan[kWarps];
+  int4 tile;
+};
+
+// Place of the 16-byte piece `chunk` of row `row` in rows of kBytes, pieces exchanged so that
+// eight rows of a column of pieces meet all banks
+template <int kBytes>
+__device__ __forceinline__ uint32_t piece_at(int row, int chunk) {
+  if constexpr (kBytes == 64) return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+  return row * kBytes + ((chunk ^ (row & 7)) << 4);
 }
-template <int kBlocks>
-cudaError_t launch_rank(const LoraParams& p, int cluster, long long tiles, cudaStream_t stream) {
-  if (p.r <= 32) return launch<kBlocks, 32>(p, cluster, tiles, stream);
-  return p.r <= 64 ? launch<kBlocks, 64>(p, cluster, tiles, stream) : launch<kBlocks, 128>(p, cluster, tiles, stream);
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+template <int kRank>
+__global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : 2) lora_many_kernel(const __grid_constant__ LoraParams p) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  using S = ManySmem<kRank>;
+  S& sm = *reinterpret_cast<S*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int size = (int)cluster_size(), rank = (int)cluster_ctarank();
+  griddep_wait();
+  griddep_launch_dependents();
+  const Tile tile = find_tile<kManyRows>(p, (int)(blockIdx.x / size), sm.scan, &sm.tile);
+  if (!tile.there) return;  // all CTAs of the cluster alike
+  const int chunks = (p.N + kSlice - 1) / kSlice;  // of columns, shared by the CTAs
+  const int c0 = (int)((long long)chunks * rank / size), c1 = (int)((long long)chunks * (rank + 1) / size);
+  if (tile.id < 0) {
+    copy_rows(p, tile, c0 * kSlice, min(p.N, c1 * kSlice));
+    return;
+  }
+  const int block = warp & 3, half = warp >> 2;
+  const bool works = 16 * block < tile.rows;
+  const uint32_t ring = smem_u32(sm.ring[0]);
+
+  // ---- t = x A^T
+  constexpr int kNT = kRank / 16;  // tiles of 8 ranks of a warp
+  {
+    const int slices = (p.K + kSlice - 1) / kSlice;
+    const int k0 = (int)((long long)slices * rank / size), k1 = (int)((long long)slices * (rank + 1) / size);
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + (long long)tile.row0 * p.ldx;
+    const __nv_bfloat16* a = static_cast<const __nv_bfloat16*>(p.a) + (long long)tile.id * p.r * p.K;
+    auto issue = [&](int k) {
+      if (k < k1) {
+        const uint32_t to = ring + (k - k0) % kStages * S::kStageBytes;
+#pragma unroll
+        for (int i = 0; i < kManyRows * 8 / kThreads; ++i) {
+          const int v = i * kThreads + tid, row = v >> 3, piece = v & 7, at = kSlice * k + 8 * piece;
+          const bool in = row < tile.rows && at < p.K;
+          cp_async16(to + piece_at<128>(row, piece), in ? x + row * p.ldx + at : x, in);
+        }
+#pragma unroll
+        for (int i = 0; i < kRank * 8 / kThreads; ++i) {
+          const int v = i * kThreads + tid, row = v >> 3, piece = v & 7, at = kSlice * k + 8 * piece;
+          const bool in = row < p.r && at < p.K;
+          cp_async16(to + kManyRows * 128 + piece_at<128>(row, piece), in ? a + (long long)row * p.K + at : a, in);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    float acc[kNT][4] = {};
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) issue(k0 + s);
+#pragma unroll 1
+    for (int k = k0; k < k1; ++k) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncthreads();  // everybody's part of the stage is there, and the stage before has been read
+      issue(k + kStages - 1);
+      if (!works) continue;
+      const uint32_t xs = ring + (k - k0) % kStages * S::kStageBytes, as = xs + kManyRows * 128;
+#pragma unroll
+      for (int j = 0; j < kSlice / 16; ++j) {
+        uint32_t f[4];
+        ldmatrix_x4(f, xs + piece_at<128>(16 * block + (lane & 15), 2 * j + (lane >> 4)));
+#pragma unroll
+        for (int n = 0; n < kNT; n += 2) {
+          uint32_t w[4];  // two tiles of 8 ranks
+          ldmatrix_x4(w, as + piece_at<128>(8 * (half * kNT + n) + (lane & 7) + 8 * (lane >> 4), 2 * j + ((lane >> 3) & 1)));
+          mma_bf16_16x8(acc[n], f, w[0], w[1]);
+          mma_bf16_16x8(acc[n + 1], f, w[2], w[3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+      float* at = &sm.sum[16 * block + g][8 * (half * kNT + n) + 2 * c];
+      *reinterpret_cast<float2*>(at) = make_float2(acc[n][0], acc[n][1]);
+      *reinterpret_cast<float2*>(at + 8 * kRank) = make_float2(acc[n][2], acc[n][3]);
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();  // the ring has been read
+  cluster_arrive();
+
+  // ---- out = y + t B^T.  Tile i of 32 columns has 8 (n / 2) + 2 i + n % 2, n = 0 .. 7, so that a
+  // lane ends with eight columns in a row.
+  constexpr int kRow = kRank * 2;  // bytes of a column of B
+  const __nv_bfloat16* bw = static_cast<const __nv_bfloat16*>(p.b) + (long long)tile.id * p.N * p.r;
+  auto issue = [&](int k) {
+    if (k < c1) {
+      const uint32_t to = ring + (k - c0) % kStages * S::kStageBytes;
+#pragma unroll
+      for (int i = 0; i < kSlice * (kRank / 8) / kThreads; ++i) {
+        const int v = i * kThreads + tid, col = v / (kRank / 8), piece = v % (kRank / 8), n = kSlice * k + col;
+        const bool in = n < p.N && 8 * piece < p.r;
+        cp_async16(to + piece_at<kRow>(col, piece), in ? bw + (long long)n * p.r + 8 * piece : bw, in);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) issue(c0 + s);
+  const int ra = 16 * block + g, rb = ra + 8;
+  Eight ya, yb;
+  auto load_y = [&](int k) {
+    const int n = kSlice * k + 32 * half + 8 * c;
+    const bool in = works && k < c1 && n < p.N;
+    ya.load(p, (long long)tile.row0 + ra, n, in && ra < tile.rows);
+    yb.load(p, (long long)tile.row0 + rb, n, in && rb < tile.rows);
+  };
+  load_y(c0);
+  __syncwarp();
+  cluster_wait();
+  gather_t<kManyRows * kRank / 4>(p, tile.id, size, &sm.sum[0][0], &sm.t[0][0][0], &sm.t[1][0][0]);
+  __syncthreads();
+  cluster_arrive();  // this CTA has read the others' sums
+  constexpr int kSteps = kRank / 16;
+  uint32_t t[2][kSteps][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j) ldmatrix_x4(t[h][j], smem_u32(&sm.t[h][16 * block + (lane & 15)][16 * j + 8 * (lane >> 4)]));
+#pragma unroll 1
+  for (int k = c0; k < c1; ++k) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncthreads();
+    issue(k + kStages - 1);
+    if (!works) continue;
+    const uint32_t bs = ring + (k - c0) % kStages * S::kStageBytes;
+    const Eight olda = ya, oldb = yb;
+    load_y(k + 1);
+    float acc[4][4] = {};
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j) {
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        // lanes 0 .. 7: column n = lane of tile i, 16 .. 23: of tile i + 1; 8 .. 15 and 24 .. 31 the next 8 ranks
+        const int n = lane & 7, col = 32 * half + 8 * (n >> 1) + 2 * (i + (lane >> 4)) + (n & 1);
+        uint32_t w[4];
+        ldmatrix_x4(w, bs + piece_at<kRow>(col, 2 * j + ((lane >> 3) & 1)));
+        mma_bf16_16x8(acc[i], t[1][j], w[0], w[1]);
+        mma_bf16_16x8(acc[i + 1], t[1][j], w[2], w[3]);
+        mma_bf16_16x8(acc[i], t[0][j], w[0], w[1]);
+        mma_bf16_16x8(acc[i + 1], t[0][j], w[2], w[3]);
+      }
+    }
+    const int n = kSlice * k + 32 * half + 8 * c;
+    olda.put(p, (long long)tile.row0 + ra, n, n < p.N && ra < tile.rows, acc, 0);
+    oldb.put(p, (long long)tile.row0 + rb, n, n < p.N && rb < tile.rows, acc, 2);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  cluster_wait();  // until the others have read this CTA's sums
+}
+
+template <int kRank>
+cudaError_t launch(const LoraParams& p, bool many, int cluster, long long tiles, cudaStream_t stream) {
+  if (!many) return launch_kernel(lora_few_kernel<kRank>, (unsigned)(tiles * cluster), kThreads, 0, stream, cluster, p);
+  constexpr int kSmem = (int)sizeof(ManySmem<kRank>);
+  const cudaError_t e = cudaFuncSetAttribute(lora_many_kernel<kRank>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(lora_many_kernel<kRank>, (unsigned)(tiles * cluster), kThreads, kSmem, stream, cluster, p);
 }
 
 }  // namespace
 
 cudaError_t launch_lora(const LoraParams& p, int sms, cudaStream_t stream) {
-  const bool many = p.T >= 32ll * p.B;
+  const bool many = p.T >= 16ll * p.B;
   // every request may end in a tile that is not full
-  const int rows = many ? 64 : 16;
-  const long long tiles = p.T / rows + (p.B < p.T ? p.B : p.T);
+  const long long tiles = p.T / (many ? kManyRows : kFewRows) + (p.B < p.T ? p.B : p.T);
   const int cluster = 8;
-  return many ? launch_rank<4>(p, cluster, tiles, stream) : launch_rank<1>(p, cluster, tiles, stream);
+  if (p.r <= 32) return launch<32>(p, many, cluster, tiles, stream);
+  return p.r <= 64 ? launch<64>(p, many, cluster, tiles, stream) : launch<128>(p, many, cluster, tiles, stream);
 }
 
 }  // namespace bsk
