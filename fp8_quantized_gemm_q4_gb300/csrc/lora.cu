@@ -127,17 +127,19 @@ __device__ __forceinline__ void gather_t(const LoraParams& p, int id, int size, 
 
 // Eight columns of a row of y: read, and written with the products added (accumulators e
 // and e + 1 of the four tiles of a chunk)
+template <bool kBf16>
 struct Eight {
-  uint4 v[2];
+  static constexpr int kSize = kBf16 ? 2 : 4;
+  uint4 v[kBf16 ? 1 : 2];
   __device__ __forceinline__ void load(const LoraParams& p, long long row, int n, bool in) {
-    const char* from = static_cast<const char*>(p.y) + (row * p.ldy + n) * (p.bf16 ? 2 : 4);
-    v[0] = load16(from, in);
-    if (!p.bf16) v[1] = load16(from + 16, in);
+    const char* from = static_cast<const char*>(p.y) + (row * p.ldy + n) * kSize;
+#pragma unroll
+    for (int i = 0; i < kSize / 2; ++i) v[i] = load16(from + 16 * i, in);
   }
   __device__ __forceinline__ void put(const LoraParams& p, long long row, int n, bool in, const float (&acc)[4][4], int e) const {
     if (!in) return;
-    char* to = static_cast<char*>(p.out) + (row * p.ldo + n) * (p.bf16 ? 2 : 4);
-    if (p.bf16) {
+    char* to = static_cast<char*>(p.out) + (row * p.ldo + n) * kSize;
+    if constexpr (kBf16) {
       const uint32_t o[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
       uint32_t w[4];
 #pragma unroll
@@ -171,7 +173,7 @@ struct FewSmem {
   int4 tile;
 };
 
-template <int kRank>
+template <int kRank, bool kBf16>
 __global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : kRank > 32 ? 2 : 4) lora_few_kernel(const __grid_constant__ LoraParams p) {
   __shared__ __align__(16) FewSmem<kRank> sm;
   constexpr int kNT = kRank / 8, kKB = kRank / 32;  // tiles of 8 ranks, blocks of 32
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : kRank > 32 ? 2 : 4)
   const __nv_bfloat16* bw = static_cast<const __nv_bfloat16*>(p.b) + (long long)tile.id * p.N * p.r;
   const long long row = tile.row0 + (long long)g;
   uint4 w[4][kKB];
-  Eight y;
+  Eight<kBf16> y;
   auto load = [&](int chunk) {
     y.load(p, row, 32 * chunk + 8 * c, row_in && chunk < c1 && 32 * chunk + 8 * c < p.N);
 #pragma unroll
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : kRank > 32 ? 2 : 4)
           mma_bf16_16x8(acc[i], f1, w[i][k].z, w[i][k].w);
         }
       }
-    const Eight old = y;
+    const Eight<kBf16> old = y;
     load(chunk + kWarps);
     old.put(p, row, 32 * chunk + 8 * c, row_in && 32 * chunk + 8 * c < p.N, acc, 0);
   }
@@ -280,30 +282,39 @@ __global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : kRank > 32 ? 2 : 4)
 }
 
 // ---------------------------------------------------------------------------
-// Many rows a request: tiles of 64 rows.  x and A, then B, come through a ring of shared
-// memory with cp.async, so that the four warps that need a slice of weights read it from
-// L2 once; y goes from global memory to registers a chunk ahead.  Warps: a block of 16
-// rows and half the ranks, then half the columns of a chunk.
+// Many rows a request: tiles of 64 rows.  x and A, then B and y, come through a ring of
+// shared memory with cp.async, so that the four warps that need a slice of weights read it
+// from L2 once.  Warps: a block of 16 rows and half the ranks, then half the columns of a
+// chunk.  Of t each CTA adds an eighth and hands it to all.
 // ---------------------------------------------------------------------------
 constexpr int kManyRows = 64, kSlice = 64;  // rows of a tile; K, or columns, of a stage
-constexpr int kStages = 4;
 
-template <int kRank>
+// Shared memory: four stages of x and A, or in their place three of B and y, the last of
+// which holds the CTA's sums until it is needed, and t (hi, lo).
+template <int kRank, bool kBf16>
 struct ManySmem {
-  static constexpr int kStageBytes = (kManyRows + kRank) * kSlice * 2;  // x and A; or B, which is smaller
-  alignas(128) uint8_t ring[kStages][kStageBytes];
-  float sum[kManyRows][kRank];           // the CTA's part of t
-  __nv_bfloat16 t[2][kManyRows][kRank];  // hi, lo of the scaled t
-  long long scan[kWarps];
-  int4 tile;
+  static constexpr int kStages1 = 4, kStages2 = 3;
+  static constexpr int kStage1 = (kManyRows + kRank) * kSlice * 2;
+  static constexpr int kB = kSlice * kRank * 2, kPieces = kBf16 ? 2 : 4;  // bytes of B; 16-byte pieces of y a thread
+  static constexpr int kStage2 = kB + kPieces * kThreads * 16;
+  static constexpr int kT = kManyRows * kRank * 2, kSums = 2 * kT;        // bytes of hi or lo, of the sums
+  static constexpr int kSumsAt = (kStages2 - 1) * kStage2;
+  static constexpr int kTAt = kSumsAt + (kSums > kStage2 ? kSums : kStage2);
+  static constexpr int kBytes = kTAt + 2 * kT > kStages1 * kStage1 ? kTAt + 2 * kT : kStages1 * kStage1;
 };
 
-// Place of the 16-byte piece `chunk` of row `row` in rows of kBytes, pieces exchanged so that
-// eight rows of a column of pieces meet all banks
+// Place of the 16-byte piece `chunk` of a row of x or A, of a column of B or of a row of t
+// (kBytes each), pieces exchanged so that the eight rows, or columns, of a matrix that
+// ldmatrix reads meet all banks
+__device__ __forceinline__ uint32_t piece_at(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
 template <int kBytes>
-__device__ __forceinline__ uint32_t piece_at(int row, int chunk) {
-  if constexpr (kBytes == 64) return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
-  return row * kBytes + ((chunk ^ (row & 7)) << 4);
+__device__ __forceinline__ uint32_t column_at(int col, int chunk) {
+  const int x = (col >> 3) & 3;
+  return col * kBytes + ((chunk ^ (kBytes == 64 ? x : 2 * x + (col & 1))) << 4);
+}
+template <int kBytes>
+__device__ __forceinline__ uint32_t t_at(int row, int chunk) {
+  return row * kBytes + ((chunk ^ (kBytes == 64 ? (row >> 1) & 3 : row & 7)) << 4);
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
@@ -314,17 +325,26 @@ __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t x, uint32_t y) {
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
 
-template <int kRank>
-__global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : 2) lora_many_kernel(const __grid_constant__ LoraParams p) {
+template <int kRank, bool kBf16>
+__global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : kBf16 ? 3 : 2) lora_many_kernel(const __grid_constant__ LoraParams p) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  using S = ManySmem<kRank>;
-  S& sm = *reinterpret_cast<S*>(smem_raw);
+  __shared__ long long scan[kWarps];
+  __shared__ int4 found;
+  using S = ManySmem<kRank, kBf16>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int size = (int)cluster_size(), rank = (int)cluster_ctarank();
   griddep_wait();
   griddep_launch_dependents();
-  const Tile tile = find_tile<kManyRows>(p, (int)(blockIdx.x / size), sm.scan, &sm.tile);
+  const Tile tile = find_tile<kManyRows>(p, (int)(blockIdx.x / size), scan, &found);
   if (!tile.there) return;  // all CTAs of the cluster alike
   const int chunks = (p.N + kSlice - 1) / kSlice;  // of columns, shared by the CTAs
   const int c0 = (int)((long long)chunks * rank / size), c1 = (int)((long long)chunks * (rank + 1) / size);
@@ -334,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : 2) lora_many_kernel
   }
   const int block = warp & 3, half = warp >> 2;
   const bool works = 16 * block < tile.rows;
-  const uint32_t ring = smem_u32(sm.ring[0]);
+  const uint32_t smem = smem_u32(smem_raw);
 
   // ---- t = x A^T
   constexpr int kNT = kRank / 16;  // tiles of 8 ranks of a warp
@@ -345,145 +365,177 @@ __global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : 2) lora_many_kernel
     const __nv_bfloat16* a = static_cast<const __nv_bfloat16*>(p.a) + (long long)tile.id * p.r * p.K;
     auto issue = [&](int k) {
       if (k < k1) {
-        const uint32_t to = ring + (k - k0) % kStages * S::kStageBytes;
+        const uint32_t to = smem + (k - k0) % S::kStages1 * S::kStage1;
 #pragma unroll
         for (int i = 0; i < kManyRows * 8 / kThreads; ++i) {
           const int v = i * kThreads + tid, row = v >> 3, piece = v & 7, at = kSlice * k + 8 * piece;
           const bool in = row < tile.rows && at < p.K;
-          cp_async16(to + piece_at<128>(row, piece), in ? x + row * p.ldx + at : x, in);
+          cp_async16(to + piece_at(row, piece), in ? x + row * p.ldx + at : x, in);
         }
 #pragma unroll
         for (int i = 0; i < kRank * 8 / kThreads; ++i) {
           const int v = i * kThreads + tid, row = v >> 3, piece = v & 7, at = kSlice * k + 8 * piece;
           const bool in = row < p.r && at < p.K;
-          cp_async16(to + kManyRows * 128 + piece_at<128>(row, piece), in ? a + (long long)row * p.K + at : a, in);
+          cp_async16(to + kManyRows * 128 + piece_at(row, piece), in ? a + (long long)row * p.K + at : a, in);
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     float acc[kNT][4] = {};
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) issue(k0 + s);
+    for (int s = 0; s < S::kStages1 - 1; ++s) issue(k0 + s);
 #pragma unroll 1
     for (int k = k0; k < k1; ++k) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages1 - 2) : "memory");
       __syncthreads();  // everybody's part of the stage is there, and the stage before has been read
-      issue(k + kStages - 1);
+      issue(k + S::kStages1 - 1);
       if (!works) continue;
-      const uint32_t xs = ring + (k - k0) % kStages * S::kStageBytes, as = xs + kManyRows * 128;
+      const uint32_t xs = smem + (k - k0) % S::kStages1 * S::kStage1, as = xs + kManyRows * 128;
 #pragma unroll
       for (int j = 0; j < kSlice / 16; ++j) {
         uint32_t f[4];
-        ldmatrix_x4(f, xs + piece_at<128>(16 * block + (lane & 15), 2 * j + (lane >> 4)));
+        ldmatrix_x4(f, xs + piece_at(16 * block + (lane & 15), 2 * j + (lane >> 4)));
 #pragma unroll
         for (int n = 0; n < kNT; n += 2) {
           uint32_t w[4];  // two tiles of 8 ranks
-          ldmatrix_x4(w, as + piece_at<128>(8 * (half * kNT + n) + (lane & 7) + 8 * (lane >> 4), 2 * j + ((lane >> 3) & 1)));
+          ldmatrix_x4(w, as + piece_at(8 * (half * kNT + n) + (lane & 7) + 8 * (lane >> 4), 2 * j + ((lane >> 3) & 1)));
           mma_bf16_16x8(acc[n], f, w[0], w[1]);
           mma_bf16_16x8(acc[n + 1], f, w[2], w[3]);
         }
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();  // the ring has been read
+    float* sums = reinterpret_cast<float*>(smem_raw + S::kSumsAt);
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
-      float* at = &sm.sum[16 * block + g][8 * (half * kNT + n) + 2 * c];
+      float* at = sums + (16 * block + g) * kRank + 8 * (half * kNT + n) + 2 * c;
       *reinterpret_cast<float2*>(at) = make_float2(acc[n][0], acc[n][1]);
       *reinterpret_cast<float2*>(at + 8 * kRank) = make_float2(acc[n][2], acc[n][3]);
     }
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncthreads();  // the ring has been read
+  __syncwarp();
   cluster_arrive();
 
   // ---- out = y + t B^T.  Tile i of 32 columns has 8 (n / 2) + 2 i + n % 2, n = 0 .. 7, so that a
   // lane ends with eight columns in a row.
-  constexpr int kRow = kRank * 2;  // bytes of a column of B
+  constexpr int kRow = kRank * 2;  // bytes of a column of B, of a row of t
   const __nv_bfloat16* bw = static_cast<const __nv_bfloat16*>(p.b) + (long long)tile.id * p.N * p.r;
+  const int ra = 16 * block + g, rb = ra + 8;
+  const long long to_a = tile.row0 + (long long)ra, to_b = tile.row0 + (long long)rb;
   auto issue = [&](int k) {
     if (k < c1) {
-      const uint32_t to = ring + (k - c0) % kStages * S::kStageBytes;
+      const uint32_t to = smem + (k - c0) % S::kStages2 * S::kStage2;
 #pragma unroll
       for (int i = 0; i < kSlice * (kRank / 8) / kThreads; ++i) {
         const int v = i * kThreads + tid, col = v / (kRank / 8), piece = v % (kRank / 8), n = kSlice * k + col;
         const bool in = n < p.N && 8 * piece < p.r;
-        cp_async16(to + piece_at<kRow>(col, piece), in ? bw + (long long)n * p.r + 8 * piece : bw, in);
+        cp_async16(to + column_at<kRow>(col, piece), in ? bw + (long long)n * p.r + 8 * piece : bw, in);
+      }
+      // y: what this thread will add to
+      const int n = kSlice * k + 32 * half + 8 * c;
+#pragma unroll
+      for (int i = 0; i < S::kPieces; ++i) {
+        const bool second = i >= S::kPieces / 2, in = n < p.N && (second ? rb : ra) < tile.rows;
+        const char* from = static_cast<const char*>(p.y) + ((second ? to_b : to_a) * p.ldy + n) * (kBf16 ? 2 : 4) + 16 * (i % (S::kPieces / 2));
+        cp_async16(to + S::kB + (i * kThreads + tid) * 16, in ? from : p.y, in);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) issue(c0 + s);
-  const int ra = 16 * block + g, rb = ra + 8;
-  Eight ya, yb;
-  auto load_y = [&](int k) {
-    const int n = kSlice * k + 32 * half + 8 * c;
-    const bool in = works && k < c1 && n < p.N;
-    ya.load(p, (long long)tile.row0 + ra, n, in && ra < tile.rows);
-    yb.load(p, (long long)tile.row0 + rb, n, in && rb < tile.rows);
-  };
-  load_y(c0);
+  for (int s = 0; s < S::kStages2 - 1; ++s) issue(c0 + s);
   __syncwarp();
   cluster_wait();
-  gather_t<kManyRows * kRank / 4>(p, tile.id, size, &sm.sum[0][0], &sm.t[0][0][0], &sm.t[1][0][0]);
-  __syncthreads();
-  cluster_arrive();  // this CTA has read the others' sums
-  constexpr int kSteps = kRank / 16;
-  uint32_t t[2][kSteps][4];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int j = 0; j < kSteps; ++j) ldmatrix_x4(t[h][j], smem_u32(&sm.t[h][16 * block + (lane & 15)][16 * j + 8 * (lane >> 4)]));
+  {
+    // this CTA's share of t: the sums of all CTAs in order of rank, scaled, as hi and lo to all
+    constexpr int kVecs = kManyRows * kRank / 4;
+    const float scale = p.scales ? p.scales[tile.id] : 1.0f;
+    for (int x = kVecs * rank / size + tid; x < kVecs * (rank + 1) / size; x += kThreads) {
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+      for (int r = 0; r < size; ++r) {
+        const float4 e = ld_cluster(mapa_shared(smem + S::kSumsAt + 16 * x, r));
+        v.x += e.x, v.y += e.y, v.z += e.z, v.w += e.w;
+      }
+      v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
+      const uint32_t h0 = pack_bf16x2(v.x, v.y), h1 = pack_bf16x2(v.z, v.w);
+      const uint32_t l0 = pack_bf16x2(v.x - __uint_as_float(h0 << 16), v.y - __uint_as_float(h0 & 0xffff0000u));
+      const uint32_t l1 = pack_bf16x2(v.z - __uint_as_float(h1 << 16), v.w - __uint_as_float(h1 & 0xffff0000u));
+      const int row = x / (kRank / 4), half_piece = x % (kRank / 4);
+      const uint32_t to = smem + S::kTAt + t_at<kRow>(row, half_piece >> 1) + 8 * (half_piece & 1);
+#pragma unroll 8
+      for (int r = 0; r < size; ++r) {
+        const uint32_t there = mapa_shared(to, r);
+        st_cluster(there, h0, h1);
+        st_cluster(there + S::kT, l0, l1);
+      }
+    }
+  }
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
 #pragma unroll 1
   for (int k = c0; k < c1; ++k) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages2 - 2) : "memory");
     __syncthreads();
-    issue(k + kStages - 1);
+    issue(k + S::kStages2 - 1);
     if (!works) continue;
-    const uint32_t bs = ring + (k - c0) % kStages * S::kStageBytes;
-    const Eight olda = ya, oldb = yb;
-    load_y(k + 1);
+    const uint32_t bs = smem + (k - c0) % S::kStages2 * S::kStage2;
     float acc[4][4] = {};
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
+    for (int j = 0; j < kRank / 16; ++j) {
+      uint32_t hi[4], lo[4];
+      const uint32_t at = smem + S::kTAt + t_at<kRow>(16 * block + (lane & 15), 2 * j + (lane >> 4));
+      ldmatrix_x4(hi, at);
+      ldmatrix_x4(lo, at + S::kT);
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {
         // lanes 0 .. 7: column n = lane of tile i, 16 .. 23: of tile i + 1; 8 .. 15 and 24 .. 31 the next 8 ranks
         const int n = lane & 7, col = 32 * half + 8 * (n >> 1) + 2 * (i + (lane >> 4)) + (n & 1);
         uint32_t w[4];
-        ldmatrix_x4(w, bs + piece_at<kRow>(col, 2 * j + ((lane >> 3) & 1)));
-        mma_bf16_16x8(acc[i], t[1][j], w[0], w[1]);
-        mma_bf16_16x8(acc[i + 1], t[1][j], w[2], w[3]);
-        mma_bf16_16x8(acc[i], t[0][j], w[0], w[1]);
-        mma_bf16_16x8(acc[i + 1], t[0][j], w[2], w[3]);
+        ldmatrix_x4(w, bs + column_at<kRow>(col, 2 * j + ((lane >> 3) & 1)));
+        mma_bf16_16x8(acc[i], lo, w[0], w[1]);
+        mma_bf16_16x8(acc[i + 1], lo, w[2], w[3]);
+        mma_bf16_16x8(acc[i], hi, w[0], w[1]);
+        mma_bf16_16x8(acc[i + 1], hi, w[2], w[3]);
       }
     }
     const int n = kSlice * k + 32 * half + 8 * c;
-    olda.put(p, (long long)tile.row0 + ra, n, n < p.N && ra < tile.rows, acc, 0);
-    oldb.put(p, (long long)tile.row0 + rb, n, n < p.N && rb < tile.rows, acc, 2);
+    const uint32_t ys = bs + S::kB + tid * 16;
+    Eight<kBf16> y;
+#pragma unroll
+    for (int i = 0; i < S::kPieces / 2; ++i) y.v[i] = lds128(ys + i * kThreads * 16);
+    y.put(p, to_a, n, n < p.N && ra < tile.rows, acc, 0);
+#pragma unroll
+    for (int i = 0; i < S::kPieces / 2; ++i) y.v[i] = lds128(ys + (S::kPieces / 2 + i) * kThreads * 16);
+    y.put(p, to_b, n, n < p.N && rb < tile.rows, acc, 2);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncwarp();
-  cluster_wait();  // until the others have read this CTA's sums
 }
 
-template <int kRank>
+template <int kRank, bool kBf16>
 cudaError_t launch(const LoraParams& p, bool many, int cluster, long long tiles, cudaStream_t stream) {
-  if (!many) return launch_kernel(lora_few_kernel<kRank>, (unsigned)(tiles * cluster), kThreads, 0, stream, cluster, p);
-  constexpr int kSmem = (int)sizeof(ManySmem<kRank>);
-  const cudaError_t e = cudaFuncSetAttribute(lora_many_kernel<kRank>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const unsigned grid = (unsigned)(tiles * cluster);
+  if (!many) return launch_kernel(lora_few_kernel<kRank, kBf16>, grid, kThreads, 0, stream, cluster, p);
+  constexpr int kSmem = ManySmem<kRank, kBf16>::kBytes;
+  const cudaError_t e = cudaFuncSetAttribute(lora_many_kernel<kRank, kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(lora_many_kernel<kRank>, (unsigned)(tiles * cluster), kThreads, kSmem, stream, cluster, p);
+  return launch_kernel(lora_many_kernel<kRank, kBf16>, grid, kThreads, kSmem, stream, cluster, p);
+}
+template <bool kBf16>
+cudaError_t launch_rank(const LoraParams& p, bool many, int cluster, long long tiles, cudaStream_t stream) {
+  if (p.r <= 32) return launch<32, kBf16>(p, many, cluster, tiles, stream);
+  return p.r <= 64 ? launch<64, kBf16>(p, many, cluster, tiles, stream) : launch<128, kBf16>(p, many, cluster, tiles, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_lora(const LoraParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_lora(const LoraParams& p, cudaStream_t stream) {
   const bool many = p.T >= 16ll * p.B;
   // every request may end in a tile that is not full
   const long long tiles = p.T / (many ? kManyRows : kFewRows) + (p.B < p.T ? p.B : p.T);
-  const int cluster = 8;
-  if (p.r <= 32) return launch<32>(p, many, cluster, tiles, stream);
-  return p.r <= 64 ? launch<64>(p, many, cluster, tiles, stream) : launch<128>(p, many, cluster, tiles, stream);
+  return p.bf16 ? launch_rank<true>(p, many, 8, tiles, stream) : launch_rank<false>(p, many, 8, tiles, stream);
 }
 
 }  // namespace bsk
