@@ -1441,8 +1441,9 @@ bs_status bs_lora_add(const bs_lora_args* a, bs_stream_t stream) {
       !aligned4(a->scales) || !aligned4(a->cu_rows) || !aligned4(a->which))
     return fail(BS_ERR_ALIGN, "lora_add: x, a, b, y and out must be 16-byte aligned, row strides multiples of 8");
   if (a->out == a->y && a->T > 1 && a->ldo != a->ldy) return fail(BS_ERR_INVALID, "lora_add: out in y's place needs its stride");
+  int sms = 0;
   bsk::LoraParams p = {};
-  if (!device_info(&p.status, nullptr)) return fail(BS_ERR_CUDA, "no current device");
+  if (!device_info(&p.status, &sms)) return fail(BS_ERR_CUDA, "no current device");
   p.x = a->x;
   p.ldx = a->ldx;
   p.a = a->a;
@@ -1461,7 +1462,7 @@ bs_status bs_lora_add(const bs_lora_args* a, bs_stream_t stream) {
   p.N = (int)a->N;
   p.r = a->r;
   p.adapters = a->adapters;
-  cudaError_t e = bsk::launch_lora(p, reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = bsk::launch_lora(p, sms, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "lora_add launch");
   return BS_OK;
 }

@@ -181,6 +181,6 @@ struct LoraParams {
   int T, B, K, N, r, adapters;
   int* status;
 };
-cudaError_t launch_lora(const LoraParams& p, cudaStream_t stream);
+cudaError_t launch_lora(const LoraParams& p, int sms, cudaStream_t stream);
 
 }  // namespace bsk

@@ -14,6 +14,7 @@ namespace bsk {
 namespace {
 
 constexpr int kThreads = 256, kWarps = 8;
+constexpr long long kManyEach = 32;  // rows a request, on average, from which tiles have 64 rows
 
 __device__ __forceinline__ void mma_bf16_16x8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -38,14 +39,15 @@ __device__ __forceinline__ uint4 load16(const void* p, bool in) {
   return in ? *static_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
 }
 
-// A request's rows within the call, and whether its numbers keep the contract
+// A request's rows within the call, its adapter, and whether its numbers break the contract
 struct Rows {
-  int row0, n;
+  int row0, n, id;
   bool bad;
 };
 __device__ __forceinline__ Rows rows_of(const LoraParams& p, int b) {
-  const int r0 = p.cu[b], r1 = p.cu[b + 1];
-  return {r0, r0 < 0 || r1 <= r0 ? 0 : max(0, min(r1, p.T) - r0), r0 < 0 || r1 < r0 || r1 > p.T || p.which[b] >= p.adapters};
+  const int r0 = p.cu[b], r1 = p.cu[b + 1], w = p.which[b];
+  return {r0, r0 < 0 || r1 <= r0 ? 0 : max(0, min(r1, p.T) - r0), w >= p.adapters ? -1 : w,
+          r0 < 0 || r1 < r0 || r1 > p.T || w >= p.adapters};
 }
 
 // The cluster's tile: requests in order, their rows in tiles of kRows.
@@ -59,8 +61,9 @@ __device__ __forceinline__ Tile find_tile(const LoraParams& p, int tile, long lo
   const int per = (p.B + kThreads - 1) / kThreads, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   if (tid == 0) *found = make_int4(0, 0, -1, 0);
   long long mine = 0;  // offsets that break the contract may claim rows twice
+  Rows r;              // of the last of them: all there is while B <= kThreads
   for (int b = b0; b < b1; ++b) {
-    const Rows r = rows_of(p, b);
+    r = rows_of(p, b);
     if (r.bad && blockIdx.x == 0) record_status(p.status, kStatusOffsets, 57);
     mine += (r.n + kRows - 1) / kRows;
   }
@@ -77,12 +80,12 @@ __device__ __forceinline__ Tile find_tile(const LoraParams& p, int tile, long lo
   for (int w = 0; w < kWarps; ++w) before += w < warp ? scan[w] : 0;
   if (tile >= before && tile < before + mine) {
     for (int b = b0; b < b1; ++b) {
-      const Rows r = rows_of(p, b);
+      if (per > 1) r = rows_of(p, b);
       const int n = (r.n + kRows - 1) / kRows;
       const long long i = tile - before;
       if (i < n) {
-        const int w = p.which[b], at = (int)i * kRows;
-        *found = make_int4(r.row0 + at, min(kRows, r.n - at), w >= p.adapters ? -1 : w, 1);
+        const int at = (int)i * kRows;
+        *found = make_int4(r.row0 + at, min(kRows, r.n - at), r.id, 1);
         break;
       }
       before += n;
@@ -531,11 +534,21 @@ cudaError_t launch_rank(const LoraParams& p, bool many, int cluster, long long t
 
 }  // namespace
 
-cudaError_t launch_lora(const LoraParams& p, cudaStream_t stream) {
-  const bool many = p.T >= 16ll * p.B;
+cudaError_t launch_lora(const LoraParams& p, int sms, cudaStream_t stream) {
+  // us, tiles of 8 / 64 rows, K = 4096, N = 6144, rank 16: 8 requests of 4 rows 6.5 / 11, of 32 rows 10.2 /
+  // 12.4; 64 requests of 4 rows 14 / 28, of 16 rows 25 / 31, of 32 rows 40 / 37
+  const bool many = p.T >= kManyEach * p.B;
   // every request may end in a tile that is not full
   const long long tiles = p.T / (many ? kManyRows : kFewRows) + (p.B < p.T ? p.B : p.T);
-  return p.bf16 ? launch_rank<true>(p, many, 8, tiles, stream) : launch_rank<false>(p, many, 8, tiles, stream);
+  // Eight CTAs a tile; of few rows fewer where not all would be on the GPU at once, for each
+  // has its own start and exchange (us with 8 / 4 / 2 / 1, K = 4096, N = 6144: rank 16, 1 request
+  // 6.3 / 8.6 / 12 / 19, 64 requests 10.4 / 10.3 / 12.6 / 19, 256 requests 36 / 26 / 25 / 28; rank 64, 256
+  // requests 81 / 62 / 53 / 49).  Of many rows the next CTAs start while others end (8190 rows,
+  // rank 64: 77 / 77 / 99 / 91; 8192 rows, rank 16: 67 / 80 / 77 / 82; 512 rows: 13 / 21 / 37 / 69).
+  int cluster = 8;
+  const long long at_once = (long long)sms * (p.r <= 32 ? 4 : p.r <= 64 ? 2 : 1);
+  while (!many && cluster > 1 && tiles * cluster > at_once) cluster /= 2;
+  return p.bf16 ? launch_rank<true>(p, many, cluster, tiles, stream) : launch_rank<false>(p, many, cluster, tiles, stream);
 }
 
 }  // namespace bsk
