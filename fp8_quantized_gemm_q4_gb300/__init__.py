@@ -23,7 +23,7 @@ from ._build import LIB as _LIB_PATH
 
 __all__ = [
     "load", "sf_bytes", "sf_offset", "q4_quantize", "tensor_amax", "q4_quantize_two_level", "fp4_gather_rows", "fp8_gather_rows", "q8_quantize", "gemm_fp4", "gemm_fp8", "gemm_fp8_multi", "gemm_fp4_multi",
-    "grouped_gemm_fp4", "grouped_gemm_fp4_swiglu_q4", "grouped_gemm_fp8", "moe_router_topk", "moe_dispatch", "moe_finalize", "moe_combine", "moe_rows_bound", "kv_plan", "kv_release", "kv_append", "kv_append_rotary", "kv_gather", "kv_attention", "kv_attention_workspace", "matvec_fp4", "lora_add", "rotary_angles", "KVCache", "KVCacheFP4", "device_status",
+    "grouped_gemm_fp4", "grouped_gemm_fp4_swiglu_q4", "grouped_gemm_fp8", "moe_router_topk", "moe_dispatch", "moe_finalize", "moe_combine", "moe_rows_bound", "kv_plan", "kv_release", "kv_append", "kv_positions", "kv_append_rotary", "kv_gather", "kv_attention", "kv_attention_workspace", "matvec_fp4", "lora_add", "rotary_angles", "KVCache", "KVCacheFP4", "device_status",
     "clear_device_status", "BSError", "EPI_STORE", "EPI_SWIGLU", "EPI_COMBINE", "EPI_ROWS", "kernel_options",
     "current_kernel_options", "FP4_ONE_CTA", "FP4_PAIR",
 ]
@@ -169,6 +169,8 @@ def load(path: str | None = None):
         lib.bs_kv_attention_workspace_bytes.argtypes = [ctypes.c_char_p]
         lib.bs_kv_attention.restype = I
         lib.bs_kv_attention.argtypes = [ctypes.c_char_p, P]
+        lib.bs_kv_positions.restype = I
+        lib.bs_kv_positions.argtypes = [P, P, I, I64, P, P]
         lib.bs_kv_attention_fp4.restype = I
         lib.bs_kv_attention_fp4.argtypes = [ctypes.c_char_p, P, P, P]
         lib.bs_kv_append_rotary.restype = I
@@ -750,6 +752,23 @@ def rotary_angles(max_positions: int, rotary_dim: int, base: float = 10000.0, de
     f = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device) / rotary_dim)
     a = torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] * f
     return torch.cat([a.cos(), a.sin()], 1).float()
+
+
+def kv_positions(seq_lens, cu_new, total_new: int, out=None, stream=None):
+    """The place of each new token in its request, int32 [total_new]: seq_lens[b] + i for
+    row cu_new[b] + i (both as kv_plan takes and gives them), 0 behind the last request."""
+    B = seq_lens.numel()
+    if out is None:
+        out = _empty((total_new,), _I32, seq_lens.device, stream)
+    _ints("kv_positions", seq_lens, cu_new, out)
+    if cu_new.numel() != B + 1 or out.numel() != total_new:
+        raise ValueError("kv_positions: cu_new is [B + 1], out [total_new]")
+    here = seq_lens.get_device()
+    if here < 0 or cu_new.get_device() != here or out.get_device() != here or here != _device():
+        _misplaced("kv_positions")
+    _check((_lib or load()).bs_kv_positions(seq_lens.data_ptr(), cu_new.data_ptr(), B, total_new, out.data_ptr(),
+                                            _stream(stream)))
+    return out
 
 
 def kv_append_rotary(q, k, v, slots, positions, angles, cache, q_out=None, interleaved: bool = False, stream=None):

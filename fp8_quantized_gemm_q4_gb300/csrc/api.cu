@@ -1135,6 +1135,20 @@ bs_status bs_kv_release(const int32_t* lens, const int32_t* done, int B, int32_t
   return BS_OK;
 }
 
+bs_status bs_kv_positions(const int32_t* seq_lens, const int32_t* cu_new, int B, int64_t T, int32_t* positions, bs_stream_t stream) {
+  if (B < 0 || T < 0 || T > INT32_MAX) return fail(BS_ERR_INVALID, "kv_positions: B=%d T=%lld", B, (long long)T);
+  if (B > bsk::kKvPlanMaxB) return fail(BS_ERR_UNSUPPORTED, "kv_positions: B=%d above %d", B, bsk::kKvPlanMaxB);
+  if (T == 0) return BS_OK;
+  if (!positions || !cu_new || (B > 0 && !seq_lens)) return fail(BS_ERR_INVALID, "kv_positions: null pointer");
+  if (!aligned4(seq_lens) || !aligned4(cu_new) || !aligned4(positions))
+    return fail(BS_ERR_ALIGN, "kv_positions: buffers must be 4-byte aligned");
+  if (positions == seq_lens || positions == cu_new) return fail(BS_ERR_INVALID, "kv_positions: the output buffer is an input buffer");
+  if (!device_info(nullptr, nullptr)) return fail(BS_ERR_CUDA, "no current device");
+  cudaError_t e = bsk::launch_kv_positions(seq_lens, cu_new, B, (int)T, positions, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_positions launch");
+  return BS_OK;
+}
+
 // Cache geometry shared by append and attention.
 static bs_status check_kv_cache(const char* what, int Hkv, int D, int64_t num_pages, int page_size) {
   if (Hkv <= 0 || num_pages < 0)

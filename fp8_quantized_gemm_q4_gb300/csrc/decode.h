@@ -50,6 +50,7 @@ struct KvReleaseParams {
   int* status;
 };
 cudaError_t launch_kv_release(const KvReleaseParams& p, cudaStream_t stream);
+cudaError_t launch_kv_positions(const int* seq_lens, const int* cu_new, int B, int T, int* positions, cudaStream_t stream);
 struct KvAppendParams {
   const void* x[2];       // keys, values
   long long tok_stride[2], head_stride[2];  // elements

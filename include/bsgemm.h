@@ -578,6 +578,15 @@ bs_status bs_kv_release(const int32_t *lens, const int32_t *done, int B, int32_t
                         bs_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * bs_kv_positions -- positions[r] = seq_lens[b] + r - cu_new[b] for the rows r =
+ * cu_new[b] .. cu_new[b + 1] - 1 of request b (its token's place, as the rotation wants
+ * it), 0 for rows from cu_new[B] on.  seq_lens int32 [B], cu_new int32 [B + 1] as
+ * bs_kv_plan writes it, positions int32 [T]; B up to 8192.
+ * ------------------------------------------------------------------------- */
+bs_status bs_kv_positions(const int32_t *seq_lens, const int32_t *cu_new, int B, int64_t T, int32_t *positions,
+                          bs_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * bs_kv_append -- quantize new keys and values into their slots.
  * The rows that go into one page follow one another with consecutive slots (as
  * bs_kv_plan gives them; a page that a call names twice apart, with a gap or a

@@ -52,6 +52,16 @@ def test_append_rotary_refusals(bs):
     assert call(T=0, k=None) == bs.BS_OK
 
 
+def test_positions_refusals(bs):
+    f = bs.load().bs_kv_positions
+    for args, want in (((F, F + 64, -1, 3, F + 128), bs.BS_ERR_INVALID), ((F, F + 64, 9000, 3, F + 128), bs.BS_ERR_UNSUPPORTED),
+                       ((F, F + 64, 2, -1, F + 128), bs.BS_ERR_INVALID), ((F, F + 64, 2, 1 << 31, F + 128), bs.BS_ERR_INVALID),
+                       ((F, F + 64, 2, 3, None), bs.BS_ERR_INVALID), ((None, F + 64, 2, 3, F + 128), bs.BS_ERR_INVALID),
+                       ((F, None, 2, 3, F + 128), bs.BS_ERR_INVALID), ((F, F + 2, 2, 3, F + 128), bs.BS_ERR_ALIGN),
+                       ((F, F + 64, 2, 3, F), bs.BS_ERR_INVALID), ((F, F + 64, 2, 0, None), bs.BS_OK)):
+        assert f(*args, None) == want, args
+
+
 def test_gather_refusals(bs):
     names = "slots T Hkv D k v k_token_stride k_head_stride v_token_stride v_head_stride cache_format page_size k_codes v_codes " \
             "k_scales v_scales num_pages".split()
@@ -136,7 +146,9 @@ def test_binding_refusals(stopped):
               lambda: att(bs.KVCacheFP4(*c8)), lambda: att(tuple(c4)), lambda: bs.kv_gather(c4, at, out=(k, k[:2])),
               lambda: lora(y=y[:5]), lambda: lora(b=b[:1]), lambda: lora(a=z(2, 8, 56, dt=bf)), lambda: lora(cu_rows=z(2)),
               lambda: lora(x=x.t().contiguous().t()), lambda: lora(out=y[:, :16]), lambda: lora(b=b.transpose(1, 2)),
+              lambda: bs.kv_positions(at, at, 3),
               # the last check of each: nothing is on a GPU
+              lambda: bs.kv_positions(at, z(4), 3),
               app, lambda: app(cache=c8), lambda: att(c4), lambda: bs.kv_gather(c4, at), lambda: bs.kv_gather(c8, at), lora,
               lambda: bs.kv_append(k, k, at, c4)]
     types = [lambda: app(slots=at.long()), lambda: app(positions=at.long()), lambda: app(positions=at[:2]), lambda: app(positions=None),
