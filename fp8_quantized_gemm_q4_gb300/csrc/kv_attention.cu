@@ -147,25 +147,40 @@ __device__ __forceinline__ void softmax_step(float (&u)[4], float inv_sv, float 
 // warp takes, from the stage's codes and the scales of those tokens on; [h]: 16 of them.
 template <int D>
 struct Fp4At {
-  uint32_t k[2][2], v[2][D / 64], ks, vs;
+  // of the second 16 tokens of D = 128: 1024 bytes on, with the same exchange of pieces
+  static constexpr int kHalves = D == 128 ? 1 : 2;
+  uint32_t k_[kHalves][2], v_[kHalves][D / 64], ks, vs;
   __device__ __forceinline__ Fp4At(int warp, int lane) {
     const int g = lane >> 2, c = lane & 3;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kHalves; ++h) {
       const int tok = warp * 32 + 16 * h;
 #pragma unroll
       for (int i = 0; i < 2; ++i)  // D / 4 columns of tokens g and g + 8
-        k[h][i] = D == 128 ? code_at<64>(tok + 8 * i + g, c) : code_at<32>(tok + 8 * i + g, c >> 1) + 8 * (c & 1);
+        k_[h][i] = D == 128 ? code_at<64>(tok + 8 * i + g, c) : code_at<32>(tok + 8 * i + g, c >> 1) + 8 * (c & 1);
 #pragma unroll
       for (int a = 0; a < D / 64; ++a)  // rows for ldmatrix: tokens 0 .. 15 at 16-byte chunk 2 a, then 2 a + 1
-        v[h][a] = kTileOf<true> * (D / 2) + code_at<D / 2>(tok + (lane & 15), 2 * a + (lane >> 4));
+        v_[h][a] = kTileOf<true> * (D / 2) + code_at<D / 2>(tok + (lane & 15), 2 * a + (lane >> 4));
     }
     ks = g * (D / 16) + (D == 128 ? 2 : 1) * c;
     vs = kTileOf<true> * (D / 16) + 2 * c * (D / 16);
   }
+  __device__ __forceinline__ uint32_t k(int h, int i) const { return D == 128 ? k_[0][i] + 1024 * h : k_[h % kHalves][i]; }
+  __device__ __forceinline__ uint32_t v(int h, int a) const { return D == 128 ? v_[0][a] + 1024 * h : v_[h % kHalves][a]; }
 };
+// mma_f16 that the compiler may move among the loads and conversions
+__device__ __forceinline__ void mma_f16_free(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+constexpr int kAllThere = 16 | 16 << 8;
 constexpr float kNone = -3.0e38f;  // reference of a row that has seen no token
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -211,13 +226,14 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 // softmax_step, with the distance from the reference, score * qscale - m, in place of the
 // logit, and the rows' maxima looked for only where some distance passes 8), and the
 // product with V.  codes, scales: the stage's in shared memory; vs the same of V; cnt:
-// tokens that are there of each 16.
+// there: tokens that are there, of the first 16 in the low byte, of the others above it.
 template <int D>
-__device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_t* vs, const int (&cnt)[2], int tok0,
+__device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_t* vs, int there, int tok0,
                                          int all_seen, const int (&seen)[2], const float (&qscale)[2],
                                          uint32_t q, float (&m)[2], float (&l)[2], float (&o)[D / 16][4],
                                          const Fp4At<D>& at, int lane) {
-  const bool edge = min(cnt[0], cnt[1]) < 16 || tok0 + 32 > all_seen;
+  const bool edge = there != kAllThere || tok0 + 32 > all_seen;
+  const int cnt[2] = {there & 0xff, there >> 8};
   if (edge) {
     // a NaN scale of V behind the last token, or where some row does not look
     uint32_t any = 0;
@@ -247,11 +263,11 @@ __device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_
     for (int i = 0; i < 2; ++i) {
       const uint32_t at_scale = scales + at.ks + (16 * h + 8 * i) * (D / 16);
       if constexpr (D == 128) {
-        const uint4 a = lds128(codes + at.k[h][i]);
+        const uint4 a = lds128(codes + at.k(h, i));
         w[i][0] = a.x, w[i][1] = a.y, w[i][2] = a.z, w[i][3] = a.w;
         f[i] = e4m3x2_to_f16x2(lds16(at_scale));
       } else {
-        const uint2 a = lds64(codes + at.k[h][i]);
+        const uint2 a = lds64(codes + at.k(h, i));
         w[i][0] = a.x, w[i][1] = a.y;
         f[i] = e4m3x2_to_f16x2(lds8(at_scale));
       }
@@ -265,8 +281,8 @@ __device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_
       e2m1x8_to_f16(w[1][y], kb);
       const uint32_t lo[4] = {hmul2(ka[0], fa), hmul2(kb[0], fb), hmul2(ka[1], fa), hmul2(kb[1], fb)};
       const uint32_t hi[4] = {hmul2(ka[2], fa), hmul2(kb[2], fb), hmul2(ka[3], fa), hmul2(kb[3], fb)};
-      mma_f16(s[h], lo, b.x, b.y);
-      mma_f16(s[h], hi, b.z, b.w);
+      mma_f16_free(s[h], lo, b.x, b.y);
+      mma_f16_free(s[h], hi, b.z, b.w);
     }
   }
   if (edge) {
@@ -286,9 +302,7 @@ __device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_
       for (int e = 0; e < 4; ++e) z[h][e] = fmaf(s[h][e], qscale[e & 1], -m[e & 1]);
   };
   distances();
-  float far = fmaxf(fmaxf(z[0][0], z[0][1]), z[0][2]);
-  far = fmaxf(fmaxf(far, z[0][3]), z[1][0]);
-  far = fmaxf(fmaxf(far, z[1][1]), fmaxf(z[1][2], z[1][3]));
+  const float far = max3(max3(z[0][0], z[0][1], z[0][2]), max3(z[0][3], z[1][0], z[1][1]), fmaxf(z[1][2], z[1][3]));
   if (__any_sync(kFullMask, far > 8.0f)) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -330,7 +344,7 @@ __device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_
       // matrix i: tokens 8 (i % 2) .. + 7 at the 32 columns of chunk 2 a + i / 2; a register has four
       // columns (4 g .. + 3) of two tokens, which become pairs of tokens after their conversion
       uint32_t v[4];
-      ldmatrix_x4_trans(v, codes + at.v[h][a]);
+      ldmatrix_x4_trans(v, codes + at.v(h, a));
 #pragma unroll
       for (int x = 0; x < 2; ++x) {  // columns 2 x and 2 x + 1 of the four
         uint32_t lo[4], hi[4];
@@ -342,11 +356,10 @@ __device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_
           hi[i] = hmul2(__byte_perm(e, f, 0x7632), sv[i >> 1][i & 1]);
         }
         const uint32_t va[4] = {lo[0], lo[2], lo[1], lo[3]}, vb[4] = {hi[0], hi[2], hi[1], hi[3]};
-        mma_f16(o[4 * a + 2 * x], va, pb[h][0], pb[h][1]);
-        mma_f16(o[4 * a + 2 * x + 1], vb, pb[h][0], pb[h][1]);
+        mma_f16_free(o[4 * a + 2 * x], va, pb[h][0], pb[h][1]);
+        mma_f16_free(o[4 * a + 2 * x + 1], vb, pb[h][0], pb[h][1]);
       }
     }
-  if (edge) fence_proxy_async_smem();  // the zeros, before the next copy into this stage
 }
 
 // ---------------------------------------------------------------------------
@@ -391,7 +404,8 @@ struct FewSmem {
   uint4 q[kFp4 ? D / 32 : 1][kFp4 ? 32 : 1];  // of 4 bits: the unit's q as B fragments (in registers otherwise)
   float red[kFewWarps / 2][8 * D];
   float2 ml[kFewWarps][8];
-  float4 group[kStages][kTile / 16];  // per 16 tokens: K scale, log2 of V scale, 1 / V scale (8 bits), valid tokens (int)
+  float4 group[kFp4 ? 1 : kStages][4];  // per 16 tokens: K scale, log2 of V scale, 1 / V scale, valid tokens (int)
+  int there[kFp4 ? kStages : 1][kFewWarps];  // of 4 bits: valid tokens of a warp's first 16, and 256 times those of the others
   // units of this share: request, KV head, first of the 8 rows, cached tokens;
   // first row, rows (true), rows within T; the share's tile at which the unit
   // would begin, its end tile within the share (0: no unit)
@@ -450,7 +464,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
   auto consumer_sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); };
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.full[s], kFp4 ? 1 + kTile / 16 : 1);  // 4 bits: and a lane's scales of 16 tokens each
       mbar_init(&sm.empty[s], kFewWarps);
     }
     fence_barrier_init();
@@ -612,6 +626,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
         const long long token = (((long long)now.id * p.Hkv + now.h) << p.page_shift) + (now.tok & ((1 << p.page_shift) - 1));
         const int row = (int)(token * kRow / 128);
         const int rounds = min(kRound, k_end - k0);
+        const int both = max(now.cnt, 0) | max(__shfl_down_sync(kFullMask, now.cnt, 1), 0) << 8;  // on even lanes
         float log_vs = 0.0f, inv_vs = 0.0f;
         for (int i = 0; i < rounds; ++i) {
           const bool ok = mbar_wait(&sm.empty[s], ph ^ 1, wg, 51);
@@ -620,16 +635,30 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
             if (k == i && copies) {
               tma_load_2d(&sm.kv[s][16 * j * kRow], &tm_k, &sm.full[s], 0, row);
               tma_load_2d(&sm.kv[s][(kTile + 16 * j) * kRow], &tm_v, &sm.full[s], 0, row);
-              if constexpr (kFp4) {
-                bulk_load(&sm.scale[s][0][j * D], static_cast<const uint8_t*>(p.k_scales) + token * (D / 16), box * D / 16, &sm.full[s]);
-                bulk_load(&sm.scale[s][1][j * D], static_cast<const uint8_t*>(p.v_scales) + token * (D / 16), box * D / 16, &sm.full[s]);
+            }
+            // scales: pieces of 16 bytes that do not pass through the TMA unit, whose requests
+            // bound calls on 16-token pages (drafts over 16 heads: @@)
+            if (kFp4 && k == i) {
+              if (now.cnt > 0) {
+                const uint8_t* ks = static_cast<const uint8_t*>(p.k_scales) + token * (D / 16);
+                const uint8_t* vs = static_cast<const uint8_t*>(p.v_scales) + token * (D / 16);
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                  cp_async16(smem_u32(&sm.scale[s][0][j * D + 16 * x]), ks + 16 * x);
+                  cp_async16(smem_u32(&sm.scale[s][1][j * D + 16 * x]), vs + 16 * x);
+                }
               }
+              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sm.full[s])) : "memory");
             }
             if (!kFp4 && i == 0) log_vs = log2f(now.vs), inv_vs = 1.0f / now.vs;  // the scales may still be on their way
-            if (k == i) sm.group[s][j] = make_float4(now.ks, log_vs, inv_vs, __int_as_float(now.cnt));
+            if constexpr (kFp4) {
+              if (k == i && !(j & 1)) sm.there[s][j >> 1] = both;
+            } else {
+              if (k == i) sm.group[s][j] = make_float4(now.ks, log_vs, inv_vs, __int_as_float(now.cnt));
+            }
             __syncwarp();
             const int n = __popc((copy_mask >> (kGroups * i)) & ((1u << kGroups) - 1));
-            if (lane == kGroups * i) mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(n * box * (kFp4 ? kRow + D / 16 : kRow) * 2));
+            if (lane == kGroups * i) mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(n * box * kRow * 2));
             issued = k0 + i + 1;
           }
           if (++s == kStages) s = 0, ph ^= 1;
@@ -708,14 +737,12 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
         const int begin = sm.begin[im];
         for (; tile < end; ++tile) {
           mbar_wait(&sm.full[stage], phase, wg, 52);
-          const float4 sc = sm.group[stage][kFp4 ? 2 * warp : warp];
+          const float4 sc = kFp4 ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : sm.group[stage][warp];
           // after a wait that gave up, whatever lies here
-          const int cnt = min(__float_as_int(sc.w), 16);
-          const int cnt2 = kFp4 ? min(max(__float_as_int(sm.group[stage][2 * warp + 1].w), 0), 16) : 0;
-          if (max(cnt, cnt2) <= 0) {
+          const int cnt = kFp4 ? sm.there[stage][warp] & 0x1f1f : min(__float_as_int(sc.w), 16);
+          if (cnt <= 0) {
           } else if constexpr (kFp4) {
-            const int there[2] = {max(cnt, 0), cnt2};
-            fp4_tile<D>(smem_u32(sm.kv[stage]), smem_u32(sm.scale[stage]) + warp * 2 * D, &sm.scale[stage][1][warp * 2 * D], there,
+            fp4_tile<D>(smem_u32(sm.kv[stage]), smem_u32(sm.scale[stage]) + warp * 2 * D, &sm.scale[stage][1][warp * 2 * D], cnt,
                         (tile - begin) * kTile + warp * 32, all_seen, seen, qscale, smem_u32(&sm.q[0][lane]), m, l, o, at, lane);
           } else {
             uint8_t* kt = &sm.kv[stage][warp * 16 * D];

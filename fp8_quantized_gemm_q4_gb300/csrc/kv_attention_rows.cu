@@ -147,11 +147,6 @@ template <int D>
 __device__ __forceinline__ long long piece_at(int cta, int first_cta) {
   return ((long long)cta * 2 + (cta == first_cta)) * (kM * (D + 2));
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float y;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
 // NaN into the columns part * D / 4 .. of a row whose tokens from .. to - 1 hold NaN
 // codes (4 bits: scales) of V there, in the output (dst) or the unit's piece.  Out of
 // line, for units that meet none.
