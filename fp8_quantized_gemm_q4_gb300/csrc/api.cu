@@ -1327,7 +1327,8 @@ bs_status bs_kv_append_rotary(const bs_kv_append_rotary_args* a, bs_stream_t str
     return fail(BS_ERR_INVALID, "kv_append_rotary: rotary_dim=%d not a multiple of 16 up to D=%d", a->rotary_dim, a->D);
   if (a->rotary_dim > 0 && (a->max_positions <= 0 || a->max_positions > INT32_MAX))
     return fail(BS_ERR_INVALID, "kv_append_rotary: max_positions=%lld", (long long)a->max_positions);
-  if (a->Hkv > 16384 || a->Hq > 65535 || (a->T + 3) / 4 * (2 * (int64_t)a->Hkv + a->Hq + 1) > INT32_MAX)  // the launch grid
+  if (a->T > 1 << 30 || a->Hkv > 16384 || a->Hq > 65535 ||
+      (a->T + 3) / 4 * (2 * (int64_t)a->Hkv + a->Hq + 1) > INT32_MAX)  // rows in 32 bits with room, the launch grid
     return fail(BS_ERR_UNSUPPORTED, "kv_append_rotary: T=%lld rows of Hq=%d and Hkv=%d heads in one call", (long long)a->T,
                 a->Hq, a->Hkv);
   if (a->T == 0) return BS_OK;
@@ -1455,6 +1456,7 @@ bs_status bs_lora_add(const bs_lora_args* a, bs_stream_t stream) {
       !aligned4(a->scales) || !aligned4(a->cu_rows) || !aligned4(a->which))
     return fail(BS_ERR_ALIGN, "lora_add: x, a, b, y and out must be 16-byte aligned, row strides multiples of 8");
   if (a->out == a->y && a->T > 1 && a->ldo != a->ldy) return fail(BS_ERR_INVALID, "lora_add: out in y's place needs its stride");
+  if (a->out == a->x) return fail(BS_ERR_INVALID, "lora_add: out is x, which other CTAs still read");
   int sms = 0;
   bsk::LoraParams p = {};
   if (!device_info(&p.status, &sms)) return fail(BS_ERR_CUDA, "no current device");

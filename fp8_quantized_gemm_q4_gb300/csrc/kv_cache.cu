@@ -231,10 +231,10 @@ __global__ void __launch_bounds__(256) kv_positions_kernel(const int* seq_lens, 
   extern __shared__ int ends[];
   for (int b = threadIdx.x; b < B; b += 256) ends[b] = cu_new[b + 1];
   __syncthreads();
-  const int r = blockIdx.x * 256 + threadIdx.x;
-  if (r >= T) return;
-  const int b = upper_bound(ends, B, r);
-  positions[r] = b < B ? seq_lens[b] + (r - cu_new[b]) : 0;
+  const unsigned r = blockIdx.x * 256 + threadIdx.x;
+  if (r >= (unsigned)T) return;
+  const int b = upper_bound(ends, B, (int)r);
+  positions[r] = b < B ? seq_lens[b] + ((int)r - cu_new[b]) : 0;
 }
 
 cudaError_t launch_kv_positions(const int* seq_lens, const int* cu_new, int B, int T, int* positions, cudaStream_t stream) {

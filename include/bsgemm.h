@@ -720,7 +720,10 @@ bs_status bs_kv_attention_fp4(const bs_kv_attention_args *args, const uint8_t *k
  *   q_out      bf16 [T, Hq, D], likewise; may be q itself (bf16, the same strides), no
  *              other overlap of outputs and inputs
  *   slots      int32 [T]; a row with a negative slot is skipped, its query too; one
- *              past the cache likewise, and sets BS_ERR_OFFSETS
+ *              past the cache likewise, and sets BS_ERR_OFFSETS.  A slot that a call names
+ *              twice holds nothing of use afterwards (its codes and scales may be
+ *              those of different rows)
+ *   T          up to 2^30
  *   positions  int32 [T]; one outside [0, max_positions) sets BS_ERR_OFFSETS and is
  *              taken as the nearest
  *   angles     fp32 [max_positions, rotary_dim], 16-byte aligned
@@ -815,7 +818,7 @@ bs_status bs_fp4_matvec(const bs_fp4_matvec_args *args, bs_stream_t stream);
  *   which      int32 [B]; negative: no adapter; adapters and above: none either, and
  *              sets BS_ERR_OFFSETS
  *   y, out     fp32 or bf16 (dtype) [T, ldy], [T, ldo]; out may be y (same stride), no
- *              other overlap
+ *              other overlap (out at x's address is refused)
  *   r          a multiple of 8, 8 .. 128; K and N multiples of 8, K <= 2^22, B <= 8192
  *   all matrices 16-byte aligned, row strides multiples of 8 elements
  * ------------------------------------------------------------------------- */

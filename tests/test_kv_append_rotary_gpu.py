@@ -233,3 +233,75 @@ def test_gather(cuda_lib, fp4, D, page, Hkv):
     bs.clear_device_status()
     empty = bs.kv_gather(cache, i32([]))
     assert empty[0].shape == (0, Hkv, D)
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_cache_past_32_bits(cuda_lib, fp4):
+    """Pages whose byte offset passes 2^32, written and read back, against the same rows in a small cache."""
+    bs = cuda_lib
+    page, H, D = 128, 8, 128
+    kind = bs.KVCacheFP4 if fp4 else bs.KVCache
+    pages = (1 << 32) // (page * H * (D // 2 if fp4 else D)) + 3
+    big, small = kind.empty(pages, H, page, D), kind.empty(3, H, page, D)
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    T = 300
+    x = torch.randn((T, 3 * H, D), device=DEV, generator=gen).to(torch.bfloat16)
+    q, k, v = x.split(H, 1)
+    at = torch.arange(T, device=DEV, dtype=torch.int32)
+    angles = bs.rotary_angles(T, D)
+    here, there = at + 50, at + 50 + (pages - 3) * page
+    a = bs.kv_append_rotary(q, k, v, here, at, angles, small)
+    b = bs.kv_append_rotary(q, k, v, there, at, angles, big)
+    assert torch.equal(a, b) and all(torch.equal(s, t[-3:]) for s, t in zip(small, big))
+    assert all(torch.equal(s, t) for s, t in zip(bs.kv_gather(small, here), bs.kv_gather(big, there)))
+    assert all(bool((t[:4] == (0 if t.dtype == torch.uint8 else 1)).all()) for t in big)
+    assert bs.device_status()[0] == bs.BS_OK
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_rows_past_32_bits(cuda_lib, fp4):
+    """Inputs and outputs whose offsets pass 2^32 bytes."""
+    bs = cuda_lib
+    cache, want = ((bs.KVCacheFP4 if fp4 else bs.KVCache).empty(2, 1, 16, 64) for _ in range(2))
+    wide = torch.zeros(((1 << 31) + (1 << 20),), device=DEV, dtype=torch.bfloat16)      # 4 GiB and more
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    x = torch.randn((3, 1, 64), device=DEV, generator=gen).to(torch.bfloat16)
+    far = torch.as_strided(wide, (3, 1, 64), (1 << 30, 64, 1))
+    far.copy_(x)
+    out = torch.as_strided(wide, (3, 1, 64), (1 << 30, 64, 1), 64)
+    slots, pos, angles = i32([0, 1, 2]), i32([4, 5, 6]), bs.rotary_angles(9, 64)
+    a = bs.kv_append_rotary(x, x, x, slots, pos, angles, want)
+    assert bs.kv_append_rotary(far, far, far, slots, pos, angles, cache, q_out=out) is out
+    assert torch.equal(out, a) and all(torch.equal(s, t) for s, t in zip(cache, want))
+    assert torch.equal(far, x)
+    k, v = (torch.as_strided(wide, (3, 1, 64), (1 << 30, 64, 1), n) for n in (128, 192))
+    bs.kv_gather(cache, slots, out=(k, v))
+    assert all(torch.equal(s, t) for s, t in zip((k, v), bs.kv_gather(want, slots)))
+
+
+def test_on_two_streams_and_captured(cuda_lib):
+    """Two calls at once on caches of their own, one of them a replayed graph."""
+    bs = cuda_lib
+    sets = []
+    for seed, fp4, T in ((1, True, 700), (2, False, 3000)):
+        gen = torch.Generator(device=DEV).manual_seed(seed)
+        x = torch.randn((T, 6, 64), device=DEV, generator=gen).to(torch.bfloat16)
+        slots, pos, pages = layout(seed, [5, 0], [T // 2, T - T // 2], 64)
+        cache = (bs.KVCacheFP4 if fp4 else bs.KVCache).empty(pages, 2, 64, 64)
+        args = (*x.split([2, 2, 2], 1), i32(slots), i32(pos), bs.rotary_angles(max(pos) + 1, 32), cache)
+        want = bs.kv_append_rotary(*args), *(t.clone() for t in cache)
+        sets.append((args, cache, want, torch.cuda.Stream()))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = bs.kv_append_rotary(*sets[0][0])
+    for _ in range(10):
+        for args, cache, _, side in sets:
+            side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(sets[0][3]):
+            g.replay()
+        other = bs.kv_append_rotary(*sets[1][0], stream=sets[1][3])
+        torch.cuda.synchronize()
+        for got, (_, cache, want, _) in zip((out, other), sets):
+            assert torch.equal(got, want[0]) and all(torch.equal(s, t) for s, t in zip(cache, want[1:]))
+        out.zero_()
+        torch.cuda.synchronize()

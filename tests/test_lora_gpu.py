@@ -186,3 +186,26 @@ def test_empty(cuda_lib):
     assert bool((out == 3).all())
     assert bs.lora_add(x[:0], y[:0], a, b, i32([0, 0]), i32([0])).shape == (0, 64)
     assert torch.equal(bs.lora_add(x, y, a[:0], b[:0], i32([0, 4]), i32([-1])), y)
+
+
+@pytest.mark.parametrize("lens", [[1, 1, 1], [40, 60, 90]])
+def test_rows_past_32_bits(cuda_lib, lens):
+    """Rows of x, y and out, and adapters, whose offsets pass 2^32 bytes."""
+    bs = cuda_lib
+    T, K, N, r = sum(lens), 64, 72, 8
+    x, y, a, b, s = build(9, T, K, N, r, 3, torch.bfloat16)
+    want = bs.lora_add(x, y, a, b, i32(offsets(lens)), i32([0, 2, 1]), scales=s)
+    step = ((1 << 31) // (T - 1) + 64) // 8 * 8
+    room = torch.zeros((T * step,), device=DEV, dtype=torch.bfloat16)
+    wx, wy, wo = (torch.as_strided(room, (T, n), (step, 1), at) for n, at in ((K, 0), (N, 64), (N, 136)))
+    wx.copy_(x), wy.copy_(y)
+    bs.lora_add(wx, wy, a, b, i32(offsets(lens)), i32([0, 2, 1]), scales=s, out=wo)
+    assert torch.equal(wo, want) and torch.equal(wx, x) and torch.equal(wy, y)
+    # an adapter behind 2^32 bytes of others
+    n = (1 << 31) // (r * K) + 2
+    big = torch.zeros((n, r, K), device=DEV, dtype=torch.bfloat16)
+    big[-1] = a[0]
+    small_b = torch.zeros((n, N, r), device=DEV, dtype=torch.bfloat16)
+    small_b[-1] = b[0]
+    got = bs.lora_add(x, y, big, small_b, i32([0, T]), i32([n - 1]))
+    assert torch.equal(got, bs.lora_add(x, y, a, b, i32([0, T]), i32([0])))

@@ -49,6 +49,7 @@ def test_append_rotary_refusals(bs):
     for name in "q q_out k v slots positions angles k_codes v_codes k_scales v_scales".split():
         assert call(**{name: None}) == bs.BS_ERR_INVALID, name
         assert call(**{name: G + 2}) == bs.BS_ERR_ALIGN, name
+    assert call(T=(1 << 30) + 4, Hq=0, Hkv=1, q=None, q_out=None) == bs.BS_ERR_UNSUPPORTED
     assert call(T=0, k=None) == bs.BS_OK
 
 
@@ -104,7 +105,7 @@ def test_lora_refusals(bs):
     assert lib.bs_lora_add(None, None) == bs.BS_ERR_INVALID
     call = caller(lib.bs_lora_add, bs._LORA_ARGS, good)
     for kw in (dict(T=-1), dict(T=1 << 31), dict(B=-1), dict(K=0), dict(N=-8), dict(adapters=-1), dict(dtype=3), dict(ldx=248),
-               dict(ldy=504), dict(ldo=504), dict(out=F, ldo=1024)):
+               dict(ldy=504), dict(ldo=504), dict(out=4 * F, y=4 * F, ldo=1024), dict(out=F, y=4 * F)):
         assert call(**kw) == bs.BS_ERR_INVALID, kw
     for kw in (dict(r=0), dict(r=12), dict(r=136), dict(B=9000), dict(K=1 << 23, ldx=1 << 23)):
         assert call(**kw) == bs.BS_ERR_UNSUPPORTED, kw
