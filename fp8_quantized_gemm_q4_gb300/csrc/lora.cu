@@ -5,8 +5,8 @@
 // launch: the CTAs share K, and their partial products t = x A^T (mma.sync, rows on M,
 // ranks on N) meet in distributed shared memory, where every CTA adds them in the same
 // order; then the CTAs share N.  t stays fp32 and enters the second product scaled and
-// split into two bf16 (hi + lo, within 2^-17 of it; products with the bf16 B are exact,
-// sums fp32).
+// split into two bf16 (within 2^-17 of it), or three where out is fp32 (within 2^-25);
+// products with the bf16 B are exact, sums fp32.
 #include "decode.h"
 #include "decode.cuh"
 
@@ -106,10 +106,21 @@ __device__ __forceinline__ void copy_rows(const LoraParams& p, const Tile& t, in
   }
 }
 
+// Terms that t is split into for outputs of this type, and the next of them: v to bf16
+// pairs, v becomes what they leave
+template <bool kBf16>
+constexpr int kTerms = kBf16 ? 2 : 3;
+__device__ __forceinline__ uint2 next_term(float4& v) {
+  const uint32_t a = pack_bf16x2(v.x, v.y), b = pack_bf16x2(v.z, v.w);
+  v.x -= __uint_as_float(a << 16), v.y -= __uint_as_float(a & 0xffff0000u);
+  v.z -= __uint_as_float(b << 16), v.w -= __uint_as_float(b & 0xffff0000u);
+  return make_uint2(a, b);
+}
+
 // t of the cluster: the CTAs' sums (kVecs float4 at `sums` in each) added in order of rank,
-// scaled, as two bf16 at hi and lo
-template <int kVecs>
-__device__ __forceinline__ void gather_t(const LoraParams& p, int id, int size, const float* sums, __nv_bfloat16* hi, __nv_bfloat16* lo) {
+// scaled, as its terms at t, kVecs times 8 bytes each
+template <int kVecs, int kTerm>
+__device__ __forceinline__ void gather_t(const LoraParams& p, int id, int size, const float* sums, void* t) {
   const float scale = p.scales ? p.scales[id] : 1.0f;
   const uint32_t mine = smem_u32(sums);
   for (int x = threadIdx.x; x < kVecs; x += kThreads) {
@@ -120,11 +131,8 @@ __device__ __forceinline__ void gather_t(const LoraParams& p, int id, int size, 
       v.x += e.x, v.y += e.y, v.z += e.z, v.w += e.w;
     }
     v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
-    const uint32_t h0 = pack_bf16x2(v.x, v.y), h1 = pack_bf16x2(v.z, v.w);
-    const uint32_t l0 = pack_bf16x2(v.x - __uint_as_float(h0 << 16), v.y - __uint_as_float(h0 & 0xffff0000u));
-    const uint32_t l1 = pack_bf16x2(v.z - __uint_as_float(h1 << 16), v.w - __uint_as_float(h1 & 0xffff0000u));
-    reinterpret_cast<uint2*>(hi)[x] = make_uint2(h0, h1);
-    reinterpret_cast<uint2*>(lo)[x] = make_uint2(l0, l1);
+#pragma unroll
+    for (int i = 0; i < kTerm; ++i) static_cast<uint2*>(t)[i * kVecs + x] = next_term(v);
   }
 }
 
@@ -168,17 +176,18 @@ struct Eight {
 // ---------------------------------------------------------------------------
 constexpr int kFewRows = 8;
 
-template <int kRank>
+template <int kRank, int kTerm>
 struct FewSmem {
-  float part[kWarps][kFewRows][kRank];  // of the warps; [0]: of the CTA
-  __nv_bfloat16 t[2][kFewRows][kRank];  // hi, lo of the scaled t
+  float part[kWarps][kFewRows][kRank];      // of the warps; [0]: of the CTA
+  __nv_bfloat16 t[kTerm][kFewRows][kRank];  // the terms of the scaled t
   long long scan[kWarps];
   int4 tile;
 };
 
 template <int kRank, bool kBf16>
 __global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : kRank > 32 ? 2 : 4) lora_few_kernel(const __grid_constant__ LoraParams p) {
-  __shared__ __align__(16) FewSmem<kRank> sm;
+  constexpr int kTerm = kTerms<kBf16>;
+  __shared__ __align__(16) FewSmem<kRank, kTerm> sm;
   constexpr int kNT = kRank / 8, kKB = kRank / 32;  // tiles of 8 ranks, blocks of 32
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int size = (int)cluster_size(), rank = (int)cluster_ctarank();
@@ -254,19 +263,19 @@ __global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : kRank > 32 ? 2 : 4)
   load(chunk);
   __syncwarp();
   cluster_wait();
-  gather_t<kVecs>(p, tile.id, size, &sm.part[0][0][0], &sm.t[0][0][0], &sm.t[1][0][0]);
+  gather_t<kVecs, kTerm>(p, tile.id, size, &sm.part[0][0][0], sm.t);
   __syncthreads();
   cluster_arrive();  // this CTA has read the others' sums
-  uint4 t[2][kKB];
+  uint4 t[kTerm][kKB];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < kTerm; ++h)
 #pragma unroll
     for (int k = 0; k < kKB; ++k) t[h][k] = *reinterpret_cast<const uint4*>(&sm.t[h][g][32 * k + 8 * c]);
 #pragma unroll 1
   for (; chunk < c1; chunk += kWarps) {
     float acc[4][4] = {};
 #pragma unroll
-    for (int h = 1; h >= 0; --h)
+    for (int h = kTerm - 1; h >= 0; --h)
 #pragma unroll
       for (int k = 0; k < kKB; ++k) {
         const uint32_t f0[4] = {t[h][k].x, 0, t[h][k].y, 0}, f1[4] = {t[h][k].z, 0, t[h][k].w, 0};
@@ -293,17 +302,18 @@ __global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : kRank > 32 ? 2 : 4)
 constexpr int kManyRows = 64, kSlice = 64;  // rows of a tile; K, or columns, of a stage
 
 // Shared memory: four stages of x and A, or in their place three of B and y, the last of
-// which holds the CTA's sums until it is needed, and t (hi, lo).
+// which holds the CTA's sums until it is needed, and t's terms.
 template <int kRank, bool kBf16>
 struct ManySmem {
   static constexpr int kStages1 = 4, kStages2 = 3;
   static constexpr int kStage1 = (kManyRows + kRank) * kSlice * 2;
   static constexpr int kB = kSlice * kRank * 2, kPieces = kBf16 ? 2 : 4;  // bytes of B; 16-byte pieces of y a thread
   static constexpr int kStage2 = kB + kPieces * kThreads * 16;
-  static constexpr int kT = kManyRows * kRank * 2, kSums = 2 * kT;        // bytes of hi or lo, of the sums
+  static constexpr int kT = kManyRows * kRank * 2, kSums = 2 * kT;        // bytes of a term of t, of the sums
   static constexpr int kSumsAt = (kStages2 - 1) * kStage2;
   static constexpr int kTAt = kSumsAt + (kSums > kStage2 ? kSums : kStage2);
-  static constexpr int kBytes = kTAt + 2 * kT > kStages1 * kStage1 ? kTAt + 2 * kT : kStages1 * kStage1;
+  static constexpr int kEnd = kTAt + kTerms<kBf16> * kT;
+  static constexpr int kBytes = kEnd > kStages1 * kStage1 ? kEnd : kStages1 * kStage1;
 };
 
 // Place of the 16-byte piece `chunk` of a row of x or A, of a column of B or of a row of t
@@ -451,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : kBf16 ? 3 : 2) lora
   __syncwarp();
   cluster_wait();
   {
-    // this CTA's share of t: the sums of all CTAs in order of rank, scaled, as hi and lo to all
+    // this CTA's share of t: the sums of all CTAs in order of rank, scaled, its terms to all
     constexpr int kVecs = kManyRows * kRank / 4;
     const float scale = p.scales ? p.scales[tile.id] : 1.0f;
     for (int x = kVecs * rank / size + tid; x < kVecs * (rank + 1) / size; x += kThreads) {
@@ -462,16 +472,13 @@ __global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : kBf16 ? 3 : 2) lora
         v.x += e.x, v.y += e.y, v.z += e.z, v.w += e.w;
       }
       v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
-      const uint32_t h0 = pack_bf16x2(v.x, v.y), h1 = pack_bf16x2(v.z, v.w);
-      const uint32_t l0 = pack_bf16x2(v.x - __uint_as_float(h0 << 16), v.y - __uint_as_float(h0 & 0xffff0000u));
-      const uint32_t l1 = pack_bf16x2(v.z - __uint_as_float(h1 << 16), v.w - __uint_as_float(h1 & 0xffff0000u));
       const int row = x / (kRank / 4), half_piece = x % (kRank / 4);
       const uint32_t to = smem + S::kTAt + t_at<kRow>(row, half_piece >> 1) + 8 * (half_piece & 1);
+#pragma unroll
+      for (int i = 0; i < kTerms<kBf16>; ++i) {
+        const uint2 w = next_term(v);
 #pragma unroll 8
-      for (int r = 0; r < size; ++r) {
-        const uint32_t there = mapa_shared(to, r);
-        st_cluster(there, h0, h1);
-        st_cluster(there + S::kT, l0, l1);
+        for (int r = 0; r < size; ++r) st_cluster(mapa_shared(to, r) + i * S::kT, w.x, w.y);
       }
     }
   }
@@ -488,20 +495,21 @@ __global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : kBf16 ? 3 : 2) lora
     float acc[4][4] = {};
 #pragma unroll
     for (int j = 0; j < kRank / 16; ++j) {
-      uint32_t hi[4], lo[4];
-      const uint32_t at = smem + S::kTAt + t_at<kRow>(16 * block + (lane & 15), 2 * j + (lane >> 4));
-      ldmatrix_x4(hi, at);
-      ldmatrix_x4(lo, at + S::kT);
+      uint32_t t[kTerms<kBf16>][4];
+#pragma unroll
+      for (int h = 0; h < kTerms<kBf16>; ++h)
+        ldmatrix_x4(t[h], smem + S::kTAt + h * S::kT + t_at<kRow>(16 * block + (lane & 15), 2 * j + (lane >> 4)));
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {
         // lanes 0 .. 7: column n = lane of tile i, 16 .. 23: of tile i + 1; 8 .. 15 and 24 .. 31 the next 8 ranks
         const int n = lane & 7, col = 32 * half + 8 * (n >> 1) + 2 * (i + (lane >> 4)) + (n & 1);
         uint32_t w[4];
         ldmatrix_x4(w, bs + column_at<kRow>(col, 2 * j + ((lane >> 3) & 1)));
-        mma_bf16_16x8(acc[i], lo, w[0], w[1]);
-        mma_bf16_16x8(acc[i + 1], lo, w[2], w[3]);
-        mma_bf16_16x8(acc[i], hi, w[0], w[1]);
-        mma_bf16_16x8(acc[i + 1], hi, w[2], w[3]);
+#pragma unroll
+        for (int h = kTerms<kBf16> - 1; h >= 0; --h) {
+          mma_bf16_16x8(acc[i], t[h], w[0], w[1]);
+          mma_bf16_16x8(acc[i + 1], t[h], w[2], w[3]);
+        }
       }
     }
     const int n = kSlice * k + 32 * half + 8 * c;

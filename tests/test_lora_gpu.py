@@ -2,9 +2,9 @@
 
 Bound: with t = x A^T and S = scale |x| |A|^T |B|^T, fp32 sums of exact products over K
 (any order: relative K 2^-24 of the sum of magnitudes, at most) and over r, and t as a
-pair of bf16 (2^-8 of 2^-9: 2^-16 at most):
-    |out - ref| <= (2^-16 + (K + 2 r + 8) 2^-24) S + round |ref|
-with round 2^-8 for bf16 outputs and 2^-23 for fp32."""
+pair of bf16 (2^-8 of 2^-9: 2^-16 at most; for fp32 outputs three: 2^-24):
+    |out - ref| <= (term + (K + 3 r + 8) 2^-24) S + round |ref|
+with term and round 2^-16 and 2^-8 for bf16 outputs, 2^-24 and 2^-23 for fp32."""
 import random
 
 import pytest
@@ -35,8 +35,8 @@ def check(bs, x, y, a, b, cu, which, scales, **kw):
     got = bs.lora_add(x, y, a, b, i32(cu), i32(which), scales=scales, **kw)
     assert bs.device_status()[0] == bs.BS_OK
     n, K, r = cu[-1], x.shape[1], a.shape[1]
-    step = 2.0 ** -8 if y.dtype == torch.bfloat16 else 2.0 ** -23
-    bound = (2.0 ** -16 + (K + 2 * r + 8) * 2.0 ** -24) * size[:n] + step * want[:n].abs()
+    term, step = (2.0 ** -16, 2.0 ** -8) if y.dtype == torch.bfloat16 else (2.0 ** -24, 2.0 ** -23)
+    bound = (term + (K + 3 * r + 8) * 2.0 ** -24) * size[:n] + step * want[:n].abs()
     err = (got[:n].double() - want[:n]).abs()
     assert bool((err <= bound).all()), float((err / bound.clamp(min=1e-30)).max())
     return got
