@@ -347,8 +347,11 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t x, uint32_t y
   asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
 }
 
+// CTAs of an SM
+constexpr int many_resident(int rank, bool bf16) { return rank > 64 ? 1 : rank > 32 && !bf16 ? 2 : 3; }
+
 template <int kRank, bool kBf16>
-__global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : kBf16 ? 3 : 2) lora_many_kernel(const __grid_constant__ LoraParams p) {
+__global__ void __launch_bounds__(kThreads, many_resident(kRank, kBf16)) lora_many_kernel(const __grid_constant__ LoraParams p) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ long long scan[kWarps];
   __shared__ int4 found;
@@ -547,15 +550,27 @@ cudaError_t launch_lora(const LoraParams& p, int sms, cudaStream_t stream) {
   // 12.4; 64 requests of 4 rows 14 / 28, of 16 rows 25 / 31, of 32 rows 40 / 37
   const bool many = p.T >= kManyEach * p.B;
   // every request may end in a tile that is not full
-  const long long tiles = p.T / (many ? kManyRows : kFewRows) + (p.B < p.T ? p.B : p.T);
-  // Eight CTAs a tile; of few rows fewer where not all would be on the GPU at once, for each
-  // has its own start and exchange (us with 8 / 4 / 2 / 1, K = 4096, N = 6144: rank 16, 1 request
-  // 6.3 / 8.6 / 12 / 19, 64 requests 10.4 / 10.3 / 12.6 / 19, 256 requests 36 / 26 / 25 / 28; rank 64, 256
-  // requests 81 / 62 / 53 / 49).  Of many rows the next CTAs start while others end (8190 rows,
-  // rank 64: 77 / 77 / 99 / 91; 8192 rows, rank 16: 67 / 80 / 77 / 82; 512 rows: 13 / 21 / 37 / 69).
+  const long long full = p.T / (many ? kManyRows : kFewRows), requests = p.B < p.T ? p.B : p.T, tiles = full + requests;
   int cluster = 8;
-  const long long at_once = (long long)sms * (p.r <= 32 ? 4 : p.r <= 64 ? 2 : 1);
-  while (!many && cluster > 1 && tiles * cluster > at_once) cluster /= 2;
+  if (many) {
+    // The size whose CTAs take the fewest rounds on the GPU for their shares of a tile, the
+    // smaller of equals: a round that is not full costs as much as one that is.  Clusters do
+    // not fill the last twentieth (us with 8 / 6 / 4 / 3 / 2, K = N = 4096 but where given: rank 16, bf16,
+    // 3584 rows 31 / 26 / 33 / 32 / 34, 4800 rows 37 / 38 / 34 / 42 / 36, 8192 rows, N = 6144, 66 / 62 / 79 / 57 / 77,
+    // 9600 rows 56 / 60 / 62 / 67 / 60; rank 64, 8190 rows, K = 7168, 77 / 74 / 77 / 72 / 99; rank 128, 4096 rows
+    // 94 / 76 / 65 / 83 / 59, 1200 rows 38 / 26 / 33 / 42 / 58; fp32, rank 16, 3000 rows 37 / 49 / 46 / 60 / 51).
+    const long long at_once = (long long)sms * many_resident(p.r <= 32 ? 32 : p.r <= 64 ? 64 : 128, p.bf16) * 19 / 20;
+    const long long expected = full + (requests + 1) / 2;
+    const auto rounds = [&](int size) { return (expected * size + at_once - 1) / at_once; };
+    for (const int size : {6, 4, 3, 2})
+      if (rounds(size) * cluster <= rounds(cluster) * size) cluster = size;
+  } else {
+    // Eight CTAs a tile, fewer where not all would be on the GPU at once, for each has its own
+    // start and exchange (us with 8 / 4 / 2 / 1, K = 4096, N = 6144: rank 16, 1 request 6.3 / 8.6 / 12 / 19, 64
+    // requests 10.4 / 10.3 / 12.6 / 19, 256 requests 36 / 26 / 25 / 28; rank 64, 256 requests 81 / 62 / 53 / 49).
+    const long long at_once = (long long)sms * (p.r <= 32 ? 4 : p.r <= 64 ? 2 : 1);
+    while (cluster > 1 && tiles * cluster > at_once) cluster /= 2;
+  }
   return p.bf16 ? launch_rank<true>(p, many, cluster, tiles, stream) : launch_rank<false>(p, many, cluster, tiles, stream);
 }
 

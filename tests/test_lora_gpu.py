@@ -91,6 +91,16 @@ def test_many_rows_and_requests(cuda_lib):
         check(cuda_lib, x, y, a, b, offsets(lens), [rng.randint(-1, 69) for _ in lens], s)
 
 
+@pytest.mark.parametrize("lens,r,dt", [([3500, 31], 16, torch.bfloat16), ([2800, 0, 3200], 32, torch.bfloat16),
+                                       ([8200], 64, torch.bfloat16), ([11900, 100], 8, torch.bfloat16),
+                                       ([1190], 128, torch.bfloat16), ([1000, 3090], 128, torch.float32),
+                                       ([4000, 100], 24, torch.float32), ([9000], 40, torch.float32)])
+def test_rounds(cuda_lib, lens, r, dt):
+    """Rows enough for more than one round of tiles on the GPU: clusters of eight down to two CTAs."""
+    x, y, a, b, s = build(r, sum(lens), 328, 264, r, 3, dt)
+    check(cuda_lib, x, y, a, b, offsets(lens), [2, 0, 1][:len(lens)], s)
+
+
 def test_strides(cuda_lib):
     """Rows of x, y and out as slices of wider matrices, what is beside them untouched; another stream."""
     lens, which = [3, 40, 1], [1, 0, 1]
