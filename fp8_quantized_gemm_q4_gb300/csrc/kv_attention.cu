@@ -1,5 +1,5 @@
-// kv_attention.cu -- causal attention of new tokens over the paged 8-bit
-// cache:  o = softmax(scale q K^T) V  with K = s_K[page, head] * code and V
+// kv_attention.cu -- causal attention of new tokens over the paged 8-bit or 4-bit
+// cache.  Of 8 bits:  o = softmax(scale q K^T) V  with K = s_K[page, head] * code and V
 // likewise; row i of a request with n new and m cached tokens (the new ones
 // included) sees the cached positions 0 .. m - n + i.
 //
@@ -13,6 +13,10 @@
 // fits fp16 (rounded to 11 bits, the only rounding below fp32), and o, lse
 // follow from (m, l, sum).  m moves, and the accumulators are rescaled, only
 // when max u passes m + 8.
+//
+// 4-bit cache: a value is an E2M1 code times the e4m3 scale of its 16 elements of a
+// token, 1 + 3 significant bits from 2^-10 to 2688: exact in fp16, as K and V are.  So
+// u_t = scale log2(e) q.k_t, w_t = 2^(u_t - m), and o, lse = sum w_t v_t / sum w_t, m + log2.
 #include "kv_attention.cuh"
 
 namespace bsk {
@@ -365,9 +369,9 @@ __device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_
 // ---------------------------------------------------------------------------
 // Requests with at most few_rows rows per KV head (decode, drafts): bound by the
 // cache stream.  Work is a list of (request, head, 8 rows) units of 64-token
-// tiles, cut into contiguous shares of equal cost, whatever the lengths.  Three CTAs an
+// tiles (4 bits: 128), cut into contiguous shares of equal cost, whatever the lengths.  Three CTAs an
 // SM take one each: a producer warp keeps 64 KB of codes in flight with TMA copies
-// page by page, four consumer warps take 16 tokens of a tile each, and while one
+// page by page, four consumer warps take 16 tokens of a tile each (4 bits: 32), and while one
 // CTA joins the warps' results of a unit, the other two stream (one CTA with 12
 // consumer warps lost 25 of 134 us to that).  Both products run transposed,
 // tokens and then head columns on the MMA's M and the rows on its N = 8:
@@ -379,13 +383,24 @@ __device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_
 // 24 us, bound by what a unit costs beside its tiles (q, the join of the warps, its
 // piece); one token over 1000: 10 us, a chain of dependent reads.  Three CTAs an SM
 // leave 128 registers a thread, of which 16 to 20 bytes are spilled.
+// Of 4 bits, which halve the stream, the same calls take 76 us (340 MB, 0.66 of HBM), 23 us
+// (34 MB) and 9 to 15 us.  A cached element costs what it does with 8 bits and the product
+// with its scale: 324 instructions a warp and 16 tokens, 156 of them for one pipe
+// (conversions, byte exchanges), in 0.57 of the issue slots.  So 32 tokens a step, whose
+// chains of products run side by side, maxima looked for only where a score passes its
+// reference by 8, and q as fragments in shared memory (107 / 83 / 77 us with each).  The
+// CTAs of an SM end their equal shares after 50 to 75 us.  Measured beside it: smaller shares
+// for CTAs that take the place of those that end first 91 to 93 (against 83 in the same
+// graph: a start costs more than the waiting), shares by place in the grid and four CTAs
+// of 96 registers no gain.
 // ---------------------------------------------------------------------------
 constexpr int kItems = 32;         // units listed at a time
-template <bool kFp4>
-constexpr int kMinTilesOf = kFp4 ? 2 : 2;  // least cost worth a CTA of its own
+constexpr int kMinTiles = 2;       // least cost worth a CTA of its own
 // What a unit costs beside its tiles (q, the join of the warps, a piece), in tiles.
 // us with 0 / 2 / 4 / 10: 64 decode requests 107.6 / 106.1 / 105.5 / 106, drafts over 16
-// heads 24.8 / 23.3 / 22.9 / 23.9, 64 requests of 30 to 14000 tokens 20.6 / 17.4 / 16.6 / 16.7
+// heads 24.8 / 23.3 / 22.9 / 23.9, 64 requests of 30 to 14000 tokens 20.6 / 17.4 / 16.6 / 16.7.  Of 4 bits,
+// tiles twice as long, with 0 / 1 / 2 / 4: 64 decode requests 86 / 83 / 83 / 84, drafts 26.4 / 26.1 /
+// 25.4 / 26.2, 300 requests of 200 to 2000 tokens 94 / 87 / 84 / 89
 template <bool kFp4>
 constexpr int kUnitTilesOf = kFp4 ? 2 : 4;
 constexpr int kCounters = 1024;    // arrival counters at the head of the workspace
@@ -455,7 +470,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
                             const __grid_constant__ KvAttentionParams p) {
   extern __shared__ uint8_t smem_raw[];
   using Smem = FewSmem<D, kFp4>;
-  constexpr int kRow = Smem::kRow, kTile = Smem::kTile, kUnitTiles = kUnitTilesOf<kFp4>, kMinTiles = kMinTilesOf<kFp4>;
+  constexpr int kRow = Smem::kRow, kTile = Smem::kTile, kUnitTiles = kUnitTilesOf<kFp4>;
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr int kStages = Smem::kStages, kWarps = kFewWarps, kThreads = kFewThreads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -637,7 +652,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
               tma_load_2d(&sm.kv[s][(kTile + 16 * j) * kRow], &tm_v, &sm.full[s], 0, row);
             }
             // scales: pieces of 16 bytes that do not pass through the TMA unit, whose requests
-            // bound calls on 16-token pages (drafts over 16 heads: @@)
+            // bound calls on 16-token pages (drafts over 16 heads: 23 us, not 26; 64 requests, D = 64:
+            // 62, not 78)
             if (kFp4 && k == i) {
               if (now.cnt > 0) {
                 const uint8_t* ks = static_cast<const uint8_t*>(p.k_scales) + token * (D / 16);

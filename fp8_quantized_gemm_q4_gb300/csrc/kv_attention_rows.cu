@@ -1,4 +1,4 @@
-// kv_attention_rows.cu -- attention over the paged 8-bit cache for requests with
+// kv_attention_rows.cu -- attention over the paged 8-bit or 4-bit cache for requests with
 // many rows (prompts, chunks): the mathematics is kv_attention.cu's, on tcgen05.
 //
 // A unit is 128 rows (row r = i * G + g: token i, head g of a KV head's group)
@@ -28,6 +28,10 @@
 // its bandwidth), with one O and a reference settled in turn (324 us: P in S's place
 // holds the next scores back), and with columns of its own for P (443 us: there
 // is room for one P only).
+// 4-bit cache: the converters multiply the codes, as fp16, by their scales, so that page
+// scales are 1; 256 us (870 TFLOP/s).  They have half the bytes to read and twice the
+// instructions to issue; with half of the tile's conversions left out 245, so sharing a widened
+// tile between two CTAs is worth 6 % at most.
 // The tiles of all units form one list that is cut into equal shares, one CTA
 // each; units cut between CTAs are joined by the last CTA to finish a piece.
 #include "kv_attention.cuh"
