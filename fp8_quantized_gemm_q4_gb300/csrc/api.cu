@@ -1345,6 +1345,8 @@ bs_status bs_kv_append_rotary(const bs_kv_append_rotary_args* a, bs_stream_t str
       (a->Hq > 0 && (!aligned16(a->q) || !aligned16(a->q_out))) || (a->rotary_dim > 0 && !aligned16(a->angles)) ||
       !aligned4(a->k_scales) || !aligned4(a->v_scales) || !aligned4(a->slots) || !aligned4(a->positions))
     return fail(BS_ERR_ALIGN, "kv_append_rotary: q, k, v, q_out, angles and codes must be 16-byte aligned, strides multiples of 8 elements");
+  if (a->Hq > 0 && (a->q_out == a->k || a->q_out == a->v))
+    return fail(BS_ERR_INVALID, "kv_append_rotary: q_out is k or v, which other warps still read");
   // a row in place is read before it is written, any other order of rows is not
   if (a->Hq > 0 && a->q == a->q_out &&
       (a->dtype != BS_DTYPE_BF16 || (a->T > 1 && a->q_token_stride != a->q_out_token_stride) ||
@@ -1405,6 +1407,7 @@ bs_status bs_kv_gather(const bs_kv_gather_args* a, bs_stream_t stream) {
   if (strides % 8 || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->k_codes) || !aligned16(a->v_codes) ||
       !aligned4(a->k_scales) || !aligned4(a->v_scales) || !aligned4(a->slots))
     return fail(BS_ERR_ALIGN, "kv_gather: k, v and codes must be 16-byte aligned, strides multiples of 8 elements");
+  if (a->k == a->v) return fail(BS_ERR_INVALID, "kv_gather: k and v are one buffer");
   bsk::KvGatherParams p = {};
   if (!device_info(&p.status, nullptr)) return fail(BS_ERR_CUDA, "no current device");
   p.codes[0] = a->k_codes;
@@ -1456,7 +1459,8 @@ bs_status bs_lora_add(const bs_lora_args* a, bs_stream_t stream) {
       !aligned4(a->scales) || !aligned4(a->cu_rows) || !aligned4(a->which))
     return fail(BS_ERR_ALIGN, "lora_add: x, a, b, y and out must be 16-byte aligned, row strides multiples of 8");
   if (a->out == a->y && a->T > 1 && a->ldo != a->ldy) return fail(BS_ERR_INVALID, "lora_add: out in y's place needs its stride");
-  if (a->out == a->x) return fail(BS_ERR_INVALID, "lora_add: out is x, which other CTAs still read");
+  if (a->out == a->x || a->out == a->a || a->out == a->b)
+    return fail(BS_ERR_INVALID, "lora_add: out is x, a or b, which other CTAs still read");
   int sms = 0;
   bsk::LoraParams p = {};
   if (!device_info(&p.status, &sms)) return fail(BS_ERR_CUDA, "no current device");

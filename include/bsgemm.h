@@ -718,7 +718,7 @@ bs_status bs_kv_attention_fp4(const bs_kv_attention_args *args, const uint8_t *k
  *              elements; D contiguous, strides multiples of 8, pointers 16-byte
  *              aligned.  Hq = 0: no queries
  *   q_out      bf16 [T, Hq, D], likewise; may be q itself (bf16, the same strides), no
- *              other overlap of outputs and inputs
+ *              other overlap of outputs and inputs (q_out at k's or v's address is refused)
  *   slots      int32 [T]; a row with a negative slot is skipped, its query too; one
  *              past the cache likewise, and sets BS_ERR_OFFSETS.  A slot that a call names
  *              twice holds nothing of use afterwards (its codes and scales may be
@@ -758,7 +758,8 @@ bs_status bs_kv_append_rotary(const bs_kv_append_rotary_args *args, bs_stream_t 
  * slots[r], to look at what a cache holds, or to move requests elsewhere.
  *   slots      int32 [T]; a negative slot leaves its rows of k and v as they were, one
  *              past the cache does too and sets BS_ERR_OFFSETS
- *   k, v       bf16 [T, Hkv, D], strides in elements (multiples of 8), 16-byte aligned
+ *   k, v       bf16 [T, Hkv, D], strides in elements (multiples of 8), 16-byte aligned,
+ *              apart from each other (one address for both is refused)
  * ------------------------------------------------------------------------- */
 typedef struct {
     const int32_t *slots;
@@ -818,7 +819,7 @@ bs_status bs_fp4_matvec(const bs_fp4_matvec_args *args, bs_stream_t stream);
  *   which      int32 [B]; negative: no adapter; adapters and above: none either, and
  *              sets BS_ERR_OFFSETS
  *   y, out     fp32 or bf16 (dtype) [T, ldy], [T, ldo]; out may be y (same stride), no
- *              other overlap (out at x's address is refused)
+ *              other overlap (out at the address of x, a or b is refused)
  *   r          a multiple of 8, 8 .. 128; K and N multiples of 8, K <= 2^22, B <= 8192
  *   all matrices 16-byte aligned, row strides multiples of 8 elements
  * ------------------------------------------------------------------------- */

@@ -118,6 +118,20 @@ def test_lora_refusals(bs):
     assert call(T=0) == bs.BS_OK and call(B=0) == bs.BS_OK and call(N=0) == bs.BS_OK
 
 
+def test_outputs_at_inputs_are_refused(bs):
+    """An output at the address of an input that others still read, or of the other output."""
+    lib, A = bs.load(), [F << i for i in range(12)]
+    q, q_out, k, v, x, y, a, b, out = A[:9]
+    pack = bs._KV_APPEND_ROTARY_ARGS.pack
+    for o, qq in ((k, q), (v, q), (k, k), (v, v)):
+        assert lib.bs_kv_append_rotary(pack(qq, 1024, 128, o, 1024, 128, k, v, bs.DTYPE_BF16, 8, 2, 128, 10, 256, 128, 256, 128, F, F, F,
+                                            50, 128, 0, bs.FMT_FP4, 64, F, F, F, F, 100), None) == bs.BS_ERR_INVALID
+    assert lib.bs_kv_gather(bs._KV_GATHER_ARGS.pack(F, 10, 8, 128, k, k, 1024, 128, 1024, 128, bs.FMT_FP8, 64, F, F, F, F, 100),
+                            None) == bs.BS_ERR_INVALID
+    for o in (x, a, b):
+        assert lib.bs_lora_add(bs._LORA_ARGS.pack(x, 256, a, b, 0, F, F, y, 512, o, 512, 1, 3, 10, 256, 512, 16, 4), None) == bs.BS_ERR_INVALID
+
+
 @pytest.fixture
 def stopped(bs, monkeypatch):
     """The binding, whose calls must not reach the library."""
