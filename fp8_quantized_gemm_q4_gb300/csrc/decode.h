@@ -99,7 +99,7 @@ struct KvGatherParams {
 };
 cudaError_t launch_kv_gather(const KvGatherParams& p, cudaStream_t stream);
 
-// Attention over the paged 8-bit cache (kv_attention.cu)
+// Attention over the paged cache (kv_attention.cu)
 // Most rows (new tokens x heads of a group) per KV head of a request for the
 // few-rows kernel; kv_attention_rows.cu takes the others.  A call whose rows do not
 // fill the GPU with units of 8 lets the few-rows kernel read a request's cache
@@ -107,7 +107,9 @@ cudaError_t launch_kv_gather(const KvGatherParams& p, cudaStream_t stream);
 // tokens, 32 rows per KV head 22 / 43, 64 rows 27 / 45, 128 rows 40 / 59; 8 requests, 4
 // heads, 2000 tokens, 32 rows 20 / 26, 64 rows 28 / 27, and where requests of both kinds
 // meet, one kernel instead of two, 16 / 38); a larger one does not (64 requests, 8
-// heads, 3000 tokens, 16 rows 131 / 166, 32 rows 247 / 158, 64 rows 477 / 163).
+// heads, 3000 tokens, 16 rows 131 / 166, 32 rows 247 / 158, 64 rows 477 / 163).  Over 4 bits: one
+// request 32 rows 20 / 39, 128 rows 38 / 57; 8 requests, 64 rows 28 / 24; 64 requests, 16 rows 98 / 144,
+// 32 rows 182 / 139 (D = 64: 16 rows 63 / 133, 32 rows 113 / 127).
 constexpr int few_rows(long long T, int Hq) { return T * Hq <= 2048 ? 128 : 16; }
 struct KvAttentionParams {
   const void* q;          // bf16 [T, Hq, D]

@@ -383,24 +383,25 @@ __device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_
 // 24 us, bound by what a unit costs beside its tiles (q, the join of the warps, its
 // piece); one token over 1000: 10 us, a chain of dependent reads.  Three CTAs an SM
 // leave 128 registers a thread, of which 16 to 20 bytes are spilled.
-// Of 4 bits, which halve the stream, the same calls take 76 us (340 MB, 0.66 of HBM), 23 us
-// (34 MB) and 9 to 15 us.  A cached element costs what it does with 8 bits and the product
+// Of 4 bits, which halve the stream, the same calls take 75 us (340 MB, 0.66 of HBM), 22 us
+// (34 MB) and 10 us.  A cached element costs what it does with 8 bits and the product
 // with its scale: 324 instructions a warp and 16 tokens, 156 of them for one pipe
 // (conversions, byte exchanges), in 0.57 of the issue slots.  So 32 tokens a step, whose
 // chains of products run side by side, maxima looked for only where a score passes its
-// reference by 8, and q as fragments in shared memory (107 / 83 / 77 us with each).  The
-// CTAs of an SM end their equal shares after 50 to 75 us.  Measured beside it: smaller shares
-// for CTAs that take the place of those that end first 91 to 93 (against 83 in the same
-// graph: a start costs more than the waiting), shares by place in the grid and four CTAs
-// of 96 registers no gain.
+// reference by 8, and q as fragments in shared memory (101 / 77 / 75 us with each).  The three
+// CTAs of an SM end their equal shares one after the other, after 57, 66 and 72 us.  Measured
+// beside it: smaller shares for CTAs that take the place of those that end first 84 to 86 (a start
+// costs more than the waiting), shares by place in the grid and four CTAs of 96 registers
+// no gain; units of 16 rows, whose K and V are converted once, by two CTAs an SM: 64 requests of
+// 16 rows 82, not 98, but one such request 28, not 18, and 64 of 8 rows beside one of 12 77, not 57.
 // ---------------------------------------------------------------------------
 constexpr int kItems = 32;         // units listed at a time
 constexpr int kMinTiles = 2;       // least cost worth a CTA of its own
 // What a unit costs beside its tiles (q, the join of the warps, a piece), in tiles.
 // us with 0 / 2 / 4 / 10: 64 decode requests 107.6 / 106.1 / 105.5 / 106, drafts over 16
 // heads 24.8 / 23.3 / 22.9 / 23.9, 64 requests of 30 to 14000 tokens 20.6 / 17.4 / 16.6 / 16.7.  Of 4 bits,
-// tiles twice as long, with 0 / 1 / 2 / 4: 64 decode requests 86 / 83 / 83 / 84, drafts 26.4 / 26.1 /
-// 25.4 / 26.2, 300 requests of 200 to 2000 tokens 94 / 87 / 84 / 89
+// tiles twice as long, with 0 / 1 / 2 / 4: 64 decode requests 80 / 77 / 75 / 77, drafts 23.1 / 22.7 /
+// 21.9 / 23.0, 300 requests of 200 to 2000 tokens 90 / 81 / 77 / 81
 template <bool kFp4>
 constexpr int kUnitTilesOf = kFp4 ? 2 : 4;
 constexpr int kCounters = 1024;    // arrival counters at the head of the workspace
