@@ -388,7 +388,8 @@ __device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_
 // with its scale: 324 instructions a warp and 16 tokens, 156 of them for one pipe
 // (conversions, byte exchanges), in 0.57 of the issue slots.  So 32 tokens a step, whose
 // chains of products run side by side, maxima looked for only where a score passes its
-// reference by 8, and q as fragments in shared memory (101 / 77 / 75 us with each).  The three
+// reference by 8, and q as fragments in shared memory (with each 107, 83 and
+// 77 us in one setting).  The three
 // CTAs of an SM end their equal shares one after the other, after 57, 66 and 72 us.  Measured
 // beside it: smaller shares for CTAs that take the place of those that end first 84 to 86 (a start
 // costs more than the waiting), shares by place in the grid and four CTAs of 96 registers

@@ -30,8 +30,8 @@
 // is room for one P only).
 // 4-bit cache: the converters multiply the codes, as fp16, by their scales, so that page
 // scales are 1; 256 us (870 TFLOP/s).  They have half the bytes to read and twice the
-// instructions to issue; with half of the tile's conversions left out 245, so sharing a widened
-// tile between two CTAs is worth 6 % at most.
+// instructions to issue; with half of the tile's conversions left out 6 % less, so sharing a
+// widened tile between two CTAs is worth no more than that.
 // The tiles of all units form one list that is cut into equal shares, one CTA
 // each; units cut between CTAs are joined by the last CTA to finish a piece.
 #include "kv_attention.cuh"
