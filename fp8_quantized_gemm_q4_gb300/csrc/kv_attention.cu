@@ -97,16 +97,13 @@ __device__ __noinline__ uint32_t take_nan(uint8_t* vt, int cnt, int seen0, int s
 }
 
 // The same of a 4-bit cache, where a NaN scale stands for a NaN in its 16 columns:
-// `scales` are those of V, the accumulators at bit 2 x + e: o[4 (x / 2) + j][2 (x % 2) + e]
-// for every j.
+// `scales` are those of V.  Bit e is returned if row e's columns of this lane, which are of
+// one group, have met one.
 template <int D>
 __device__ __noinline__ uint32_t take_nan_scales(uint8_t* scales, int cnt, int seen0, int seen1, int lane) {
   uint32_t hit = 0;
   for (int tok = 0; tok < cnt; ++tok)
-#pragma unroll
-    for (int x = 0; x < D / 32; ++x)
-      if ((scales[tok * (D / 16) + 2 * x + (lane >> 4)] & 0x7f) == 0x7f)
-        hit |= (tok < seen0 ? 1u : 0u) << (2 * x) | (tok < seen1 ? 2u : 0u) << (2 * x);
+    if ((scales[tok * (D / 16) + (lane >> 2) * D / 128] & 0x7f) == 0x7f) hit |= (tok < seen0 ? 1u : 0u) | (tok < seen1 ? 2u : 0u);
   __syncwarp();
   for (int x = lane; x < cnt * (D / 16); x += 32)
     if ((scales[x] & 0x7f) == 0x7f) scales[x] = 0;
@@ -147,30 +144,47 @@ __device__ __forceinline__ void softmax_step(float (&u)[4], float inv_sv, float 
   }
 }
 
+// Which of 16 tokens of a 4-bit tile stands at place n of the MMA's token axis: an order in
+// which neither the loads of K (a token a lane, 8 lanes' at once) nor those of V (four tokens a
+// lane) meet a bank twice.
+template <int D>
+__device__ __forceinline__ constexpr int fp4_token(int n) {
+  return D == 128 ? 4 * ((n & 7) >> 1) + (n & 1) + 2 * (n >> 3) : n ^ ((n >> 2) & 1);
+}
+
 // Places in shared memory of what a lane reads of the 32 tokens of a 4-bit tile that its
-// warp takes, from the stage's codes and the scales of those tokens on; [h]: 16 of them.
+// warp takes, from the stage's codes and the scales of those tokens on; h: 16 of them.
 template <int D>
 struct Fp4At {
   // of the second 16 tokens of D = 128: 1024 bytes on, with the same exchange of pieces
   static constexpr int kHalves = D == 128 ? 1 : 2;
-  uint32_t k_[kHalves][2], v_[kHalves][D / 64], ks, vs;
+  uint32_t k_[kHalves][2], v_[kHalves][4], ks, vs_[2];
   __device__ __forceinline__ Fp4At(int warp, int lane) {
     const int g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
       const int tok = warp * 32 + 16 * h;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)  // D / 4 columns of tokens g and g + 8
-        k_[h][i] = D == 128 ? code_at<64>(tok + 8 * i + g, c) : code_at<32>(tok + 8 * i + g, c >> 1) + 8 * (c & 1);
+      for (int i = 0; i < 2; ++i) {  // D / 4 columns of the tokens at places g and g + 8
+        const int t = tok + fp4_token<D>(8 * i + g);
+        k_[h][i] = D == 128 ? code_at<64>(t, c) : code_at<32>(t, c >> 1) + 8 * (c & 1);
+      }
 #pragma unroll
-      for (int a = 0; a < D / 64; ++a)  // rows for ldmatrix: tokens 0 .. 15 at 16-byte chunk 2 a, then 2 a + 1
-        v_[h][a] = kTileOf<true> * (D / 2) + code_at<D / 2>(tok + (lane & 15), 2 * a + (lane >> 4));
+      for (int i = 0; i < 4; ++i) {  // D / 8 columns of those at places 2 c, 2 c + 1, 2 c + 8, 2 c + 9
+        const int t = tok + fp4_token<D>(2 * c + (i & 1) + 8 * (i >> 1));
+        v_[h][i] = kTileOf<true> * (D / 2) + (D == 128 ? code_at<64>(t, g >> 1) + 8 * (g & 1) : code_at<32>(t, g >> 2) + 4 * (g & 3));
+      }
     }
-    ks = g * (D / 16) + (D == 128 ? 2 : 1) * c;
-    vs = kTileOf<true> * (D / 16) + 2 * c * (D / 16);
+    ks = fp4_token<D>(g) * (D / 16) + (D == 128 ? 2 : 1) * c;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) vs_[i] = (kTileOf<true> + fp4_token<D>(2 * c + i)) * (D / 16) + g * D / 128;
   }
   __device__ __forceinline__ uint32_t k(int h, int i) const { return D == 128 ? k_[0][i] + 1024 * h : k_[h % kHalves][i]; }
-  __device__ __forceinline__ uint32_t v(int h, int a) const { return D == 128 ? v_[0][a] + 1024 * h : v_[h % kHalves][a]; }
+  __device__ __forceinline__ uint32_t v(int h, int i) const { return D == 128 ? v_[0][i] + 1024 * h : v_[h % kHalves][i]; }
+  // scales of the same tokens; places eight apart are two tokens apart, or eight
+  static constexpr int kEight = fp4_token<D>(8) * (D / 16);
+  __device__ __forceinline__ uint32_t k_scale(int h, int i) const { return ks + 16 * h * (D / 16) + kEight * i; }
+  __device__ __forceinline__ uint32_t v_scale(int h, int i) const { return vs_[i & 1] + 16 * h * (D / 16) + kEight * (i >> 1); }
 };
 // mma_f16 that the compiler may move among the loads and conversions
 __device__ __forceinline__ void mma_f16_free(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -206,20 +220,6 @@ __device__ __forceinline__ uint16_t lds16(uint32_t a) {
   return v;
 }
 
-// Byte kByte of w, two E2M1 codes, as f16x2
-template <int kByte>
-__device__ __forceinline__ uint32_t e2m1x2_to_f16(uint32_t w) {
-  uint32_t r;
-  if constexpr (kByte == 0)
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t}\n" : "=r"(r) : "r"(w));
-  else if constexpr (kByte == 1)
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b1;\n\t}\n" : "=r"(r) : "r"(w));
-  else if constexpr (kByte == 2)
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b2;\n\t}\n" : "=r"(r) : "r"(w));
-  else
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b3;\n\t}\n" : "=r"(r) : "r"(w));
-  return r;
-}
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
@@ -255,17 +255,17 @@ __device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_
       for (int a = 0; a < D / 16; ++a)
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-          if (hit >> (4 * (a >> 2) + x) & 1) o[a][x] = __int_as_float(0x7fffffff);
+          if (hit >> (x & 1) & 1) o[a][x] = __int_as_float(0x7fffffff);
     }
     __syncwarp();
   }
   float s[2][4] = {};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t w[2][D / 32], f[2];  // [i]: columns of token 16 h + 8 i + g, their one or two scales
+    uint32_t w[2][D / 32], f[2];  // [i]: columns of the token at place 8 i + g, their one or two scales
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t at_scale = scales + at.ks + (16 * h + 8 * i) * (D / 16);
+      const uint32_t at_scale = scales + at.k_scale(h, i);
       if constexpr (D == 128) {
         const uint4 a = lds128(codes + at.k(h, i));
         w[i][0] = a.x, w[i][1] = a.y, w[i][2] = a.z, w[i][3] = a.w;
@@ -294,7 +294,7 @@ __device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int tok = 8 * (e >> 1) + (lane >> 2);
+        const int tok = fp4_token<D>(lane >> 2) + fp4_token<D>(8) * (e >> 1);
         if (tok >= cnt[h] || tok0 + 16 * h + tok >= seen[e & 1]) s[h][e] = -INFINITY;
       }
   }
@@ -331,39 +331,41 @@ __device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_
       l[0] += a, l[1] += b;
       pb[h][t] = movmatrix_trans(pack_f16x2(a, b));
     }
-  const uint32_t pick = (lane >> 4) ? 0x7351 : 0x6240;
+  // A lane has D / 8 columns, of one group, of four tokens: a byte of two columns of a token
+  // and that of its neighbour exchange a column, and each byte's conversion gives a column of two tokens.
+  // Tile 4 w + b has the columns D / 8 g + 8 w + 2 b (g on its first rows) and + 1.
+  constexpr uint32_t kLow = 0x0f0f0f0fu;
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < 2; ++h) {
+    uint32_t sv[2], v[4][D / 64];
 #pragma unroll
-    for (int a = 0; a < D / 64; ++a) {
-      // scales of the pairs of tokens 2 c, 2 c + 1 (and 8 more) for the group 4 a + g / 4 and the one two behind
-      uint32_t sv[2][2];
+    for (int t = 0; t < 2; ++t)
+      sv[t] = e4m3x2_to_f16x2((uint16_t)__byte_perm(lds8(scales + at.v_scale(h, 2 * t)), lds8(scales + at.v_scale(h, 2 * t + 1)), 0x0040));
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const uint32_t from = scales + at.vs + (16 * h + 8 * t) * (D / 16) + 4 * a;
-        const uint32_t b = __byte_perm(lds32(from), lds32(from + D / 16), pick);
-        sv[0][t] = e4m3x2_to_f16x2((uint16_t)b);
-        sv[1][t] = e4m3x2_to_f16x2((uint16_t)(b >> 16));
-      }
-      // matrix i: tokens 8 (i % 2) .. + 7 at the 32 columns of chunk 2 a + i / 2; a register has four
-      // columns (4 g .. + 3) of two tokens, which become pairs of tokens after their conversion
-      uint32_t v[4];
-      ldmatrix_x4_trans(v, codes + at.v(h, a));
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {  // columns 2 x and 2 x + 1 of the four
-        uint32_t lo[4], hi[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t e = x ? e2m1x2_to_f16<1>(v[i]) : e2m1x2_to_f16<0>(v[i]);
-          const uint32_t f = x ? e2m1x2_to_f16<3>(v[i]) : e2m1x2_to_f16<2>(v[i]);
-          lo[i] = hmul2(__byte_perm(e, f, 0x5410), sv[i >> 1][i & 1]);
-          hi[i] = hmul2(__byte_perm(e, f, 0x7632), sv[i >> 1][i & 1]);
-        }
-        const uint32_t va[4] = {lo[0], lo[2], lo[1], lo[3]}, vb[4] = {hi[0], hi[2], hi[1], hi[3]};
-        mma_f16_free(o[4 * a + 2 * x], va, pb[h][0], pb[h][1]);
-        mma_f16_free(o[4 * a + 2 * x + 1], vb, pb[h][0], pb[h][1]);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (D == 128) {
+        const uint2 a = lds64(codes + at.v(h, i));
+        v[i][0] = a.x, v[i][1] = a.y;
+      } else {
+        v[i][0] = lds32(codes + at.v(h, i));
       }
     }
+#pragma unroll
+    for (int w = 0; w < D / 64; ++w) {
+      uint32_t even[2][4], odd[2][4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t x = v[2 * t][w], y = v[2 * t + 1][w];
+        e2m1x8_to_f16((x & kLow) | ((y << 4) & ~kLow), even[t]);
+        e2m1x8_to_f16(((x >> 4) & kLow) | (y & ~kLow), odd[t]);
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const uint32_t va[4] = {hmul2(even[0][b], sv[0]), hmul2(odd[0][b], sv[0]), hmul2(even[1][b], sv[1]), hmul2(odd[1][b], sv[1])};
+        mma_f16_free(o[4 * w + b], va, pb[h][0], pb[h][1]);
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -459,10 +461,10 @@ __device__ __forceinline__ long long piece_at(int cta, int first_cta) {
 }
 // Place of column d of a row in a reduction buffer: 16-column windows and their
 // halves exchanged by row, so that the fragments' stores meet no bank twice.
-// For 4 bits, whose fragments store four columns at a time, 4-column windows by row.
+// For 4 bits, whose fragments store four of D / 8 columns at a time, pieces of 4 by row.
 template <int D, bool kFp4>
 __device__ __forceinline__ int red_at(int r, int d) {
-  if constexpr (kFp4) return r * D + (d ^ (((r >> 1) & 3) << 3));
+  if constexpr (kFp4) return r * D + (d ^ (D == 128 ? ((r >> 1) & 3) << 2 : ((r >> 1) & 1) << 2 | ((r >> 2) & 1) << 4));
   return r * D + ((((d >> 4) ^ ((r >> 1) & 1)) << 4) | ((d & 15) ^ (((r >> 2) & 1) << 3)));
 }
 
@@ -842,7 +844,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
           for (int e = 0; e < 2; ++e) m[e] = m[e] == kNone ? -INFINITY : m[e];
         }
         // ---- the warps' (m, l, o) to one: o[a] holds columns 16 a + 2 g and + 1
-        // (e / 2) of rows 2 c and + 1 (e % 2); of 4 bits, columns 64 (a / 4) + 4 g + a % 4 and + 32
+        // (e / 2) of rows 2 c and + 1 (e % 2); of 4 bits, columns D / 8 g + 2 a and + 1
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -867,9 +869,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
             for (int x = 0; x < D / 32; ++x)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                float* at = buf + red_at<D, true>(2 * c + e, 32 * x + 4 * g);
-                const int a = 4 * (x >> 1), i = 2 * (x & 1) + e;
-                f(reinterpret_cast<float4*>(at), o[a][i], o[a + 1][i], o[a + 2][i], o[a + 3][i]);
+                float* at = buf + red_at<D, true>(2 * c + e, D / 8 * g + 4 * x);
+                f(reinterpret_cast<float4*>(at), o[2 * x][e], o[2 * x][2 + e], o[2 * x + 1][e], o[2 * x + 1][2 + e]);
               }
           } else {
             float none = 0.0f;
@@ -923,15 +924,12 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
           consumer_sync();  // ml and red have been read
           continue;
         }
-        __threadfence();
         // the shares that hold the unit's first and last tile
         const long long first = t_first + begin + (base + im + 1) * kUnitTiles;  // on the axis of costs
         const int c0 = (int)quotient((first + 1) * shares - 1, cost), c1 = (int)quotient((first + nt) * shares - 1, cost);
         consumer_sync();
         if (tid == 0) {
-          const int old = atomicAdd(p.counters + c0, 1);
-          __threadfence();
-          sm.last = old == c1 - c0;
+          sm.last = arrive_piece(p.counters + c0) == c1 - c0;
           if (sm.last) p.counters[c0] = 0;
         }
         consumer_sync();

@@ -1,4 +1,4 @@
-// kv_attention.cuh -- what the two attention kernels over the 8-bit cache share.
+// kv_attention.cuh -- what the two attention kernels over the paged cache share.
 #pragma once
 #include "decode.cuh"
 #include "decode.h"
@@ -60,5 +60,15 @@ __device__ __forceinline__ int cached(const KvAttentionParams& p, int b) {
 }
 __device__ __forceinline__ bool length_bad(const KvAttentionParams& p, int b) {
   return (unsigned)p.kv_lens[b] > (unsigned)(p.max_pages << p.page_shift);
+}
+
+// Arrival of a piece: how many came before it.  Called by one thread between two
+// barriers of those that wrote it and will read the others': the barrier before makes
+// their stores part of what this releases, the one after makes what this acquires theirs
+// (a fence by every thread instead took 1 us more of 10 and of 75 us calls).
+__device__ __forceinline__ int arrive_piece(int* counter) {
+  int old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+  return old;
 }
 }  // namespace bsk

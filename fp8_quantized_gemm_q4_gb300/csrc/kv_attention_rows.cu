@@ -505,14 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         if (in && part == 0 && p.lse) p.lse[lse_at] = lse_of(m, l);
       } else {
         if (in && part == 0) *reinterpret_cast<float2*>(slot + kM * D + 2 * r128) = make_float2(m, l);
-        __threadfence();
         const long long all = sm.total;
         const int c0 = (int)(((at + 1) * sm.shares - 1) / all), c1 = (int)(((at + nt) * sm.shares - 1) / all);
         softmax_sync();
         if (tid == 0) {
-          const int old = atomicAdd(p.counters + c0, 1);
-          __threadfence();
-          sm.last = old == c1 - c0;
+          sm.last = arrive_piece(p.counters + c0) == c1 - c0;
           if (sm.last) p.counters[c0] = 0;
         }
         softmax_sync();
