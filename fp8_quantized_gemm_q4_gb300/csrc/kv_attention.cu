@@ -385,16 +385,18 @@ __device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_
 // 24 us, bound by what a unit costs beside its tiles (q, the join of the warps, its
 // piece); one token over 1000: 10 us, a chain of dependent reads.  Three CTAs an SM
 // leave 128 registers a thread, of which 16 to 20 bytes are spilled.
-// Of 4 bits, which halve the stream, the same calls take 75 us (340 MB, 0.66 of HBM), 22 us
-// (34 MB) and 10 us.  A cached element costs what it does with 8 bits and the product
-// with its scale: 324 instructions a warp and 16 tokens, 156 of them for one pipe
-// (conversions, byte exchanges), in 0.57 of the issue slots.  So 32 tokens a step, whose
+// Of 4 bits, which halve the stream, the same calls take 73 us (340 MB, 0.68 of HBM; with 16000
+// tokens each 218, 0.80), 22 us (34 MB) and 10 us: about 14 us that no stream fills (shares,
+// lists and the first tiles, the joins) and then 0.86 of HBM.  A cached element costs what it does
+// with 8 bits and the product with its scale: 335 instructions a warp and 16 tokens, 0.55 of the
+// issue slots and 0.54 of the pipe that converts and exchanges bytes.  So 32 tokens a step, whose
 // chains of products run side by side, maxima looked for only where a score passes its
-// reference by 8, and q as fragments in shared memory (with each 107, 83 and
-// 77 us in one setting).  The three
-// CTAs of an SM end their equal shares one after the other, after 57, 66 and 72 us.  Measured
-// beside it: smaller shares for CTAs that take the place of those that end first 84 to 86 (a start
-// costs more than the waiting), shares by place in the grid and four CTAs of 96 registers
+// reference by 8, q as fragments in shared memory (with each 107, 83 and 77 us in one
+// setting), and V as four tokens a lane, whose columns share a scale (75.5, then 74.5; two tokens
+// by ldmatrix before).  The three CTAs of an SM end their equal shares one after the other, after
+// 57, 66 and 72 us, and what goes on has the stream for itself.  Measured beside it: smaller
+// shares for CTAs that take the place of those that end first 84 to 86 (a start costs more
+// than the waiting), shares by place in the grid and four CTAs of 96 registers
 // no gain; units of 16 rows, whose K and V are converted once, by two CTAs an SM: 64 requests of
 // 16 rows 82, not 98, but one such request 28, not 18, and 64 of 8 rows beside one of 12 77, not 57.
 // ---------------------------------------------------------------------------
