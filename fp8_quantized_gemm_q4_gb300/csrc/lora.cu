@@ -300,8 +300,11 @@ __global__ void __launch_bounds__(kThreads, kRank > 64 ? 1 : kRank > 32 ? 2 : 4)
 // chunk.  Of t each CTA adds its share and hands it to all.
 // 8190 rows of rank 64, K = 7168, N = 4096: 72 us (240 MB, 0.49 of HBM; 151 with the few rows' operands
 // straight from L2, 133 with y not through the ring and one CTA adding all of t); 20000 rows of rank
-// 32: 99 us, 0.73.  A CTA's 27 us there: 1 to find its tile, 11 x A^T, 5 waiting for the cluster and
-// exchanging, 9 t B^T; each part waits for its first slices, which three CTAs an SM cover in part.
+// 32: 99 us, 0.73.  A CTA's 27 us there with clusters of eight: 1 to find its tile, 11 x A^T, 5 waiting
+// for the cluster and exchanging, 9 t B^T; each part waits for its first slices, which three CTAs an SM
+// cover in part, and then for shared memory (its data pipe 0.63 of the active cycles, the tensor pipe
+// 0.35).  Tiles of 128 rows, which halve the reads of A and B and leave room for two CTAs: 71 us there, 106
+// for 124 at 16384 rows, but 32 for 27 at 2048 rows and 64 for 40 over 64 requests; not kept.
 // ---------------------------------------------------------------------------
 constexpr int kManyRows = 64, kSlice = 64;  // rows of a tile; K, or columns, of a stage
 
