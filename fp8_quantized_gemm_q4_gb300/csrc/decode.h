@@ -111,6 +111,18 @@ cudaError_t launch_kv_gather(const KvGatherParams& p, cudaStream_t stream);
 // request 32 rows 20 / 39, 128 rows 38 / 57; 8 requests, 64 rows 28 / 24; 64 requests, 16 rows 98 / 144,
 // 32 rows 182 / 139 (D = 64: 16 rows 63 / 133, 32 rows 113 / 127).
 constexpr int few_rows(long long T, int Hq) { return T * Hq <= 2048 ? 128 : 16; }
+// Over 4 bits the few-rows kernel takes whole calls whose rows (of all heads) times the
+// tokens that a request can have are few: at most 2^23 over one or two KV heads, which leave the
+// many-rows kernel short of units, 15 2^18 over more; else as above (us, few / many rows, one
+// request: 512 tokens x 8 heads over 512 cached 20 / 33, over 1024 26 / 36, over 2048 40 / 40; 128 x 32
+// heads, 8 of KV, over 512 20 / 19, over 2048 40 / 26; three requests, 75 x 3 heads, 1 of KV, over 2700
+// 18 / 44, 50 x 24 heads, 8 of KV, over 1000 18 / 25; 8 requests of 16 x 32 heads over 1000 26 / 23).
+// No request of a call that keeps the contract has more than T tokens.
+constexpr int few_rows_fp4(long long T, int Hq, int Hkv, long long most_tokens) {
+  const bool all = T * Hq <= 1 << 23 && T * Hq * most_tokens <= (Hkv <= 2 ? 1ll << 23 : 15ll << 18);
+  const int rows = few_rows(T, Hq), most = all ? (int)T * (Hq / Hkv) : 0;
+  return most > rows ? most : rows;
+}
 struct KvAttentionParams {
   const void* q;          // bf16 [T, Hq, D]
   long long q_tok_stride, q_head_stride;
@@ -131,7 +143,7 @@ struct KvAttentionParams {
   int fp4;                // the cache holds 4 bits
   float scale_log2;       // softmax scale * log2(e)
   int most_rows;          // bound of the rows per KV head of a request (at most 2^30)
-  int few_rows;           // few_rows(T, Hq)
+  int few_rows;           // few_rows(T, Hq), or few_rows_fp4
   float* work;            // pieces of (request, head) pairs cut between CTAs
   int* counters;          // arrivals of those pieces (zero between calls)
   int* status;

@@ -8,6 +8,7 @@ carry an fp32 sum over D, the output is rounded to bf16 (2^-8):
 with A = sum p |v| / sum p, S = max_t sum_d |q k| * scale, m tokens seen."""
 import math
 import random
+import sys
 
 import pytest
 import torch
@@ -23,6 +24,15 @@ def i32(v):
     return torch.tensor(v, dtype=torch.int32, device=DEV)
 
 
+ROOM = 0   # tokens that a block table has room for beyond those that are cached
+
+
+@pytest.fixture(params=[0, 1 << 18], ids=["", "roomy"])
+def room(request, monkeypatch):
+    """Small calls whose tables leave room for long requests are shared out among both kernels, others are one's."""
+    monkeypatch.setattr(sys.modules[__name__], "ROOM", request.param)
+
+
 def build(bs, seed, kv_lens, q_lens, Hq, Hkv, D, page, spread=1.0, extra_T=0, low=0x20, high=0x30):
     """Random codes; scale codes low .. high - 1 (by default 2^-3 .. 1)."""
     rng = random.Random(seed)
@@ -30,7 +40,7 @@ def build(bs, seed, kv_lens, q_lens, Hq, Hkv, D, page, spread=1.0, extra_T=0, lo
     pages = [-(-m // page) for m in kv_lens]
     ids = list(range(sum(pages) + 2))
     rng.shuffle(ids)
-    width = max(pages + [1]) + 1
+    width = max(pages + [1]) + 1 + ROOM // page
     table, at = [], 0
     for n in pages:
         table.append(ids[at:at + n] + [-1] * (width - n))
@@ -88,6 +98,7 @@ RAGGED = [([3, 0, 5, 1], [3, 70, 700, 0]), ([1, 17, 2, 64], [500, 17, 1, 64]), (
           ([200], [100]), ([9, 9], [4, 5]), ([130, 65, 33, 1, 4], [2000, 66, 1000, 90, 3000])]
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("Hq,Hkv,D,page", [(32, 8, 128, 64), (8, 8, 64, 16), (12, 4, 128, 16), (16, 2, 64, 128)])
 @pytest.mark.parametrize("q_lens,kv_lens", RAGGED)
 def test_ragged(cuda_lib, Hq, Hkv, D, page, q_lens, kv_lens):
@@ -120,6 +131,7 @@ def test_many_requests(cuda_lib):
     check(cuda_lib, q, cache, table, cu, kv, 16)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [300, 70]), ([100, 2], [300, 70])])
 def test_sharp_and_flat_scores(cuda_lib, q_lens, kv_lens):
     for spread, scale in ((30.0, 0.5), (1e-3, 1e-3), (1.0, 4.0)):
@@ -127,6 +139,7 @@ def test_sharp_and_flat_scores(cuda_lib, q_lens, kv_lens):
         check(cuda_lib, q, cache, table, cu, kv_lens, 16, scale=scale)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [301, 77]), ([90, 3], [301, 77])])
 def test_every_scale(cuda_lib, q_lens, kv_lens):
     """Scales from 0 and the smallest (2^-9) to 448 beside each other."""
@@ -136,6 +149,7 @@ def test_every_scale(cuda_lib, q_lens, kv_lens):
     check(cuda_lib, q, cache, table, cu, kv_lens, 16)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("Hq,Hkv,D,page", [(8, 2, 128, 64), (16, 2, 64, 16), (24, 8, 128, 32), (4, 4, 64, 128)])
 @pytest.mark.parametrize("q_lens,kv_lens", [([3, 5], [70, 300]), ([150, 90], [200, 1300]), ([40], [6000]),
                                             ([200, 2, 130], [150, 70, 900]), ([60, 300], [20, 40])])
@@ -193,6 +207,7 @@ def test_nan_scales(cuda_lib, Hq, Hkv, D, page, q_lens, kv_lens):
         scales.copy_(kept)
 
 
+@pytest.mark.usefixtures("room")
 def test_nan_query(cuda_lib):
     """A row that sees no token gets 0 and -infinity whatever its query holds; NaN rows stay among themselves."""
     for q_lens, kv_lens in (([4, 6], [0, 3]), ([100, 60], [0, 30])):
@@ -205,6 +220,7 @@ def test_nan_query(cuda_lib):
         assert bool(out[none:].isnan().all()) and bool(lse[none:].isnan().all())
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("Hq,Hkv,D,page", [(16, 2, 128, 64), (24, 8, 64, 16)])
 def test_contract_breaks(cuda_lib, Hq, Hkv, D, page):
     """Bad page ids, lengths and offsets set the status; rows outside the call are not touched; the next call is served."""
@@ -244,6 +260,7 @@ def test_contract_breaks(cuda_lib, Hq, Hkv, D, page):
         assert bs.device_status()[0] == bs.BS_OK
 
 
+@pytest.mark.usefixtures("room")
 def test_strides_streams_and_workspaces(cuda_lib):
     """q and out as slices, [H, T, D] in memory, on a stream of their own, with a workspace of their own; both
     caches and both kernels in turn on one workspace."""
