@@ -449,11 +449,6 @@ __device__ __forceinline__ int few_tiles(const KvAttentionParams& p, int n, int 
   return n <= 0 || (long long)n * G > p.few_rows ? 0 : max(1, (len + kTile - 1) / kTile);
 }
 
-// a / b for a >= 0 and b > 0: 64-bit division only where it takes one
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
-}
-
 // A piece of a unit that is cut between CTAs: partial sums [8][D], then (m, l) of
 // the 8 rows.  A CTA has at most two: of the unit that begins before its share
 // (0) and of one that begins in it (1).

@@ -36,6 +36,11 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7
 // w with the codes marked by n at 0
 __device__ __forceinline__ uint32_t without(uint32_t w, uint32_t n) { return w & ~((n >> 7) * 0xffu); }
 
+// a / b for a >= 0 and b > 0: 64-bit division only where it takes one
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
 // natural log of the softmax sum 2^m l
 __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;  // NaN sums stay NaN

@@ -79,8 +79,10 @@ struct RowsSmem {
   // sees them: the number + 1, request, KV head, the first token of such tiles
   int4 nan_unit[8];
   long long scan[kThreads / 32];
-  long long start_at;
+  long long start_at;  // the share's first unit: its first tile's place in the list, request, KV head, row tile
   int start[3];
+  int4 found;          // of its request: rows, cached tokens, row tiles
+  long long found_at;  // and the place of the first tile of its KV head
   // tiles in the list and CTAs that share them, for the joins: in registers through
   // the tiles they cost the softmax its room there (287 us, not 265, for the prompts above)
   long long total;
@@ -123,8 +125,21 @@ __device__ __forceinline__ bool takes(const KvAttentionParams& p, const Rows& r,
 __device__ __forceinline__ int row_tiles(const Rows& r, int G) { return (int)(((long long)r.in * G + kM - 1) / kM); }
 // Tiles that the unit's last row sees (one at least)
 __device__ __forceinline__ int unit_tiles(int n, int len, int G, int rt) {
-  const int last = (int)min((long long)n - 1, ((long long)rt * kM + kM - 1) / G);
+  const int last = (int)min((long long)n - 1, quotient((long long)rt * kM + kM - 1, G));
   return max(1, (len - n + last + 1 + kN - 1) / kN);
+}
+// Those of a request's first m row tiles, of less than all.  Row tile rt, whose last row is of token
+// (128 rt + 127) / G, has floor((rt + c) / G) of them, or 1, with c = floor((G (len - n + 128) + 127) / 128).
+// (Summed tile by tile, with a division each, a request of 77 row tiles took 23 us.)
+__device__ __forceinline__ long long tiles_before(int n, int len, int G, int m) {
+  static_assert(kM == kN, "a row tile more is 1 / G of a tile more");
+  const long long c = ((long long)G * ((long long)len - n + kN) + kM - 1) >> 7, end = c + m;
+  const long long ones = max(0ll, min(end, (long long)G) - c), from = max(c, (long long)G);
+  auto below = [&](long long x) {  // the sum of floor(i / G), i < x
+    const unsigned long long q = quotient(x, G);
+    return q * (q - 1) / 2 * G + q * (x - q * G);
+  };
+  return ones + (end > from ? (long long)(below(end) - below(from)) : 0);
 }
 __device__ __forceinline__ void load_request(const KvAttentionParams& p, int G, Unit& u) {
   const Rows r = rows_of(p, u.b);
@@ -233,24 +248,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
   griddep_wait();
   griddep_launch_dependents();
 
-  // Each thread sums the tiles of `per` requests in a row; the one whose
-  // requests hold the share's first tile finds its unit.
+  // Each thread sums the tiles of `per` requests in a row; the one whose requests hold the
+  // share's first tile finds its request and head, all of them together its row tile.
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  auto request_tiles = [&](int b) {  // of one KV head
-    const Rows r = rows_of(p, b);
+  auto request_tiles = [&](const Rows& r, int len) {  // of one KV head
     if (!takes(p, r, G)) return 0ll;
-    const int len = cached(p, b), rts = row_tiles(r, G);
-    long long x = 0;
-    for (int rt = 0; rt < rts; ++rt) x += unit_tiles(r.n, len, G, rt);
-    return x;
+    const int rts = row_tiles(r, G);
+    return tiles_before(r.n, len, G, rts - 1) + unit_tiles(r.n, len, G, rts - 1);
   };
+  Rows own = {};  // of the last of them: all there is while B <= threads
+  int own_len = 0;
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
-    mine += request_tiles(b);
-    const Rows r = rows_of(p, b);
-    if ((long long)r.n * G > p.most_rows) record_status(p.status, kStatusOffsets, 53);
-    if (r.bad || length_bad(p, b)) record_status(p.status, kStatusOffsets, 54);
+    own = rows_of(p, b);
+    own_len = cached(p, b);
+    mine += request_tiles(own, own_len);
+    if ((long long)own.n * G > p.most_rows) record_status(p.status, kStatusOffsets, 53);
+    if (own.bad || length_bad(p, b)) record_status(p.status, kStatusOffsets, 54);
   }
   long long incl = mine;
 #pragma unroll
@@ -272,29 +287,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
   const int shares = (int)min((long long)gridDim.x, (total + kMinTiles - 1) / kMinTiles);
   if (tid == 0) sm.total = total, sm.shares = shares;
   const bool works = (int)blockIdx.x < shares;
-  const long long t_first = works ? total * blockIdx.x / shares : 0;
-  const long long t_last = works ? total * (blockIdx.x + 1) / shares : 0;
+  const long long t_first = works ? quotient(total * blockIdx.x, shares) : 0;
+  const long long t_last = works ? quotient(total * (blockIdx.x + 1), shares) : 0;
   if (works && t_first >= before && t_first < before + mine * p.Hkv) {
-    long long at = before;
+    long long at = before, x = mine;
     for (int b = b0; b < b1; ++b) {
-      const long long x = request_tiles(b);
+      if (per > 1) {
+        own = rows_of(p, b);
+        own_len = cached(p, b);
+        x = request_tiles(own, own_len);
+      }
       if (x && t_first < at + x * p.Hkv) {
-        const int h = (int)((t_first - at) / x);
-        at += h * x;
-        const int n = rows_of(p, b).n, len = cached(p, b);
-        int rt = 0;
-        for (;; ++rt) {
-          const int nt = unit_tiles(n, len, G, rt);
-          if (t_first < at + nt) break;
-          at += nt;
-        }
+        const int h = (int)quotient(t_first - at, x);
         sm.start[0] = b;
         sm.start[1] = h;
-        sm.start[2] = rt;
-        sm.start_at = at;
+        sm.found = make_int4(own.n, own_len, row_tiles(own, G), 0);
+        sm.found_at = at + h * x;
         break;
       }
       at += x * p.Hkv;
+    }
+  }
+  __syncthreads();
+  if (works) {
+    const int4 r = sm.found;  // rows, cached tokens, row tiles
+    const long long off = t_first - sm.found_at;
+    for (int rt = tid; rt < r.z; rt += kThreads) {
+      const long long x = off - tiles_before(r.x, r.y, G, rt);
+      if (x >= 0 && x < unit_tiles(r.x, r.y, G, rt)) {
+        sm.start[2] = rt;
+        sm.start_at = t_first - x;
+      }
     }
   }
   __syncthreads();
@@ -328,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
     auto load_q = [&](const UnitInfo& u) {
       Row w;
       const long long r = (long long)u.rt * kM + r128;
-      w.i = (int)(r / G), w.hq = u.h * G + (int)(r % G);
+      w.i = (int)quotient(r, G), w.hq = u.h * G + (int)(r - (long long)w.i * G);
       w.in = r < (long long)u.n * G && u.row0 + w.i < p.T;
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (u.row0 + (long long)w.i) * p.q_tok_stride +
                                w.hq * p.q_head_stride + part * (D / 4);
@@ -506,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       } else {
         if (in && part == 0) *reinterpret_cast<float2*>(slot + kM * D + 2 * r128) = make_float2(m, l);
         const long long all = sm.total;
-        const int c0 = (int)(((at + 1) * sm.shares - 1) / all), c1 = (int)(((at + nt) * sm.shares - 1) / all);
+        const int c0 = (int)quotient((at + 1) * sm.shares - 1, all), c1 = (int)quotient((at + nt) * sm.shares - 1, all);
         softmax_sync();
         if (tid == 0) {
           sm.last = arrive_piece(p.counters + c0) == c1 - c0;
@@ -588,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       // from this token on, some row of the unit does not see V: a NaN code there
       // would reach that row with a weight of 0.  Tiles with such tokens go without
       // theirs, and the rows that see one get the NaN at the end.
-      const int hidden = max(0, len - u->n + (int)((long long)u->rt * kM / G) + 1);
+      const int hidden = max(0, len - u->n + (int)quotient((long long)u->rt * kM, G) + 1);
       const int4 bad = make_int4((int)k + 1, u->b, u->h, hidden / kN * kN);
       unit_close();
       uint4 raw[kSteps];
