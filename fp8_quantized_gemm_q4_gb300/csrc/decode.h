@@ -114,9 +114,9 @@ constexpr int few_rows(long long T, int Hq) { return T * Hq <= 2048 ? 128 : 16; 
 // Over 4 bits the few-rows kernel takes whole calls whose rows (of all heads) times the
 // tokens that a request can have are few: at most 2^23 over one or two KV heads, which leave the
 // many-rows kernel short of units, 15 2^18 over more; else as above (us, few / many rows, one
-// request: 512 tokens x 8 heads over 512 cached 20 / 33, over 1024 26 / 36, over 2048 40 / 40; 128 x 32
-// heads, 8 of KV, over 512 20 / 19, over 2048 40 / 26; three requests, 75 x 3 heads, 1 of KV, over 2700
-// 18 / 44, 50 x 24 heads, 8 of KV, over 1000 18 / 25; 8 requests of 16 x 32 heads over 1000 26 / 23).
+// request: 512 tokens x 8 heads over 512 cached 20 / 31, over 1024 27 / 34, over 2048 40 / 38; 128 x 32
+// heads, 8 of KV, over 512 20 / 19, over 2048 40 / 27; three requests, 75 x 3 heads, 1 of KV, over 2700
+// 18 / 45, 50 x 24 heads, 8 of KV, over 1000 18 / 25; 8 requests of 16 x 32 heads over 1000 26 / 23).
 // No request of a call that keeps the contract has more than T tokens.
 constexpr int few_rows_fp4(long long T, int Hq, int Hkv, long long most_tokens) {
   const bool all = T * Hq <= 1 << 23 && T * Hq * most_tokens <= (Hkv <= 2 ? 1ll << 23 : 15ll << 18);

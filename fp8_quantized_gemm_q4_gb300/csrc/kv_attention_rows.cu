@@ -21,15 +21,15 @@
 // maximum, the vote on the reference, the exponentials, the store) and whose
 // warps have 1540 issue slots of about 2800 clocks a tile with the converters.  832
 // threads leave 72 registers each, 20 bytes of which are spilled.
-// B = 2, 2048 rows x 32 heads over 4000 to 8000 tokens, D = 128: 265 us (840 TFLOP/s); the
-// same with D = 64, half the MMAs: 225.  With two threads per row 303, with one 2.5 times the MMAs' time.  Also built and
+// B = 2, 2048 rows x 32 heads over 4000 to 8000 tokens, D = 128: 254 us (880 TFLOP/s); the
+// same with D = 64, half the MMAs: 218.  With two threads per row 303, with one 2.5 times the MMAs' time.  Also built and
 // measured: two groups of warps on alternate tiles, each with an O of its own and
 // Q in shared memory (303 us: both operands of Q K^T from shared memory take all of
 // its bandwidth), with one O and a reference settled in turn (324 us: P in S's place
 // holds the next scores back), and with columns of its own for P (443 us: there
 // is room for one P only).
 // 4-bit cache: the converters multiply the codes, as fp16, by their scales, so that page
-// scales are 1; 256 us (870 TFLOP/s).  They have half the bytes to read and twice the
+// scales are 1; 251 us (890 TFLOP/s).  They have half the bytes to read and twice the
 // instructions to issue; with half of the tile's conversions left out 6 % less, so sharing a
 // widened tile between two CTAs is worth no more than that.
 // The tiles of all units form one list that is cut into equal shares, one CTA
