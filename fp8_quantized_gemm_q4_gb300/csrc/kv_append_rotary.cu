@@ -164,16 +164,12 @@ __device__ __forceinline__ void flat_heads(const KvRotaryParams& p, int first, i
   const long long line = ((((long long)(slot >> p.page_shift) * p.Hkv + head) << p.page_shift) + (slot & ((1 << p.page_shift) - 1)));
 #pragma unroll 1
   for (int h0 = 0; h0 < heads; h0 += kBatch) {
-    if (h0) {
-#pragma unroll
-      for (int h = 0; h < kBatch; ++h)
-        if (h0 + h < heads) raw[h].load(x, from + (h0 + h) * step, at);
-    }
 #pragma unroll
     for (int h = 0; h < kBatch; ++h) {
       if (h0 + h >= heads) break;
       float v[16];
       raw[h].values(v);
+      if (h0 + h + kBatch < heads) raw[h].load(x, from + (h0 + h + kBatch) * step, at);
       turn.apply(v, p.interleaved);
       if constexpr (kQ) {
         if (!ok) continue;
