@@ -15,7 +15,8 @@
 // kv_append, a run of rows that lie in one page shares a scale.
 //
 // Bound by the stream of rows, angles and codes.  16384 rows, 32 + 16 heads of 128, bf16:
-// 8 bits 77 us (372 MB, 0.71 of HBM), 4 bits 69 us (355 MB, 0.76), the cached rows read back
+// 8 bits 77 us (372 MB, 0.71 of HBM; the queries alone 0.9, keys and values 41 us of them, at 64 rows a CTA a
+// chain of reads, maxima and codes), 4 bits 63 us (355 MB, 0.83), the cached rows read back
 // 19 us (88 MB, most of them in L2).  A third of the warps' time is waiting for rows, the rest issue (0.5
 // of the slots); 46 % of the SM's warps at 64 registers.  64 rows: 2.7 and 4.7 us, of which a
 // launch that does nothing is about 2.
