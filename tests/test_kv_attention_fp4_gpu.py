@@ -131,6 +131,16 @@ def test_many_requests(cuda_lib):
     check(cuda_lib, q, cache, table, cu, kv, 16)
 
 
+def test_many_requests_of_both_kinds(cuda_lib, monkeypatch):
+    """More requests than a CTA has threads, single tokens and prompts among one another, some without rows or tokens."""
+    monkeypatch.setattr(sys.modules[__name__], "ROOM", 2048)
+    rng = random.Random(6)
+    q_lens = [rng.choice([1, 1, 1, 1, 1, 1, 0, 5, 33, 70]) for _ in range(1700)]
+    kv = [max(0, n + rng.choice([0, 3, 90, -4])) for n in q_lens]
+    q, cache, table, cu = build(cuda_lib, 6, kv, q_lens, 8, 2, 64, 16)
+    check(cuda_lib, q, cache, table, cu, kv, 16)
+
+
 @pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [300, 70]), ([100, 2], [300, 70])])
 def test_sharp_and_flat_scores(cuda_lib, q_lens, kv_lens):
