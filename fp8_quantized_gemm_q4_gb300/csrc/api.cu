@@ -1293,7 +1293,7 @@ static bs_status kv_attention(const bs_kv_attention_args* a, bool fp4, const voi
   const int64_t most = a->max_q_len ? a->max_q_len : a->T;
   const int64_t most_rows = most * (a->Hq / a->Hkv);
   p.most_rows = (int)(most_rows < (1 << 30) ? most_rows : (1 << 30));
-  p.few_rows = fp4 ? bsk::few_rows_fp4(a->T, a->Hq, a->Hkv, (int64_t)a->max_pages * a->page_size) : bsk::few_rows(a->T, a->Hq);
+  p.few_rows = fp4 ? bsk::few_rows_fp4(a->T, a->B, a->Hq, a->Hkv, (int64_t)a->max_pages * a->page_size) : bsk::few_rows(a->T, a->Hq);
   p.counters = static_cast<int*>(a->workspace);
   p.work = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + kStreamKCounterBytes);
   p.wait_ns = wait_ns_of(a->wait_timeout_us);

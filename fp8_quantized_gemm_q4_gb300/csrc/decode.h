@@ -117,9 +117,11 @@ constexpr int few_rows(long long T, int Hq) { return T * Hq <= 2048 ? 128 : 16; 
 // request: 512 tokens x 8 heads over 512 cached 20 / 31, over 1024 27 / 34, over 2048 40 / 38; 128 x 32
 // heads, 8 of KV, over 512 20 / 19, over 2048 40 / 27; three requests, 75 x 3 heads, 1 of KV, over 2700
 // 18 / 45, 50 x 24 heads, 8 of KV, over 1000 18 / 25; 8 requests of 16 x 32 heads over 1000 26 / 23).
-// No request of a call that keeps the contract has more than T tokens.
-constexpr int few_rows_fp4(long long T, int Hq, int Hkv, long long most_tokens) {
-  const bool all = T * Hq <= 1 << 23 && T * Hq * most_tokens <= (Hkv <= 2 ? 1ll << 23 : 15ll << 18);
+// No request of a call that keeps the contract has more than T tokens; of one that breaks it, each
+// may claim as many, and up to 4096 of them the kernel's sums of tiles stay within 32 bits.
+constexpr int few_rows_fp4(long long T, int B, int Hq, int Hkv, long long most_tokens) {
+  const long long tokens = most_tokens > 128 ? most_tokens : 128;  // a tile
+  const bool all = B <= 4096 && T * Hq <= 1 << 16 && T * Hq * tokens <= (Hkv <= 2 ? 1ll << 23 : 15ll << 18);
   const int rows = few_rows(T, Hq), most = all ? (int)T * (Hq / Hkv) : 0;
   return most > rows ? most : rows;
 }

@@ -270,6 +270,22 @@ def test_contract_breaks(cuda_lib, Hq, Hkv, D, page):
         assert bs.device_status()[0] == bs.BS_OK
 
 
+def test_many_requests_claim_the_same_rows(cuda_lib):
+    """Offsets that rise and fall, each pair of them the whole call: the status, and no row outside it."""
+    bs = cuda_lib
+    q, cache, table, cu = build(bs, 41, [40], [30], 8, 2, 64, 16)
+    T, n = 30, 4000
+    room, lse = torch.full((3 * T, 8, 64), 3.0, device=DEV, dtype=torch.bfloat16), torch.full((3 * T, 8), 7.0, device=DEV)
+    for B in (n, 5000):     # the few-rows kernel's whole, and shared out
+        bs.clear_device_status()
+        bs.kv_attention(q, cache, i32(table * B), i32([0, T] * (B // 2) + [0]), i32([40] * B), 0, out=room[T:2 * T], lse=lse[T:2 * T])
+        assert bs.device_status()[0] == bs.BS_ERR_OFFSETS
+        assert bool((room[:T] == 3).all()) and bool((room[2 * T:] == 3).all())
+        assert bool((lse[:T] == 7).all()) and bool((lse[2 * T:] == 7).all())
+    bs.clear_device_status()
+    check(bs, q, cache, table, cu, [40], 16)
+
+
 @pytest.mark.usefixtures("room")
 def test_strides_streams_and_workspaces(cuda_lib):
     """q and out as slices, [H, T, D] in memory, on a stream of their own, with a workspace of their own; both
