@@ -5,7 +5,7 @@
 // launch: the CTAs share K, and their partial products t = x A^T (mma.sync, rows on M,
 // ranks on N) meet in distributed shared memory, where every CTA adds them in the same
 // order; then the CTAs share N.  t stays fp32 and enters the second product scaled and
-// split into two bf16 (within 2^-17 of it), or three where out is fp32 (within 2^-25);
+// split into two bf16 (within 2^-16 of it), or three where out is fp32 (within 2^-28);
 // products with the bf16 B are exact, sums fp32.
 #include "decode.h"
 #include "decode.cuh"
@@ -106,15 +106,32 @@ __device__ __forceinline__ void copy_rows(const LoraParams& p, const Tile& t, in
   }
 }
 
-// Terms that t is split into for outputs of this type, and the next of them: v to bf16
-// pairs, v becomes what they leave
+// Terms that t is split into for outputs of this type, and their bits.  All but the last are
+// cut, not rounded, so that every term has t's sign and none is infinite where t is not;
+// a remainder of 0 becomes 2^-30 of t.  So the terms' products with an infinite element of B
+// are infinities of one sign, as t's own, and those of an infinite t never meet inf - inf
+// (down to |t| = 2^-96, below which that remainder underflows).
 template <bool kBf16>
 constexpr int kTerms = kBf16 ? 2 : 3;
-__device__ __forceinline__ uint2 next_term(float4& v) {
-  const uint32_t a = pack_bf16x2(v.x, v.y), b = pack_bf16x2(v.z, v.w);
-  v.x -= __uint_as_float(a << 16), v.y -= __uint_as_float(a & 0xffff0000u);
-  v.z -= __uint_as_float(b << 16), v.w -= __uint_as_float(b & 0xffff0000u);
-  return make_uint2(a, b);
+template <int kTerm>
+__device__ __forceinline__ void split(float t, uint32_t (&term)[kTerm]) {
+  const uint32_t head = t == t ? __float_as_uint(t) & 0xffff0000u : 0x7fff0000u;
+  const float least = __uint_as_float(head) * 0x1p-30f;
+  term[0] = head >> 16;
+#pragma unroll
+  for (int i = 1; i < kTerm; ++i) {
+    t -= __uint_as_float(term[i - 1] << 16);
+    t = fabsf(t) > 0.0f ? t : least;  // of an infinite t the difference is NaN
+    term[i] = i + 1 < kTerm ? __float_as_uint(t) >> 16 : pack_bf16x2(t, 0.0f) & 0xffffu;
+  }
+}
+// Those of four values, two in a word
+template <int kTerm>
+__device__ __forceinline__ void split4(const float4& v, uint2 (&w)[kTerm]) {
+  uint32_t a[kTerm], b[kTerm], c[kTerm], d[kTerm];
+  split(v.x, a), split(v.y, b), split(v.z, c), split(v.w, d);
+#pragma unroll
+  for (int i = 0; i < kTerm; ++i) w[i] = make_uint2(a[i] | b[i] << 16, c[i] | d[i] << 16);
 }
 
 // t of the cluster: the CTAs' sums (kVecs float4 at `sums` in each) added in order of rank,
@@ -131,8 +148,10 @@ __device__ __forceinline__ void gather_t(const LoraParams& p, int id, int size, 
       v.x += e.x, v.y += e.y, v.z += e.z, v.w += e.w;
     }
     v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
+    uint2 w[kTerm];
+    split4(v, w);
 #pragma unroll
-    for (int i = 0; i < kTerm; ++i) static_cast<uint2*>(t)[i * kVecs + x] = next_term(v);
+    for (int i = 0; i < kTerm; ++i) static_cast<uint2*>(t)[i * kVecs + x] = w[i];
   }
 }
 
@@ -483,12 +502,15 @@ __global__ void __launch_bounds__(kThreads, many_resident(kRank, kBf16)) lora_ma
       }
       v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
       const int row = x / (kRank / 4), half_piece = x % (kRank / 4);
+      // ranks that there are not: an infinite x times their zeros in A is NaN
+      if (4 * half_piece >= p.r) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      uint2 w[kTerms<kBf16>];
+      split4(v, w);
       const uint32_t to = smem + S::kTAt + t_at<kRow>(row, half_piece >> 1) + 8 * (half_piece & 1);
 #pragma unroll
       for (int i = 0; i < kTerms<kBf16>; ++i) {
-        const uint2 w = next_term(v);
 #pragma unroll 8
-        for (int r = 0; r < size; ++r) st_cluster(mapa_shared(to, r) + i * S::kT, w.x, w.y);
+        for (int r = 0; r < size; ++r) st_cluster(mapa_shared(to, r) + i * S::kT, w[i].x, w[i].y);
       }
     }
   }

@@ -807,7 +807,9 @@ bs_status bs_fp4_matvec(const bs_fp4_matvec_args *args, bs_stream_t stream);
  * share.  Rows cu_rows[b] .. cu_rows[b + 1] - 1 belong to request b, w = which[b]:
  *     out[t] = y[t] + scales[w] (x[t] A_w^T) B_w^T        (y[t] where w < 0)
  * Sums are fp32; x A^T enters the second product as a pair of bf16 (within 2^-16 of
- * it), or as three for fp32 outputs (within 2^-24); out is rounded once.
+ * it), or as three for fp32 outputs (within 2^-24); out is rounded once.  Infinities and
+ * NaN in x, A, B and y give what the formula gives, in the rows and columns that use them
+ * (an infinity of B where scales (x A^T) is below 2^-96 gives NaN).
  *
  *   x          bf16 [T, ldx]
  *   a, b       bf16 [adapters, r, K] and [adapters, N, r]
