@@ -196,6 +196,7 @@ struct LoraParams {
   long long ldo;
   int bf16;               // type of y and out
   int T, B, K, N, r, adapters;
+  int least, most;        // rows of the requests that a launch takes; the launch's choice
   int* status;
 };
 cudaError_t launch_lora(const LoraParams& p, int sms, cudaStream_t stream);

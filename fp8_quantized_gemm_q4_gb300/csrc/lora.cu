@@ -1,10 +1,9 @@
 // lora.cu -- low-rank adapters of many requests beside a projection that they share:
 //   out = y + s_a (x A_a^T) B_a^T,  a = the adapter of the row's request.
 //
-// A tile is up to 8 or 64 rows of one request, and a cluster of CTAs takes it in one
-// launch: the CTAs share K, and their partial products t = x A^T (mma.sync, rows on M,
-// ranks on N) meet in distributed shared memory, where every CTA adds them in the same
-// order; then the CTAs share N.  t stays fp32 and enters the second product scaled and
+// A tile is up to 8 or 64 rows of one request, and a cluster of CTAs takes it: the CTAs
+// share K, and their partial products t = x A^T (mma.sync, rows on M, ranks on N) meet in
+// distributed shared memory, where every CTA adds them in the same order; then the CTAs share N.  t stays fp32 and enters the second product scaled and
 // split into two bf16 (within 2^-16 of it), or three where out is fp32 (within 2^-28);
 // products with the bf16 B are exact, sums fp32.
 #include "decode.h"
@@ -14,7 +13,6 @@ namespace bsk {
 namespace {
 
 constexpr int kThreads = 256, kWarps = 8;
-constexpr long long kManyEach = 32;  // rows a request, on average, from which tiles have 64 rows
 
 __device__ __forceinline__ void mma_bf16_16x8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -39,14 +37,15 @@ __device__ __forceinline__ uint4 load16(const void* p, bool in) {
   return in ? *static_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
 }
 
-// A request's rows within the call, its adapter, and whether its numbers break the contract
+// A request's rows within the call (none if they are not this launch's to take), its adapter,
+// and whether its numbers break the contract
 struct Rows {
   int row0, n, id;
   bool bad;
 };
 __device__ __forceinline__ Rows rows_of(const LoraParams& p, int b) {
-  const int r0 = p.cu[b], r1 = p.cu[b + 1], w = p.which[b];
-  return {r0, r0 < 0 || r1 <= r0 ? 0 : max(0, min(r1, p.T) - r0), w >= p.adapters ? -1 : w,
+  const int r0 = p.cu[b], r1 = p.cu[b + 1], w = p.which[b], n = r0 < 0 || r1 <= r0 ? 0 : max(0, min(r1, p.T) - r0);
+  return {r0, n < p.least || n > p.most ? 0 : n, w >= p.adapters ? -1 : w,
           r0 < 0 || r1 < r0 || r1 > p.T || w >= p.adapters};
 }
 
@@ -572,35 +571,64 @@ cudaError_t launch_rank(const LoraParams& p, bool many, int cluster, long long t
   return p.r <= 64 ? launch<64, kBf16>(p, many, cluster, tiles, stream) : launch<128, kBf16>(p, many, cluster, tiles, stream);
 }
 
+// Which tiles a request gets follows from its own rows, in two launches; T and B, which also count
+// padding and requests without rows, say only whether one launch would do.  Tiles of 8 rows alone
+// do up to kFewEach rows a request, and where all of them stand on the GPU at once in clusters of
+// two; tiles of 64 alone where they are mostly full ones whatever the requests' lengths; what is
+// between may hold prompts beside single tokens (us, 8 rows / 64 rows / both, K = 4096, N = 6144: rank 16, 4096
+// rows of one request and 255 single ones 75 / 86 / 58, and 127 single ones 72 / 82 / 49, the one of 256 requests alone
+// 47 / 62 / 37; rank 64 131 / 116 / 89, 128 / 111 / 71, 92 / 82 / 46; but 64 requests of 32 rows 27 / 24 / 29 and
+// 40 / 28 / 31, for a launch without tiles takes 2 to 10).
+constexpr int kTall = 32;  // rows from which a request's tiles have 64
+constexpr long long kManyEach = 64, kFewEach = 8;
+constexpr long long few_places(int r, int sms) { return (long long)sms * (r <= 32 ? 4 : r <= 64 ? 2 : 1); }
+
+// Tiles of 8 rows for requests of up to `most`; at most `tiles` of them, of which `expected` to expect
+cudaError_t launch_few(LoraParams p, int most, long long tiles, long long expected, int sms, cudaStream_t stream) {
+  // Eight CTAs a tile, fewer where not all would be on the GPU at once, for each has its own
+  // start and exchange (us with 8 / 4 / 2 / 1, K = 4096, N = 6144: rank 16, 1 request 6.3 / 8.6 / 12 / 19, 64
+  // requests 10.4 / 10.3 / 12.6 / 19, 256 requests 36 / 26 / 25 / 28; rank 64, 256 requests 81 / 62 / 53 / 49).
+  int cluster = 8;
+  while (cluster > 1 && expected * cluster > few_places(p.r, sms)) cluster /= 2;
+  p.least = 1, p.most = most;
+  return p.bf16 ? launch_rank<true>(p, false, cluster, tiles, stream) : launch_rank<false>(p, false, cluster, tiles, stream);
+}
+
+// Tiles of 64 rows for requests of `least` rows and more, `requests` of them at most
+cudaError_t launch_many(LoraParams p, int least, long long requests, int sms, cudaStream_t stream) {
+  // The size whose CTAs take the fewest rounds on the GPU for their shares of a tile, the
+  // smaller of equals: a round that is not full costs as much as one that is.  Clusters do
+  // not fill the last twentieth (us with 8 / 6 / 4 / 3 / 2, K = N = 4096 but where given: rank 16, bf16,
+  // 3584 rows 31 / 26 / 33 / 32 / 34, 4800 rows 37 / 38 / 34 / 42 / 36, 8192 rows, N = 6144, 66 / 62 / 79 / 57 / 77,
+  // 9600 rows 56 / 60 / 62 / 67 / 60; rank 64, 8190 rows, K = 7168, 77 / 74 / 77 / 72 / 99; rank 128, 4096 rows
+  // 94 / 76 / 65 / 83 / 59, 1200 rows 38 / 26 / 33 / 42 / 58; fp32, rank 16, 3000 rows 37 / 49 / 46 / 60 / 51).
+  // Where other requests are the other launch's, the rounds of as few tiles as there may be count as well.
+  const long long full = p.T / kManyRows, expected = full + (requests + 1) / 2;
+  const long long at_once = (long long)sms * many_resident(p.r <= 32 ? 32 : p.r <= 64 ? 64 : 128, p.bf16) * 19 / 20;
+  const auto rounds = [&](int size) {
+    return (expected * size + at_once - 1) / at_once + (least > 1 ? ((full + 1) * size + at_once - 1) / at_once : 0);
+  };
+  int cluster = 8;
+  for (const int size : {6, 4, 3, 2})
+    if (rounds(size) * cluster <= rounds(cluster) * size) cluster = size;
+  p.least = least, p.most = p.T;
+  return p.bf16 ? launch_rank<true>(p, true, cluster, full + requests, stream)
+                : launch_rank<false>(p, true, cluster, full + requests, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_lora(const LoraParams& p, int sms, cudaStream_t stream) {
-  // us, tiles of 8 / 64 rows, K = 4096, N = 6144, rank 16: 8 requests of 4 rows 6.5 / 11, of 32 rows 10.2 /
-  // 12.4; 64 requests of 4 rows 14 / 28, of 16 rows 25 / 31, of 32 rows 40 / 37
-  const bool many = p.T >= kManyEach * p.B;
-  // every request may end in a tile that is not full
-  const long long full = p.T / (many ? kManyRows : kFewRows), requests = p.B < p.T ? p.B : p.T, tiles = full + requests;
-  int cluster = 8;
-  if (many) {
-    // The size whose CTAs take the fewest rounds on the GPU for their shares of a tile, the
-    // smaller of equals: a round that is not full costs as much as one that is.  Clusters do
-    // not fill the last twentieth (us with 8 / 6 / 4 / 3 / 2, K = N = 4096 but where given: rank 16, bf16,
-    // 3584 rows 31 / 26 / 33 / 32 / 34, 4800 rows 37 / 38 / 34 / 42 / 36, 8192 rows, N = 6144, 66 / 62 / 79 / 57 / 77,
-    // 9600 rows 56 / 60 / 62 / 67 / 60; rank 64, 8190 rows, K = 7168, 77 / 74 / 77 / 72 / 99; rank 128, 4096 rows
-    // 94 / 76 / 65 / 83 / 59, 1200 rows 38 / 26 / 33 / 42 / 58; fp32, rank 16, 3000 rows 37 / 49 / 46 / 60 / 51).
-    const long long at_once = (long long)sms * many_resident(p.r <= 32 ? 32 : p.r <= 64 ? 64 : 128, p.bf16) * 19 / 20;
-    const long long expected = full + (requests + 1) / 2;
-    const auto rounds = [&](int size) { return (expected * size + at_once - 1) / at_once; };
-    for (const int size : {6, 4, 3, 2})
-      if (rounds(size) * cluster <= rounds(cluster) * size) cluster = size;
-  } else {
-    // Eight CTAs a tile, fewer where not all would be on the GPU at once, for each has its own
-    // start and exchange (us with 8 / 4 / 2 / 1, K = 4096, N = 6144: rank 16, 1 request 6.3 / 8.6 / 12 / 19, 64
-    // requests 10.4 / 10.3 / 12.6 / 19, 256 requests 36 / 26 / 25 / 28; rank 64, 256 requests 81 / 62 / 53 / 49).
-    const long long at_once = (long long)sms * (p.r <= 32 ? 4 : p.r <= 64 ? 2 : 1);
-    while (cluster > 1 && tiles * cluster > at_once) cluster /= 2;
-  }
-  return p.bf16 ? launch_rank<true>(p, many, cluster, tiles, stream) : launch_rank<false>(p, many, cluster, tiles, stream);
+  // every request may end in a tile that is not full, half of them do
+  const long long requests = p.B < p.T ? p.B : p.T, few = p.T / kFewRows;
+  const long long expected = p.T <= kFewRows * requests ? requests : few + requests / 2;
+  if (p.T >= kManyEach * p.B) return launch_many(p, 1, requests, sms, stream);
+  if (p.T <= kFewEach * p.B || 2 * expected <= few_places(p.r, sms))
+    return launch_few(p, p.T, few + requests, expected, sms, stream);
+  constexpr int kEach = (kTall - 1 + kFewRows - 1) / kFewRows;  // most tiles of a request that is not tall
+  const cudaError_t e = launch_few(p, kTall - 1, few < (kEach - 1) * requests ? few + requests : kEach * requests, requests, sms, stream);
+  if (e != cudaSuccess) return e;
+  return launch_many(p, kTall, requests < p.T / kTall ? requests : p.T / kTall, sms, stream);
 }
 
 }  // namespace bsk
