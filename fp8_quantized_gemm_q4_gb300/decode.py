@@ -80,7 +80,8 @@ class DecodeAttention:
                     device status BS_ERR_OFFSETS
     lora_qkv, lora_out  (a, b, scales or None) of low-rank adapters beside the two
                     products, as lora_add takes them; None: none
-    which           int32 [B] (device), each request's adapter, -1 (as at the start): none
+    which           int32 [B] (device), each request's adapter, -1 (as at the start and after
+                    release): none
     lens            int32 [B], the cached tokens of each request (device)
     n_free          int32 [1], the pages left (device)
     """
@@ -144,6 +145,9 @@ class DecodeAttention:
         return self._linear(att.view(T, q_rows), self.w_out, self.lora_out, cu)
 
     def release(self, done):
-        """Give back the pages of the requests with done[b] != 0 (int32 [B])."""
+        """Give back the pages of the requests with done[b] != 0 (int32 [B]); what they leave is an
+        empty request without an adapter, as at the start."""
         kv_release(self.lens, done, self.table, self.free, self.n_free, self.page_size)
-        self.lens.masked_fill_(done != 0, 0)
+        ended = done != 0
+        self.lens.masked_fill_(ended, 0)
+        self.which.masked_fill_(ended, -1)
