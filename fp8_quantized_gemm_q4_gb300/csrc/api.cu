@@ -1293,7 +1293,20 @@ static bs_status kv_attention(const bs_kv_attention_args* a, bool fp4, const voi
   const int64_t most = a->max_q_len ? a->max_q_len : a->T;
   const int64_t most_rows = most * (a->Hq / a->Hkv);
   p.most_rows = (int)(most_rows < (1 << 30) ? most_rows : (1 << 30));
-  p.few_rows = fp4 ? bsk::few_rows_fp4(a->T, a->B, a->Hq, a->Hkv, (int64_t)a->max_pages * a->page_size) : bsk::few_rows(a->T, a->Hq);
+  p.few_rows = bsk::few_rows(a->T, a->Hq);
+  L.few_only = p.most_rows <= p.few_rows;
+  const int64_t all = a->T * a->Hq, tokens = (int64_t)a->max_pages * a->page_size;  // the most that a request can have
+  if (fp4 && !L.few_only && all * 128 <= bsk::whole_most(a->Hkv)) {
+    p.whole_most = bsk::whole_most(a->Hkv);
+    L.few_only = all * (tokens > 128 ? tokens : 128) <= p.whole_most;
+    // nothing to ask, but where offsets that break the contract let more requests claim all rows
+    // than the kernel's 32-bit sums of tiles hold
+    if (L.few_only && a->B <= 4096) {
+      p.whole_most = 0;
+      const int rows = (int)a->T * (a->Hq / a->Hkv);
+      if (rows > p.few_rows) p.few_rows = rows;
+    }
+  }
   p.counters = static_cast<int*>(a->workspace);
   p.work = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + kStreamKCounterBytes);
   p.wait_ns = wait_ns_of(a->wait_timeout_us);

@@ -111,20 +111,19 @@ cudaError_t launch_kv_gather(const KvGatherParams& p, cudaStream_t stream);
 // request 32 rows 20 / 39, 128 rows 38 / 57; 8 requests, 64 rows 28 / 24; 64 requests, 16 rows 98 / 144,
 // 32 rows 182 / 139 (D = 64: 16 rows 63 / 133, 32 rows 113 / 127).
 constexpr int few_rows(long long T, int Hq) { return T * Hq <= 2048 ? 128 : 16; }
-// Over 4 bits the few-rows kernel takes whole calls whose rows (of all heads) times the
-// tokens that a request can have are few: at most 2^23 over one or two KV heads, which leave the
-// many-rows kernel short of units, 15 2^18 over more; else as above (us, few / many rows, one
+// Over 4 bits the few-rows kernel also takes whole calls of few rows times tokens: a request's rows
+// (of all heads) times its cached tokens, 128 (a tile) at least, summed over the requests, are at
+// most 2^23 over one or two KV heads, which leave the many-rows kernel short of units, 15 2^18 over
+// more; else as above (us, few / many rows, one
 // request: 512 tokens x 8 heads over 512 cached 20 / 31, over 1024 27 / 34, over 2048 40 / 38; 128 x 32
 // heads, 8 of KV, over 512 20 / 19, over 2048 40 / 27; three requests, 75 x 3 heads, 1 of KV, over 2700
 // 18 / 45, 50 x 24 heads, 8 of KV, over 1000 18 / 25; 8 requests of 16 x 32 heads over 1000 26 / 23).
-// No request of a call that keeps the contract has more than T tokens; of one that breaks it, each
-// may claim as many, and up to 4096 of them the kernel's sums of tiles stay within 32 bits.
-constexpr int few_rows_fp4(long long T, int B, int Hq, int Hkv, long long most_tokens) {
-  const long long tokens = most_tokens > 128 ? most_tokens : 128;  // a tile
-  const bool all = B <= 4096 && T * Hq <= 1 << 16 && T * Hq * tokens <= (Hkv <= 2 ? 1ll << 23 : 15ll << 18);
-  const int rows = few_rows(T, Hq), most = all ? (int)T * (Hq / Hkv) : 0;
-  return most > rows ? most : rows;
-}
+// Both kernels form that sum from the lengths, so they agree, and the width of the table changes
+// no result; a call whose T rows pass it with 128 tokens each is not asked.  Where the table has
+// room for more, the many-rows kernel starts only to find nothing, which takes 6 us (one request, 32
+// heads, 8 of KV, 64 tokens, nothing cached: 7 and 13, by the many-rows kernel 31; 128 tokens, 600 cached 20
+// and 26, 29; four requests of 64 tokens, 400 cached 26 and 32, 29).
+constexpr int whole_most(int Hkv) { return Hkv <= 2 ? 1 << 23 : 15 << 18; }
 struct KvAttentionParams {
   const void* q;          // bf16 [T, Hq, D]
   long long q_tok_stride, q_head_stride;
@@ -145,7 +144,8 @@ struct KvAttentionParams {
   int fp4;                // the cache holds 4 bits
   float scale_log2;       // softmax scale * log2(e)
   int most_rows;          // bound of the rows per KV head of a request (at most 2^30)
-  int few_rows;           // few_rows(T, Hq), or few_rows_fp4
+  int few_rows;           // few_rows(T, Hq)
+  int whole_most;         // 4 bits: the few-rows kernel takes all of a call of no more rows times tokens; 0: do not ask
   float* work;            // pieces of (request, head) pairs cut between CTAs
   int* counters;          // arrivals of those pieces (zero between calls)
   int* status;
@@ -155,6 +155,7 @@ struct KvAttentionLaunch {
   KvAttentionParams p;
   CUtensorMap tm_k, tm_v; // codes as rows of 128 bytes, box kv_attention_box tokens
   int few_grid, rows_grid;
+  bool few_only;          // no request is the many-rows kernel's
 };
 int kv_attention_few_grid(int sms);
 size_t kv_attention_piece_bytes(int D);  // per CTA of the few-rows grid

@@ -436,18 +436,21 @@ struct FewSmem {
   int begin[kItems], end[kItems];
   uint64_t full[kStages], empty[kStages];
   int2 scan[kFewThreads / 32];
+  int parts[kFewThreads / 32];
+  int few;  // of 4 bits: most rows per KV head of a request that this kernel takes
   long long first_unit;      // of this share, counted over requests with tiles
   long long bound[2];        // its first tile in the list, the next share's
   int abort_flag, last;
 };
 
 // Tiles of each unit of a request in this kernel's list: none without rows or
-// with more than few_rows per KV head, else one at least (rows that see nothing
-// are written too).  Which kernel serves a request follows from its own rows and
-// the call's, so that its result does not depend on the bound that the call gives.
+// with more than `few` per KV head, else one at least (rows that see nothing
+// are written too).  Which kernel serves a request follows from its own rows, the call's
+// and (4 bits) their tokens, so that its result depends neither on the bound that the call
+// gives nor on the width of its table.
 template <int kTile>
-__device__ __forceinline__ int few_tiles(const KvAttentionParams& p, int n, int len, int G) {
-  return n <= 0 || (long long)n * G > p.few_rows ? 0 : max(1, (len + kTile - 1) / kTile);
+__device__ __forceinline__ int few_tiles(int few, int n, int len, int G) {
+  return n <= 0 || (long long)n * G > few ? 0 : max(1, (len + kTile - 1) / kTile);
 }
 
 // A piece of a unit that is cut between CTAs: partial sums [8][D], then (m, l) of
@@ -494,18 +497,21 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
   // over the block, place its units in the list.
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  int row0_own = 0, n_own = 0, len_own = 0;  // of the last of them: all there is while B <= threads
+  Rows own = {};  // of the last of them: all there is while B <= threads
+  int len_own = 0;
+  int few = p.few_rows;
+  if (kFp4 && b0 < b1) own = rows_of(p, b0), len_own = cached(p, b0);
+  if (kFp4 && p.whole_most) few = most_few_rows<kThreads>(p, b0, b1, own, len_own, sm.parts, G);
+  if (kFp4 && tid == 0) sm.few = few;
   int2 mine = make_int2(0, 0);
   for (int b = b0; b < b1; ++b) {
-    const Rows own = rows_of(p, b);
-    row0_own = own.row0, n_own = own.n;
-    len_own = cached(p, b);
-    const int nt = few_tiles<kTile>(p, n_own, len_own, G), rt = nt ? (n_own * G + 7) / 8 : 0;
+    if (!kFp4 || b > b0) own = rows_of(p, b), len_own = cached(p, b);
+    const int nt = few_tiles<kTile>(few, own.n, len_own, G), rt = nt ? (own.n * G + 7) / 8 : 0;
     mine.x += nt * rt;
     mine.y += rt;
     // one CTA tells: the check in all of them cost a call of prompts, whose other kernel
     // waits for this one to end, 11 of 276 us
-    if (blockIdx.x == 0 && ((long long)n_own * G > p.most_rows || own.bad || length_bad(p, b)))
+    if (blockIdx.x == 0 && ((long long)own.n * G > p.most_rows || own.bad || length_bad(p, b)))
       record_status(p.status, kStatusOffsets, 53);
   }
   int2 incl = mine;
@@ -537,9 +543,9 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
     const long long from = at + units * kUnitTiles;
     if (c < from || c >= from + (long long)mine.x * p.Hkv + (long long)mine.y * p.Hkv * kUnitTiles) continue;
     for (int b = b0; b < b1; ++b) {
-      int n = n_own, len = len_own;
+      int n = own.n, len = len_own;
       if (per > 1) n = rows_of(p, b).n, len = cached(p, b);
-      const int nt = few_tiles<kTile>(p, n, len, G);
+      const int nt = few_tiles<kTile>(kFp4 ? sm.few : p.few_rows, n, len, G);
       if (!nt) continue;
       const int u = p.Hkv * ((n * G + 7) / 8);
       const long long off = c - (at + units * kUnitTiles);
@@ -571,12 +577,12 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas)
     {
       long long at = own_at, units = (long long)before.y * p.Hkv;
       for (int b = b0; b < b1 && units < base + kItems && at < t_first + tiles; ++b) {
-        int row0 = row0_own, n = n_own, len = len_own;
+        int row0 = own.row0, n = own.n, len = len_own;
         if (per > 1) {
           const Rows r = rows_of(p, b);
           row0 = r.row0, n = r.n, len = cached(p, b);
         }
-        const int nt = few_tiles<kTile>(p, n, len, G);
+        const int nt = few_tiles<kTile>(kFp4 ? sm.few : p.few_rows, n, len, G);
         if (!nt) continue;
         const int rt = (n * G + 7) / 8, u = p.Hkv * rt;
         for (int h = (int)max(0ll, base - units); h < u && units + h < base + kItems; ++h) {
@@ -1011,7 +1017,7 @@ cudaError_t launch_kv_attention(const KvAttentionLaunch& L, cudaStream_t stream)
                           : (p.D == 64 ? launch_few<64, false>(L, stream) : launch_few<128, false>(L, stream));
     if (e != cudaSuccess) return e;
   }
-  if (p.most_rows <= p.few_rows) return cudaSuccess;
+  if (L.few_only) return cudaSuccess;
   return launch_kv_attention_rows(L, stream);
 }
 

@@ -67,6 +67,29 @@ __device__ __forceinline__ bool length_bad(const KvAttentionParams& p, int b) {
   return (unsigned)p.kv_lens[b] > (unsigned)(p.max_pages << p.page_shift);
 }
 
+// Rows of all heads times tokens of a request in the sum that decides whether the few-rows kernel
+// takes the whole call.  Whatever passes the bound counts as just above it: offsets that break
+// the contract may claim any number of rows, and 32 bits hold a CTA's sum.
+__device__ __forceinline__ int whole_part(const KvAttentionParams& p, const Rows& r, int len) {
+  return (int)min((long long)min(r.n, p.T) * p.Hq * max(len, 128), (long long)p.whole_most + 1);
+}
+// The most rows per KV head of a request that the few-rows kernel takes, from that sum over the
+// CTA's requests: a thread's are b0 .. b1 - 1, the first as read already.  parts: a place a warp, free
+// again after another barrier.
+template <int kThreads>
+__device__ __forceinline__ int most_few_rows(const KvAttentionParams& p, int b0, int b1, const Rows& first, int len, int* parts, int G) {
+  const int over = p.whole_most + 1;
+  int sum = b0 < b1 ? whole_part(p, first, len) : 0;
+  for (int b = b0 + 1; b < b1; ++b) sum = min(sum + whole_part(p, rows_of(p, b), cached(p, b)), over);
+  sum = __reduce_add_sync(kFullMask, sum);
+  if ((threadIdx.x & 31) == 0) parts[threadIdx.x >> 5] = min(sum, over);
+  __syncthreads();
+  int all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) all += parts[w];
+  return all <= p.whole_most ? max(p.few_rows, p.T * G) : p.few_rows;
+}
+
 // Arrival of a piece: how many came before it.  Called by one thread between two
 // barriers of those that wrote it and will read the others': the barrier before makes
 // their stores part of what this releases, the one after makes what this acquires theirs

@@ -79,6 +79,7 @@ struct RowsSmem {
   // sees them: the number + 1, request, KV head, the first token of such tiles
   int4 nan_unit[8];
   long long scan[kThreads / 32];
+  int parts[kThreads / 32];
   long long start_at;  // the share's first unit: its first tile's place in the list, request, KV head, row tile
   int start[3];
   int4 found;          // of its request: rows, cached tokens, row tiles
@@ -87,6 +88,7 @@ struct RowsSmem {
   // the tiles they cost the softmax its room there (287 us, not 265, for the prompts above)
   long long total;
   int shares;
+  int few;  // 4 bits: most rows per KV head of a request that the few-rows kernel takes
   uint32_t tmem;
   int abort_flag, last;
 };
@@ -119,9 +121,7 @@ struct Unit {
   int nt;                    // tiles
   long long at;              // the first one's place in the list
 };
-__device__ __forceinline__ bool takes(const KvAttentionParams& p, const Rows& r, int G) {
-  return r.in > 0 && (long long)r.n * G > p.few_rows;
-}
+__device__ __forceinline__ bool takes(int few, const Rows& r, int G) { return r.in > 0 && (long long)r.n * G > few; }
 __device__ __forceinline__ int row_tiles(const Rows& r, int G) { return (int)(((long long)r.in * G + kM - 1) / kM); }
 // Tiles that the unit's last row sees (one at least)
 __device__ __forceinline__ int unit_tiles(int n, int len, int G, int rt) {
@@ -148,14 +148,14 @@ __device__ __forceinline__ void load_request(const KvAttentionParams& p, int G, 
   u.len = cached(p, u.b);
   u.rts = row_tiles(r, G);
 }
-__device__ __forceinline__ void next_unit(const KvAttentionParams& p, int G, Unit& u) {
+__device__ __forceinline__ void next_unit(const KvAttentionParams& p, int few, int G, Unit& u) {
   u.at += u.nt;
   if (++u.rt == u.rts) {
     u.rt = 0;
     if (++u.h == p.Hkv) {
       u.h = 0;
       while (++u.b < p.B)
-        if (takes(p, rows_of(p, u.b), G)) break;
+        if (takes(few, rows_of(p, u.b), G)) break;
       if (u.b >= p.B) return;  // the list ends here, and so does the last share
       load_request(p, G, u);
     }
@@ -252,17 +252,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
   // share's first tile finds its request and head, all of them together its row tile.
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  Rows own = {};  // of the last of them: all there is while B <= threads
+  int own_len = 0;
+  int few = p.few_rows;
+  if (kFp4 && b0 < b1) own = rows_of(p, b0), own_len = cached(p, b0);
+  if (kFp4 && p.whole_most) few = most_few_rows<kThreads>(p, b0, b1, own, own_len, sm.parts, G);
+  if (kFp4 && tid == 0) sm.few = few;
   auto request_tiles = [&](const Rows& r, int len) {  // of one KV head
-    if (!takes(p, r, G)) return 0ll;
+    if (!takes(few, r, G)) return 0ll;
     const int rts = row_tiles(r, G);
     return tiles_before(r.n, len, G, rts - 1) + unit_tiles(r.n, len, G, rts - 1);
   };
-  Rows own = {};  // of the last of them: all there is while B <= threads
-  int own_len = 0;
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
-    own = rows_of(p, b);
-    own_len = cached(p, b);
+    if (!kFp4 || b > b0) own = rows_of(p, b), own_len = cached(p, b);
     mine += request_tiles(own, own_len);
     if ((long long)own.n * G > p.most_rows) record_status(p.status, kStatusOffsets, 53);
     if (own.bad || length_bad(p, b)) record_status(p.status, kStatusOffsets, 54);
@@ -572,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
       w.b = sm.start[0], w.h = sm.start[1], w.rt = sm.start[2], w.at = sm.start_at;
       load_request(p, G, w);
       w.nt = unit_tiles(w.n, w.len, G, w.rt);
-      for (uint32_t x = 0; w.at < t_last; ++x, next_unit(p, G, w)) {
+      for (uint32_t x = 0; w.at < t_last; ++x, next_unit(p, kFp4 ? sm.few : p.few_rows, G, w)) {
         if (x < k || (w.at >= t_first && w.at + w.nt <= t_last)) continue;
         const int c0 = (int)(((w.at + 1) * sm.shares - 1) / sm.total), c1 = (int)(((w.at + w.nt) * sm.shares - 1) / sm.total);
         if (atomicAdd(p.counters + c0, 1) == c1 - c0) p.counters[c0] = 0;
@@ -801,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
           if (lane == 0) mbar_arrive(&sm.page_full[slot]);
         }
       }
-      next_unit(p, G, u);
+      next_unit(p, kFp4 ? sm.few : p.few_rows, G, u);
     }
     if (ok) announce(0, 0);
   }
