@@ -625,6 +625,7 @@ cudaError_t launch_lora(const LoraParams& p, int sms, cudaStream_t stream) {
   if (p.T >= kManyEach * p.B) return launch_many(p, 1, requests, sms, stream);
   if (p.T <= kFewEach * p.B || 2 * expected <= few_places(p.r, sms))
     return launch_few(p, p.T, few + requests, expected, sms, stream);
+  // (calls of less than kTall rows all fit, so neither grid is empty)
   constexpr int kEach = (kTall - 1 + kFewRows - 1) / kFewRows;  // most tiles of a request that is not tall
   const cudaError_t e = launch_few(p, kTall - 1, few < (kEach - 1) * requests ? few + requests : kEach * requests, requests, sms, stream);
   if (e != cudaSuccess) return e;
