@@ -638,11 +638,6 @@ def _check_kv_cache_fp4(cache):
     return k, v, ks, vs, (shape[0], shape[1], shape[2], 2 * shape[3])
 
 
-def _misplaced(name):
-    """The calls hand addresses to kernels on the current GPU's stream: a tensor elsewhere is refused before that."""
-    raise ValueError(f"{name}: every tensor is on the current GPU")
-
-
 def _empty(shape, dtype, device, stream):
     """A new tensor of the stream that the call goes to: memory of another stream's may still be in use there."""
     if stream is None:
@@ -652,8 +647,8 @@ def _empty(shape, dtype, device, stream):
 
 
 def _not_on_gpu(name):
-    """The calls hand addresses to kernels: a tensor elsewhere is refused before that."""
-    raise ValueError(f"{name}: every tensor is on the GPU")
+    """The calls hand addresses to kernels on the current GPU's stream: a tensor elsewhere is refused before that."""
+    raise ValueError(f"{name}: every tensor is on the current GPU")
 
 
 def _ints(name, *tensors):
@@ -692,8 +687,10 @@ def kv_plan(seq_lens, new_lens, block_table, free_pages, n_free, page_size: int,
         raise ValueError("kv_plan: outputs are [B + 1], [B], [total_new] and [1]")
     if n_free.numel() != 1:
         raise ValueError("kv_plan: n_free is an int32 tensor of one element")
-    if not (seq_lens.is_cuda and new_lens.is_cuda and block_table.is_cuda and free_pages.is_cuda and n_free.is_cuda
-            and cu.is_cuda and kv.is_cuda and slots.is_cuda and left.is_cuda):
+    here = seq_lens.get_device()
+    if (here < 0 or new_lens.get_device() != here or block_table.get_device() != here or free_pages.get_device() != here
+            or n_free.get_device() != here or cu.get_device() != here or kv.get_device() != here
+            or slots.get_device() != here or left.get_device() != here or here != _device()):
         _not_on_gpu("kv_plan")
     a = _KV_PLAN_ARGS.pack(seq_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(), ld, width,
                            free_pages.data_ptr(), n_free.data_ptr(), free_pages.numel(), page_size, total_new,
@@ -712,7 +709,9 @@ def kv_release(lens, done, block_table, free_pages, n_free, page_size: int, stre
     if n_free.numel() != 1:
         raise ValueError("kv_release: n_free is an int32 tensor of one element")
     ld, width = _check_table("kv_release", block_table, B)
-    if not (lens.is_cuda and done.is_cuda and block_table.is_cuda and free_pages.is_cuda and n_free.is_cuda):
+    here = lens.get_device()
+    if (here < 0 or done.get_device() != here or block_table.get_device() != here or free_pages.get_device() != here
+            or n_free.get_device() != here or here != _device()):
         _not_on_gpu("kv_release")
     _check((_lib or load()).bs_kv_release(
         lens.data_ptr(), done.data_ptr(), B, block_table.data_ptr(), ld, width, free_pages.data_ptr(),
@@ -738,7 +737,9 @@ def kv_append(k, v, slots, cache, stream=None):
         raise TypeError(f"unsupported dtype {dt}")
     if slots.dtype is not _I32 or not slots.is_contiguous():
         raise TypeError("kv_append: slots is a contiguous int32 tensor")
-    if not (k.is_cuda and v.is_cuda and slots.is_cuda and kc.is_cuda and vc.is_cuda and ks.is_cuda and vs.is_cuda):
+    here = k.get_device()
+    if (here < 0 or v.get_device() != here or slots.get_device() != here or kc.get_device() != here
+            or vc.get_device() != here or ks.get_device() != here or vs.get_device() != here or here != _device()):
         _not_on_gpu("kv_append")
     a = _KV_APPEND_ARGS.pack(k.data_ptr(), v.data_ptr(), DTYPE_BF16 if dt is _BF16 else DTYPE_F32, T, Hkv, D, kt, kh,
                              vt, vh, slots.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(),
@@ -765,7 +766,7 @@ def kv_positions(seq_lens, cu_new, total_new: int, out=None, stream=None):
         raise ValueError("kv_positions: cu_new is [B + 1], out [total_new]")
     here = seq_lens.get_device()
     if here < 0 or cu_new.get_device() != here or out.get_device() != here or here != _device():
-        _misplaced("kv_positions")
+        _not_on_gpu("kv_positions")
     _check((_lib or load()).bs_kv_positions(seq_lens.data_ptr(), cu_new.data_ptr(), B, total_new, out.data_ptr(),
                                             _stream(stream)))
     return out
@@ -823,7 +824,7 @@ def kv_append_rotary(q, k, v, slots, positions, angles, cache, q_out=None, inter
         at_ptr, angles_ptr = positions.data_ptr(), angles.data_ptr()
         elsewhere = elsewhere or positions.get_device() != here or angles.get_device() != here
     if elsewhere or here != _device():
-        _misplaced("kv_append_rotary")
+        _not_on_gpu("kv_append_rotary")
     a = _KV_APPEND_ROTARY_ARGS.pack(q_ptr, qt, qh, out_ptr, ot, oh, k.data_ptr(), v.data_ptr(),
                                     DTYPE_BF16 if dt is _BF16 else DTYPE_F32, Hq, Hkv, D, T, kt, kh, vt, vh,
                                     slots.data_ptr(), at_ptr, angles_ptr, rows, R, 1 if interleaved else 0,
@@ -855,7 +856,7 @@ def kv_gather(cache, slots, out=None, stream=None):
     here = slots.get_device()
     if (here < 0 or here != _device() or kc.get_device() != here or vc.get_device() != here or ks.get_device() != here
             or vs.get_device() != here or k.get_device() != here or v.get_device() != here):
-        _misplaced("kv_gather")
+        _not_on_gpu("kv_gather")
     a = _KV_GATHER_ARGS.pack(slots.data_ptr(), shape[0], Hkv, D, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh,
                              FMT_FP4 if fp4 else FMT_FP8, page, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(),
                              vs.data_ptr(), pages)
@@ -915,21 +916,23 @@ def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_s
         raise ValueError("kv_attention: cu_q is [B + 1] and kv_lens [B]")
     if cu_q.dtype is not _I32 or kv_lens.dtype is not _I32 or not cu_q.is_contiguous() or not kv_lens.is_contiguous():
         raise TypeError("kv_attention: cu_q and kv_lens are contiguous int32 tensors")
+    here = q.get_device()
     if lse is None:
         lse_ptr = 0
     else:
         if lse.dtype is not _F32 or lse.shape != (T, Hq) or not lse.is_contiguous():
             raise ValueError("kv_attention: lse is a contiguous float32 [T, Hq] tensor")
-        if not lse.is_cuda:
+        if here < 0 or lse.get_device() != here:
             _not_on_gpu("kv_attention")
         lse_ptr = lse.data_ptr()
     if workspace is not None:
         if workspace.dtype is not _U8 or not workspace.is_contiguous():
             raise TypeError("kv_attention: workspace is a contiguous uint8 tensor of kv_attention_workspace")
-        if not workspace.is_cuda:
+        if here < 0 or workspace.get_device() != here:
             _not_on_gpu("kv_attention")
-    if not (q.is_cuda and out.is_cuda and kc.is_cuda and vc.is_cuda and ks.is_cuda and vs.is_cuda and block_table.is_cuda
-            and cu_q.is_cuda and kv_lens.is_cuda):
+    if (here < 0 or out.get_device() != here or kc.get_device() != here or vc.get_device() != here
+            or ks.get_device() != here or vs.get_device() != here or block_table.get_device() != here
+            or cu_q.get_device() != here or kv_lens.get_device() != here or here != _device()):
         _not_on_gpu("kv_attention")
     handle = _stream(stream)
     opts = getattr(_tls, "opts", None)
@@ -938,12 +941,11 @@ def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_s
             Hq, Hkv, D, max_q_len, D ** -0.5 if softmax_scale is None else softmax_scale,
             opts.get("wait_timeout_us", 0) if opts else 0)
     lib = _lib or load()
-    dev = q.get_device()
     if workspace is not None:
         ws, nbytes = workspace, workspace.numel()
     else:
-        nbytes = _kv_workspace_bytes(lib, dev, D)
-        ws = _workspaces.get((dev, handle))
+        nbytes = _kv_workspace_bytes(lib, here, D)
+        ws = _workspaces.get((here, handle))
         if ws is None or ws.numel() < nbytes:
             ws = _workspace_of(q.device, handle, nbytes)
     packed = _KV_ATTENTION_ARGS.pack(*args, ws.data_ptr(), nbytes)
@@ -976,8 +978,10 @@ def matvec_fp4(x, codes, sf, out_dtype=torch.bfloat16, alpha: float = 1.0, bias=
     ldo, one = out.stride()
     if out.shape != (M, N) or one != 1:
         raise ValueError(f"matvec_fp4: out is [{M}, {N}] with contiguous rows")
-    if not (x.is_cuda and codes.is_cuda and sf.is_cuda and out.is_cuda and (bias is None or bias.is_cuda)
-            and (tensor_scale is None or tensor_scale.is_cuda)):
+    here = x.get_device()
+    if (here < 0 or codes.get_device() != here or sf.get_device() != here or out.get_device() != here
+            or (bias is not None and bias.get_device() != here)
+            or (tensor_scale is not None and tensor_scale.get_device() != here) or here != _device()):
         _not_on_gpu("matvec_fp4")
     if M <= 1:
         ldx, ldo = K, N   # the stride of a single row means nothing
@@ -1019,7 +1023,7 @@ def lora_add(x, y, a, b, cu_rows, which, scales=None, out=None, stream=None):
     if (here < 0 or y.get_device() != here or a.get_device() != here or b.get_device() != here or out.get_device() != here
             or cu_rows.get_device() != here or which.get_device() != here
             or (scales is not None and scales.get_device() != here) or here != _device()):
-        _misplaced("lora_add")
+        _not_on_gpu("lora_add")
     packed = _LORA_ARGS.pack(x.data_ptr(), ldx, a.data_ptr(), b.data_ptr(), 0 if scales is None else scales.data_ptr(),
                              cu_rows.data_ptr(), which.data_ptr(), y.data_ptr(), ldy, out.data_ptr(), ldo, _dt(y), B, T,
                              K, N, r, n)
