@@ -676,8 +676,8 @@ def kv_plan(seq_lens, new_lens, block_table, free_pages, n_free, page_size: int,
     B = seq_lens.numel()
     if out is None:
         dev = seq_lens.device
-        out = (torch.empty(B + 1, dtype=_I32, device=dev), torch.empty(B, dtype=_I32, device=dev),
-               torch.empty(total_new, dtype=_I32, device=dev), torch.empty(1, dtype=_I32, device=dev))
+        out = (_empty(B + 1, _I32, dev, stream), _empty(B, _I32, dev, stream), _empty(total_new, _I32, dev, stream),
+               _empty(1, _I32, dev, stream))
     cu, kv, slots, left = out
     _ints("kv_plan", seq_lens, new_lens, free_pages, n_free, cu, kv, slots, left)
     if new_lens.numel() != B:
@@ -901,7 +901,7 @@ def kv_attention(q, cache, block_table, cu_q, kv_lens, max_q_len: int, softmax_s
     kc, vc, ks, vs, (pages, Hkv, page, D) = _check_kv_cache_fp4(cache) if fp4 else _check_kv_cache(cache)
     shape = q.shape
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=q.device)
+        out = _empty(shape, _BF16, q.device, stream)
     if q.dtype is not _BF16 or out.dtype is not _BF16:
         raise TypeError("kv_attention: q and out are bfloat16")
     if len(shape) != 3 or shape[2] != D or out.shape != shape:
@@ -974,7 +974,7 @@ def matvec_fp4(x, codes, sf, out_dtype=torch.bfloat16, alpha: float = 1.0, bias=
     if tensor_scale is not None and (tensor_scale.dtype is not _F32 or tensor_scale.numel() != 1):
         raise TypeError("matvec_fp4: tensor_scale is a float32 tensor of one element")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        out = _empty((M, N), out_dtype, x.device, stream)
     ldo, one = out.stride()
     if out.shape != (M, N) or one != 1:
         raise ValueError(f"matvec_fp4: out is [{M}, {N}] with contiguous rows")
