@@ -219,6 +219,14 @@ def _stream(stream=None):
     return _raw_stream(_device())
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor of the stream that the call goes to: memory of another stream's may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dt(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return DTYPE_F32
@@ -245,9 +253,9 @@ def q4_quantize(x: torch.Tensor, gather: torch.Tensor | None = None, rows: int |
     M = int(rows if rows is not None else (gather.numel() if gather is not None else x.shape[0]))
     K = x.shape[1]
     if out is None:
-        codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
-        sf = torch.empty(sf_bytes(M, K), dtype=torch.uint8, device=x.device)
-        lt = torch.empty((M, 64), dtype=torch.bfloat16, device=x.device) if lora_a_t is not None else None
+        codes = _empty((M, K // 2), torch.uint8, x.device, stream)
+        sf = _empty(sf_bytes(M, K), torch.uint8, x.device, stream)
+        lt = _empty((M, 64), torch.bfloat16, x.device, stream) if lora_a_t is not None else None
     else:
         codes, sf, lt = out
     _check(load().q4_quantize(_ptr(x), _dt(x), M, K, x.stride(0), _ptr(gather), _ptr(codes), _ptr(sf),
@@ -257,7 +265,7 @@ def q4_quantize(x: torch.Tensor, gather: torch.Tensor | None = None, rows: int |
 
 def tensor_amax(x: torch.Tensor, out=None, stream=None):
     """max |x| over the whole [M, K] tensor, as a device fp32 tensor [1]."""
-    amax = out if out is not None else torch.empty(1, dtype=torch.float32, device=x.device)
+    amax = out if out is not None else _empty(1, torch.float32, x.device, stream)
     _check(load().bs_tensor_amax(_ptr(x), _dt(x), x.shape[0], x.shape[1], x.stride(0), _ptr(amax), _stream(stream)))
     return amax
 
@@ -271,9 +279,9 @@ def q4_quantize_two_level(x: torch.Tensor, amax=None, out=None, stream=None):
     if amax is None:
         amax = tensor_amax(x, stream=stream)
     if out is None:
-        out = (torch.empty((M, K // 2), dtype=torch.uint8, device=x.device),
-               torch.empty(sf_bytes(M, K), dtype=torch.uint8, device=x.device),
-               torch.empty(1, dtype=torch.float32, device=x.device))
+        out = (_empty((M, K // 2), torch.uint8, x.device, stream),
+               _empty(sf_bytes(M, K), torch.uint8, x.device, stream),
+               _empty(1, torch.float32, x.device, stream))
     codes, sf, ts = out
     _check(load().q4_quantize_two_level(_ptr(x), _dt(x), M, K, x.stride(0), _ptr(amax), _ptr(codes), _ptr(sf),
                                         _ptr(ts), _stream(stream)))
@@ -284,8 +292,8 @@ def fp4_gather_rows(codes, sf, K: int, gather, out=None, stream=None):
     """Rows gather[i] of an FP4 matrix (codes + MMA-layout scales); -1 -> zero row."""
     rows_out = gather.numel()
     if out is None:
-        out = (torch.empty((rows_out, K // 2), dtype=torch.uint8, device=codes.device),
-               torch.empty(sf_bytes(rows_out, K), dtype=torch.uint8, device=codes.device))
+        out = (_empty((rows_out, K // 2), torch.uint8, codes.device, stream),
+               _empty(sf_bytes(rows_out, K), torch.uint8, codes.device, stream))
     _check(load().bs_fp4_gather_rows(_ptr(codes), _ptr(sf), codes.shape[0], K, _ptr(gather), rows_out,
                                      _ptr(out[0]), _ptr(out[1]), _stream(stream)))
     return out
@@ -297,8 +305,8 @@ def fp8_gather_rows(codes, scales, gather, out=None, stream=None):
     rows_in, K = codes.shape
     rows_out = gather.numel()
     if out is None:
-        out = (torch.empty((rows_out, K), dtype=torch.uint8, device=codes.device),
-               torch.empty((K // 128, rows_out), dtype=torch.float32, device=codes.device))
+        out = (_empty((rows_out, K), torch.uint8, codes.device, stream),
+               _empty((K // 128, rows_out), torch.float32, codes.device, stream))
     _check(load().bs_fp8_gather_rows(_ptr(codes), _ptr(scales), rows_in, K, _ptr(gather), rows_out,
                                      _ptr(out[0]), _ptr(out[1]), _stream(stream)))
     return out
@@ -310,9 +318,9 @@ def q8_quantize(x: torch.Tensor, mode: int = Q8_TOKEN, out=None, stream=None):
     assert x.is_cuda and x.dim() == 2 and x.stride(1) == 1
     M, K = x.shape
     if out is None:
-        codes = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        codes = _empty((M, K), torch.uint8, x.device, stream)
         shape = {Q8_TOKEN: (K // 128, M), Q8_BLOCK: ((M + 127) // 128, K // 128), Q8_ROW: (M,)}[mode]
-        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+        scales = _empty(shape, torch.float32, x.device, stream)
     else:
         codes, scales = out
     _check(load().q8_quantize(_ptr(x), _dt(x), M, K, x.stride(0), mode, _ptr(codes), _ptr(scales),
@@ -349,7 +357,7 @@ def gemm_fp4(a, sfa, b, sfb, K: int, out_dtype=torch.bfloat16, alpha: float = 1.
     (two-level operands: their device tensor scales from q4_quantize_two_level)."""
     M, N = a.shape[0], b.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        out = _empty((M, N), out_dtype, a.device, stream)
     g = _args(FMT_FP4, a, sfa, b, sfb, M, N, K, out, alpha, col_scale, lora_t, lora_b_t, bias, num_sms)
     g.a_tensor_scale = None if a_tensor_scale is None else a_tensor_scale.data_ptr()
     g.b_tensor_scale = None if b_tensor_scale is None else b_tensor_scale.data_ptr()
@@ -407,7 +415,7 @@ def gemm_fp8(a, sa, b, sb, out_dtype=torch.bfloat16, out=None, num_sms: int = 0,
     M, K = a.shape
     N = b.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        out = _empty((M, N), out_dtype, a.device, stream)
     g = _args(FMT_FP8, a, sa, b, sb, M, N, K, out, num_sms=num_sms)
     g.weights_ready = 1 if weights_ready else 0
     g.fp8_scaling = 2 if rowwise else 0   # W8A8: sa [M] per token, sb [N] per channel
@@ -429,7 +437,7 @@ def _gemm_multi(fmt, a, sa, weights, M, N, K, out_dtype, outs, num_sms, weights_
     if outs is not None and len(outs) != G:
         raise ValueError(f"{len(outs)} outputs for {G} weight sets")
     if outs is None:
-        outs = [torch.empty((M, N), dtype=out_dtype, device=a.device) for _ in range(G)]
+        outs = [_empty((M, N), out_dtype, a.device, stream) for _ in range(G)]
     b0, sb0 = weights[0]
     g = _args(fmt, a, sa, b0, sb0, M, N, K, outs[0], alpha=alpha, num_sms=num_sms)
     g.weights_ready = 1 if weights_ready else 0
@@ -492,7 +500,7 @@ def grouped_gemm_fp8(a, sfa, b, sfb, N: int, E: int, offsets, counts, epilogue: 
     M, K = a.shape
     if out is None:
         dt = torch.float32 if epilogue == EPI_ROWS else torch.bfloat16
-        out = torch.empty((M, N), dtype=dt, device=a.device)
+        out = _empty((M, N), dt, a.device, stream)
     g = _args(FMT_FP8, a, sfa, b, sfb, M, N, K, out, num_sms=num_sms)
     _check(load().bs_grouped_gemm(ctypes.byref(g), E, _ptr(offsets), _ptr(counts), epilogue, None,
                                   _ptr(weight_of), None, 0, _stream(stream)))
@@ -506,9 +514,9 @@ def grouped_gemm_fp4_swiglu_q4(a, sfa, b, sfb, K: int, N: int, E: int, offsets, 
     q4_quantize would write them for the segment rows."""
     M = a.shape[0]
     if h_codes is None:
-        h_codes = torch.empty((M, N // 2), dtype=torch.uint8, device=a.device)
+        h_codes = _empty((M, N // 2), torch.uint8, a.device, stream)
     if h_sf is None:
-        h_sf = torch.empty(sf_bytes(M, N), dtype=torch.uint8, device=a.device)
+        h_sf = _empty(sf_bytes(M, N), torch.uint8, a.device, stream)
     g = _args(FMT_FP4, a, sfa, b, sfb, M, N, K, None, num_sms=num_sms)
     g.n_chunk_blocks = n_chunk_blocks
     _check(load().bs_grouped_gemm_swiglu_q4(ctypes.byref(g), E, _ptr(offsets), _ptr(counts), _ptr(h_codes),
@@ -526,8 +534,8 @@ def moe_router_topk(logits, k: int, out=None, stream=None):
     softmax of the chosen logits)."""
     T, E = logits.shape
     if out is None:
-        out = (torch.empty((T, k), dtype=torch.int32, device=logits.device),
-               torch.empty((T, k), dtype=torch.float32, device=logits.device))
+        out = (_empty((T, k), torch.int32, logits.device, stream),
+               _empty((T, k), torch.float32, logits.device, stream))
     _check(load().bs_moe_router_topk(_ptr(logits), T, E, k, _ptr(out[0]), _ptr(out[1]), _stream(stream)))
     return out
 
@@ -540,14 +548,14 @@ def moe_dispatch(topk_ids, topk_w, E: int, out=None, workspace=None, stream=None
     dev = topk_ids.device
     rows = moe_rows_bound(T, k, E)
     if out is None:
-        out = dict(counts=torch.empty(E, dtype=torch.int32, device=dev),
-                   offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
-                   pair_of_row=torch.empty(rows, dtype=torch.int32, device=dev),
-                   token_of=torch.empty(rows, dtype=torch.int32, device=dev),
-                   weight_of=torch.empty(rows, dtype=torch.float32, device=dev))
+        out = dict(counts=_empty(E, torch.int32, dev, stream),
+                   offsets=_empty(E + 1, torch.int32, dev, stream),
+                   pair_of_row=_empty(rows, torch.int32, dev, stream),
+                   token_of=_empty(rows, torch.int32, dev, stream),
+                   weight_of=_empty(rows, torch.float32, dev, stream))
     wsb = int(lib.bs_moe_dispatch_workspace_bytes(T, k, E))
     if workspace is None:
-        workspace = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
+        workspace = _empty(max(wsb, 16), torch.uint8, dev, stream)
     _check(lib.bs_moe_dispatch(_ptr(topk_ids), _ptr(topk_w), T, k, E, _ptr(out["counts"]), _ptr(out["offsets"]),
                                _ptr(out["pair_of_row"]), _ptr(out["token_of"]), _ptr(out["weight_of"]),
                                _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -564,9 +572,9 @@ def moe_combine(rows, pair_of_row, T: int, k: int, out=None, row_of_pair=None, s
     ``rows`` fp32 [n_rows, H] from a grouped GEMM with EPI_ROWS."""
     n_rows, H = rows.shape
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=rows.device)
+        out = _empty((T, H), torch.bfloat16, rows.device, stream)
     if row_of_pair is None:
-        row_of_pair = torch.empty(max(T * k, 1), dtype=torch.int32, device=rows.device)
+        row_of_pair = _empty(max(T * k, 1), torch.int32, rows.device, stream)
     _check(load().bs_moe_combine(_ptr(rows), rows.stride(0), _ptr(pair_of_row), n_rows, T, k, H, _ptr(row_of_pair),
                                  _ptr(out), out.stride(0), _stream(stream)))
     return out
@@ -636,14 +644,6 @@ def _check_kv_cache_fp4(cache):
     if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
         raise ValueError("KV cache buffers must be contiguous")
     return k, v, ks, vs, (shape[0], shape[1], shape[2], 2 * shape[3])
-
-
-def _empty(shape, dtype, device, stream):
-    """A new tensor of the stream that the call goes to: memory of another stream's may still be in use there."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _not_on_gpu(name):
