@@ -384,10 +384,10 @@ __device__ __forceinline__ void fp4_tile(uint32_t codes, uint32_t scales, uint8_
 // 64 requests of 500 to 16000 tokens, 32 heads over 8, D = 128 (604 MB): 105 us, 0.85
 // of HBM.  63 drafted tokens of 16 requests, 16 heads, D = 64, 16-token pages (60 MB):
 // 24 us, bound by what a unit costs beside its tiles (q, the join of the warps, its
-// piece); one token over 1000: 10 us, a chain of dependent reads.  Three CTAs an SM
-// leave 128 registers a thread, of which 16 to 20 bytes are spilled.
-// Of 4 bits, which halve the stream, the same calls take 73 us (340 MB, 0.68 of HBM; with 16000
-// tokens each 218, 0.80), 22 us (34 MB) and 10 us: about 14 us that no stream fills (shares,
+// piece); one token over 1000: 9.5 us, a chain of dependent reads.  Three CTAs an SM
+// leave 128 registers a thread, and 20 to 24 bytes of it are spilled.
+// Of 4 bits, which halve the stream, the same calls take 73 us (340 MB, 0.69 of HBM; with 16000
+// tokens each 216, 0.81), 21 us (34 MB) and 9 us: about 14 us that no stream fills (shares,
 // lists and the first tiles, the joins) and then 0.86 of HBM.  A cached element costs what it does
 // with 8 bits and the product with its scale: 335 instructions a warp and 16 tokens, 0.55 of the
 // issue slots and 0.54 of the pipe that converts and exchanges bytes.  So 32 tokens a step, whose

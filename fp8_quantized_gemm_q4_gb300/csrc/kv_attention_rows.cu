@@ -21,7 +21,7 @@
 // maximum, the vote on the reference, the exponentials, the store) and whose
 // warps have 1540 issue slots of about 2800 clocks a tile with the converters.  832
 // threads leave 72 registers each, 20 bytes of which are spilled.
-// B = 2, 2048 rows x 32 heads over 4000 to 8000 tokens, D = 128: 254 us (880 TFLOP/s); the
+// B = 2, 2048 rows x 32 heads over 4000 to 8000 tokens, D = 128: 252 us (885 TFLOP/s); the
 // same with D = 64, half the MMAs: 218.  With two threads per row 303, with one 2.5 times the MMAs' time.  Also built and
 // measured: two groups of warps on alternate tiles, each with an O of its own and
 // Q in shared memory (303 us: both operands of Q K^T from shared memory take all of

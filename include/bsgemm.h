@@ -689,7 +689,10 @@ bs_status bs_kv_attention(const bs_kv_attention_args *args, bs_stream_t stream);
  *                      in the low nibble of byte j
  *   k_scales, v_scales e4m3 [num_pages, Hkv, page_size, D / 16]
  * 9/16 byte an element; element d stands for code * scale[d / 16].  Pages, block
- * tables and slots are those of the 8-bit cache (bs_kv_plan, bs_kv_release).
+ * tables and slots are those of the 8-bit cache (bs_kv_plan, bs_kv_release).  A scale
+ * reaches from 2^-9 to 448, and there is none above it: 16 elements of at most 6 * 2^-10
+ * become 0, and where the largest is below 6 * 2^-6 the scale is a subnormal e4m3
+ * number, of fewer bits; elements above 6 * 448 are held there.
  *
  * bs_kv_attention_fp4 -- bs_kv_attention over that cache.  args are bs_kv_attention's,
  * with the 4-bit codes; args->k_scales and v_scales are not used, these are (16-byte
